@@ -306,6 +306,181 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
                                    void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Gated linear recurrence: a mixer of q, k and v like the HyenaND mixer, with
+ * a matrix state per head in place of the convolution ("Week 11: Hyena, Long
+ * Convolution, and Linear Attention": linear attention, retention and the
+ * gated form are its cases g = 0, g fixed per head, g from the data).
+ *
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T        (dk x dv, float32)
+ *   o_t = scale * S_t^T q_t                   t = 1..length, S_0 = state or 0
+ *
+ * g_t is one log decay per token and head.  g_t = -infinity starts a new
+ * sequence inside a row (nothing before it is seen), and so does any g_t below
+ * -87.34 (its exp is below the smallest normal float32).
+ *
+ * Layouts: q, k [B][N][heads][dk] and v [B][N][heads][dv] in the plan's io
+ * dtype, g float32 [B][N][heads], each given as a strided view (below);
+ * states float32 [B][heads][dk][dv], dense; outputs and gradients dense in
+ * the shape of what they belong to.
+ *
+ * lengths (int32 [B] on the device, or NULL: all N) makes a padded batch:
+ * tokens at lengths[b] and after it are never read, their rows of o and of
+ * the gradients are written as zeros, and the final state is the state at the
+ * length.  Values are clamped to 0..N.
+ *
+ * Precision.  States, decays, their sums and every accumulation are float32
+ * (sums of log decays: float64).  With 16-bit storage the scores between
+ * tokens and, for o, dk, dq and dv, the state are rounded to the storage type
+ * as operands of the matrix products (relative error up to 2^-8 for bfloat16,
+ * 2^-11 for binary16 scores, or 2^-25 absolutely where they are subnormal); the states
+ * and the gradient of g are computed from operands split so that they keep
+ * float32 accuracy.  Inputs within a row's length have to be finite (g may be
+ * -infinity): an infinity or a NaN reaches its own and later tokens' results,
+ * and may reach those of up to 63 tokens before it.
+ *
+ * No atomics are used: the same call gives the same bits.
+ */
+
+/* A tensor [B][N][heads][width] seen through strides in elements; the last
+ * axis is contiguous.  A stride of 0 shares one tensor among rows, tokens or
+ * heads (gradients are then written for each use, and the caller sums them).
+ * data is aligned to its element. */
+typedef struct hyena_view {
+    const void* data;
+    int64_t batch, token, head;
+} hyena_view;
+
+typedef struct hyena_recurrence_s* hyena_recurrence_t;
+
+/*
+ * Create a recurrence plan: B >= 1 rows of up to N >= 1 tokens (N below 2^31),
+ * heads >= 1, 1 <= dk, dv <= 128, B * heads at most 2^24.  Touches no GPU
+ * state.  Release with hyena_recurrence_destroy.
+ */
+hyena_status hyena_recurrence_create(hyena_recurrence_t* plan, int64_t B, int64_t N,
+                                     int64_t heads, int64_t dk, int64_t dv, int32_t io_dtype);
+
+/* Workspace bytes of hyena_recurrence_forward and hyena_recurrence_backward
+ * (either output pointer may be NULL).  The workspace needs no initialisation
+ * and keeps nothing between calls; it must not be shared by calls that run
+ * concurrently.  A size may be 0 (the workspace may then be NULL). */
+hyena_status hyena_recurrence_query(hyena_recurrence_t plan, size_t* forward_bytes,
+                                    size_t* backward_bytes);
+
+typedef struct hyena_recurrence_inputs {
+    hyena_view q, k, v; /* io dtype */
+    hyena_view g;       /* float32, width 1 */
+    const float* state; /* S_0, or NULL for zeros */
+    const int32_t* lengths;
+    float scale;
+} hyena_recurrence_inputs;
+
+/* o: [B][N][heads][dv] (io dtype).  final_state: float32 or NULL.  Neither may
+ * overlap an input, each other or the workspace. */
+hyena_status hyena_recurrence_forward(hyena_recurrence_t plan, const hyena_recurrence_inputs* in,
+                                      void* o, float* final_state, void* workspace, void* stream);
+
+/*
+ * Backward pass: from d_o (io dtype, a view like v) and d_final (gradient of
+ * the final state, or NULL for zero) the gradients dq, dk, dv (io dtype,
+ * dense), dg (float32 [B][N][heads]) and d_state (float32, or NULL).
+ *   dS_t = exp(g_{t+1}) dS_{t+1} + scale * q_t d_o_t^T
+ *   dq_t = scale * S_t d_o_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t,
+ *   dg_t = exp(g_t) <S_{t-1}, dS_t>,  d_state = exp(g_1) dS_1
+ * dg is 0 where g starts a new sequence.  The states are computed again, not
+ * kept from a forward call.
+ */
+typedef struct hyena_recurrence_grads {
+    void* dq;
+    void* dk;
+    void* dv;
+    float* dg;
+    float* d_state;
+} hyena_recurrence_grads;
+
+hyena_status hyena_recurrence_backward(hyena_recurrence_t plan,
+                                       const hyena_recurrence_inputs* in, const hyena_view* d_o,
+                                       const float* d_final, const hyena_recurrence_grads* out,
+                                       void* workspace, void* stream);
+
+/*
+ * One token for each of the plan's B rows, on a table of states: row b uses
+ * and updates states[slots[b]] (float32 [n_slots][heads][dk][dv]).  q, k, v, g
+ * are read at token 0 of their views; o: [B][heads][dv].  in->state and
+ * in->lengths are ignored.  slots: int32 [B] on the device, or NULL for
+ * slots[b] = b (then n_slots >= B).  A slot outside 0..n_slots-1 marks a row
+ * that takes no part: its row of o is written as zeros and no state is touched.
+ * The other slots have to differ from each other: two rows on one state would
+ * update it in no order.
+ */
+hyena_status hyena_recurrence_step(hyena_recurrence_t plan, const hyena_recurrence_inputs* in,
+                                   const int32_t* slots, int64_t n_slots, float* states, void* o,
+                                   void* stream);
+
+hyena_status hyena_recurrence_destroy(hyena_recurrence_t plan);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Norms of queries and keys per head, with the position rotation in the same
+ * pass: the step in front of a mixer of q, k and v ("How HyenaND works",
+ * section "A worked trace": the L2 norm of q and k).  For each head of width D,
+ *
+ *   n = w . x / sqrt(sum(x^2) / m + eps)   m = D (RMS) or 1 (L2); or n = x
+ *   y[a] = s (n[a] cos t - n[b] sin t),  y[b] = s (n[a] sin t + n[b] cos t)
+ *
+ * over the pairs (a, b) of the first rotary_dim channels: (i, i + rotary_dim/2)
+ * in the half layout, (2i, 2i + 1) in the interleaved one, t = position *
+ * freqs[i], i < rotary_dim/2, s = rotary_scale.  The other channels of n stay
+ * as they are.  freqs is a float64 table on the device, so a long context's
+ * scaling is in the caller's frequencies; angles are float64, reduced before
+ * their sine and cosine are taken in float32, sums and norms float32 (sums of
+ * the weights' gradients: float64 between workgroups).
+ *
+ * position of token n in row b: positions[b * N + n] (int32 on the device) or,
+ * with positions = NULL, position_offset + n.
+ */
+#define HYENA_NORM_NONE 0
+#define HYENA_NORM_RMS 1
+#define HYENA_NORM_L2 2
+#define HYENA_ROTARY_HALF 0
+#define HYENA_ROTARY_INTERLEAVED 1
+
+typedef struct hyena_qk_norm {
+    int64_t B, N;              /* rows, tokens */
+    int64_t q_heads, k_heads;  /* 1..4096 each */
+    int64_t D;                 /* head width, 1..1024 */
+    int32_t io_dtype;
+    int32_t norm;              /* HYENA_NORM_* */
+    int32_t layout;            /* HYENA_ROTARY_* */
+    int64_t rotary_dim;        /* even, 0..D */
+    float eps;                 /* >= 0 */
+    float rotary_scale;
+    const double* freqs;       /* [rotary_dim / 2]; NULL allowed for rotary_dim = 0 */
+    const float* q_weight;     /* [D], or NULL for ones */
+    const float* k_weight;
+    const int32_t* positions;  /* [B][N] or NULL */
+    int64_t position_offset;
+    hyena_view q, k;           /* inputs */
+} hyena_qk_norm;
+
+/* q_out [B][N][q_heads][D], k_out [B][N][k_heads][D]: dense, in the io dtype.
+ * They must not overlap an input or each other. */
+hyena_status hyena_qk_norm_forward(const hyena_qk_norm* op, void* q_out, void* k_out,
+                                   void* stream);
+
+/* Scratch bytes of hyena_qk_norm_backward. */
+hyena_status hyena_qk_norm_scratch_bytes(const hyena_qk_norm* op, size_t* bytes);
+
+/* Gradients of q, k (dense, io dtype) and of the weights (float32 [D]; NULL:
+ * not wanted) from those of the outputs, given as views.  With
+ * HYENA_NORM_NONE the weights have no part and no gradient. */
+hyena_status hyena_qk_norm_backward(const hyena_qk_norm* op, const hyena_view* dq_out,
+                                    const hyena_view* dk_out, void* dq, void* dk,
+                                    float* dq_weight, float* dk_weight, void* scratch,
+                                    void* stream);
+
+/*
  * Launch timing, a profiling aid that computes nothing.  After
  * hyena_timing_begin(max_launches), every kernel that a hyena_* call made on
  * this host thread enqueues is bracketed by two HIP timing events recorded on

@@ -1,0 +1,553 @@
+// qk_norm.hip -- norms of queries and keys per head with the position rotation
+// in the same pass, and their backward pass (include/hyena.h).
+//
+// Bound by memory: each channel is read and written once (the backward pass
+// reads two tensors).  What is shared by all heads of a token, the sines and
+// cosines, is computed once per token and kept in LDS; everything else of a
+// head stays in the registers of the few lanes that hold it.
+//
+// A head is cut into units of 2 W channels, two vectors of W: W pairs of the
+// rotation (in the half layout the vectors are rotary_dim / 2 apart, else side
+// by side) or 2 W channels that are not rotated.  A lane holds U units, a power
+// of two of lanes one head, so a pair is always within a lane and the norm's
+// sum is a few shuffles.
+#include <hip/hip_runtime.h>
+
+#include <string>
+#include <type_traits>
+
+#include "recurrence_device.h"
+#include "recurrence_plan.h"
+#include "plan.h"
+#include "timing.h"
+
+namespace hy {
+
+namespace {
+
+constexpr int kQkThreads = 256;
+constexpr int kQkTokens = 16;      // most tokens of a workgroup's tile
+constexpr int kQkAngles = 2048;    // most (token, frequency) pairs of a tile: 16 KB of LDS
+constexpr int kQkGradGroups = 512; // most workgroups of the backward pass: rows of its partial sums
+
+struct QkTensor {
+    RView x, dy;
+    void* out;
+    const float* w;
+    float* dw_part;     // [groups][D]
+    int32_t heads;
+    uint32_t magic;     // ceil(2^32 / heads), heads > 1: item / heads = item * magic >> 32, item < 2^16
+};
+
+struct QkArgs {
+    QkTensor t[2];
+    const double* freqs;
+    const int32_t* positions;
+    int64_t offset;
+    int64_t N, rows;    // rows: B * N
+    int64_t tiles;
+    int32_t tokens;     // per tile
+    int32_t D, rotary;
+    int32_t half, norm;
+    int32_t lanes;      // per head, a power of two
+    float mean;         // 1 / m
+    float eps, rscale;
+};
+
+template <typename T, int W>
+__device__ __forceinline__ void qk_load(float (&x)[W], const T* p)
+{
+    if constexpr (W == 1) {
+        x[0] = load_one<T>(p);
+    } else {
+        typename Mx<T>::vec4 v[W / 4];
+        if constexpr (W == 8) *(uint4*)v = *(const uint4*)p;
+        else v[0] = *(const typename Mx<T>::vec4*)p;
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const f32x4 f = Mx<T>::widen(v[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * i + j] = f[j];
+        }
+    }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void qk_store(T* p, const float (&x)[W])
+{
+    if constexpr (W == 1) {
+        store_one<T>(p, x[0]);
+    } else {
+        typename Mx<T>::vec4 v[W / 4];
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            f32x4 f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = x[4 * i + j];
+            v[i] = Mx<T>::narrow(f);
+        }
+        if constexpr (W == 8) *(uint4*)p = *(const uint4*)v;
+        else *(typename Mx<T>::vec4*)p = v[0];
+    }
+}
+
+// Sine and cosine of position * frequency.  The angle in float64 is reduced by
+// 2 pi in two parts (error below 2^-52 of the angle plus 2e-16 at 2^31 turns),
+// so far positions keep float32 accuracy.
+__device__ __forceinline__ float2 qk_turn(int64_t pos, double freq, float scale)
+{
+    const double a = (double)pos * freq;
+    const double n = rint(a * 0.15915494309189533577);
+    double r = fma(-n, 6.283185307179586232, a);
+    r = fma(-n, 2.4492935982947064e-16, r);
+    float s, c;
+    sincosf((float)r, &s, &c);
+    return make_float2(c * scale, s * scale);
+}
+
+// y = turn(x) for GRAD = false, its transpose for GRAD = true; a pair's members
+// are (x0[e], x1[e]) in the half layout, neighbours otherwise.
+template <int W, bool GRAD>
+__device__ __forceinline__ void qk_rotate(float (&x0)[W], float (&x1)[W], const float2* turn, bool half)
+{
+    auto one = [](float& a, float& b, float2 t) {
+        const float s = GRAD ? -t.y : t.y;
+        const float u = a * t.x - b * s;
+        b = a * s + b * t.x;
+        a = u;
+    };
+    if (half || W == 1) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) one(x0[e], x1[e], turn[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < W / 2; ++e) {
+            one(x0[2 * e], x0[2 * e + 1], turn[e]);
+            one(x1[2 * e], x1[2 * e + 1], turn[W / 2 + e]);
+        }
+    }
+}
+
+template <typename T, int W, int U, bool GRAD>
+__global__ __launch_bounds__(kQkThreads) void hyena_qk_norm_pass(QkArgs p)
+{
+    __shared__ float2 turns[kQkAngles];
+    __shared__ float sums[GRAD ? kQkThreads * 2 * W : 1];
+    const int tid = threadIdx.x;
+    const int lane = tid & (p.lanes - 1), group = tid / p.lanes, groups = kQkThreads / p.lanes;
+    const int units = (p.D + 2 * W - 1) / (2 * W), turned = p.rotary / (2 * W), nf = p.rotary / 2;
+
+    // the lane's units: places of their two vectors, weights
+    int c0[U], c1[U];
+    bool in0[U], in1[U], rot[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int n = lane + u * p.lanes;
+        rot[u] = n < turned;
+        const bool apart = rot[u] && p.half;
+        c0[u] = apart ? n * W : 2 * n * W;
+        c1[u] = apart ? nf + n * W : 2 * n * W + W;
+        in0[u] = n < units;
+        in1[u] = n < units && c1[u] < p.D;
+    }
+    float dw[GRAD ? 2 : 1][U][2][W];
+    if constexpr (GRAD) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < W; ++e) dw[k][u][0][e] = dw[k][u][1][e] = 0.0f;
+    }
+
+    for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+        const int64_t row0 = tile * p.tokens;
+        const int ntok = p.rows - row0 < p.tokens ? (int)(p.rows - row0) : p.tokens;
+        if (GRAD) __syncthreads();
+        for (int i = tid; i < ntok * nf; i += kQkThreads) {
+            const int64_t row = row0 + i / nf;
+            const int64_t pos = p.positions ? (int64_t)p.positions[row] : p.offset + row % p.N;
+            turns[i] = qk_turn(pos, p.freqs[i % nf], p.rscale);
+        }
+        __syncthreads();
+        auto tensor = [&](auto which) {
+            constexpr int K = decltype(which)::value;
+            const QkTensor& q = p.t[K];
+            float w[U][2][W];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    w[u][0][e] = q.w && in0[u] ? q.w[c0[u] + e] : 1.0f;
+                    w[u][1][e] = q.w && in1[u] ? q.w[c1[u] + e] : 1.0f;
+                }
+            const int items = ntok * q.heads;
+            for (int item = group; item < items; item += groups) {
+                const int tok = q.heads == 1 ? item : (int)__umulhi((uint32_t)item, q.magic), head = item - tok * q.heads;
+                const int64_t row = row0 + tok, b = row / p.N, t = row - b * p.N;
+                const T* xp = (const T*)q.x.p + b * q.x.b + t * q.x.t + head * q.x.h;
+                T* op = (T*)q.out + (row * q.heads + head) * p.D;
+                float x[U][2][W], d[U][2][W];
+                float ss = 0.0f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) x[u][0][e] = x[u][1][e] = d[u][0][e] = d[u][1][e] = 0.0f;
+                    if (in0[u]) qk_load<T, W>(x[u][0], xp + c0[u]);
+                    if (in1[u]) qk_load<T, W>(x[u][1], xp + c1[u]);
+                }
+                if constexpr (GRAD) {
+                    const T* dp = (const T*)q.dy.p + b * q.dy.b + t * q.dy.t + head * q.dy.h;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (in0[u]) qk_load<T, W>(d[u][0], dp + c0[u]);
+                        if (in1[u]) qk_load<T, W>(d[u][1], dp + c1[u]);
+                    }
+                }
+                float r = 1.0f;
+                if (p.norm) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int e = 0; e < W; ++e) ss += x[u][0][e] * x[u][0][e] + x[u][1][e] * x[u][1][e];
+                    for (int m = 1; m < p.lanes; m <<= 1) ss += __shfl_xor(ss, m);
+                    r = 1.0f / sqrtf(ss * p.mean + p.eps);
+                }
+                const float2* turn = turns + tok * nf;
+                if constexpr (!GRAD) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (p.norm) {
+#pragma unroll
+                            for (int e = 0; e < W; ++e) {
+                                x[u][0][e] *= r * w[u][0][e];
+                                x[u][1][e] *= r * w[u][1][e];
+                            }
+                        }
+                        if (rot[u]) qk_rotate<W, false>(x[u][0], x[u][1], turn + (lane + u * p.lanes) * W, p.half);
+                        if (in0[u]) qk_store<T, W>(op + c0[u], x[u][0]);
+                        if (in1[u]) qk_store<T, W>(op + c1[u], x[u][1]);
+                    }
+                } else {
+                    float along = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (rot[u]) qk_rotate<W, true>(d[u][0], d[u][1], turn + (lane + u * p.lanes) * W, p.half);
+                        if (p.norm) {
+#pragma unroll
+                            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                                for (int e = 0; e < W; ++e) {
+                                    x[u][v][e] *= r;
+                                    dw[K][u][v][e] += d[u][v][e] * x[u][v][e];
+                                    d[u][v][e] *= w[u][v][e];
+                                    along += d[u][v][e] * x[u][v][e];
+                                }
+                        }
+                    }
+                    if (p.norm) {
+                        for (int m = 1; m < p.lanes; m <<= 1) along += __shfl_xor(along, m);
+                        along *= p.mean;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (p.norm) {
+#pragma unroll
+                            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                                for (int e = 0; e < W; ++e) d[u][v][e] = (d[u][v][e] - x[u][v][e] * along) * r;
+                        }
+                        if (in0[u]) qk_store<T, W>(op + c0[u], d[u][0]);
+                        if (in1[u]) qk_store<T, W>(op + c1[u], d[u][1]);
+                    }
+                }
+            }
+        };
+        tensor(std::integral_constant<int, 0>{});
+        tensor(std::integral_constant<int, 1>{});
+    }
+    if constexpr (GRAD) {
+        // the workgroup's sums for the weights, over its groups in order
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (p.t[k].dw_part == nullptr) continue;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    sums[(e * 2) * kQkThreads + tid] = dw[k][u][0][e];
+                    sums[(e * 2 + 1) * kQkThreads + tid] = dw[k][u][1][e];
+                }
+                __syncthreads();
+                for (int i = tid; i < p.lanes * 2 * W; i += kQkThreads) {
+                    const int l = i / (2 * W), ev = i % (2 * W), e = ev / 2, v = ev % 2;
+                    const int n = l + u * p.lanes;
+                    const bool apart = n < turned && p.half;
+                    const int c = (v ? (apart ? nf + n * W : 2 * n * W + W) : (apart ? n * W : 2 * n * W)) + e;
+                    if (n < units && c < p.D) {
+                        float s = 0.0f;
+                        for (int g = 0; g < groups; ++g) s += sums[ev * kQkThreads + g * p.lanes + l];
+                        p.t[k].dw_part[(int64_t)blockIdx.x * p.D + c] = s;
+                    }
+                }
+            }
+        }
+    }
+}
+
+// dw[c] = sum over the workgroups' rows, 16 channels by 16 rows at a time.
+__global__ __launch_bounds__(256) void hyena_qk_weight_grad(const float* part0, const float* part1, float* out0,
+                                                            float* out1, int groups, int D)
+{
+    __shared__ double sums[256];
+    const float* part = blockIdx.y ? part1 : part0;
+    float* out = blockIdx.y ? out1 : out0;
+    if (out == nullptr) return;
+    const int c = blockIdx.x * 16 + (threadIdx.x & 15), r = threadIdx.x >> 4;
+    double s = 0.0;
+    if (c < D) {
+#pragma unroll 8
+        for (int g = r; g < groups; g += 16) s += (double)part[(int64_t)g * D + c];
+    }
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (r == 0 && c < D) {
+        double x = 0.0;
+        for (int i = 0; i < 16; ++i) x += sums[i * 16 + threadIdx.x];
+        out[c] = (float)x;
+    }
+}
+
+bool all_zero_mod(const RView& v, size_t element, int w)
+{
+    return (uintptr_t)v.p % (element * w) == 0 && v.b % w == 0 && v.t % w == 0 && v.h % w == 0;
+}
+
+// Largest W whose vectors stay whole and aligned: the width in groups of W
+// channels, the rotated part in units of 2 W.
+int vector_width(const QkArgs& a, size_t element, bool grad)
+{
+    for (int w = element == 2 ? 8 : 4; w >= 4; w /= 2) {
+        bool ok = a.D % w == 0 && a.rotary % (2 * w) == 0;
+        for (int k = 0; k < 2 && ok; ++k)
+            ok = all_zero_mod(a.t[k].x, element, w) && (!grad || all_zero_mod(a.t[k].dy, element, w)) &&
+                 (uintptr_t)a.t[k].out % (element * w) == 0;
+        if (ok) return w;
+    }
+    return 1;
+}
+
+// Tokens per tile: up to 16, as few as keep about 1024 tiles.
+void shape_tiles(QkArgs& a, int64_t most_heads)
+{
+    int64_t t = a.rows / 1024;
+    const int64_t nf = a.rotary / 2 > 0 ? a.rotary / 2 : 1;
+    if (t > kQkTokens) t = kQkTokens;
+    if (t > kQkAngles / nf) t = kQkAngles / nf;
+    if (t > 65535 / most_heads) t = 65535 / most_heads;
+    if (t < 1) t = 1;
+    a.tokens = (int32_t)t;
+    a.tiles = (a.rows + t - 1) / t;
+}
+
+template <typename T, int W, int U, bool GRAD>
+hyena_status qk_launch_one(const QkArgs& a, int64_t grid, hipStream_t s)
+{
+    HY_LAUNCH(kernel_label("hyena_qk_norm_pass", type_label<T>(), W, U, GRAD), (hyena_qk_norm_pass<T, W, U, GRAD>),
+              dim3((unsigned)grid), dim3(kQkThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? HYENA_OK : fail(HYENA_ERR_DEVICE, hipGetErrorString(e));
+}
+
+template <typename T, int W, bool GRAD> hyena_status qk_launch_w(QkArgs& a, int64_t grid, hipStream_t s)
+{
+    // lanes per head: a power of two, at most a wave; more units go to a lane
+    const int units = (a.D + 2 * W - 1) / (2 * W);
+    int lanes = 1;
+    while (lanes < units && lanes < 64) lanes *= 2;
+    a.lanes = lanes;
+    const int per = (units + lanes - 1) / lanes;
+    if (per <= 1) return qk_launch_one<T, W, 1, GRAD>(a, grid, s);
+    if (per <= 2) return qk_launch_one<T, W, 2, GRAD>(a, grid, s);
+    if constexpr (W == 1) return qk_launch_one<T, W, 8, GRAD>(a, grid, s);
+    else return fail(HYENA_ERR_UNSUPPORTED, "qk norm: head width");
+}
+
+template <typename T, bool GRAD> hyena_status qk_launch(QkArgs& a, int64_t grid, hipStream_t s)
+{
+    const int w = vector_width(a, sizeof(T), GRAD);
+    if constexpr (sizeof(T) == 2)
+        if (w == 8) return qk_launch_w<T, 8, GRAD>(a, grid, s);
+    if (w == 4) return qk_launch_w<T, 4, GRAD>(a, grid, s);
+    return qk_launch_w<T, 1, GRAD>(a, grid, s);
+}
+
+hyena_status qk_refuse(const char* what) { return fail(HYENA_ERR_INVALID_ARGUMENT, std::string("qk norm: ") + what); }
+
+RView plain_view(const hyena_view& v) { return RView{v.data, v.batch, v.token, v.head, 0}; }
+
+hyena_status qk_sizes(const hyena_qk_norm* op)
+{
+    if (op == nullptr) return qk_refuse("the description is NULL");
+    if (op->B < 1 || op->N < 1 || op->q_heads < 1 || op->k_heads < 1 || op->D < 1)
+        return qk_refuse("B, N, q_heads, k_heads and D must be at least 1");
+    if (op->D > 1024) return fail(HYENA_ERR_UNSUPPORTED, "qk norm: D must be in 1..1024");
+    if (op->q_heads > 4096 || op->k_heads > 4096)
+        return fail(HYENA_ERR_UNSUPPORTED, "qk norm: at most 4096 heads");
+    if (op->B > ((int64_t)1 << 31) || op->N > ((int64_t)1 << 31) || op->B * op->N > ((int64_t)1 << 31))
+        return fail(HYENA_ERR_UNSUPPORTED, "qk norm: at most 2^31 tokens");
+    if (op->io_dtype != HYENA_F32 && op->io_dtype != HYENA_BF16 && op->io_dtype != HYENA_F16)
+        return fail(HYENA_ERR_UNSUPPORTED, "qk norm: unknown io dtype");
+    if (op->norm != HYENA_NORM_NONE && op->norm != HYENA_NORM_RMS && op->norm != HYENA_NORM_L2)
+        return fail(HYENA_ERR_UNSUPPORTED, "qk norm: unknown norm");
+    if (op->layout != HYENA_ROTARY_HALF && op->layout != HYENA_ROTARY_INTERLEAVED)
+        return fail(HYENA_ERR_UNSUPPORTED, "qk norm: unknown layout");
+    if (op->rotary_dim < 0 || op->rotary_dim > op->D || op->rotary_dim % 2 != 0)
+        return qk_refuse("rotary_dim must be even and in 0..D");
+    if (op->rotary_dim > 0 && op->freqs == nullptr) return qk_refuse("freqs is NULL");
+    if (!(op->eps >= 0.0f)) return qk_refuse("eps must be at least 0");
+    return HYENA_OK;
+}
+
+// Checks and kernel arguments shared by both directions; ins: 7 spans.
+hyena_status qk_args(const hyena_qk_norm* op, void* q_out, void* k_out, QkArgs& a, Span* ins, Span* outs)
+{
+    hyena_status st = qk_sizes(op);
+    if (st != HYENA_OK) return st;
+    const size_t e = element_bytes(op->io_dtype);
+    if ((st = check_view(op->q, "q", e)) != HYENA_OK || (st = check_view(op->k, "k", e)) != HYENA_OK) return st;
+    if (q_out == nullptr || k_out == nullptr) return qk_refuse("an output pointer is NULL");
+    if ((uintptr_t)q_out % 16 != 0 || (uintptr_t)k_out % 16 != 0) return qk_refuse("outputs must be 16-byte aligned");
+    if ((uintptr_t)op->freqs % 8 != 0 || (uintptr_t)op->q_weight % 4 != 0 || (uintptr_t)op->k_weight % 4 != 0 ||
+        (uintptr_t)op->positions % 4 != 0)
+        return qk_refuse("freqs, a weight or positions is not aligned to its element");
+    const size_t rows = (size_t)(op->B * op->N);
+    ins[0] = view_span(op->q, op->B, op->N, op->q_heads, op->D, e);
+    ins[1] = view_span(op->k, op->B, op->N, op->k_heads, op->D, e);
+    ins[2] = Span{op->freqs, (size_t)op->rotary_dim / 2 * 8};
+    ins[3] = Span{op->q_weight, (size_t)op->D * 4};
+    ins[4] = Span{op->k_weight, (size_t)op->D * 4};
+    ins[5] = Span{op->positions, rows * 4};
+    outs[0] = Span{q_out, rows * (size_t)(op->q_heads * op->D) * e};
+    outs[1] = Span{k_out, rows * (size_t)(op->k_heads * op->D) * e};
+
+    a = QkArgs{};
+    a.t[0].x = plain_view(op->q);
+    a.t[1].x = plain_view(op->k);
+    a.t[0].out = q_out;
+    a.t[1].out = k_out;
+    a.t[0].w = op->norm == HYENA_NORM_NONE ? nullptr : op->q_weight;
+    a.t[1].w = op->norm == HYENA_NORM_NONE ? nullptr : op->k_weight;
+    a.t[0].heads = (int32_t)op->q_heads;
+    a.t[1].heads = (int32_t)op->k_heads;
+    for (int k = 0; k < 2; ++k)
+        a.t[k].magic = (uint32_t)((((uint64_t)1 << 32) + (uint64_t)a.t[k].heads - 1) / (uint64_t)a.t[k].heads);
+    a.freqs = op->freqs;
+    a.positions = op->positions;
+    a.offset = op->position_offset;
+    a.N = op->N;
+    a.rows = op->B * op->N;
+    a.D = (int32_t)op->D;
+    a.rotary = (int32_t)op->rotary_dim;
+    a.half = op->layout == HYENA_ROTARY_HALF;
+    a.norm = op->norm;
+    a.mean = op->norm == HYENA_NORM_RMS ? 1.0f / (float)op->D : 1.0f;
+    a.eps = op->eps;
+    a.rscale = op->rotary_scale;
+    shape_tiles(a, op->q_heads > op->k_heads ? op->q_heads : op->k_heads);
+    return HYENA_OK;
+}
+
+hyena_status qk_overlaps(const Span* ins, int nin, const Span* outs, int nout)
+{
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (spans_overlap(outs[i], ins[j])) return qk_refuse("an output overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (spans_overlap(outs[i], outs[j])) return qk_refuse("two outputs overlap");
+    }
+    return HYENA_OK;
+}
+
+int64_t grad_groups(const QkArgs& a) { return a.tiles < kQkGradGroups ? a.tiles : kQkGradGroups; }
+
+size_t part_bytes(int64_t groups, int64_t D) { return ((size_t)groups * (size_t)D * 4 + 255) & ~(size_t)255; }
+
+template <bool GRAD> hyena_status qk_by_type(int32_t io_dtype, QkArgs& a, int64_t grid, hipStream_t s)
+{
+    if (io_dtype == HYENA_F32) return qk_launch<float, GRAD>(a, grid, s);
+    if (io_dtype == HYENA_BF16) return qk_launch<uint16_t, GRAD>(a, grid, s);
+    return qk_launch<_Float16, GRAD>(a, grid, s);
+}
+
+}  // namespace
+}  // namespace hy
+
+using namespace hy;
+
+extern "C" {
+
+hyena_status hyena_qk_norm_forward(const hyena_qk_norm* op, void* q_out, void* k_out, void* stream)
+{
+    QkArgs a;
+    Span ins[6], outs[2];
+    hyena_status st = qk_args(op, q_out, k_out, a, ins, outs);
+    if (st != HYENA_OK) return st;
+    if ((st = qk_overlaps(ins, 6, outs, 2)) != HYENA_OK) return st;
+    return qk_by_type<false>(op->io_dtype, a, a.tiles, (hipStream_t)stream);
+}
+
+hyena_status hyena_qk_norm_scratch_bytes(const hyena_qk_norm* op, size_t* bytes)
+{
+    const hyena_status st = qk_sizes(op);
+    if (st != HYENA_OK) return st;
+    if (bytes == nullptr) return qk_refuse("bytes is NULL");
+    QkArgs a{};
+    a.rows = op->B * op->N;
+    a.rotary = (int32_t)op->rotary_dim;
+    shape_tiles(a, op->q_heads > op->k_heads ? op->q_heads : op->k_heads);
+    *bytes = 2 * part_bytes(grad_groups(a), op->D);
+    return HYENA_OK;
+}
+
+hyena_status hyena_qk_norm_backward(const hyena_qk_norm* op, const hyena_view* dq_out, const hyena_view* dk_out,
+                                    void* dq, void* dk, float* dq_weight, float* dk_weight, void* scratch,
+                                    void* stream)
+{
+    QkArgs a;
+    Span ins[8], outs[5];
+    hyena_status st = qk_args(op, dq, dk, a, ins, outs);
+    if (st != HYENA_OK) return st;
+    if (dq_out == nullptr || dk_out == nullptr) return qk_refuse("a gradient view is NULL");
+    const size_t e = element_bytes(op->io_dtype);
+    if ((st = check_view(*dq_out, "dq_out", e)) != HYENA_OK || (st = check_view(*dk_out, "dk_out", e)) != HYENA_OK)
+        return st;
+    ins[6] = view_span(*dq_out, op->B, op->N, op->q_heads, op->D, e);
+    ins[7] = view_span(*dk_out, op->B, op->N, op->k_heads, op->D, e);
+    if ((uintptr_t)dq_weight % 4 != 0 || (uintptr_t)dk_weight % 4 != 0)
+        return qk_refuse("a weight's gradient is not aligned to its element");
+    const bool weights = op->norm != HYENA_NORM_NONE && (dq_weight || dk_weight);
+    if (op->norm == HYENA_NORM_NONE && (dq_weight || dk_weight)) return qk_refuse("no norm, so no weights' gradients");
+    if (weights && (scratch == nullptr || (uintptr_t)scratch % 16 != 0))
+        return qk_refuse("scratch is NULL or not 16-byte aligned");
+    const int64_t groups = grad_groups(a);
+    const size_t part = part_bytes(groups, op->D);
+    outs[2] = Span{dq_weight, (size_t)op->D * 4};
+    outs[3] = Span{dk_weight, (size_t)op->D * 4};
+    outs[4] = Span{weights ? scratch : nullptr, 2 * part};
+    if ((st = qk_overlaps(ins, 8, outs, 5)) != HYENA_OK) return st;
+    a.t[0].dy = plain_view(*dq_out);
+    a.t[1].dy = plain_view(*dk_out);
+    a.t[0].dw_part = dq_weight ? (float*)scratch : nullptr;
+    a.t[1].dw_part = dk_weight ? (float*)((char*)scratch + part) : nullptr;
+    const hipStream_t s = (hipStream_t)stream;
+    if ((st = qk_by_type<true>(op->io_dtype, a, groups, s)) != HYENA_OK) return st;
+    if (!weights) return HYENA_OK;
+    HY_LAUNCH(kernel_label("hyena_qk_weight_grad"), hyena_qk_weight_grad, dim3((unsigned)((a.D + 15) / 16), 2), dim3(256),
+              0, s, a.t[0].dw_part, a.t[1].dw_part, dq_weight, dk_weight, (int)groups, a.D);
+    const hipError_t err = hipGetLastError();
+    return err == hipSuccess ? HYENA_OK : fail(HYENA_ERR_DEVICE, hipGetErrorString(err));
+}
+
+}  // extern "C"

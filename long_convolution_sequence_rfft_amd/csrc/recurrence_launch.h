@@ -1,0 +1,82 @@
+// recurrence_launch.h -- instantiates the recurrence's kernels for one storage
+// type: head widths are padded to 64 or 128 channels.
+#pragma once
+
+#include "recurrence_kernels.h"
+
+namespace hy {
+
+inline hyena_status rec_done()
+{
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? HYENA_OK : fail(HYENA_ERR_DEVICE, hipGetErrorString(e));
+}
+
+template <typename T, int DK, int DV>
+hyena_status rec_states_one(const RecStateArgs& a, int64_t bh, int roles, hipStream_t s)
+{
+    HY_LAUNCH(kernel_label("hyena_rec_states", type_label<T>(), DK, DV), (hyena_rec_states<T, DK, DV>),
+              dim3((unsigned)(bh * a.nseg), (unsigned)roles), dim3(256), 0, s, a);
+    return rec_done();
+}
+
+template <typename T> hyena_status rec_launch_states(const RecStateArgs& a, int64_t bh, int roles, hipStream_t s)
+{
+    if (a.dk <= 64) return a.dv <= 64 ? rec_states_one<T, 64, 64>(a, bh, roles, s) : rec_states_one<T, 64, 128>(a, bh, roles, s);
+    return a.dv <= 64 ? rec_states_one<T, 128, 64>(a, bh, roles, s) : rec_states_one<T, 128, 128>(a, bh, roles, s);
+}
+
+template <typename T, int DA, int DC, bool TRANS>
+hyena_status rec_out_one(const RecArgs& a, int64_t bh, hipStream_t s)
+{
+    HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS), (hyena_rec_out<T, DA, DC, TRANS>),
+              dim3((unsigned)(bh * a.nseg)), dim3(256), 0, s, a);
+    return rec_done();
+}
+
+template <typename T, bool TRANS> hyena_status rec_out_pick(const RecArgs& a, int64_t bh, hipStream_t s)
+{
+    if (a.da <= 64) return a.dc <= 64 ? rec_out_one<T, 64, 64, TRANS>(a, bh, s) : rec_out_one<T, 64, 128, TRANS>(a, bh, s);
+    return a.dc <= 64 ? rec_out_one<T, 128, 64, TRANS>(a, bh, s) : rec_out_one<T, 128, 128, TRANS>(a, bh, s);
+}
+
+template <typename T> hyena_status rec_launch_out(const RecArgs& a, int64_t bh, bool transposed, hipStream_t s)
+{
+    return transposed ? rec_out_pick<T, true>(a, bh, s) : rec_out_pick<T, false>(a, bh, s);
+}
+
+template <typename T, int DK, int DV> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
+{
+    HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), DK, DV), (hyena_rec_grad<T, DK, DV>),
+              dim3((unsigned)(bh * a.nseg)), dim3(512), 0, s, a);
+    return rec_done();
+}
+
+template <typename T> hyena_status rec_launch_grad(const RecGradArgs& a, int64_t bh, hipStream_t s)
+{
+    if (a.dk <= 64) return a.dv <= 64 ? rec_grad_one<T, 64, 64>(a, bh, s) : rec_grad_one<T, 64, 128>(a, bh, s);
+    return a.dv <= 64 ? rec_grad_one<T, 128, 64>(a, bh, s) : rec_grad_one<T, 128, 128>(a, bh, s);
+}
+
+template <typename T> hyena_status rec_launch_step(const RecStepArgs& a, int64_t B, hipStream_t s)
+{
+    const bool vec = a.dv % 4 == 0 && ((uintptr_t)a.states & 15) == 0;
+    if (vec) {
+        HY_LAUNCH(kernel_label("hyena_rec_step", type_label<T>(), 4), (hyena_rec_step<T, 4>),
+                  dim3((unsigned)(B * a.heads)), dim3(256), 0, s, a);
+    } else {
+        HY_LAUNCH(kernel_label("hyena_rec_step", type_label<T>(), 1), (hyena_rec_step<T, 1>),
+                  dim3((unsigned)(B * a.heads)), dim3(256), 0, s, a);
+    }
+    return rec_done();
+}
+
+}  // namespace hy
+
+#define HY_REC_INSTANTIATE(T)                                                                        \
+    namespace hy {                                                                                   \
+    template hyena_status rec_launch_states<T>(const RecStateArgs&, int64_t, int, hipStream_t);      \
+    template hyena_status rec_launch_out<T>(const RecArgs&, int64_t, bool, hipStream_t);             \
+    template hyena_status rec_launch_grad<T>(const RecGradArgs&, int64_t, hipStream_t);              \
+    template hyena_status rec_launch_step<T>(const RecStepArgs&, int64_t, hipStream_t);              \
+    }

@@ -1,0 +1,53 @@
+// recurrence_plan.h -- the gated linear recurrence's plan, and checks of strided
+// views (pure host code, no HIP).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "hyena.h"
+
+namespace hy {
+
+// Workgroups that the cut into segments aims at: four (two) for each of the
+// 256 compute units.
+constexpr int64_t kRecForwardGroups = 1024;
+constexpr int64_t kRecBackwardGroups = 512;
+
+struct RecPlan {
+    int64_t B = 0, N = 0, heads = 0;
+    int32_t dk = 0, dv = 0;
+    int32_t io_dtype = HYENA_F32;
+    // The sequence is cut into nseg segments of seg tokens (a multiple of 64)
+    // that run in parallel; nseg_b, seg_b: the backward pass's own cut.
+    int32_t seg = 0, nseg = 0;
+    int32_t seg_b = 0, nseg_b = 0;
+    size_t forward_bytes = 0, backward_bytes = 0;
+};
+
+// Workspace, all float32.  start: [B heads][nseg + 1][dk dv] states before each
+// segment (the last entry: the final state); decay [B heads][nseg].  Backward
+// also end: gradients of the states after each segment (entry 0: of the initial
+// state), and rq [B heads][N].
+struct RecSpace {
+    float* start = nullptr;
+    float* end = nullptr;
+    float* decay = nullptr;
+    float* rq = nullptr;
+};
+
+hyena_status rec_plan_build(RecPlan& p, int64_t B, int64_t N, int64_t heads, int64_t dk, int64_t dv,
+                            int32_t io_dtype);
+RecSpace rec_space(const RecPlan& p, bool backward, void* workspace);
+
+inline size_t element_bytes(int32_t io_dtype) { return io_dtype == HYENA_F32 ? 4 : 2; }
+
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+hyena_status check_view(const hyena_view& v, const char* name, size_t element);
+Span view_span(const hyena_view& v, int64_t B, int64_t N, int64_t heads, int64_t width, size_t element);
+bool spans_overlap(const Span& a, const Span& b);
+
+}  // namespace hy

@@ -9,6 +9,7 @@ There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -40,6 +41,9 @@ EXPORTED_SYMBOLS = (
     "hyena_plan_create_ex", "hyena_nd_mixer_forward", "hyena_workspace_release",
     "hyena_plan_path",
     "hyena_forward_noalloc",
+    "hyena_recurrence_create", "hyena_recurrence_query", "hyena_recurrence_forward",
+    "hyena_recurrence_backward", "hyena_recurrence_step", "hyena_recurrence_destroy",
+    "hyena_qk_norm_forward", "hyena_qk_norm_scratch_bytes", "hyena_qk_norm_backward",
 )
 
 HYENA_NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -60,6 +64,42 @@ class ImplicitFilter(ctypes.Structure):
                 ("omega", ctypes.c_float), ("W1", ctypes.c_void_p), ("b1", ctypes.c_void_p),
                 ("W2", ctypes.c_void_p), ("b2", ctypes.c_void_p), ("W3", ctypes.c_void_p),
                 ("b3", ctypes.c_void_p), ("alpha", ctypes.c_void_p)]
+
+
+HYENA_NORM_NONE = 0
+HYENA_NORM_RMS = 1
+HYENA_NORM_L2 = 2
+HYENA_ROTARY_HALF = 0
+HYENA_ROTARY_INTERLEAVED = 1
+
+
+class View(ctypes.Structure):
+    """hyena_view: a [B, N, heads, width] tensor seen through element strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
+class RecurrenceInputs(ctypes.Structure):
+    """hyena_recurrence_inputs (device pointers as ints; see include/hyena.h)."""
+    _fields_ = [("q", View), ("k", View), ("v", View), ("g", View), ("state", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class RecurrenceGrads(ctypes.Structure):
+    """hyena_recurrence_grads."""
+    _fields_ = [("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p),
+                ("dg", ctypes.c_void_p), ("d_state", ctypes.c_void_p)]
+
+
+class QkNorm(ctypes.Structure):
+    """hyena_qk_norm: norms of queries and keys with the position rotation."""
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+                ("k_heads", ctypes.c_int64), ("D", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("rotary_scale", ctypes.c_float),
+                ("freqs", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("position_offset", ctypes.c_int64), ("q", View), ("k", View)]
 
 _lock = threading.Lock()
 _lib = None
@@ -109,6 +149,17 @@ def load():
             lib.hyena_nd_mixer_forward.argtypes = [p, ctypes.POINTER(NdMixer), p, p, p, p, p]
             lib.hyena_filter_spectrum_implicit.argtypes = [p, ctypes.POINTER(ImplicitFilter), p, p,
                                                            p, p]
+            pin, pout = ctypes.POINTER(RecurrenceInputs), ctypes.POINTER(RecurrenceGrads)
+            pview, pqk = ctypes.POINTER(View), ctypes.POINTER(QkNorm)
+            lib.hyena_recurrence_create.argtypes = [ctypes.POINTER(p), i64, i64, i64, i64, i64, i32]
+            lib.hyena_recurrence_query.argtypes = [p, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+            lib.hyena_recurrence_forward.argtypes = [p, pin, p, p, p, p]
+            lib.hyena_recurrence_backward.argtypes = [p, pin, pview, p, pout, p, p]
+            lib.hyena_recurrence_step.argtypes = [p, pin, p, i64, p, p, p]
+            lib.hyena_recurrence_destroy.argtypes = [p]
+            lib.hyena_qk_norm_forward.argtypes = [pqk, p, p, p]
+            lib.hyena_qk_norm_scratch_bytes.argtypes = [pqk, ctypes.POINTER(sz)]
+            lib.hyena_qk_norm_backward.argtypes = [pqk, pview, pview] + [p] * 6
             for name in ("hyena_plan_create", "hyena_plan_create_ex", "hyena_plan_query",
                          "hyena_plan_path",
                          "hyena_workspace_init", "hyena_workspace_release",
@@ -117,7 +168,11 @@ def load():
                          "hyena_plan_destroy", "hyena_timing_begin", "hyena_timing_end",
                          "hyena_timing_kernel", "hyena_timing_release",
                          "hyena_implicit_scratch_bytes", "hyena_filter_spectrum_implicit",
-                         "hyena_nd_mixer_forward"):
+                         "hyena_nd_mixer_forward", "hyena_recurrence_create",
+                         "hyena_recurrence_query", "hyena_recurrence_forward",
+                         "hyena_recurrence_backward", "hyena_recurrence_step",
+                         "hyena_recurrence_destroy", "hyena_qk_norm_forward",
+                         "hyena_qk_norm_scratch_bytes", "hyena_qk_norm_backward"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -247,6 +302,61 @@ def hyena_timing_end():
 
 def hyena_timing_release():
     _check(load().hyena_timing_release(), "hyena_timing_release")
+
+
+def _ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def hyena_recurrence_create(B, N, heads, dk, dv, io_dtype=HYENA_F32, check=True):
+    """Returns (status, plan handle or None)."""
+    h = ctypes.c_void_p()
+    st = load().hyena_recurrence_create(ctypes.byref(h), int(B), int(N), int(heads), int(dk), int(dv),
+                                        int(io_dtype))
+    if check:
+        _check(st, "hyena_recurrence_create")
+    return st, (h.value if st == HYENA_OK else None)
+
+
+def hyena_recurrence_query(plan):
+    """Returns (forward, backward) workspace bytes."""
+    fwd, bwd = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().hyena_recurrence_query(plan, ctypes.byref(fwd), ctypes.byref(bwd)),
+           "hyena_recurrence_query")
+    return fwd.value, bwd.value
+
+
+def hyena_recurrence_forward(plan, inputs, o, final_state, workspace, stream=0):
+    return load().hyena_recurrence_forward(plan, _ref(inputs), o, final_state, workspace, stream)
+
+
+def hyena_recurrence_backward(plan, inputs, d_o, d_final, grads, workspace, stream=0):
+    return load().hyena_recurrence_backward(plan, _ref(inputs), _ref(d_o), d_final, _ref(grads),
+                                            workspace, stream)
+
+
+def hyena_recurrence_step(plan, inputs, slots, n_slots, states, o, stream=0):
+    return load().hyena_recurrence_step(plan, _ref(inputs), slots, int(n_slots), states, o, stream)
+
+
+def hyena_recurrence_destroy(plan):
+    return load().hyena_recurrence_destroy(plan)
+
+
+def hyena_qk_norm_forward(op, q_out, k_out, stream=0):
+    return load().hyena_qk_norm_forward(_ref(op), q_out, k_out, stream)
+
+
+def hyena_qk_norm_scratch_bytes(op):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t()
+    st = load().hyena_qk_norm_scratch_bytes(_ref(op), ctypes.byref(n))
+    return st, n.value
+
+
+def hyena_qk_norm_backward(op, dq_out, dk_out, dq, dk, dq_weight, dk_weight, scratch, stream=0):
+    return load().hyena_qk_norm_backward(_ref(op), _ref(dq_out), _ref(dk_out), dq, dk, dq_weight,
+                                         dk_weight, scratch, stream)
 
 
 # --------------------------------------------------------------------------
@@ -452,3 +562,270 @@ class Plan:
                 self.handle = None
         except Exception:
             pass
+
+
+class _Mixer:
+    """Checks and stream plumbing shared by the operators on q, k and v."""
+
+    def _place(self, io_dtype, device):
+        import torch
+        self.torch = torch
+        dtypes = {HYENA_F32: torch.float32, HYENA_BF16: torch.bfloat16, HYENA_F16: torch.float16}
+        if io_dtype not in dtypes:
+            raise ValueError(f"unknown io dtype {io_dtype}")
+        self.io_dtype, self.dtype = io_dtype, dtypes[io_dtype]
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError(f"the device must be a GPU, got {dev}")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+
+    def _stream(self):
+        return self.torch.cuda.current_stream(self.device).cuda_stream
+
+    def _on_device(self):
+        # launches go to the current device; a plan of another one makes its own current
+        cuda = self.torch.cuda
+        if cuda.current_device() == self.device.index:
+            return contextlib.nullcontext()
+        return cuda.device(self.device)
+
+    def _keep(self, buffer):
+        """The buffer the plan owns may be used on a stream other than the one
+        it was allocated on: its memory is not given out again before that
+        stream's work is done."""
+        if buffer is None:
+            return None
+        buffer.record_stream(self.torch.cuda.current_stream(self.device))
+        return buffer.data_ptr()
+
+    def _check_tensor(self, t, name, shape, dtype):
+        if not isinstance(t, self.torch.Tensor):
+            raise ValueError(f"{name} must be a torch tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+    def _dense(self, t, name, shape, dtype):
+        """Address of a contiguous tensor; None stays None."""
+        if t is None:
+            return None
+        self._check_tensor(t, name, shape, dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def _view(self, t, name, shape, dtype):
+        """A [B, N, heads, width] or [B, N, heads] tensor as a View."""
+        self._check_tensor(t, name, shape, dtype)
+        st = list(t.stride())
+        if len(shape) == 4 and shape[3] > 1 and st[3] != 1:
+            raise ValueError(f"the last axis of {name} must be contiguous")
+        # torch gives axes of one element any stride
+        st = [0 if n == 1 else s for n, s in zip(shape, st)]
+        return View(t.data_ptr(), st[0], st[1], st[2])
+
+    def _out(self, out, name, shape, dtype):
+        if out is None:
+            out = self.torch.empty(shape, dtype=dtype, device=self.device)
+        self._dense(out, name, shape, dtype)
+        return out
+
+
+class Recurrence(_Mixer):
+    """Gated linear recurrence S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t
+    for rows of N tokens (see include/hyena.h for shapes, masks and precision).
+
+    q, k: [B, N, heads, dk], v: [B, N, heads, dv] in the io dtype, g: float32
+    [B, N, heads] (log decays); views are taken as they are as long as the last
+    axis of q, k and v is contiguous.  States are float32 [B, heads, dk, dv].
+    ``training`` allocates the backward pass's workspace.  Calls of one plan
+    share its workspace and must not run concurrently on different streams.
+    """
+
+    def __init__(self, B, N, heads, dk, dv, io_dtype=HYENA_F32, training=False, device="cuda"):
+        self._place(io_dtype, device)
+        self.B, self.N, self.heads, self.dk, self.dv = (int(x) for x in (B, N, heads, dk, dv))
+        _, self.handle = hyena_recurrence_create(B, N, heads, dk, dv, io_dtype)
+        self.forward_bytes, self.backward_bytes = hyena_recurrence_query(self.handle)
+        self.training = bool(training)
+        n = max(self.forward_bytes, self.backward_bytes if training else 0)
+        self.workspace = self.torch.empty(n, dtype=self.torch.uint8, device=self.device) if n else None
+
+    @property
+    def state_shape(self):
+        return (self.B, self.heads, self.dk, self.dv)
+
+    def _inputs(self, q, k, v, g, scale, state=None, lengths=None):
+        torch = self.torch
+        rows = (self.B, self.N, self.heads)
+        return RecurrenceInputs(
+            self._view(q, "q", rows + (self.dk,), self.dtype), self._view(k, "k", rows + (self.dk,), self.dtype),
+            self._view(v, "v", rows + (self.dv,), self.dtype), self._view(g, "g", rows, torch.float32),
+            self._dense(state, "state", self.state_shape, torch.float32),
+            self._dense(lengths, "lengths", (self.B,), torch.int32),
+            float(self.dk ** -0.5 if scale is None else scale))
+
+    def forward(self, q, k, v, g, scale=None, state=None, lengths=None, return_state=False, o=None,
+                final_state=None):
+        """(o, final state or None).  scale: 1 / sqrt(dk) by default.  state: the state before
+        token 0.  lengths: int32 [B], tokens per row (the others' o is 0)."""
+        torch = self.torch
+        x = self._inputs(q, k, v, g, scale, state, lengths)
+        o = self._out(o, "o", (self.B, self.N, self.heads, self.dv), self.dtype)
+        if return_state or final_state is not None:
+            final_state = self._out(final_state, "final_state", self.state_shape, torch.float32)
+        with self._on_device():
+            _check(hyena_recurrence_forward(self.handle, x, o.data_ptr(),
+                                            final_state.data_ptr() if final_state is not None else None,
+                                            self._keep(self.workspace), self._stream()),
+                   "hyena_recurrence_forward")
+        return o, final_state
+
+    def backward(self, d_o, q, k, v, g, scale=None, state=None, lengths=None, d_final=None):
+        """(dq, dk, dv, dg, d_state) from the gradients of o and (or None) of the final state;
+        d_state is None without a state."""
+        torch = self.torch
+        if not self.training:
+            raise ValueError("backward needs a plan made with training=True")
+        x = self._inputs(q, k, v, g, scale, state, lengths)
+        rows = (self.B, self.N, self.heads)
+        d = self._view(d_o, "d_o", rows + (self.dv,), self.dtype)
+        df = self._dense(d_final, "d_final", self.state_shape, torch.float32)
+        new = lambda *s, dt=self.dtype: torch.empty(s, dtype=dt, device=self.device)  # noqa: E731
+        dq, dk, dv = new(*rows, self.dk), new(*rows, self.dk), new(*rows, self.dv)
+        dg = new(*rows, dt=torch.float32)
+        ds = new(*self.state_shape, dt=torch.float32) if state is not None else None
+        grads = RecurrenceGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
+                                ds.data_ptr() if ds is not None else None)
+        with self._on_device():
+            _check(hyena_recurrence_backward(self.handle, x, d, df, grads, self._keep(self.workspace),
+                                             self._stream()),
+                   "hyena_recurrence_backward")
+        return dq, dk, dv, dg, ds
+
+    def step(self, q, k, v, g, states, scale=None, slots=None, o=None):
+        """One token per row: q, k [B, heads, dk], v [B, heads, dv], g [B, heads].  Updates
+        states[slots] (float32 [n, heads, dk, dv], slots int32 [B], row b by default) in place and
+        returns o [B, heads, dv].  Rows with a slot outside the table take no part (o = 0); the
+        other slots have to differ."""
+        torch = self.torch
+        rows = (self.B, 1, self.heads)
+        up = lambda t: t.unsqueeze(1) if isinstance(t, torch.Tensor) and t.dim() > 0 else t  # noqa: E731
+        x = RecurrenceInputs(
+            self._view(up(q), "q", rows + (self.dk,), self.dtype), self._view(up(k), "k", rows + (self.dk,), self.dtype),
+            self._view(up(v), "v", rows + (self.dv,), self.dtype), self._view(up(g), "g", rows, torch.float32),
+            None, None, float(self.dk ** -0.5 if scale is None else scale))
+        n = int(states.shape[0]) if isinstance(states, torch.Tensor) and states.dim() == 4 else 0
+        table = self._dense(states, "states", (n, self.heads, self.dk, self.dv), torch.float32)
+        if table is None:
+            raise ValueError("states must be a torch tensor")
+        at = self._dense(slots, "slots", (self.B,), torch.int32)
+        o = self._out(o, "o", (self.B, self.heads, self.dv), self.dtype)
+        with self._on_device():
+            _check(hyena_recurrence_step(self.handle, x, at, n, table, o.data_ptr(), self._stream()),
+                   "hyena_recurrence_step")
+        return o
+
+    def __del__(self):
+        try:
+            if getattr(self, "handle", None):
+                hyena_recurrence_destroy(self.handle)
+                self.handle = None
+        except Exception:
+            pass
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, stretch=1.0, device="cuda"):
+    """float64 [rotary_dim / 2]: base^(-2 i / rotary_dim) / stretch.  stretch > 1 spreads the
+    positions of a longer context over the trained range; any other scaling is a table of the
+    caller's own."""
+    import torch
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    return base ** (-i / max(rotary_dim, 1)) / stretch
+
+
+class QKNorm(_Mixer):
+    """Norms of queries and keys per head with the position rotation in the same pass.
+
+    q: [B, N, q_heads, D], k: [B, N, k_heads, D] in the io dtype (views; the last axis
+    contiguous); norm "rms", "l2" or "none"; weights float32 [D] or None.  The first
+    ``rotary_dim`` channels are rotated (D by default, 0: none), pairs (i, i + rotary_dim / 2)
+    in the "half" layout and (2i, 2i + 1) in the "interleaved" one, by position * freqs[i]
+    (float64, by default ``rotary_frequencies(rotary_dim)``); sines and cosines are multiplied
+    by ``rotary_scale``.
+    """
+
+    _NORMS = {"none": HYENA_NORM_NONE, "rms": HYENA_NORM_RMS, "l2": HYENA_NORM_L2}
+    _LAYOUTS = {"half": HYENA_ROTARY_HALF, "interleaved": HYENA_ROTARY_INTERLEAVED}
+
+    def __init__(self, B, N, q_heads, k_heads, D, io_dtype=HYENA_F32, norm="rms", rotary_dim=None,
+                 layout="half", eps=1e-6, freqs=None, rotary_scale=1.0, device="cuda"):
+        self._place(io_dtype, device)
+        if norm not in self._NORMS:
+            raise ValueError(f"norm must be one of {sorted(self._NORMS)}, got {norm!r}")
+        if layout not in self._LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(self._LAYOUTS)}, got {layout!r}")
+        self.B, self.N, self.q_heads, self.k_heads, self.D = (int(x) for x in (B, N, q_heads, k_heads, D))
+        self.rotary_dim = int(D if rotary_dim is None else rotary_dim)
+        if self.rotary_dim % 2 or not 0 <= self.rotary_dim <= self.D:
+            raise ValueError(f"rotary_dim must be even and in 0..{self.D}, got {self.rotary_dim}")
+        if freqs is None:
+            freqs = rotary_frequencies(self.rotary_dim, device=self.device)
+        self._dense(freqs, "freqs", (self.rotary_dim // 2,), self.torch.float64)
+        self.norm, self.layout, self.eps, self.freqs = norm, layout, float(eps), freqs
+        self.rotary_scale = float(rotary_scale)
+        st, n = hyena_qk_norm_scratch_bytes(self._op(View(), View()))
+        _check(st, "hyena_qk_norm_scratch_bytes")
+        self.scratch_bytes = n
+
+    def _op(self, q, k, q_weight=None, k_weight=None, positions=None, offset=0):
+        return QkNorm(self.B, self.N, self.q_heads, self.k_heads, self.D, self.io_dtype,
+                      self._NORMS[self.norm], self._LAYOUTS[self.layout], self.rotary_dim, self.eps,
+                      self.rotary_scale, self.freqs.data_ptr() if self.rotary_dim else None,
+                      q_weight, k_weight, positions, int(offset), q, k)
+
+    def _describe(self, q, k, q_weight, k_weight, positions, offset):
+        torch = self.torch
+        return self._op(self._view(q, "q", (self.B, self.N, self.q_heads, self.D), self.dtype),
+                        self._view(k, "k", (self.B, self.N, self.k_heads, self.D), self.dtype),
+                        self._dense(q_weight, "q_weight", (self.D,), torch.float32),
+                        self._dense(k_weight, "k_weight", (self.D,), torch.float32),
+                        self._dense(positions, "positions", (self.B, self.N), torch.int32), offset)
+
+    def forward(self, q, k, q_weight=None, k_weight=None, positions=None, offset=0, q_out=None,
+                k_out=None):
+        """(normed and rotated q, k), dense.  positions: int32 [B, N], or token n is at
+        offset + n."""
+        op = self._describe(q, k, q_weight, k_weight, positions, offset)
+        q_out = self._out(q_out, "q_out", (self.B, self.N, self.q_heads, self.D), self.dtype)
+        k_out = self._out(k_out, "k_out", (self.B, self.N, self.k_heads, self.D), self.dtype)
+        self._keep(self.freqs)
+        with self._on_device():
+            _check(hyena_qk_norm_forward(op, q_out.data_ptr(), k_out.data_ptr(), self._stream()),
+                   "hyena_qk_norm_forward")
+        return q_out, k_out
+
+    def backward(self, dq_out, dk_out, q, k, q_weight=None, k_weight=None, positions=None, offset=0):
+        """(dq, dk, dq_weight, dk_weight) from the gradients of forward's outputs; a weight that is
+        None has no gradient."""
+        torch = self.torch
+        op = self._describe(q, k, q_weight, k_weight, positions, offset)
+        dqo = self._view(dq_out, "dq_out", (self.B, self.N, self.q_heads, self.D), self.dtype)
+        dko = self._view(dk_out, "dk_out", (self.B, self.N, self.k_heads, self.D), self.dtype)
+        dq = self._out(None, "dq", (self.B, self.N, self.q_heads, self.D), self.dtype)
+        dk = self._out(None, "dk", (self.B, self.N, self.k_heads, self.D), self.dtype)
+        has = [w is not None and self.norm != "none" for w in (q_weight, k_weight)]
+        dqw, dkw = (torch.empty(self.D, dtype=torch.float32, device=self.device) if h else None for h in has)
+        scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=self.device) if any(has) else None
+        self._keep(self.freqs)
+        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        with self._on_device():
+            _check(hyena_qk_norm_backward(op, dqo, dko, dq.data_ptr(), dk.data_ptr(), ptr(dqw), ptr(dkw),
+                                          ptr(scratch), self._stream()),
+                   "hyena_qk_norm_backward")
+        return dq, dk, dqw, dkw
