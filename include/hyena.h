@@ -355,8 +355,9 @@ typedef struct hyena_recurrence_s* hyena_recurrence_t;
 
 /*
  * Create a recurrence plan: B >= 1 rows of up to N >= 1 tokens (N below 2^31),
- * heads >= 1, 1 <= dk, dv <= 128, B * heads at most 2^24.  Touches no GPU
- * state.  Release with hyena_recurrence_destroy.
+ * 1 <= heads <= 65536, 1 <= dk, dv <= 128, B * heads at most 2^24.  Touches no
+ * GPU state.  Release with hyena_recurrence_destroy.  The token strides of a
+ * recurrence's views are below 2^23 elements (any where N = 1).
  */
 hyena_status hyena_recurrence_create(hyena_recurrence_t* plan, int64_t B, int64_t N,
                                      int64_t heads, int64_t dk, int64_t dv, int32_t io_dtype);

@@ -15,29 +15,38 @@ namespace hy {
 
 // The states before the segments (role 0: S <- decay S + local, first to last)
 // and the gradients after them (role 1: the same backwards), in place of the
-// local sums; one thread per element.
+// local sums; one thread per element.  Local sums are read kScanBatch segments
+// at a time, ahead of the stores that a compiler cannot tell apart from them:
+// what bounds this kernel is the latency of its chain of loads.
+constexpr int kScanBatch = 16;
+
 __global__ __launch_bounds__(256) void hyena_rec_scan(RecScanArgs p)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= p.total) return;
     const int role = blockIdx.y;
     const int64_t bh = i / p.per, e = i % p.per;
-    float* x = p.local[role] + bh * (p.nseg + 1) * p.per + e;
-    const float* d = p.decay + bh * p.nseg;
+    // entry n of role 0 goes to n + 1; role 1 counts entries and segments from the last
+    const int64_t step = role ? -p.per : p.per;
+    float* x = p.local[role] + bh * (p.nseg + 1) * p.per + e + (role ? p.nseg * p.per : 0);
+    const float* d = p.decay + bh * p.nseg + (role ? p.nseg - 1 : 0);
+    const int dstep = role ? -1 : 1;
     float s = p.first[role] ? p.first[role][i] : 0.0f;
-    if (role == 0) {
-        x[0] = s;
-        for (int n = 0; n < p.nseg; ++n) {
-            s = fmaf(d[n], s, x[(n + 1) * p.per]);
-            x[(n + 1) * p.per] = s;
-        }
-    } else {
-        for (int n = p.nseg - 1; n >= 0; --n) {
-            const float local = x[n * p.per];
-            x[(n + 1) * p.per] = s;
-            s = fmaf(d[n], s, local);
-        }
-        x[0] = s;
+    *x = s;
+    for (int n0 = 0; n0 < p.nseg; n0 += kScanBatch) {
+        float local[kScanBatch], decay[kScanBatch];
+#pragma unroll
+        for (int n = 0; n < kScanBatch; ++n)
+            if (n0 + n < p.nseg) {
+                local[n] = x[(n0 + n + 1) * step];
+                decay[n] = d[(n0 + n) * dstep];
+            }
+#pragma unroll
+        for (int n = 0; n < kScanBatch; ++n)
+            if (n0 + n < p.nseg) {
+                s = fmaf(decay[n], s, local[n]);
+                x[(n0 + n + 1) * step] = s;
+            }
     }
     if (p.last[role]) p.last[role][i] = s;
 }
@@ -65,6 +74,9 @@ hyena_status check_inputs(const RecPlan& p, const hyena_recurrence_inputs* in, i
     hyena_status st;
     if ((st = check_view(in->q, "q", e)) != HYENA_OK || (st = check_view(in->k, "k", e)) != HYENA_OK ||
         (st = check_view(in->v, "v", e)) != HYENA_OK || (st = check_view(in->g, "g", 4)) != HYENA_OK)
+        return st;
+    if ((st = check_token_stride(in->q, "q", n)) != HYENA_OK || (st = check_token_stride(in->k, "k", n)) != HYENA_OK ||
+        (st = check_token_stride(in->v, "v", n)) != HYENA_OK || (st = check_token_stride(in->g, "g", n)) != HYENA_OK)
         return st;
     spans[0] = view_span(in->q, p.B, n, p.heads, p.dk, e);
     spans[1] = view_span(in->k, p.B, n, p.heads, p.dk, e);
@@ -322,7 +334,7 @@ hyena_status hyena_recurrence_backward(hyena_recurrence_t plan, const hyena_recu
     if (st != HYENA_OK) return st;
     if (d_o == nullptr) return refuse("d_o is NULL");
     const size_t e = element_bytes(p.io_dtype);
-    if ((st = check_view(*d_o, "d_o", e)) != HYENA_OK) return st;
+    if ((st = check_view(*d_o, "d_o", e)) != HYENA_OK || (st = check_token_stride(*d_o, "d_o", p.N)) != HYENA_OK) return st;
     if (out == nullptr || out->dq == nullptr || out->dk == nullptr || out->dv == nullptr || out->dg == nullptr)
         return refuse("an output pointer is NULL");
     if (workspace == nullptr) return refuse("workspace is NULL");

@@ -23,6 +23,7 @@
 namespace hy {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -172,6 +173,103 @@ struct RView {
     int32_t vec;  // rows of 4-channel groups can be read as one vector each
 };
 
+// Rows of one (batch row, head) of a tensor, read and written through a buffer
+// descriptor: an access whose offset is kOutside is dropped (a load gives 0),
+// so what a mask leaves out costs a select and no branch, and all loads of a
+// tile are under way together.
+constexpr uint32_t kOutside = 0xffffffffu;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, 0x7fffffff, 0x00020000);
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+__device__ __forceinline__ typename Mx<T>::vec4 load4(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t scalar = 0)
+{
+    if constexpr (sizeof(T) == 4)
+        return __builtin_bit_cast(typename Mx<T>::vec4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, (int)scalar, 0));
+    else
+        return __builtin_bit_cast(typename Mx<T>::vec4, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, (int)scalar, 0));
+}
+// Stores take their whole offset in a vector register: after a 16-byte store
+// with a scalar offset the compiler puts no wait before an instruction that
+// overwrites the stored registers, and such a store was seen to write the new
+// value.
+template <typename T>
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, typename Mx<T>::vec4 x)
+{
+    if constexpr (sizeof(T) == 4)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, (int)off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, (int)off, 0, 0);
+}
+template <typename T> __device__ __forceinline__ T load1(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t scalar = 0)
+{
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, (int)scalar, 0));
+    else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, (int)off, (int)scalar, 0));
+}
+template <typename T> __device__ __forceinline__ void store1(__amdgpu_buffer_rsrc_t r, uint32_t off, T x)
+{
+    if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, (int)off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, x), r, (int)off, 0, 0);
+}
+
+// 4 channels from `ch` on of the row at byte `off`; width: the row's channels.
+template <typename T>
+__device__ __forceinline__ void store_row4(__amdgpu_buffer_rsrc_t r, uint32_t off, bool in, int ch, int width, f32x4 x)
+{
+    const typename Mx<T>::vec4 y = Mx<T>::narrow(x);
+    if ((width & 3) == 0) {
+        store4<T>(r, in & (ch < width) ? off + ch * (uint32_t)sizeof(T) : kOutside, y);
+    } else {
+        const T* e = (const T*)&y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            store1<T>(r, in & (ch + j < width) ? off + (ch + j) * (uint32_t)sizeof(T) : kOutside, e[j]);
+    }
+}
+
+// The same value, newly made: what is computed from it stays in the loop it is
+// used in, instead of in a register of its own (or in scratch) through all of it.
+__device__ __forceinline__ int again(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+__device__ __forceinline__ int again_uniform(int x)
+{
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
+// The rows of one (batch row, head), walked a chunk at a time; step: bytes from
+// token to token (token strides are below 2^23 elements).
+struct Stream {
+    const char* p;
+    uint32_t step;
+    template <typename T> __device__ __forceinline__ void start(const RView& v, int64_t b, int64_t h, int64_t t)
+    {
+        p = (const char*)v.p + (b * v.b + h * v.h + t * v.t) * (int64_t)sizeof(T);
+        step = (uint32_t)v.t * (uint32_t)sizeof(T);
+    }
+    __device__ __forceinline__ void move(int tokens) { p += (int64_t)tokens * (int64_t)step; }
+};
+
+// Place of (channel, token) in a transposed tile: rows of C tokens are 128 bytes,
+// eight units of 16.  Unit u of a row is kept at u ^ key: eight rows in turn, and
+// every fourth of 32, have eight keys, so neither the column stores of a tile
+// (every fourth row) nor the fragment loads (16 rows in turn) meet in a bank.
+template <typename T, int C> __device__ __forceinline__ int col_at(int channel, int token)
+{
+    constexpr int U = 16 / (int)sizeof(T);
+    static_assert(C * sizeof(T) == 128, "a row is eight units");
+    return channel * C + (((token / U) ^ ((channel ^ (channel >> 3)) & 7)) * U) + token % U;
+}
+
 // C tokens x D channels of a tensor as blocks of 4 tokens x 4 channels, held
 // in registers between the global load and the LDS store.
 template <typename T, int C, int D, int THREADS> struct Tile {
@@ -180,33 +278,55 @@ template <typename T, int C, int D, int THREADS> struct Tile {
     static constexpr int kPer = (kBlocks + THREADS - 1) / THREADS;
     vec4 x[kPer][4];
 
-    // tokens t0 .. t0 + C - 1 of the row whose first element is `base`; tokens
-    // at n_valid and after it, and channels at `width` and after it, are zero
-    // and not read
-    __device__ __forceinline__ void load(const T* base, int64_t stride, int vec, int64_t t0,
-                                         int64_t n_valid, int width, int tid)
+    // First token and channel of block b: lanes follow the rows, so that a load
+    // instruction asks for whole 128-byte lines (with 64-byte pieces of rows the
+    // reading rate fell from 5.8 to 4.0 TB/s).
+    static __device__ __forceinline__ int token(int b) { return 4 * (b / (D / 4)); }
+    static __device__ __forceinline__ int channel(int b) { return 4 * (b % (D / 4)); }
+
+    // Byte offsets of a thread's blocks from the stream's place: kept through the
+    // loop, kOutside where the block's channels do not exist.
+    struct Places {
+        uint32_t off[kPer];
+        __device__ __forceinline__ Places(const Stream& s, int width, int tid)
+        {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int b = tid + i * THREADS;
+                const bool in = (kBlocks % THREADS == 0 || b < kBlocks) && channel(b) < width;
+                off[i] = in ? (uint32_t)token(b) * s.step + (uint32_t)channel(b) * (uint32_t)sizeof(T) : kOutside;
+            }
+        }
+    };
+
+    // The first n tokens of the stream from its place on; tokens at n and after
+    // it, and channels at `width` and after it, are zero and not read.  VEC:
+    // each group of 4 channels is one vector.
+    template <bool VEC> __device__ __forceinline__ void load(const Stream& s, const Places& at, int n, int width, int tid)
     {
+        const __amdgpu_buffer_rsrc_t rsrc = rows_at(s.p);
+        if (VEC && n >= C) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[i][r] = load4<T>(rsrc, at.off[i], r * s.step);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int b = tid + i * THREADS;
-            const int c = 4 * (b % (D / 4));
-            const int64_t t = t0 + 4 * (b / (D / 4));
-            const bool in = kBlocks % THREADS == 0 || b < kBlocks;
+            const int t = token(tid + i * THREADS), c = channel(tid + i * THREADS);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                vec4 v = {};
-                if (in && t + r < n_valid && c < width) {
-                    const T* q = base + (t + r) * stride + c;
-                    if (vec) {
-                        v = *(const vec4*)q;
-                    } else {
-                        T* e = (T*)&v;
+                const uint32_t off = t + r < n ? at.off[i] : kOutside;
+                if constexpr (VEC) {
+                    x[i][r] = load4<T>(rsrc, off, r * s.step);
+                } else {
+                    T e[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (c + j < width) e[j] = q[j];
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        e[j] = load1<T>(rsrc, c + j < width && off != kOutside ? off + j * (uint32_t)sizeof(T) : kOutside, r * s.step);
+                    x[i][r] = *(const vec4*)e;
                 }
-                x[i][r] = v;
             }
         }
     }
@@ -217,25 +337,54 @@ template <typename T, int C, int D, int THREADS> struct Tile {
         for (int i = 0; i < kPer; ++i) {
             const int b = tid + i * THREADS;
             if (kBlocks % THREADS != 0 && b >= kBlocks) break;
-            const int c = perm4(b % (D / 4)), t = 4 * (b / (D / 4));
+            const int c = perm4(channel(b) / 4), t = token(b);
 #pragma unroll
             for (int r = 0; r < 4; ++r) *(vec4*)(lds + (t + r) * LD + c) = x[i][r];
         }
     }
-    // cols[channel][token]
-    template <int LD> __device__ __forceinline__ void store_cols(T* lds, int tid) const
+    // cols[channel][token], in units of 16 bytes swapped within a row (col_at)
+    __device__ __forceinline__ void store_cols(T* lds, int tid) const
     {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int b = tid + i * THREADS;
             if (kBlocks % THREADS != 0 && b >= kBlocks) break;
-            const int c = 4 * (b % (D / 4)), t = 4 * (b / (D / 4));
+            const int c = channel(b), t = token(b);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 vec4 v = {x[i][0][j], x[i][1][j], x[i][2][j], x[i][3][j]};
-                *(vec4*)(lds + (c + j) * LD + t) = v;
+                *(vec4*)(lds + col_at<T, C>(c + j, t)) = v;
             }
         }
+    }
+};
+
+// Fragments of a transposed tile: 8 tokens 32 j + 8 grp .. of the row 16 k + l16.
+// Of the key only bits of k and j change from fragment to fragment, so four
+// places per lane serve all of them (float32: and their neighbours, unit ^ 1).
+template <typename T, int C> struct ColFrags {
+    static constexpr int U = 16 / (int)sizeof(T);
+    uint32_t at[4];
+    __device__ __forceinline__ ColFrags(int l16, int grp)
+    {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            at[x] = l16 * C + (((grp * (8 / U)) ^ ((l16 ^ (l16 >> 3)) & 7) ^ (2 * x)) & 7) * U;
+    }
+    static __device__ __forceinline__ typename Mx<T>::frag load(const T* lds, uint32_t p)
+    {
+        if constexpr (sizeof(T) == 4) return join8(*(const f32x4*)(lds + p), *(const f32x4*)(lds + (p ^ 4)));
+        else return *(const typename Mx<T>::frag*)(lds + p);
+    }
+    // k and j known to the compiler
+    __device__ __forceinline__ typename Mx<T>::frag operator()(const T* lds, int k, int j) const
+    {
+        return load(lds, at[(k ^ (2 * j)) & 3] + 16 * k * C);
+    }
+    // any k
+    __device__ __forceinline__ typename Mx<T>::frag any(const T* lds, int k, int j) const
+    {
+        return load(lds, (at[0] ^ (2 * ((k ^ (2 * j)) & 3) * U)) + 16 * k * C);
     }
 };
 
@@ -246,62 +395,113 @@ __device__ __forceinline__ typename Mx<T>::frag frag_at(const T* lds)
     else return *(const typename Mx<T>::frag*)lds;
 }
 
-// The decays of one chunk, in LDS.  logs: sum of the log2 decays up to and
-// with each token, float64 (differences of sums of up to 64 terms keep float32
-// accuracy); count: resets so far (a reset's own log counts as 0; a pair of
-// tokens with a reset between them has factor 0); head: from the chunk's start
-// through each token; tail: from after each token to the chunk's end; inner:
-// from after the chunk's first token through each, head[i] = head[0] inner[i].
-template <int C> struct alignas(16) Decays {
+// The decays of one chunk, in LDS.  A pair of tokens i >= j of different 16-token
+// tiles has the factor within[i] cross[i / 16 - 1][j]: from the tile's start
+// through i, and from after j to that start.  Pairs of one tile take the
+// difference of logs: sums of the log2 decays from the chunk's start, float64, so
+// that differences of up to 64 terms keep float32 accuracy.  A reset's own log
+// counts as 0; count is the number of resets so far, and a factor that spans one
+// is 0.  head: from the chunk's start through each token; tail: from after each
+// token to the chunk's end; inner: from after the chunk's first token through
+// each, head[i] = head[0] inner[i] (binary16 only).
+template <int C, bool INNER> struct alignas(16) Decays {
     double logs[C];
     int count[C];
-    float head[C], tail[C], inner[C];
+    float head[C], tail[C], within[C];
+    float cross[C / 16 - 1][C];
+    float inner[INNER ? C : 4];
+    unsigned long long resets;  // bit per token
 };
 
 // exp2 of anything below this is no normal float32 (v_exp_f32 gives 0)
 constexpr float kResetLog2 = -126.0f;
 
-__device__ __forceinline__ double shfl_up_f64(double x, int d)
+// Cross-lane sums by DPP and lane swaps: they cost an instruction or two each,
+// where a shuffle through the LDS crossbar costs its latency.
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_f64(double x)
 {
     const int2 v = __builtin_bit_cast(int2, x);
-    return __builtin_bit_cast(double, make_int2(__shfl_up(v.x, d), __shfl_up(v.y, d)));
+    return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_update_dpp(0, v.x, CTRL, ROWS, 0xf, false),
+                                                __builtin_amdgcn_update_dpp(0, v.y, CTRL, ROWS, 0xf, false)));
+}
+// sum over lanes 0 .. lane
+__device__ __forceinline__ double scan_f64(double x)
+{
+    x += dpp_f64<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8: within 16 lanes
+    x += dpp_f64<0x112, 0xf>(x);
+    x += dpp_f64<0x114, 0xf>(x);
+    x += dpp_f64<0x118, 0xf>(x);
+    x += dpp_f64<0x142, 0xa>(x);  // row_bcast 15, 31: the sums of the rows before
+    x += dpp_f64<0x143, 0xc>(x);
+    return x;
+}
+__device__ __forceinline__ double lane_f64(double x, int lane)
+{
+    const int2 v = __builtin_bit_cast(int2, x);
+    return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_readlane(v.x, lane), __builtin_amdgcn_readlane(v.y, lane)));
+}
+template <int CTRL> __device__ __forceinline__ float dpp_f32(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+// sum over the 16 lanes of a row, in each of them
+__device__ __forceinline__ float sum16(float x)
+{
+    x += dpp_f32<0xb1>(x);   // quad_perm 1, 0, 3, 2
+    x += dpp_f32<0x4e>(x);   // quad_perm 2, 3, 0, 1
+    x += dpp_f32<0x141>(x);  // row_half_mirror
+    x += dpp_f32<0x140>(x);  // row_mirror
+    return x;
+}
+// sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48, in each of them
+__device__ __forceinline__ float sum_rows(float x)
+{
+    typedef uint32_t u32x2_ __attribute__((ext_vector_type(2)));
+    u32x2_ s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
 // One wave fills the decays of a chunk from its log decay per lane (lane =
 // token, 0 where the token does not exist).
-template <int C>
-__device__ __forceinline__ void fill_decays(Decays<C>& d, float g, int lane)
+template <int C, bool INNER>
+__device__ __forceinline__ void fill_decays(Decays<C, INNER>& d, float g, int lane)
 {
-    const float l2 = g * 1.44269504088896340736f;
-    const bool reset = l2 < kResetLog2;
+    const bool reset = g * 1.44269504088896340736f < kResetLog2;
     const unsigned long long resets = __ballot(reset && lane < C);
-    double s = reset ? 0.0 : (double)g * 1.44269504088896340736;
+    const double s = scan_f64(reset ? 0.0 : (double)g * 1.44269504088896340736);
+    // resets up to and with token t
+    auto upto = [&](int t) { return __popcll(resets & (~0ull >> (63 - t))); };
+    auto factor = [](bool same, double log) { return same ? __builtin_amdgcn_exp2f((float)log) : 0.0f; };
+    const int count = upto(lane);
+    double edge[C / 16];
 #pragma unroll
-    for (int k = 1; k < C; k <<= 1) {
-        const double o = shfl_up_f64(s, k);
-        if (lane >= k) s += o;
+    for (int i = 0; i < C / 16; ++i) edge[i] = lane_f64(s, 16 * i + 15);
+    double before = 0.0;
+    int count_before = 0;
+#pragma unroll
+    for (int i = 1; i < C / 16; ++i) {
+        before = lane >= 16 * i ? edge[i - 1] : before;
+        count_before = lane >= 16 * i ? upto(16 * i - 1) : count_before;
     }
-    const int2 sv = __builtin_bit_cast(int2, s);
-    const double end = __builtin_bit_cast(double, make_int2(__shfl(sv.x, C - 1), __shfl(sv.y, C - 1)));
-    const double first = __builtin_bit_cast(double, make_int2(__shfl(sv.x, 0), __shfl(sv.y, 0)));
-    const int first_count = (int)(resets & 1);
-    const int before = __popcll(resets & (~0ull >> (63 - lane)));
-    const int all = __popcll(resets);
     if (lane < C) {
         d.logs[lane] = s;
-        d.count[lane] = before;
-        d.head[lane] = before == 0 ? __builtin_amdgcn_exp2f((float)s) : 0.0f;
-        d.inner[lane] = before == first_count ? __builtin_amdgcn_exp2f((float)(s - first)) : 0.0f;
-        d.tail[lane] = before == all ? __builtin_amdgcn_exp2f((float)(end - s)) : 0.0f;
+        d.count[lane] = count;
+        d.head[lane] = factor(count == 0, s);
+        d.tail[lane] = factor(count == upto(C - 1), edge[C / 16 - 1] - s);
+        d.within[lane] = factor(count == count_before, s - before);
+        if constexpr (INNER) d.inner[lane] = factor(count == upto(0), s - lane_f64(s, 0));
+#pragma unroll
+        for (int i = 1; i < C / 16; ++i)
+            d.cross[i - 1][lane] = factor(lane < 16 * i && count == upto(16 * i - 1), edge[i - 1] - s);
+        if (lane == 0) d.resets = resets;
     }
 }
 
-// Decay from after token j through token i >= j of a chunk.
-template <int C>
-__device__ __forceinline__ float pair_decay(const Decays<C>& d, double log_i, int count_i, int j)
-{
-    return count_i == d.count[j] ? __builtin_amdgcn_exp2f((float)(log_i - d.logs[j])) : 0.0f;
-}
+// The decays of kDecayBatch chunks at a time: wave w < kDecayBatch fills the
+// w-th of a batch, so the scan's latency is paid once per batch.
+constexpr int kDecayBatch = 2;
 
 __device__ __forceinline__ int64_t valid_tokens(const int32_t* lengths, int64_t b, int64_t N)
 {

@@ -23,30 +23,50 @@ __device__ __forceinline__ const T* row_base(const RView& v, int64_t b, int64_t 
     return (const T*)v.p + b * v.b + h * v.h;
 }
 
+template <typename T> using DecaysOf = Decays<kRecChunk<T>, Mx<T>::kTerms == 2>;
+
+// Waves per SIMD that the registers leave room for: with 64 x 64 states three.
+constexpr int rec_waves(int d0, int d1, bool light) { return d0 * d1 <= 64 * 64 && light ? 3 : 2; }
+
+// Wide states: nothing moves across, so that the operands of one part of a
+// chunk's work are not all fetched during the one before (which spilled).
+template <bool HOLD> __device__ __forceinline__ void hold_schedule()
+{
+    if constexpr (HOLD) __builtin_amdgcn_sched_barrier(0);
+}
+
+// out[16 i + l16] = sum over the four lanes of a column of x[i]
+template <int IT> __device__ __forceinline__ void store_token_sums(float* out, const float (&x)[IT], int lane, int grp)
+{
+    float y = sum_rows(x[0]);
+#pragma unroll
+    for (int i = 1; i < IT; ++i) {
+        const float z = sum_rows(x[i]);
+        y = grp == i ? z : y;
+    }
+    if (lane < 16 * IT) out[lane] = y;
+}
+
 // ---------------------------------------------------------------------------
 // Local states of the segments.  One workgroup per (row, head, segment, role);
 // wave w owns every fourth 16-column tile of the state.
 // ---------------------------------------------------------------------------
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(256) void hyena_rec_states(RecStateArgs p)
+template <typename T, int DK, int DV, bool VEC>
+__global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states(RecStateArgs p)
 {
-    constexpr int C = kRecChunk<T>, LC = C + kPad<T>, NT = Mx<T>::kTerms;
+    constexpr int C = kRecChunk<T>, NT = Mx<T>::kTerms;
     constexpr int KT = DK / 16, VW = DV / 64;
     using frag = typename Mx<T>::frag;
-    __shared__ __attribute__((aligned(16))) T xt[DK * LC];
-    __shared__ __attribute__((aligned(16))) T yt[DV * LC];
-    __shared__ Decays<C> dec;
+    __shared__ __attribute__((aligned(16))) T xt[DK * C];
+    __shared__ __attribute__((aligned(16))) T yt[DV * C];
+    __shared__ DecaysOf<T> decays[kDecayBatch];
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const ColFrags<T, C> cols_of(l16, grp);
     const int64_t bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
     const int role = blockIdx.y;
     const int64_t b = bh / p.heads, h = bh % p.heads;
-    const RView& xv = p.x[role];
-    const RView& yv = p.y[role];
-    const T* xp = row_base<T>(xv, b, h);
-    const T* yp = row_base<T>(yv, b, h);
-    const float* gp = row_base<float>(p.g, b, h);
     const int64_t nv = valid_tokens(p.lengths, b, p.N);
     const int64_t t0 = seg * (int64_t)p.seg;
     const int64_t t1 = t0 + p.seg < nv ? t0 + p.seg : nv;
@@ -56,20 +76,44 @@ __global__ __launch_bounds__(256) void hyena_rec_states(RecStateArgs p)
     float total = 1.0f;
     Tile<T, C, DK, 256> tx;
     Tile<T, C, DV, 256> ty;
-    float g = 0.0f;
+    // the chunks are walked forward (role 0) or from the last one back
+    Stream xs, ys, gs;
+    const int64_t first = t0 + (role ? (int64_t)(nchunk - 1) * C : 0);
+    const int way = role ? -C : C;
+    xs.start<T>(p.x[role], b, h, first);
+    ys.start<T>(p.y[role], b, h, first);
+    gs.start<float>(p.g, b, h, first + wave * way);
+    const typename Tile<T, C, DK, 256>::Places px(xs, p.dk, tid);
+    const typename Tile<T, C, DV, 256>::Places py(ys, p.dv, tid);
+    const int len = (int)(t1 - t0);
+    // tokens of the c-th chunk walked
+    auto tokens = [&](int c) { return len - (role ? nchunk - 1 - c : c) * C; };
     auto fetch = [&](int c) {
-        const int64_t t = t0 + (int64_t)(role ? nchunk - 1 - c : c) * C;
-        tx.load(xp, xv.t, xv.vec, t, t1, p.dk, tid);
-        ty.load(yp, yv.t, yv.vec, t, t1, p.dv, tid);
-        g = wave == 0 && lane < C && t + lane < t1 ? gp[(t + lane) * p.g.t] : 0.0f;
+        tx.template load<VEC>(xs, px, tokens(c), p.dk, tid);
+        ty.template load<VEC>(ys, py, tokens(c), p.dv, tid);
+        xs.move(way);
+        ys.move(way);
     };
-    if (nchunk > 0) fetch(0);
+    float g = 0.0f;
+    auto fetch_g = [&](int c) {
+        g = load1<float>(rows_at(gs.p), lane < C && c < nchunk && lane < tokens(c) ? lane * gs.step : kOutside);
+        gs.move(kDecayBatch * way);
+    };
+    if (nchunk > 0) {
+        fetch_g(wave);
+        fetch(0);
+    }
     for (int c = 0; c < nchunk; ++c) {
-        tx.template store_cols<LC>(xt, tid);
-        ty.template store_cols<LC>(yt, tid);
-        if (wave == 0) fill_decays<C>(dec, g, lane);
+        const int slot = c % kDecayBatch;
+        if (slot == 0 && wave < kDecayBatch) fill_decays<C, Mx<T>::kTerms == 2>(decays[wave], g, lane);
+        const DecaysOf<T>& dec = decays[slot];
+        tx.store_cols(xt, tid);
+        ty.store_cols(yt, tid);
         __syncthreads();
-        if (c + 1 < nchunk) fetch(c + 1);
+        if (c + 1 < nchunk) {
+            fetch(c + 1);
+            if (slot == 0) fetch_g(c + kDecayBatch + wave);
+        }
         const float all = dec.head[C - 1];
         constexpr bool kLead = Mx<T>::kTerms == 2;
         const float* f = role ? (kLead ? dec.inner : dec.head) : dec.tail;
@@ -83,12 +127,12 @@ __global__ __launch_bounds__(256) void hyena_rec_states(RecStateArgs p)
             for (int j = 0; j < C / 32; ++j) {
                 const f32x8 w = join8(*(const f32x4*)(f + 32 * j + 8 * grp),
                                       *(const f32x4*)(f + 32 * j + 8 * grp + 4));
-                y[j].set(Mx<T>::widen8(frag_at<T>(yt + (16 * vt + l16) * LC + 32 * j + 8 * grp)) * w);
+                y[j].set(Mx<T>::widen8(cols_of.any(yt, vt, j)) * w);
             }
 #pragma unroll
             for (int k = 0; k < KT; ++k)
                 S[k][v] = update<T>(S[k][v], all, lead, y,
-                                    [&](int j) { return frag_at<T>(xt + (16 * k + l16) * LC + 32 * j + 8 * grp); });
+                                    [&](int j) { return cols_of(xt, k, j); });
         }
         __syncthreads();
     }
@@ -111,15 +155,18 @@ __global__ __launch_bounds__(256) void hyena_rec_states(RecStateArgs p)
 template <typename T, int DA, int DC, bool TRANS> constexpr size_t rec_out_lds()
 {
     constexpr int C = kRecChunk<T>, LA = DA + kPad<T>, LR = DC + kPad<T>, LC = C + kPad<T>;
-    return sizeof(T) * (size_t)(2 * C * LA + DA * LC + DC * LC + C * LC + (TRANS ? C * LR : 0)) +
-           sizeof(Decays<C>) + (TRANS ? 4 * C * sizeof(float) : 0);
+    return sizeof(T) * (size_t)(2 * C * LA + DA * C + DC * C + C * LC + (TRANS ? C * LR : 0)) +
+           kDecayBatch * sizeof(DecaysOf<T>) + (TRANS ? 4 * C * sizeof(float) : 0);
 }
 
-template <typename T, int DK, int DV> constexpr size_t rec_grad_lds()
+// Chunks whose terms of dg are held before they are summed up.
+constexpr int kGradHold = 16;
+
+template <typename T, int D> constexpr size_t rec_grad_lds()
 {
-    constexpr int C = kRecChunk<T>, LK = DK + kPad<T>, LV = DV + kPad<T>, LC = C + kPad<T>;
-    return sizeof(T) * (size_t)(2 * C * LK + 2 * C * LV + DK * LC + DV * LC + 2 * C * LC) +
-           sizeof(Decays<C>) + sizeof(float) * (size_t)(2 * (C / 16) * C + 4 * C + 8);
+    constexpr int C = kRecChunk<T>, LD = D + kPad<T>, LC = C + kPad<T>;
+    return sizeof(T) * (size_t)(4 * C * LD + 2 * D * C + 2 * C * LC) + kDecayBatch * sizeof(DecaysOf<T>) +
+           sizeof(float) * (size_t)(2 * (C / 16) * C + 4 * C + kDecayBatch * C + kGradHold * C) + kGradHold * 16;
 }
 
 // ---------------------------------------------------------------------------
@@ -133,8 +180,8 @@ template <typename T, int DK, int DV> constexpr size_t rec_grad_lds()
 // tiles of a chunk (written to LDS in storage type) and each owns every fourth
 // 16-channel tile of c: its part of the state never leaves its registers.
 // ---------------------------------------------------------------------------
-template <typename T, int DA, int DC, bool TRANS>
-__global__ __launch_bounds__(256) void hyena_rec_out(RecArgs p)
+template <typename T, int DA, int DC, bool TRANS, bool VEC>
+__global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) void hyena_rec_out(RecArgs p)
 {
     constexpr int C = kRecChunk<T>, LA = DA + kPad<T>, LR = DC + kPad<T>, LC = C + kPad<T>;
     constexpr int NT = Mx<T>::kTerms;                              // state update
@@ -145,23 +192,19 @@ __global__ __launch_bounds__(256) void hyena_rec_out(RecArgs p)
     __shared__ __attribute__((aligned(16))) char smem[rec_out_lds<T, DA, DC, TRANS>()];
     T* ar = (T*)smem;              // [C][LA]
     T* br = ar + C * LA;           // [C][LA]
-    T* bt = br + C * LA;           // [DA][LC]
-    T* ct = bt + DA * LC;          // [DC][LC]
-    T* ps = ct + DC * LC;          // [C][LC]
+    T* bt = br + C * LA;           // [DA][C] transposed
+    T* ct = bt + DA * C;           // [DC][C] transposed
+    T* ps = ct + DC * C;           // [C][LC]
     T* rr = ps + C * LC;           // [C][LR], TRANS
     char* tail = (char*)(rr + (TRANS ? C * LR : 0));
-    Decays<C>& dec = *(Decays<C>*)tail;
-    float* part = (float*)(tail + sizeof(Decays<C>));  // [4][C], TRANS
+    DecaysOf<T>* const decays = (DecaysOf<T>*)tail;
+    float* part = (float*)(tail + kDecayBatch * sizeof(DecaysOf<T>));  // [4][C], TRANS
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const ColFrags<T, C> cols_of(l16, grp);
     const int64_t bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
     const int64_t b = bh / p.heads, h = bh % p.heads;
-    const T* ap = row_base<T>(p.a, b, h);
-    const T* bp = row_base<T>(p.b, b, h);
-    const T* cp = row_base<T>(p.c, b, h);
-    const T* rp = TRANS ? row_base<T>(p.r, b, h) : nullptr;
-    const float* gp = row_base<float>(p.g, b, h);
     const int64_t nv = valid_tokens(p.lengths, b, p.N);
     const int64_t t0 = seg * (int64_t)p.seg;
     const int64_t tN = t0 + p.seg < p.N ? t0 + p.seg : p.N;
@@ -169,7 +212,7 @@ __global__ __launch_bounds__(256) void hyena_rec_out(RecArgs p)
     const int nchunk = t1 > t0 ? (int)((t1 - t0 + C - 1) / C) : 0;
     T* const op = (T*)p.out + (b * p.N * p.heads + h) * p.dc;
     const int64_t ostride = p.heads * (int64_t)p.dc;
-    const bool ovec = (p.dc & 3) == 0;
+    const uint32_t ostep = (uint32_t)ostride * (uint32_t)sizeof(T);
 
     // the state before this segment
     f32x4 S[AT][CW];
@@ -188,104 +231,132 @@ __global__ __launch_bounds__(256) void hyena_rec_out(RecArgs p)
 
     Tile<T, C, DA, 256> ta, tb;
     Tile<T, C, DC, 256> tc, tr;
-    float g = 0.0f;
+    Stream as, bs, cs, rs, gs;
+    as.start<T>(p.a, b, h, t0);
+    bs.start<T>(p.b, b, h, t0);
+    cs.start<T>(p.c, b, h, t0);
+    if constexpr (TRANS) rs.start<T>(p.r, b, h, t0);
+    gs.start<float>(p.g, b, h, t0 + wave * C);
+    const typename Tile<T, C, DA, 256>::Places pa(as, p.da, tid), pb(bs, p.da, tid);
+    const typename Tile<T, C, DC, 256>::Places pc(cs, p.dc, tid), pr(TRANS ? rs : cs, p.dc, tid);
+    const int len = (int)(t1 - t0);
     auto fetch = [&](int c) {
-        const int64_t t = t0 + (int64_t)c * C;
-        ta.load(ap, p.a.t, p.a.vec, t, t1, p.da, tid);
-        tb.load(bp, p.b.t, p.b.vec, t, t1, p.da, tid);
-        tc.load(cp, p.c.t, p.c.vec, t, t1, p.dc, tid);
-        if constexpr (TRANS) tr.load(rp, p.r.t, p.r.vec, t, t1, p.dc, tid);
-        g = wave == 0 && lane < C && t + lane < t1 ? gp[(t + lane) * p.g.t] : 0.0f;
+        const int n = len - c * C;
+        ta.template load<VEC>(as, pa, n, p.da, tid);
+        tb.template load<VEC>(bs, pb, n, p.da, tid);
+        tc.template load<VEC>(cs, pc, n, p.dc, tid);
+        if constexpr (TRANS) tr.template load<VEC>(rs, pr, n, p.dc, tid);
+        as.move(C);
+        bs.move(C);
+        cs.move(C);
+        if constexpr (TRANS) rs.move(C);
     };
-    if (nchunk > 0) fetch(0);
+    float g = 0.0f;
+    auto fetch_g = [&](int c) {
+        g = load1<float>(rows_at(gs.p), lane < C && lane < len - c * C ? lane * gs.step : kOutside);
+        gs.move(kDecayBatch * C);
+    };
+    if (nchunk > 0) {
+        fetch_g(wave);
+        fetch(0);
+    }
     for (int c = 0; c < nchunk; ++c) {
+        const int slot = c % kDecayBatch;
+        if (slot == 0 && wave < kDecayBatch) fill_decays<C, Mx<T>::kTerms == 2>(decays[wave], g, lane);
+        const DecaysOf<T>& dec = decays[slot];
         ta.template store_rows<LA>(ar, tid);
         tb.template store_rows<LA>(br, tid);
-        tb.template store_cols<LC>(bt, tid);
-        tc.template store_cols<LC>(ct, tid);
+        tb.store_cols(bt, tid);
+        tc.store_cols(ct, tid);
         if constexpr (TRANS) tr.template store_rows<LR>(rr, tid);
-        if (wave == 0) fill_decays<C>(dec, g, lane);
         __syncthreads();
         const int64_t tb0 = t0 + (int64_t)c * C;
-        if (c + 1 < nchunk) fetch(c + 1);
+        const __amdgpu_buffer_rsrc_t orows = rows_at(op + tb0 * ostride);
+        const int left = t1 - tb0 < C ? (int)(t1 - tb0) : C;
+        if (c + 1 < nchunk) {
+            fetch(c + 1);
+            if (slot == 0) fetch_g(c + kDecayBatch + wave);
+        }
 
-        // scores: lower triangle of IT x IT tiles, in turn by the waves; the
-        // tile right of a diagonal tile in an even row is read too: zero it
+        // scores of the tokens of tile `wave` against all before them and their
+        // own tile; tiles right of that are zero (and their products not used).
+        // C = 32 has two tiles: the other waves repeat the work of the first two.
         {
-            int n = 0;
+            const int it = again_uniform(wave) % IT, ti = 16 * it + l16, to = 16 * it + 4 * grp;
+            const double li = dec.logs[ti];
+            double lj[4];
 #pragma unroll
-            for (int i = 0; i < IT; ++i)
+            for (int r = 0; r < 4; ++r) lj[r] = dec.logs[to + r];
+            const int ci = dec.count[ti];
+            const i32x4 cj = *(const i32x4*)(dec.count + to);
+            const float wi = it > 0 ? p.scale : 0.0f;
+            const float within = wi * dec.within[ti];
+            const float* cross = dec.cross[it > 0 ? it - 1 : 0];
+            f32x4 cw[IT - 1];
 #pragma unroll
-                for (int j = 0; j <= i; ++j, ++n) {
-                    if ((n & 3) != wave) continue;
-                    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < IT - 1; ++j) cw[j] = *(const f32x4*)(cross + 16 * j + 4 * grp);
+            frag af[DA / 32];
 #pragma unroll
-                    for (int k = 0; k < DA / 32; ++k)
-                        s = Mx<T>::mma(frag_at<T>(br + (16 * j + l16) * LA + 32 * k + 8 * grp),
-                                       frag_at<T>(ar + (16 * i + l16) * LA + 32 * k + 8 * grp), s);
-                    const int ti = 16 * i + l16, tj = 16 * j + 4 * grp;
-                    const double li = dec.logs[ti];
-                    const int ci = dec.count[ti];
+            for (int k = 0; k < DA / 32; ++k) af[k] = frag_at<T>(ar + ti * LA + 32 * k + 8 * grp);
+            auto tile = [&](int j) {
+                f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        s[r] = tj + r <= ti ? s[r] * (p.scale * pair_decay<C>(dec, li, ci, tj + r)) : 0.0f;
-                    *(vec4*)(ps + ti * LC + tj) = Mx<T>::narrow(s);
-                    if (i == j && (i & 1) == 0) {
-                        const vec4 z = {};
-                        *(vec4*)(ps + ti * LC + tj + 16) = z;
-                    }
-                }
+                for (int k = 0; k < DA / 32; ++k)
+                    s = Mx<T>::mma(frag_at<T>(br + (16 * j + l16) * LA + 32 * k + 8 * grp), af[k], s);
+                return s;
+            };
+            f32x4 own = tile(it), s[IT - 1];
+#pragma unroll
+            for (int j = 0; j < IT - 1; ++j) s[j] = tile(j);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool in = (to + r <= ti) & (cj[r] == ci);
+                const float w = p.scale * __builtin_amdgcn_exp2f((float)(li - lj[r]));
+                own[r] = in ? own[r] * w : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < IT - 1; ++j)
+                *(vec4*)(ps + ti * LC + 16 * j + 4 * grp) = Mx<T>::narrow(s[j] * (cw[j] * within));
+            // the tile right of the last own one is not among the above; then the own tile itself
+            *(vec4*)(ps + ti * LC + 16 * (IT - 1) + 4 * grp) = vec4{};
+            *(vec4*)(ps + ti * LC + to) = Mx<T>::narrow(own);
         }
         __syncthreads();
 
         const float all = dec.head[C - 1];
+        float rdot[IT] = {};
 #pragma unroll
         for (int v = 0; v < CW; ++v) {
             const int vt = wave + 4 * v;
             frag cf[C / 32];
 #pragma unroll
-            for (int j = 0; j < C / 32; ++j) cf[j] = frag_at<T>(ct + (16 * vt + l16) * LC + 32 * j + 8 * grp);
-            Split<T, NS> sf[DA / 32];
-#pragma unroll
-            for (int k = 0; k < DA / 32; ++k)
-                sf[k].set(join8(S[2 * k][v], S[2 * k + 1][v]) * StateScale<T>::down);
+            for (int j = 0; j < C / 32; ++j) cf[j] = cols_of.any(ct, vt, j);
+            const uint32_t orow = (uint32_t)again(l16) * ostep;
             // outputs: column = token, rows = 4 channels
+            f32x4 so[IT] = {};
+#pragma unroll
+            for (int k = 0; k < DA / 32; ++k) {
+                Split<T, NS> sf;
+                sf.set(join8(S[2 * k][v], S[2 * k + 1][v]) * StateScale<T>::down);
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+                    so[i] = mma_split<T, NS, true>(sf, frag_at<T>(ar + (16 * i + l16) * LA + 32 * k + 8 * grp), so[i]);
+            }
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int ti = 16 * i + l16;
-                f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int k = 0; k < DA / 32; ++k)
-                    o = mma_split<T, NS, true>(sf[k], frag_at<T>(ar + ti * LA + 32 * k + 8 * grp), o);
-                o = o * (p.scale * StateScale<T>::up * dec.head[ti]);
+                f32x4 o = so[i] * (p.scale * StateScale<T>::up * dec.head[ti]);
                 if constexpr (TRANS) {
                     const f32x4 r = Mx<T>::widen(*(const vec4*)(rr + ti * LR + perm4(4 * vt + grp)));
-                    float q = o[0] * r[0] + o[1] * r[1] + o[2] * r[2] + o[3] * r[3];
-                    q += __shfl_xor(q, 16);
-                    q += __shfl_xor(q, 32);
-                    if (grp == 0) {
-                        if (v == 0) part[wave * C + ti] = q;
-                        else part[wave * C + ti] += q;
-                    }
+                    rdot[i] += o[0] * r[0] + o[1] * r[1] + o[2] * r[2] + o[3] * r[3];
                 }
 #pragma unroll
                 for (int j = 0; j <= i / 2; ++j)
                     o = Mx<T>::mma(cf[j], frag_at<T>(ps + ti * LC + 32 * j + 8 * grp), o);
-                const int ch = 16 * vt + 4 * grp;
-                if (tb0 + ti < t1 && ch < p.dc) {
-                    T* q = op + (tb0 + ti) * ostride + ch;
-                    const vec4 x = Mx<T>::narrow(o);
-                    if (ovec) {
-                        *(vec4*)q = x;
-                    } else {
-                        const T* e = (const T*)&x;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (ch + r < p.dc) q[r] = e[r];
-                    }
-                }
+                store_row4<T>(orows, orow + 16 * i * ostep, ti < left, 16 * vt + 4 * grp, p.dc, o);
             }
             // the state after this chunk
+            hold_schedule<(DA * DC > 64 * 64)>();
             Split<T, NT> y[C / 32];
 #pragma unroll
             for (int j = 0; j < C / 32; ++j) {
@@ -296,8 +367,10 @@ __global__ __launch_bounds__(256) void hyena_rec_out(RecArgs p)
 #pragma unroll
             for (int k = 0; k < AT; ++k)
                 S[k][v] = update<T>(S[k][v], all, 1.0f, y,
-                                    [&](int j) { return frag_at<T>(bt + (16 * k + l16) * LC + 32 * j + 8 * grp); });
+                                    [&](int j) { return cols_of(bt, k, j); });
+            hold_schedule<(DA * DC > 64 * 64)>();
         }
+        if constexpr (TRANS) store_token_sums<IT>(part + wave * C, rdot, lane, grp);
         __syncthreads();
         if constexpr (TRANS) {
             if (tid < C && tb0 + tid < t1)
@@ -329,46 +402,48 @@ __global__ __launch_bounds__(256) void hyena_rec_out(RecArgs p)
 //   dk_j = sum_i w_ij (do_i . v_j) q_i + tail_j dS v_j
 //   dv_j = sum_i w_ij (q_i . k_j) do_i + tail_j dS^T k_j      (q, do times scale)
 // Eight waves: four own tiles of dk (their part of dS has the channels of v as
-// rows), four own tiles of dv (the other way round).
+// rows) and bring in q and k, four own tiles of dv (the other way round) and
+// bring in do and v.
 //
 // dg_t = <S_end, dS_end> + sum_{s >= t} (q_s . dq_s - k_s . dk_s), s up to the
 // segment's end: both dot products are made of float32 values (scores weighted
-// by both products before any rounding, the states' parts from split operands).
+// by both products before any rounding, the states' parts from split operands)
+// and kept in LDS for kGradHold chunks, then summed up in float64 by all waves.
 // ---------------------------------------------------------------------------
-template <typename T, int DK, int DV>
+template <typename T, int D, bool VEC>
 __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 {
-    constexpr int C = kRecChunk<T>, LK = DK + kPad<T>, LV = DV + kPad<T>, LC = C + kPad<T>;
+    constexpr int C = kRecChunk<T>, LD = D + kPad<T>, LC = C + kPad<T>;
     constexpr int NT = Mx<T>::kTerms;
-    constexpr int IT = C / 16;
+    constexpr int IT = C / 16, MT = D / 16, MW = D / 64;
+    using frag = typename Mx<T>::frag;
     using vec4 = typename Mx<T>::vec4;
-    __shared__ __attribute__((aligned(16))) char smem[rec_grad_lds<T, DK, DV>()];
-    T* qr = (T*)smem;              // [C][LK]
-    T* kr = qr + C * LK;           // [C][LK]
-    T* vr = kr + C * LK;           // [C][LV]
-    T* dr = vr + C * LV;           // [C][LV]
-    T* qt = dr + C * LV;           // [DK][LC]
-    T* dt = qt + DK * LC;          // [DV][LC]
-    T* pa = dt + DV * LC;          // [C][LC] row j, column i: w_ij (q_i . k_j)
+    __shared__ __attribute__((aligned(16))) char smem[rec_grad_lds<T, D>()];
+    T* qr = (T*)smem;              // [C][LD]
+    T* kr = qr + C * LD;           // [C][LD]
+    T* dr = kr + C * LD;           // [C][LD]
+    T* vr = dr + C * LD;           // [C][LD]
+    T* qt = vr + C * LD;           // [D][C] transposed
+    T* dt = qt + D * C;            // [D][C] transposed
+    T* pa = dt + D * C;            // [C][LC] row j, column i: w_ij (q_i . k_j)
     T* pd = pa + C * LC;           // [C][LC] w_ij (do_i . v_j)
     char* rest = (char*)(pd + C * LC);
-    Decays<C>& dec = *(Decays<C>*)rest;
-    float* rows = (float*)(rest + sizeof(Decays<C>));  // [IT][C] by j tile: sum over its j, per i
+    DecaysOf<T>* const decays = (DecaysOf<T>*)rest;
+    float* rows = (float*)(rest + kDecayBatch * sizeof(DecaysOf<T>));  // [IT][C] by j tile: sum over its j, per i
     float* cols = rows + IT * C;                       // [IT][C] by i tile: sum over its i, per j
     float* part = cols + IT * C;                       // [4][C] k . (state's part of dk), per wave
-    float* xs = part + 4 * C;                          // [8]
+    float* rqs = part + 4 * C;                         // [kDecayBatch][C]
+    float* hold = rqs + kDecayBatch * C;               // [kGradHold][C] q . dq - k . dk
+    double* sums = (double*)(hold + kGradHold * C);    // [kGradHold] their sums, [8] at the start
+    unsigned long long* resets = (unsigned long long*)(sums + kGradHold);  // [kGradHold]
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const ColFrags<T, C> cols_of(l16, grp);
     const bool own_k = wave < 4;
-    const int w4 = wave & 3;
+    const int w4 = wave & 3, half = tid & 255;
     const int64_t bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
     const int64_t b = bh / p.heads, h = bh % p.heads;
-    const T* qp = row_base<T>(p.q, b, h);
-    const T* kp = row_base<T>(p.k, b, h);
-    const T* vp = row_base<T>(p.v, b, h);
-    const T* dp = row_base<T>(p.o, b, h);
-    const float* gp = row_base<float>(p.g, b, h);
     const int64_t nv = valid_tokens(p.lengths, b, p.N);
     const int64_t t0 = seg * (int64_t)p.seg;
     const int64_t tN = t0 + p.seg < p.N ? t0 + p.seg : p.N;
@@ -377,8 +452,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     T* const kout = (T*)p.dk_out + (b * p.N * p.heads + h) * p.dk;
     T* const vout = (T*)p.dv_out + (b * p.N * p.heads + h) * p.dv;
 
-    // gradient of the state after this segment; xs: its product with the state
-    constexpr int MT = (DK > DV ? DK : DV) / 16, MW = (DK > DV ? DK : DV) / 64;
+    // gradient of the state after this segment, and its product with the state
     f32x4 S[MT][MW];
     const int64_t per = (int64_t)p.dk * p.dv;
     const float* ep = p.end ? p.end + (bh * (p.nseg + 1) + seg + 1) * per : nullptr;
@@ -396,148 +470,164 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                 S[m][n][r] = ep && in ? ep[kk * p.dv + vv] : 0.0f;
                 if (own_k && ep && sp && in) cross += S[m][n][r] * sp[kk * p.dv + vv];
             }
-#pragma unroll
-    for (int k = 32; k > 0; k >>= 1) cross += __shfl_xor(cross, k);
-    if (lane == 0) xs[wave] = cross;
+    cross = sum_rows(sum16(cross));
+    if (lane == 0) sums[wave] = own_k ? (double)cross : 0.0;
     __syncthreads();
-    double over = 0.0;  // wave 0: <S, dS> after the chunk at hand
-    if (wave == 0) over = ((double)xs[0] + (double)xs[1]) + ((double)xs[2] + (double)xs[3]);
+    double over = ((sums[0] + sums[1]) + (sums[2] + sums[3]));  // <S, dS> after the chunks held
+    __syncthreads();
 
-    Tile<T, C, DK, 512> tq, tk;
-    Tile<T, C, DV, 512> tv, td;
-    float g = 0.0f, rq = 0.0f;
+    // two tensors per half of the workgroup: x, also needed transposed (q, do),
+    // and y (k, v)
+    Tile<T, C, D, 256> tx, ty;
+    Stream xs, ys, gs;
+    const int64_t last = t0 + (int64_t)(nchunk - 1) * C;
+    xs.start<T>(own_k ? p.q : p.o, b, h, last);
+    ys.start<T>(own_k ? p.k : p.v, b, h, last);
+    gs.start<float>(p.g, b, h, last - w4 * C);
+    const int width = own_k ? p.dk : p.dv;
+    T* const xr = own_k ? qr : dr;
+    T* const yr = own_k ? kr : vr;
+    T* const xt = own_k ? qt : dt;
+    const typename Tile<T, C, D, 256>::Places px(xs, width, half), py(ys, width, half);
+    const int len = (int)(t1 - t0);
     auto fetch = [&](int c) {
-        const int64_t t = t0 + (int64_t)(nchunk - 1 - c) * C;
-        tq.load(qp, p.q.t, p.q.vec, t, t1, p.dk, tid);
-        tk.load(kp, p.k.t, p.k.vec, t, t1, p.dk, tid);
-        tv.load(vp, p.v.t, p.v.vec, t, t1, p.dv, tid);
-        td.load(dp, p.o.t, p.o.vec, t, t1, p.dv, tid);
-        const bool in = wave == 0 && lane < C && t + lane < t1;
-        g = in ? gp[(t + lane) * p.g.t] : 0.0f;
-        rq = in ? p.rq[bh * p.N + t + lane] : 0.0f;
+        const int n = len - (nchunk - 1 - c) * C;
+        tx.template load<VEC>(xs, px, n, width, half);
+        ty.template load<VEC>(ys, py, n, width, half);
+        xs.move(-C);
+        ys.move(-C);
     };
-    if (nchunk > 0) fetch(0);
+    // wave w fills the decays of the w-th chunk of a batch, wave 4 + w hands over
+    // the state's part of q . dq
+    float g = 0.0f;
+    auto fetch_g = [&](int c) {
+        const int n = c < nchunk ? len - (nchunk - 1 - c) * C : 0;
+        const bool in = lane < C && lane < n;
+        if (own_k) g = load1<float>(rows_at(gs.p), in ? lane * gs.step : kOutside);
+        else g = load1<float>(rows_at(p.rq + bh * p.N + t0 + (int64_t)(nchunk - 1 - c) * C), in ? lane * 4 : kOutside);
+        gs.move(-kDecayBatch * C);
+    };
+    if (nchunk > 0) {
+        fetch_g(w4);
+        fetch(0);
+    }
     for (int c = 0; c < nchunk; ++c) {
-        tq.template store_rows<LK>(qr, tid);
-        tk.template store_rows<LK>(kr, tid);
-        tv.template store_rows<LV>(vr, tid);
-        td.template store_rows<LV>(dr, tid);
-        tq.template store_cols<LC>(qt, tid);
-        td.template store_cols<LC>(dt, tid);
-        const float rq_now = rq, g_now = g;
-        if (wave == 0) fill_decays<C>(dec, g, lane);
+        const int slot = c % kDecayBatch;
+        if (slot == 0 && w4 < kDecayBatch) {
+            if (own_k) fill_decays<C, Mx<T>::kTerms == 2>(decays[w4], g, lane);
+            else if (lane < C) rqs[w4 * C + lane] = g;
+        }
+        const DecaysOf<T>& dec = decays[slot];
+        const int at = D > 64 ? again(half) : half;
+        tx.template store_rows<LD>(xr, at);
+        ty.template store_rows<LD>(yr, at);
+        tx.store_cols(xt, at);
         __syncthreads();
         const int64_t tb0 = t0 + (int64_t)(nchunk - 1 - c) * C;
-        if (c + 1 < nchunk) fetch(c + 1);
+        const int left = t1 - tb0 < C ? (int)(t1 - tb0) : C;
+        if (c + 1 < nchunk) {
+            fetch(c + 1);
+            if (slot == 0) fetch_g(c + kDecayBatch + w4);
+        }
+        // what the last wave adds up below, read before others may refill it
+        float rq_now = 0.0f;
+        unsigned long long resets_now = 0;
+        if (wave == 7) {
+            rq_now = rqs[slot * C + lane % C];
+            resets_now = dec.resets;
+        }
 
         // both scores of each pair of tiles: rows i, columns j <= i
-        {
-            int n = 0;
 #pragma unroll
-            for (int i = 0; i < IT; ++i)
+        for (int n = 0; n < (IT * (IT + 1) / 2 + 7) / 8; ++n) {
+            // tiles in the order of (i, j): 0 (0, 0), 1 (1, 0), 2 (1, 1), 3 (2, 0) ..
+            const int at = again_uniform(wave) + 8 * n;
+            if (at >= IT * (IT + 1) / 2) break;
+            const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
+            const int i = at < 1 ? 0 : at < 3 ? 1 : at < 6 ? 2 : 3, j = at - i * (i + 1) / 2;
+            const int tj = 16 * j + l16, ti = 16 * i + 4 * grp;
+            const bool own = i == j;
+            const double lj = dec.logs[tj];
+            const int cj = dec.count[tj];
+            double li[4];
 #pragma unroll
-                for (int j = 0; j <= i; ++j, ++n) {
-                    if ((n & 7) != wave) continue;
-                    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f}, d = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r = 0; r < 4; ++r) li[r] = dec.logs[ti + r];
+            const i32x4 ci = *(const i32x4*)(dec.count + ti);
+            const f32x4 within = *(const f32x4*)(dec.within + ti);
+            const float crossed = p.scale * dec.cross[i > 0 ? i - 1 : 0][tj];
+            f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f}, d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int k = 0; k < DK / 32; ++k)
-                        s = Mx<T>::mma(frag_at<T>(qr + (16 * i + l16) * LK + 32 * k + 8 * grp),
-                                       frag_at<T>(kr + (16 * j + l16) * LK + 32 * k + 8 * grp), s);
+            for (int k = 0; k < D / 32; ++k) {
+                s = Mx<T>::mma(frag_at<T>(qr + (16 * i + l16) * LD + 32 * k + 8 * grp),
+                               frag_at<T>(kr + (16 * j + l16) * LD + 32 * k + 8 * grp), s);
+                d = Mx<T>::mma(frag_at<T>(dr + (16 * i + l16) * LD + 32 * k + 8 * grp),
+                               frag_at<T>(vr + (16 * j + l16) * LD + 32 * k + 8 * grp), d);
+            }
+            f32x4 both;
 #pragma unroll
-                    for (int k = 0; k < DV / 32; ++k)
-                        d = Mx<T>::mma(frag_at<T>(dr + (16 * i + l16) * LV + 32 * k + 8 * grp),
-                                       frag_at<T>(vr + (16 * j + l16) * LV + 32 * k + 8 * grp), d);
-                    const int tj = 16 * j + l16, ti = 16 * i + 4 * grp;
-                    const double lj = dec.logs[tj];
-                    const int cj = dec.count[tj];
-                    f32x4 both;
+            for (int r = 0; r < 4; ++r) {
+                const bool in = !own | ((tj <= ti + r) & (ci[r] == cj));
+                const float w = own ? p.scale * __builtin_amdgcn_exp2f((float)(li[r] - lj)) : within[r] * crossed;
+                const float sw = s[r] * w;
+                both[r] = in ? sw * d[r] : 0.0f;
+                s[r] = in ? sw : 0.0f;
+                d[r] = in ? d[r] * w : 0.0f;
+            }
+            *(vec4*)(pa + tj * LC + ti) = Mx<T>::narrow(s);
+            *(vec4*)(pd + tj * LC + ti) = Mx<T>::narrow(d);
+            if (own && (j & 1) == 1) {  // the tile above an odd own one is read with it
+                *(vec4*)(pa + tj * LC + ti - 16) = vec4{};
+                *(vec4*)(pd + tj * LC + ti - 16) = vec4{};
+            }
+            // every lane of a row or column writes the same sum
+            cols[i * C + tj] = sum_rows((both[0] + both[1]) + (both[2] + both[3]));
+            f32x4 row;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool in = tj <= ti + r && dec.count[ti + r] == cj;
-                        const float w = p.scale * __builtin_amdgcn_exp2f((float)(dec.logs[ti + r] - lj));
-                        const float sw = s[r] * w;
-                        both[r] = in ? sw * d[r] : 0.0f;
-                        s[r] = in ? sw : 0.0f;
-                        d[r] = in ? d[r] * w : 0.0f;
-                    }
-                    *(vec4*)(pa + tj * LC + ti) = Mx<T>::narrow(s);
-                    *(vec4*)(pd + tj * LC + ti) = Mx<T>::narrow(d);
-                    if (i == j && (j & 1) == 1) {
-                        const vec4 z = {};
-                        *(vec4*)(pa + tj * LC + ti - 16) = z;
-                        *(vec4*)(pd + tj * LC + ti - 16) = z;
-                    }
-                    float col = (both[0] + both[1]) + (both[2] + both[3]);
-                    col += __shfl_xor(col, 16);
-                    col += __shfl_xor(col, 32);
-                    if (grp == 0) cols[i * C + tj] = col;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float x = both[r];
-                        x += __shfl_xor(x, 1);
-                        x += __shfl_xor(x, 2);
-                        x += __shfl_xor(x, 4);
-                        x += __shfl_xor(x, 8);
-                        if (l16 == 0) rows[j * C + ti + r] = x;
-                    }
-                }
+            for (int r = 0; r < 4; ++r) row[r] = sum16(both[r]);
+            *(f32x4*)(rows + j * C + ti) = row;
         }
         __syncthreads();
 
         const float all = dec.head[C - 1];
-        auto work = [&](auto own, const T* across, int la, const T* scores, const T* fold, const T* add,
-                        T* out, int width) {
-            // own (0: dk, 1: dv); across: rows that dS multiplies (v or k);
-            // scores and fold: dk_j += scores_ij fold_i; add: the other tensor of dS's update
-            constexpr int O = decltype(own)::value;
-            constexpr int DM = O == 0 ? DV : DK, DN = O == 0 ? DK : DV;  // dS rows, columns
-            constexpr int NS = O == 0 ? NT : NT == 2 ? 2 : 1;
+        // across: rows that dS multiplies (v or k); scores and fold: out_j += scores_ij fold_i; add: the other
+        // tensor of dS's update
+        auto work = [&](auto is_dk, const T* across, const T* scores, const T* fold, const T* add, T* out) {
+            constexpr bool kSums = decltype(is_dk)::value;
+            const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
+            constexpr int NS = kSums ? NT : NT == 2 ? 2 : 1;
+            const __amdgpu_buffer_rsrc_t orows = rows_at(out + tb0 * p.heads * width);
+            const uint32_t ostep = (uint32_t)p.heads * (uint32_t)width * (uint32_t)sizeof(T);
+            const uint32_t orow = (uint32_t)again(l16) * ostep;
+            float kdot[IT] = {};
 #pragma unroll
-            for (int n = 0; n < DN / 64; ++n) {
+            for (int n = 0; n < MW; ++n) {
                 const int nt = w4 + 4 * n;
-                typename Mx<T>::frag ff[C / 32];
+                frag ff[C / 32];
 #pragma unroll
-                for (int i = 0; i < C / 32; ++i)
-                    ff[i] = frag_at<T>(fold + (16 * nt + l16) * LC + 32 * i + 8 * grp);
-                Split<T, NS> sf[DM / 32];
+                for (int i = 0; i < C / 32; ++i) ff[i] = cols_of.any(fold, nt, i);
+                f32x4 sx[IT] = {};
 #pragma unroll
-                for (int k = 0; k < DM / 32; ++k)
-                    sf[k].set(join8(S[2 * k][n], S[2 * k + 1][n]) * StateScale<T>::down);
+                for (int k = 0; k < D / 32; ++k) {
+                    Split<T, NS> sf;
+                    sf.set(join8(S[2 * k][n], S[2 * k + 1][n]) * StateScale<T>::down);
+#pragma unroll
+                    for (int j = 0; j < IT; ++j)
+                        sx[j] = mma_split<T, NS, true>(sf, frag_at<T>(across + (16 * j + l16) * LD + 32 * k + 8 * grp), sx[j]);
+                }
 #pragma unroll
                 for (int j = 0; j < IT; ++j) {
                     const int tj = 16 * j + l16;
-                    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int k = 0; k < DM / 32; ++k)
-                        x = mma_split<T, NS, true>(sf[k], frag_at<T>(across + tj * la + 32 * k + 8 * grp), x);
-                    x = x * (StateScale<T>::up * dec.tail[tj]);
-                    if constexpr (O == 0) {
-                        const f32x4 kk = Mx<T>::widen(*(const vec4*)(kr + tj * LK + perm4(4 * nt + grp)));
-                        float q = x[0] * kk[0] + x[1] * kk[1] + x[2] * kk[2] + x[3] * kk[3];
-                        q += __shfl_xor(q, 16);
-                        q += __shfl_xor(q, 32);
-                        if (grp == 0) {
-                            if (n == 0) part[w4 * C + tj] = q;
-                            else part[w4 * C + tj] += q;
-                        }
+                    f32x4 x = sx[j] * (StateScale<T>::up * dec.tail[tj]);
+                    if constexpr (kSums) {
+                        const f32x4 kk = Mx<T>::widen(*(const vec4*)(kr + tj * LD + perm4(4 * nt + grp)));
+                        kdot[j] += x[0] * kk[0] + x[1] * kk[1] + x[2] * kk[2] + x[3] * kk[3];
                     }
 #pragma unroll
                     for (int i = j / 2; i < C / 32; ++i)
                         x = Mx<T>::mma(ff[i], frag_at<T>(scores + tj * LC + 32 * i + 8 * grp), x);
-                    const int ch = 16 * nt + 4 * grp;
-                    if (tb0 + tj < t1 && ch < width) {
-                        T* q = out + (tb0 + tj) * p.heads * width + ch;
-                        const vec4 y = Mx<T>::narrow(x);
-                        if ((width & 3) == 0) {
-                            *(vec4*)q = y;
-                        } else {
-                            const T* e = (const T*)&y;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (ch + r < width) q[r] = e[r];
-                        }
-                    }
+                    store_row4<T>(orows, orow + 16 * j * ostep, tj < left, 16 * nt + 4 * grp, width, x);
                 }
+                hold_schedule<(D > 64)>();
                 constexpr bool kLead = Mx<T>::kTerms == 2;
                 const float* f = kLead ? dec.inner : dec.head;
                 const float lead = kLead ? p.scale * dec.head[0] : 1.0f;
@@ -548,38 +638,48 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                     y[i].set(Mx<T>::widen8(ff[i]) * (kLead ? w : w * p.scale));
                 }
 #pragma unroll
-                for (int m = 0; m < DM / 16; ++m)
-                    S[m][n] = update<T>(S[m][n], all, lead, y,
-                                        [&](int i) { return frag_at<T>(add + (16 * m + l16) * LC + 32 * i + 8 * grp); });
+                for (int m = 0; m < MT; ++m)
+                    S[m][n] = update<T>(S[m][n], all, lead, y, [&](int i) { return cols_of(add, m, i); });
+                hold_schedule<(D > 64)>();
             }
+            if constexpr (kSums) store_token_sums<IT>(part + w4 * C, kdot, lane, grp);
         };
-        if (own_k) work(std::integral_constant<int, 0>{}, vr, LV, pd, qt, dt, kout, p.dk);
-        else work(std::integral_constant<int, 1>{}, kr, LK, pa, dt, qt, vout, p.dv);
+        if (own_k) work(std::true_type{}, vr, pd, qt, dt, kout);
+        else work(std::false_type{}, kr, pa, dt, qt, vout);
         __syncthreads();
 
-        if (wave == 0) {
-            // per token: q . dq - k . dk, then the sum from each token to the chunk's end
-            double x = 0.0;
-            if (lane < C) {
-                float r = rq_now, k = (part[lane] + part[C + lane]) + (part[2 * C + lane] + part[3 * C + lane]);
-                const int it = lane >> 4;
-                for (int j = 0; j <= it; ++j) r += rows[j * C + lane];
-                for (int i = it; i < IT; ++i) k += cols[i * C + lane];
-                x = (double)r - (double)k;
-            }
+        const int held = c % kGradHold;
+        if (wave == 7 && lane < C) {
+            float r = rq_now, k = (part[lane] + part[C + lane]) + (part[2 * C + lane] + part[3 * C + lane]);
+            const int it = lane >> 4;
 #pragma unroll
-            for (int k = 1; k < C; k <<= 1) {
-                const int2 v = __builtin_bit_cast(int2, x);
-                const double o = __builtin_bit_cast(double, make_int2(__shfl_down(v.x, k), __shfl_down(v.y, k)));
-                if (lane + k < C) x += o;
+            for (int x = 0; x < IT; ++x) {
+                const float rx = rows[x * C + lane], cx = cols[x * C + lane];
+                r += x <= it ? rx : 0.0f;
+                k += x >= it ? cx : 0.0f;
             }
-            const int2 v = __builtin_bit_cast(int2, x);
-            const double first = __builtin_bit_cast(double, make_int2(__shfl(v.x, 0), __shfl(v.y, 0)));
-            if (lane < C && tb0 + lane < t1) {
-                const bool reset = g_now * 1.44269504088896340736f < kResetLog2;
-                p.dg[(b * p.N + tb0 + lane) * p.heads + h] = reset ? 0.0f : (float)(over + x);
+            hold[held * C + lane] = r - k;
+            if (lane == 0) resets[held] = resets_now;
+        }
+        if (held == kGradHold - 1 || c == nchunk - 1) {
+            // chunk held - h (h from 0: the first of them in time) follows all later held ones
+            __syncthreads();
+            for (int x = wave; x <= held; x += 8) {
+                const double s = scan_f64(lane < C ? (double)hold[x * C + C - 1 - lane] : 0.0);
+                if (lane == C - 1) sums[x] = s;
             }
-            over += first;
+            __syncthreads();
+            for (int x = wave; x <= held; x += 8) {
+                double before = over;
+                for (int y = 0; y < x; ++y) before += sums[y];
+                const double s = scan_f64(lane < C ? (double)hold[x * C + C - 1 - lane] : 0.0);
+                const int t = C - 1 - lane;
+                const int64_t tc = t0 + (int64_t)(nchunk - 1 - (c - held + x)) * C + t;
+                if (lane < C && tc < t1)
+                    p.dg[(b * p.N + tc) * p.heads + h] = resets[x] >> t & 1 ? 0.0f : (float)(before + s);
+            }
+            for (int y = 0; y <= held; ++y) over += sums[y];
+            __syncthreads();
         }
     }
     const int64_t tz = t1 > t0 ? t1 : t0;

@@ -12,11 +12,19 @@ inline hyena_status rec_done()
     return e == hipSuccess ? HYENA_OK : fail(HYENA_ERR_DEVICE, hipGetErrorString(e));
 }
 
+// Rows whose groups of 4 channels are whole, aligned vectors (VEC) have kernels
+// of their own: one load where the others take four.
 template <typename T, int DK, int DV>
 hyena_status rec_states_one(const RecStateArgs& a, int64_t bh, int roles, hipStream_t s)
 {
-    HY_LAUNCH(kernel_label("hyena_rec_states", type_label<T>(), DK, DV), (hyena_rec_states<T, DK, DV>),
-              dim3((unsigned)(bh * a.nseg), (unsigned)roles), dim3(256), 0, s, a);
+    const bool vec = a.x[0].vec && a.y[0].vec && (roles == 1 || (a.x[1].vec && a.y[1].vec));
+    const dim3 grid((unsigned)(bh * a.nseg), (unsigned)roles);
+    if (vec)
+        HY_LAUNCH(kernel_label("hyena_rec_states", type_label<T>(), DK, DV, true), (hyena_rec_states<T, DK, DV, true>), grid,
+                  dim3(256), 0, s, a);
+    else
+        HY_LAUNCH(kernel_label("hyena_rec_states", type_label<T>(), DK, DV, false), (hyena_rec_states<T, DK, DV, false>), grid,
+                  dim3(256), 0, s, a);
     return rec_done();
 }
 
@@ -29,8 +37,14 @@ template <typename T> hyena_status rec_launch_states(const RecStateArgs& a, int6
 template <typename T, int DA, int DC, bool TRANS>
 hyena_status rec_out_one(const RecArgs& a, int64_t bh, hipStream_t s)
 {
-    HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS), (hyena_rec_out<T, DA, DC, TRANS>),
-              dim3((unsigned)(bh * a.nseg)), dim3(256), 0, s, a);
+    const bool vec = a.a.vec && a.b.vec && a.c.vec && (!TRANS || a.r.vec);
+    const dim3 grid((unsigned)(bh * a.nseg));
+    if (vec)
+        HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, true), (hyena_rec_out<T, DA, DC, TRANS, true>),
+                  grid, dim3(256), 0, s, a);
+    else
+        HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, false), (hyena_rec_out<T, DA, DC, TRANS, false>),
+                  grid, dim3(256), 0, s, a);
     return rec_done();
 }
 
@@ -45,17 +59,22 @@ template <typename T> hyena_status rec_launch_out(const RecArgs& a, int64_t bh, 
     return transposed ? rec_out_pick<T, true>(a, bh, s) : rec_out_pick<T, false>(a, bh, s);
 }
 
-template <typename T, int DK, int DV> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
+template <typename T, int D> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
 {
-    HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), DK, DV), (hyena_rec_grad<T, DK, DV>),
-              dim3((unsigned)(bh * a.nseg)), dim3(512), 0, s, a);
+    const bool vec = a.q.vec && a.k.vec && a.v.vec && a.o.vec;
+    const dim3 grid((unsigned)(bh * a.nseg));
+    if (vec)
+        HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), D, true), (hyena_rec_grad<T, D, true>), grid, dim3(512), 0,
+                  s, a);
+    else
+        HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), D, false), (hyena_rec_grad<T, D, false>), grid, dim3(512),
+                  0, s, a);
     return rec_done();
 }
 
 template <typename T> hyena_status rec_launch_grad(const RecGradArgs& a, int64_t bh, hipStream_t s)
 {
-    if (a.dk <= 64) return a.dv <= 64 ? rec_grad_one<T, 64, 64>(a, bh, s) : rec_grad_one<T, 64, 128>(a, bh, s);
-    return a.dv <= 64 ? rec_grad_one<T, 128, 64>(a, bh, s) : rec_grad_one<T, 128, 128>(a, bh, s);
+    return a.dk <= 64 && a.dv <= 64 ? rec_grad_one<T, 64>(a, bh, s) : rec_grad_one<T, 128>(a, bh, s);
 }
 
 template <typename T> hyena_status rec_launch_step(const RecStepArgs& a, int64_t B, hipStream_t s)

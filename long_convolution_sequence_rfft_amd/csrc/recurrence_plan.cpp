@@ -8,11 +8,11 @@
 namespace hy {
 
 namespace {
-// Segments per (row, head): enough for `want` workgroups in all, of at least
-// two chunks of 64 tokens each.
+// Segments per (row, head): as many as give `want` workgroups in all and no
+// more (one round of the chip), of at least two chunks of 64 tokens each.
 void cut(int64_t N, int64_t bh, int64_t want, int32_t& seg, int32_t& nseg)
 {
-    int64_t n = (want + bh - 1) / bh;
+    int64_t n = want / bh;
     const int64_t most = (N + 127) / 128;
     if (n > most) n = most;
     if (n < 1) n = 1;
@@ -30,7 +30,8 @@ hyena_status rec_plan_build(RecPlan& p, int64_t B, int64_t N, int64_t heads, int
         return fail(HYENA_ERR_INVALID_ARGUMENT, "recurrence: B, N, heads, dk and dv must be at least 1");
     if (dk > 128 || dv > 128) return fail(HYENA_ERR_UNSUPPORTED, "recurrence: dk and dv must be in 1..128");
     if (N >= ((int64_t)1 << 31) - 64) return fail(HYENA_ERR_UNSUPPORTED, "recurrence: N must be below 2^31 - 64");
-    if (B > ((int64_t)1 << 24) || heads > ((int64_t)1 << 24) || B * heads > ((int64_t)1 << 24))
+    if (heads > 65536) return fail(HYENA_ERR_UNSUPPORTED, "recurrence: at most 65536 heads");
+    if (B > ((int64_t)1 << 24) || B * heads > ((int64_t)1 << 24))
         return fail(HYENA_ERR_UNSUPPORTED, "recurrence: B * heads must be at most 2^24");
     if (io_dtype != HYENA_F32 && io_dtype != HYENA_BF16 && io_dtype != HYENA_F16)
         return fail(HYENA_ERR_UNSUPPORTED, "recurrence: unknown io dtype");
@@ -41,7 +42,7 @@ hyena_status rec_plan_build(RecPlan& p, int64_t B, int64_t N, int64_t heads, int
     p.dv = (int32_t)dv;
     p.io_dtype = io_dtype;
     const int64_t bh = B * heads;
-    cut(N, bh, kRecForwardGroups, p.seg, p.nseg);
+    cut(N, bh, dk <= 64 && dv <= 64 ? kRecForwardGroups : kRecWideGroups, p.seg, p.nseg);
     cut(N, bh, kRecBackwardGroups, p.seg_b, p.nseg_b);
     const size_t state = (size_t)bh * (size_t)(dk * dv) * sizeof(float);
     p.forward_bytes = p.nseg == 1 ? 0 : align256(state * (p.nseg + 1)) + align256((size_t)bh * p.nseg * 4);
@@ -81,6 +82,13 @@ hyena_status check_view(const hyena_view& v, const char* name, size_t element)
         return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(name) + " is not aligned to its element");
     if (v.batch < 0 || v.token < 0 || v.head < 0)
         return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(name) + " has a negative stride");
+    return HYENA_OK;
+}
+
+hyena_status check_token_stride(const hyena_view& v, const char* name, int64_t N)
+{
+    if (N > 1 && v.token >= ((int64_t)1 << 23))
+        return fail(HYENA_ERR_UNSUPPORTED, std::string(name) + " has a token stride of 2^23 elements or more");
     return HYENA_OK;
 }
 

@@ -9,10 +9,16 @@
 
 namespace hy {
 
-// Workgroups that the cut into segments aims at: four (two) for each of the
-// 256 compute units.
-constexpr int64_t kRecForwardGroups = 1024;
-constexpr int64_t kRecBackwardGroups = 512;
+// Workgroups that the cut into segments aims at: one round of those that are
+// resident together.  More segments mean more states to write, scan and read,
+// fewer leave compute units empty.  Measured, all kernels of a call:
+// forward, 64K tokens, 12 heads of 64, bfloat16: 219, 203, 178, 168, 187 us at
+// 256, 384, 512, 768, 1024; 2 x 8K tokens, 6 heads of 128: 92, 85, 85, 97, 97;
+// backward, 2 x 8K tokens, 12 heads of 64: 190, 169, 179, 174, 175 at 192,
+// 256, 384, 512, 768.
+constexpr int64_t kRecForwardGroups = 768;
+constexpr int64_t kRecWideGroups = 512;  // forward, dk or dv above 64
+constexpr int64_t kRecBackwardGroups = 256;
 
 struct RecPlan {
     int64_t B = 0, N = 0, heads = 0;
@@ -47,6 +53,8 @@ struct Span {
     size_t bytes;
 };
 hyena_status check_view(const hyena_view& v, const char* name, size_t element);
+// The recurrence's kernels address the tokens of a chunk by 32-bit byte offsets.
+hyena_status check_token_stride(const hyena_view& v, const char* name, int64_t N);
 Span view_span(const hyena_view& v, int64_t B, int64_t N, int64_t heads, int64_t width, size_t element);
 bool spans_overlap(const Span& a, const Span& b);
 
