@@ -55,12 +55,12 @@ namespace {
 
 bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 
-// A view as the kernels take it: vec, whether each group of 4 channels can be
-// read as one vector (rows of such groups, their ends included, are in bounds).
+// A view as the kernels take it: vec, whether a row is made of whole, aligned
+// 16-byte vectors.
 RView rview(const hyena_view& v, int64_t width, size_t element)
 {
-    const bool vec = width % 4 == 0 && aligned(v.data, 4 * element) && v.batch % 4 == 0 &&
-                     v.token % 4 == 0 && v.head % 4 == 0;
+    const int64_t w = 16 / (int64_t)element;
+    const bool vec = width % w == 0 && aligned(v.data, 16) && v.batch % w == 0 && v.token % w == 0 && v.head % w == 0;
     return RView{v.data, v.batch, v.token, v.head, vec ? 1 : 0};
 }
 

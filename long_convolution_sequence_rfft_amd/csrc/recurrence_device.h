@@ -84,16 +84,34 @@ template <> struct Mx<_Float16> {
 
 // A float32 operand as NT fragments whose sum (binary16: first + 2^-11 second)
 // is the operand: NT = kTerms keeps float32 accuracy, NT = 1 rounds to T.
+// bfloat16 terms before the last are cut, not rounded: the upper half of the
+// word, then that of the exact remainder; three cut terms are all 24 bits.
 template <typename T, int NT> struct Split {
     typename Mx<T>::frag f[NT];
     __device__ __forceinline__ void set(f32x8 x)
     {
+        if constexpr (Mx<T>::kTerms == 3 && NT > 1) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            f[n] = Mx<T>::narrow8(x);
-            if (n + 1 < NT) {
-                x = x - Mx<T>::widen8(f[n]);
-                if constexpr (sizeof(T) == 2 && Mx<T>::kTerms == 2) x = x * 2048.0f;
+            for (int n = 0; n < NT; ++n) {
+                if (n + 1 == NT && NT < 3) {
+                    f[n] = Mx<T>::narrow8(x);
+                    break;
+                }
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)  // the upper halves of two words
+                    w[e] = __builtin_amdgcn_perm(__float_as_uint(x[2 * e + 1]), __float_as_uint(x[2 * e]), 0x07060302);
+                f[n] = __builtin_bit_cast(typename Mx<T>::frag, w);
+                if (n + 1 < NT) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] -= __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                f[n] = Mx<T>::narrow8(x);
+                if (n + 1 < NT) x = (x - Mx<T>::widen8(f[n])) * 2048.0f;
             }
         }
     }
@@ -170,7 +188,7 @@ template <typename T> constexpr int kPad = 16 / (int)sizeof(T);
 struct RView {
     const void* p;
     int64_t b, t, h;
-    int32_t vec;  // rows of 4-channel groups can be read as one vector each
+    int32_t vec;  // each 16 bytes of a row are one aligned vector
 };
 
 // Rows of one (batch row, head) of a tensor, read and written through a buffer
@@ -270,19 +288,20 @@ template <typename T, int C> __device__ __forceinline__ int col_at(int channel, 
     return channel * C + (((token / U) ^ ((channel ^ (channel >> 3)) & 7)) * U) + token % U;
 }
 
-// C tokens x D channels of a tensor as blocks of 4 tokens x 4 channels, held
-// in registers between the global load and the LDS store.
-template <typename T, int C, int D, int THREADS> struct Tile {
+// C tokens x D channels of a tensor, held in registers between the global load
+// and the LDS store as blocks of R tokens x W channels, W channels being 16
+// bytes: lanes follow the rows, so that a load instruction asks for whole
+// 128-byte lines (with 64-byte pieces of rows, and 8-byte loads, the reading
+// rate fell from 5.8 to 4.0 TB/s).  Blocks of 4 tokens can be stored transposed.
+template <typename T, int C, int D, int THREADS, int R> struct Tile {
     using vec4 = typename Mx<T>::vec4;
-    static constexpr int kBlocks = (C / 4) * (D / 4);
+    static constexpr int W = 16 / (int)sizeof(T), V = W / 4;
+    static constexpr int kBlocks = (C / R) * (D / W);
     static constexpr int kPer = (kBlocks + THREADS - 1) / THREADS;
-    vec4 x[kPer][4];
+    vec4 x[kPer][R][V];
 
-    // First token and channel of block b: lanes follow the rows, so that a load
-    // instruction asks for whole 128-byte lines (with 64-byte pieces of rows the
-    // reading rate fell from 5.8 to 4.0 TB/s).
-    static __device__ __forceinline__ int token(int b) { return 4 * (b / (D / 4)); }
-    static __device__ __forceinline__ int channel(int b) { return 4 * (b % (D / 4)); }
+    static __device__ __forceinline__ int token(int b) { return R * (b / (D / W)); }
+    static __device__ __forceinline__ int channel(int b) { return W * (b % (D / W)); }
 
     // Byte offsets of a thread's blocks from the stream's place: kept through the
     // loop, kOutside where the block's channels do not exist.
@@ -301,31 +320,26 @@ template <typename T, int C, int D, int THREADS> struct Tile {
 
     // The first n tokens of the stream from its place on; tokens at n and after
     // it, and channels at `width` and after it, are zero and not read.  VEC:
-    // each group of 4 channels is one vector.
+    // each group of W channels is one vector.
     template <bool VEC> __device__ __forceinline__ void load(const Stream& s, const Places& at, int n, int width, int tid)
     {
         const __amdgpu_buffer_rsrc_t rsrc = rows_at(s.p);
-        if (VEC && n >= C) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[i][r] = load4<T>(rsrc, at.off[i], r * s.step);
-            return;
-        }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int t = token(tid + i * THREADS), c = channel(tid + i * THREADS);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < R; ++r) {
                 const uint32_t off = t + r < n ? at.off[i] : kOutside;
                 if constexpr (VEC) {
-                    x[i][r] = load4<T>(rsrc, off, r * s.step);
+                    *(u32x4*)x[i][r] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)off, (int)(r * s.step), 0));
                 } else {
-                    T e[4];
+                    T e[W];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        e[j] = load1<T>(rsrc, c + j < width && off != kOutside ? off + j * (uint32_t)sizeof(T) : kOutside, r * s.step);
-                    x[i][r] = *(const vec4*)e;
+                    for (int j = 0; j < W; ++j)
+                        e[j] = load1<T>(rsrc, (c + j < width) & (off != kOutside) ? off + j * (uint32_t)sizeof(T) : kOutside,
+                                        r * s.step);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) x[i][r][v] = *(const vec4*)(e + 4 * v);
                 }
             }
         }
@@ -337,25 +351,56 @@ template <typename T, int C, int D, int THREADS> struct Tile {
         for (int i = 0; i < kPer; ++i) {
             const int b = tid + i * THREADS;
             if (kBlocks % THREADS != 0 && b >= kBlocks) break;
-            const int c = perm4(channel(b) / 4), t = token(b);
+            const int c = channel(b), t = token(b);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) *(vec4*)(lds + (t + r) * LD + c) = x[i][r];
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < V; ++v) *(vec4*)(lds + (t + r) * LD + perm4(c / 4 + v)) = x[i][r][v];
         }
     }
     // cols[channel][token], in units of 16 bytes swapped within a row (col_at)
     __device__ __forceinline__ void store_cols(T* lds, int tid) const
     {
+        static_assert(R == 4, "a column's piece is a vector");
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int b = tid + i * THREADS;
             if (kBlocks % THREADS != 0 && b >= kBlocks) break;
             const int c = channel(b), t = token(b);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                vec4 v = {x[i][0][j], x[i][1][j], x[i][2][j], x[i][3][j]};
+            for (int j = 0; j < W; ++j) {
+                vec4 v = {x[i][0][j / 4][j % 4], x[i][1][j / 4][j % 4], x[i][2][j / 4][j % 4], x[i][3][j / 4][j % 4]};
                 *(vec4*)(lds + col_at<T, C>(c + j, t)) = v;
             }
         }
+    }
+};
+
+// The elements of a tensor under a tile of results (column = token 16 i + l16,
+// rows = channels 16 t + 4 grp ..), read straight into that place.
+template <typename T, int IT, int CW> struct UnderResults {
+    typename Mx<T>::vec4 x[IT][CW];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const Stream& s, int n, int width, int l16, int grp, int wave)
+    {
+        const __amdgpu_buffer_rsrc_t rsrc = rows_at(s.p);
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int v = 0; v < CW; ++v) {
+                const int c = 16 * (wave + 4 * v) + 4 * grp;
+                const uint32_t off = (uint32_t)l16 * s.step + (uint32_t)c * (uint32_t)sizeof(T);
+                const bool in = 16 * i + l16 < n;
+                if constexpr (VEC) {
+                    x[i][v] = load4<T>(rsrc, in & (c < width) ? off : kOutside, 16 * i * s.step);
+                } else {
+                    T e[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        e[j] = load1<T>(rsrc, in & (c + j < width) ? off + j * (uint32_t)sizeof(T) : kOutside, 16 * i * s.step);
+                    x[i][v] = *(const typename Mx<T>::vec4*)e;
+                }
+            }
     }
 };
 

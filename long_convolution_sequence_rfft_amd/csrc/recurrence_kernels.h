@@ -57,8 +57,8 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
     constexpr int C = kRecChunk<T>, NT = Mx<T>::kTerms;
     constexpr int KT = DK / 16, VW = DV / 64;
     using frag = typename Mx<T>::frag;
-    __shared__ __attribute__((aligned(16))) T xt[DK * C];
-    __shared__ __attribute__((aligned(16))) T yt[DV * C];
+    __shared__ __attribute__((aligned(16))) T xt[(DK > DV ? DK : DV) * C];
+    __shared__ __attribute__((aligned(16))) T yt[(DK > DV ? DK : DV) * C];
     __shared__ DecaysOf<T> decays[kDecayBatch];
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
@@ -74,25 +74,25 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
 
     f32x4 S[KT][VW] = {};
     float total = 1.0f;
-    Tile<T, C, DK, 256> tx;
-    Tile<T, C, DV, 256> ty;
-    // the chunks are walked forward (role 0) or from the last one back
-    Stream xs, ys, gs;
+    // the chunks are walked forward (role 0) or from the last one back; two
+    // waves bring in x, two y
+    const bool is_x = wave < 2;
+    constexpr int DM = DK > DV ? DK : DV;
+    using Half = Tile<T, C, DM, 128, 4>;
+    Half tile;
+    Stream xs, gs;
     const int64_t first = t0 + (role ? (int64_t)(nchunk - 1) * C : 0);
     const int way = role ? -C : C;
-    xs.start<T>(p.x[role], b, h, first);
-    ys.start<T>(p.y[role], b, h, first);
+    xs.start<T>(is_x ? p.x[role] : p.y[role], b, h, first);
     gs.start<float>(p.g, b, h, first + wave * way);
-    const typename Tile<T, C, DK, 256>::Places px(xs, p.dk, tid);
-    const typename Tile<T, C, DV, 256>::Places py(ys, p.dv, tid);
+    const int width = is_x ? p.dk : p.dv, half = tid & 127;
+    const typename Half::Places place(xs, width, half);
     const int len = (int)(t1 - t0);
     // tokens of the c-th chunk walked
     auto tokens = [&](int c) { return len - (role ? nchunk - 1 - c : c) * C; };
     auto fetch = [&](int c) {
-        tx.template load<VEC>(xs, px, tokens(c), p.dk, tid);
-        ty.template load<VEC>(ys, py, tokens(c), p.dv, tid);
+        tile.template load<VEC>(xs, place, tokens(c), width, half);
         xs.move(way);
-        ys.move(way);
     };
     float g = 0.0f;
     auto fetch_g = [&](int c) {
@@ -107,8 +107,7 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
         const int slot = c % kDecayBatch;
         if (slot == 0 && wave < kDecayBatch) fill_decays<C, Mx<T>::kTerms == 2>(decays[wave], g, lane);
         const DecaysOf<T>& dec = decays[slot];
-        tx.store_cols(xt, tid);
-        ty.store_cols(yt, tid);
+        tile.store_cols(is_x ? xt : yt, half);
         __syncthreads();
         if (c + 1 < nchunk) {
             fetch(c + 1);
@@ -154,8 +153,8 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
 // LDS of the two kernels below.
 template <typename T, int DA, int DC, bool TRANS> constexpr size_t rec_out_lds()
 {
-    constexpr int C = kRecChunk<T>, LA = DA + kPad<T>, LR = DC + kPad<T>, LC = C + kPad<T>;
-    return sizeof(T) * (size_t)(2 * C * LA + DA * C + DC * C + C * LC + (TRANS ? C * LR : 0)) +
+    constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
+    return sizeof(T) * (size_t)(C * LA + C * LB + 2 * DM * C + C * LC) +
            kDecayBatch * sizeof(DecaysOf<T>) + (TRANS ? 4 * C * sizeof(float) : 0);
 }
 
@@ -174,29 +173,30 @@ template <typename T, int D> constexpr size_t rec_grad_lds()
 // (a_i . b_j) c_j).  a = q, b = k, c = v gives o; a = do, b = v, c = k gives dq
 // (TRANS: the state's rows are then the channels of c).  TRANS also writes
 // rq_i = r_i . (the state's part of out_i), with the state as a split operand
-// so that it keeps float32 accuracy.
+// so that it keeps float32 accuracy.  EXACT: so does the state itself through
+// the segment (needed where it is an output, and for rq); else its updates keep
+// 16 bits, as it only meets q as a 16-bit operand.
 //
 // One workgroup of four waves per (row, head, segment).  Waves share the score
 // tiles of a chunk (written to LDS in storage type) and each owns every fourth
 // 16-channel tile of c: its part of the state never leaves its registers.
 // ---------------------------------------------------------------------------
-template <typename T, int DA, int DC, bool TRANS, bool VEC>
+template <typename T, int DA, int DC, bool TRANS, bool EXACT, bool VEC>
 __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) void hyena_rec_out(RecArgs p)
 {
-    constexpr int C = kRecChunk<T>, LA = DA + kPad<T>, LR = DC + kPad<T>, LC = C + kPad<T>;
-    constexpr int NT = Mx<T>::kTerms;                              // state update
-    constexpr int NS = TRANS ? NT : NT == 2 ? 2 : 1;               // state as an operand
+    constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
+    constexpr int NT = EXACT || Mx<T>::kTerms < 2 ? Mx<T>::kTerms : 2;  // state update
+    constexpr int NS = TRANS ? Mx<T>::kTerms : Mx<T>::kTerms == 2 ? 2 : 1;  // state as an operand
     constexpr int AT = DA / 16, CW = DC / 64, IT = C / 16;
     using frag = typename Mx<T>::frag;
     using vec4 = typename Mx<T>::vec4;
     __shared__ __attribute__((aligned(16))) char smem[rec_out_lds<T, DA, DC, TRANS>()];
     T* ar = (T*)smem;              // [C][LA]
-    T* br = ar + C * LA;           // [C][LA]
-    T* bt = br + C * LA;           // [DA][C] transposed
-    T* ct = bt + DA * C;           // [DC][C] transposed
-    T* ps = ct + DC * C;           // [C][LC]
-    T* rr = ps + C * LC;           // [C][LR], TRANS
-    char* tail = (char*)(rr + (TRANS ? C * LR : 0));
+    T* br = ar + C * LA;           // [C][LB]
+    T* bt = br + C * LB;           // [DM][C] transposed
+    T* ct = bt + DM * C;           // [DM][C] transposed
+    T* ps = ct + DM * C;           // [C][LC]
+    char* tail = (char*)(ps + C * LC);
     DecaysOf<T>* const decays = (DecaysOf<T>*)tail;
     float* part = (float*)(tail + kDecayBatch * sizeof(DecaysOf<T>));  // [4][C], TRANS
 
@@ -229,27 +229,28 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
                 S[k][v][r] = sp && aa < p.da && cc < p.dc ? sp[at] : 0.0f;
             }
 
-    Tile<T, C, DA, 256> ta, tb;
-    Tile<T, C, DC, 256> tc, tr;
-    Stream as, bs, cs, rs, gs;
+    // all waves bring in a, two b and two c
+    const bool is_b = wave < 2;
+    using Rows = Tile<T, C, DA, 256, 1>;
+    using Half = Tile<T, C, DM, 128, 4>;
+    Rows ta;
+    Half tile;
+    UnderResults<T, IT, CW> under;
+    Stream as, xs, rs, gs;
     as.start<T>(p.a, b, h, t0);
-    bs.start<T>(p.b, b, h, t0);
-    cs.start<T>(p.c, b, h, t0);
+    xs.start<T>(is_b ? p.b : p.c, b, h, t0);
     if constexpr (TRANS) rs.start<T>(p.r, b, h, t0);
     gs.start<float>(p.g, b, h, t0 + wave * C);
-    const typename Tile<T, C, DA, 256>::Places pa(as, p.da, tid), pb(bs, p.da, tid);
-    const typename Tile<T, C, DC, 256>::Places pc(cs, p.dc, tid), pr(TRANS ? rs : cs, p.dc, tid);
+    const int width = is_b ? p.da : p.dc, half = tid & 127;
+    const typename Rows::Places pa(as, p.da, tid);
+    const typename Half::Places px(xs, width, half);
     const int len = (int)(t1 - t0);
     auto fetch = [&](int c) {
         const int n = len - c * C;
         ta.template load<VEC>(as, pa, n, p.da, tid);
-        tb.template load<VEC>(bs, pb, n, p.da, tid);
-        tc.template load<VEC>(cs, pc, n, p.dc, tid);
-        if constexpr (TRANS) tr.template load<VEC>(rs, pr, n, p.dc, tid);
+        tile.template load<VEC>(xs, px, n, width, half);
         as.move(C);
-        bs.move(C);
-        cs.move(C);
-        if constexpr (TRANS) rs.move(C);
+        xs.move(C);
     };
     float g = 0.0f;
     auto fetch_g = [&](int c) {
@@ -265,10 +266,13 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
         if (slot == 0 && wave < kDecayBatch) fill_decays<C, Mx<T>::kTerms == 2>(decays[wave], g, lane);
         const DecaysOf<T>& dec = decays[slot];
         ta.template store_rows<LA>(ar, tid);
-        tb.template store_rows<LA>(br, tid);
-        tb.store_cols(bt, tid);
-        tc.store_cols(ct, tid);
-        if constexpr (TRANS) tr.template store_rows<LR>(rr, tid);
+        if (is_b) tile.template store_rows<LB>(br, half);
+        tile.store_cols(is_b ? bt : ct, half);
+        if constexpr (TRANS) {
+            // used at the end of this chunk: a load ahead of the next chunk's
+            under.template load<VEC>(rs, len - c * C, p.dc, l16, grp, wave);
+            rs.move(C);
+        }
         __syncthreads();
         const int64_t tb0 = t0 + (int64_t)c * C;
         const __amdgpu_buffer_rsrc_t orows = rows_at(op + tb0 * ostride);
@@ -302,7 +306,7 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
                 f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int k = 0; k < DA / 32; ++k)
-                    s = Mx<T>::mma(frag_at<T>(br + (16 * j + l16) * LA + 32 * k + 8 * grp), af[k], s);
+                    s = Mx<T>::mma(frag_at<T>(br + (16 * j + l16) * LB + 32 * k + 8 * grp), af[k], s);
                 return s;
             };
             f32x4 own = tile(it), s[IT - 1];
@@ -347,7 +351,7 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
                 const int ti = 16 * i + l16;
                 f32x4 o = so[i] * (p.scale * StateScale<T>::up * dec.head[ti]);
                 if constexpr (TRANS) {
-                    const f32x4 r = Mx<T>::widen(*(const vec4*)(rr + ti * LR + perm4(4 * vt + grp)));
+                    const f32x4 r = Mx<T>::widen(under.x[i][v]);
                     rdot[i] += o[0] * r[0] + o[1] * r[1] + o[2] * r[2] + o[3] * r[3];
                 }
 #pragma unroll
@@ -441,7 +445,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const ColFrags<T, C> cols_of(l16, grp);
     const bool own_k = wave < 4;
-    const int w4 = wave & 3, half = tid & 255;
+    const int w4 = wave & 3, half = tid & 127;
     const int64_t bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
     const int64_t b = bh / p.heads, h = bh % p.heads;
     const int64_t nv = valid_tokens(p.lengths, b, p.N);
@@ -476,26 +480,23 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     double over = ((sums[0] + sums[1]) + (sums[2] + sums[3]));  // <S, dS> after the chunks held
     __syncthreads();
 
-    // two tensors per half of the workgroup: x, also needed transposed (q, do),
-    // and y (k, v)
-    Tile<T, C, D, 256> tx, ty;
-    Stream xs, ys, gs;
+    // two waves bring in each tensor: q and do are also needed transposed
+    const bool is_x = w4 < 2;
+    using Half = Tile<T, C, D, 128, 4>;
+    Half tile;
+    Stream xs, gs;
     const int64_t last = t0 + (int64_t)(nchunk - 1) * C;
-    xs.start<T>(own_k ? p.q : p.o, b, h, last);
-    ys.start<T>(own_k ? p.k : p.v, b, h, last);
+    xs.start<T>(own_k ? is_x ? p.q : p.k : is_x ? p.o : p.v, b, h, last);
     gs.start<float>(p.g, b, h, last - w4 * C);
     const int width = own_k ? p.dk : p.dv;
-    T* const xr = own_k ? qr : dr;
-    T* const yr = own_k ? kr : vr;
+    T* const xr = own_k ? is_x ? qr : kr : is_x ? dr : vr;
     T* const xt = own_k ? qt : dt;
-    const typename Tile<T, C, D, 256>::Places px(xs, width, half), py(ys, width, half);
+    const typename Half::Places px(xs, width, half);
     const int len = (int)(t1 - t0);
     auto fetch = [&](int c) {
         const int n = len - (nchunk - 1 - c) * C;
-        tx.template load<VEC>(xs, px, n, width, half);
-        ty.template load<VEC>(ys, py, n, width, half);
+        tile.template load<VEC>(xs, px, n, width, half);
         xs.move(-C);
-        ys.move(-C);
     };
     // wave w fills the decays of the w-th chunk of a batch, wave 4 + w hands over
     // the state's part of q . dq
@@ -519,9 +520,8 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
         }
         const DecaysOf<T>& dec = decays[slot];
         const int at = D > 64 ? again(half) : half;
-        tx.template store_rows<LD>(xr, at);
-        ty.template store_rows<LD>(yr, at);
-        tx.store_cols(xt, at);
+        tile.template store_rows<LD>(xr, at);
+        if (is_x) tile.store_cols(xt, at);
         __syncthreads();
         const int64_t tb0 = t0 + (int64_t)(nchunk - 1 - c) * C;
         const int left = t1 - tb0 < C ? (int)(t1 - tb0) : C;

@@ -34,29 +34,34 @@ template <typename T> hyena_status rec_launch_states(const RecStateArgs& a, int6
     return a.dv <= 64 ? rec_states_one<T, 128, 64>(a, bh, roles, s) : rec_states_one<T, 128, 128>(a, bh, roles, s);
 }
 
-template <typename T, int DA, int DC, bool TRANS>
+template <typename T, int DA, int DC, bool TRANS, bool EXACT>
 hyena_status rec_out_one(const RecArgs& a, int64_t bh, hipStream_t s)
 {
     const bool vec = a.a.vec && a.b.vec && a.c.vec && (!TRANS || a.r.vec);
     const dim3 grid((unsigned)(bh * a.nseg));
     if (vec)
-        HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, true), (hyena_rec_out<T, DA, DC, TRANS, true>),
-                  grid, dim3(256), 0, s, a);
+        HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, EXACT, true),
+                  (hyena_rec_out<T, DA, DC, TRANS, EXACT, true>), grid, dim3(256), 0, s, a);
     else
-        HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, false), (hyena_rec_out<T, DA, DC, TRANS, false>),
-                  grid, dim3(256), 0, s, a);
+        HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, EXACT, false),
+                  (hyena_rec_out<T, DA, DC, TRANS, EXACT, false>), grid, dim3(256), 0, s, a);
     return rec_done();
 }
 
-template <typename T, bool TRANS> hyena_status rec_out_pick(const RecArgs& a, int64_t bh, hipStream_t s)
+template <typename T, bool TRANS, bool EXACT> hyena_status rec_out_pick(const RecArgs& a, int64_t bh, hipStream_t s)
 {
-    if (a.da <= 64) return a.dc <= 64 ? rec_out_one<T, 64, 64, TRANS>(a, bh, s) : rec_out_one<T, 64, 128, TRANS>(a, bh, s);
-    return a.dc <= 64 ? rec_out_one<T, 128, 64, TRANS>(a, bh, s) : rec_out_one<T, 128, 128, TRANS>(a, bh, s);
+    if (a.da <= 64)
+        return a.dc <= 64 ? rec_out_one<T, 64, 64, TRANS, EXACT>(a, bh, s) : rec_out_one<T, 64, 128, TRANS, EXACT>(a, bh, s);
+    return a.dc <= 64 ? rec_out_one<T, 128, 64, TRANS, EXACT>(a, bh, s) : rec_out_one<T, 128, 128, TRANS, EXACT>(a, bh, s);
 }
 
+// Only bfloat16 has a cheaper form of the state than the exact one.
 template <typename T> hyena_status rec_launch_out(const RecArgs& a, int64_t bh, bool transposed, hipStream_t s)
 {
-    return transposed ? rec_out_pick<T, true>(a, bh, s) : rec_out_pick<T, false>(a, bh, s);
+    if (transposed) return rec_out_pick<T, true, true>(a, bh, s);
+    if constexpr (Mx<T>::kTerms == 3)
+        if (a.last == nullptr) return rec_out_pick<T, false, false>(a, bh, s);
+    return rec_out_pick<T, false, true>(a, bh, s);
 }
 
 template <typename T, int D> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
