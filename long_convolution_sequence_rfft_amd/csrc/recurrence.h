@@ -67,7 +67,6 @@ struct RecGradArgs {
     const float* rq;       // [bh][N]: q . (state's part of dq)
     const float* start;    // [bh][nseg + 1][dk dv] or NULL (no gradient comes from the end)
     const float* end;      // [bh][nseg + 1][dk dv], or NULL with start
-    float* d_state;        // written with nseg = 1
     int64_t N, heads;
     int32_t dk, dv;
     int32_t seg, nseg;

@@ -189,9 +189,9 @@ hyena_status run_backward(const RecPlan& p, const hyena_recurrence_inputs& in, c
     const RecSpace w = rec_space(p, true, workspace);
     const int64_t bh = p.B * p.heads;
     const size_t e = sizeof(T);
-    // one segment and nothing coming from the end: no state is needed before
-    // the main passes
-    const bool states = p.nseg_b > 1 || d_final != nullptr;
+    // one segment and nothing coming from the end or asked for at the start: no
+    // state is needed before the main passes
+    const bool states = p.nseg_b > 1 || d_final != nullptr || out.d_state != nullptr;
     if (states) {
         const hyena_status st =
             rec_states<T>(p, in, &d_o, d_final, nullptr, out.d_state, w, p.seg_b, p.nseg_b, s);
@@ -230,7 +230,6 @@ hyena_status run_backward(const RecPlan& p, const hyena_recurrence_inputs& in, c
     g.rq = w.rq;
     g.start = states ? w.start : nullptr;
     g.end = states ? w.end : nullptr;
-    g.d_state = states ? nullptr : out.d_state;
     g.N = p.N;
     g.heads = p.heads;
     g.dk = p.dk;

@@ -487,7 +487,8 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     Stream xs, gs;
     const int64_t last = t0 + (int64_t)(nchunk - 1) * C;
     xs.start<T>(own_k ? is_x ? p.q : p.k : is_x ? p.o : p.v, b, h, last);
-    gs.start<float>(p.g, b, h, last - w4 * C);
+    static_assert(kDecayBatch == 2, "two waves fill a batch");
+    gs.start<float>(p.g, b, h, last - (w4 - 2) * C);
     const int width = own_k ? p.dk : p.dv;
     T* const xr = own_k ? is_x ? qr : kr : is_x ? dr : vr;
     T* const xt = own_k ? qt : dt;
@@ -498,25 +499,25 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
         tile.template load<VEC>(xs, px, n, width, half);
         xs.move(-C);
     };
-    // wave w fills the decays of the w-th chunk of a batch, wave 4 + w hands over
-    // the state's part of q . dq
+    // of the waves with less to store, 2 + w fills the decays of the w-th chunk of
+    // a batch and 6 + w hands over the state's part of q . dq
     float g = 0.0f;
     auto fetch_g = [&](int c) {
         const int n = c < nchunk ? len - (nchunk - 1 - c) * C : 0;
-        const bool in = lane < C && lane < n;
+        const bool in = !is_x & (lane < C) & (lane < n);
         if (own_k) g = load1<float>(rows_at(gs.p), in ? lane * gs.step : kOutside);
         else g = load1<float>(rows_at(p.rq + bh * p.N + t0 + (int64_t)(nchunk - 1 - c) * C), in ? lane * 4 : kOutside);
         gs.move(-kDecayBatch * C);
     };
     if (nchunk > 0) {
-        fetch_g(w4);
+        fetch_g(w4 - 2);
         fetch(0);
     }
     for (int c = 0; c < nchunk; ++c) {
         const int slot = c % kDecayBatch;
-        if (slot == 0 && w4 < kDecayBatch) {
-            if (own_k) fill_decays<C, Mx<T>::kTerms == 2>(decays[w4], g, lane);
-            else if (lane < C) rqs[w4 * C + lane] = g;
+        if (slot == 0 && !is_x) {
+            if (own_k) fill_decays<C, Mx<T>::kTerms == 2>(decays[w4 - 2], g, lane);
+            else if (lane < C) rqs[(w4 - 2) * C + lane] = g;
         }
         const DecaysOf<T>& dec = decays[slot];
         const int at = D > 64 ? again(half) : half;
@@ -527,7 +528,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
         const int left = t1 - tb0 < C ? (int)(t1 - tb0) : C;
         if (c + 1 < nchunk) {
             fetch(c + 1);
-            if (slot == 0) fetch_g(c + kDecayBatch + w4);
+            if (slot == 0) fetch_g(c + kDecayBatch + w4 - 2);
         }
         // what the last wave adds up below, read before others may refill it
         float rq_now = 0.0f;
@@ -537,54 +538,89 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
             resets_now = dec.resets;
         }
 
-        // both scores of each pair of tiles: rows i, columns j <= i
-#pragma unroll
-        for (int n = 0; n < (IT * (IT + 1) / 2 + 7) / 8; ++n) {
-            // tiles in the order of (i, j): 0 (0, 0), 1 (1, 0), 2 (1, 1), 3 (2, 0) ..
-            const int at = again_uniform(wave) + 8 * n;
-            if (at >= IT * (IT + 1) / 2) break;
+        // both scores of each pair of tiles: rows i, columns j <= i.  Waves 0 to 3
+        // take the tiles of one's own (an exp2 per pair), 4 and 5 those left of
+        // an odd one, 6 and 7 the two left of tiles 2 and 3 (their decays are
+        // products of two factors); with two tiles, wave 2 takes (1, 0)
+        if (wave < IT) {
             const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
-            const int i = at < 1 ? 0 : at < 3 ? 1 : at < 6 ? 2 : 3, j = at - i * (i + 1) / 2;
-            const int tj = 16 * j + l16, ti = 16 * i + 4 * grp;
-            const bool own = i == j;
+            const int at = again_uniform(wave);
+            const int tj = 16 * at + l16, ti = 16 * at + 4 * grp;
             const double lj = dec.logs[tj];
             const int cj = dec.count[tj];
             double li[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) li[r] = dec.logs[ti + r];
             const i32x4 ci = *(const i32x4*)(dec.count + ti);
-            const f32x4 within = *(const f32x4*)(dec.within + ti);
-            const float crossed = p.scale * dec.cross[i > 0 ? i - 1 : 0][tj];
             f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f}, d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
-                s = Mx<T>::mma(frag_at<T>(qr + (16 * i + l16) * LD + 32 * k + 8 * grp),
-                               frag_at<T>(kr + (16 * j + l16) * LD + 32 * k + 8 * grp), s);
-                d = Mx<T>::mma(frag_at<T>(dr + (16 * i + l16) * LD + 32 * k + 8 * grp),
-                               frag_at<T>(vr + (16 * j + l16) * LD + 32 * k + 8 * grp), d);
+                s = Mx<T>::mma(frag_at<T>(qr + tj * LD + 32 * k + 8 * grp), frag_at<T>(kr + tj * LD + 32 * k + 8 * grp), s);
+                d = Mx<T>::mma(frag_at<T>(dr + tj * LD + 32 * k + 8 * grp), frag_at<T>(vr + tj * LD + 32 * k + 8 * grp), d);
             }
-            f32x4 both;
+            f32x4 w;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                w[r] = (tj <= ti + r) & (ci[r] == cj) ? p.scale * __builtin_amdgcn_exp2f((float)(li[r] - lj)) : 0.0f;
+            // (products that a mask leaves out may not be finite)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const bool in = !own | ((tj <= ti + r) & (ci[r] == cj));
-                const float w = own ? p.scale * __builtin_amdgcn_exp2f((float)(li[r] - lj)) : within[r] * crossed;
-                const float sw = s[r] * w;
-                both[r] = in ? sw * d[r] : 0.0f;
-                s[r] = in ? sw : 0.0f;
-                d[r] = in ? d[r] * w : 0.0f;
+                s[r] = tj <= ti + r ? s[r] * w[r] : 0.0f;
+                d[r] = tj <= ti + r ? d[r] : 0.0f;
             }
+            const f32x4 both = s * d;
+            d = d * w;
             *(vec4*)(pa + tj * LC + ti) = Mx<T>::narrow(s);
             *(vec4*)(pd + tj * LC + ti) = Mx<T>::narrow(d);
-            if (own && (j & 1) == 1) {  // the tile above an odd own one is read with it
+            if (at & 1) {  // the tile above an odd own one is read with it
                 *(vec4*)(pa + tj * LC + ti - 16) = vec4{};
                 *(vec4*)(pd + tj * LC + ti - 16) = vec4{};
             }
             // every lane of a row or column writes the same sum
-            cols[i * C + tj] = sum_rows((both[0] + both[1]) + (both[2] + both[3]));
+            cols[at * C + tj] = sum_rows((both[0] + both[1]) + (both[2] + both[3]));
             f32x4 row;
 #pragma unroll
             for (int r = 0; r < 4; ++r) row[r] = sum16(both[r]);
-            *(f32x4*)(rows + j * C + ti) = row;
+            *(f32x4*)(rows + at * C + ti) = row;
+        } else if (IT == 4 ? wave >= 4 : wave == 2) {
+            const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
+            const int at = again_uniform(wave);
+            // (1, 0), (3, 2), (2, 0) and (2, 1), (3, 0) and (3, 1)
+            const int i = IT == 2 || at == 4 ? 1 : at == 6 ? 2 : 3, j0 = at == 5 ? 2 : 0;
+            const bool two = at >= 6;
+            const int ti = 16 * i + 4 * grp, tr = 16 * i + l16;
+            const f32x4 within = *(const f32x4*)(dec.within + ti) * p.scale;
+            f32x4 s[2] = {}, d[2] = {};
+            float crossed[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) crossed[n] = dec.cross[i - 1][16 * (j0 + n) + l16];
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const frag qf = frag_at<T>(qr + tr * LD + 32 * k + 8 * grp), df = frag_at<T>(dr + tr * LD + 32 * k + 8 * grp);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    if (n == 1 && !two) break;
+                    const int tj = 16 * (j0 + n) + l16;
+                    s[n] = Mx<T>::mma(qf, frag_at<T>(kr + tj * LD + 32 * k + 8 * grp), s[n]);
+                    d[n] = Mx<T>::mma(df, frag_at<T>(vr + tj * LD + 32 * k + 8 * grp), d[n]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (n == 1 && !two) break;
+                const int j = j0 + n, tj = 16 * j + l16;
+                const f32x4 w = within * crossed[n];
+                s[n] = s[n] * w;
+                const f32x4 both = s[n] * d[n];
+                d[n] = d[n] * w;
+                *(vec4*)(pa + tj * LC + ti) = Mx<T>::narrow(s[n]);
+                *(vec4*)(pd + tj * LC + ti) = Mx<T>::narrow(d[n]);
+                cols[i * C + tj] = sum_rows((both[0] + both[1]) + (both[2] + both[3]));
+                f32x4 row;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) row[r] = sum16(both[r]);
+                *(f32x4*)(rows + j * C + ti) = row;
+            }
         }
         __syncthreads();
 
@@ -594,7 +630,8 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
         auto work = [&](auto is_dk, const T* across, const T* scores, const T* fold, const T* add, T* out) {
             constexpr bool kSums = decltype(is_dk)::value;
             const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
-            constexpr int NS = kSums ? NT : NT == 2 ? 2 : 1;
+            constexpr int NS = kSums ? NT : NT == 2 ? 2 : 1;  // dS as an operand
+            constexpr int NU = kSums ? NT : NT < 2 ? NT : 2;  // and in its updates
             const __amdgpu_buffer_rsrc_t orows = rows_at(out + tb0 * p.heads * width);
             const uint32_t ostep = (uint32_t)p.heads * (uint32_t)width * (uint32_t)sizeof(T);
             const uint32_t orow = (uint32_t)again(l16) * ostep;
@@ -631,7 +668,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                 constexpr bool kLead = Mx<T>::kTerms == 2;
                 const float* f = kLead ? dec.inner : dec.head;
                 const float lead = kLead ? p.scale * dec.head[0] : 1.0f;
-                Split<T, NT> y[C / 32];
+                Split<T, NU> y[C / 32];
 #pragma unroll
                 for (int i = 0; i < C / 32; ++i) {
                     const f32x8 w = join8(*(const f32x4*)(f + 32 * i + 8 * grp), *(const f32x4*)(f + 32 * i + 8 * grp + 4));
@@ -686,18 +723,6 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     for (int64_t i = tid; i < (tN - tz) * p.dk; i += 512) kout[(tz + i / p.dk) * p.heads * p.dk + i % p.dk] = T(0);
     for (int64_t i = tid; i < (tN - tz) * p.dv; i += 512) vout[(tz + i / p.dv) * p.heads * p.dv + i % p.dv] = T(0);
     for (int64_t i = tid; i < tN - tz; i += 512) p.dg[(b * p.N + tz + i) * p.heads + h] = 0.0f;
-    if (p.d_state != nullptr && !own_k) {
-        float* out = p.d_state + bh * per;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < MW; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int kk = 16 * m + 4 * grp + r, vv = 16 * (w4 + 4 * n) + l16;
-                    if (kk < p.dk && vv < p.dv) out[kk * p.dv + vv] = S[m][n][r];
-                }
-    }
 }
 
 // ---------------------------------------------------------------------------
