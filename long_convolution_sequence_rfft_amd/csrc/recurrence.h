@@ -29,7 +29,7 @@ struct RecArgs {
     float* rq;             // [bh][N]
     int64_t N, heads;
     int32_t da, dc;
-    int32_t seg, nseg, state_n;
+    int32_t nseg, state_n;
     float scale;
 };
 
@@ -43,7 +43,7 @@ struct RecStateArgs {
     float* decay;          // [bh][nseg]
     int64_t N, heads;
     int32_t dk, dv;
-    int32_t seg, nseg;
+    int32_t nseg;
     float scale;           // role 1
 };
 
@@ -65,11 +65,11 @@ struct RecGradArgs {
     void* dv_out;
     float* dg;
     const float* rq;       // [bh][N]: q . (state's part of dq)
-    const float* start;    // [bh][nseg + 1][dk dv] or NULL (no gradient comes from the end)
-    const float* end;      // [bh][nseg + 1][dk dv], or NULL with start
+    const float* start;    // [bh][nseg every + 1][dk dv] or NULL (no gradient comes from the end)
+    const float* end;      // the same, or NULL with start
     int64_t N, heads;
     int32_t dk, dv;
-    int32_t seg, nseg;
+    int32_t nseg, every;   // its segments are `every` of those that have states
     float scale;
 };
 

@@ -113,7 +113,7 @@ hyena_status launch_scan(const RecScanArgs& a, int roles, hipStream_t s)
 // States before the segments (and, roles = 2, gradients after them).
 template <typename T>
 hyena_status rec_states(const RecPlan& p, const hyena_recurrence_inputs& in, const hyena_view* d_o, const float* d_final,
-                        float* last, float* d_state, const RecSpace& w, int seg, int nseg, hipStream_t s)
+                        float* last, float* d_state, const RecSpace& w, int nseg, hipStream_t s)
 {
     const size_t e = sizeof(T);
     const int roles = d_o ? 2 : 1;
@@ -133,7 +133,6 @@ hyena_status rec_states(const RecPlan& p, const hyena_recurrence_inputs& in, con
     a.heads = p.heads;
     a.dk = p.dk;
     a.dv = p.dv;
-    a.seg = seg;
     a.nseg = nseg;
     a.scale = in.scale;
     hyena_status st = rec_launch_states<T>(a, p.B * p.heads, roles, s);
@@ -158,7 +157,7 @@ hyena_status run_forward(const RecPlan& p, const hyena_recurrence_inputs& in, vo
 {
     const RecSpace w = p.nseg > 1 ? rec_space(p, false, workspace) : RecSpace{};
     if (p.nseg > 1) {
-        const hyena_status st = rec_states<T>(p, in, nullptr, nullptr, last, nullptr, w, p.seg, p.nseg, s);
+        const hyena_status st = rec_states<T>(p, in, nullptr, nullptr, last, nullptr, w, p.nseg, s);
         if (st != HYENA_OK) return st;
     }
     const size_t e = sizeof(T);
@@ -176,7 +175,6 @@ hyena_status run_forward(const RecPlan& p, const hyena_recurrence_inputs& in, vo
     a.heads = p.heads;
     a.da = p.dk;
     a.dc = p.dv;
-    a.seg = p.seg;
     a.nseg = p.nseg;
     a.scale = in.scale;
     return rec_launch_out<T>(a, p.B * p.heads, false, s);
@@ -194,7 +192,7 @@ hyena_status run_backward(const RecPlan& p, const hyena_recurrence_inputs& in, c
     const bool states = p.nseg_b > 1 || d_final != nullptr || out.d_state != nullptr;
     if (states) {
         const hyena_status st =
-            rec_states<T>(p, in, &d_o, d_final, nullptr, out.d_state, w, p.seg_b, p.nseg_b, s);
+            rec_states<T>(p, in, &d_o, d_final, nullptr, out.d_state, w, p.nseg_b * p.every, s);
         if (st != HYENA_OK) return st;
     }
     RecArgs a{};
@@ -206,14 +204,13 @@ hyena_status run_backward(const RecPlan& p, const hyena_recurrence_inputs& in, c
     a.lengths = in.lengths;
     a.out = out.dq;
     a.state = states ? w.start : in.state;
-    a.state_n = states ? p.nseg_b + 1 : 1;
+    a.state_n = states ? p.nseg_b * p.every + 1 : 1;
     a.rq = w.rq;
     a.N = p.N;
     a.heads = p.heads;
     a.da = p.dv;
     a.dc = p.dk;
-    a.seg = p.seg_b;
-    a.nseg = p.nseg_b;
+    a.nseg = p.nseg_b * p.every;
     a.scale = in.scale;
     hyena_status st = rec_launch_out<T>(a, bh, true, s);
     if (st != HYENA_OK) return st;
@@ -234,7 +231,7 @@ hyena_status run_backward(const RecPlan& p, const hyena_recurrence_inputs& in, c
     g.heads = p.heads;
     g.dk = p.dk;
     g.dv = p.dv;
-    g.seg = p.seg_b;
+    g.every = p.every;
     g.nseg = p.nseg_b;
     g.scale = in.scale;
     return rec_launch_grad<T>(g, bh, s);

@@ -548,6 +548,15 @@ __device__ __forceinline__ void fill_decays(Decays<C, INNER>& d, float g, int la
 // w-th of a batch, so the scan's latency is paid once per batch.
 constexpr int kDecayBatch = 2;
 
+// First token of a segment: whole pieces of 64 tokens, spread evenly (segments
+// differ by one piece at most, and every m-th segment of a cut into m n is a
+// segment of the cut into n).
+__device__ __forceinline__ int64_t segment_start(int64_t N, int nseg, int64_t seg)
+{
+    const int64_t t = seg * ((N + 63) / 64) / nseg * 64;
+    return t < N ? t : N;
+}
+
 __device__ __forceinline__ int64_t valid_tokens(const int32_t* lengths, int64_t b, int64_t N)
 {
     if (lengths == nullptr) return N;

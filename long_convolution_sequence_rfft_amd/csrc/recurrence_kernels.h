@@ -68,8 +68,8 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
     const int role = blockIdx.y;
     const int64_t b = bh / p.heads, h = bh % p.heads;
     const int64_t nv = valid_tokens(p.lengths, b, p.N);
-    const int64_t t0 = seg * (int64_t)p.seg;
-    const int64_t t1 = t0 + p.seg < nv ? t0 + p.seg : nv;
+    const int64_t t0 = segment_start(p.N, p.nseg, seg), tN = segment_start(p.N, p.nseg, seg + 1);
+    const int64_t t1 = tN < nv ? tN : nv;
     const int nchunk = t1 > t0 ? (int)((t1 - t0 + C - 1) / C) : 0;
 
     f32x4 S[KT][VW] = {};
@@ -206,8 +206,7 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
     const int64_t bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
     const int64_t b = bh / p.heads, h = bh % p.heads;
     const int64_t nv = valid_tokens(p.lengths, b, p.N);
-    const int64_t t0 = seg * (int64_t)p.seg;
-    const int64_t tN = t0 + p.seg < p.N ? t0 + p.seg : p.N;
+    const int64_t t0 = segment_start(p.N, p.nseg, seg), tN = segment_start(p.N, p.nseg, seg + 1);
     const int64_t t1 = tN < nv ? tN : nv;
     const int nchunk = t1 > t0 ? (int)((t1 - t0 + C - 1) / C) : 0;
     T* const op = (T*)p.out + (b * p.N * p.heads + h) * p.dc;
@@ -449,8 +448,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     const int64_t bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
     const int64_t b = bh / p.heads, h = bh % p.heads;
     const int64_t nv = valid_tokens(p.lengths, b, p.N);
-    const int64_t t0 = seg * (int64_t)p.seg;
-    const int64_t tN = t0 + p.seg < p.N ? t0 + p.seg : p.N;
+    const int64_t t0 = segment_start(p.N, p.nseg, seg), tN = segment_start(p.N, p.nseg, seg + 1);
     const int64_t t1 = tN < nv ? tN : nv;
     const int nchunk = t1 > t0 ? (int)((t1 - t0 + C - 1) / C) : 0;
     T* const kout = (T*)p.dk_out + (b * p.N * p.heads + h) * p.dk;
@@ -459,8 +457,9 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     // gradient of the state after this segment, and its product with the state
     f32x4 S[MT][MW];
     const int64_t per = (int64_t)p.dk * p.dv;
-    const float* ep = p.end ? p.end + (bh * (p.nseg + 1) + seg + 1) * per : nullptr;
-    const float* sp = p.start ? p.start + (bh * (p.nseg + 1) + seg + 1) * per : nullptr;
+    const int64_t entry = (bh * ((int64_t)p.nseg * p.every + 1) + (seg + 1) * p.every) * per;
+    const float* ep = p.end ? p.end + entry : nullptr;
+    const float* sp = p.start ? p.start + entry : nullptr;
     float cross = 0.0f;
 #pragma unroll
     for (int m = 0; m < MT; ++m)

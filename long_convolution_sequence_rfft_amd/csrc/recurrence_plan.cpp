@@ -9,16 +9,13 @@ namespace hy {
 
 namespace {
 // Segments per (row, head): as many as give `want` workgroups in all and no
-// more (one round of the chip), of at least two chunks of 64 tokens each.
-void cut(int64_t N, int64_t bh, int64_t want, int32_t& seg, int32_t& nseg)
+// more (one round of the chip), of at least about 128 tokens each.
+int32_t cut(int64_t N, int64_t bh, int64_t want)
 {
     int64_t n = want / bh;
     const int64_t most = (N + 127) / 128;
     if (n > most) n = most;
-    if (n < 1) n = 1;
-    const int64_t s = ((N + n - 1) / n + 63) / 64 * 64;
-    seg = (int32_t)s;
-    nseg = (int32_t)((N + s - 1) / s);
+    return (int32_t)(n < 1 ? 1 : n);
 }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
@@ -42,16 +39,19 @@ hyena_status rec_plan_build(RecPlan& p, int64_t B, int64_t N, int64_t heads, int
     p.dv = (int32_t)dv;
     p.io_dtype = io_dtype;
     const int64_t bh = B * heads;
-    cut(N, bh, dk <= 64 && dv <= 64 ? kRecForwardGroups : kRecWideGroups, p.seg, p.nseg);
-    cut(N, bh, kRecBackwardGroups, p.seg_b, p.nseg_b);
+    p.nseg = cut(N, bh, dk <= 64 && dv <= 64 ? kRecForwardGroups : kRecWideGroups);
+    p.nseg_b = cut(N, bh, kRecBackwardGroups);
+    p.every = cut(N, bh, kRecStateGroups) / p.nseg_b;
+    if (p.every < 1) p.every = 1;
     const size_t state = (size_t)bh * (size_t)(dk * dv) * sizeof(float);
     p.forward_bytes = p.nseg == 1 ? 0 : align256(state * (p.nseg + 1)) + align256((size_t)bh * p.nseg * 4);
-    p.backward_bytes = 2 * align256(state * (p.nseg_b + 1)) + align256((size_t)bh * p.nseg_b * 4) +
+    const size_t n = (size_t)p.nseg_b * p.every;
+    p.backward_bytes = 2 * align256(state * (n + 1)) + align256((size_t)bh * n * 4) +
                        align256((size_t)bh * (size_t)N * 4);
-    log_msg("recurrence plan: B %lld N %lld heads %lld dk %lld dv %lld dtype %d, segments %d x %d (backward %d x %d), "
+    log_msg("recurrence plan: B %lld N %lld heads %lld dk %lld dv %lld dtype %d, segments %d (backward %d, %d), "
             "workspace %zu (backward %zu)",
-            (long long)B, (long long)N, (long long)heads, (long long)dk, (long long)dv, (int)io_dtype, p.nseg, p.seg,
-            p.nseg_b, p.seg_b, p.forward_bytes, p.backward_bytes);
+            (long long)B, (long long)N, (long long)heads, (long long)dk, (long long)dv, (int)io_dtype, p.nseg,
+            p.nseg_b, p.nseg_b * p.every, p.forward_bytes, p.backward_bytes);
     return HYENA_OK;
 }
 
@@ -60,7 +60,7 @@ RecSpace rec_space(const RecPlan& p, bool backward, void* workspace)
     RecSpace w;
     if (workspace == nullptr) return w;
     const size_t bh = (size_t)(p.B * p.heads);
-    const size_t n = (size_t)(backward ? p.nseg_b : p.nseg);
+    const size_t n = backward ? (size_t)p.nseg_b * p.every : (size_t)p.nseg;
     const size_t states = align256(bh * (size_t)p.dk * (size_t)p.dv * sizeof(float) * (n + 1));
     char* at = (char*)workspace;
     w.start = (float*)at;

@@ -15,19 +15,21 @@ namespace hy {
 // forward, 64K tokens, 12 heads of 64, bfloat16: 219, 203, 178, 168, 187 us at
 // 256, 384, 512, 768, 1024; 2 x 8K tokens, 6 heads of 128: 92, 85, 85, 97, 97;
 // backward, 2 x 8K tokens, 12 heads of 64: 190, 169, 179, 174, 175 at 192,
-// 256, 384, 512, 768.
+// 256, 384, 512, 768, and, with its states and dq in finer segments (256, 512,
+// 768, 1024): 155, 150, 153, 160.
 constexpr int64_t kRecForwardGroups = 768;
-constexpr int64_t kRecWideGroups = 512;  // forward, dk or dv above 64
+constexpr int64_t kRecWideGroups = 384;  // forward, dk or dv above 64
 constexpr int64_t kRecBackwardGroups = 256;
+constexpr int64_t kRecStateGroups = 512;
 
 struct RecPlan {
     int64_t B = 0, N = 0, heads = 0;
     int32_t dk = 0, dv = 0;
     int32_t io_dtype = HYENA_F32;
-    // The sequence is cut into nseg segments of seg tokens (a multiple of 64)
-    // that run in parallel; nseg_b, seg_b: the backward pass's own cut.
-    int32_t seg = 0, nseg = 0;
-    int32_t seg_b = 0, nseg_b = 0;
+    // The sequence is cut into nseg segments that run in parallel; the backward
+    // pass's dk and dv into nseg_b, its states and dq into nseg_b * every.
+    int32_t nseg = 0;
+    int32_t nseg_b = 0, every = 1;
     size_t forward_bytes = 0, backward_bytes = 0;
 };
 

@@ -12,6 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -149,17 +150,15 @@ def load():
             lib.hyena_nd_mixer_forward.argtypes = [p, ctypes.POINTER(NdMixer), p, p, p, p, p]
             lib.hyena_filter_spectrum_implicit.argtypes = [p, ctypes.POINTER(ImplicitFilter), p, p,
                                                            p, p]
-            pin, pout = ctypes.POINTER(RecurrenceInputs), ctypes.POINTER(RecurrenceGrads)
-            pview, pqk = ctypes.POINTER(View), ctypes.POINTER(QkNorm)
             lib.hyena_recurrence_create.argtypes = [ctypes.POINTER(p), i64, i64, i64, i64, i64, i32]
             lib.hyena_recurrence_query.argtypes = [p, ctypes.POINTER(sz), ctypes.POINTER(sz)]
-            lib.hyena_recurrence_forward.argtypes = [p, pin, p, p, p, p]
-            lib.hyena_recurrence_backward.argtypes = [p, pin, pview, p, pout, p, p]
-            lib.hyena_recurrence_step.argtypes = [p, pin, p, i64, p, p, p]
+            lib.hyena_recurrence_forward.argtypes = [p, p, p, p, p, p]
+            lib.hyena_recurrence_backward.argtypes = [p, p, p, p, p, p, p]
+            lib.hyena_recurrence_step.argtypes = [p, p, p, i64, p, p, p]
             lib.hyena_recurrence_destroy.argtypes = [p]
-            lib.hyena_qk_norm_forward.argtypes = [pqk, p, p, p]
-            lib.hyena_qk_norm_scratch_bytes.argtypes = [pqk, ctypes.POINTER(sz)]
-            lib.hyena_qk_norm_backward.argtypes = [pqk, pview, pview] + [p] * 6
+            lib.hyena_qk_norm_forward.argtypes = [p, p, p, p]
+            lib.hyena_qk_norm_scratch_bytes.argtypes = [p, ctypes.POINTER(sz)]
+            lib.hyena_qk_norm_backward.argtypes = [p] * 9
             for name in ("hyena_plan_create", "hyena_plan_create_ex", "hyena_plan_query",
                          "hyena_plan_path",
                          "hyena_workspace_init", "hyena_workspace_release",
@@ -305,7 +304,8 @@ def hyena_timing_release():
 
 
 def _ref(x):
-    return ctypes.byref(x) if x is not None else None
+    """Address of a structure; the wrapper's packed bytes stand for themselves."""
+    return ctypes.byref(x) if isinstance(x, ctypes.Structure) else x
 
 
 def hyena_recurrence_create(B, N, heads, dk, dv, io_dtype=HYENA_F32, check=True):
@@ -565,7 +565,11 @@ class Plan:
 
 
 class _Mixer:
-    """Checks and stream plumbing shared by the operators on q, k and v."""
+    """Checks and stream plumbing shared by the operators on q, k and v.
+
+    A call's structures are packed in one go (their layouts are those of View,
+    RecurrenceInputs and QkNorm): a decoded token's kernel takes a few
+    microseconds, and so may not its arguments."""
 
     def _place(self, io_dtype, device):
         import torch
@@ -580,24 +584,30 @@ class _Mixer:
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
+        self._first_stream = self._stream()
 
     def _stream(self):
-        return self.torch.cuda.current_stream(self.device).cuda_stream
+        return self.torch._C._cuda_getCurrentRawStream(self.device.index)
 
-    def _on_device(self):
+    def _call(self, where, fn, *args):
         # launches go to the current device; a plan of another one makes its own current
         cuda = self.torch.cuda
         if cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        return cuda.device(self.device)
+            st = fn(*args)
+        else:
+            with cuda.device(self.device):
+                st = fn(*args)
+        if st != HYENA_OK:
+            _check(st, where)
 
-    def _keep(self, buffer):
-        """The buffer the plan owns may be used on a stream other than the one
-        it was allocated on: its memory is not given out again before that
-        stream's work is done."""
+    def _keep(self, buffer, stream):
+        """Address of a buffer the plan owns.  It may be used on a stream other
+        than the one it was allocated on: its memory is not given out again
+        before that stream's work is done."""
         if buffer is None:
             return None
-        buffer.record_stream(self.torch.cuda.current_stream(self.device))
+        if stream != self._first_stream:
+            buffer.record_stream(self.torch.cuda.current_stream(self.device))
         return buffer.data_ptr()
 
     def _check_tensor(self, t, name, shape, dtype):
@@ -607,33 +617,48 @@ class _Mixer:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         if t.device != self.device:
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
     def _dense(self, t, name, shape, dtype):
-        """Address of a contiguous tensor; None stays None."""
+        """Address of a contiguous tensor, 0 for None."""
         if t is None:
-            return None
+            return 0
         self._check_tensor(t, name, shape, dtype)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
     def _view(self, t, name, shape, dtype):
-        """A [B, N, heads, width] or [B, N, heads] tensor as a View."""
+        """Address and strides (batch, token, head) of a [B, N, heads, width] or [B, N, heads]
+        tensor."""
         self._check_tensor(t, name, shape, dtype)
-        st = list(t.stride())
-        if len(shape) == 4 and shape[3] > 1 and st[3] != 1:
+        st = t.stride()
+        if len(shape) == 4 and st[3] != 1 and shape[3] > 1:
             raise ValueError(f"the last axis of {name} must be contiguous")
         # torch gives axes of one element any stride
-        st = [0 if n == 1 else s for n, s in zip(shape, st)]
-        return View(t.data_ptr(), st[0], st[1], st[2])
+        return (t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0,
+                st[2] if shape[2] > 1 else 0)
+
+    def _token_view(self, t, name, shape, dtype):
+        """The same of one token per row: [B, heads, width] or [B, heads]."""
+        self._check_tensor(t, name, shape, dtype)
+        st = t.stride()
+        if len(shape) == 3 and st[2] != 1 and shape[2] > 1:
+            raise ValueError(f"the last axis of {name} must be contiguous")
+        return (t.data_ptr(), st[0] if shape[0] > 1 else 0, 0, st[1] if shape[1] > 1 else 0)
 
     def _out(self, out, name, shape, dtype):
         if out is None:
-            out = self.torch.empty(shape, dtype=dtype, device=self.device)
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
         self._dense(out, name, shape, dtype)
         return out
+
+
+_PACK_VIEW = struct.Struct("P3q").pack
+_PACK_RECURRENCE = struct.Struct("P3q" * 4 + "PPf4x").pack
+_PACK_GRADS = struct.Struct("5P").pack
+_PACK_QK_NORM = struct.Struct("5q3i4xq2f4Pq" + "P3q" * 2).pack
 
 
 class Recurrence(_Mixer):
@@ -662,28 +687,25 @@ class Recurrence(_Mixer):
 
     def _inputs(self, q, k, v, g, scale, state=None, lengths=None):
         torch = self.torch
-        rows = (self.B, self.N, self.heads)
-        return RecurrenceInputs(
-            self._view(q, "q", rows + (self.dk,), self.dtype), self._view(k, "k", rows + (self.dk,), self.dtype),
-            self._view(v, "v", rows + (self.dv,), self.dtype), self._view(g, "g", rows, torch.float32),
+        B, N, H = self.B, self.N, self.heads
+        return _PACK_RECURRENCE(
+            *self._view(q, "q", (B, N, H, self.dk), self.dtype), *self._view(k, "k", (B, N, H, self.dk), self.dtype),
+            *self._view(v, "v", (B, N, H, self.dv), self.dtype), *self._view(g, "g", (B, N, H), torch.float32),
             self._dense(state, "state", self.state_shape, torch.float32),
-            self._dense(lengths, "lengths", (self.B,), torch.int32),
-            float(self.dk ** -0.5 if scale is None else scale))
+            self._dense(lengths, "lengths", (B,), torch.int32), self.dk ** -0.5 if scale is None else scale)
 
     def forward(self, q, k, v, g, scale=None, state=None, lengths=None, return_state=False, o=None,
                 final_state=None):
         """(o, final state or None).  scale: 1 / sqrt(dk) by default.  state: the state before
         token 0.  lengths: int32 [B], tokens per row (the others' o is 0)."""
-        torch = self.torch
         x = self._inputs(q, k, v, g, scale, state, lengths)
         o = self._out(o, "o", (self.B, self.N, self.heads, self.dv), self.dtype)
         if return_state or final_state is not None:
-            final_state = self._out(final_state, "final_state", self.state_shape, torch.float32)
-        with self._on_device():
-            _check(hyena_recurrence_forward(self.handle, x, o.data_ptr(),
-                                            final_state.data_ptr() if final_state is not None else None,
-                                            self._keep(self.workspace), self._stream()),
-                   "hyena_recurrence_forward")
+            final_state = self._out(final_state, "final_state", self.state_shape, self.torch.float32)
+        stream = self._stream()
+        self._call("hyena_recurrence_forward", hyena_recurrence_forward, self.handle, x, o.data_ptr(),
+                   final_state.data_ptr() if final_state is not None else None,
+                   self._keep(self.workspace, stream), stream)
         return o, final_state
 
     def backward(self, d_o, q, k, v, g, scale=None, state=None, lengths=None, d_final=None):
@@ -694,18 +716,17 @@ class Recurrence(_Mixer):
             raise ValueError("backward needs a plan made with training=True")
         x = self._inputs(q, k, v, g, scale, state, lengths)
         rows = (self.B, self.N, self.heads)
-        d = self._view(d_o, "d_o", rows + (self.dv,), self.dtype)
+        d = _PACK_VIEW(*self._view(d_o, "d_o", rows + (self.dv,), self.dtype))
         df = self._dense(d_final, "d_final", self.state_shape, torch.float32)
-        new = lambda *s, dt=self.dtype: torch.empty(s, dtype=dt, device=self.device)  # noqa: E731
-        dq, dk, dv = new(*rows, self.dk), new(*rows, self.dk), new(*rows, self.dv)
-        dg = new(*rows, dt=torch.float32)
-        ds = new(*self.state_shape, dt=torch.float32) if state is not None else None
-        grads = RecurrenceGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
-                                ds.data_ptr() if ds is not None else None)
-        with self._on_device():
-            _check(hyena_recurrence_backward(self.handle, x, d, df, grads, self._keep(self.workspace),
-                                             self._stream()),
-                   "hyena_recurrence_backward")
+        new = lambda shape, dt=self.dtype: torch.empty(shape, dtype=dt, device=self.device)  # noqa: E731
+        dq, dk, dv = new(rows + (self.dk,)), new(rows + (self.dk,)), new(rows + (self.dv,))
+        dg = new(rows, torch.float32)
+        ds = new(self.state_shape, torch.float32) if state is not None else None
+        grads = _PACK_GRADS(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
+                            ds.data_ptr() if ds is not None else 0)
+        stream = self._stream()
+        self._call("hyena_recurrence_backward", hyena_recurrence_backward, self.handle, x, d, df, grads,
+                   self._keep(self.workspace, stream), stream)
         return dq, dk, dv, dg, ds
 
     def step(self, q, k, v, g, states, scale=None, slots=None, o=None):
@@ -714,21 +735,19 @@ class Recurrence(_Mixer):
         returns o [B, heads, dv].  Rows with a slot outside the table take no part (o = 0); the
         other slots have to differ."""
         torch = self.torch
-        rows = (self.B, 1, self.heads)
-        up = lambda t: t.unsqueeze(1) if isinstance(t, torch.Tensor) and t.dim() > 0 else t  # noqa: E731
-        x = RecurrenceInputs(
-            self._view(up(q), "q", rows + (self.dk,), self.dtype), self._view(up(k), "k", rows + (self.dk,), self.dtype),
-            self._view(up(v), "v", rows + (self.dv,), self.dtype), self._view(up(g), "g", rows, torch.float32),
-            None, None, float(self.dk ** -0.5 if scale is None else scale))
-        n = int(states.shape[0]) if isinstance(states, torch.Tensor) and states.dim() == 4 else 0
-        table = self._dense(states, "states", (n, self.heads, self.dk, self.dv), torch.float32)
-        if table is None:
-            raise ValueError("states must be a torch tensor")
-        at = self._dense(slots, "slots", (self.B,), torch.int32)
-        o = self._out(o, "o", (self.B, self.heads, self.dv), self.dtype)
-        with self._on_device():
-            _check(hyena_recurrence_step(self.handle, x, at, n, table, o.data_ptr(), self._stream()),
-                   "hyena_recurrence_step")
+        B, H = self.B, self.heads
+        x = _PACK_RECURRENCE(
+            *self._token_view(q, "q", (B, H, self.dk), self.dtype), *self._token_view(k, "k", (B, H, self.dk), self.dtype),
+            *self._token_view(v, "v", (B, H, self.dv), self.dtype), *self._token_view(g, "g", (B, H), torch.float32),
+            0, 0, self.dk ** -0.5 if scale is None else scale)
+        n = states.shape[0] if isinstance(states, torch.Tensor) and states.dim() == 4 else 0
+        table = self._dense(states, "states", (n, H, self.dk, self.dv), torch.float32)
+        if not table:
+            raise ValueError("states must be a torch tensor of at least one state")
+        at = self._dense(slots, "slots", (B,), torch.int32)
+        o = self._out(o, "o", (B, H, self.dv), self.dtype)
+        self._call("hyena_recurrence_step", hyena_recurrence_step, self.handle, x, at, n, table, o.data_ptr(),
+                   self._stream())
         return o
 
     def __del__(self):
@@ -745,8 +764,9 @@ def rotary_frequencies(rotary_dim, base=10000.0, stretch=1.0, device="cuda"):
     positions of a longer context over the trained range; any other scaling is a table of the
     caller's own."""
     import torch
-    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
-    return base ** (-i / max(rotary_dim, 1)) / stretch
+    # made on the host: the copy is done before this returns, so any stream may read it
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    return (base ** (-i / max(rotary_dim, 1)) / stretch).to(device)
 
 
 class QKNorm(_Mixer):
@@ -779,15 +799,15 @@ class QKNorm(_Mixer):
         self._dense(freqs, "freqs", (self.rotary_dim // 2,), self.torch.float64)
         self.norm, self.layout, self.eps, self.freqs = norm, layout, float(eps), freqs
         self.rotary_scale = float(rotary_scale)
-        st, n = hyena_qk_norm_scratch_bytes(self._op(View(), View()))
+        st, n = hyena_qk_norm_scratch_bytes(self._op((0, 0, 0, 0), (0, 0, 0, 0)))
         _check(st, "hyena_qk_norm_scratch_bytes")
         self.scratch_bytes = n
 
-    def _op(self, q, k, q_weight=None, k_weight=None, positions=None, offset=0):
-        return QkNorm(self.B, self.N, self.q_heads, self.k_heads, self.D, self.io_dtype,
-                      self._NORMS[self.norm], self._LAYOUTS[self.layout], self.rotary_dim, self.eps,
-                      self.rotary_scale, self.freqs.data_ptr() if self.rotary_dim else None,
-                      q_weight, k_weight, positions, int(offset), q, k)
+    def _op(self, q, k, q_weight=0, k_weight=0, positions=0, offset=0):
+        return _PACK_QK_NORM(self.B, self.N, self.q_heads, self.k_heads, self.D, self.io_dtype,
+                             self._NORMS[self.norm], self._LAYOUTS[self.layout], self.rotary_dim, self.eps,
+                             self.rotary_scale, self.freqs.data_ptr() if self.rotary_dim else 0,
+                             q_weight, k_weight, positions, offset, *q, *k)
 
     def _describe(self, q, k, q_weight, k_weight, positions, offset):
         torch = self.torch
@@ -804,10 +824,9 @@ class QKNorm(_Mixer):
         op = self._describe(q, k, q_weight, k_weight, positions, offset)
         q_out = self._out(q_out, "q_out", (self.B, self.N, self.q_heads, self.D), self.dtype)
         k_out = self._out(k_out, "k_out", (self.B, self.N, self.k_heads, self.D), self.dtype)
-        self._keep(self.freqs)
-        with self._on_device():
-            _check(hyena_qk_norm_forward(op, q_out.data_ptr(), k_out.data_ptr(), self._stream()),
-                   "hyena_qk_norm_forward")
+        stream = self._stream()
+        self._keep(self.freqs, stream)
+        self._call("hyena_qk_norm_forward", hyena_qk_norm_forward, op, q_out.data_ptr(), k_out.data_ptr(), stream)
         return q_out, k_out
 
     def backward(self, dq_out, dk_out, q, k, q_weight=None, k_weight=None, positions=None, offset=0):
@@ -815,17 +834,17 @@ class QKNorm(_Mixer):
         None has no gradient."""
         torch = self.torch
         op = self._describe(q, k, q_weight, k_weight, positions, offset)
-        dqo = self._view(dq_out, "dq_out", (self.B, self.N, self.q_heads, self.D), self.dtype)
-        dko = self._view(dk_out, "dk_out", (self.B, self.N, self.k_heads, self.D), self.dtype)
-        dq = self._out(None, "dq", (self.B, self.N, self.q_heads, self.D), self.dtype)
-        dk = self._out(None, "dk", (self.B, self.N, self.k_heads, self.D), self.dtype)
+        qs, ks = (self.B, self.N, self.q_heads, self.D), (self.B, self.N, self.k_heads, self.D)
+        dqo = _PACK_VIEW(*self._view(dq_out, "dq_out", qs, self.dtype))
+        dko = _PACK_VIEW(*self._view(dk_out, "dk_out", ks, self.dtype))
+        new = lambda shape, dt=self.dtype: torch.empty(shape, dtype=dt, device=self.device)  # noqa: E731
+        dq, dk = new(qs), new(ks)
         has = [w is not None and self.norm != "none" for w in (q_weight, k_weight)]
-        dqw, dkw = (torch.empty(self.D, dtype=torch.float32, device=self.device) if h else None for h in has)
-        scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=self.device) if any(has) else None
-        self._keep(self.freqs)
+        dqw, dkw = (new((self.D,), torch.float32) if h else None for h in has)
+        scratch = new((self.scratch_bytes,), torch.uint8) if any(has) else None
+        stream = self._stream()
+        self._keep(self.freqs, stream)
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-        with self._on_device():
-            _check(hyena_qk_norm_backward(op, dqo, dko, dq.data_ptr(), dk.data_ptr(), ptr(dqw), ptr(dkw),
-                                          ptr(scratch), self._stream()),
-                   "hyena_qk_norm_backward")
+        self._call("hyena_qk_norm_backward", hyena_qk_norm_backward, op, dqo, dko, dq.data_ptr(), dk.data_ptr(),
+                   ptr(dqw), ptr(dkw), ptr(scratch), stream)
         return dq, dk, dqw, dkw
