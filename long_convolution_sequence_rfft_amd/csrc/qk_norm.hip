@@ -1,16 +1,31 @@
 // qk_norm.hip -- norms of queries and keys per head with the position rotation
 // in the same pass, and their backward pass (include/hyena.h).
 //
+// With r = 1 / sqrt(mean(x^2) + eps) (L2: the sum) a head's x becomes
+//   y = turn(w r x),
+// and its gradient, with d = w turn^T(dy) and z = r x,
+//   dx = r (d - z mean(d z)),   dw = sum over tokens and heads of turn^T(dy) z.
+//
 // Bound by memory: each channel is read and written once (the backward pass
 // reads two tensors).  What is shared by all heads of a token, the sines and
-// cosines, is computed once per token and kept in LDS; everything else of a
-// head stays in the registers of the few lanes that hold it.
+// cosines and the token's place, is computed once per tile and kept in LDS;
+// everything else of a head stays in the registers of the few lanes that hold
+// it.  A workgroup serves one of the two tensors: with both, the kernel held
+// two sets of weights and of their sums, 165 instead of 131 registers, and the
+// two heads' worth of a decoding token came one after the other (8.0 us
+// instead of 6.5).
 //
 // A head is cut into units of 2 W channels, two vectors of W: W pairs of the
 // rotation (in the half layout the vectors are rotary_dim / 2 apart, else side
 // by side) or 2 W channels that are not rotated.  A lane holds U units, a power
 // of two of lanes one head, so a pair is always within a lane and the norm's
-// sum is a few shuffles.
+// sum is a few steps across lanes.
+//
+// Tiles of 48 KB: the backward pass at 16384 tokens of 12 + 4 heads of 64 in
+// bf16 takes 26.7 us (100 MB, 4.4 TB/s less 4 us of launch), with 32 KB 31,
+// with 64 KB 30 (fewer workgroups than the card holds); at 8192 tokens of
+// 12 + 12 heads in float32 35.6 us (151 MB) against 39.6 and 40.0.  Forward at
+// 16384 tokens of 12 + 12 heads, bf16: 24.6 us (101 MB).
 #include <hip/hip_runtime.h>
 
 #include <string>
@@ -26,9 +41,12 @@ namespace hy {
 namespace {
 
 constexpr int kQkThreads = 256;
-constexpr int kQkTokens = 16;      // most tokens of a workgroup's tile
+constexpr int kQkTokens = 64;      // most tokens of a workgroup's tile
+constexpr int kQkTile = 48 << 10;  // bytes of a tensor that a tile is meant to hold
 constexpr int kQkAngles = 2048;    // most (token, frequency) pairs of a tile: 16 KB of LDS
-constexpr int kQkGradGroups = 512; // most workgroups of the backward pass: rows of its partial sums
+constexpr int kQkTiles = 256;      // fewest tiles of a tensor, if it has that many tokens
+constexpr int kQkGroups = 1 << 16; // most workgroups of a tensor, forward: the rest of the tiles is looped over
+constexpr int kQkGradGroups = 1024; // backward: rows of the partial sums
 
 struct QkTensor {
     RView x, dy;
@@ -37,6 +55,9 @@ struct QkTensor {
     float* dw_part;     // [groups][D]
     int32_t heads;
     uint32_t magic;     // ceil(2^32 / heads), heads > 1: item / heads = item * magic >> 32, item < 2^16
+    int32_t tokens;     // per tile
+    int32_t groups;     // workgroups
+    int64_t tiles;
 };
 
 struct QkArgs {
@@ -45,8 +66,6 @@ struct QkArgs {
     const int32_t* positions;
     int64_t offset;
     int64_t N, rows;    // rows: B * N
-    int64_t tiles;
-    int32_t tokens;     // per tile
     int32_t D, rotary;
     int32_t half, norm;
     int32_t lanes;      // per head, a power of two
@@ -54,15 +73,16 @@ struct QkArgs {
     float eps, rscale;
 };
 
-template <typename T, int W>
-__device__ __forceinline__ void qk_load(float (&x)[W], const T* p)
-{
-    if constexpr (W == 1) {
-        x[0] = load_one<T>(p);
-    } else {
-        typename Mx<T>::vec4 v[W / 4];
+// W channels as loaded, and widened.
+template <typename T, int W> struct QkRaw {
+    typename Mx<T>::vec4 v[W / 4];
+    __device__ __forceinline__ void load(const T* p)
+    {
         if constexpr (W == 8) *(uint4*)v = *(const uint4*)p;
         else v[0] = *(const typename Mx<T>::vec4*)p;
+    }
+    __device__ __forceinline__ void widen(float (&x)[W]) const
+    {
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
             const f32x4 f = Mx<T>::widen(v[i]);
@@ -70,7 +90,12 @@ __device__ __forceinline__ void qk_load(float (&x)[W], const T* p)
             for (int j = 0; j < 4; ++j) x[4 * i + j] = f[j];
         }
     }
-}
+};
+template <typename T> struct QkRaw<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T* p) { v = *p; }
+    __device__ __forceinline__ void widen(float (&x)[1]) const { x[0] = load_one<T>(&v); }
+};
 
 template <typename T, int W>
 __device__ __forceinline__ void qk_store(T* p, const float (&x)[W])
@@ -92,17 +117,28 @@ __device__ __forceinline__ void qk_store(T* p, const float (&x)[W])
 }
 
 // Sine and cosine of position * frequency.  The angle in float64 is reduced by
-// 2 pi in two parts (error below 2^-52 of the angle plus 2e-16 at 2^31 turns),
-// so far positions keep float32 accuracy.
+// pi / 2 in two parts (error below 2^-52 of the angle plus 2e-16 at 2^31 turns),
+// so far positions keep float32 accuracy.  What is left is within pi / 4, where
+// Taylor's series end: the terms left out are below 2e-9 of the sum.
 __device__ __forceinline__ float2 qk_turn(int64_t pos, double freq, float scale)
 {
     const double a = (double)pos * freq;
-    const double n = rint(a * 0.15915494309189533577);
-    double r = fma(-n, 6.283185307179586232, a);
-    r = fma(-n, 2.4492935982947064e-16, r);
-    float s, c;
-    sincosf((float)r, &s, &c);
-    return make_float2(c * scale, s * scale);
+    const double n = rint(a * 0.63661977236758134308);
+    double r = fma(-n, 1.5707963267948965580, a);
+    r = fma(-n, 6.123233995736766036e-17, r);
+    const float x = (float)r, z = x * x;
+    float s = fmaf(z, 1.0f / 362880, -1.0f / 5040), c = fmaf(z, -1.0f / 3628800, 1.0f / 40320);
+    s = fmaf(z, s, 1.0f / 120);
+    c = fmaf(z, c, -1.0f / 720);
+    s = fmaf(z, s, -1.0f / 6);
+    c = fmaf(z, c, 1.0f / 24);
+    s = fmaf(z * x, s, x);
+    c = fmaf(z, c, -0.5f);
+    c = fmaf(z, c, 1.0f);
+    const int turn = (int)(int64_t)n & 3;  // quarter turns
+    const float u = turn & 1 ? s : c, v = turn & 1 ? c : s;
+    const float co = turn == 1 || turn == 2 ? -u : u, si = turn & 2 ? -v : v;
+    return make_float2(co * scale, si * scale);
 }
 
 // y = turn(x) for GRAD = false, its transpose for GRAD = true; a pair's members
@@ -128,16 +164,32 @@ __device__ __forceinline__ void qk_rotate(float (&x0)[W], float (&x1)[W], const 
     }
 }
 
+// Sum over a group of `lanes` (a power of two) lanes, in each of them.
+__device__ __forceinline__ float sum_lanes(float x, int lanes)
+{
+    if (lanes > 1) x += dpp_f32<0xb1>(x);   // the steps of sum16
+    if (lanes > 2) x += dpp_f32<0x4e>(x);
+    if (lanes > 4) x += dpp_f32<0x141>(x);
+    if (lanes > 8) x += dpp_f32<0x140>(x);
+    if (lanes > 16) x += __shfl_xor(x, 16);
+    if (lanes > 32) x += __shfl_xor(x, 32);
+    return x;
+}
+
 template <typename T, int W, int U, bool GRAD>
-__global__ __launch_bounds__(kQkThreads) void hyena_qk_norm_pass(QkArgs p)
+__global__ __launch_bounds__(kQkThreads, U == 1 ? 3 : 2) void hyena_qk_norm_pass(QkArgs p)
 {
     __shared__ float2 turns[kQkAngles];
+    __shared__ int64_t at[GRAD ? 2 : 1][kQkTokens];  // elements to each token of the tile, in x and dy
     __shared__ float sums[GRAD ? kQkThreads * 2 * W : 1];
+    const bool second = (int)blockIdx.x >= p.t[0].groups;
+    const QkTensor q = second ? p.t[1] : p.t[0];
+    const int mine = (int)blockIdx.x - (second ? p.t[0].groups : 0);
     const int tid = threadIdx.x;
     const int lane = tid & (p.lanes - 1), group = tid / p.lanes, groups = kQkThreads / p.lanes;
     const int units = (p.D + 2 * W - 1) / (2 * W), turned = p.rotary / (2 * W), nf = p.rotary / 2;
 
-    // the lane's units: places of their two vectors, weights
+    // the lane's units: places of their two vectors
     int c0[U], c1[U];
     bool in0[U], in1[U], rot[U];
 #pragma unroll
@@ -150,171 +202,168 @@ __global__ __launch_bounds__(kQkThreads) void hyena_qk_norm_pass(QkArgs p)
         in0[u] = n < units;
         in1[u] = n < units && c1[u] < p.D;
     }
-    float dw[GRAD ? 2 : 1][U][2][W];
-    if constexpr (GRAD) {
+    float w[U][2][W], dw[GRAD ? U : 1][2][W];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < W; ++e) dw[k][u][0][e] = dw[k][u][1][e] = 0.0f;
-    }
+        for (int e = 0; e < W; ++e) {
+            w[u][0][e] = q.w && in0[u] ? q.w[c0[u] + e] : 1.0f;
+            w[u][1][e] = q.w && in1[u] ? q.w[c1[u] + e] : 1.0f;
+            if constexpr (GRAD) dw[u][0][e] = dw[u][1][e] = 0.0f;
+        }
 
-    for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-        const int64_t row0 = tile * p.tokens;
-        const int ntok = p.rows - row0 < p.tokens ? (int)(p.rows - row0) : p.tokens;
-        if (GRAD) __syncthreads();
+    for (int64_t tile = mine; tile < q.tiles; tile += q.groups) {
+        const int64_t row0 = tile * q.tokens;
+        const int ntok = p.rows - row0 < q.tokens ? (int)(p.rows - row0) : q.tokens;
+        if (tile != mine) __syncthreads();
+        if (tid < ntok) {
+            const uint64_t row = (uint64_t)(row0 + tid);
+            const int64_t b = (int64_t)(row / (uint64_t)p.N), t = (int64_t)(row - (uint64_t)b * (uint64_t)p.N);
+            at[0][tid] = b * q.x.b + t * q.x.t;
+            if constexpr (GRAD) at[1][tid] = b * q.dy.b + t * q.dy.t;
+        }
         for (int i = tid; i < ntok * nf; i += kQkThreads) {
-            const int64_t row = row0 + i / nf;
-            const int64_t pos = p.positions ? (int64_t)p.positions[row] : p.offset + row % p.N;
+            const uint64_t row = (uint64_t)(row0 + i / nf);
+            const int64_t pos = p.positions ? (int64_t)p.positions[row] : p.offset + (int64_t)(row % (uint64_t)p.N);
             turns[i] = qk_turn(pos, p.freqs[i % nf], p.rscale);
         }
         __syncthreads();
-        auto tensor = [&](auto which) {
-            constexpr int K = decltype(which)::value;
-            const QkTensor& q = p.t[K];
-            float w[U][2][W];
+        const int items = ntok * q.heads;
+        for (int item = group; item < items; item += groups) {
+            QkRaw<T, W> rx[U][2], rd[GRAD ? U : 1][2];
+            const int tok = q.heads == 1 ? item : (int)__umulhi((uint32_t)item, q.magic), head = item - tok * q.heads;
+            const T* xp = (const T*)q.x.p + at[0][tok] + head * q.x.h;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    w[u][0][e] = q.w && in0[u] ? q.w[c0[u] + e] : 1.0f;
-                    w[u][1][e] = q.w && in1[u] ? q.w[c1[u] + e] : 1.0f;
-                }
-            const int items = ntok * q.heads;
-            for (int item = group; item < items; item += groups) {
-                const int tok = q.heads == 1 ? item : (int)__umulhi((uint32_t)item, q.magic), head = item - tok * q.heads;
-                const int64_t row = row0 + tok, b = row / p.N, t = row - b * p.N;
-                const T* xp = (const T*)q.x.p + b * q.x.b + t * q.x.t + head * q.x.h;
-                T* op = (T*)q.out + (row * q.heads + head) * p.D;
-                float x[U][2][W], d[U][2][W];
-                float ss = 0.0f;
+            for (int u = 0; u < U; ++u) {
+                if (in0[u]) rx[u][0].load(xp + c0[u]);
+                if (in1[u]) rx[u][1].load(xp + c1[u]);
+            }
+            if constexpr (GRAD) {
+                const T* dp = (const T*)q.dy.p + at[1][tok] + head * q.dy.h;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-#pragma unroll
-                    for (int e = 0; e < W; ++e) x[u][0][e] = x[u][1][e] = d[u][0][e] = d[u][1][e] = 0.0f;
-                    if (in0[u]) qk_load<T, W>(x[u][0], xp + c0[u]);
-                    if (in1[u]) qk_load<T, W>(x[u][1], xp + c1[u]);
-                }
-                if constexpr (GRAD) {
-                    const T* dp = (const T*)q.dy.p + b * q.dy.b + t * q.dy.t + head * q.dy.h;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (in0[u]) qk_load<T, W>(d[u][0], dp + c0[u]);
-                        if (in1[u]) qk_load<T, W>(d[u][1], dp + c1[u]);
-                    }
-                }
-                float r = 1.0f;
-                if (p.norm) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-#pragma unroll
-                        for (int e = 0; e < W; ++e) ss += x[u][0][e] * x[u][0][e] + x[u][1][e] * x[u][1][e];
-                    for (int m = 1; m < p.lanes; m <<= 1) ss += __shfl_xor(ss, m);
-                    r = 1.0f / sqrtf(ss * p.mean + p.eps);
-                }
-                const float2* turn = turns + tok * nf;
-                if constexpr (!GRAD) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (p.norm) {
-#pragma unroll
-                            for (int e = 0; e < W; ++e) {
-                                x[u][0][e] *= r * w[u][0][e];
-                                x[u][1][e] *= r * w[u][1][e];
-                            }
-                        }
-                        if (rot[u]) qk_rotate<W, false>(x[u][0], x[u][1], turn + (lane + u * p.lanes) * W, p.half);
-                        if (in0[u]) qk_store<T, W>(op + c0[u], x[u][0]);
-                        if (in1[u]) qk_store<T, W>(op + c1[u], x[u][1]);
-                    }
-                } else {
-                    float along = 0.0f;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (rot[u]) qk_rotate<W, true>(d[u][0], d[u][1], turn + (lane + u * p.lanes) * W, p.half);
-                        if (p.norm) {
-#pragma unroll
-                            for (int v = 0; v < 2; ++v)
-#pragma unroll
-                                for (int e = 0; e < W; ++e) {
-                                    x[u][v][e] *= r;
-                                    dw[K][u][v][e] += d[u][v][e] * x[u][v][e];
-                                    d[u][v][e] *= w[u][v][e];
-                                    along += d[u][v][e] * x[u][v][e];
-                                }
-                        }
-                    }
-                    if (p.norm) {
-                        for (int m = 1; m < p.lanes; m <<= 1) along += __shfl_xor(along, m);
-                        along *= p.mean;
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (p.norm) {
-#pragma unroll
-                            for (int v = 0; v < 2; ++v)
-#pragma unroll
-                                for (int e = 0; e < W; ++e) d[u][v][e] = (d[u][v][e] - x[u][v][e] * along) * r;
-                        }
-                        if (in0[u]) qk_store<T, W>(op + c0[u], d[u][0]);
-                        if (in1[u]) qk_store<T, W>(op + c1[u], d[u][1]);
-                    }
+                    if (in0[u]) rd[u][0].load(dp + c0[u]);
+                    if (in1[u]) rd[u][1].load(dp + c1[u]);
                 }
             }
-        };
-        tensor(std::integral_constant<int, 0>{});
-        tensor(std::integral_constant<int, 1>{});
+            T* op = (T*)q.out + (row0 * q.heads + item) * p.D;
+            float x[U][2][W], d[U][2][W];
+            float ss = 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) x[u][0][e] = x[u][1][e] = d[u][0][e] = d[u][1][e] = 0.0f;
+                if (in0[u]) rx[u][0].widen(x[u][0]);
+                if (in1[u]) rx[u][1].widen(x[u][1]);
+                if constexpr (GRAD) {
+                    if (in0[u]) rd[u][0].widen(d[u][0]);
+                    if (in1[u]) rd[u][1].widen(d[u][1]);
+                }
+            }
+            float r = 1.0f;
+            if (p.norm) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) ss += x[u][0][e] * x[u][0][e] + x[u][1][e] * x[u][1][e];
+                ss = sum_lanes(ss, p.lanes);
+                r = 1.0f / sqrtf(ss * p.mean + p.eps);
+            }
+            const float2* turn = turns + tok * nf;
+            if constexpr (!GRAD) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (p.norm) {
+#pragma unroll
+                        for (int e = 0; e < W; ++e) {
+                            x[u][0][e] *= r * w[u][0][e];
+                            x[u][1][e] *= r * w[u][1][e];
+                        }
+                    }
+                    if (rot[u]) qk_rotate<W, false>(x[u][0], x[u][1], turn + (lane + u * p.lanes) * W, p.half);
+                    if (in0[u]) qk_store<T, W>(op + c0[u], x[u][0]);
+                    if (in1[u]) qk_store<T, W>(op + c1[u], x[u][1]);
+                }
+            } else {
+                float along = 0.0f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (rot[u]) qk_rotate<W, true>(d[u][0], d[u][1], turn + (lane + u * p.lanes) * W, p.half);
+                    if (p.norm) {
+#pragma unroll
+                        for (int v = 0; v < 2; ++v)
+#pragma unroll
+                            for (int e = 0; e < W; ++e) {
+                                x[u][v][e] *= r;
+                                dw[u][v][e] += d[u][v][e] * x[u][v][e];
+                                d[u][v][e] *= w[u][v][e];
+                                along += d[u][v][e] * x[u][v][e];
+                            }
+                    }
+                }
+                if (p.norm) along = sum_lanes(along, p.lanes) * p.mean;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (p.norm) {
+#pragma unroll
+                        for (int v = 0; v < 2; ++v)
+#pragma unroll
+                            for (int e = 0; e < W; ++e) d[u][v][e] = (d[u][v][e] - x[u][v][e] * along) * r;
+                    }
+                    if (in0[u]) qk_store<T, W>(op + c0[u], d[u][0]);
+                    if (in1[u]) qk_store<T, W>(op + c1[u], d[u][1]);
+                }
+            }
+        }
     }
     if constexpr (GRAD) {
         // the workgroup's sums for the weights, over its groups in order
+        if (q.dw_part == nullptr) return;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (p.t[k].dw_part == nullptr) continue;
+        for (int u = 0; u < U; ++u) {
+            __syncthreads();
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                __syncthreads();
-#pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    sums[(e * 2) * kQkThreads + tid] = dw[k][u][0][e];
-                    sums[(e * 2 + 1) * kQkThreads + tid] = dw[k][u][1][e];
-                }
-                __syncthreads();
-                for (int i = tid; i < p.lanes * 2 * W; i += kQkThreads) {
-                    const int l = i / (2 * W), ev = i % (2 * W), e = ev / 2, v = ev % 2;
-                    const int n = l + u * p.lanes;
-                    const bool apart = n < turned && p.half;
-                    const int c = (v ? (apart ? nf + n * W : 2 * n * W + W) : (apart ? n * W : 2 * n * W)) + e;
-                    if (n < units && c < p.D) {
-                        float s = 0.0f;
-                        for (int g = 0; g < groups; ++g) s += sums[ev * kQkThreads + g * p.lanes + l];
-                        p.t[k].dw_part[(int64_t)blockIdx.x * p.D + c] = s;
-                    }
+            for (int e = 0; e < W; ++e) {
+                sums[(e * 2) * kQkThreads + tid] = dw[u][0][e];
+                sums[(e * 2 + 1) * kQkThreads + tid] = dw[u][1][e];
+            }
+            __syncthreads();
+            for (int i = tid; i < p.lanes * 2 * W; i += kQkThreads) {
+                const int l = i / (2 * W), ev = i % (2 * W), e = ev / 2, v = ev % 2;
+                const int n = l + u * p.lanes;
+                const bool apart = n < turned && p.half;
+                const int c = (v ? (apart ? nf + n * W : 2 * n * W + W) : (apart ? n * W : 2 * n * W)) + e;
+                if (n < units && c < p.D) {
+                    float s = 0.0f;
+                    for (int g = 0; g < groups; ++g) s += sums[ev * kQkThreads + g * p.lanes + l];
+                    q.dw_part[(int64_t)mine * p.D + c] = s;
                 }
             }
         }
     }
 }
 
-// dw[c] = sum over the workgroups' rows, 16 channels by 16 rows at a time.
-__global__ __launch_bounds__(256) void hyena_qk_weight_grad(const float* part0, const float* part1, float* out0,
-                                                            float* out1, int groups, int D)
+// dw[c] = sum over the workgroups' rows, 16 channels by 64 rows at a time: what
+// takes time here is one load after the other.
+__global__ __launch_bounds__(1024) void hyena_qk_weight_grad(const float* part0, const float* part1, float* out0,
+                                                            float* out1, int groups0, int groups1, int D)
 {
-    __shared__ double sums[256];
+    __shared__ double sums[1024];
     const float* part = blockIdx.y ? part1 : part0;
     float* out = blockIdx.y ? out1 : out0;
+    const int groups = blockIdx.y ? groups1 : groups0;
     if (out == nullptr) return;
     const int c = blockIdx.x * 16 + (threadIdx.x & 15), r = threadIdx.x >> 4;
     double s = 0.0;
     if (c < D) {
 #pragma unroll 8
-        for (int g = r; g < groups; g += 16) s += (double)part[(int64_t)g * D + c];
+        for (int g = r; g < groups; g += 64) s += (double)part[(int64_t)g * D + c];
     }
     sums[threadIdx.x] = s;
     __syncthreads();
     if (r == 0 && c < D) {
         double x = 0.0;
-        for (int i = 0; i < 16; ++i) x += sums[i * 16 + threadIdx.x];
+        for (int i = 0; i < 64; ++i) x += sums[i * 16 + threadIdx.x];
         out[c] = (float)x;
     }
 }
@@ -338,29 +387,35 @@ int vector_width(const QkArgs& a, size_t element, bool grad)
     return 1;
 }
 
-// Tokens per tile: up to 16, as few as keep about 1024 tiles.
-void shape_tiles(QkArgs& a, int64_t most_heads)
+// The tensors' tiles and workgroups: kQkTile channels each, or fewer so that
+// there are kQkTiles of them.
+void shape_tiles(QkArgs& a, size_t element, bool grad)
 {
-    int64_t t = a.rows / 1024;
-    const int64_t nf = a.rotary / 2 > 0 ? a.rotary / 2 : 1;
-    if (t > kQkTokens) t = kQkTokens;
-    if (t > kQkAngles / nf) t = kQkAngles / nf;
-    if (t > 65535 / most_heads) t = 65535 / most_heads;
-    if (t < 1) t = 1;
-    a.tokens = (int32_t)t;
-    a.tiles = (a.rows + t - 1) / t;
+    const int64_t nf = a.rotary / 2 > 0 ? a.rotary / 2 : 1, heads = a.t[0].heads + a.t[1].heads;
+    for (QkTensor& q : a.t) {
+        int64_t t = kQkTile / ((int64_t)q.heads * a.D * (int64_t)element);
+        if (t > a.rows / kQkTiles) t = a.rows / kQkTiles;
+        if (t > kQkTokens) t = kQkTokens;
+        if (t > kQkAngles / nf) t = kQkAngles / nf;
+        if (t < 1) t = 1;
+        q.tokens = (int32_t)t;
+        q.tiles = (a.rows + t - 1) / t;
+        int64_t most = grad ? kQkGradGroups * (int64_t)q.heads / heads : kQkGroups;
+        if (most < 1) most = 1;
+        q.groups = (int32_t)(q.tiles < most ? q.tiles : most);
+    }
 }
 
 template <typename T, int W, int U, bool GRAD>
-hyena_status qk_launch_one(const QkArgs& a, int64_t grid, hipStream_t s)
+hyena_status qk_launch_one(const QkArgs& a, hipStream_t s)
 {
     HY_LAUNCH(kernel_label("hyena_qk_norm_pass", type_label<T>(), W, U, GRAD), (hyena_qk_norm_pass<T, W, U, GRAD>),
-              dim3((unsigned)grid), dim3(kQkThreads), 0, s, a);
+              dim3((unsigned)(a.t[0].groups + a.t[1].groups)), dim3(kQkThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? HYENA_OK : fail(HYENA_ERR_DEVICE, hipGetErrorString(e));
 }
 
-template <typename T, int W, bool GRAD> hyena_status qk_launch_w(QkArgs& a, int64_t grid, hipStream_t s)
+template <typename T, int W, bool GRAD> hyena_status qk_launch_w(QkArgs& a, hipStream_t s)
 {
     // lanes per head: a power of two, at most a wave; more units go to a lane
     const int units = (a.D + 2 * W - 1) / (2 * W);
@@ -368,19 +423,19 @@ template <typename T, int W, bool GRAD> hyena_status qk_launch_w(QkArgs& a, int6
     while (lanes < units && lanes < 64) lanes *= 2;
     a.lanes = lanes;
     const int per = (units + lanes - 1) / lanes;
-    if (per <= 1) return qk_launch_one<T, W, 1, GRAD>(a, grid, s);
-    if (per <= 2) return qk_launch_one<T, W, 2, GRAD>(a, grid, s);
-    if constexpr (W == 1) return qk_launch_one<T, W, 8, GRAD>(a, grid, s);
+    if (per <= 1) return qk_launch_one<T, W, 1, GRAD>(a, s);
+    if (per <= 2) return qk_launch_one<T, W, 2, GRAD>(a, s);
+    if constexpr (W == 1) return qk_launch_one<T, W, 8, GRAD>(a, s);
     else return fail(HYENA_ERR_UNSUPPORTED, "qk norm: head width");
 }
 
-template <typename T, bool GRAD> hyena_status qk_launch(QkArgs& a, int64_t grid, hipStream_t s)
+template <typename T, bool GRAD> hyena_status qk_launch(QkArgs& a, hipStream_t s)
 {
     const int w = vector_width(a, sizeof(T), GRAD);
     if constexpr (sizeof(T) == 2)
-        if (w == 8) return qk_launch_w<T, 8, GRAD>(a, grid, s);
-    if (w == 4) return qk_launch_w<T, 4, GRAD>(a, grid, s);
-    return qk_launch_w<T, 1, GRAD>(a, grid, s);
+        if (w == 8) return qk_launch_w<T, 8, GRAD>(a, s);
+    if (w == 4) return qk_launch_w<T, 4, GRAD>(a, s);
+    return qk_launch_w<T, 1, GRAD>(a, s);
 }
 
 hyena_status qk_refuse(const char* what) { return fail(HYENA_ERR_INVALID_ARGUMENT, std::string("qk norm: ") + what); }
@@ -455,7 +510,6 @@ hyena_status qk_args(const hyena_qk_norm* op, void* q_out, void* k_out, QkArgs& 
     a.mean = op->norm == HYENA_NORM_RMS ? 1.0f / (float)op->D : 1.0f;
     a.eps = op->eps;
     a.rscale = op->rotary_scale;
-    shape_tiles(a, op->q_heads > op->k_heads ? op->q_heads : op->k_heads);
     return HYENA_OK;
 }
 
@@ -470,15 +524,13 @@ hyena_status qk_overlaps(const Span* ins, int nin, const Span* outs, int nout)
     return HYENA_OK;
 }
 
-int64_t grad_groups(const QkArgs& a) { return a.tiles < kQkGradGroups ? a.tiles : kQkGradGroups; }
-
 size_t part_bytes(int64_t groups, int64_t D) { return ((size_t)groups * (size_t)D * 4 + 255) & ~(size_t)255; }
 
-template <bool GRAD> hyena_status qk_by_type(int32_t io_dtype, QkArgs& a, int64_t grid, hipStream_t s)
+template <bool GRAD> hyena_status qk_by_type(int32_t io_dtype, QkArgs& a, hipStream_t s)
 {
-    if (io_dtype == HYENA_F32) return qk_launch<float, GRAD>(a, grid, s);
-    if (io_dtype == HYENA_BF16) return qk_launch<uint16_t, GRAD>(a, grid, s);
-    return qk_launch<_Float16, GRAD>(a, grid, s);
+    if (io_dtype == HYENA_F32) return qk_launch<float, GRAD>(a, s);
+    if (io_dtype == HYENA_BF16) return qk_launch<uint16_t, GRAD>(a, s);
+    return qk_launch<_Float16, GRAD>(a, s);
 }
 
 }  // namespace
@@ -495,7 +547,8 @@ hyena_status hyena_qk_norm_forward(const hyena_qk_norm* op, void* q_out, void* k
     hyena_status st = qk_args(op, q_out, k_out, a, ins, outs);
     if (st != HYENA_OK) return st;
     if ((st = qk_overlaps(ins, 6, outs, 2)) != HYENA_OK) return st;
-    return qk_by_type<false>(op->io_dtype, a, a.tiles, (hipStream_t)stream);
+    shape_tiles(a, element_bytes(op->io_dtype), false);
+    return qk_by_type<false>(op->io_dtype, a, (hipStream_t)stream);
 }
 
 hyena_status hyena_qk_norm_scratch_bytes(const hyena_qk_norm* op, size_t* bytes)
@@ -505,9 +558,12 @@ hyena_status hyena_qk_norm_scratch_bytes(const hyena_qk_norm* op, size_t* bytes)
     if (bytes == nullptr) return qk_refuse("bytes is NULL");
     QkArgs a{};
     a.rows = op->B * op->N;
+    a.D = (int32_t)op->D;
     a.rotary = (int32_t)op->rotary_dim;
-    shape_tiles(a, op->q_heads > op->k_heads ? op->q_heads : op->k_heads);
-    *bytes = 2 * part_bytes(grad_groups(a), op->D);
+    a.t[0].heads = (int32_t)op->q_heads;
+    a.t[1].heads = (int32_t)op->k_heads;
+    shape_tiles(a, element_bytes(op->io_dtype), true);
+    *bytes = part_bytes(a.t[0].groups, op->D) + part_bytes(a.t[1].groups, op->D);
     return HYENA_OK;
 }
 
@@ -531,21 +587,21 @@ hyena_status hyena_qk_norm_backward(const hyena_qk_norm* op, const hyena_view* d
     if (op->norm == HYENA_NORM_NONE && (dq_weight || dk_weight)) return qk_refuse("no norm, so no weights' gradients");
     if (weights && (scratch == nullptr || (uintptr_t)scratch % 16 != 0))
         return qk_refuse("scratch is NULL or not 16-byte aligned");
-    const int64_t groups = grad_groups(a);
-    const size_t part = part_bytes(groups, op->D);
+    shape_tiles(a, e, true);
+    const size_t part = part_bytes(a.t[0].groups, op->D), parts = part + part_bytes(a.t[1].groups, op->D);
     outs[2] = Span{dq_weight, (size_t)op->D * 4};
     outs[3] = Span{dk_weight, (size_t)op->D * 4};
-    outs[4] = Span{weights ? scratch : nullptr, 2 * part};
+    outs[4] = Span{weights ? scratch : nullptr, parts};
     if ((st = qk_overlaps(ins, 8, outs, 5)) != HYENA_OK) return st;
     a.t[0].dy = plain_view(*dq_out);
     a.t[1].dy = plain_view(*dk_out);
     a.t[0].dw_part = dq_weight ? (float*)scratch : nullptr;
     a.t[1].dw_part = dk_weight ? (float*)((char*)scratch + part) : nullptr;
     const hipStream_t s = (hipStream_t)stream;
-    if ((st = qk_by_type<true>(op->io_dtype, a, groups, s)) != HYENA_OK) return st;
+    if ((st = qk_by_type<true>(op->io_dtype, a, s)) != HYENA_OK) return st;
     if (!weights) return HYENA_OK;
-    HY_LAUNCH(kernel_label("hyena_qk_weight_grad"), hyena_qk_weight_grad, dim3((unsigned)((a.D + 15) / 16), 2), dim3(256),
-              0, s, a.t[0].dw_part, a.t[1].dw_part, dq_weight, dk_weight, (int)groups, a.D);
+    HY_LAUNCH(kernel_label("hyena_qk_weight_grad"), hyena_qk_weight_grad, dim3((unsigned)((a.D + 15) / 16), 2), dim3(1024),
+              0, s, a.t[0].dw_part, a.t[1].dw_part, dq_weight, dk_weight, a.t[0].groups, a.t[1].groups, a.D);
     const hipError_t err = hipGetLastError();
     return err == hipSuccess ? HYENA_OK : fail(HYENA_ERR_DEVICE, hipGetErrorString(err));
 }
