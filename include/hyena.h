@@ -331,11 +331,13 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  *
  * Precision.  States, decays, their sums and every accumulation are float32
  * (sums of log decays: float64).  With 16-bit storage the scores between
- * tokens and, for o, dk, dq and dv, the state are rounded to the storage type
- * as operands of the matrix products (relative error up to 2^-8 for bfloat16,
- * 2^-11 for binary16 scores, or 2^-25 absolutely where they are subnormal); the states
- * and the gradient of g are computed from operands split so that they keep
- * float32 accuracy.  Inputs within a row's length have to be finite (g may be
+ * tokens and, in bfloat16 for o and dv, the state are rounded to the storage
+ * type as operands of the matrix products (relative error up to 2^-8 for
+ * bfloat16, 2^-11 for binary16 scores, or 2^-25 absolutely where they are
+ * subnormal); the states, their gradients and the gradient of g are computed
+ * from operands split so that they keep float32 accuracy.  With binary16 the
+ * scores (times decay and scale) have to stay within its range, and the states
+ * and their gradients below 2^26.  Inputs within a row's length have to be finite (g may be
  * -infinity): an infinity or a NaN reaches its own and later tokens' results,
  * and may reach those of up to 63 tokens before it.
  *
@@ -355,7 +357,7 @@ typedef struct hyena_recurrence_s* hyena_recurrence_t;
 
 /*
  * Create a recurrence plan: B >= 1 rows of up to N >= 1 tokens (N below 2^31),
- * 1 <= heads <= 65536, 1 <= dk, dv <= 128, B * heads at most 2^24.  Touches no
+ * 1 <= heads <= 65536, 1 <= dk, dv <= 128, B * heads at most 2^22.  Touches no
  * GPU state.  Release with hyena_recurrence_destroy.  The token strides of a
  * recurrence's views are below 2^23 elements (any where N = 1).
  */

@@ -22,33 +22,33 @@ constexpr int kScanBatch = 16;
 
 __global__ __launch_bounds__(256) void hyena_rec_scan(RecScanArgs p)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= p.total) return;
     const int role = blockIdx.y;
-    const int64_t bh = i / p.per, e = i % p.per;
-    // entry n of role 0 goes to n + 1; role 1 counts entries and segments from the last
-    const int64_t step = role ? -p.per : p.per;
-    float* x = p.local[role] + bh * (p.nseg + 1) * p.per + e + (role ? p.nseg * p.per : 0);
-    const float* d = p.decay + bh * p.nseg + (role ? p.nseg - 1 : 0);
-    const int dstep = role ? -1 : 1;
-    float s = p.first[role] ? p.first[role][i] : 0.0f;
-    *x = s;
-    for (int n0 = 0; n0 < p.nseg; n0 += kScanBatch) {
-        float local[kScanBatch], decay[kScanBatch];
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.total; i += (int64_t)gridDim.x * 256) {
+        const int64_t bh = i / p.per, e = i % p.per;
+        // entry n of role 0 goes to n + 1; role 1 counts entries and segments from the last
+        const int64_t step = role ? -p.per : p.per;
+        float* x = p.local[role] + bh * (p.nseg + 1) * p.per + e + (role ? p.nseg * p.per : 0);
+        const float* d = p.decay + bh * p.nseg + (role ? p.nseg - 1 : 0);
+        const int dstep = role ? -1 : 1;
+        float s = p.first[role] ? p.first[role][i] : 0.0f;
+        *x = s;
+        for (int n0 = 0; n0 < p.nseg; n0 += kScanBatch) {
+            float local[kScanBatch], decay[kScanBatch];
 #pragma unroll
-        for (int n = 0; n < kScanBatch; ++n)
-            if (n0 + n < p.nseg) {
-                local[n] = x[(n0 + n + 1) * step];
-                decay[n] = d[(n0 + n) * dstep];
-            }
+            for (int n = 0; n < kScanBatch; ++n)
+                if (n0 + n < p.nseg) {
+                    local[n] = x[(n0 + n + 1) * step];
+                    decay[n] = d[(n0 + n) * dstep];
+                }
 #pragma unroll
-        for (int n = 0; n < kScanBatch; ++n)
-            if (n0 + n < p.nseg) {
-                s = fmaf(decay[n], s, local[n]);
-                x[(n0 + n + 1) * step] = s;
-            }
+            for (int n = 0; n < kScanBatch; ++n)
+                if (n0 + n < p.nseg) {
+                    s = fmaf(decay[n], s, local[n]);
+                    x[(n0 + n + 1) * step] = s;
+                }
+        }
+        if (p.last[role]) p.last[role][i] = s;
     }
-    if (p.last[role]) p.last[role][i] = s;
 }
 
 namespace {
@@ -104,7 +104,8 @@ hyena_status check_outputs(const Span* in, int nin, const Span* out, const char*
 
 hyena_status launch_scan(const RecScanArgs& a, int roles, hipStream_t s)
 {
-    HY_LAUNCH(kernel_label("hyena_rec_scan"), hyena_rec_scan, dim3((unsigned)((a.total + 255) / 256), (unsigned)roles),
+    const int64_t groups = (a.total + 255) / 256, most = (int64_t)1 << 22;  // the rest is looped over
+    HY_LAUNCH(kernel_label("hyena_rec_scan"), hyena_rec_scan, dim3((unsigned)(groups < most ? groups : most), (unsigned)roles),
               dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? HYENA_OK : fail(HYENA_ERR_DEVICE, hipGetErrorString(e));

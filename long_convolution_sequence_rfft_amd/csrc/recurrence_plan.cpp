@@ -28,8 +28,9 @@ hyena_status rec_plan_build(RecPlan& p, int64_t B, int64_t N, int64_t heads, int
     if (dk > 128 || dv > 128) return fail(HYENA_ERR_UNSUPPORTED, "recurrence: dk and dv must be in 1..128");
     if (N >= ((int64_t)1 << 31) - 64) return fail(HYENA_ERR_UNSUPPORTED, "recurrence: N must be below 2^31 - 64");
     if (heads > 65536) return fail(HYENA_ERR_UNSUPPORTED, "recurrence: at most 65536 heads");
-    if (B > ((int64_t)1 << 24) || B * heads > ((int64_t)1 << 24))
-        return fail(HYENA_ERR_UNSUPPORTED, "recurrence: B * heads must be at most 2^24");
+    // (a launch holds less than 2^32 threads: a workgroup per row and head has up to 512)
+    if (B > ((int64_t)1 << 22) || B * heads > ((int64_t)1 << 22))
+        return fail(HYENA_ERR_UNSUPPORTED, "recurrence: B * heads must be at most 2^22");
     if (io_dtype != HYENA_F32 && io_dtype != HYENA_BF16 && io_dtype != HYENA_F16)
         return fail(HYENA_ERR_UNSUPPORTED, "recurrence: unknown io dtype");
     p.B = B;

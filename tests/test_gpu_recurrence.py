@@ -107,7 +107,7 @@ def check_backward(c):
     dq, dk, dv, dg, ds = c.backward()
     ref = mixer_ref.recurrence_grad(do, q, k, v, g, c.scale, state, n, df)
     ab = [np.abs(x) if x is not None else None for x in (do, q, k, v)]
-    absolute = mixer_ref.recurrence_grad(*ab, g, c.scale, None if state is None else np.abs(state), n,
+    absolute = mixer_ref.recurrence_grad(*ab, g, abs(c.scale), None if state is None else np.abs(state), n,
                                          None if df is None else np.abs(df))
     u = mixer_ref.HALF_STEP[c.dtype]
     for got, r, a, x, what in zip((dq, dk, dv), ref, absolute, (k, q, do), ("dq", "dk", "dv")):

@@ -20,12 +20,19 @@ def ptr(i):
     ((0, 8, 2, 4, 4), INVALID), ((1, 0, 2, 4, 4), INVALID), ((1, 8, 0, 4, 4), INVALID), ((1, 8, 2, 0, 4), INVALID),
     ((1, 8, 2, 4, -1), INVALID), ((1, 8, 2, 129, 4), UNSUPPORTED), ((1, 8, 2, 4, 129), UNSUPPORTED),
     ((1, 1 << 31, 2, 4, 4), UNSUPPORTED), ((1 << 13, 8, 1 << 12, 4, 4), UNSUPPORTED),
+    ((1, 8, 65537, 4, 4), UNSUPPORTED), (((1 << 22) + 1, 8, 1, 4, 4), UNSUPPORTED),
     ((1 << 62, 8, 4, 4, 4), UNSUPPORTED), ((1, 8, 2, 4, 4, 3), UNSUPPORTED), ((1, 8, 2, 4, 4, -1), UNSUPPORTED),
 ])
 def test_recurrence_plans(args, code):
     st, plan = hyena.hyena_recurrence_create(*args, check=False)
     assert st == code and plan is None
     assert "recurrence" in hyena.hyena_last_error()
+
+
+def test_recurrence_largest_plans():
+    for args in ((1 << 22, 1, 1, 128, 128), (1 << 6, 8, 1 << 16, 1, 1), (1, (1 << 31) - 65, 1, 1, 1)):
+        _, plan = hyena.hyena_recurrence_create(*args)
+        hyena.hyena_recurrence_destroy(plan)
 
 
 def test_recurrence_null_plan_and_sizes():
@@ -68,6 +75,16 @@ BAD_INPUTS = [
     dict(v=hyena.View(ptr(2), -1, 48, 16)), dict(g=hyena.View(ptr(3), 900, 3, -1)), dict(g=hyena.View(None, 0, 0, 0)),
     dict(state=ptr(4) + 1), dict(lengths=ptr(5) + 2),
 ]
+
+
+def test_recurrence_token_strides(plan):
+    far = hyena.View(ptr(0), 1 << 34, 1 << 23, 8)
+    for name in ("q", "k", "v", "g"):
+        x = inputs(**{name: far})
+        assert hyena.hyena_recurrence_forward(plan, x, ptr(6), None, ptr(7)) == UNSUPPORTED
+        assert name + " has a token stride" in hyena.hyena_last_error()
+    out = hyena.RecurrenceGrads(ptr(8), ptr(9), ptr(10), ptr(11), None)
+    assert hyena.hyena_recurrence_backward(plan, inputs(), far, None, out, ptr(7)) == UNSUPPORTED
 
 
 @pytest.mark.parametrize("bad", BAD_INPUTS)
