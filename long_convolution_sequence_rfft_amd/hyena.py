@@ -583,19 +583,20 @@ class _Mixer:
             raise ValueError(f"the device must be a GPU, got {dev}")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.device = dev
+        self.device, self.index = dev, dev.index
+        self._lib = load()
+        self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         self._first_stream = self._stream()
 
     def _stream(self):
-        return self.torch._C._cuda_getCurrentRawStream(self.device.index)
+        return self._raw_stream(self.index)
 
     def _call(self, where, fn, *args):
         # launches go to the current device; a plan of another one makes its own current
-        cuda = self.torch.cuda
-        if cuda.current_device() == self.device.index:
+        if self._current() == self.index:
             st = fn(*args)
         else:
-            with cuda.device(self.device):
+            with self.torch.cuda.device(self.device):
                 st = fn(*args)
         if st != HYENA_OK:
             _check(st, where)
@@ -609,6 +610,9 @@ class _Mixer:
         if stream != self._first_stream:
             buffer.record_stream(self.torch.cuda.current_stream(self.device))
         return buffer.data_ptr()
+
+    def _fits(self, t, shape, dtype):
+        return isinstance(t, self.torch.Tensor) and t.dtype == dtype and t.device == self.device and t.shape == shape
 
     def _check_tensor(self, t, name, shape, dtype):
         if not isinstance(t, self.torch.Tensor):
@@ -624,7 +628,8 @@ class _Mixer:
         """Address of a contiguous tensor, 0 for None."""
         if t is None:
             return 0
-        self._check_tensor(t, name, shape, dtype)
+        if not self._fits(t, shape, dtype):
+            self._check_tensor(t, name, shape, dtype)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
@@ -632,7 +637,8 @@ class _Mixer:
     def _view(self, t, name, shape, dtype):
         """Address and strides (batch, token, head) of a [B, N, heads, width] or [B, N, heads]
         tensor."""
-        self._check_tensor(t, name, shape, dtype)
+        if not self._fits(t, shape, dtype):
+            self._check_tensor(t, name, shape, dtype)
         st = t.stride()
         if len(shape) == 4 and st[3] != 1 and shape[3] > 1:
             raise ValueError(f"the last axis of {name} must be contiguous")
@@ -642,14 +648,19 @@ class _Mixer:
 
     def _token_view(self, t, name, shape, dtype):
         """The same of one token per row: [B, heads, width] or [B, heads]."""
-        self._check_tensor(t, name, shape, dtype)
+        if not self._fits(t, shape, dtype):
+            self._check_tensor(t, name, shape, dtype)
         st = t.stride()
         if len(shape) == 3 and st[2] != 1 and shape[2] > 1:
             raise ValueError(f"the last axis of {name} must be contiguous")
         return (t.data_ptr(), st[0] if shape[0] > 1 else 0, 0, st[1] if shape[1] > 1 else 0)
 
-    def _out(self, out, name, shape, dtype):
+    def _out(self, out, name, shape, dtype, like=None):
+        """An output: the caller's, checked, or a new one (like a checked input of its shape and type,
+        which is made sooner)."""
         if out is None:
+            if like is not None:
+                return self.torch.empty_like(like, memory_format=self.torch.contiguous_format)
             return self.torch.empty(shape, dtype=dtype, device=self.device)
         self._dense(out, name, shape, dtype)
         return out
@@ -699,11 +710,11 @@ class Recurrence(_Mixer):
         """(o, final state or None).  scale: 1 / sqrt(dk) by default.  state: the state before
         token 0.  lengths: int32 [B], tokens per row (the others' o is 0)."""
         x = self._inputs(q, k, v, g, scale, state, lengths)
-        o = self._out(o, "o", (self.B, self.N, self.heads, self.dv), self.dtype)
+        o = self._out(o, "o", (self.B, self.N, self.heads, self.dv), self.dtype, v)
         if return_state or final_state is not None:
             final_state = self._out(final_state, "final_state", self.state_shape, self.torch.float32)
         stream = self._stream()
-        self._call("hyena_recurrence_forward", hyena_recurrence_forward, self.handle, x, o.data_ptr(),
+        self._call("hyena_recurrence_forward", self._lib.hyena_recurrence_forward, self.handle, x, o.data_ptr(),
                    final_state.data_ptr() if final_state is not None else None,
                    self._keep(self.workspace, stream), stream)
         return o, final_state
@@ -725,7 +736,7 @@ class Recurrence(_Mixer):
         grads = _PACK_GRADS(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
                             ds.data_ptr() if ds is not None else 0)
         stream = self._stream()
-        self._call("hyena_recurrence_backward", hyena_recurrence_backward, self.handle, x, d, df, grads,
+        self._call("hyena_recurrence_backward", self._lib.hyena_recurrence_backward, self.handle, x, d, df, grads,
                    self._keep(self.workspace, stream), stream)
         return dq, dk, dv, dg, ds
 
@@ -740,13 +751,13 @@ class Recurrence(_Mixer):
             *self._token_view(q, "q", (B, H, self.dk), self.dtype), *self._token_view(k, "k", (B, H, self.dk), self.dtype),
             *self._token_view(v, "v", (B, H, self.dv), self.dtype), *self._token_view(g, "g", (B, H), torch.float32),
             0, 0, self.dk ** -0.5 if scale is None else scale)
-        n = states.shape[0] if isinstance(states, torch.Tensor) and states.dim() == 4 else 0
+        n = states.shape[0] if isinstance(states, self.torch.Tensor) and states.dim() == 4 else 0
         table = self._dense(states, "states", (n, H, self.dk, self.dv), torch.float32)
         if not table:
             raise ValueError("states must be a torch tensor of at least one state")
         at = self._dense(slots, "slots", (B,), torch.int32)
-        o = self._out(o, "o", (B, H, self.dv), self.dtype)
-        self._call("hyena_recurrence_step", hyena_recurrence_step, self.handle, x, at, n, table, o.data_ptr(),
+        o = self._out(o, "o", (B, H, self.dv), self.dtype, v)
+        self._call("hyena_recurrence_step", self._lib.hyena_recurrence_step, self.handle, x, at, n, table, o.data_ptr(),
                    self._stream())
         return o
 
@@ -822,11 +833,11 @@ class QKNorm(_Mixer):
         """(normed and rotated q, k), dense.  positions: int32 [B, N], or token n is at
         offset + n."""
         op = self._describe(q, k, q_weight, k_weight, positions, offset)
-        q_out = self._out(q_out, "q_out", (self.B, self.N, self.q_heads, self.D), self.dtype)
-        k_out = self._out(k_out, "k_out", (self.B, self.N, self.k_heads, self.D), self.dtype)
+        q_out = self._out(q_out, "q_out", (self.B, self.N, self.q_heads, self.D), self.dtype, q)
+        k_out = self._out(k_out, "k_out", (self.B, self.N, self.k_heads, self.D), self.dtype, k)
         stream = self._stream()
         self._keep(self.freqs, stream)
-        self._call("hyena_qk_norm_forward", hyena_qk_norm_forward, op, q_out.data_ptr(), k_out.data_ptr(), stream)
+        self._call("hyena_qk_norm_forward", self._lib.hyena_qk_norm_forward, op, q_out.data_ptr(), k_out.data_ptr(), stream)
         return q_out, k_out
 
     def backward(self, dq_out, dk_out, q, k, q_weight=None, k_weight=None, positions=None, offset=0):
@@ -845,6 +856,6 @@ class QKNorm(_Mixer):
         stream = self._stream()
         self._keep(self.freqs, stream)
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-        self._call("hyena_qk_norm_backward", hyena_qk_norm_backward, op, dqo, dko, dq.data_ptr(), dk.data_ptr(),
+        self._call("hyena_qk_norm_backward", self._lib.hyena_qk_norm_backward, op, dqo, dko, dq.data_ptr(), dk.data_ptr(),
                    ptr(dqw), ptr(dkw), ptr(scratch), stream)
         return dq, dk, dqw, dkw
