@@ -413,12 +413,13 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
 // by both products before any rounding, the states' parts from split operands)
 // and kept in LDS for kGradHold chunks, then summed up in float64 by all waves.
 // ---------------------------------------------------------------------------
-template <typename T, int D, bool VEC>
+template <typename T, int DK, int DV, bool VEC>
 __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 {
+    constexpr int D = DK > DV ? DK : DV;
     constexpr int C = kRecChunk<T>, LD = D + kPad<T>, LC = C + kPad<T>;
     constexpr int NT = Mx<T>::kTerms;
-    constexpr int IT = C / 16, MT = D / 16, MW = D / 64;
+    constexpr int IT = C / 16, kCells = (DK / 16) * (DV / 64);
     using frag = typename Mx<T>::frag;
     using vec4 = typename Mx<T>::vec4;
     __shared__ __attribute__((aligned(16))) char smem[rec_grad_lds<T, D>()];
@@ -455,24 +456,24 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     T* const vout = (T*)p.dv_out + (b * p.N * p.heads + h) * p.dv;
 
     // gradient of the state after this segment, and its product with the state
-    f32x4 S[MT][MW];
+    // (waves of dk: [DV / 16][DK / 64] tiles, of dv: [DK / 16][DV / 64])
+    f32x4 S[kCells];
     const int64_t per = (int64_t)p.dk * p.dv;
     const int64_t entry = (bh * ((int64_t)p.nseg * p.every + 1) + (seg + 1) * p.every) * per;
     const float* ep = p.end ? p.end + entry : nullptr;
     const float* sp = p.start ? p.start + entry : nullptr;
     float cross = 0.0f;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int x = 0; x < kCells; ++x)
 #pragma unroll
-        for (int n = 0; n < MW; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * m + 4 * grp + r, col = 16 * (w4 + 4 * n) + l16;
-                const int kk = own_k ? col : row, vv = own_k ? row : col;
-                const bool in = kk < p.dk && vv < p.dv;
-                S[m][n][r] = ep && in ? ep[kk * p.dv + vv] : 0.0f;
-                if (own_k && ep && sp && in) cross += S[m][n][r] * sp[kk * p.dv + vv];
-            }
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * (own_k ? x / (DK / 64) : x / (DV / 64)) + 4 * grp + r;
+            const int col = 16 * (w4 + 4 * (own_k ? x % (DK / 64) : x % (DV / 64))) + l16;
+            const int kk = own_k ? col : row, vv = own_k ? row : col;
+            const bool in = kk < p.dk && vv < p.dv;
+            S[x][r] = ep && in ? ep[kk * p.dv + vv] : 0.0f;
+            if (own_k && ep && sp && in) cross += S[x][r] * sp[kk * p.dv + vv];
+        }
     cross = sum_rows(sum16(cross));
     if (lane == 0) sums[wave] = own_k ? (double)cross : 0.0;
     __syncthreads();
@@ -554,8 +555,10 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
             f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f}, d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
-                s = Mx<T>::mma(frag_at<T>(qr + tj * LD + 32 * k + 8 * grp), frag_at<T>(kr + tj * LD + 32 * k + 8 * grp), s);
-                d = Mx<T>::mma(frag_at<T>(dr + tj * LD + 32 * k + 8 * grp), frag_at<T>(vr + tj * LD + 32 * k + 8 * grp), d);
+                if (k < DK / 32)
+                    s = Mx<T>::mma(frag_at<T>(qr + tj * LD + 32 * k + 8 * grp), frag_at<T>(kr + tj * LD + 32 * k + 8 * grp), s);
+                if (k < DV / 32)
+                    d = Mx<T>::mma(frag_at<T>(dr + tj * LD + 32 * k + 8 * grp), frag_at<T>(vr + tj * LD + 32 * k + 8 * grp), d);
             }
             f32x4 w;
 #pragma unroll
@@ -595,13 +598,15 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
             for (int n = 0; n < 2; ++n) crossed[n] = dec.cross[i - 1][16 * (j0 + n) + l16];
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
-                const frag qf = frag_at<T>(qr + tr * LD + 32 * k + 8 * grp), df = frag_at<T>(dr + tr * LD + 32 * k + 8 * grp);
+                frag qf, df;
+                if (k < DK / 32) qf = frag_at<T>(qr + tr * LD + 32 * k + 8 * grp);
+                if (k < DV / 32) df = frag_at<T>(dr + tr * LD + 32 * k + 8 * grp);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     if (n == 1 && !two) break;
                     const int tj = 16 * (j0 + n) + l16;
-                    s[n] = Mx<T>::mma(qf, frag_at<T>(kr + tj * LD + 32 * k + 8 * grp), s[n]);
-                    d[n] = Mx<T>::mma(df, frag_at<T>(vr + tj * LD + 32 * k + 8 * grp), d[n]);
+                    if (k < DK / 32) s[n] = Mx<T>::mma(qf, frag_at<T>(kr + tj * LD + 32 * k + 8 * grp), s[n]);
+                    if (k < DV / 32) d[n] = Mx<T>::mma(df, frag_at<T>(vr + tj * LD + 32 * k + 8 * grp), d[n]);
                 }
             }
 #pragma unroll
@@ -628,6 +633,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
         // tensor of dS's update
         auto work = [&](auto is_dk, const T* across, const T* scores, const T* fold, const T* add, T* out) {
             constexpr bool kSums = decltype(is_dk)::value;
+            constexpr int kAcross = kSums ? DV : DK, MT = kAcross / 16, MW = (kSums ? DK : DV) / 64;
             const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
             constexpr int NS = kSums ? NT : NT == 2 ? 2 : 1;  // dS as an operand
             constexpr int NU = kSums ? NT : NT < 2 ? NT : 2;  // and in its updates
@@ -643,9 +649,9 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                 for (int i = 0; i < C / 32; ++i) ff[i] = cols_of.any(fold, nt, i);
                 f32x4 sx[IT] = {};
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
+                for (int k = 0; k < kAcross / 32; ++k) {
                     Split<T, NS> sf;
-                    sf.set(join8(S[2 * k][n], S[2 * k + 1][n]) * StateScale<T>::down);
+                    sf.set(join8(S[2 * k * MW + n], S[(2 * k + 1) * MW + n]) * StateScale<T>::down);
 #pragma unroll
                     for (int j = 0; j < IT; ++j)
                         sx[j] = mma_split<T, NS, true>(sf, frag_at<T>(across + (16 * j + l16) * LD + 32 * k + 8 * grp), sx[j]);
@@ -663,7 +669,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                         x = Mx<T>::mma(ff[i], frag_at<T>(scores + tj * LC + 32 * i + 8 * grp), x);
                     store_row4<T>(orows, orow + 16 * j * ostep, tj < left, 16 * nt + 4 * grp, width, x);
                 }
-                hold_schedule<(D > 64)>();
+                hold_schedule<(DK * DV > 64 * 64)>();
                 constexpr bool kLead = Mx<T>::kTerms == 2;
                 const float* f = kLead ? dec.inner : dec.head;
                 const float lead = kLead ? p.scale * dec.head[0] : 1.0f;
@@ -675,8 +681,8 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                 }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    S[m][n] = update<T>(S[m][n], all, lead, y, [&](int i) { return cols_of(add, m, i); });
-                hold_schedule<(D > 64)>();
+                    S[m * MW + n] = update<T>(S[m * MW + n], all, lead, y, [&](int i) { return cols_of(add, m, i); });
+                hold_schedule<(DK * DV > 64 * 64)>();
             }
             if constexpr (kSums) store_token_sums<IT>(part + w4 * C, kdot, lane, grp);
         };

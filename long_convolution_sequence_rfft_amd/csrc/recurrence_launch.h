@@ -64,22 +64,23 @@ template <typename T> hyena_status rec_launch_out(const RecArgs& a, int64_t bh, 
     return rec_out_pick<T, false, true>(a, bh, s);
 }
 
-template <typename T, int D> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
+template <typename T, int DK, int DV> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
 {
     const bool vec = a.q.vec && a.k.vec && a.v.vec && a.o.vec;
     const dim3 grid((unsigned)(bh * a.nseg));
     if (vec)
-        HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), D, true), (hyena_rec_grad<T, D, true>), grid, dim3(512), 0,
-                  s, a);
+        HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), DK, DV, true), (hyena_rec_grad<T, DK, DV, true>), grid,
+                  dim3(512), 0, s, a);
     else
-        HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), D, false), (hyena_rec_grad<T, D, false>), grid, dim3(512),
-                  0, s, a);
+        HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), DK, DV, false), (hyena_rec_grad<T, DK, DV, false>), grid,
+                  dim3(512), 0, s, a);
     return rec_done();
 }
 
 template <typename T> hyena_status rec_launch_grad(const RecGradArgs& a, int64_t bh, hipStream_t s)
 {
-    return a.dk <= 64 && a.dv <= 64 ? rec_grad_one<T, 64>(a, bh, s) : rec_grad_one<T, 128>(a, bh, s);
+    if (a.dk <= 64) return a.dv <= 64 ? rec_grad_one<T, 64, 64>(a, bh, s) : rec_grad_one<T, 64, 128>(a, bh, s);
+    return a.dv <= 64 ? rec_grad_one<T, 128, 64>(a, bh, s) : rec_grad_one<T, 128, 128>(a, bh, s);
 }
 
 template <typename T> hyena_status rec_launch_step(const RecStepArgs& a, int64_t B, hipStream_t s)
