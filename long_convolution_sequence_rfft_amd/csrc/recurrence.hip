@@ -55,13 +55,14 @@ namespace {
 
 bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 
-// A view as the kernels take it: vec, whether a row is made of whole, aligned
-// 16-byte vectors.
+// A view as the kernels take it.
 RView rview(const hyena_view& v, int64_t width, size_t element)
 {
-    const int64_t w = 16 / (int64_t)element;
-    const bool vec = width % w == 0 && aligned(v.data, 16) && v.batch % w == 0 && v.token % w == 0 && v.head % w == 0;
-    return RView{v.data, v.batch, v.token, v.head, vec ? 1 : 0};
+    auto made_of = [&](int64_t n) {
+        return width % n == 0 && aligned(v.data, (size_t)n * element) && v.batch % n == 0 && v.token % n == 0 && v.head % n == 0;
+    };
+    const int32_t vec = made_of(16 / (int64_t)element) ? kRowVectors : made_of(2) ? kRowPairs : kRowElements;
+    return RView{v.data, v.batch, v.token, v.head, vec};
 }
 
 hyena_status refuse(const char* what) { return fail(HYENA_ERR_INVALID_ARGUMENT, std::string("recurrence: ") + what); }

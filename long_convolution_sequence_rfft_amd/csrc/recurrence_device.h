@@ -188,8 +188,12 @@ template <typename T> constexpr int kPad = 16 / (int)sizeof(T);
 struct RView {
     const void* p;
     int64_t b, t, h;
-    int32_t vec;  // each 16 bytes of a row are one aligned vector
+    int32_t vec;  // kRowVectors, kRowPairs or kRowElements
 };
+// What a row is read by: its 16-byte groups are whole, aligned vectors; the same
+// of pairs of elements; or anything.  (2 x 4096 tokens, 8 heads of 62 in bf16:
+// forward 47 us by elements, 34 by pairs; heads of 64 by vectors 27.)
+enum : int32_t { kRowElements = 0, kRowPairs = 1, kRowVectors = 2 };
 
 // Rows of one (batch row, head) of a tensor, read and written through a buffer
 // descriptor: an access whose offset is kOutside is dropped (a load gives 0),
@@ -230,6 +234,19 @@ template <typename T> __device__ __forceinline__ T load1(__amdgpu_buffer_rsrc_t 
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, (int)scalar, 0));
     else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, (int)off, (int)scalar, 0));
 }
+// two elements that make an aligned pair
+template <typename T> __device__ __forceinline__ void load2(T* e, __amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t scalar = 0)
+{
+    if constexpr (sizeof(T) == 4) {
+        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, (int)scalar, 0);
+        e[0] = __builtin_bit_cast(T, (uint32_t)x[0]);
+        e[1] = __builtin_bit_cast(T, (uint32_t)x[1]);
+    } else {
+        const uint32_t x = __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, (int)scalar, 0);
+        e[0] = __builtin_bit_cast(T, (uint16_t)(x & 0xffff));
+        e[1] = __builtin_bit_cast(T, (uint16_t)(x >> 16));
+    }
+}
 template <typename T> __device__ __forceinline__ void store1(__amdgpu_buffer_rsrc_t r, uint32_t off, T x)
 {
     if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, (int)off, 0, 0);
@@ -243,6 +260,14 @@ __device__ __forceinline__ void store_row4(__amdgpu_buffer_rsrc_t r, uint32_t of
     const typename Mx<T>::vec4 y = Mx<T>::narrow(x);
     if ((width & 3) == 0) {
         store4<T>(r, in & (ch < width) ? off + ch * (uint32_t)sizeof(T) : kOutside, y);
+    } else if ((width & 1) == 0) {
+        const u32x2* e = (const u32x2*)&y;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t at = in & (ch + 2 * j < width) ? off + (ch + 2 * j) * (uint32_t)sizeof(T) : kOutside;
+            if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b64(e[j], r, (int)at, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b32((*e)[j], r, (int)at, 0, 0);
+        }
     } else {
         const T* e = (const T*)&y;
 #pragma unroll
@@ -269,10 +294,12 @@ __device__ __forceinline__ int again_uniform(int x)
 struct Stream {
     const char* p;
     uint32_t step;
+    int32_t vec;
     template <typename T> __device__ __forceinline__ void start(const RView& v, int64_t b, int64_t h, int64_t t)
     {
         p = (const char*)v.p + (b * v.b + h * v.h + t * v.t) * (int64_t)sizeof(T);
         step = (uint32_t)v.t * (uint32_t)sizeof(T);
+        vec = v.vec;
     }
     __device__ __forceinline__ void move(int tokens) { p += (int64_t)tokens * (int64_t)step; }
 };
@@ -320,28 +347,41 @@ template <typename T, int C, int D, int THREADS, int R> struct Tile {
 
     // The first n tokens of the stream from its place on; tokens at n and after
     // it, and channels at `width` and after it, are zero and not read.  VEC:
-    // each group of W channels is one vector.
+    // known to be kRowVectors.
     template <bool VEC> __device__ __forceinline__ void load(const Stream& s, const Places& at, int n, int width, int tid)
     {
         const __amdgpu_buffer_rsrc_t rsrc = rows_at(s.p);
+        // each block's rows by `one`, of its registers, byte offset and first channel
+        auto blocks = [&](auto one) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int t = token(tid + i * THREADS), c = channel(tid + i * THREADS);
+            for (int i = 0; i < kPer; ++i) {
+                const int t = token(tid + i * THREADS), c = channel(tid + i * THREADS);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t off = t + r < n ? at.off[i] : kOutside;
-                if constexpr (VEC) {
-                    *(u32x4*)x[i][r] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)off, (int)(r * s.step), 0));
-                } else {
-                    T e[W];
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        e[j] = load1<T>(rsrc, (c + j < width) & (off != kOutside) ? off + j * (uint32_t)sizeof(T) : kOutside,
-                                        r * s.step);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) x[i][r][v] = *(const vec4*)(e + 4 * v);
-                }
+                for (int r = 0; r < R; ++r) one(x[i][r], t + r < n ? at.off[i] : kOutside, c, r * s.step);
             }
+        };
+        if (VEC || s.vec == kRowVectors) {
+            blocks([&](vec4* to, uint32_t off, int, uint32_t scalar) {
+                *(u32x4*)to = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)off, (int)scalar, 0));
+            });
+        } else if (s.vec == kRowPairs) {
+            blocks([&](vec4* to, uint32_t off, int c, uint32_t scalar) {
+                T e[W];
+#pragma unroll
+                for (int j = 0; j < W; j += 2)
+                    load2<T>(e + j, rsrc, (c + j < width) & (off != kOutside) ? off + j * (uint32_t)sizeof(T) : kOutside, scalar);
+#pragma unroll
+                for (int v = 0; v < V; ++v) to[v] = *(const vec4*)(e + 4 * v);
+            });
+        } else {
+            blocks([&](vec4* to, uint32_t off, int c, uint32_t scalar) {
+                T e[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    e[j] = load1<T>(rsrc, (c + j < width) & (off != kOutside) ? off + j * (uint32_t)sizeof(T) : kOutside, scalar);
+#pragma unroll
+                for (int v = 0; v < V; ++v) to[v] = *(const vec4*)(e + 4 * v);
+            });
         }
     }
     // rows[token][channel], channels in operand order (perm4)
@@ -391,8 +431,14 @@ template <typename T, int IT, int CW> struct UnderResults {
                 const int c = 16 * (wave + 4 * v) + 4 * grp;
                 const uint32_t off = (uint32_t)l16 * s.step + (uint32_t)c * (uint32_t)sizeof(T);
                 const bool in = 16 * i + l16 < n;
-                if constexpr (VEC) {
+                if (VEC || s.vec == kRowVectors) {
                     x[i][v] = load4<T>(rsrc, in & (c < width) ? off : kOutside, 16 * i * s.step);
+                } else if (s.vec == kRowPairs) {
+                    T e[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2)
+                        load2<T>(e + j, rsrc, in & (c + j < width) ? off + j * (uint32_t)sizeof(T) : kOutside, 16 * i * s.step);
+                    x[i][v] = *(const typename Mx<T>::vec4*)e;
                 } else {
                     T e[4];
 #pragma unroll

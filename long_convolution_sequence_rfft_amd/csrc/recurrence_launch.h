@@ -12,12 +12,14 @@ inline hyena_status rec_done()
     return e == hipSuccess ? HYENA_OK : fail(HYENA_ERR_DEVICE, hipGetErrorString(e));
 }
 
-// Rows whose groups of 4 channels are whole, aligned vectors (VEC) have kernels
-// of their own: one load where the others take four.
+// Rows that are all made of 16-byte vectors have kernels of their own (VEC): the
+// others choose by tensor what they load.
+template <typename... V> bool by_vectors(const V&... v) { return ((v.vec == kRowVectors) && ...); }
+
 template <typename T, int DK, int DV>
 hyena_status rec_states_one(const RecStateArgs& a, int64_t bh, int roles, hipStream_t s)
 {
-    const bool vec = a.x[0].vec && a.y[0].vec && (roles == 1 || (a.x[1].vec && a.y[1].vec));
+    const bool vec = by_vectors(a.x[0], a.y[0]) && (roles == 1 || by_vectors(a.x[1], a.y[1]));
     const dim3 grid((unsigned)(bh * a.nseg), (unsigned)roles);
     if (vec)
         HY_LAUNCH(kernel_label("hyena_rec_states", type_label<T>(), DK, DV, true), (hyena_rec_states<T, DK, DV, true>), grid,
@@ -37,7 +39,7 @@ template <typename T> hyena_status rec_launch_states(const RecStateArgs& a, int6
 template <typename T, int DA, int DC, bool TRANS, bool EXACT>
 hyena_status rec_out_one(const RecArgs& a, int64_t bh, hipStream_t s)
 {
-    const bool vec = a.a.vec && a.b.vec && a.c.vec && (!TRANS || a.r.vec);
+    const bool vec = by_vectors(a.a, a.b, a.c) && (!TRANS || by_vectors(a.r));
     const dim3 grid((unsigned)(bh * a.nseg));
     if (vec)
         HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, EXACT, true),
@@ -66,7 +68,7 @@ template <typename T> hyena_status rec_launch_out(const RecArgs& a, int64_t bh, 
 
 template <typename T, int DK, int DV> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
 {
-    const bool vec = a.q.vec && a.k.vec && a.v.vec && a.o.vec;
+    const bool vec = by_vectors(a.q, a.k, a.v, a.o);
     const dim3 grid((unsigned)(bh * a.nseg));
     if (vec)
         HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), DK, DV, true), (hyena_rec_grad<T, DK, DV, true>), grid,

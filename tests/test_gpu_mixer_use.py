@@ -32,6 +32,31 @@ def test_aligned_slices_of_one_projection(dtype):
     check_backward(c)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", [(2, 150, 2, 62, 62), (1, 130, 1, 126, 90), (1, 140, 2, 64, 75), (1, 140, 2, 75, 64),
+                                   (2, 70, 3, 2, 6), (1, 90, 2, 30, 128)])
+def test_rows_of_pairs_and_of_single_elements(shape, dtype):
+    """Each tensor's rows are read by 16-byte vectors, by pairs or by elements, as its width and strides
+    allow; here they differ from tensor to tensor."""
+    c = Case(*shape, dtype, seed=sum(shape) + 2)
+    check_forward(c)
+    check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_slices_that_start_at_an_even_or_odd_element(dtype):
+    import torch
+    c = Case(2, 140, 2, 24, 40, dtype, seed=14)
+    for at in (2, 3):
+        full = torch.zeros((2, 140, 2, 24 + 24 + 40 + 8), dtype=c.q.dtype, device="cuda")
+        q, k, v = full[..., at:at + 24], full[..., at + 24:at + 48], full[..., 52:92]
+        for view, x in ((q, c.q), (k, c.k), (v, c.v)):
+            view.copy_(x)
+        c.q, c.k, c.v = q, k, v
+        check_forward(c)
+        check_backward(c)
+
+
 def test_large_values_and_scale():
     """States far from 1 (binary16: up to 2^26) and a negative scale."""
     for dtype in ("f32", "bf16", "f16"):
