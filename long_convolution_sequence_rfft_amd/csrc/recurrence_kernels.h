@@ -8,6 +8,18 @@
 // per C tokens and stays in registers.  The chunks of a segment run one after
 // the other; segments run in parallel, each from the state that
 // hyena_rec_states and hyena_rec_scan have put before it.
+//
+// With A_i the product of the decays from the chunk's start through token i, the
+// decay between tokens j <= i of a chunk is w_ij = A_i / A_j, made of differences
+// of logs (see Decays), and with S the state before the chunk
+//   o_i = scale (A_i S^T q_i + sum_{j <= i} w_ij (q_i . k_j) v_j),
+//   S <- A_last S + sum_j (A_last / A_j) k_j v_j^T.
+// Chunks are 64 tokens (32 in float32, whose operands take twice the LDS), so a
+// row of a transposed tile is 128 bytes.  Two passes over k and v, one for the
+// segments' states and one for the outputs, are the price of walking a long
+// sequence in parallel: at 65536 tokens of 12 heads of 64 in bfloat16 the three
+// kernels take 148 us for 604 MB (403 without the first pass), 4.1 TB/s, where
+// a large copy reaches 5.1.
 #pragma once
 
 #include <type_traits>
@@ -49,7 +61,9 @@ template <int IT> __device__ __forceinline__ void store_token_sums(float* out, c
 
 // ---------------------------------------------------------------------------
 // Local states of the segments.  One workgroup per (row, head, segment, role);
-// wave w owns every fourth 16-column tile of the state.
+// wave w owns every fourth 16-column tile of the state.  Bound by memory: 54 us
+// at 65536 tokens of 12 heads of 64 in bfloat16 (201 MB, 4.0 TB/s without the
+// 4 us that any launch takes), 32 us with both roles at 2 x 8192 (100 MB).
 // ---------------------------------------------------------------------------
 template <typename T, int DK, int DV, bool VEC>
 __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states(RecStateArgs p)
@@ -180,6 +194,12 @@ template <typename T, int D> constexpr size_t rec_grad_lds()
 // One workgroup of four waves per (row, head, segment).  Waves share the score
 // tiles of a chunk (written to LDS in storage type) and each owns every fourth
 // 16-channel tile of c: its part of the state never leaves its registers.
+//
+// The outputs are bound by memory: 65536 tokens of 12 heads of 64 in bfloat16 in
+// 91 us (403 MB, 4.6 TB/s without the launch); with heads of 128 (2 x 8192
+// tokens of 6, 41 us, 126 MB) and with split operands (dq at 2 x 8192 tokens of
+// 12 heads of 64: 42 us, 126 MB; 620 vector instructions per wave and chunk)
+// by the instructions of a chunk, with two or three waves per SIMD.
 // ---------------------------------------------------------------------------
 template <typename T, int DA, int DC, bool TRANS, bool EXACT, bool VEC>
 __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) void hyena_rec_out(RecArgs p)
@@ -412,6 +432,15 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
 // segment's end: both dot products are made of float32 values (scores weighted
 // by both products before any rounding, the states' parts from split operands)
 // and kept in LDS for kGradHold chunks, then summed up in float64 by all waves.
+//
+// Bound by a chunk's instructions: 66 us at 2 x 8192 tokens of 12 heads of 64 in
+// bfloat16 (176 MB), 80 us at 4 x 2048 in float32; 610 vector instructions per
+// wave and chunk keep the vector units busy for half the time, LDS accesses the
+// LDS for 40%, matrix products the matrix units for 17%.  Two workgroups per
+// compute unit, with 128 registers and 81 KB of LDS each, came to 64 us, two
+// chunks in LDS with the next one's scores made beside this one's gradients to
+// 66: not kept.  dk and dv are padded apart: with both at 128 heads of 40 and 72
+// in float16 took 69 us, now 41 (3 x 4100 tokens, 5 heads).
 // ---------------------------------------------------------------------------
 template <typename T, int DK, int DV, bool VEC>
 __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
@@ -732,7 +761,10 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 
 // ---------------------------------------------------------------------------
 // One token: S <- exp(g) S + k v^T in place, o = scale S^T q.  One workgroup per
-// (row, head); a thread owns VEC columns and every (256 / columns)th row.
+// (row, head); a thread owns VEC columns and every (256 / columns)th row.  Bound
+// by memory, for few rows by the launch: 256 requests of 12 heads of 64 in 17 us
+// (101 MB of states read and written, in part from the last-level cache), one
+// request in 6 us on the device.
 // ---------------------------------------------------------------------------
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void hyena_rec_step(RecStepArgs p)
