@@ -334,12 +334,13 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  * tokens and, in bfloat16 for o and dv, the state are rounded to the storage
  * type as operands of the matrix products (relative error up to 2^-8 for
  * bfloat16, 2^-11 for binary16 scores, or 2^-25 absolutely where they are
- * subnormal); the states, their gradients and the gradient of g are computed
- * from operands split so that they keep float32 accuracy.  With binary16 the
+ * subnormal), but in calls of few tokens (N <= 64 and B * heads <= 256) neither
+ * is; the states, their gradients and the gradient of g are computed from
+ * operands split so that they keep float32 accuracy.  With binary16 the
  * scores (times decay and scale) have to stay within its range, and the states
- * and their gradients below 2^26.  Inputs within a row's length have to be finite (g may be
- * -infinity): an infinity or a NaN reaches its own and later tokens' results,
- * and may reach those of up to 63 tokens before it.
+ * and their gradients below 2^26.  Inputs within a row's length have to be
+ * finite (g may be -infinity): an infinity or a NaN reaches its own and later
+ * tokens' results, and may reach those of up to 63 tokens before it.
  *
  * No atomics are used: the same call gives the same bits.
  */

@@ -164,21 +164,27 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
     if (role == 0 && tid == 0) p.decay[bh * p.nseg + seg] = total;
 }
 
+// FINE: of 16-bit types the scores, too, are split operands, and no state is
+// rounded to one term, so that a result's own rounding is the only one.  In long
+// rows a result sums many scores and the others' roundings add as much as its
+// own; in rows of a few tokens they do not average out.
+template <typename T, bool FINE> constexpr int kScoreTerms = FINE && sizeof(T) == 2 ? 2 : 1;
+
 // LDS of the two kernels below.
-template <typename T, int DA, int DC, bool TRANS> constexpr size_t rec_out_lds()
+template <typename T, int DA, int DC, bool TRANS, bool FINE> constexpr size_t rec_out_lds()
 {
     constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
-    return sizeof(T) * (size_t)(C * LA + C * LB + 2 * DM * C + C * LC) +
+    return sizeof(T) * (size_t)(C * LA + C * LB + 2 * DM * C + kScoreTerms<T, FINE> * C * LC) +
            kDecayBatch * sizeof(DecaysOf<T>) + (TRANS ? 4 * C * sizeof(float) : 0);
 }
 
 // Chunks whose terms of dg are held before they are summed up.
 constexpr int kGradHold = 16;
 
-template <typename T, int D> constexpr size_t rec_grad_lds()
+template <typename T, int D, bool FINE> constexpr size_t rec_grad_lds()
 {
     constexpr int C = kRecChunk<T>, LD = D + kPad<T>, LC = C + kPad<T>;
-    return sizeof(T) * (size_t)(4 * C * LD + 2 * D * C + 2 * C * LC) + kDecayBatch * sizeof(DecaysOf<T>) +
+    return sizeof(T) * (size_t)(4 * C * LD + 2 * D * C + 2 * kScoreTerms<T, FINE> * C * LC) + kDecayBatch * sizeof(DecaysOf<T>) +
            sizeof(float) * (size_t)(2 * (C / 16) * C + 4 * C + kDecayBatch * C + kGradHold * C) + kGradHold * 16;
 }
 
@@ -201,22 +207,23 @@ template <typename T, int D> constexpr size_t rec_grad_lds()
 // 12 heads of 64: 42 us, 126 MB; 620 vector instructions per wave and chunk)
 // by the instructions of a chunk, with two or three waves per SIMD.
 // ---------------------------------------------------------------------------
-template <typename T, int DA, int DC, bool TRANS, bool EXACT, bool VEC>
+template <typename T, int DA, int DC, bool TRANS, bool EXACT, bool VEC, bool FINE>
 __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) void hyena_rec_out(RecArgs p)
 {
     constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
     constexpr int NT = EXACT || Mx<T>::kTerms < 2 ? Mx<T>::kTerms : 2;  // state update
-    constexpr int NS = TRANS ? Mx<T>::kTerms : Mx<T>::kTerms == 2 ? 2 : 1;  // state as an operand
+    constexpr int NS = TRANS ? Mx<T>::kTerms : Mx<T>::kTerms < 2 ? 1 : Mx<T>::kTerms == 2 || FINE ? 2 : 1;  // state as an operand
+    constexpr int NP = kScoreTerms<T, FINE>;
     constexpr int AT = DA / 16, CW = DC / 64, IT = C / 16;
     using frag = typename Mx<T>::frag;
     using vec4 = typename Mx<T>::vec4;
-    __shared__ __attribute__((aligned(16))) char smem[rec_out_lds<T, DA, DC, TRANS>()];
+    __shared__ __attribute__((aligned(16))) char smem[rec_out_lds<T, DA, DC, TRANS, FINE>()];
     T* ar = (T*)smem;              // [C][LA]
     T* br = ar + C * LA;           // [C][LB]
     T* bt = br + C * LB;           // [DM][C] transposed
     T* ct = bt + DM * C;           // [DM][C] transposed
     T* ps = ct + DM * C;           // [C][LC]
-    char* tail = (char*)(ps + C * LC);
+    char* tail = (char*)(ps + NP * C * LC);
     DecaysOf<T>* const decays = (DecaysOf<T>*)tail;
     float* part = (float*)(tail + kDecayBatch * sizeof(DecaysOf<T>));  // [4][C], TRANS
 
@@ -339,10 +346,11 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
             }
 #pragma unroll
             for (int j = 0; j < IT - 1; ++j)
-                *(vec4*)(ps + ti * LC + 16 * j + 4 * grp) = Mx<T>::narrow(s[j] * (cw[j] * within));
+                store_split<T, NP>(ps + ti * LC + 16 * j + 4 * grp, C * LC, s[j] * (cw[j] * within));
             // the tile right of the last own one is not among the above; then the own tile itself
-            *(vec4*)(ps + ti * LC + 16 * (IT - 1) + 4 * grp) = vec4{};
-            *(vec4*)(ps + ti * LC + to) = Mx<T>::narrow(own);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) *(vec4*)(ps + n * C * LC + ti * LC + 16 * (IT - 1) + 4 * grp) = vec4{};
+            store_split<T, NP>(ps + ti * LC + to, C * LC, own);
         }
         __syncthreads();
 
@@ -374,8 +382,12 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
                     rdot[i] += o[0] * r[0] + o[1] * r[1] + o[2] * r[2] + o[3] * r[3];
                 }
 #pragma unroll
-                for (int j = 0; j <= i / 2; ++j)
-                    o = Mx<T>::mma(cf[j], frag_at<T>(ps + ti * LC + 32 * j + 8 * grp), o);
+                for (int j = 0; j <= i / 2; ++j) {
+                    Split<T, NP> w;
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) w.f[n] = frag_at<T>(ps + n * C * LC + ti * LC + 32 * j + 8 * grp);
+                    o = mma_split<T, NP, false>(w, cf[j], o);
+                }
                 store_row4<T>(orows, orow + 16 * i * ostep, ti < left, 16 * vt + 4 * grp, p.dc, o);
             }
             // the state after this chunk
@@ -442,16 +454,17 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
 // 66: not kept.  dk and dv are padded apart: with both at 128 heads of 40 and 72
 // in float16 took 69 us, now 41 (3 x 4100 tokens, 5 heads).
 // ---------------------------------------------------------------------------
-template <typename T, int DK, int DV, bool VEC>
+template <typename T, int DK, int DV, bool VEC, bool FINE>
 __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 {
     constexpr int D = DK > DV ? DK : DV;
     constexpr int C = kRecChunk<T>, LD = D + kPad<T>, LC = C + kPad<T>;
     constexpr int NT = Mx<T>::kTerms;
+    constexpr int NP = kScoreTerms<T, FINE>;
     constexpr int IT = C / 16, kCells = (DK / 16) * (DV / 64);
     using frag = typename Mx<T>::frag;
     using vec4 = typename Mx<T>::vec4;
-    __shared__ __attribute__((aligned(16))) char smem[rec_grad_lds<T, D>()];
+    __shared__ __attribute__((aligned(16))) char smem[rec_grad_lds<T, D, FINE>()];
     T* qr = (T*)smem;              // [C][LD]
     T* kr = qr + C * LD;           // [C][LD]
     T* dr = kr + C * LD;           // [C][LD]
@@ -459,8 +472,8 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     T* qt = vr + C * LD;           // [D][C] transposed
     T* dt = qt + D * C;            // [D][C] transposed
     T* pa = dt + D * C;            // [C][LC] row j, column i: w_ij (q_i . k_j)
-    T* pd = pa + C * LC;           // [C][LC] w_ij (do_i . v_j)
-    char* rest = (char*)(pd + C * LC);
+    T* pd = pa + NP * C * LC;      // [C][LC] w_ij (do_i . v_j)
+    char* rest = (char*)(pd + NP * C * LC);
     DecaysOf<T>* const decays = (DecaysOf<T>*)rest;
     float* rows = (float*)(rest + kDecayBatch * sizeof(DecaysOf<T>));  // [IT][C] by j tile: sum over its j, per i
     float* cols = rows + IT * C;                       // [IT][C] by i tile: sum over its i, per j
@@ -601,11 +614,14 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
             }
             const f32x4 both = s * d;
             d = d * w;
-            *(vec4*)(pa + tj * LC + ti) = Mx<T>::narrow(s);
-            *(vec4*)(pd + tj * LC + ti) = Mx<T>::narrow(d);
+            store_split<T, NP>(pa + tj * LC + ti, C * LC, s);
+            store_split<T, NP>(pd + tj * LC + ti, C * LC, d);
             if (at & 1) {  // the tile above an odd own one is read with it
-                *(vec4*)(pa + tj * LC + ti - 16) = vec4{};
-                *(vec4*)(pd + tj * LC + ti - 16) = vec4{};
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    *(vec4*)(pa + n * C * LC + tj * LC + ti - 16) = vec4{};
+                    *(vec4*)(pd + n * C * LC + tj * LC + ti - 16) = vec4{};
+                }
             }
             // every lane of a row or column writes the same sum
             cols[at * C + tj] = sum_rows((both[0] + both[1]) + (both[2] + both[3]));
@@ -646,8 +662,8 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                 s[n] = s[n] * w;
                 const f32x4 both = s[n] * d[n];
                 d[n] = d[n] * w;
-                *(vec4*)(pa + tj * LC + ti) = Mx<T>::narrow(s[n]);
-                *(vec4*)(pd + tj * LC + ti) = Mx<T>::narrow(d[n]);
+                store_split<T, NP>(pa + tj * LC + ti, C * LC, s[n]);
+                store_split<T, NP>(pd + tj * LC + ti, C * LC, d[n]);
                 cols[i * C + tj] = sum_rows((both[0] + both[1]) + (both[2] + both[3]));
                 f32x4 row;
 #pragma unroll
@@ -664,7 +680,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
             constexpr bool kSums = decltype(is_dk)::value;
             constexpr int kAcross = kSums ? DV : DK, MT = kAcross / 16, MW = (kSums ? DK : DV) / 64;
             const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
-            constexpr int NS = kSums ? NT : NT == 2 ? 2 : 1;  // dS as an operand
+            constexpr int NS = kSums ? NT : NT < 2 ? 1 : NT == 2 || FINE ? 2 : 1;  // dS as an operand
             constexpr int NU = kSums ? NT : NT < 2 ? NT : 2;  // and in its updates
             const __amdgpu_buffer_rsrc_t orows = rows_at(out + tb0 * p.heads * width);
             const uint32_t ostep = (uint32_t)p.heads * (uint32_t)width * (uint32_t)sizeof(T);
@@ -694,8 +710,12 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                         kdot[j] += x[0] * kk[0] + x[1] * kk[1] + x[2] * kk[2] + x[3] * kk[3];
                     }
 #pragma unroll
-                    for (int i = j / 2; i < C / 32; ++i)
-                        x = Mx<T>::mma(ff[i], frag_at<T>(scores + tj * LC + 32 * i + 8 * grp), x);
+                    for (int i = j / 2; i < C / 32; ++i) {
+                        Split<T, NP> w;
+#pragma unroll
+                        for (int n = 0; n < NP; ++n) w.f[n] = frag_at<T>(scores + n * C * LC + tj * LC + 32 * i + 8 * grp);
+                        x = mma_split<T, NP, false>(w, ff[i], x);
+                    }
                     store_row4<T>(orows, orow + 16 * j * ostep, tj < left, 16 * nt + 4 * grp, width, x);
                 }
                 hold_schedule<(DK * DV > 64 * 64)>();

@@ -57,6 +57,28 @@ def test_slices_that_start_at_an_even_or_odd_element(dtype):
         check_backward(c)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(1, 1, 3, 64, 64), (2, 5, 3, 128, 96), (4, 64, 2, 40, 128), (3, 33, 5, 128, 128),
+                                   (1, 64, 1, 7, 20)])
+def test_calls_of_few_tokens_round_only_their_results(shape, dtype):
+    """No score and no state is rounded to 16 bits on the way: half a step of the value, and 2^-15 of the
+    sum of absolute values that float32 may lose."""
+    import torch
+    c = Case(*shape, dtype, seed=sum(shape) + 3)
+    (q, k, v, g), state, n, df = c.inputs64()
+    u, do = mixer_ref.HALF_STEP[dtype], f64(c.do)
+    o, _ = c.forward()
+    ro, _, ao, _ = mixer_ref.recurrence(q, k, v, g, c.scale, state, n)
+    plain = c.plan.forward(c.q, c.k, c.v, c.g, scale=c.scale, state=c.state)[0]
+    assert torch.equal(plain, o)
+    close(o, ro, u * np.abs(ro) + SMALL * ao, "o")
+    grads = c.backward()
+    ref = mixer_ref.recurrence_grad(do, q, k, v, g, c.scale, state, n, df)
+    size = mixer_ref.recurrence_grad(*(np.abs(x) for x in (do, q, k, v)), g, c.scale, np.abs(state), n, np.abs(df))
+    for got, r, a, what in zip(grads[:3], ref, size, ("dq", "dk", "dv")):
+        close(got, r, u * np.abs(r) + SMALL * a, what)
+
+
 def test_large_values_and_scale():
     """States far from 1 (binary16: up to 2^26) and a negative scale."""
     for dtype in ("f32", "bf16", "f16"):
