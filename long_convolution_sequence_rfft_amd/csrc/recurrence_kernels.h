@@ -37,8 +37,15 @@ __device__ __forceinline__ const T* row_base(const RView& v, int64_t b, int64_t 
 
 template <typename T> using DecaysOf = Decays<kRecChunk<T>, Mx<T>::kTerms == 2>;
 
-// Waves per SIMD that the registers leave room for: with 64 x 64 states three.
+// Waves per SIMD that the registers leave room for: with 64 x 64 states three,
+// with 128 x 128 ones and binary16's second accumulators one (with two, 88
+// spilled registers: 8192 tokens of 8 heads forward 91 us, backward 217, with one
+// 87 and 197; 128 x 64 with two 42 and 112, with one 57 and 113).
 constexpr int rec_waves(int d0, int d1, bool light) { return d0 * d1 <= 64 * 64 && light ? 3 : 2; }
+template <typename T> constexpr int rec_out_waves(int d0, int d1, bool trans)
+{
+    return Mx<T>::kTerms == 2 && d0 * d1 == 128 * 128 ? 1 : rec_waves(d0, d1, !trans && sizeof(T) == 2);
+}
 
 // Wide states: nothing moves across, so that the operands of one part of a
 // chunk's work are not all fetched during the one before (which spilled).
@@ -171,11 +178,11 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
 template <typename T, bool FINE> constexpr int kScoreTerms = FINE && sizeof(T) == 2 ? 2 : 1;
 
 // LDS of the two kernels below.
-template <typename T, int DA, int DC, bool TRANS, bool FINE> constexpr size_t rec_out_lds()
+template <typename T, int DA, int DC, bool FINE> constexpr size_t rec_out_lds()
 {
     constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
     return sizeof(T) * (size_t)(C * LA + C * LB + 2 * DM * C + kScoreTerms<T, FINE> * C * LC) +
-           kDecayBatch * sizeof(DecaysOf<T>) + (TRANS ? 4 * C * sizeof(float) : 0);
+           kDecayBatch * sizeof(Decays<C, false>);
 }
 
 // Chunks whose terms of dg are held before they are summed up.
@@ -208,7 +215,7 @@ template <typename T, int D, bool FINE> constexpr size_t rec_grad_lds()
 // by the instructions of a chunk, with two or three waves per SIMD.
 // ---------------------------------------------------------------------------
 template <typename T, int DA, int DC, bool TRANS, bool EXACT, bool VEC, bool FINE>
-__global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) void hyena_rec_out(RecArgs p)
+__global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_rec_out(RecArgs p)
 {
     constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
     constexpr int NT = EXACT || Mx<T>::kTerms < 2 ? Mx<T>::kTerms : 2;  // state update
@@ -217,15 +224,17 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
     constexpr int AT = DA / 16, CW = DC / 64, IT = C / 16;
     using frag = typename Mx<T>::frag;
     using vec4 = typename Mx<T>::vec4;
-    __shared__ __attribute__((aligned(16))) char smem[rec_out_lds<T, DA, DC, TRANS, FINE>()];
+    __shared__ __attribute__((aligned(16))) char smem[rec_out_lds<T, DA, DC, FINE>()];
     T* ar = (T*)smem;              // [C][LA]
     T* br = ar + C * LA;           // [C][LB]
     T* bt = br + C * LB;           // [DM][C] transposed
     T* ct = bt + DM * C;           // [DM][C] transposed
     T* ps = ct + DM * C;           // [C][LC]
-    char* tail = (char*)(ps + NP * C * LC);
-    DecaysOf<T>* const decays = (DecaysOf<T>*)tail;
-    float* part = (float*)(tail + kDecayBatch * sizeof(DecaysOf<T>));  // [4][C], TRANS
+    Decays<C, false>* const decays = (Decays<C, false>*)(ps + NP * C * LC);
+    // [4][C], TRANS: over the first rows of b, read for the last time when it is
+    // written; the wave that reads it is the one that stores those rows again
+    float* part = (float*)br;
+    static_assert(4 * C * sizeof(float) <= 4 * 64 * (16 / sizeof(T)) / DM * LB * sizeof(T), "within wave 0's first rows");
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -289,8 +298,8 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
     }
     for (int c = 0; c < nchunk; ++c) {
         const int slot = c % kDecayBatch;
-        if (slot == 0 && wave < kDecayBatch) fill_decays<C, Mx<T>::kTerms == 2>(decays[wave], g, lane);
-        const DecaysOf<T>& dec = decays[slot];
+        if (slot == 0 && wave < kDecayBatch) fill_decays<C, false>(decays[wave], g, lane);
+        const Decays<C, false>& dec = decays[slot];
         ta.template store_rows<LA>(ar, tid);
         if (is_b) tile.template store_rows<LB>(br, half);
         tile.store_cols(is_b ? bt : ct, half);
@@ -410,6 +419,7 @@ __global__ __launch_bounds__(256, rec_waves(DA, DC, !TRANS && sizeof(T) == 2)) v
         if constexpr (TRANS) {
             if (tid < C && tb0 + tid < t1)
                 p.rq[bh * p.N + tb0 + tid] = (part[tid] + part[C + tid]) + (part[2 * C + tid] + part[3 * C + tid]);
+            asm volatile("" ::: "memory");  // before this wave's next rows of b are stored there
         }
     }
     // rows of a padded batch past the length
