@@ -315,7 +315,7 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  *   S_t = exp(g_t) S_{t-1} + k_t v_t^T        (dk x dv, float32)
  *   o_t = scale * S_t^T q_t                   t = 1..length, S_0 = state or 0
  *
- * g_t is one log decay per token and head.  g_t = -infinity starts a new
+ * g_t <= 0 is one log decay per token and head.  g_t = -infinity starts a new
  * sequence inside a row (nothing before it is seen), and so does any g_t below
  * -87.34 (its exp is below the smallest normal float32).
  *

@@ -677,7 +677,7 @@ class Recurrence(_Mixer):
     for rows of N tokens (see include/hyena.h for shapes, masks and precision).
 
     q, k: [B, N, heads, dk], v: [B, N, heads, dv] in the io dtype, g: float32
-    [B, N, heads] (log decays); views are taken as they are as long as the last
+    [B, N, heads] (log decays, at most 0); views are taken as they are as long as the last
     axis of q, k and v is contiguous.  States are float32 [B, heads, dk, dv].
     ``training`` allocates the backward pass's workspace.  Calls of one plan
     share its workspace and must not run concurrently on different streams.
