@@ -22,6 +22,18 @@ def test_many_rows_and_heads(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", [(1, 1500, 2, 64, 64), (12, 1100, 5, 16, 24), (7, 700, 9, 72, 40)])
+def test_many_segments(shape, dtype):
+    """Sequences cut into several segments, the backward's states (second shape) into finer ones than its
+    gradients, with documents packed into the rows and rows that end inside a segment."""
+    B, N = shape[:2]
+    lengths = None if B == 1 else tuple((0, 1, N // 2, N - 1, N, N - 64, 65)[i % 7] for i in range(B))
+    c = Case(*shape, dtype, seed=sum(shape), lengths=lengths, resets=((129, -np.inf), (N // 2 - 7, -np.inf)), decay=0.05)
+    check_forward(c)
+    check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_aligned_slices_of_one_projection(dtype):
     """16-byte vectors in rows that are not dense."""
     c = Case(2, 330, 3, 64, 64, dtype, seed=6)
