@@ -19,7 +19,9 @@
 // rotation (in the half layout the vectors are rotary_dim / 2 apart, else side
 // by side) or 2 W channels that are not rotated.  A lane holds U units, a power
 // of two of lanes one head, so a pair is always within a lane and the norm's
-// sum is a few steps across lanes.
+// sum is a few steps across lanes.  W is as wide as the widths and strides allow
+// (2 x 8192 tokens, 12 + 12 heads of 100 in bf16: 93 us forward with W = 1, 56
+// with 2, where heads of 128 take 38 with 8).
 //
 // Tiles of 48 KB: the backward pass at 16384 tokens of 12 + 4 heads of 64 in
 // bf16 takes 26.7 us (100 MB, 4.4 TB/s less 4 us of launch), with 32 KB 31,
@@ -46,7 +48,8 @@ constexpr int kQkTile = 48 << 10;  // bytes of a tensor that a tile is meant to 
 constexpr int kQkAngles = 2048;    // most (token, frequency) pairs of a tile: 16 KB of LDS
 constexpr int kQkTiles = 256;      // fewest tiles of a tensor, if it has that many tokens
 constexpr int kQkGroups = 1 << 16; // most workgroups of a tensor, forward: the rest of the tiles is looped over
-constexpr int kQkGradGroups = 1024; // backward: rows of the partial sums
+constexpr int kQkGradGroups = 1024;    // backward: what runs at once, the most rows of the partial sums
+constexpr int kQkGradGroupsWide = 768; // the same where a lane holds 16 channels (W = 8)
 
 struct QkTensor {
     RView x, dy;
@@ -91,6 +94,17 @@ template <typename T, int W> struct QkRaw {
         }
     }
 };
+template <typename T> struct QkRaw<T, 2> {
+    typedef T pair __attribute__((ext_vector_type(2)));
+    pair v;
+    __device__ __forceinline__ void load(const T* p) { v = *(const pair*)p; }
+    __device__ __forceinline__ void widen(float (&x)[2]) const
+    {
+        const T a = v[0], b = v[1];
+        x[0] = load_one<T>(&a);
+        x[1] = load_one<T>(&b);
+    }
+};
 template <typename T> struct QkRaw<T, 1> {
     T v;
     __device__ __forceinline__ void load(const T* p) { v = *p; }
@@ -102,6 +116,11 @@ __device__ __forceinline__ void qk_store(T* p, const float (&x)[W])
 {
     if constexpr (W == 1) {
         store_one<T>(p, x[0]);
+    } else if constexpr (W == 2) {
+        T a, b;
+        store_one<T>(&a, x[0]);
+        store_one<T>(&b, x[1]);
+        *(typename QkRaw<T, 2>::pair*)p = typename QkRaw<T, 2>::pair{a, b};
     } else {
         typename Mx<T>::vec4 v[W / 4];
 #pragma unroll
@@ -377,7 +396,7 @@ bool all_zero_mod(const RView& v, size_t element, int w)
 // channels, the rotated part in units of 2 W.
 int vector_width(const QkArgs& a, size_t element, bool grad)
 {
-    for (int w = element == 2 ? 8 : 4; w >= 4; w /= 2) {
+    for (int w = element == 2 ? 8 : 4; w >= 2; w /= 2) {
         bool ok = a.D % w == 0 && a.rotary % (2 * w) == 0;
         for (int k = 0; k < 2 && ok; ++k)
             ok = all_zero_mod(a.t[k].x, element, w) && (!grad || all_zero_mod(a.t[k].dy, element, w)) &&
@@ -387,22 +406,39 @@ int vector_width(const QkArgs& a, size_t element, bool grad)
     return 1;
 }
 
-// The tensors' tiles and workgroups: kQkTile channels each, or fewer so that
-// there are kQkTiles of them.
+// The tensors' tiles and workgroups.  Tiles of kQkTile bytes, or less so that
+// there are kQkTiles of them, and a workgroup for each.  Backward, where a
+// workgroup keeps sums for the weights, no more workgroups than run at once: if
+// there are more tiles, they are shared out by heads, and the tiles made smaller
+// so that each workgroup of a tensor has as many (2 x 8192 tokens, 12 + 12 heads
+// of 64, 128 and 256 in bf16, a workgroup per tile up to 1024 of them: 41, 106
+// and 171 us, so: 40, 92 and 141).
 void shape_tiles(QkArgs& a, size_t element, bool grad)
 {
     const int64_t nf = a.rotary / 2 > 0 ? a.rotary / 2 : 1, heads = a.t[0].heads + a.t[1].heads;
-    for (QkTensor& q : a.t) {
-        int64_t t = kQkTile / ((int64_t)q.heads * a.D * (int64_t)element);
-        if (t > a.rows / kQkTiles) t = a.rows / kQkTiles;
+    const bool wide = element == 2 && a.D % 8 == 0 && a.rotary % 16 == 0;
+    const int64_t resident = wide ? kQkGradGroupsWide : kQkGradGroups;
+    int64_t most[2], total = 0;
+    for (int k = 0; k < 2; ++k) {
+        int64_t t = kQkTile / ((int64_t)a.t[k].heads * a.D * (int64_t)element);
         if (t > kQkTokens) t = kQkTokens;
         if (t > kQkAngles / nf) t = kQkAngles / nf;
-        if (t < 1) t = 1;
+        if (t > a.rows / kQkTiles) t = a.rows / kQkTiles;
+        most[k] = t < 1 ? 1 : t;
+        total += (a.rows + most[k] - 1) / most[k];
+    }
+    for (int k = 0; k < 2; ++k) {
+        QkTensor& q = a.t[k];
+        int64_t t = most[k], groups = kQkGroups;
+        if (grad && total > resident) {
+            groups = resident * (int64_t)q.heads / heads;
+            if (groups < 1) groups = 1;
+            const int64_t each = (a.rows + groups * t - 1) / (groups * t);
+            t = (a.rows + groups * each - 1) / (groups * each);
+        }
         q.tokens = (int32_t)t;
         q.tiles = (a.rows + t - 1) / t;
-        int64_t most = grad ? kQkGradGroups * (int64_t)q.heads / heads : kQkGroups;
-        if (most < 1) most = 1;
-        q.groups = (int32_t)(q.tiles < most ? q.tiles : most);
+        q.groups = (int32_t)(q.tiles < groups ? q.tiles : groups);
     }
 }
 
@@ -425,7 +461,8 @@ template <typename T, int W, bool GRAD> hyena_status qk_launch_w(QkArgs& a, hipS
     const int per = (units + lanes - 1) / lanes;
     if (per <= 1) return qk_launch_one<T, W, 1, GRAD>(a, s);
     if (per <= 2) return qk_launch_one<T, W, 2, GRAD>(a, s);
-    if constexpr (W == 1) return qk_launch_one<T, W, 8, GRAD>(a, s);
+    if constexpr (W == 2) return qk_launch_one<T, W, 4, GRAD>(a, s);
+    else if constexpr (W == 1) return qk_launch_one<T, W, 8, GRAD>(a, s);
     else return fail(HYENA_ERR_UNSUPPORTED, "qk norm: head width");
 }
 
@@ -435,6 +472,7 @@ template <typename T, bool GRAD> hyena_status qk_launch(QkArgs& a, hipStream_t s
     if constexpr (sizeof(T) == 2)
         if (w == 8) return qk_launch_w<T, 8, GRAD>(a, s);
     if (w == 4) return qk_launch_w<T, 4, GRAD>(a, s);
+    if (w == 2) return qk_launch_w<T, 2, GRAD>(a, s);
     return qk_launch_w<T, 1, GRAD>(a, s);
 }
 

@@ -29,6 +29,8 @@ CASES = [
     (1, 3, 1, 1, 1000, 10, "rms", "interleaved"), (1, 2, 1, 1, 1023, 1022, "l2", "half"), (1, 4, 2, 1, 1, 0, "rms", "half"),
     (3, 50, 2, 2, 24, 0, "rms", "half"), (1, 40, 5, 5, 16, 16, "none", "interleaved"),
     (1, 2500, 4, 1, 64, 64, "rms", "half"),
+    (2, 7, 3, 2, 100, 100, "rms", "half"), (1, 5, 2, 2, 66, 64, "l2", "interleaved"), (1, 3, 1, 1, 1022, 1020, "rms", "half"),
+    (1, 3, 2, 1, 514, 4, "rms", "interleaved"), (4, 2000, 4, 4, 128, 128, "rms", "half"),
 ]
 
 
