@@ -191,9 +191,9 @@ hyena_status run_backward(const RecPlan& p, const hyena_recurrence_inputs& in, c
     const RecSpace w = rec_space(p, true, workspace);
     const int64_t bh = p.B * p.heads;
     const size_t e = sizeof(T);
-    // one segment and nothing coming from the end or asked for at the start: no
-    // state is needed before the main passes
-    const bool states = p.nseg_b > 1 || d_final != nullptr || out.d_state != nullptr;
+    // one segment, dq's (nseg_b * every) included, and nothing coming from the end
+    // or asked for at the start: no state is needed before the main passes
+    const bool states = p.nseg_b * p.every > 1 || d_final != nullptr || out.d_state != nullptr;
     if (states) {
         const hyena_status st =
             rec_states<T>(p, in, &d_o, d_final, nullptr, out.d_state, w, p.nseg_b * p.every, s);
