@@ -336,9 +336,10 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  * bfloat16, 2^-11 for binary16 scores, or 2^-25 absolutely where they are
  * subnormal), but in calls of few tokens (N <= 64 and B * heads <= 256) neither
  * is; the states, their gradients and the gradient of g are computed from
- * operands split so that they keep float32 accuracy.  With binary16 the
- * scores (times decay and scale) have to stay within its range, and the states
- * and their gradients below 2^26.  Inputs within a row's length have to be
+ * operands split so that they keep float32 accuracy (binary16: in each column,
+ * or row, of a state relative to its largest element, 2^-36 of it at least).
+ * With binary16 the scores (times decay and scale) have to stay within its
+ * range.  Inputs within a row's length have to be
  * finite (g may be -infinity): an infinity or a NaN reaches its own and later
  * tokens' results, and may reach those of up to 63 tokens before it.
  *

@@ -35,7 +35,7 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 //
 // kTerms / split: how many fragments of T carry a float32 operand to float32
 // accuracy: 8 bits each for bfloat16 (three), 11 for binary16 (two, the second
-// scaled by 2^11 so that it stays above the subnormals).
+// scaled by 2^11 so that it stays above the subnormals; see Fit for its range).
 template <typename T> struct Mx;
 
 template <> struct Mx<float> {
@@ -146,16 +146,68 @@ __device__ __forceinline__ f32x4 mma_split(const Split<T, NT>& s, typename Mx<T>
     }
 }
 
-// s * all + x y^T summed over NB blocks; y is split and, for binary16, without
-// the common factor `lead` of its decays, which may be far below its range.
-template <typename T, int NT, int NB, typename F>
-__device__ __forceinline__ f32x4 update(f32x4 s, float all, float lead, const Split<T, NT> (&y)[NB], F x)
+// binary16 holds 2^-24 .. 65504 only, 11 bits from 2^-14 on.  The columns of a
+// float32 operand are brought there by a power of two each, made of the column's
+// largest magnitude, and their results taken back: what is lost is below 2^-36 of
+// that, wherever a state or a decay is.  down leaves the largest in 2^14 .. 2^15;
+// up = 1 / down.  Nothing for the other types, whose exponents are float32's.
+struct Fit {
+    float down, up;
+    __device__ __forceinline__ explicit Fit(float largest)
+    {
+        uint32_t e = __float_as_uint(largest) >> 23;
+        e = e < 15 ? 15 : e;  // up is normal
+        down = __uint_as_float((268 - e) << 23);
+        up = __uint_as_float((e - 14) << 23);
+    }
+};
+template <typename T> constexpr bool kFit = Mx<T>::kTerms == 2;
+
+// Largest over the four lanes l, l ^ 16, l ^ 32, l ^ 48, in each of them: the rows
+// of a fragment's column are in these lanes.
+__device__ __forceinline__ float max_rows(float x)
 {
-    if constexpr (Mx<T>::kTerms == 2) {
+    typedef uint32_t u32x2_ __attribute__((ext_vector_type(2)));
+    u32x2_ s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+
+// NB fragments of one operand, value(j) the j-th in float32, split; returns what
+// the results of their columns (a lane's own) are to be multiplied by.
+template <typename T, int NT, int NB, typename F>
+__device__ __forceinline__ float split_columns(Split<T, NT> (&y)[NB], F value)
+{
+    if constexpr (kFit<T>) {
+        f32x8 x[NB];
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            x[j] = value(j);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[j][e]));
+        }
+        const Fit fit(max_rows(m));
+#pragma unroll
+        for (int j = 0; j < NB; ++j) y[j].set(x[j] * fit.down);
+        return fit.up;
+    } else {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) y[j].set(value(j));
+        return 1.0f;
+    }
+}
+
+// s * all + x y^T summed over NB blocks; up: of split_columns.
+template <typename T, int NT, int NB, typename F>
+__device__ __forceinline__ f32x4 update(f32x4 s, float all, float up, const Split<T, NT> (&y)[NB], F x)
+{
+    if constexpr (kFit<T>) {
         f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NB; ++j) t = mma_split<T, NT, false>(y[j], x(j), t);
-        return s * all + t * lead;
+        return s * all + t * up;
     } else {
         s = s * all;
 #pragma unroll
@@ -164,10 +216,37 @@ __device__ __forceinline__ f32x4 update(f32x4 s, float all, float lead, const Sp
     }
 }
 
-// binary16 holds a state of up to 65504 only: as an operand it is scaled by
-// 2^-10 (and always split in two, so that small states lose nothing).
-template <typename T> struct StateScale { static constexpr float down = 1.0f, up = 1.0f; };
-template <> struct StateScale<_Float16> { static constexpr float down = 0.0009765625f, up = 1024.0f; };
+// A tile column of a state as an operand: M 16 x 16 tiles of registers, tile(m) the
+// m-th.  down: for its operands; up: for results whose rows are its columns.
+template <typename T> struct StateFit {
+    float down = 1.0f;
+    f32x4 up = {1.0f, 1.0f, 1.0f, 1.0f};
+    template <int M, typename F> __device__ __forceinline__ void set(F tile, int grp)
+    {
+        if constexpr (kFit<T>) {
+            float m = 0.0f;
+#pragma unroll
+            for (int x = 0; x < M; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(tile(x)[r]));
+            const Fit fit(max_rows(m));
+            down = fit.down;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) up[r] = __shfl(fit.up, 4 * grp + r);
+        }
+    }
+    __device__ __forceinline__ f32x8 fitted(f32x8 x) const
+    {
+        if constexpr (kFit<T>) return x * down;
+        else return x;
+    }
+    // a tile of results times f
+    __device__ __forceinline__ f32x4 results(f32x4 x, float f) const
+    {
+        if constexpr (kFit<T>) return x * (up * f);
+        else return x * f;
+    }
+};
 
 __device__ __forceinline__ f32x8 join8(f32x4 a, f32x4 b)
 {
@@ -505,14 +584,12 @@ __device__ __forceinline__ typename Mx<T>::frag frag_at(const T* lds)
 // that differences of up to 64 terms keep float32 accuracy.  A reset's own log
 // counts as 0; count is the number of resets so far, and a factor that spans one
 // is 0.  head: from the chunk's start through each token; tail: from after each
-// token to the chunk's end; inner: from after the chunk's first token through
-// each, head[i] = head[0] inner[i] (binary16 only).
-template <int C, bool INNER> struct alignas(16) Decays {
+// token to the chunk's end.
+template <int C> struct alignas(16) Decays {
     double logs[C];
     int count[C];
     float head[C], tail[C], within[C];
     float cross[C / 16 - 1][C];
-    float inner[INNER ? C : 4];
     unsigned long long resets;  // bit per token
 };
 
@@ -568,8 +645,8 @@ __device__ __forceinline__ float sum_rows(float x)
 
 // One wave fills the decays of a chunk from its log decay per lane (lane =
 // token, 0 where the token does not exist).
-template <int C, bool INNER>
-__device__ __forceinline__ void fill_decays(Decays<C, INNER>& d, float g, int lane)
+template <int C>
+__device__ __forceinline__ void fill_decays(Decays<C>& d, float g, int lane)
 {
     const bool reset = g * 1.44269504088896340736f < kResetLog2;
     const unsigned long long resets = __ballot(reset && lane < C);
@@ -594,7 +671,6 @@ __device__ __forceinline__ void fill_decays(Decays<C, INNER>& d, float g, int la
         d.head[lane] = factor(count == 0, s);
         d.tail[lane] = factor(count == upto(C - 1), edge[C / 16 - 1] - s);
         d.within[lane] = factor(count == count_before, s - before);
-        if constexpr (INNER) d.inner[lane] = factor(count == upto(0), s - lane_f64(s, 0));
 #pragma unroll
         for (int i = 1; i < C / 16; ++i)
             d.cross[i - 1][lane] = factor(lane < 16 * i && count == upto(16 * i - 1), edge[i - 1] - s);

@@ -35,7 +35,7 @@ __device__ __forceinline__ const T* row_base(const RView& v, int64_t b, int64_t 
     return (const T*)v.p + b * v.b + h * v.h;
 }
 
-template <typename T> using DecaysOf = Decays<kRecChunk<T>, Mx<T>::kTerms == 2>;
+template <typename T> using DecaysOf = Decays<kRecChunk<T>>;
 
 // Waves per SIMD that the registers leave room for: with 64 x 64 states three,
 // with 128 x 128 ones and binary16's second accumulators one (with two, 88
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
     }
     for (int c = 0; c < nchunk; ++c) {
         const int slot = c % kDecayBatch;
-        if (slot == 0 && wave < kDecayBatch) fill_decays<C, Mx<T>::kTerms == 2>(decays[wave], g, lane);
+        if (slot == 0 && wave < kDecayBatch) fill_decays<C>(decays[wave], g, lane);
         const DecaysOf<T>& dec = decays[slot];
         tile.store_cols(is_x ? xt : yt, half);
         __syncthreads();
@@ -135,23 +135,20 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
             if (slot == 0) fetch_g(c + kDecayBatch + wave);
         }
         const float all = dec.head[C - 1];
-        constexpr bool kLead = Mx<T>::kTerms == 2;
-        const float* f = role ? (kLead ? dec.inner : dec.head) : dec.tail;
-        const float lead = kLead && role ? dec.head[0] : 1.0f;
+        const float* f = role ? dec.head : dec.tail;
         total *= all;
 #pragma unroll
         for (int v = 0; v < VW; ++v) {
             const int vt = wave + 4 * v;
             Split<T, NT> y[C / 32];
-#pragma unroll
-            for (int j = 0; j < C / 32; ++j) {
+            const float up = split_columns<T>(y, [&](int j) {
                 const f32x8 w = join8(*(const f32x4*)(f + 32 * j + 8 * grp),
                                       *(const f32x4*)(f + 32 * j + 8 * grp + 4));
-                y[j].set(Mx<T>::widen8(cols_of.any(yt, vt, j)) * w);
-            }
+                return Mx<T>::widen8(cols_of.any(yt, vt, j)) * w;
+            });
 #pragma unroll
             for (int k = 0; k < KT; ++k)
-                S[k][v] = update<T>(S[k][v], all, lead, y,
+                S[k][v] = update<T>(S[k][v], all, up, y,
                                     [&](int j) { return cols_of(xt, k, j); });
         }
         __syncthreads();
@@ -182,7 +179,7 @@ template <typename T, int DA, int DC, bool FINE> constexpr size_t rec_out_lds()
 {
     constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
     return sizeof(T) * (size_t)(C * LA + C * LB + 2 * DM * C + kScoreTerms<T, FINE> * C * LC) +
-           kDecayBatch * sizeof(Decays<C, false>);
+           kDecayBatch * sizeof(DecaysOf<T>);
 }
 
 // Chunks whose terms of dg are held before they are summed up.
@@ -230,7 +227,7 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
     T* bt = br + C * LB;           // [DM][C] transposed
     T* ct = bt + DM * C;           // [DM][C] transposed
     T* ps = ct + DM * C;           // [C][LC]
-    Decays<C, false>* const decays = (Decays<C, false>*)(ps + NP * C * LC);
+    DecaysOf<T>* const decays = (DecaysOf<T>*)(ps + NP * C * LC);
     // [4][C], TRANS: over the first rows of b, read for the last time when it is
     // written; the wave that reads it is the one that stores those rows again
     float* part = (float*)br;
@@ -298,8 +295,8 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
     }
     for (int c = 0; c < nchunk; ++c) {
         const int slot = c % kDecayBatch;
-        if (slot == 0 && wave < kDecayBatch) fill_decays<C, false>(decays[wave], g, lane);
-        const Decays<C, false>& dec = decays[slot];
+        if (slot == 0 && wave < kDecayBatch) fill_decays<C>(decays[wave], g, lane);
+        const DecaysOf<T>& dec = decays[slot];
         ta.template store_rows<LA>(ar, tid);
         if (is_b) tile.template store_rows<LB>(br, half);
         tile.store_cols(is_b ? bt : ct, half);
@@ -374,10 +371,12 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
             const uint32_t orow = (uint32_t)again(l16) * ostep;
             // outputs: column = token, rows = 4 channels
             f32x4 so[IT] = {};
+            StateFit<T> fit;
+            fit.template set<AT>([&](int k) { return S[k][v]; }, grp);
 #pragma unroll
             for (int k = 0; k < DA / 32; ++k) {
                 Split<T, NS> sf;
-                sf.set(join8(S[2 * k][v], S[2 * k + 1][v]) * StateScale<T>::down);
+                sf.set(fit.fitted(join8(S[2 * k][v], S[2 * k + 1][v])));
 #pragma unroll
                 for (int i = 0; i < IT; ++i)
                     so[i] = mma_split<T, NS, true>(sf, frag_at<T>(ar + (16 * i + l16) * LA + 32 * k + 8 * grp), so[i]);
@@ -385,7 +384,7 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int ti = 16 * i + l16;
-                f32x4 o = so[i] * (p.scale * StateScale<T>::up * dec.head[ti]);
+                f32x4 o = fit.results(so[i], p.scale * dec.head[ti]);
                 if constexpr (TRANS) {
                     const f32x4 r = Mx<T>::widen(under.x[i][v]);
                     rdot[i] += o[0] * r[0] + o[1] * r[1] + o[2] * r[2] + o[3] * r[3];
@@ -402,15 +401,14 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
             // the state after this chunk
             hold_schedule<(DA * DC > 64 * 64)>();
             Split<T, NT> y[C / 32];
-#pragma unroll
-            for (int j = 0; j < C / 32; ++j) {
+            const float up = split_columns<T>(y, [&](int j) {
                 const f32x8 w = join8(*(const f32x4*)(dec.tail + 32 * j + 8 * grp),
                                       *(const f32x4*)(dec.tail + 32 * j + 8 * grp + 4));
-                y[j].set(Mx<T>::widen8(cf[j]) * w);
-            }
+                return Mx<T>::widen8(cf[j]) * w;
+            });
 #pragma unroll
             for (int k = 0; k < AT; ++k)
-                S[k][v] = update<T>(S[k][v], all, 1.0f, y,
+                S[k][v] = update<T>(S[k][v], all, up, y,
                                     [&](int j) { return cols_of(bt, k, j); });
             hold_schedule<(DA * DC > 64 * 64)>();
         }
@@ -568,7 +566,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     for (int c = 0; c < nchunk; ++c) {
         const int slot = c % kDecayBatch;
         if (slot == 0 && !is_x) {
-            if (own_k) fill_decays<C, Mx<T>::kTerms == 2>(decays[w4 - 2], g, lane);
+            if (own_k) fill_decays<C>(decays[w4 - 2], g, lane);
             else if (lane < C) rqs[(w4 - 2) * C + lane] = g;
         }
         const DecaysOf<T>& dec = decays[slot];
@@ -703,10 +701,12 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 #pragma unroll
                 for (int i = 0; i < C / 32; ++i) ff[i] = cols_of.any(fold, nt, i);
                 f32x4 sx[IT] = {};
+                StateFit<T> fit;
+                fit.template set<MT>([&](int m) { return S[m * MW + n]; }, grp);
 #pragma unroll
                 for (int k = 0; k < kAcross / 32; ++k) {
                     Split<T, NS> sf;
-                    sf.set(join8(S[2 * k * MW + n], S[(2 * k + 1) * MW + n]) * StateScale<T>::down);
+                    sf.set(fit.fitted(join8(S[2 * k * MW + n], S[(2 * k + 1) * MW + n])));
 #pragma unroll
                     for (int j = 0; j < IT; ++j)
                         sx[j] = mma_split<T, NS, true>(sf, frag_at<T>(across + (16 * j + l16) * LD + 32 * k + 8 * grp), sx[j]);
@@ -714,7 +714,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 #pragma unroll
                 for (int j = 0; j < IT; ++j) {
                     const int tj = 16 * j + l16;
-                    f32x4 x = sx[j] * (StateScale<T>::up * dec.tail[tj]);
+                    f32x4 x = fit.results(sx[j], dec.tail[tj]);
                     if constexpr (kSums) {
                         const f32x4 kk = Mx<T>::widen(*(const vec4*)(kr + tj * LD + perm4(4 * nt + grp)));
                         kdot[j] += x[0] * kk[0] + x[1] * kk[1] + x[2] * kk[2] + x[3] * kk[3];
@@ -729,18 +729,14 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                     store_row4<T>(orows, orow + 16 * j * ostep, tj < left, 16 * nt + 4 * grp, width, x);
                 }
                 hold_schedule<(DK * DV > 64 * 64)>();
-                constexpr bool kLead = Mx<T>::kTerms == 2;
-                const float* f = kLead ? dec.inner : dec.head;
-                const float lead = kLead ? p.scale * dec.head[0] : 1.0f;
                 Split<T, NU> y[C / 32];
-#pragma unroll
-                for (int i = 0; i < C / 32; ++i) {
-                    const f32x8 w = join8(*(const f32x4*)(f + 32 * i + 8 * grp), *(const f32x4*)(f + 32 * i + 8 * grp + 4));
-                    y[i].set(Mx<T>::widen8(ff[i]) * (kLead ? w : w * p.scale));
-                }
+                const float up = split_columns<T>(y, [&](int i) {
+                    const f32x8 w = join8(*(const f32x4*)(dec.head + 32 * i + 8 * grp), *(const f32x4*)(dec.head + 32 * i + 8 * grp + 4));
+                    return Mx<T>::widen8(ff[i]) * (w * p.scale);
+                });
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    S[m * MW + n] = update<T>(S[m * MW + n], all, lead, y, [&](int i) { return cols_of(add, m, i); });
+                    S[m * MW + n] = update<T>(S[m * MW + n], all, up, y, [&](int i) { return cols_of(add, m, i); });
                 hold_schedule<(DK * DV > 64 * 64)>();
             }
             if constexpr (kSums) store_token_sums<IT>(part + w4 * C, kdot, lane, grp);

@@ -45,3 +45,97 @@ def test_a_state_whose_gradient_is_not_asked_for(shape, dtype):
     torch.cuda.synchronize()
     assert st == hyena.HYENA_OK
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------- the gradient of g
+#
+# dg_t is summed from q_s . dq_s - k_s . dk_s over the tokens s from t to the end of its sequence, a
+# token's own pair left out of both.  With W_s = exp(g_s) <|S_{s-1}|, |dS_s|>, dg's own terms without
+# their signs, the two products of token s are at most W_s and W_{s+1} in size, and what leaves the row
+# with d_final is W of one token more.  Each is good to SMALL of its size, so dg_t to
+#   SMALL (2 sum_{s >= t, same sequence} W_s + <|S_N|, |d_final|> in the last sequence).
+
+def dg_bound(c):
+    (q, k, v, g), state, n, df = c.inputs64()
+    n = np.full(c.B, c.N) if n is None else np.clip(n, 0, c.N)
+    ab = [np.abs(x) for x in (f64(c.do), q, k, v)]
+    state = None if state is None else np.abs(state)
+    W = mixer_ref.recurrence_grad(*ab, g, abs(c.scale), state, n, None if df is None else np.abs(df))[3]
+    bound = np.zeros_like(W)
+    if df is not None:
+        leaves = (np.abs(mixer_ref.recurrence(*ab[1:], g, 1.0, state, n)[1]) * np.abs(df)).sum((-1, -2))
+    for b in range(c.B):
+        over = np.zeros(c.H) if df is None else leaves[b]
+        for t in range(int(n[b]) - 1, -1, -1):
+            over = over + 2 * W[b, t]
+            bound[b, t] = over
+            over = np.where(g[b, t] * np.log2(np.e) < -126, 0.0, over)
+    return SMALL * bound
+
+
+# ------------------------------------------------------------- magnitudes
+
+@pytest.mark.parametrize("N", [50, 200])
+@pytest.mark.parametrize("size", [2.0 ** -20, 2.0 ** -30, 2.0 ** 20])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_states_and_their_gradients_far_from_one(size, N, dtype):
+    """Everything comes from the initial state (v = 0) and from d_final (do = 0), so that no score
+    takes part; other operands around 64, so that 16-bit results are in their range.  One column of the
+    state is 2^10 times the others."""
+    import torch
+    c = Case(2, N, 2, 24, 40, dtype, seed=9, decay=0.02)
+    for t, by in ((c.state, size), (c.d_final, size), (c.v, 0.0), (c.do, 0.0)):
+        t.mul_(by)
+    c.state[..., 5] *= 1024.0
+    c.d_final[..., 7] *= 1024.0
+    for t in (c.q, c.k):
+        t.mul_(64.0)
+    if dtype == "f16" and size > 1:
+        # o is q (64) times the largest column (2^30) summed over 24 channels, about 2^38: below 65504
+        c.scale = 2.0 ** -30
+    (q, k, v, g), state, n, df = c.inputs64()
+    u = mixer_ref.HALF_STEP[dtype]
+    least = 2.0 ** -25 if dtype == "f16" else 0.0  # half a step of the smallest float16 results
+    o, last = c.forward()
+    ro, rs, ao, as_ = mixer_ref.recurrence(q, k, v, g, c.scale, state, n)
+    # bfloat16 reads the state rounded once
+    held = u if dtype == "bf16" and N > 64 else 0.0
+    close(o, ro, u * np.abs(ro) + (held + SMALL) * ao + least, "o")
+    close(last, rs, SMALL * as_ + 1e-30, "state")
+    if dtype == "f16" and size > 1:
+        return  # gradients above float16's largest
+    # dk is dS v: values for it alone
+    c.v.copy_(64.0 * torch.randn(c.v.shape, generator=torch.Generator().manual_seed(10)))
+    c.state.zero_()
+    (q, k, v, g), state, n, df = c.inputs64()
+    dq, dk, dv, dg, ds = c.backward()
+    ref = mixer_ref.recurrence_grad(f64(c.do), q, k, v, g, c.scale, state, n, df)
+    a = mixer_ref.recurrence_grad(np.abs(f64(c.do)), *(np.abs(x) for x in (q, k, v)), g, abs(c.scale), state, n, np.abs(df))
+    assert not dq.any()
+    close(dk, ref[1], u * np.abs(ref[1]) + SMALL * a[1] + least, "dk")
+    close(dv, ref[2], u * np.abs(ref[2]) + (held + SMALL) * a[2] + least, "dv")
+    close(ds, ref[4], SMALL * a[4] + 1e-30, "d_state")
+    close(dg, ref[3], dg_bound(c), "dg")
+
+
+@pytest.mark.parametrize("N", [30, 60])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_states_that_have_decayed_far(N, dtype):
+    """One token, then nothing but decays of e^-1: down to e^-59 the state has the accuracy of its size, and
+    so has the gradient of the initial state, which comes from the last token alone."""
+    c = Case(2, N, 2, 24, 40, dtype, seed=12)
+    c.g.fill_(-1.0)
+    c.g[:, 5] = -np.inf
+    c.v[:, 1:].zero_()
+    c.v[:, 5].normal_()
+    (q, k, v, g), state, n, df = c.inputs64()
+    _, last = c.forward()
+    _, rs, _, as_ = mixer_ref.recurrence(q, k, v, g, c.scale, state, n)
+    close(last, rs, SMALL * as_, "state")
+    c.g[:, 5] = -1.0
+    c.do[:, :-1].zero_()
+    c.d_final.zero_()
+    (q, k, v, g), state, n, df = c.inputs64()
+    ds = c.backward()[4]
+    grad = lambda x, y: mixer_ref.recurrence_grad(x, y, k, v, g, c.scale, state, n, df)[4]  # noqa: E731
+    close(ds, grad(f64(c.do), q), SMALL * grad(np.abs(f64(c.do)), np.abs(q)), "d_state")
