@@ -449,9 +449,10 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
 // bring in do and v.
 //
 // dg_t = <S_end, dS_end> + sum_{s >= t} (q_s . dq_s - k_s . dk_s), s up to the
-// segment's end: both dot products are made of float32 values (scores weighted
-// by both products before any rounding, the states' parts from split operands)
-// and kept in LDS for kGradHold chunks, then summed up in float64 by all waves.
+// segment's end, without a token's own pair in either product: both are made of
+// float32 values (scores weighted by both products before any rounding, the states' parts
+// from split operands) and kept in LDS for kGradHold chunks, then summed up in
+// float64 by all waves.
 //
 // Bound by a chunk's instructions: 66 us at 2 x 8192 tokens of 12 heads of 64 in
 // bfloat16 (176 MB), 80 us at 4 x 2048 in float32; 610 vector instructions per
@@ -620,7 +621,11 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                 s[r] = tj <= ti + r ? s[r] * w[r] : 0.0f;
                 d[r] = tj <= ti + r ? d[r] : 0.0f;
             }
-            const f32x4 both = s * d;
+            // (a token's own pair has no part in the gradient of g; it would cancel in
+            // q . dq - k . dk, but only after either sum was rounded at its size)
+            f32x4 both;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) both[r] = tj < ti + r ? s[r] * d[r] : 0.0f;
             d = d * w;
             store_split<T, NP>(pa + tj * LC + ti, C * LC, s);
             store_split<T, NP>(pd + tj * LC + ti, C * LC, d);

@@ -73,6 +73,22 @@ def dg_bound(c):
     return SMALL * bound
 
 
+def check_dg(c):
+    (q, k, v, g), state, n, df = c.inputs64()
+    ref = mixer_ref.recurrence_grad(f64(c.do), q, k, v, g, c.scale, state, n, df)[3]
+    close(c.backward()[3], ref, dg_bound(c), "dg")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("carry", [False, True])
+@pytest.mark.parametrize("shape", [(2, 60, 2, 64, 64), (2, 200, 2, 64, 64), (1, 1500, 2, 16, 24), (1, 300, 200, 8, 8)])
+def test_dg_of_fast_decays(shape, carry, dtype):
+    for g in (-4.0, -12.0, -20.0):
+        c = Case(*shape, dtype, seed=17, carry=carry)
+        c.g.fill_(g)
+        check_dg(c)
+
+
 # ------------------------------------------------------------- magnitudes
 
 @pytest.mark.parametrize("N", [50, 200])
