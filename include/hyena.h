@@ -338,6 +338,10 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  * is; the states, their gradients and the gradient of g are computed from
  * operands split so that they keep float32 accuracy (binary16: in each column,
  * or row, of a state relative to its largest element, 2^-36 of it at least).
+ * The gradient of g at a token is a sum of terms of that token and the later ones
+ * of its sequence, each with the decays of g; its accuracy is that of the sum of their
+ * absolute values, so a decay much faster than all those after it has a small
+ * gradient with an error of their size.
  * With binary16 the scores (times decay and scale) have to stay within its
  * range.  Inputs within a row's length have to be
  * finite (g may be -infinity): an infinity or a NaN reaches its own and later

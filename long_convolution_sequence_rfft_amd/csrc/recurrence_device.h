@@ -615,6 +615,20 @@ __device__ __forceinline__ double scan_f64(double x)
     x += dpp_f64<0x143, 0xc>(x);
     return x;
 }
+// The same over the last `span` lanes up to and with this one, where lanes between two
+// borders all sum from the lower border on: a step adds a lower lane's sum if that
+// lane is within the span, so what lies before a border is never added.
+__device__ __forceinline__ double scan_spans_f64(double x, int span, int lane)
+{
+    auto add = [&](double y, int apart) { x += span > apart ? y : 0.0; };
+    add(dpp_f64<0x111, 0xf>(x), 1);
+    add(dpp_f64<0x112, 0xf>(x), 2);
+    add(dpp_f64<0x114, 0xf>(x), 4);
+    add(dpp_f64<0x118, 0xf>(x), 8);
+    add(dpp_f64<0x142, 0xa>(x), (lane & 15) + 1);
+    add(dpp_f64<0x143, 0xc>(x), lane - 31);
+    return x;
+}
 __device__ __forceinline__ double lane_f64(double x, int lane)
 {
     const int2 v = __builtin_bit_cast(int2, x);

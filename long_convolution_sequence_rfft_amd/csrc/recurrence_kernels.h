@@ -452,7 +452,8 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
 // segment's end, without a token's own pair in either product: both are made of
 // float32 values (scores weighted by both products before any rounding, the states' parts
 // from split operands) and kept in LDS for kGradHold chunks, then summed up in
-// float64 by all waves.
+// float64 by all waves.  Over a whole sequence the sum is zero, so at a reset it
+// starts anew: a sequence's dg holds no rounding of those after it.
 //
 // Bound by a chunk's instructions: 66 us at 2 x 8192 tokens of 12 heads of 64 in
 // bfloat16 (176 MB), 80 us at 4 x 2048 in float32; 610 vector instructions per
@@ -528,7 +529,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
     cross = sum_rows(sum16(cross));
     if (lane == 0) sums[wave] = own_k ? (double)cross : 0.0;
     __syncthreads();
-    double over = ((sums[0] + sums[1]) + (sums[2] + sums[3]));  // <S, dS> after the chunks held
+    double over = ((sums[0] + sums[1]) + (sums[2] + sums[3]));  // <S, dS> after the chunks held, or their sum up to a reset
     __syncthreads();
 
     // two waves bring in each tensor: q and do are also needed transposed
@@ -764,23 +765,31 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
             if (lane == 0) resets[held] = resets_now;
         }
         if (held == kGradHold - 1 || c == nchunk - 1) {
-            // chunk held - h (h from 0: the first of them in time) follows all later held ones
+            // chunk held - h (h from 0: the first of them in time) follows all later held ones; lane l has
+            // the chunk's token C - 1 - l and sums from it to the next reset or the chunk's end
             __syncthreads();
+            const int t = lane < C ? C - 1 - lane : 0;
+            auto later = [&](int x) { return resets[x] >> t >> 1; };  // resets after the lane's token
+            auto scan = [&](int x) {
+                const unsigned long long next = later(x);
+                return scan_spans_f64(lane < C ? (double)hold[x * C + t] : 0.0, next ? __builtin_ctzll(next) + 1 : C, lane);
+            };
+            // what the tokens before chunk y add, if `after` is what follows the chunk
+            auto across = [&](double after, int y) { return (resets[y] ? 0.0 : after) + sums[y]; };
             for (int x = wave; x <= held; x += 8) {
-                const double s = scan_f64(lane < C ? (double)hold[x * C + C - 1 - lane] : 0.0);
-                if (lane == C - 1) sums[x] = s;
+                const double s = scan(x);
+                if (lane == C - 1) sums[x] = resets[x] & 1 ? 0.0 : s;
             }
             __syncthreads();
             for (int x = wave; x <= held; x += 8) {
-                double before = over;
-                for (int y = 0; y < x; ++y) before += sums[y];
-                const double s = scan_f64(lane < C ? (double)hold[x * C + C - 1 - lane] : 0.0);
-                const int t = C - 1 - lane;
+                double after = over;
+                for (int y = 0; y < x; ++y) after = across(after, y);
+                const double s = scan(x);
                 const int64_t tc = t0 + (int64_t)(nchunk - 1 - (c - held + x)) * C + t;
                 if (lane < C && tc < t1)
-                    p.dg[(b * p.N + tc) * p.heads + h] = resets[x] >> t & 1 ? 0.0f : (float)(before + s);
+                    p.dg[(b * p.N + tc) * p.heads + h] = resets[x] >> t & 1 ? 0.0f : (float)((later(x) ? 0.0 : after) + s);
             }
-            for (int y = 0; y <= held; ++y) over += sums[y];
+            for (int y = 0; y <= held; ++y) over = across(over, y);
             __syncthreads();
         }
     }

@@ -89,6 +89,28 @@ def test_dg_of_fast_decays(shape, carry, dtype):
         check_dg(c)
 
 
+# second sequence's values, as many times the first one's (binary16: scores have to stay below 65504)
+LARGER = {"f32": 1000.0, "bf16": 1000.0, "f16": 30.0}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(2, 60, 2, 32, 32), (1, 420, 3, 16, 24), (1, 420, 200, 8, 8), (1, 2600, 1, 64, 64)])
+def test_dg_of_a_sequence_beside_a_larger_one(shape, dtype):
+    """Sequences packed into a row: a sequence's gradient has the accuracy of its own terms, whatever
+    follows it.  Starts at a chunk's first token, at its last, and two in one chunk."""
+    B, N = shape[:2]
+    starts = (20, 41) if N < 64 else (64, 127, 130, 256, N - 100)
+    c = Case(*shape, dtype, seed=23, carry=False, resets=[(t, -np.inf) for t in starts])
+    for i, t in enumerate(starts):
+        if i % 2 == 0:
+            end = starts[i + 1] if i + 1 < len(starts) else N
+            c.v[:, t:end] *= LARGER[dtype]
+            c.do[:, t:end] *= LARGER[dtype]
+    check_dg(c)
+    c = Case(*shape, dtype, seed=24, carry=True, lengths=(N - 1,) * B, resets=[(t, -88.0) for t in starts])
+    check_dg(c)
+
+
 # ------------------------------------------------------------- magnitudes
 
 @pytest.mark.parametrize("N", [50, 200])
