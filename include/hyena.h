@@ -345,7 +345,9 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  * With binary16 the scores (times decay and scale) have to stay within its
  * range.  Inputs within a row's length have to be
  * finite (g may be -infinity): an infinity or a NaN reaches its own and later
- * tokens' results, and may reach those of up to 63 tokens before it.
+ * tokens' results of its sequence (their gradients: all of the sequence), and may
+ * reach those of up to 63 tokens before and after it and all of another sequence
+ * that starts or ends among these.  What comes further on in a row does not see it.
  *
  * No atomics are used: the same call gives the same bits.
  */

@@ -45,7 +45,7 @@ __global__ __launch_bounds__(256) void hyena_rec_scan(RecScanArgs p)
 #pragma unroll
             for (int n = 0; n < kScanBatch; ++n)
                 if (n0 + n < p.nseg) {
-                    s = fmaf(decay[n], s, local[n]);
+                    s = decay[n] != 0.0f ? fmaf(decay[n], s, local[n]) : local[n];  // (s may be infinite)
                     x[(n0 + n + 1) * step] = s;
                 }
         }

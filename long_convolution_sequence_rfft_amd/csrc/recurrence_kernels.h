@@ -54,6 +54,19 @@ template <bool HOLD> __device__ __forceinline__ void hold_schedule()
     if constexpr (HOLD) __builtin_amdgcn_sched_barrier(0);
 }
 
+// A state in front of a reset has no part in what comes after it, whatever it
+// holds: zero times an infinity would not be zero.  restarts: the chunk has a reset
+// (the same for all lanes).
+template <typename D> __device__ __forceinline__ bool restarts(const D& d, int last)
+{
+    return __builtin_amdgcn_readfirstlane(d.count[last]) != 0;
+}
+// the state's part of a tile of results whose column is the lane's token
+__device__ __forceinline__ f32x4 unless_zero(f32x4 x, float factor)
+{
+    return factor != 0.0f ? x : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
 // out[16 i + l16] = sum over the four lanes of a column of x[i]
 template <int IT> __device__ __forceinline__ void store_token_sums(float* out, const float (&x)[IT], int lane, int grp)
 {
@@ -135,8 +148,15 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
             if (slot == 0) fetch_g(c + kDecayBatch + wave);
         }
         const float all = dec.head[C - 1];
+        const bool fresh = restarts(dec, C - 1);
         const float* f = role ? dec.head : dec.tail;
-        total *= all;
+        total = fresh || total == 0.0f ? 0.0f : total * all;  // (all may not be a number)
+        if (fresh) {
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int v = 0; v < VW; ++v) S[k][v] = f32x4{};
+        }
 #pragma unroll
         for (int v = 0; v < VW; ++v) {
             const int vt = wave + 4 * v;
@@ -361,6 +381,7 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
         __syncthreads();
 
         const float all = dec.head[C - 1];
+        const bool fresh = restarts(dec, C - 1);
         float rdot[IT] = {};
 #pragma unroll
         for (int v = 0; v < CW; ++v) {
@@ -384,6 +405,7 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int ti = 16 * i + l16;
+                if (fresh) so[i] = unless_zero(so[i], dec.head[ti]);
                 f32x4 o = fit.results(so[i], p.scale * dec.head[ti]);
                 if constexpr (TRANS) {
                     const f32x4 r = Mx<T>::widen(under.x[i][v]);
@@ -400,6 +422,10 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
             }
             // the state after this chunk
             hold_schedule<(DA * DC > 64 * 64)>();
+            if (fresh) {
+#pragma unroll
+                for (int k = 0; k < AT; ++k) S[k][v] = f32x4{};
+            }
             Split<T, NT> y[C / 32];
             const float up = split_columns<T>(y, [&](int j) {
                 const f32x8 w = join8(*(const f32x4*)(dec.tail + 32 * j + 8 * grp),
@@ -688,6 +714,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
         __syncthreads();
 
         const float all = dec.head[C - 1];
+        const bool fresh = restarts(dec, C - 1);
         // across: rows that dS multiplies (v or k); scores and fold: out_j += scores_ij fold_i; add: the other
         // tensor of dS's update
         auto work = [&](auto is_dk, const T* across, const T* scores, const T* fold, const T* add, T* out) {
@@ -720,6 +747,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 #pragma unroll
                 for (int j = 0; j < IT; ++j) {
                     const int tj = 16 * j + l16;
+                    if (fresh) sx[j] = unless_zero(sx[j], dec.tail[tj]);
                     f32x4 x = fit.results(sx[j], dec.tail[tj]);
                     if constexpr (kSums) {
                         const f32x4 kk = Mx<T>::widen(*(const vec4*)(kr + tj * LD + perm4(4 * nt + grp)));
@@ -735,6 +763,10 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                     store_row4<T>(orows, orow + 16 * j * ostep, tj < left, 16 * nt + 4 * grp, width, x);
                 }
                 hold_schedule<(DK * DV > 64 * 64)>();
+                if (fresh) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) S[m * MW + n] = f32x4{};
+                }
                 Split<T, NU> y[C / 32];
                 const float up = split_columns<T>(y, [&](int i) {
                     const f32x8 w = join8(*(const f32x4*)(dec.head + 32 * i + 8 * grp), *(const f32x4*)(dec.head + 32 * i + 8 * grp + 4));

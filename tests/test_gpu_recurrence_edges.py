@@ -111,6 +111,34 @@ def test_dg_of_a_sequence_beside_a_larger_one(shape, dtype):
     check_dg(c)
 
 
+# ------------------------------------------------------------- sequences side by side
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(1, 470, 2, 64, 64), (1, 470, 400, 8, 8), (2, 1900, 1, 16, 100)])
+def test_infinities_stay_near_their_sequence(shape, dtype):
+    """Not finite: tokens in the middle of the second of three sequences, 64 tokens and more from both of
+    its ends.  More than 63 tokens before its start and after its end everything is the same bits."""
+    import torch
+    N = shape[1]
+    start, end = 130, N - 140
+    c = Case(*shape, dtype, seed=31, resets=((start, -np.inf), (end, -100.0)))
+    want = [*c.forward(), *c.backward()]
+    for name, value in (("q", np.nan), ("k", np.inf), ("v", -np.inf), ("do", np.nan), ("g", np.nan)):
+        t = getattr(c, name)
+        kept = t.clone()
+        t[:, 200] = float(value)
+        say(f"[gpu]   {name} = {value}")
+        got = [*c.forward(), *c.backward()]
+        torch.cuda.synchronize()
+        t.copy_(kept)
+        for a, b, what in zip(got, want, ("o", "state", "dq", "dk", "dv", "dg", "d_state")):
+            if "state" in what:
+                assert torch.equal(a, b), (name, what)
+                continue
+            assert torch.equal(a[:, :start - 63], b[:, :start - 63]), (name, what)
+            assert torch.equal(a[:, end + 63:], b[:, end + 63:]), (name, what)
+
+
 # ------------------------------------------------------------- magnitudes
 
 @pytest.mark.parametrize("N", [50, 200])
