@@ -420,7 +420,8 @@ hyena_status hyena_recurrence_backward(hyena_recurrence_t plan,
  * and updates states[slots[b]] (float32 [n_slots][heads][dk][dv]).  q, k, v, g
  * are read at token 0 of their views; o: [B][heads][dv].  in->state and
  * in->lengths are ignored.  slots: int32 [B] on the device, or NULL for
- * slots[b] = b (then n_slots >= B).  A slot outside 0..n_slots-1 marks a row
+ * slots[b] = b (then n_slots >= B).  Where g starts a new sequence the state is
+ * written without being read, so a new request's may be uninitialised.  A slot outside 0..n_slots-1 marks a row
  * that takes no part: its row of o is written as zeros and no state is touched.
  * The other slots have to differ from each other: two rows on one state would
  * update it in no order.

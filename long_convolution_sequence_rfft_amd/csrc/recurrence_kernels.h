@@ -833,7 +833,8 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 
 // ---------------------------------------------------------------------------
 // One token: S <- exp(g) S + k v^T in place, o = scale S^T q.  One workgroup per
-// (row, head); a thread owns VEC columns and every (256 / columns)th row.  Bound
+// (row, head); a thread owns VEC columns and every (256 / columns)th row.  Where g
+// starts a new sequence the old state is not read: it may be what memory held.  Bound
 // by memory, for few rows by the launch: 256 requests of 12 heads of 64 in 17 us
 // (101 MB of states read and written, in part from the last-level cache), one
 // request in 6 us on the device.
@@ -857,7 +858,8 @@ __global__ __launch_bounds__(256) void hyena_rec_step(RecStepArgs p)
         qs[tid] = load_one<T>(q + tid) * p.scale;
         ks[tid] = load_one<T>(k + tid);
     }
-    const float a = expf(*row_base<float>(p.g, b, h));
+    const float g = *row_base<float>(p.g, b, h), a = expf(g);
+    const bool fresh = g * 1.44269504088896340736f < kResetLog2;  // a new sequence, whatever the state holds
     const int cols = (p.dv + VEC - 1) / VEC, groups = 256 / cols;
     const int col = tid % cols, row0 = tid / cols;
     float* s = p.states + ((slot * p.heads + h) * p.dk) * p.dv + col * VEC;
@@ -866,18 +868,26 @@ __global__ __launch_bounds__(256) void hyena_rec_step(RecStepArgs p)
     for (int j = 0; j < VEC; ++j) vv[j] = load_one<T>(v + col * VEC + j);
     __syncthreads();
     if (row0 < groups) {
-        for (int r = row0; r < p.dk; r += groups) {
-            alignas(16) float x[VEC];
-            if constexpr (VEC == 4) *(f32x4*)x = *(const f32x4*)(s + (int64_t)r * p.dv);
-            else x[0] = s[(int64_t)r * p.dv];
+        auto rows = [&](auto old) {
+            for (int r = row0; r < p.dk; r += groups) {
+                alignas(16) float x[VEC];
+                if constexpr (!decltype(old)::value) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                x[j] = fmaf(a, x[j], ks[r] * vv[j]);
-                sum[j] = fmaf(qs[r], x[j], sum[j]);
+                    for (int j = 0; j < VEC; ++j) x[j] = ks[r] * vv[j];
+                } else {
+                    if constexpr (VEC == 4) *(f32x4*)x = *(const f32x4*)(s + (int64_t)r * p.dv);
+                    else x[0] = s[(int64_t)r * p.dv];
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) x[j] = fmaf(a, x[j], ks[r] * vv[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) sum[j] = fmaf(qs[r], x[j], sum[j]);
+                if constexpr (VEC == 4) *(f32x4*)(s + (int64_t)r * p.dv) = *(const f32x4*)x;
+                else s[(int64_t)r * p.dv] = x[0];
             }
-            if constexpr (VEC == 4) *(f32x4*)(s + (int64_t)r * p.dv) = *(const f32x4*)x;
-            else s[(int64_t)r * p.dv] = x[0];
-        }
+        };
+        if (fresh) rows(std::false_type{});
+        else rows(std::true_type{});
 #pragma unroll
         for (int j = 0; j < VEC; ++j) acc[(row0 * cols + col) * VEC + j] = sum[j];
     }

@@ -139,6 +139,26 @@ def test_infinities_stay_near_their_sequence(shape, dtype):
             assert torch.equal(a[:, end + 63:], b[:, end + 63:]), (name, what)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dv", [64, 7])
+def test_step_starts_a_sequence_over_whatever_the_slot_held(dv, dtype):
+    """g = -infinity, and any below -87.34, leaves nothing of a state: the bits of a state of zeros."""
+    import torch
+    B, H, dk = 5, 2, 24
+    gen = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn((B, H, d), generator=gen).to(torch_dtype(dtype)).cuda() for d in (dk, dk, dv))
+    g = torch.tensor([-np.inf, -np.inf, -88.0, -103.0, -87.4], dtype=torch.float32)[:, None].expand(B, H).cuda()
+    table = torch.zeros((B, H, dk, dv), device="cuda")
+    plan = hyena.Recurrence(B, 1, H, dk, dv, io_dtype=IO[dtype])
+    want = plan.step(q, k, v, g, table).clone()
+    states = table.clone()
+    for i, left in enumerate((float("nan"), float("inf"), 3e38, -3e38, 3e38)):
+        table[i] = left
+    got = plan.step(q, k, v, g, table)
+    assert torch.isfinite(want.float()).all()
+    assert torch.equal(got, want) and torch.equal(table, states)
+
+
 # ------------------------------------------------------------- magnitudes
 
 @pytest.mark.parametrize("N", [50, 200])
