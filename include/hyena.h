@@ -334,20 +334,20 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  * tokens and, in bfloat16 for o and dv, the state are rounded to the storage
  * type as operands of the matrix products (relative error up to 2^-8 for
  * bfloat16, 2^-11 for binary16 scores, or 2^-25 absolutely where they are
- * subnormal), but in calls of few tokens (N <= 64 and B * heads <= 256) neither
- * is; the states, their gradients and the gradient of g are computed from
- * operands split so that they keep float32 accuracy (binary16: in each column,
- * or row, of a state relative to its largest element, 2^-36 of it at least).
- * The gradient of g at a token is a sum of terms of that token and the later ones
- * of its sequence, each with the decays of g; its accuracy is that of the sum of their
- * absolute values, so a decay much faster than all those after it has a small
- * gradient with an error of their size.
- * With binary16 the scores (times decay and scale) have to stay within its
- * range.  Inputs within a row's length have to be
- * finite (g may be -infinity): an infinity or a NaN reaches its own and later
- * tokens' results of its sequence (their gradients: all of the sequence), and may
- * reach those of up to 63 tokens before and after it and all of another sequence
- * that starts or ends among these.  What comes further on in a row does not see it.
+ * subnormal), but with N <= 64 neither is.  The states, their gradients and the
+ * gradient of g are computed from operands split so that they keep float32
+ * accuracy (binary16: in each column, or row, of a state relative to its largest
+ * element, 2^-36 of it at least).  The gradient of g at a token is a sum of terms
+ * of that token and the later ones of its sequence; its accuracy is that of the sum
+ * of their absolute values, so a decay much faster than all those after it has a
+ * small gradient with an error of their size.  With binary16 the scores (times
+ * decay and scale) have to stay within its range.
+ *
+ * Inputs within a row's length have to be finite (g may be -infinity): an infinity
+ * or a NaN reaches its own and later tokens' results of its sequence (their
+ * gradients: all of the sequence), and may reach those of up to 63 tokens before
+ * and after it and all of another sequence that starts or ends among these.  What
+ * comes further on in a row does not see it.
  *
  * No atomics are used: the same call gives the same bits.
  */

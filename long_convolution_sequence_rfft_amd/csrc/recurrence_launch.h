@@ -36,13 +36,13 @@ template <typename T> hyena_status rec_launch_states(const RecStateArgs& a, int6
     return a.dv <= 64 ? rec_states_one<T, 128, 64>(a, bh, roles, s) : rec_states_one<T, 128, 128>(a, bh, roles, s);
 }
 
-// Calls of few tokens take the FINE forms: rows of one chunk, whose workgroups
-// run in one round of the chip (there an error may not average out, and the
-// launch takes most of the time).  12 rows and heads of 64 tokens, the other
-// forms and these: heads of 64 in bfloat16 forward 7.7 and 7.8 us, backward 16.8
-// and 18.2; of 128 10.1 and 12.1, 29.8 and 33.7.  6144 of them: 48 and 76, 250
-// and 294; 140 and 285, 699 and 865.
-inline bool fine_call(int64_t N, int64_t bh) { return N <= 64 && bh <= 256; }
+// Rows of few tokens take the FINE forms: rows of one chunk (there an error may not
+// average out), however many there are, so that a row's results do not depend on
+// the others in its batch.  12 rows and heads of 64 tokens, the other forms and these:
+// heads of 64 in bfloat16 forward 7.7 and 7.8 us, backward 16.8 and 18.2; of 128
+// 10.1 and 12.1, 29.8 and 33.7.  6144 of them: 48 and 76, 250 and 294; 140 and
+// 285, 699 and 865.
+inline bool fine_rows(int64_t N) { return N <= 64; }
 
 template <typename T, int DA, int DC, bool TRANS, bool EXACT, bool VEC, bool FINE>
 hyena_status rec_out_as(const RecArgs& a, int64_t bh, hipStream_t s)
@@ -56,7 +56,7 @@ template <typename T, int DA, int DC, bool TRANS, bool EXACT>
 hyena_status rec_out_one(const RecArgs& a, int64_t bh, hipStream_t s)
 {
     if constexpr (sizeof(T) == 2 && EXACT)
-        if (fine_call(a.N, bh)) return rec_out_as<T, DA, DC, TRANS, true, false, true>(a, bh, s);
+        if (fine_rows(a.N)) return rec_out_as<T, DA, DC, TRANS, true, false, true>(a, bh, s);
     const bool vec = by_vectors(a.a, a.b, a.c) && (!TRANS || by_vectors(a.r));
     return vec ? rec_out_as<T, DA, DC, TRANS, EXACT, true, false>(a, bh, s)
                : rec_out_as<T, DA, DC, TRANS, EXACT, false, false>(a, bh, s);
@@ -74,7 +74,7 @@ template <typename T> hyena_status rec_launch_out(const RecArgs& a, int64_t bh, 
 {
     if (transposed) return rec_out_pick<T, true, true>(a, bh, s);
     if constexpr (Mx<T>::kTerms == 3)
-        if (a.last == nullptr && !fine_call(a.N, bh)) return rec_out_pick<T, false, false>(a, bh, s);
+        if (a.last == nullptr && !fine_rows(a.N)) return rec_out_pick<T, false, false>(a, bh, s);
     return rec_out_pick<T, false, true>(a, bh, s);
 }
 
@@ -89,7 +89,7 @@ hyena_status rec_grad_as(const RecGradArgs& a, int64_t bh, hipStream_t s)
 template <typename T, int DK, int DV> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
 {
     if constexpr (sizeof(T) == 2)
-        if (fine_call(a.N, bh)) return rec_grad_as<T, DK, DV, false, true>(a, bh, s);
+        if (fine_rows(a.N)) return rec_grad_as<T, DK, DV, false, true>(a, bh, s);
     return by_vectors(a.q, a.k, a.v, a.o) ? rec_grad_as<T, DK, DV, true, false>(a, bh, s)
                                           : rec_grad_as<T, DK, DV, false, false>(a, bh, s);
 }

@@ -159,6 +159,22 @@ def test_step_starts_a_sequence_over_whatever_the_slot_held(dv, dtype):
     assert torch.equal(got, want) and torch.equal(table, states)
 
 
+# ------------------------------------------------------------- what else is in a call
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(2, 40, 3, 64, 64), (1, 64, 2, 40, 72), (1, 1, 5, 128, 128), (1, 17, 2, 7, 5)])
+def test_a_short_row_has_the_same_bits_in_any_batch(shape, dtype):
+    import torch
+    B, N, H, dk, dv = shape
+    c = Case(*shape, dtype, seed=3)
+    many = -(-300 // (B * H))
+    d = Case(B * many, N, H, dk, dv, dtype, seed=4)
+    for name in ("q", "k", "v", "g", "do", "state", "d_final"):
+        getattr(d, name)[-B:] = getattr(c, name)
+    for a, b in zip([*c.forward(), *c.backward()], [*d.forward(), *d.backward()]):
+        assert torch.equal(a, b[-B:])
+
+
 # ------------------------------------------------------------- magnitudes
 
 @pytest.mark.parametrize("N", [50, 200])
