@@ -217,9 +217,11 @@ template <typename T, int D, bool FINE> constexpr size_t rec_grad_lds()
 // (a_i . b_j) c_j).  a = q, b = k, c = v gives o; a = do, b = v, c = k gives dq
 // (TRANS: the state's rows are then the channels of c).  TRANS also writes
 // rq_i = r_i . (the state's part of out_i), with the state as a split operand
-// so that it keeps float32 accuracy.  EXACT: so does the state itself through
-// the segment (needed where it is an output, and for rq); else its updates keep
-// 16 bits, as it only meets q as a 16-bit operand.
+// so that it keeps float32 accuracy.  So does the state itself through the segment:
+// with updates of two bfloat16 terms what is left of values that cancel would be
+// lost, and o would depend on whether the final state is asked for (65536 tokens
+// of 12 heads of 64 in bfloat16 91 us so, 93 with three; 2 x 8192 of 6 heads of 128
+// 41 and 43.5).
 //
 // One workgroup of four waves per (row, head, segment).  Waves share the score
 // tiles of a chunk (written to LDS in storage type) and each owns every fourth
@@ -231,11 +233,11 @@ template <typename T, int D, bool FINE> constexpr size_t rec_grad_lds()
 // 12 heads of 64: 42 us, 126 MB; 620 vector instructions per wave and chunk)
 // by the instructions of a chunk, with two or three waves per SIMD.
 // ---------------------------------------------------------------------------
-template <typename T, int DA, int DC, bool TRANS, bool EXACT, bool VEC, bool FINE>
+template <typename T, int DA, int DC, bool TRANS, bool VEC, bool FINE>
 __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_rec_out(RecArgs p)
 {
     constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
-    constexpr int NT = EXACT || Mx<T>::kTerms < 2 ? Mx<T>::kTerms : 2;  // state update
+    constexpr int NT = Mx<T>::kTerms;  // state update
     constexpr int NS = TRANS ? Mx<T>::kTerms : Mx<T>::kTerms < 2 ? 1 : Mx<T>::kTerms == 2 || FINE ? 2 : 1;  // state as an operand
     constexpr int NP = kScoreTerms<T, FINE>;
     constexpr int AT = DA / 16, CW = DC / 64, IT = C / 16;
@@ -722,7 +724,6 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
             constexpr int kAcross = kSums ? DV : DK, MT = kAcross / 16, MW = (kSums ? DK : DV) / 64;
             const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
             constexpr int NS = kSums ? NT : NT < 2 ? 1 : NT == 2 || FINE ? 2 : 1;  // dS as an operand
-            constexpr int NU = kSums ? NT : NT < 2 ? NT : 2;  // and in its updates
             const __amdgpu_buffer_rsrc_t orows = rows_at(out + tb0 * p.heads * width);
             const uint32_t ostep = (uint32_t)p.heads * (uint32_t)width * (uint32_t)sizeof(T);
             const uint32_t orow = (uint32_t)again(l16) * ostep;
@@ -767,7 +768,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 #pragma unroll
                     for (int m = 0; m < MT; ++m) S[m * MW + n] = f32x4{};
                 }
-                Split<T, NU> y[C / 32];
+                Split<T, NT> y[C / 32];
                 const float up = split_columns<T>(y, [&](int i) {
                     const f32x8 w = join8(*(const f32x4*)(dec.head + 32 * i + 8 * grp), *(const f32x4*)(dec.head + 32 * i + 8 * grp + 4));
                     return Mx<T>::widen8(ff[i]) * (w * p.scale);

@@ -44,38 +44,33 @@ template <typename T> hyena_status rec_launch_states(const RecStateArgs& a, int6
 // 285, 699 and 865.
 inline bool fine_rows(int64_t N) { return N <= 64; }
 
-template <typename T, int DA, int DC, bool TRANS, bool EXACT, bool VEC, bool FINE>
+template <typename T, int DA, int DC, bool TRANS, bool VEC, bool FINE>
 hyena_status rec_out_as(const RecArgs& a, int64_t bh, hipStream_t s)
 {
-    HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, EXACT, VEC, FINE),
-              (hyena_rec_out<T, DA, DC, TRANS, EXACT, VEC, FINE>), dim3((unsigned)(bh * a.nseg)), dim3(256), 0, s, a);
+    HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, VEC, FINE),
+              (hyena_rec_out<T, DA, DC, TRANS, VEC, FINE>), dim3((unsigned)(bh * a.nseg)), dim3(256), 0, s, a);
     return rec_done();
 }
 
-template <typename T, int DA, int DC, bool TRANS, bool EXACT>
+template <typename T, int DA, int DC, bool TRANS>
 hyena_status rec_out_one(const RecArgs& a, int64_t bh, hipStream_t s)
 {
-    if constexpr (sizeof(T) == 2 && EXACT)
-        if (fine_rows(a.N)) return rec_out_as<T, DA, DC, TRANS, true, false, true>(a, bh, s);
+    if constexpr (sizeof(T) == 2)
+        if (fine_rows(a.N)) return rec_out_as<T, DA, DC, TRANS, false, true>(a, bh, s);
     const bool vec = by_vectors(a.a, a.b, a.c) && (!TRANS || by_vectors(a.r));
-    return vec ? rec_out_as<T, DA, DC, TRANS, EXACT, true, false>(a, bh, s)
-               : rec_out_as<T, DA, DC, TRANS, EXACT, false, false>(a, bh, s);
+    return vec ? rec_out_as<T, DA, DC, TRANS, true, false>(a, bh, s) : rec_out_as<T, DA, DC, TRANS, false, false>(a, bh, s);
 }
 
-template <typename T, bool TRANS, bool EXACT> hyena_status rec_out_pick(const RecArgs& a, int64_t bh, hipStream_t s)
+template <typename T, bool TRANS> hyena_status rec_out_pick(const RecArgs& a, int64_t bh, hipStream_t s)
 {
     if (a.da <= 64)
-        return a.dc <= 64 ? rec_out_one<T, 64, 64, TRANS, EXACT>(a, bh, s) : rec_out_one<T, 64, 128, TRANS, EXACT>(a, bh, s);
-    return a.dc <= 64 ? rec_out_one<T, 128, 64, TRANS, EXACT>(a, bh, s) : rec_out_one<T, 128, 128, TRANS, EXACT>(a, bh, s);
+        return a.dc <= 64 ? rec_out_one<T, 64, 64, TRANS>(a, bh, s) : rec_out_one<T, 64, 128, TRANS>(a, bh, s);
+    return a.dc <= 64 ? rec_out_one<T, 128, 64, TRANS>(a, bh, s) : rec_out_one<T, 128, 128, TRANS>(a, bh, s);
 }
 
-// Only bfloat16 has a cheaper form of the state than the exact one.
 template <typename T> hyena_status rec_launch_out(const RecArgs& a, int64_t bh, bool transposed, hipStream_t s)
 {
-    if (transposed) return rec_out_pick<T, true, true>(a, bh, s);
-    if constexpr (Mx<T>::kTerms == 3)
-        if (a.last == nullptr && !fine_rows(a.N)) return rec_out_pick<T, false, false>(a, bh, s);
-    return rec_out_pick<T, false, true>(a, bh, s);
+    return transposed ? rec_out_pick<T, true>(a, bh, s) : rec_out_pick<T, false>(a, bh, s);
 }
 
 template <typename T, int DK, int DV, bool VEC, bool FINE>

@@ -175,6 +175,59 @@ def test_a_short_row_has_the_same_bits_in_any_batch(shape, dtype):
         assert torch.equal(a, b[-B:])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(2, 100, 2, 64, 64), (1, 128, 3, 40, 128), (1, 300, 2, 128, 128), (1, 150, 800, 8, 8)])
+def test_asking_for_the_final_state_leaves_the_outputs_as_they_are(shape, dtype):
+    import torch
+    c = Case(*shape, dtype, seed=5)
+    o = c.plan.forward(c.q, c.k, c.v, c.g, scale=c.scale, state=c.state)[0]
+    assert torch.equal(o, c.forward()[0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H", [2, 400])
+def test_states_are_held_in_32_bits(H, dtype):
+    """Values that cancel: a first token's V, what decays leave of it less its rounding to the storage
+    type, and less the rounding of that.  What bfloat16 leaves of V = 1..2 is about 2^-16; a token of another
+    chunk reads it.  A state of 32 bits gets there with eleven roundings of at most 2^-24 of V (V times its
+    decay, the state times its, two of each for the exponentials; the two subtracted values and their
+    decays): below 2^-19.  Reading rounds the state and the result to the storage type."""
+    import torch
+    N, d = 192, 8
+    say(f"[gpu] cancelling states H={H} {dtype}")
+    dt, u = torch_dtype(dtype), mixer_ref.HALF_STEP[dtype]
+    gen = torch.Generator().manual_seed(6)
+    for reverse in (False, True):
+        # e: the direction in which everything is; other keys and queries are 0
+        g = torch.full((1, N, H), -0.013)
+        V = (1 + torch.rand((1, H, d), generator=gen)).to(dt).double()
+        at = (3, 70, 90, 180)          # a chunk of its own, two of the next, the reader in a third
+        if reverse:
+            at = tuple(N - 1 - t for t in at)
+        write, read = torch.zeros((1, N, H, d), dtype=dt), torch.zeros((1, N, H, d), dtype=dt)
+        write[:, at[0]] = V.to(dt)
+        # decay from token i to a later one (reversed: earlier) is the sum of g between
+        gd = g.double()
+        left = V
+        for i in (1, 2):
+            left = left * torch.exp(gd[:, 0] * abs(at[i] - at[i - 1]))[..., None]
+            write[:, at[i]] = -left.to(dt)
+            left = left + write[:, at[i]].double()
+        left = left * torch.exp(gd[:, 0] * abs(at[3] - at[2]))[..., None]
+        one = torch.zeros((1, N, H, d), dtype=dt)
+        for t in at[:3]:
+            one[:, t, :, 0] = 1.0
+        read[:, at[3], :, 0] = 1.0
+        plan = hyena.Recurrence(1, N, H, d, d, io_dtype=IO[dtype], training=True)
+        one, read, write, gg = (t.cuda() for t in (one, read, write, g))
+        if not reverse:  # o of the reader
+            got = plan.forward(read, one, write, gg, scale=1.0)[0][:, at[3]]
+        else:            # dv of the reader, from do of the writers
+            got = plan.backward(write, one, read, torch.zeros_like(write), gg, scale=1.0)[2][:, at[3]]
+        ref = left.numpy()
+        close(got, ref, 2 * u * np.abs(ref) + 2.0 ** -19 + (2.0 ** -25 if dtype == "f16" else 0.0), f"reverse={reverse}")
+
+
 # ------------------------------------------------------------- magnitudes
 
 @pytest.mark.parametrize("N", [50, 200])
