@@ -322,7 +322,8 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  * Layouts: q, k [B][N][heads][dk] and v [B][N][heads][dv] in the plan's io
  * dtype, g float32 [B][N][heads], each given as a strided view (below);
  * states float32 [B][heads][dk][dv], dense; outputs and gradients dense in
- * the shape of what they belong to.
+ * the shape of what they belong to.  o, dq, dk, dv and the workspace are 16-byte
+ * aligned; states, their gradients and dg, as all inputs, to their element.
  *
  * lengths (int32 [B] on the device, or NULL: all N) makes a padded batch:
  * tokens at lengths[b] and after it are never read, their rows of o and of
@@ -476,8 +477,9 @@ typedef struct hyena_qk_norm {
     hyena_view q, k;           /* inputs */
 } hyena_qk_norm;
 
-/* q_out [B][N][q_heads][D], k_out [B][N][k_heads][D]: dense, in the io dtype.
- * They must not overlap an input or each other. */
+/* q_out [B][N][q_heads][D], k_out [B][N][k_heads][D]: dense, in the io dtype,
+ * 16-byte aligned (so are dq, dk and the scratch of the backward pass).  They must
+ * not overlap an input or each other. */
 hyena_status hyena_qk_norm_forward(const hyena_qk_norm* op, void* q_out, void* k_out,
                                    void* stream);
 

@@ -88,13 +88,16 @@ hyena_status check_inputs(const RecPlan& p, const hyena_recurrence_inputs* in, i
     return HYENA_OK;
 }
 
-// Outputs may not overlap each other, an input or the workspace.
-hyena_status check_outputs(const Span* in, int nin, const Span* out, const char* const* names, int nout)
+// Outputs may not overlap each other, an input or the workspace.  The first `vectors`
+// of them are stored by vectors, the others, all float32, by elements.
+hyena_status check_outputs(const Span* in, int nin, const Span* out, const char* const* names, int nout, int vectors)
 {
     for (int i = 0; i < nout; ++i) {
         if (out[i].p == nullptr) continue;
-        if (!aligned(out[i].p, 16))
+        if (i < vectors && !aligned(out[i].p, 16))
             return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(names[i]) + " must be 16-byte aligned");
+        if (!aligned(out[i].p, 4))
+            return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(names[i]) + " is not aligned to its element");
         for (int j = 0; j < nin; ++j)
             if (spans_overlap(out[i], in[j]))
                 return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(names[i]) + " overlaps an input or the workspace");
@@ -317,7 +320,7 @@ hyena_status hyena_recurrence_forward(hyena_recurrence_t plan, const hyena_recur
     const Span out[2] = {{o, (size_t)(p.B * p.heads) * (size_t)p.N * (size_t)p.dv * element_bytes(p.io_dtype)},
                          {final_state, state}};
     const char* const names[2] = {"o", "final_state"};
-    if ((st = check_outputs(spans, 7, out, names, 2)) != HYENA_OK) return st;
+    if ((st = check_outputs(spans, 7, out, names, 2, 1)) != HYENA_OK) return st;
     return by_type(p.io_dtype, [&](auto t) {
         return run_forward<decltype(t)>(p, *in, o, final_state, workspace, (hipStream_t)stream);
     });
@@ -351,7 +354,7 @@ hyena_status hyena_recurrence_backward(hyena_recurrence_t plan, const hyena_recu
     const Span outs[5] = {{out->dq, n * p.dk * e}, {out->dk, n * p.dk * e}, {out->dv, n * p.dv * e},
                           {out->dg, n * 4}, {out->d_state, state}};
     const char* const names[5] = {"dq", "dk", "dv", "dg", "d_state"};
-    if ((st = check_outputs(spans, 9, outs, names, 5)) != HYENA_OK) return st;
+    if ((st = check_outputs(spans, 9, outs, names, 5, 3)) != HYENA_OK) return st;
     return by_type(p.io_dtype, [&](auto t) {
         return run_backward<decltype(t)>(p, *in, *d_o, d_final, *out, workspace, (hipStream_t)stream);
     });
@@ -370,10 +373,10 @@ hyena_status hyena_recurrence_step(hyena_recurrence_t plan, const hyena_recurren
     if (n_slots > ((int64_t)1 << 31) - 1) return refuse("n_slots must be below 2^31");
     if (!aligned(slots, 4)) return refuse("slots is not aligned to its element");
     spans[4] = Span{slots, (size_t)p.B * 4};
-    const Span outs[2] = {{states, (size_t)n_slots * (size_t)p.heads * (size_t)p.dk * (size_t)p.dv * 4},
-                          {o, (size_t)(p.B * p.heads) * (size_t)p.dv * element_bytes(p.io_dtype)}};
-    const char* const names[2] = {"states", "o"};
-    if ((st = check_outputs(spans, 5, outs, names, 2)) != HYENA_OK) return st;
+    const Span outs[2] = {{o, (size_t)(p.B * p.heads) * (size_t)p.dv * element_bytes(p.io_dtype)},
+                          {states, (size_t)n_slots * (size_t)p.heads * (size_t)p.dk * (size_t)p.dv * 4}};
+    const char* const names[2] = {"o", "states"};
+    if ((st = check_outputs(spans, 5, outs, names, 2, 1)) != HYENA_OK) return st;
     return by_type(p.io_dtype, [&](auto t) {
         return run_step<decltype(t)>(p, *in, slots, n_slots, states, o, (hipStream_t)stream);
     });

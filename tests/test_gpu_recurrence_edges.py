@@ -294,3 +294,48 @@ def test_states_that_have_decayed_far(N, dtype):
     ds = c.backward()[4]
     grad = lambda x, y: mixer_ref.recurrence_grad(x, y, k, v, g, c.scale, state, n, df)[4]  # noqa: E731
     close(ds, grad(f64(c.do), q), SMALL * grad(np.abs(f64(c.do)), np.abs(q)), "d_state")
+
+
+# ------------------------------------------------------------- where outputs may lie
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("widths", [(5, 7), (16, 8)])
+def test_float32_outputs_and_tables_at_any_element(widths, dtype):
+    """States, their gradients and dg may start at any float32: a slice of a pool of states."""
+    import torch
+    dk, dv = widths
+    c = Case(1, 150, 1, dk, dv, dtype, seed=10)
+    o, last = c.forward()
+    pool = torch.full((2 + dk * dv,), 7.0, device="cuda")
+    mine = pool[1:1 + dk * dv].view(1, 1, dk, dv)
+    o2, last2 = c.forward(final_state=mine)
+    assert last2 is mine and torch.equal(o, o2) and torch.equal(last, mine)
+    assert pool[0] == 7.0 and pool[-1] == 7.0
+    # the backward pass through the C entry
+    want = c.backward()
+    view = lambda t: hyena.View(t.data_ptr(), *t.stride()[:3])  # noqa: E731
+    x = hyena.RecurrenceInputs(view(c.q), view(c.k), view(c.v), view(c.g), c.state.data_ptr(), None, c.scale)
+    got = [torch.empty_like(t) for t in want[:3]]
+    floats = torch.full((1 + 150 + 1 + dk * dv + 1,), 7.0, device="cuda")
+    dg, ds = floats[1:151], floats[152:152 + dk * dv]
+    assert dg.data_ptr() % 16 and ds.data_ptr() % 4 == 0
+    grads = hyena.RecurrenceGrads(*(t.data_ptr() for t in got), dg.data_ptr(), ds.data_ptr())
+    st = hyena.hyena_recurrence_backward(c.plan.handle, x, view(c.do), c.d_final.data_ptr(), grads,
+                                         c.plan.workspace.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == hyena.HYENA_OK
+    assert torch.equal(dg, want[3].flatten()) and torch.equal(ds, want[4].flatten())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert floats[0] == 7.0 and floats[151] == 7.0 and floats[-1] == 7.0
+    # one token on a table that is a slice of a pool
+    one = hyena.Recurrence(1, 1, 1, dk, dv, io_dtype=IO[dtype])
+    token = [t[:, 3] for t in (c.q, c.k, c.v, c.g)]
+    table = torch.randn((3, 1, dk, dv), device="cuda")
+    whole = torch.zeros(1 + 3 * dk * dv, device="cuda")
+    part = whole[1:].view(3, 1, dk, dv)
+    part.copy_(table)
+    slots = torch.tensor([2], dtype=torch.int32, device="cuda")
+    a, b = one.step(*token, table, slots=slots), one.step(*token, part, slots=slots)
+    # (rows may be read in another order)
+    close(b, f64(a), 2 * mixer_ref.HALF_STEP[dtype] * np.abs(f64(a)) + SMALL * np.abs(f64(table[2])).sum(1) * 20, "o")
+    assert torch.equal(part, table) and whole[0] == 0.0
