@@ -459,11 +459,11 @@ template <typename T, int W, bool GRAD> hyena_status qk_launch_w(QkArgs& a, hipS
     while (lanes < units && lanes < 64) lanes *= 2;
     a.lanes = lanes;
     const int per = (units + lanes - 1) / lanes;
+    constexpr int most = 1024 / (2 * W * 64);  // of the widest heads: 1, 2, 4, 8
     if (per <= 1) return qk_launch_one<T, W, 1, GRAD>(a, s);
-    if (per <= 2) return qk_launch_one<T, W, 2, GRAD>(a, s);
-    if constexpr (W == 2) return qk_launch_one<T, W, 4, GRAD>(a, s);
-    else if constexpr (W == 1) return qk_launch_one<T, W, 8, GRAD>(a, s);
-    else return fail(HYENA_ERR_UNSUPPORTED, "qk norm: head width");
+    if constexpr (most > 2)
+        if (per <= 2) return qk_launch_one<T, W, 2, GRAD>(a, s);
+    return qk_launch_one<T, W, most, GRAD>(a, s);
 }
 
 template <typename T, bool GRAD> hyena_status qk_launch(QkArgs& a, hipStream_t s)
