@@ -331,18 +331,18 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  * length.  Values are clamped to 0..N.
  *
  * Precision.  States, decays, their sums and every accumulation are float32
- * (sums of log decays: float64).  With 16-bit storage the scores between
- * tokens and, in bfloat16 for o and dv, the state are rounded to the storage
- * type as operands of the matrix products (relative error up to 2^-8 for
- * bfloat16, 2^-11 for binary16 scores, or 2^-25 absolutely where they are
- * subnormal), but with N <= 64 neither is.  The states, their gradients and the
- * gradient of g are computed from operands split so that they keep float32
- * accuracy (binary16: in each column, or row, of a state relative to its largest
- * element, 2^-36 of it at least).  The gradient of g at a token is a sum of terms
- * of that token and the later ones of its sequence; its accuracy is that of the sum
- * of their absolute values, so a decay much faster than all those after it has a
- * small gradient with an error of their size.  With binary16 the scores (times
- * decay and scale) have to stay within its range.
+ * (sums of log decays: float64), and only results are rounded to the storage
+ * type.  With 16-bit storage the matrix products take their float32 operands as
+ * sums of terms of that type: in bfloat16 the scores between tokens, and the state
+ * as it meets q (for o) and k (for dv), keep 16 bits; all other operands,
+ * those behind the states, their gradients and the gradient of g among them, keep
+ * float32 accuracy (binary16: 22 bits; of a score down to 2^-36 absolutely, of a
+ * state down to 2^-36 of the largest element in its column or row).  With binary16
+ * the scores (times decay and scale) have to stay within its range.  The gradient
+ * of g at a token is a sum of terms of that token and the later ones of its
+ * sequence; its accuracy is that of the sum of their absolute values, so a decay
+ * much faster than all those after it has a small gradient with an error of their
+ * size.
  *
  * Inputs within a row's length have to be finite (g may be -infinity): an infinity
  * or a NaN reaches its own and later tokens' results of its sequence (their

@@ -117,16 +117,25 @@ template <typename T, int NT> struct Split {
     }
 };
 
-// Four values as NT vectors in LDS, `apart` elements from each other, whose sum
-// (binary16: first + 2^-11 second) is the values, as above but rounded.
+// Four values as NT vectors whose sum (binary16: first + 2^-11 second) is the
+// values, as above but rounded; stored in LDS `apart` elements from each other.
+template <typename T, int NT> struct Split4 {
+    typename Mx<T>::vec4 y[NT];
+    __device__ __forceinline__ void set(f32x4 x)
+    {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            y[n] = Mx<T>::narrow(x);
+            if (n + 1 < NT) x = (x - Mx<T>::widen(y[n])) * (Mx<T>::kTerms == 2 ? 2048.0f : 1.0f);
+        }
+    }
+};
 template <typename T, int NT> __device__ __forceinline__ void store_split(T* to, int apart, f32x4 x)
 {
+    Split4<T, NT> s;
+    s.set(x);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const typename Mx<T>::vec4 y = Mx<T>::narrow(x);
-        *(typename Mx<T>::vec4*)(to + n * apart) = y;
-        if (n + 1 < NT) x = (x - Mx<T>::widen(y)) * (Mx<T>::kTerms == 2 ? 2048.0f : 1.0f);
-    }
+    for (int n = 0; n < NT; ++n) *(typename Mx<T>::vec4*)(to + n * apart) = s.y[n];
 }
 
 // c + a * s for a split operand (on either side: the tile's orientation is set

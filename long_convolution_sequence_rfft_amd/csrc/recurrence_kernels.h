@@ -67,8 +67,8 @@ __device__ __forceinline__ f32x4 unless_zero(f32x4 x, float factor)
     return factor != 0.0f ? x : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
-// out[16 i + l16] = sum over the four lanes of a column of x[i]
-template <int IT> __device__ __forceinline__ void store_token_sums(float* out, const float (&x)[IT], int lane, int grp)
+// *out(16 i + l16) = sum over the four lanes of a column of x[i]
+template <int IT, typename F> __device__ __forceinline__ void store_token_sums(F out, const float (&x)[IT], int lane, int grp)
 {
     float y = sum_rows(x[0]);
 #pragma unroll
@@ -76,7 +76,7 @@ template <int IT> __device__ __forceinline__ void store_token_sums(float* out, c
         const float z = sum_rows(x[i]);
         y = grp == i ? z : y;
     }
-    if (lane < 16 * IT) out[lane] = y;
+    if (lane < 16 * IT) *out(lane) = y;
 }
 
 // ---------------------------------------------------------------------------
@@ -188,27 +188,28 @@ __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states
     if (role == 0 && tid == 0) p.decay[bh * p.nseg + seg] = total;
 }
 
-// FINE: of 16-bit types the scores, too, are split operands, and no state is
-// rounded to one term, so that a result's own rounding is the only one.  In long
-// rows a result sums many scores and the others' roundings add as much as its
-// own; in rows of a few tokens they do not average out.
-template <typename T, bool FINE> constexpr int kScoreTerms = FINE && sizeof(T) == 2 ? 2 : 1;
+// Scores of 16-bit types are split operands of two terms, and no state is read as one,
+// so that a result's own rounding is the only one of 8 (binary16: 11) bits.  With
+// scores, and bfloat16 states, of one term a result's error was 1.4 times that, and
+// 65536 tokens of 12 heads of 64 took 93 instead of 105 us, 2 x 8192 of 6 heads of
+// 128 43.5 instead of 50; of 12 heads of 64 dq 41 instead of 44.5, dk and dv 65
+// instead of 71.5.
+template <typename T> constexpr int kScoreTerms = sizeof(T) == 2 ? 2 : 1;
 
 // LDS of the two kernels below.
-template <typename T, int DA, int DC, bool FINE> constexpr size_t rec_out_lds()
+template <typename T, int DA, int DC> constexpr size_t rec_out_lds()
 {
     constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
-    return sizeof(T) * (size_t)(C * LA + C * LB + 2 * DM * C + kScoreTerms<T, FINE> * C * LC) +
-           kDecayBatch * sizeof(DecaysOf<T>);
+    return sizeof(T) * (size_t)(C * LA + C * LB + 2 * DM * C + C * LC) + kDecayBatch * sizeof(DecaysOf<T>);
 }
 
 // Chunks whose terms of dg are held before they are summed up.
 constexpr int kGradHold = 16;
 
-template <typename T, int D, bool FINE> constexpr size_t rec_grad_lds()
+template <typename T, int D> constexpr size_t rec_grad_lds()
 {
     constexpr int C = kRecChunk<T>, LD = D + kPad<T>, LC = C + kPad<T>;
-    return sizeof(T) * (size_t)(4 * C * LD + 2 * D * C + 2 * kScoreTerms<T, FINE> * C * LC) + kDecayBatch * sizeof(DecaysOf<T>) +
+    return sizeof(T) * (size_t)(4 * C * LD + 2 * D * C + 2 * kScoreTerms<T> * C * LC) + kDecayBatch * sizeof(DecaysOf<T>) +
            sizeof(float) * (size_t)(2 * (C / 16) * C + 4 * C + kDecayBatch * C + kGradHold * C) + kGradHold * 16;
 }
 
@@ -224,7 +225,7 @@ template <typename T, int D, bool FINE> constexpr size_t rec_grad_lds()
 // 41 and 43.5).
 //
 // One workgroup of four waves per (row, head, segment).  Waves share the score
-// tiles of a chunk (written to LDS in storage type) and each owns every fourth
+// tiles of a chunk (written to LDS as terms of storage type) and each owns every fourth
 // 16-channel tile of c: its part of the state never leaves its registers.
 //
 // The outputs are bound by memory: 65536 tokens of 12 heads of 64 in bfloat16 in
@@ -233,27 +234,28 @@ template <typename T, int D, bool FINE> constexpr size_t rec_grad_lds()
 // 12 heads of 64: 42 us, 126 MB; 620 vector instructions per wave and chunk)
 // by the instructions of a chunk, with two or three waves per SIMD.
 // ---------------------------------------------------------------------------
-template <typename T, int DA, int DC, bool TRANS, bool VEC, bool FINE>
+template <typename T, int DA, int DC, bool TRANS, bool VEC>
 __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_rec_out(RecArgs p)
 {
     constexpr int C = kRecChunk<T>, DM = DA > DC ? DA : DC, LA = DA + kPad<T>, LB = DM + kPad<T>, LC = C + kPad<T>;
     constexpr int NT = Mx<T>::kTerms;  // state update
-    constexpr int NS = TRANS ? Mx<T>::kTerms : Mx<T>::kTerms < 2 ? 1 : Mx<T>::kTerms == 2 || FINE ? 2 : 1;  // state as an operand
-    constexpr int NP = kScoreTerms<T, FINE>;
+    constexpr int NS = TRANS || Mx<T>::kTerms < 2 ? Mx<T>::kTerms : 2;  // state as an operand
+    constexpr int NP = kScoreTerms<T>;
     constexpr int AT = DA / 16, CW = DC / 64, IT = C / 16;
     using frag = typename Mx<T>::frag;
     using vec4 = typename Mx<T>::vec4;
-    __shared__ __attribute__((aligned(16))) char smem[rec_out_lds<T, DA, DC, FINE>()];
+    __shared__ __attribute__((aligned(16))) char smem[rec_out_lds<T, DA, DC>()];
     T* ar = (T*)smem;              // [C][LA]
     T* br = ar + C * LA;           // [C][LB]
     T* bt = br + C * LB;           // [DM][C] transposed
     T* ct = bt + DM * C;           // [DM][C] transposed
-    T* ps = ct + DM * C;           // [C][LC]
-    DecaysOf<T>* const decays = (DecaysOf<T>*)(ps + NP * C * LC);
-    // [4][C], TRANS: over the first rows of b, read for the last time when it is
-    // written; the wave that reads it is the one that stores those rows again
-    float* part = (float*)br;
-    static_assert(4 * C * sizeof(float) <= 4 * 64 * (16 / sizeof(T)) / DM * LB * sizeof(T), "within wave 0's first rows");
+    T* ps = ct + DM * C;           // [C][LC] scores; their second terms over the rows of b, whose last use they are
+    constexpr int kApart = -(C * LB + 2 * DM * C);  // from ps to br
+    static_assert(LB >= LC, "second terms fit");
+    DecaysOf<T>* const decays = (DecaysOf<T>*)(ps + C * LC);
+    // [C][4], TRANS: a wave's sum of a token in the padding behind its scores
+    auto part = [&](int token) { return (float*)(ps + token * LC + C); };
+    static_assert(kPad<T> * sizeof(T) == 4 * sizeof(float), "a sum for each wave");
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -372,13 +374,20 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
                 const float w = p.scale * __builtin_amdgcn_exp2f((float)(li - lj[r]));
                 own[r] = in ? own[r] * w : 0.0f;
             }
+            Split4<T, NP> w[IT];
 #pragma unroll
-            for (int j = 0; j < IT - 1; ++j)
-                store_split<T, NP>(ps + ti * LC + 16 * j + 4 * grp, C * LC, s[j] * (cw[j] * within));
-            // the tile right of the last own one is not among the above; then the own tile itself
+            for (int j = 0; j < IT - 1; ++j) w[j].set(s[j] * (cw[j] * within));
+            w[IT - 1].set(own);
+            if constexpr (NP > 1) __syncthreads();  // the rows of b are done with
+            // the tile right of the last own one is not among the s; the own tile itself comes last
 #pragma unroll
-            for (int n = 0; n < NP; ++n) *(vec4*)(ps + n * C * LC + ti * LC + 16 * (IT - 1) + 4 * grp) = vec4{};
-            store_split<T, NP>(ps + ti * LC + to, C * LC, own);
+            for (int n = 0; n < NP; ++n) {
+                T* const row = ps + n * kApart + ti * LC;
+#pragma unroll
+                for (int j = 0; j < IT - 1; ++j) *(vec4*)(row + 16 * j + 4 * grp) = w[j].y[n];
+                *(vec4*)(row + 16 * (IT - 1) + 4 * grp) = vec4{};
+                *(vec4*)(row + to) = w[IT - 1].y[n];
+            }
         }
         __syncthreads();
 
@@ -417,7 +426,7 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
                 for (int j = 0; j <= i / 2; ++j) {
                     Split<T, NP> w;
 #pragma unroll
-                    for (int n = 0; n < NP; ++n) w.f[n] = frag_at<T>(ps + n * C * LC + ti * LC + 32 * j + 8 * grp);
+                    for (int n = 0; n < NP; ++n) w.f[n] = frag_at<T>(ps + n * kApart + ti * LC + 32 * j + 8 * grp);
                     o = mma_split<T, NP, false>(w, cf[j], o);
                 }
                 store_row4<T>(orows, orow + 16 * i * ostep, ti < left, 16 * vt + 4 * grp, p.dc, o);
@@ -440,12 +449,13 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
                                     [&](int j) { return cols_of(bt, k, j); });
             hold_schedule<(DA * DC > 64 * 64)>();
         }
-        if constexpr (TRANS) store_token_sums<IT>(part + wave * C, rdot, lane, grp);
+        if constexpr (TRANS) store_token_sums<IT>([&](int token) { return part(token) + wave; }, rdot, lane, grp);
         __syncthreads();
         if constexpr (TRANS) {
-            if (tid < C && tb0 + tid < t1)
-                p.rq[bh * p.N + tb0 + tid] = (part[tid] + part[C + tid]) + (part[2 * C + tid] + part[3 * C + tid]);
-            asm volatile("" ::: "memory");  // before this wave's next rows of b are stored there
+            if (tid < C && tb0 + tid < t1) {
+                const f32x4 y = *(const f32x4*)part(tid);
+                p.rq[bh * p.N + tb0 + tid] = (y[0] + y[1]) + (y[2] + y[3]);
+            }
         }
     }
     // rows of a padded batch past the length
@@ -492,17 +502,17 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
 // 66: not kept.  dk and dv are padded apart: with both at 128 heads of 40 and 72
 // in float16 took 69 us, now 41 (3 x 4100 tokens, 5 heads).
 // ---------------------------------------------------------------------------
-template <typename T, int DK, int DV, bool VEC, bool FINE>
+template <typename T, int DK, int DV, bool VEC>
 __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
 {
     constexpr int D = DK > DV ? DK : DV;
     constexpr int C = kRecChunk<T>, LD = D + kPad<T>, LC = C + kPad<T>;
     constexpr int NT = Mx<T>::kTerms;
-    constexpr int NP = kScoreTerms<T, FINE>;
+    constexpr int NP = kScoreTerms<T>;
     constexpr int IT = C / 16, kCells = (DK / 16) * (DV / 64);
     using frag = typename Mx<T>::frag;
     using vec4 = typename Mx<T>::vec4;
-    __shared__ __attribute__((aligned(16))) char smem[rec_grad_lds<T, D, FINE>()];
+    __shared__ __attribute__((aligned(16))) char smem[rec_grad_lds<T, D>()];
     T* qr = (T*)smem;              // [C][LD]
     T* kr = qr + C * LD;           // [C][LD]
     T* dr = kr + C * LD;           // [C][LD]
@@ -723,7 +733,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
             constexpr bool kSums = decltype(is_dk)::value;
             constexpr int kAcross = kSums ? DV : DK, MT = kAcross / 16, MW = (kSums ? DK : DV) / 64;
             const int l16 = D > 64 ? again(lane & 15) : lane & 15, grp = D > 64 ? again(lane >> 4) : lane >> 4;
-            constexpr int NS = kSums ? NT : NT < 2 ? 1 : NT == 2 || FINE ? 2 : 1;  // dS as an operand
+            constexpr int NS = kSums || NT < 2 ? NT : 2;  // dS as an operand
             const __amdgpu_buffer_rsrc_t orows = rows_at(out + tb0 * p.heads * width);
             const uint32_t ostep = (uint32_t)p.heads * (uint32_t)width * (uint32_t)sizeof(T);
             const uint32_t orow = (uint32_t)again(l16) * ostep;
@@ -778,7 +788,7 @@ __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)
                     S[m * MW + n] = update<T>(S[m * MW + n], all, up, y, [&](int i) { return cols_of(add, m, i); });
                 hold_schedule<(DK * DV > 64 * 64)>();
             }
-            if constexpr (kSums) store_token_sums<IT>(part + w4 * C, kdot, lane, grp);
+            if constexpr (kSums) store_token_sums<IT>([&](int token) { return part + w4 * C + token; }, kdot, lane, grp);
         };
         if (own_k) work(std::true_type{}, vr, pd, qt, dt, kout);
         else work(std::false_type{}, kr, pa, dt, qt, vout);

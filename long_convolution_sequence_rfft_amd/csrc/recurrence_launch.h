@@ -36,29 +36,19 @@ template <typename T> hyena_status rec_launch_states(const RecStateArgs& a, int6
     return a.dv <= 64 ? rec_states_one<T, 128, 64>(a, bh, roles, s) : rec_states_one<T, 128, 128>(a, bh, roles, s);
 }
 
-// Rows of few tokens take the FINE forms: rows of one chunk (there an error may not
-// average out), however many there are, so that a row's results do not depend on
-// the others in its batch.  12 rows and heads of 64 tokens, the other forms and these:
-// heads of 64 in bfloat16 forward 7.7 and 7.8 us, backward 16.8 and 18.2; of 128
-// 10.1 and 12.1, 29.8 and 33.7.  6144 of them: 48 and 76, 250 and 294; 140 and
-// 285, 699 and 865.
-inline bool fine_rows(int64_t N) { return N <= 64; }
-
-template <typename T, int DA, int DC, bool TRANS, bool VEC, bool FINE>
+template <typename T, int DA, int DC, bool TRANS, bool VEC>
 hyena_status rec_out_as(const RecArgs& a, int64_t bh, hipStream_t s)
 {
-    HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, VEC, FINE),
-              (hyena_rec_out<T, DA, DC, TRANS, VEC, FINE>), dim3((unsigned)(bh * a.nseg)), dim3(256), 0, s, a);
+    HY_LAUNCH(kernel_label("hyena_rec_out", type_label<T>(), DA, DC, TRANS, VEC),
+              (hyena_rec_out<T, DA, DC, TRANS, VEC>), dim3((unsigned)(bh * a.nseg)), dim3(256), 0, s, a);
     return rec_done();
 }
 
 template <typename T, int DA, int DC, bool TRANS>
 hyena_status rec_out_one(const RecArgs& a, int64_t bh, hipStream_t s)
 {
-    if constexpr (sizeof(T) == 2)
-        if (fine_rows(a.N)) return rec_out_as<T, DA, DC, TRANS, false, true>(a, bh, s);
     const bool vec = by_vectors(a.a, a.b, a.c) && (!TRANS || by_vectors(a.r));
-    return vec ? rec_out_as<T, DA, DC, TRANS, true, false>(a, bh, s) : rec_out_as<T, DA, DC, TRANS, false, false>(a, bh, s);
+    return vec ? rec_out_as<T, DA, DC, TRANS, true>(a, bh, s) : rec_out_as<T, DA, DC, TRANS, false>(a, bh, s);
 }
 
 template <typename T, bool TRANS> hyena_status rec_out_pick(const RecArgs& a, int64_t bh, hipStream_t s)
@@ -73,20 +63,17 @@ template <typename T> hyena_status rec_launch_out(const RecArgs& a, int64_t bh, 
     return transposed ? rec_out_pick<T, true>(a, bh, s) : rec_out_pick<T, false>(a, bh, s);
 }
 
-template <typename T, int DK, int DV, bool VEC, bool FINE>
+template <typename T, int DK, int DV, bool VEC>
 hyena_status rec_grad_as(const RecGradArgs& a, int64_t bh, hipStream_t s)
 {
-    HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), DK, DV, VEC, FINE), (hyena_rec_grad<T, DK, DV, VEC, FINE>),
+    HY_LAUNCH(kernel_label("hyena_rec_grad", type_label<T>(), DK, DV, VEC), (hyena_rec_grad<T, DK, DV, VEC>),
               dim3((unsigned)(bh * a.nseg)), dim3(512), 0, s, a);
     return rec_done();
 }
 
 template <typename T, int DK, int DV> hyena_status rec_grad_one(const RecGradArgs& a, int64_t bh, hipStream_t s)
 {
-    if constexpr (sizeof(T) == 2)
-        if (fine_rows(a.N)) return rec_grad_as<T, DK, DV, false, true>(a, bh, s);
-    return by_vectors(a.q, a.k, a.v, a.o) ? rec_grad_as<T, DK, DV, true, false>(a, bh, s)
-                                          : rec_grad_as<T, DK, DV, false, false>(a, bh, s);
+    return by_vectors(a.q, a.k, a.v, a.o) ? rec_grad_as<T, DK, DV, true>(a, bh, s) : rec_grad_as<T, DK, DV, false>(a, bh, s);
 }
 
 template <typename T> hyena_status rec_launch_grad(const RecGradArgs& a, int64_t bh, hipStream_t s)

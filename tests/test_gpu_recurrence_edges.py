@@ -228,6 +228,26 @@ def test_states_are_held_in_32_bits(H, dtype):
         close(got, ref, 2 * u * np.abs(ref) + 2.0 ** -19 + (2.0 ** -25 if dtype == "f16" else 0.0), f"reverse={reverse}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(2, 65, 2, 64, 64), (1, 200, 3, 128, 128), (2, 330, 2, 40, 72), (1, 300, 2, 128, 64),
+                                   (1, 900, 2, 64, 128), (1, 140, 300, 7, 5)])
+@pytest.mark.parametrize("decay", [0.5, 0.01])
+def test_rows_of_any_length_round_only_their_results(shape, decay, dtype):
+    """No score and no state is rounded to 16 bits on the way: half a step of the value, and 2^-15 of the
+    sum of absolute values (float32's 2^-15 less what its sums really lose leaves 2^-16 for scores and bfloat16
+    states of two terms)."""
+    c = Case(*shape, dtype, seed=sum(shape) + 4, decay=decay, resets=((70, -np.inf),))
+    (q, k, v, g), state, n, df = c.inputs64()
+    u, do = mixer_ref.HALF_STEP[dtype], f64(c.do)
+    least = 2.0 ** -25 if dtype == "f16" else 0.0  # half a step of the smallest float16 results
+    ro, _, ao, _ = mixer_ref.recurrence(q, k, v, g, c.scale, state, n)
+    close(c.forward()[0], ro, u * np.abs(ro) + SMALL * ao + least, "o")
+    ref = mixer_ref.recurrence_grad(do, q, k, v, g, c.scale, state, n, df)
+    size = mixer_ref.recurrence_grad(*(np.abs(x) for x in (do, q, k, v)), g, c.scale, np.abs(state), n, np.abs(df))
+    for got, r, a, what in zip(c.backward()[:3], ref, size, ("dq", "dk", "dv")):
+        close(got, r, u * np.abs(r) + SMALL * a + least, what)
+
+
 # ------------------------------------------------------------- magnitudes
 
 @pytest.mark.parametrize("N", [50, 200])
