@@ -310,14 +310,16 @@ hyena_status hyena_spectrum_export(hyena_plan_t plan, const void* H, void* natur
  * Gated linear recurrence: a mixer of q, k and v like the HyenaND mixer, with
  * a matrix state per head in place of the convolution ("Week 11: Hyena, Long
  * Convolution, and Linear Attention": linear attention, retention and the
- * gated form are its cases g = 0, g fixed per head, g from the data).
+ * gated form with one decay per token and head are its cases g = 0, g fixed per
+ * head, g from the data; decays per channel are not).
  *
  *   S_t = exp(g_t) S_{t-1} + k_t v_t^T        (dk x dv, float32)
  *   o_t = scale * S_t^T q_t                   t = 1..length, S_0 = state or 0
  *
  * g_t <= 0 is one log decay per token and head.  g_t = -infinity starts a new
- * sequence inside a row (nothing before it is seen), and so does any g_t below
- * -87.34 (its exp is below the smallest normal float32).
+ * sequence inside a row (nothing before it is seen, whatever an initial state
+ * holds), and so does any g_t below -87.34 (its exp is below the smallest normal
+ * float32).
  *
  * Layouts: q, k [B][N][heads][dk] and v [B][N][heads][dv] in the plan's io
  * dtype, g float32 [B][N][heads], each given as a strided view (below);
@@ -448,7 +450,8 @@ hyena_status hyena_recurrence_destroy(hyena_recurrence_t plan);
  * as they are.  freqs is a float64 table on the device, so a long context's
  * scaling is in the caller's frequencies; angles are float64, reduced before
  * their sine and cosine are taken in float32, sums and norms float32 (sums of
- * the weights' gradients: float64 between workgroups).
+ * the weights' gradients: float64 between workgroups).  A head without a norm has
+ * no result: zeros with eps = 0 (NaN), or squares that sum to more than float32 holds.
  *
  * position of token n in row b: positions[b * N + n] (int32 on the device) or,
  * with positions = NULL, position_offset + n.

@@ -681,6 +681,7 @@ class Recurrence(_Mixer):
     axis of q, k and v is contiguous.  States are float32 [B, heads, dk, dv].
     ``training`` allocates the backward pass's workspace.  Calls of one plan
     share its workspace and must not run concurrently on different streams.
+    Outputs carry no autograd history: ``backward`` is called by the caller.
     """
 
     def __init__(self, B, N, heads, dk, dv, io_dtype=HYENA_F32, training=False, device="cuda"):
@@ -788,7 +789,7 @@ class QKNorm(_Mixer):
     ``rotary_dim`` channels are rotated (D by default, 0: none), pairs (i, i + rotary_dim / 2)
     in the "half" layout and (2i, 2i + 1) in the "interleaved" one, by position * freqs[i]
     (float64, by default ``rotary_frequencies(rotary_dim)``); sines and cosines are multiplied
-    by ``rotary_scale``.
+    by ``rotary_scale``.  Outputs carry no autograd history: ``backward`` is called by the caller.
     """
 
     _NORMS = {"none": HYENA_NORM_NONE, "rms": HYENA_NORM_RMS, "l2": HYENA_NORM_L2}

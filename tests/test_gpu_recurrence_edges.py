@@ -140,6 +140,21 @@ def test_infinities_stay_near_their_sequence(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(2, 50, 2, 64, 64), (1, 470, 2, 40, 72), (1, 300, 200, 8, 8)])
+def test_a_state_in_front_of_a_start_is_not_seen(shape, dtype):
+    """A row that begins with a new sequence: an initial state of NaN gives the bits of one of zeros."""
+    import torch
+    c = Case(*shape, dtype, seed=32)
+    c.g[:, 0] = -np.inf
+    c.state.zero_()
+    want = [*c.forward(), *c.backward()]
+    c.state.fill_(float("nan"))
+    got = [*c.forward(), *c.backward()]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert not got[-1].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("dv", [64, 7])
 def test_step_starts_a_sequence_over_whatever_the_slot_held(dv, dtype):
     """g = -infinity, and any below -87.34, leaves nothing of a state: the bits of a state of zeros."""
