@@ -18,8 +18,8 @@
 // row of a transposed tile is 128 bytes.  Two passes over k and v, one for the
 // segments' states and one for the outputs, are the price of walking a long
 // sequence in parallel: at 65536 tokens of 12 heads of 64 in bfloat16 the three
-// kernels take 148 us for 604 MB (403 without the first pass), 4.1 TB/s, where
-// a large copy reaches 5.1.
+// kernels take 165 to 175 us for 663 MB (403 without the first pass and the
+// states), 4 TB/s, where a large copy reaches 5.1.
 #pragma once
 
 #include <type_traits>
@@ -38,9 +38,12 @@ __device__ __forceinline__ const T* row_base(const RView& v, int64_t b, int64_t 
 template <typename T> using DecaysOf = Decays<kRecChunk<T>>;
 
 // Waves per SIMD that the registers leave room for: with 64 x 64 states three,
-// with 128 x 128 ones and binary16's second accumulators one (with two, 88
-// spilled registers: 8192 tokens of 8 heads forward 91 us, backward 217, with one
-// 87 and 197; 128 x 64 with two 42 and 112, with one 57 and 113).
+// with 128 x 128 ones and binary16's second accumulators one (with two, 112 to 136
+// spilled registers: 8192 tokens of 8 heads forward 102 us, backward 242, with one
+// 98 and 216; 128 x 64 with two 45 and 124, with one 62 and 126).  Two leave some
+// spilled still: at 128 x 128 18 in bfloat16's outputs and 45 in its dq, 19 and 16 in
+// float32's; 32 in binary16's dq with heads of 128 keys and 64 values; in dk and dv
+// (eight waves, 128 x 128) 53, 8 and 85 in bfloat16, float32 and binary16.
 constexpr int rec_waves(int d0, int d1, bool light) { return d0 * d1 <= 64 * 64 && light ? 3 : 2; }
 template <typename T> constexpr int rec_out_waves(int d0, int d1, bool trans)
 {
@@ -81,9 +84,9 @@ template <int IT, typename F> __device__ __forceinline__ void store_token_sums(F
 
 // ---------------------------------------------------------------------------
 // Local states of the segments.  One workgroup per (row, head, segment, role);
-// wave w owns every fourth 16-column tile of the state.  Bound by memory: 54 us
-// at 65536 tokens of 12 heads of 64 in bfloat16 (201 MB, 4.0 TB/s without the
-// 4 us that any launch takes), 32 us with both roles at 2 x 8192 (100 MB).
+// wave w owns every fourth 16-column tile of the state.  Bound by memory: 53 us
+// at 65536 tokens of 12 heads of 64 in bfloat16 (217 MB, 4.4 TB/s without the
+// 4 us that any launch takes), 31 us with both roles at 2 x 8192 (118 MB).
 // ---------------------------------------------------------------------------
 template <typename T, int DK, int DV, bool VEC>
 __global__ __launch_bounds__(256, rec_waves(DK, DV, true)) void hyena_rec_states(RecStateArgs p)
@@ -228,11 +231,14 @@ template <typename T, int D> constexpr size_t rec_grad_lds()
 // tiles of a chunk (written to LDS as terms of storage type) and each owns every fourth
 // 16-channel tile of c: its part of the state never leaves its registers.
 //
-// The outputs are bound by memory: 65536 tokens of 12 heads of 64 in bfloat16 in
-// 91 us (403 MB, 4.6 TB/s without the launch); with heads of 128 (2 x 8192
-// tokens of 6, 41 us, 126 MB) and with split operands (dq at 2 x 8192 tokens of
-// 12 heads of 64: 42 us, 126 MB; 620 vector instructions per wave and chunk)
-// by the instructions of a chunk, with two or three waves per SIMD.
+// Bound by the instructions of a chunk and the LDS beside memory: 65536 tokens of 12
+// heads of 64 in bfloat16 in 105 to 112 us (420 MB, 4 TB/s without the launch; vector
+// units busy for 62% of the time, the LDS for 61%, 39% of that bank conflicts,
+// matrix units for 27%, three waves per SIMD); with two waves per SIMD 2 x 8192
+// tokens of 6 heads of 128 in 48 us (134 MB; 35%, 36%, 22%) and dq of 12 heads of 64
+// in 45 us (137 MB; 48%, 36%, 18%; 720 vector instructions per wave and chunk).  In
+// float32 matrix instructions bound it: dq of 4 x 2048 tokens in 47 us, matrix units
+// 57%.
 // ---------------------------------------------------------------------------
 template <typename T, int DA, int DC, bool TRANS, bool VEC>
 __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_rec_out(RecArgs p)
@@ -493,14 +499,16 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
 // float64 by all waves.  Over a whole sequence the sum is zero, so at a reset it
 // starts anew: a sequence's dg holds no rounding of those after it.
 //
-// Bound by a chunk's instructions: 66 us at 2 x 8192 tokens of 12 heads of 64 in
-// bfloat16 (176 MB), 80 us at 4 x 2048 in float32; 610 vector instructions per
-// wave and chunk keep the vector units busy for half the time, LDS accesses the
-// LDS for 40%, matrix products the matrix units for 17%.  Two workgroups per
-// compute unit, with 128 registers and 81 KB of LDS each, came to 64 us, two
-// chunks in LDS with the next one's scores made beside this one's gradients to
-// 66: not kept.  dk and dv are padded apart: with both at 128 heads of 40 and 72
-// in float16 took 69 us, now 41 (3 x 4100 tokens, 5 heads).
+// Bound by a chunk's instructions and the waits between them, with two waves per
+// SIMD: 72 to 76 us at 2 x 8192 tokens of 12 heads of 64 in bfloat16 (166 MB), 82 us at
+// 4 x 2048 in float32.  In bfloat16 660 vector instructions per wave and chunk keep
+// the vector units busy for 45% of the time, the LDS is for 35% (41% of that bank
+// conflicts), the matrix units for 16%; in float32 20%, 18% and 46%.  With scores of
+// one term, where it took 66 us, two workgroups per compute unit, with 128 registers and
+// 81 KB of LDS each, came to 64, two chunks in LDS with the next one's scores made
+// beside this one's gradients to 66: not kept.  dk and dv are padded apart: with both
+// at 128 heads of 40 and 72 in float16 (3 x 4100 tokens, 5 heads) took 69 us, then
+// 41, now 44.
 // ---------------------------------------------------------------------------
 template <typename T, int DK, int DV, bool VEC>
 __global__ __launch_bounds__(512) void hyena_rec_grad(RecGradArgs p)

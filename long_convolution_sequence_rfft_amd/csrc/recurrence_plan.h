@@ -13,13 +13,13 @@ namespace hy {
 // resident together.  More segments mean more states to write, scan and read,
 // fewer leave compute units empty.  Measured, all kernels of a call repeated on
 // the same inputs:
-// forward, 64K tokens, 12 heads of 64, bfloat16: 183, 155, 136, 133, 149 us at
-// 256, 384, 512, 768, 1024; 2 x 8K tokens, 6 heads of 128: 76, 74, 67, 71, 82
+// forward, 64K tokens, 12 heads of 64, bfloat16: 220, 183, 156, 141, 161 us at
+// 256, 384, 512, 768, 1024; 2 x 8K tokens, 6 heads of 128: 89, 84, 74, 77, 87
 // at 192, 256, 384, 512, 768;
 // backward, 2 x 8K tokens, 12 heads of 64, its dk and dv in 256 and its states
-// and dq in 256, 512, 768: 134, 126, 129; all in 384 and 512: 145, 138.
-// 4 x 2K tokens in float32: 151, 146, 151; 160, 160.  3 x 4100 tokens, 5 heads
-// of 40 and 72, float16: 86, 85, 86; 90, 95.
+// and dq in 256, 512, 768: 148, 137, 140; all in 384 and 512: 157, 150.
+// 4 x 2K tokens in float32: 155, 150, 155; 165, 164.  3 x 4100 tokens, 5 heads
+// of 40 and 72, float16: 92, 92, 92; 90, 92.
 constexpr int64_t kRecForwardGroups = 768;
 constexpr int64_t kRecWideGroups = 384;  // forward, dk or dv above 64
 constexpr int64_t kRecBackwardGroups = 256;
