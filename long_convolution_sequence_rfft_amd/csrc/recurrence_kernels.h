@@ -235,10 +235,10 @@ template <typename T, int D> constexpr size_t rec_grad_lds()
 // heads of 64 in bfloat16 in 105 to 112 us (420 MB, 4 TB/s without the launch; vector
 // units busy for 62% of the time, the LDS for 61%, 39% of that bank conflicts,
 // matrix units for 27%, three waves per SIMD); with two waves per SIMD 2 x 8192
-// tokens of 6 heads of 128 in 48 us (134 MB; 35%, 36%, 22%) and dq of 12 heads of 64
-// in 45 us (137 MB; 48%, 36%, 18%; 720 vector instructions per wave and chunk).  In
+// tokens of 6 heads of 128 in 48 us (134 MB; 36%, 36%, 22%) and dq of 12 heads of 64
+// in 45 us (137 MB; 45%, 34%, 17%; 720 vector instructions per wave and chunk).  In
 // float32 matrix instructions bound it: dq of 4 x 2048 tokens in 47 us, matrix units
-// 57%.
+// 54%.
 // ---------------------------------------------------------------------------
 template <typename T, int DA, int DC, bool TRANS, bool VEC>
 __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_rec_out(RecArgs p)
@@ -503,7 +503,7 @@ __global__ __launch_bounds__(256, rec_out_waves<T>(DA, DC, TRANS)) void hyena_re
 // SIMD: 72 to 76 us at 2 x 8192 tokens of 12 heads of 64 in bfloat16 (166 MB), 82 us at
 // 4 x 2048 in float32.  In bfloat16 660 vector instructions per wave and chunk keep
 // the vector units busy for 45% of the time, the LDS is for 35% (41% of that bank
-// conflicts), the matrix units for 16%; in float32 20%, 18% and 46%.  With scores of
+// conflicts), the matrix units for 16%; in float32 20%, 19% and 46%.  With scores of
 // one term, where it took 66 us, two workgroups per compute unit, with 128 registers and
 // 81 KB of LDS each, came to 64, two chunks in LDS with the next one's scores made
 // beside this one's gradients to 66: not kept.  dk and dv are padded apart: with both
