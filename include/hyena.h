@@ -498,6 +498,162 @@ hyena_status hyena_qk_norm_backward(const hyena_qk_norm* op, const hyena_view* d
                                     void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * What stands at a model's ends and between its layers: tokens to rows of a
+ * table and back, the norm of whole tokens with the residual's addition, and the
+ * loss over the vocabulary.  None of them allocates, uses atomics on floating-point
+ * values or keeps anything between calls: the same call gives the same bits, and
+ * calls that do not share a scratch buffer may run at once.  A scratch needs no
+ * initialisation, is 16-byte aligned and must not be shared by calls that run
+ * concurrently; a size may be 0 (the scratch may then be NULL).
+ */
+
+/* A tensor [B][N][width], or [B][N] (width 1), seen through strides in elements;
+ * the last axis is contiguous.  A stride of 0 shares one row among tokens or
+ * batch rows.  data is aligned to its element. */
+typedef struct hyena_rows {
+    const void* data;
+    int64_t batch, token;
+} hyena_rows;
+
+/*
+ * Embedding: out[b][n] = scale * table[tokens[b][n]], rounded once, and the
+ * table's gradient d_table[v] = scale * sum of d_out[b][n] over the tokens that
+ * are v, summed in float32 in the tokens' order and rounded once.  A token
+ * outside 0..V-1 takes no part: its row of out is zeros, its row of d_out is not
+ * read.
+ *
+ * table, out and d_table are dense, [V][d] and [B][N][d], in the io dtype, aligned
+ * to their element.  B * N at most 2^30, V at most 2^24, d at most 65536.
+ */
+typedef struct hyena_embedding {
+    int64_t B, N;
+    int64_t V, d;
+    int32_t io_dtype;
+    float scale;
+    hyena_rows tokens; /* int32 */
+} hyena_embedding;
+
+/* out must not overlap the table or the tokens. */
+hyena_status hyena_embedding_forward(const hyena_embedding* op, const void* table, void* out,
+                                     void* stream);
+
+/* Scratch bytes of hyena_embedding_backward. */
+hyena_status hyena_embedding_scratch_bytes(const hyena_embedding* op, size_t* bytes);
+
+/* accumulate 0: every row of d_table is written, zeros where no token is.  1: the
+ * sums are added to what d_table holds (once more rounded), the other rows are
+ * neither read nor written; so the gradient of a table that is also the loss's is
+ * made in one place.  d_table must not overlap an input or the scratch. */
+hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_rows* d_out,
+                                      void* d_table, int32_t accumulate, void* scratch,
+                                      void* stream);
+
+/*
+ * RMS norm of whole tokens with the residual's addition:
+ *
+ *   s = x + residual,   y = weight * s / sqrt(mean(s^2) + eps)
+ *
+ * Sums and norms are float32; y is made from the sum before its rounding.  y is in
+ * the io dtype or (HYENA_NORM_E4M3, HYENA_NORM_INT8) in 8 bits with a float32 scale
+ * for each group of channels: scale = max|y| / 448 or / 127 over the group, and y
+ * stands for value * scale, rounded to nearest even.  A group is 32, 64 or 128
+ * channels (d a multiple of it), or a whole row (group 0).  E4M3 is the form with
+ * 448 as its largest value and no infinities.  A group whose largest is below
+ * 2^-100 is zeros with the scale 0; one that holds a NaN has a NaN scale.
+ *
+ * s (if there is a residual) and y are dense [B][N][d], scales [B][N][d / group]
+ * (group 0: [B][N][1]).  d at most 16384, B * N at most 2^31 - 1.
+ */
+#define HYENA_NORM_IO 0
+#define HYENA_NORM_E4M3 1
+#define HYENA_NORM_INT8 2
+
+typedef struct hyena_residual_norm {
+    int64_t B, N, d;
+    int32_t io_dtype;
+    int32_t format;       /* HYENA_NORM_IO, _E4M3, _INT8: of y */
+    int64_t group;        /* 0, 32, 64 or 128; 0 with HYENA_NORM_IO */
+    float eps;            /* >= 0 */
+    const float* weight;  /* [d], or NULL for ones */
+    hyena_rows x;
+    hyena_rows residual;  /* data NULL: none */
+} hyena_residual_norm;
+
+/* sum (io dtype): NULL without a residual; it may be x's or the residual's own
+ * memory where that is dense.  y: io dtype or bytes; scales: NULL with
+ * HYENA_NORM_IO.  Otherwise outputs must not overlap an input or each other. */
+hyena_status hyena_residual_norm_forward(const hyena_residual_norm* op, void* sum, void* y,
+                                         float* scales, void* stream);
+
+/* Scratch bytes of hyena_residual_norm_backward. */
+hyena_status hyena_residual_norm_scratch_bytes(const hyena_residual_norm* op, size_t* bytes);
+
+/* Backward pass.  op->x is the forward pass's sum (x itself without a residual);
+ * op->residual, format and group are ignored.  d_y: gradient of y; d_sum: gradient
+ * that reaches the sum from elsewhere, or NULL.  d_x (io dtype, dense) is the
+ * gradient of the sum, which is that of x and of the residual alike:
+ *   n = s r, r = 1 / sqrt(mean(s^2) + eps),  d_n = weight d_y
+ *   d_x = d_sum + r (d_n - n mean(d_n n)),   d_weight = sum over tokens of d_y n
+ * d_weight: float32 [d], or NULL (then no scratch is needed).  d_x may be d_sum's own memory where
+ * that is dense; otherwise outputs must not overlap an input or each other. */
+hyena_status hyena_residual_norm_backward(const hyena_residual_norm* op, const hyena_rows* d_y,
+                                          const hyena_rows* d_sum, void* d_x, float* d_weight,
+                                          void* scratch, void* stream);
+
+/*
+ * Softmax cross entropy over a vocabulary, from the rows x and the table whose
+ * products are the logits, which are never kept:
+ *
+ *   l[t][v] = scale * <x[t], table[v]>,  lse[t] = log(sum over v of exp(l[t][v]))
+ *   loss[t] = lse[t] - l[t][target[t]]
+ *   G[t][v] = d_loss[t] (exp(l[t][v] - lse[t]) - [v = target[t]])
+ *   d_x[t] = scale * sum over v of G[t][v] table[v]
+ *   d_table[v] = scale * sum over t of G[t][v] x[t]
+ *
+ * A token whose target is outside 0..V-1 takes no part: its loss, lse and d_x are
+ * zeros, nothing of it reaches d_table, and its rows of x and d_loss are not read.
+ * Such tokens cost nothing: the rows of the others are gathered first.
+ *
+ * Precision.  Products of 16-bit operands are accumulated in float32, in float32
+ * storage each operand is three bfloat16 terms (24 bits) and the six largest of their
+ * nine products are summed; lse and loss are float32.  With 16-bit storage the
+ * gradients pass through G rounded to that type; in binary16 G is divided by the
+ * largest |d_loss| first and kept times 2^15, so that probabilities down to
+ * 2^-29 keep all its bits.  In float32 storage x, table and scale must be such that the logits and
+ * all values are finite; elsewhere too an infinity or a NaN in the table reaches
+ * every token, one in x its own token and d_table.
+ *
+ * The table is dense [V][d] and 16-byte aligned, as are d_x ([B][N][d]) and
+ * d_table ([V][d]), all in the io dtype.  x, targets and d_loss are views.  d and V
+ * and B * N at least 1; d at most 16384, V at most 2^22, B * N at most 2^22.
+ */
+typedef struct hyena_token_loss {
+    int64_t B, N;
+    int64_t V, d;
+    int32_t io_dtype;
+    float scale;
+    hyena_rows x;       /* io dtype */
+    const void* table;
+    hyena_rows targets; /* int32 */
+} hyena_token_loss;
+
+/* Scratch bytes of the two passes (either output pointer may be NULL). */
+hyena_status hyena_token_loss_scratch_bytes(const hyena_token_loss* op, size_t* forward_bytes,
+                                            size_t* backward_bytes);
+
+/* loss, lse: float32 [B][N].  Outputs must not overlap an input, each other or the
+ * scratch. */
+hyena_status hyena_token_loss_forward(const hyena_token_loss* op, float* loss, float* lse,
+                                      void* scratch, void* stream);
+
+/* d_loss: float32 view; lse: float32 [B][N] of the forward pass.  d_x or d_table
+ * may be NULL (not wanted). */
+hyena_status hyena_token_loss_backward(const hyena_token_loss* op, const hyena_rows* d_loss,
+                                       const float* lse, void* d_x, void* d_table, void* scratch,
+                                       void* stream);
+
+/*
  * Launch timing, a profiling aid that computes nothing.  After
  * hyena_timing_begin(max_launches), every kernel that a hyena_* call made on
  * this host thread enqueues is bracketed by two HIP timing events recorded on

@@ -22,7 +22,9 @@ SOURCES = ["api.hip", "lds1d.hip", "lds1d_f32.hip", "lds1d_bf16.hip", "lds1d_f16
            "multipass_inner.hip", "multipass_mid.hip",
            "implicit.hip", "timing.hip", "static_scratch.hip", "plan.cpp",
            "recurrence.hip", "recurrence_f32.hip", "recurrence_bf16.hip", "recurrence_f16.hip",
-           "recurrence_plan.cpp", "qk_norm.hip"]
+           "recurrence_plan.cpp", "qk_norm.hip", "residual_norm.hip", "residual_norm_f32.hip",
+           "residual_norm_bf16.hip", "residual_norm_f16.hip", "embedding.hip",
+           "token_loss.hip", "token_loss_f32.hip", "token_loss_bf16.hip", "token_loss_f16.hip"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

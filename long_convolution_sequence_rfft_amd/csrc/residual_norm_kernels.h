@@ -1,0 +1,322 @@
+// residual_norm_kernels.h -- RMS norm of whole tokens with the residual's
+// addition, and its backward pass (include/hyena.h).
+//
+// Forward, for a row of d channels with s = x + residual:
+//   r = 1 / sqrt(mean(s^2) + eps),  y = w r s,
+// or y in 8 bits, value = round(y / a), a = max|y| of a group / the largest value.
+// Backward, with n = r s and dn = w dy:
+//   dx = ds + r (dn - n mean(dn n)),  dw = sum over rows of dy n.
+//
+// Bound by memory: each tensor is read or written once.  A row stays in the
+// registers of the team of lanes that holds it; teams go through the rows in
+// steps, so that the weights, and backward the sums for their gradient, are
+// loaded (stored) once for each team and not for each row.
+#pragma once
+
+#include "residual_norm.h"
+
+namespace hy {
+
+// Sum over a team's lanes.
+template <bool WG> __device__ __forceinline__ void team_sum(float& a, float& b, bool two, int lanes, float* lds)
+{
+    const int within = WG ? 64 : lanes;
+    for (int m = 1; m < within; m *= 2) {
+        a += __shfl_xor(a, m);
+        if (two) b += __shfl_xor(b, m);
+    }
+    if constexpr (WG) {
+        const int wave = threadIdx.x >> 6, waves = lanes >> 6;
+        __syncthreads();  // the last row's sums have been read
+        if ((threadIdx.x & 63) == 0) {
+            lds[wave] = a;
+            if (two) lds[16 + wave] = b;
+        }
+        __syncthreads();
+        a = 0.0f;
+        for (int w = 0; w < waves; ++w) a += lds[w];
+        if (two) {
+            b = 0.0f;
+            for (int w = 0; w < waves; ++w) b += lds[16 + w];
+        }
+    }
+}
+
+// Largest of the bits of absolute values: a NaN is above everything.
+template <bool WG> __device__ __forceinline__ uint32_t team_max(uint32_t a, int lanes, float* lds)
+{
+    const int within = WG ? 64 : lanes;
+    for (int m = 1; m < within; m *= 2) a = max(a, (uint32_t)__shfl_xor((int)a, m));
+    if constexpr (WG) {
+        const int wave = threadIdx.x >> 6, waves = lanes >> 6;
+        __syncthreads();  // the sums have been read
+        if ((threadIdx.x & 63) == 0) lds[wave] = __uint_as_float(a);
+        __syncthreads();
+        a = 0;
+        for (int w = 0; w < waves; ++w) a = max(a, __float_as_uint(lds[w]));
+        __syncthreads();
+    }
+    return a;
+}
+
+__device__ __forceinline__ float rms(float squares, int d, float eps) { return 1.0f / sqrtf(squares / (float)d + eps); }
+
+// K units of 8-bit values, K = 4 or 8.
+template <int K> __device__ __forceinline__ void pack8(const float (&y)[K], bool int8, uint32_t (&w)[K / 4])
+{
+#pragma unroll
+    for (int i = 0; i < K; i += 4) {
+        if (int8) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v |= ((uint32_t)(int)rintf(fminf(fmaxf(y[i + j], -127.0f), 127.0f)) & 255u) << (8 * j);
+            w[i / 4] = v;
+        } else {
+            int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[i], y[i + 1], 0, false);
+            w[i / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[i + 2], y[i + 3], v, true);
+        }
+    }
+}
+
+template <typename T, bool VEC, bool WG, int U, bool EIGHT>
+__global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm(NormArgs p)
+{
+    constexpr int K = kUnit<T>;
+    __shared__ float lds[32];
+    const int lanes = WG ? (int)blockDim.x : p.lanes;
+    const int teams = WG ? 1 : 256 / lanes, team = WG ? 0 : (int)threadIdx.x / lanes, tl = WG ? (int)threadIdx.x : (int)threadIdx.x % lanes;
+    float w[U][K];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = (tl + u * lanes) * K;
+#pragma unroll
+        for (int i = 0; i < K; ++i) w[u][i] = p.w != nullptr && c + i < p.d ? p.w[c + i] : 1.0f;
+    }
+    for (int64_t r = (int64_t)blockIdx.x * teams + team; r < p.rows; r += (int64_t)gridDim.x * teams) {
+        const T* x = row_at<T>(p.x, r, p.N);
+        const T* res = p.res.p != nullptr ? row_at<T>(p.res, r, p.N) : nullptr;
+        float s[U][K];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = (tl + u * lanes) * K;
+#pragma unroll
+            for (int i = 0; i < K; ++i) s[u][i] = 0.0f;
+            if (c < p.d) load_unit<T, VEC>(x, c, p.d, p.pairs, s[u]);
+        }
+        if (res != nullptr) {
+            float y[U][K];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (tl + u * lanes) * K;
+                if (c < p.d) {
+                    load_unit<T, VEC>(res, c, p.d, p.pairs, y[u]);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) s[u][i] += y[u][i];
+                }
+            }
+            T* sum = (T*)p.sum + r * p.d;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (tl + u * lanes) * K;
+                if (c < p.d) store_unit<T, VEC>(sum, c, p.d, p.pairs, s[u]);
+            }
+        }
+        float squares = 0.0f, none = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < K; ++i) squares = fmaf(s[u][i], s[u][i], squares);
+        team_sum<WG>(squares, none, false, lanes, lds);
+        const float rstd = rms(squares, p.d, p.eps);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < K; ++i) s[u][i] = s[u][i] * rstd * w[u][i];
+        if constexpr (!EIGHT) {
+            T* y = (T*)p.y + r * p.d;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (tl + u * lanes) * K;
+                if (c < p.d) store_unit<T, VEC>(y, c, p.d, p.pairs, s[u]);
+            }
+        } else {
+            uint32_t top[U], row = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (tl + u * lanes) * K;
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < K; ++i)
+                    if (c + i < p.d) m = max(m, __float_as_uint(s[u][i]) & 0x7fffffffu);
+                // a group is group_lanes lanes side by side
+                for (int k = 1; k < p.group_lanes; k *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, k));
+                top[u] = m;
+                row = max(row, m);
+            }
+            if (p.group_lanes == 0) {
+                row = team_max<WG>(row, lanes, lds);
+#pragma unroll
+                for (int u = 0; u < U; ++u) top[u] = row;
+            }
+            uint8_t* y = (uint8_t*)p.y + r * p.d;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int unit = tl + u * lanes, c = unit * K;
+                const float most = __uint_as_float(top[u]);
+                // (a largest value under 2^-100 has no reciprocal worth having)
+                const bool some = !(most < 0x1p-100f);
+                const float scale = some ? most * p.inverse : 0.0f, down = some ? p.largest / most : 0.0f;
+                if (c < p.d) {
+                    float v[K];
+#pragma unroll
+                    for (int i = 0; i < K; ++i) v[i] = some ? s[u][i] * down : 0.0f;
+                    uint32_t q[K / 4];
+                    pack8<K>(v, p.int8, q);
+                    if (VEC) {
+#pragma unroll
+                        for (int i = 0; i < K / 4; ++i) *(uint32_t*)(y + c + 4 * i) = q[i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < K; ++i)
+                            if (c + i < p.d) y[c + i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+                    }
+                    if (p.group_lanes != 0 && unit % p.group_lanes == 0) p.scales[r * p.groups + unit / p.group_lanes] = scale;
+                }
+                if (p.group_lanes == 0 && u == 0 && tl == 0) p.scales[r] = scale;
+            }
+        }
+    }
+}
+
+template <typename T, bool VEC, bool WG, int U>
+__global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(NormArgs p)
+{
+    constexpr int K = kUnit<T>;
+    __shared__ float lds[32];
+    extern __shared__ float sums[];  // parts of a wave each: [4][d]
+    const int lanes = WG ? (int)blockDim.x : p.lanes;
+    const int teams = WG ? 1 : 256 / lanes, team = WG ? 0 : (int)threadIdx.x / lanes, tl = WG ? (int)threadIdx.x : (int)threadIdx.x % lanes;
+    float w[U][K], dw[U][K];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = (tl + u * lanes) * K;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            w[u][i] = p.w != nullptr && c + i < p.d ? p.w[c + i] : 1.0f;
+            dw[u][i] = 0.0f;
+        }
+    }
+    for (int64_t r = (int64_t)blockIdx.x * teams + team; r < p.rows; r += (int64_t)gridDim.x * teams) {
+        const T* x = row_at<T>(p.x, r, p.N);
+        const T* dyr = row_at<T>(p.dy, r, p.N);
+        float s[U][K], dy[U][K], ds[U][K];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = (tl + u * lanes) * K;
+#pragma unroll
+            for (int i = 0; i < K; ++i) s[u][i] = dy[u][i] = ds[u][i] = 0.0f;
+            if (c < p.d) {
+                load_unit<T, VEC>(x, c, p.d, p.pairs, s[u]);
+                load_unit<T, VEC>(dyr, c, p.d, p.pairs, dy[u]);
+            }
+        }
+        if (p.res.p != nullptr) {
+            const T* dsr = row_at<T>(p.res, r, p.N);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (tl + u * lanes) * K;
+                if (c < p.d) load_unit<T, VEC>(dsr, c, p.d, p.pairs, ds[u]);
+            }
+        }
+        float squares = 0.0f, along = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+                squares = fmaf(s[u][i], s[u][i], squares);
+                along = fmaf(s[u][i], dy[u][i] * w[u][i], along);
+            }
+        team_sum<WG>(squares, along, true, lanes, lds);
+        const float rstd = rms(squares, p.d, p.eps), mean = along * rstd / (float)p.d;
+        T* dx = (T*)p.y + r * p.d;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = (tl + u * lanes) * K;
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+                const float n = s[u][i] * rstd;
+                s[u][i] = fmaf(rstd, fmaf(-n, mean, dy[u][i] * w[u][i]), ds[u][i]);
+                dw[u][i] = fmaf(dy[u][i], n, dw[u][i]);
+            }
+            if (c < p.d) store_unit<T, VEC>(dx, c, p.d, p.pairs, s[u]);
+        }
+    }
+    if (p.dw_part == nullptr) return;
+    float* part = p.dw_part + (int64_t)blockIdx.x * p.d;
+    if constexpr (WG) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = (tl + u * lanes) * K;
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (c + i < p.d) part[c + i] = dw[u][i];
+        }
+    } else {
+        // the teams of a wave, then the waves, in their order
+        const int wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = (tl + u * lanes) * K;
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+                float v = dw[u][i];
+                for (int m = lanes; m < 64; m *= 2) v += __shfl_xor(v, m);
+                if ((threadIdx.x & 63) < (unsigned)lanes && c + i < p.d) sums[wave * p.d + c + i] = v;
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.d; c += 256) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v += sums[k * p.d + c];
+            part[c] = v;
+        }
+    }
+}
+
+template <typename T, bool VEC, bool WG, int U, int KIND> hyena_status norm_as(const NormArgs& a, const NormLaunch& l, hipStream_t s)
+{
+    if constexpr (KIND == 2)
+        HY_LAUNCH(kernel_label("hyena_residual_norm_grad", type_label<T>(), VEC, WG, U), (hyena_residual_norm_grad<T, VEC, WG, U>),
+                  dim3((unsigned)l.groups), dim3((unsigned)l.threads), WG ? 0 : (size_t)4 * a.d * sizeof(float), s, a);
+    else
+        HY_LAUNCH(kernel_label("hyena_residual_norm", type_label<T>(), VEC, WG, U, KIND == 1), (hyena_residual_norm<T, VEC, WG, U, KIND == 1>),
+                  dim3((unsigned)l.groups), dim3((unsigned)l.threads), 0, s, a);
+    return launched();
+}
+
+template <typename T, bool VEC, int KIND> hyena_status norm_sized(const NormArgs& a, const NormLaunch& l, hipStream_t s)
+{
+    if (l.workgroup) return l.units <= 2 ? norm_as<T, VEC, true, 2, KIND>(a, l, s) : norm_as<T, VEC, true, 4, KIND>(a, l, s);
+    if (l.units == 1) return norm_as<T, VEC, false, 1, KIND>(a, l, s);
+    if (l.units == 2) return norm_as<T, VEC, false, 2, KIND>(a, l, s);
+    if (l.units == 3) return norm_as<T, VEC, false, 3, KIND>(a, l, s);
+    return norm_as<T, VEC, false, 4, KIND>(a, l, s);
+}
+
+template <typename T> hyena_status norm_launch(const NormArgs& a, const NormLaunch& l, int kind, hipStream_t s)
+{
+    if (l.vec) {
+        if (kind == 0) return norm_sized<T, true, 0>(a, l, s);
+        return kind == 1 ? norm_sized<T, true, 1>(a, l, s) : norm_sized<T, true, 2>(a, l, s);
+    }
+    if (kind == 0) return norm_sized<T, false, 0>(a, l, s);
+    return kind == 1 ? norm_sized<T, false, 1>(a, l, s) : norm_sized<T, false, 2>(a, l, s);
+}
+
+}  // namespace hy
+
+#define HY_NORM_INSTANTIATE(T)                                                                                       \
+    namespace hy {                                                                                                  \
+    template hyena_status norm_launch<T>(const NormArgs&, const NormLaunch&, int, hipStream_t);                      \
+    }

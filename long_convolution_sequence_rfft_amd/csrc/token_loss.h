@@ -1,0 +1,63 @@
+// token_loss.h -- arguments and scratch of the loss over a vocabulary.
+#pragma once
+
+#include "rows.h"
+
+namespace hy {
+
+// Tokens and values of the vocabulary of a tile of logits; channels and rows of a
+// tile of the gradients.
+constexpr int kLossTokens = 128, kLossValues = 256;
+constexpr int kGradRows = 128, kGradChannels = 256;
+
+struct LossArgs {
+    Rows x, targets, d_loss;
+    uint32_t x_N, targets_N, d_loss_N;  // row_at
+    int64_t total;         // B * N
+    int32_t V, d;
+    int32_t kd;            // d rounded up to 32: the width of gathered rows
+    int32_t pairs;
+    int32_t each;          // tokens of a workgroup of the gather
+    float scale;
+    const void* table;     // as given
+    const float* lse_in;
+    float* loss;
+    float* lse;
+    void* d_x;
+    void* d_table;
+
+    // scratch
+    int64_t* count;        // tokens that take part
+    float* norm;           // [0] what G is multiplied by, [1] what undoes it
+    int32_t* index;        // [tokens] which token of the call
+    int32_t* place;        // [B * N] which gathered row, or -1
+    int32_t* target;       // [tokens]
+    float* weight;         // [tokens] d_loss
+    float* lse2;           // [tokens] lse / ln 2
+    char* rows;            // gathered x: [planes][tokens rounded up][kd], 16-bit
+    int64_t rows_plane;    // bytes
+    const char* values;    // the table as matrix operand: itself, or [planes][V][kd]
+    int64_t values_row, values_plane;
+    float2* part;          // [tiles of values][tokens rounded up]: largest, sum
+    float* hit;            // [tokens] the target's logit
+    char* g;               // [planes][tokens rounded up][chunk]
+    int64_t g_row, g_plane;
+    float* acc;            // [splits][tokens rounded up][acc_row] d_x
+    int64_t tokens;        // rounded up
+    int32_t acc_row;
+    int32_t chunk;         // values of a piece of the vocabulary
+    int32_t first;         // of this piece
+    int32_t splits;        // of the sum over a piece's values, for d_x
+};
+
+// Launches of one call; P: planes (float32: three bfloat16 terms).
+template <typename T> hyena_status loss_forward(const LossArgs& a, bool pack, bool units, hipStream_t s);
+template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, bool units, hipStream_t s);
+#define HY_LOSS_EXTERN(T)                                                                                  \
+    extern template hyena_status loss_forward<T>(const LossArgs&, bool, bool, hipStream_t);                \
+    extern template hyena_status loss_backward<T>(const LossArgs&, bool, bool, hipStream_t);
+HY_LOSS_EXTERN(float)
+HY_LOSS_EXTERN(uint16_t)
+HY_LOSS_EXTERN(_Float16)
+
+}  // namespace hy

@@ -1,0 +1,188 @@
+// token_loss.hip -- entry points of the loss over a vocabulary (include/hyena.h):
+// checks, the scratch, and the pieces of the vocabulary.
+#include "token_loss.h"
+
+namespace hy {
+namespace {
+
+constexpr const char* kWho = "token loss";
+
+// G of a piece of the vocabulary takes about this much, or a tile of values if that
+// is more.
+constexpr int64_t kGradBytes = (int64_t)256 << 20;
+// Workgroups that d_x's sums are cut for.
+constexpr int64_t kSplitGroups = 512;
+
+hyena_status refuse(const char* what) { return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(kWho) + ": " + what); }
+
+hyena_status loss_sizes(const hyena_token_loss* op)
+{
+    if (op == nullptr) return refuse("the description is NULL");
+    if (op->B < 1 || op->N < 1 || op->V < 1 || op->d < 1) return refuse("B, N, V and d must be at least 1");
+    if (op->V > 1 << 22 || op->d > 16384) return fail(HYENA_ERR_UNSUPPORTED, "token loss: V at most 2^22 and d at most 16384");
+    if (op->B > 1 << 22 || op->N > 1 << 22 || op->B * op->N > 1 << 22)
+        return fail(HYENA_ERR_UNSUPPORTED, "token loss: at most 2^22 tokens");
+    return check_io(kWho, op->io_dtype);
+}
+
+bool needs_pack(const hyena_token_loss* op) { return op->io_dtype == HYENA_F32 || op->d % 8 != 0; }
+
+// Sizes, and with a scratch the addresses in it; returns the bytes.
+size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a)
+{
+    const int64_t planes = op->io_dtype == HYENA_F32 ? 3 : 1;
+    a.total = op->B * op->N;
+    a.V = (int32_t)op->V;
+    a.d = (int32_t)op->d;
+    a.kd = (int32_t)((op->d + 31) / 32 * 32);
+    a.tokens = (a.total + kLossTokens - 1) / kLossTokens * kLossTokens;
+    a.scale = op->scale;
+    a.table = op->table;
+    // a workgroup of the gather for 64 tokens, or at most 512 of them
+    const int64_t each = (a.total + 511) / 512;
+    a.each = (int32_t)(each < 64 ? 64 : each);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        char* p = scratch ? (char*)scratch + at : nullptr;
+        at += (n + 255) & ~(size_t)255;
+        return p;
+    };
+    const size_t tokens = (size_t)a.tokens;
+    a.count = (int64_t*)take(8);
+    a.norm = (float*)take(8);
+    a.index = (int32_t*)take(tokens * 4);
+    a.target = (int32_t*)take(tokens * 4);
+    a.rows_plane = (int64_t)tokens * a.kd * 2;
+    a.rows = take((size_t)(planes * a.rows_plane));
+    if (needs_pack(op)) {
+        a.values_row = (int64_t)a.kd * 2;
+        a.values_plane = (int64_t)a.V * a.values_row;
+        a.values = take((size_t)(planes * a.values_plane));
+    } else {
+        a.values_row = (int64_t)a.d * 2;
+        a.values_plane = 0;
+        a.values = (const char*)op->table;
+    }
+    if (!grad) {
+        a.part = (float2*)take((size_t)((a.V + kLossValues - 1) / kLossValues) * tokens * 8);
+        a.hit = (float*)take(tokens * 4);
+        return at;
+    }
+    a.place = (int32_t*)take((size_t)a.total * 4);
+    a.weight = (float*)take(tokens * 4);
+    a.lse2 = (float*)take(tokens * 4);
+    const int64_t whole = (a.V + kLossValues - 1) / kLossValues, fit = kGradBytes / (a.tokens * 2 * planes * kLossValues);
+    int64_t tiles = fit < 1 ? 1 : fit < whole ? fit : whole;
+    const int64_t pieces = (whole + tiles - 1) / tiles;
+    tiles = (whole + pieces - 1) / pieces;  // pieces of one size
+    a.chunk = (int32_t)(tiles * kLossValues);
+    a.g_row = (int64_t)a.chunk * 2;
+    a.g_plane = a.tokens * a.g_row;
+    a.g = take((size_t)(planes * a.g_plane));
+    const int64_t base = (a.tokens / kGradRows) * ((a.d + kGradChannels - 1) / kGradChannels);
+    int64_t splits = kSplitGroups / base;
+    const int64_t most = a.chunk / 512 < 1 ? 1 : a.chunk / 512;  // a part has 512 values at least
+    splits = splits < 1 ? 1 : splits > most ? most : splits > 16 ? 16 : splits;
+    a.splits = (int32_t)splits;
+    a.acc_row = (int32_t)((a.d + 3) / 4 * 4);
+    a.acc = (float*)take((size_t)splits * tokens * (size_t)a.acc_row * 4);
+    return at;
+}
+
+hyena_status loss_args(const hyena_token_loss* op, void* scratch, bool grad, const hyena_rows* d_loss, LossArgs& a, Span* ins,
+                       bool* units, size_t* bytes)
+{
+    hyena_status st = loss_sizes(op);
+    if (st != HYENA_OK) return st;
+    const size_t e = element_bytes(op->io_dtype);
+    if ((st = check_rows(kWho, op->x, "x", e)) != HYENA_OK || (st = check_rows(kWho, op->targets, "targets", 4)) != HYENA_OK ||
+        (d_loss != nullptr && (st = check_rows(kWho, *d_loss, "d_loss", 4)) != HYENA_OK))
+        return st;
+    if (op->table == nullptr || (uintptr_t)op->table % 16 != 0) return refuse("table is NULL or not 16-byte aligned");
+    if (scratch == nullptr || (uintptr_t)scratch % 16 != 0) return refuse("scratch is NULL or not 16-byte aligned");
+    *bytes = lay_out(op, grad, scratch, a);
+    hyena_rows x = plain_rows(op->x, op->B, op->N), targets = plain_rows(op->targets, op->B, op->N),
+               dl = d_loss ? plain_rows(*d_loss, op->B, op->N) : hyena_rows{nullptr, 0, 0};
+    ins[0] = rows_span(x, op->B, op->N, op->d, e);
+    ins[1] = rows_span(targets, op->B, op->N, 1, 4);
+    ins[2] = Span{op->table, (size_t)(op->V * op->d) * e};
+    ins[3] = d_loss ? rows_span(dl, op->B, op->N, 1, 4) : Span{nullptr, 0};
+    RowShape made(op->d, e);
+    made.add(x);
+    *units = made.made_of() == kMadeOfUnits;
+    a.pairs = made.made_of() >= kMadeOfPairs;
+    hyena_rows* v[3] = {&x, &targets, &dl};
+    uint32_t* n[3] = {&a.x_N, &a.targets_N, &a.d_loss_N};
+    Rows* to[3] = {&a.x, &a.targets, &a.d_loss};
+    for (int i = 0; i < 3; ++i) {
+        int64_t N = op->N;
+        flatten_rows(&v[i], 1, op->B, &N);
+        *n[i] = (uint32_t)N;
+        *to[i] = Rows{v[i]->data, v[i]->batch, v[i]->token};
+    }
+    return HYENA_OK;
+}
+
+}  // namespace
+}  // namespace hy
+
+using namespace hy;
+
+extern "C" {
+
+hyena_status hyena_token_loss_scratch_bytes(const hyena_token_loss* op, size_t* forward_bytes, size_t* backward_bytes)
+{
+    const hyena_status st = loss_sizes(op);
+    if (st != HYENA_OK) return st;
+    LossArgs a{};
+    if (forward_bytes) *forward_bytes = lay_out(op, false, nullptr, a);
+    if (backward_bytes) *backward_bytes = lay_out(op, true, nullptr, a);
+    return HYENA_OK;
+}
+
+hyena_status hyena_token_loss_forward(const hyena_token_loss* op, float* loss, float* lse, void* scratch, void* stream)
+{
+    LossArgs a{};
+    Span ins[4];
+    bool units;
+    size_t bytes;
+    hyena_status st = loss_args(op, scratch, false, nullptr, a, ins, &units, &bytes);
+    if (st != HYENA_OK) return st;
+    if (loss == nullptr || lse == nullptr || (uintptr_t)loss % 4 != 0 || (uintptr_t)lse % 4 != 0)
+        return refuse("loss or lse is NULL or not aligned to its element");
+    const Named outs[3] = {{Span{loss, (size_t)a.total * 4}, "loss"}, {Span{lse, (size_t)a.total * 4}, "lse"}, {Span{scratch, bytes}, "scratch"}};
+    if ((st = check_apart(kWho, ins, 4, outs, 3)) != HYENA_OK) return st;
+    a.loss = loss;
+    a.lse = lse;
+    return by_io(op->io_dtype, [&](auto* t) {
+        return loss_forward<std::remove_pointer_t<decltype(t)>>(a, needs_pack(op), units, (hipStream_t)stream);
+    });
+}
+
+hyena_status hyena_token_loss_backward(const hyena_token_loss* op, const hyena_rows* d_loss, const float* lse, void* d_x,
+                                       void* d_table, void* scratch, void* stream)
+{
+    LossArgs a{};
+    Span ins[5];
+    bool units;
+    size_t bytes;
+    if (d_loss == nullptr) return refuse("d_loss is NULL");
+    hyena_status st = loss_args(op, scratch, true, d_loss, a, ins, &units, &bytes);
+    if (st != HYENA_OK) return st;
+    if (lse == nullptr || (uintptr_t)lse % 4 != 0) return refuse("lse is NULL or not aligned to its element");
+    if (d_x == nullptr && d_table == nullptr) return refuse("neither d_x nor d_table is wanted");
+    if ((uintptr_t)d_x % 16 != 0 || (uintptr_t)d_table % 16 != 0) return refuse("d_x or d_table is not 16-byte aligned");
+    const size_t e = element_bytes(op->io_dtype);
+    ins[4] = Span{lse, (size_t)a.total * 4};
+    const Named outs[3] = {{Span{d_x, (size_t)(a.total * op->d) * e}, "d_x"}, {Span{d_table, (size_t)(op->V * op->d) * e}, "d_table"},
+                           {Span{scratch, bytes}, "scratch"}};
+    if ((st = check_apart(kWho, ins, 5, outs, 3)) != HYENA_OK) return st;
+    a.lse_in = lse;
+    a.d_x = d_x;
+    a.d_table = d_table;
+    return by_io(op->io_dtype, [&](auto* t) {
+        return loss_backward<std::remove_pointer_t<decltype(t)>>(a, needs_pack(op), units, (hipStream_t)stream);
+    });
+}
+
+}  // extern "C"

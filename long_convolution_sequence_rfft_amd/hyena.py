@@ -45,6 +45,10 @@ EXPORTED_SYMBOLS = (
     "hyena_recurrence_create", "hyena_recurrence_query", "hyena_recurrence_forward",
     "hyena_recurrence_backward", "hyena_recurrence_step", "hyena_recurrence_destroy",
     "hyena_qk_norm_forward", "hyena_qk_norm_scratch_bytes", "hyena_qk_norm_backward",
+    "hyena_embedding_forward", "hyena_embedding_scratch_bytes", "hyena_embedding_backward",
+    "hyena_residual_norm_forward", "hyena_residual_norm_scratch_bytes",
+    "hyena_residual_norm_backward",
+    "hyena_token_loss_scratch_bytes", "hyena_token_loss_forward", "hyena_token_loss_backward",
 )
 
 HYENA_NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -101,6 +105,35 @@ class QkNorm(ctypes.Structure):
                 ("freqs", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
                 ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
                 ("position_offset", ctypes.c_int64), ("q", View), ("k", View)]
+
+HYENA_NORM_IO = 0
+HYENA_NORM_E4M3 = 1
+HYENA_NORM_INT8 = 2
+
+
+class Rows(ctypes.Structure):
+    """hyena_rows: a [B, N, width] tensor seen through element strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class EmbeddingOp(ctypes.Structure):
+    """hyena_embedding (device pointers as ints; see include/hyena.h)."""
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("V", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("tokens", Rows)]
+
+
+class ResidualNormOp(ctypes.Structure):
+    """hyena_residual_norm."""
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("format", ctypes.c_int32), ("group", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("weight", ctypes.c_void_p), ("x", Rows), ("residual", Rows)]
+
+
+class TokenLossOp(ctypes.Structure):
+    """hyena_token_loss."""
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("V", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("x", Rows),
+                ("table", ctypes.c_void_p), ("targets", Rows)]
 
 _lock = threading.Lock()
 _lib = None
@@ -159,6 +192,15 @@ def load():
             lib.hyena_qk_norm_forward.argtypes = [p, p, p, p]
             lib.hyena_qk_norm_scratch_bytes.argtypes = [p, ctypes.POINTER(sz)]
             lib.hyena_qk_norm_backward.argtypes = [p] * 9
+            lib.hyena_embedding_forward.argtypes = [p] * 4
+            lib.hyena_embedding_scratch_bytes.argtypes = [p, ctypes.POINTER(sz)]
+            lib.hyena_embedding_backward.argtypes = [p, p, p, i32, p, p]
+            lib.hyena_residual_norm_forward.argtypes = [p] * 5
+            lib.hyena_residual_norm_scratch_bytes.argtypes = [p, ctypes.POINTER(sz)]
+            lib.hyena_residual_norm_backward.argtypes = [p] * 7
+            lib.hyena_token_loss_scratch_bytes.argtypes = [p, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+            lib.hyena_token_loss_forward.argtypes = [p] * 5
+            lib.hyena_token_loss_backward.argtypes = [p] * 7
             for name in ("hyena_plan_create", "hyena_plan_create_ex", "hyena_plan_query",
                          "hyena_plan_path",
                          "hyena_workspace_init", "hyena_workspace_release",
@@ -171,7 +213,12 @@ def load():
                          "hyena_recurrence_query", "hyena_recurrence_forward",
                          "hyena_recurrence_backward", "hyena_recurrence_step",
                          "hyena_recurrence_destroy", "hyena_qk_norm_forward",
-                         "hyena_qk_norm_scratch_bytes", "hyena_qk_norm_backward"):
+                         "hyena_qk_norm_scratch_bytes", "hyena_qk_norm_backward",
+                         "hyena_embedding_forward", "hyena_embedding_scratch_bytes",
+                         "hyena_embedding_backward", "hyena_residual_norm_forward",
+                         "hyena_residual_norm_scratch_bytes", "hyena_residual_norm_backward",
+                         "hyena_token_loss_scratch_bytes", "hyena_token_loss_forward",
+                         "hyena_token_loss_backward"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -357,6 +404,51 @@ def hyena_qk_norm_scratch_bytes(op):
 def hyena_qk_norm_backward(op, dq_out, dk_out, dq, dk, dq_weight, dk_weight, scratch, stream=0):
     return load().hyena_qk_norm_backward(_ref(op), _ref(dq_out), _ref(dk_out), dq, dk, dq_weight,
                                          dk_weight, scratch, stream)
+
+
+def hyena_embedding_forward(op, table, out, stream=0):
+    return load().hyena_embedding_forward(_ref(op), table, out, stream)
+
+
+def hyena_embedding_scratch_bytes(op):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t()
+    st = load().hyena_embedding_scratch_bytes(_ref(op), ctypes.byref(n))
+    return st, n.value
+
+
+def hyena_embedding_backward(op, d_out, d_table, accumulate, scratch, stream=0):
+    return load().hyena_embedding_backward(_ref(op), _ref(d_out), d_table, int(accumulate), scratch, stream)
+
+
+def hyena_residual_norm_forward(op, total, y, scales, stream=0):
+    return load().hyena_residual_norm_forward(_ref(op), total, y, scales, stream)
+
+
+def hyena_residual_norm_scratch_bytes(op):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t()
+    st = load().hyena_residual_norm_scratch_bytes(_ref(op), ctypes.byref(n))
+    return st, n.value
+
+
+def hyena_residual_norm_backward(op, d_y, d_sum, d_x, d_weight, scratch, stream=0):
+    return load().hyena_residual_norm_backward(_ref(op), _ref(d_y), _ref(d_sum), d_x, d_weight, scratch, stream)
+
+
+def hyena_token_loss_scratch_bytes(op):
+    """Returns (status, forward bytes, backward bytes)."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    st = load().hyena_token_loss_scratch_bytes(_ref(op), ctypes.byref(f), ctypes.byref(b))
+    return st, f.value, b.value
+
+
+def hyena_token_loss_forward(op, loss, lse, scratch, stream=0):
+    return load().hyena_token_loss_forward(_ref(op), loss, lse, scratch, stream)
+
+
+def hyena_token_loss_backward(op, d_loss, lse, d_x, d_table, scratch, stream=0):
+    return load().hyena_token_loss_backward(_ref(op), _ref(d_loss), lse, d_x, d_table, scratch, stream)
 
 
 # --------------------------------------------------------------------------
@@ -860,3 +952,198 @@ class QKNorm(_Mixer):
         self._call("hyena_qk_norm_backward", self._lib.hyena_qk_norm_backward, op, dqo, dko, dq.data_ptr(), dk.data_ptr(),
                    ptr(dqw), ptr(dkw), ptr(scratch), stream)
         return dq, dk, dqw, dkw
+
+
+_PACK_ROWS = struct.Struct("P2q").pack
+_PACK_EMBEDDING = struct.Struct("4qif" + "P2q").pack
+_PACK_RESIDUAL_NORM = struct.Struct("3q2iqf4xP" + "P2q" * 2).pack
+_PACK_TOKEN_LOSS = struct.Struct("4qif" + "P2q" + "P" + "P2q").pack
+
+
+class _Tokens(_Mixer):
+    """Checks shared by the operators on whole tokens."""
+
+    def _rows(self, t, name, shape, dtype):
+        """Address and strides (batch, token) of a [B, N, width] or [B, N] tensor."""
+        if not self._fits(t, shape, dtype):
+            self._check_tensor(t, name, shape, dtype)
+        st = t.stride()
+        if len(shape) == 3 and st[2] != 1 and shape[2] > 1:
+            raise ValueError(f"the last axis of {name} must be contiguous")
+        return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
+
+    def _scratch(self, n):
+        # a call's own: the allocator gives it out again once this stream's work is enqueued, so
+        # calls on different streams and captured graphs have scratches of their own
+        return self.torch.empty(n, dtype=self.torch.uint8, device=self.device) if n else None
+
+
+class Embedding(_Tokens):
+    """Rows of a table by token, times a factor, and the table's gradient (see include/hyena.h).
+
+    tokens: int32 [B, N] (a view); a token outside 0..V-1 takes no part: its row is zeros and it
+    has no gradient.  table: [V, d] in the io dtype, contiguous.  Outputs carry no autograd
+    history: ``backward`` is called by the caller.
+    """
+
+    def __init__(self, B, N, V, d, io_dtype=HYENA_F32, scale=1.0, device="cuda"):
+        self._place(io_dtype, device)
+        self.B, self.N, self.V, self.d, self.scale = int(B), int(N), int(V), int(d), float(scale)
+        st, self.scratch_bytes = hyena_embedding_scratch_bytes(self._op((0, 0, 0)))
+        _check(st, "hyena_embedding_scratch_bytes")
+
+    def _op(self, tokens):
+        return _PACK_EMBEDDING(self.B, self.N, self.V, self.d, self.io_dtype, self.scale, *tokens)
+
+    def forward(self, tokens, table, out=None):
+        """scale * table[tokens]: [B, N, d]."""
+        op = self._op(self._rows(tokens, "tokens", (self.B, self.N), self.torch.int32))
+        at = self._dense(table, "table", (self.V, self.d), self.dtype)
+        if not at:
+            raise ValueError("table must be a torch tensor")
+        out = self._out(out, "out", (self.B, self.N, self.d), self.dtype)
+        self._call("hyena_embedding_forward", self._lib.hyena_embedding_forward, op, at, out.data_ptr(), self._stream())
+        return out
+
+    def backward(self, d_out, tokens, d_table=None):
+        """The table's gradient [V, d] from that of the output.  d_table: a gradient that is there
+        already (the loss's, of a table at both ends); the sums are added to it in place."""
+        op = self._op(self._rows(tokens, "tokens", (self.B, self.N), self.torch.int32))
+        d = _PACK_ROWS(*self._rows(d_out, "d_out", (self.B, self.N, self.d), self.dtype))
+        adds = d_table is not None
+        d_table = self._out(d_table, "d_table", (self.V, self.d), self.dtype)
+        scratch = self._scratch(self.scratch_bytes)
+        self._call("hyena_embedding_backward", self._lib.hyena_embedding_backward, op, d, d_table.data_ptr(), int(adds),
+                   scratch.data_ptr(), self._stream())
+        return d_table
+
+
+class ResidualNorm(_Tokens):
+    """RMS norm of whole tokens with the residual's addition: s = x + residual,
+    y = weight * s / sqrt(mean(s^2) + eps) (see include/hyena.h).
+
+    x, residual: [B, N, d] in the io dtype (views; the last axis contiguous), weight float32 [d]
+    or None.  ``quantized`` "e4m3" or "int8" makes y in 8 bits, with a float32 scale for each
+    ``group`` channels (32, 64 or 128; None: the whole row).  Outputs carry no autograd history:
+    ``backward`` is called by the caller.
+    """
+
+    _FORMATS = {None: HYENA_NORM_IO, "e4m3": HYENA_NORM_E4M3, "int8": HYENA_NORM_INT8}
+
+    def __init__(self, B, N, d, io_dtype=HYENA_F32, eps=1e-6, quantized=None, group=None, device="cuda"):
+        self._place(io_dtype, device)
+        if quantized not in self._FORMATS:
+            raise ValueError(f"quantized must be None, 'e4m3' or 'int8', got {quantized!r}")
+        if group is not None and (quantized is None or group not in (32, 64, 128)):
+            raise ValueError(f"group must be None, or 32, 64 or 128 with quantized, got {group!r}")
+        if group is not None and int(d) % group:
+            raise ValueError(f"d must be a multiple of group, got {d} and {group}")
+        self.B, self.N, self.d, self.eps = int(B), int(N), int(d), float(eps)
+        self.quantized, self.group = quantized, group
+        st, self.scratch_bytes = hyena_residual_norm_scratch_bytes(self._op(0, (0, 0, 0), (0, 0, 0)))
+        _check(st, "hyena_residual_norm_scratch_bytes")
+        self._y_dtype = {None: self.dtype, "e4m3": self.torch.float8_e4m3fn, "int8": self.torch.int8}[quantized]
+
+    def _op(self, weight, x, residual):
+        return _PACK_RESIDUAL_NORM(self.B, self.N, self.d, self.io_dtype, self._FORMATS[self.quantized], self.group or 0,
+                                   self.eps, weight, *x, *residual)
+
+    @property
+    def scales_shape(self):
+        return (self.B, self.N, self.d // self.group if self.group else 1)
+
+    def forward(self, x, residual=None, weight=None, total=None, y=None, scales=None):
+        """(y, s), or (y, scales, s) with ``quantized``; s is None without a residual.  total: where s
+        goes, x's or the residual's own memory if wanted."""
+        shape = (self.B, self.N, self.d)
+        rows = self._rows(x, "x", shape, self.dtype)
+        op = self._op(self._dense(weight, "weight", (self.d,), self.torch.float32), rows,
+                      self._rows(residual, "residual", shape, self.dtype) if residual is not None else (0, 0, 0))
+        if residual is not None:
+            total = self._out(total, "total", shape, self.dtype, x)
+        elif total is not None:
+            raise ValueError("total is only there with a residual")
+        y = self._out(y, "y", shape, self._y_dtype, x if self.quantized is None else None)
+        if self.quantized is not None:
+            scales = self._out(scales, "scales", self.scales_shape, self.torch.float32)
+        elif scales is not None:
+            raise ValueError("scales are only there with quantized")
+        self._call("hyena_residual_norm_forward", self._lib.hyena_residual_norm_forward, op,
+                   total.data_ptr() if total is not None else None, y.data_ptr(),
+                   scales.data_ptr() if scales is not None else None, self._stream())
+        return (y, total) if self.quantized is None else (y, scales, total)
+
+    def backward(self, dy, s, weight=None, ds=None, dx=None):
+        """(dx, dweight) from the gradient of y and (or None) the sum's own, ds; s is forward's sum (x
+        without a residual).  dx is the gradient of x and of the residual; it may be ds's own memory.
+        dweight is None without a weight."""
+        shape = (self.B, self.N, self.d)
+        op = self._op(self._dense(weight, "weight", (self.d,), self.torch.float32), self._rows(s, "s", shape, self.dtype),
+                      (0, 0, 0))
+        d_y = _PACK_ROWS(*self._rows(dy, "dy", shape, self.dtype))
+        d_s = _PACK_ROWS(*self._rows(ds, "ds", shape, self.dtype)) if ds is not None else None
+        dx = self._out(dx, "dx", shape, self.dtype, s)
+        dw = scratch = None
+        if weight is not None:
+            dw = self.torch.empty(self.d, dtype=self.torch.float32, device=self.device)
+            scratch = self._scratch(self.scratch_bytes)
+        self._call("hyena_residual_norm_backward", self._lib.hyena_residual_norm_backward, op, d_y, d_s, dx.data_ptr(),
+                   dw.data_ptr() if dw is not None else None, scratch.data_ptr() if scratch is not None else None,
+                   self._stream())
+        return dx, dw
+
+
+class TokenLoss(_Tokens):
+    """Softmax cross entropy over a vocabulary: the logits are scale * x table^T and are never kept
+    (see include/hyena.h).
+
+    x: [B, N, d] in the io dtype (a view; the last axis contiguous), table [V, d], contiguous,
+    targets int32 [B, N] (a view).  A token whose target is outside 0..V-1 takes no part: loss, lse
+    and dx are 0 there and its x is not read.  Outputs carry no autograd history: ``backward`` is
+    called by the caller.
+    """
+
+    def __init__(self, B, N, V, d, io_dtype=HYENA_F32, scale=1.0, device="cuda"):
+        self._place(io_dtype, device)
+        self.B, self.N, self.V, self.d, self.scale = int(B), int(N), int(V), int(d), float(scale)
+        st, self.forward_bytes, self.backward_bytes = hyena_token_loss_scratch_bytes(self._op((0, 0, 0), 0, (0, 0, 0)))
+        _check(st, "hyena_token_loss_scratch_bytes")
+
+    def _op(self, x, table, targets):
+        return _PACK_TOKEN_LOSS(self.B, self.N, self.V, self.d, self.io_dtype, self.scale, *x, table, *targets)
+
+    def _describe(self, x, table, targets):
+        rows = self._rows(x, "x", (self.B, self.N, self.d), self.dtype)
+        at = self._dense(table, "table", (self.V, self.d), self.dtype)
+        if not at:
+            raise ValueError("table must be a torch tensor")
+        return self._op(rows, at, self._rows(targets, "targets", (self.B, self.N), self.torch.int32))
+
+    def forward(self, x, table, targets, loss=None, lse=None):
+        """(loss, lse), float32 [B, N]: the negative log probability of each token's target, and the
+        log of the sum of the logits' exponentials, which ``backward`` takes."""
+        op = self._describe(x, table, targets)
+        loss = self._out(loss, "loss", (self.B, self.N), self.torch.float32)
+        lse = self._out(lse, "lse", (self.B, self.N), self.torch.float32)
+        scratch = self._scratch(self.forward_bytes)
+        self._call("hyena_token_loss_forward", self._lib.hyena_token_loss_forward, op, loss.data_ptr(), lse.data_ptr(),
+                   scratch.data_ptr(), self._stream())
+        return loss, lse
+
+    def backward(self, d_loss, x, table, targets, lse, want_dx=True, want_table=True):
+        """(dx, d_table) from the gradient of the loss (float32 [B, N], a view: that of a mean or a sum
+        may be one value expanded); what is not wanted is None."""
+        op = self._describe(x, table, targets)
+        d = _PACK_ROWS(*self._rows(d_loss, "d_loss", (self.B, self.N), self.torch.float32))
+        at = self._dense(lse, "lse", (self.B, self.N), self.torch.float32)
+        if not at:
+            raise ValueError("lse must be a torch tensor")
+        dx = self._out(None, "dx", (self.B, self.N, self.d), self.dtype) if want_dx else None
+        d_table = self._out(None, "d_table", (self.V, self.d), self.dtype) if want_table else None
+        if dx is None and d_table is None:
+            return None, None
+        scratch = self._scratch(self.backward_bytes)
+        self._call("hyena_token_loss_backward", self._lib.hyena_token_loss_backward, op, d, at,
+                   dx.data_ptr() if dx is not None else None, d_table.data_ptr() if d_table is not None else None,
+                   scratch.data_ptr(), self._stream())
+        return dx, d_table
