@@ -28,10 +28,12 @@ namespace {
 constexpr const char* kWho = "embedding";
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortGroups = 256;   // at least; more where a group would have more values than kSortValues
-constexpr int kSortValues = 768;   // counters of a wave: 48 KB of LDS in all
-constexpr int kSortTokens = 8;     // loads of a wave under way
+constexpr int kSortValues = 384;   // counters of a wave: 24 KB of LDS in all
+constexpr int kSortTokens = 16;    // of a lane, in four loads
+constexpr int kSortKept = 512;     // tokens of its values that a wave keeps: 32 KB of LDS in all
 constexpr int kSumRows = 4;        // gradient rows of a team under way
-constexpr int64_t kSumTeams = 8192;  // runs are no shorter than kSumRows, and as short as this many of them allow
+constexpr int64_t kSumTeams = 4096;  // runs are no shorter than kSumRows, and as short as this many of them allow
+constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64;
 
 struct EmbedArgs {
     Rows tokens, rows;   // rows: d_out
@@ -40,20 +42,46 @@ struct EmbedArgs {
     int64_t total;       // B * N
     uint32_t N, rows_N;  // row_at, of the tokens and of the rows
     int32_t V, d;
-    int32_t lanes, per;  // lanes of a team, units of a lane
+    int32_t lanes;       // of a team, a power of two
     int32_t pairs;
     int32_t accumulate;
     float scale;
     int32_t groups;      // of the sort, a power of two
-    int32_t run;         // tokens of a run
+    int32_t run;         // tokens of a run, a power of two
     int32_t sum_groups;  // workgroups of the sums, fill_groups behind them
     int32_t fill_groups;
     int32_t* counts;     // [V]
     int2* sorted;        // [total] value and token, in order; [total].x the number of tokens that take part
-    float* part;         // [runs][2][d]: sums that reach over a run's start and over its end
+    int4* joins;         // [V] values that reach over runs, where they begin, tokens: group g's from g * values on
+    int32_t* join_counts;  // [groups]
+    float* part;         // [runs][2][d4]: sums that reach over a run's start and over its end
+    int32_t d4;          // d rounded up to 4
 };
 
 __device__ __forceinline__ int token_at(const EmbedArgs& p, int64_t t) { return *row_at<int32_t>(p.tokens, t, p.N); }
+
+struct __attribute__((packed, aligned(4))) Four {
+    int v[4];
+};
+
+// A lane's kSortTokens tokens of a block: token t0 + 256 (k / 4) + 4 lane + k % 4 in
+// v[k], -1 at last and after it.
+template <bool DENSE> __device__ __forceinline__ void load_tokens(const EmbedArgs& p, int64_t t0, int64_t last, int (&v)[kSortTokens])
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 0; k < kSortTokens; k += 4) {
+        const int64_t t = t0 + 64 * k + 4 * lane;
+        if (DENSE && t + 4 <= last) {
+            const Four x = *(const Four*)((const int32_t*)p.tokens.p + t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[k + j] = x.v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[k + j] = t + j < last ? token_at(p, t + j) : -1;
+        }
+    }
+}
 
 template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_embedding_gather(EmbedArgs p)
 {
@@ -88,10 +116,11 @@ __device__ __forceinline__ int workgroup_sum(int x, int* lds)
     return x;
 }
 
-__global__ __launch_bounds__(kSortThreads) void hyena_embedding_sort(EmbedArgs p)
+template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embedding_sort(EmbedArgs p)
 {
-    extern __shared__ int counters[];  // [values][waves]
-    __shared__ int lds[kSortWaves];
+    extern __shared__ int counters[];  // [waves][values]
+    __shared__ int lds[kSortWaves], join_count;
+    __shared__ uint32_t kept[kSortWaves][kSortKept];
     const int group = blockIdx.x, shift = __builtin_ctz(p.groups);
     const int values = (p.V - group + p.groups - 1) >> shift;  // v = group + groups * i, i < values
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -100,22 +129,36 @@ __global__ __launch_bounds__(kSortThreads) void hyena_embedding_sort(EmbedArgs p
     const int64_t first = each * wave, last = first + each < p.total ? first + each : p.total;
 
     for (int i = threadIdx.x; i < values * kSortWaves; i += kSortThreads) counters[i] = 0;
+    if (threadIdx.x == 0) join_count = 0;
     __syncthreads();
     int lower = 0, all = 0;
+    int n_own = 0;  // this wave's tokens of the group's values; the first kSortKept are kept: i << 22 | place in its part
     for (int64_t t0 = first; t0 < last; t0 += 64 * kSortTokens) {
         int v[kSortTokens];
+        load_tokens<DENSE>(p, t0, last, v);
 #pragma unroll
-        for (int k = 0; k < kSortTokens; ++k) {
-            const int64_t t = t0 + 64 * k + lane;
-            v[k] = t < last ? token_at(p, t) : -1;
-        }
+        for (int k = 0; k < kSortTokens; k += 4) {
+            bool any = false;
 #pragma unroll
-        for (int k = 0; k < kSortTokens; ++k) {
-            const bool in = (uint32_t)v[k] < (uint32_t)p.V;
-            const int g = v[k] & (p.groups - 1);
-            all += in;
-            lower += in && g < group;
-            if (in && g == group) atomicAdd(&counters[(v[k] >> shift) * kSortWaves + wave], 1);
+            for (int j = 0; j < 4; ++j) {
+                const bool in = (uint32_t)v[k + j] < (uint32_t)p.V;
+                const int g = v[k + j] & (p.groups - 1);
+                all += in;
+                lower += in && g < group;
+                any = any || (in && g == group);
+            }
+            if (__ballot(any) == 0) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool own = (uint32_t)v[k + j] < (uint32_t)p.V && (v[k + j] & (p.groups - 1)) == group;
+                const uint64_t who = __ballot(own);
+                const int at = n_own + __popcll(who & (((uint64_t)1 << lane) - 1)), i = v[k + j] >> shift;
+                if (own) {
+                    atomicAdd(&counters[wave * values + i], 1);
+                    if (at < kSortKept) kept[wave][at] = (uint32_t)i << 22 | (uint32_t)(t0 - first + 64 * k + 4 * lane + j);
+                }
+                n_own += __popcll(who);
+            }
         }
     }
     lower = workgroup_sum(lower, lds);
@@ -128,7 +171,7 @@ __global__ __launch_bounds__(kSortThreads) void hyena_embedding_sort(EmbedArgs p
         const int i = threadIdx.x * n + k;
         if (i >= values) break;
         int c = 0;
-        for (int w = 0; w < kSortWaves; ++w) c += counters[i * kSortWaves + w];
+        for (int w = 0; w < kSortWaves; ++w) c += counters[w * values + i];
         p.counts[group + (int64_t)p.groups * i] = c;
         mine += c;
     }
@@ -143,71 +186,64 @@ __global__ __launch_bounds__(kSortThreads) void hyena_embedding_sort(EmbedArgs p
     before -= mine;
     for (int w = 0; w < wave; ++w) before += lds[w];
     before += lower;
+    const int run_shift = __builtin_ctz(p.run), most = (p.V + p.groups - 1) >> shift;
     for (int k = 0; k < n; ++k) {
         const int i = threadIdx.x * n + k;
         if (i >= values) break;
+        const int start = before;
         for (int w = 0; w < kSortWaves; ++w) {
-            const int c = counters[i * kSortWaves + w];
-            counters[i * kSortWaves + w] = before;
+            const int c = counters[w * values + i];
+            counters[w * values + i] = before;
             before += c;
         }
+        // (which of the list's places a value takes does not matter)
+        if (before > start && start >> run_shift != (before - 1) >> run_shift)
+            p.joins[(int64_t)group * most + atomicAdd(&join_count, 1)] = make_int4(group + p.groups * i, start, before - start, 0);
     }
     __syncthreads();
-    if (group == 0 && threadIdx.x == 0) p.sorted[p.total] = make_int2(all, 0);
-    // the same tokens again, each to its value's place; a wave's are in order
+    if (threadIdx.x == 0) {
+        p.join_counts[group] = join_count;
+        if (group == 0) p.sorted[p.total] = make_int2(all, 0);
+    }
+    // this wave's tokens, in the order they were read, each to its value's place
+    auto put = [&](bool own, int i, int64_t t) {
+        uint64_t left = __ballot(own);
+        while (left != 0) {  // one value of 64 tokens after the other
+            const int one = __builtin_amdgcn_readlane(i, __builtin_ctzll(left));
+            const bool same = own && i == one;
+            const uint64_t all_same = __ballot(same);
+            int* counter = &counters[wave * values + one];
+            const int place = *counter;
+            if (same) p.sorted[place + __popcll(all_same & (((uint64_t)1 << lane) - 1))] = make_int2(group + p.groups * i, (int)t);
+            *counter = place + __popcll(all_same);  // every lane the same value
+            left &= ~all_same;
+        }
+    };
+    if (n_own <= kSortKept && each <= 1 << 22) {
+        for (int k = 0; k < n_own; k += 64) {
+            const bool own = k + lane < n_own;
+            const uint32_t x = own ? kept[wave][k + lane] : 0;
+            put(own, (int)(x >> 22), first + (x & 0x3fffff));
+        }
+        return;
+    }
+    // too many to keep: the tokens again
     for (int64_t t0 = first; t0 < last; t0 += 64 * kSortTokens) {
         int v[kSortTokens];
+        load_tokens<DENSE>(p, t0, last, v);
 #pragma unroll
-        for (int k = 0; k < kSortTokens; ++k) {
-            const int64_t t = t0 + 64 * k + lane;
-            v[k] = t < last ? token_at(p, t) : -1;
-        }
-#pragma unroll
-        for (int k = 0; k < kSortTokens; ++k) {
-            const bool own = (uint32_t)v[k] < (uint32_t)p.V && (v[k] & (p.groups - 1)) == group;
-            uint64_t left = __ballot(own);
-            while (left != 0) {  // one value of these 64 tokens after the other
-                const int one = __builtin_amdgcn_readlane(v[k], __builtin_ctzll(left));
-                const bool same = own && v[k] == one;
-                const uint64_t all_same = __ballot(same);
-                int* counter = &counters[(one >> shift) * kSortWaves + wave];
-                const int place = *counter;
-                if (same) {
-                    const int at = place + __popcll(all_same & (((uint64_t)1 << lane) - 1));
-                    p.sorted[at] = make_int2(one, (int)(t0 + 64 * k + lane));
-                }
-                *counter = place + __popcll(all_same);  // every lane the same value
-                left &= ~all_same;
-            }
-        }
+        for (int k = 0; k < kSortTokens; ++k)
+            put((uint32_t)v[k] < (uint32_t)p.V && (v[k] & (p.groups - 1)) == group, v[k] >> shift, t0 + 64 * (k & ~3) + 4 * lane + (k & 3));
     }
 }
 
-// The unit at channel c of a row of the table's gradient: x times the scale, or
-// added to what is there.
-template <typename T, bool VEC>
-__device__ __forceinline__ void write_sum(const EmbedArgs& p, int v, int c, float (&x)[kUnit<T>])
-{
-    constexpr int K = kUnit<T>;
-    T* row = (T*)p.out + (int64_t)v * p.d;
-    if (p.accumulate) {
-        float old[K];
-        load_unit<T, VEC>(row, c, p.d, p.pairs, old);
-#pragma unroll
-        for (int i = 0; i < K; ++i) x[i] = fmaf(x[i], p.scale, old[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < K; ++i) x[i] *= p.scale;
-    }
-    store_unit<T, VEC>(row, c, p.d, p.pairs, x);
-}
-
-// U units of a lane at a time; blockIdx.y: which of the row's blocks of U * lanes units.
-template <typename T, bool VEC, int U> __global__ __launch_bounds__(256) void hyena_embedding_sums(EmbedArgs p)
+// blockIdx.y: which of the row's blocks of `lanes` units.
+template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_embedding_sums(EmbedArgs p)
 {
     constexpr int K = kUnit<T>;
     const int teams = 256 / p.lanes, team = threadIdx.x / p.lanes, tl = threadIdx.x % p.lanes;
-    const int c0 = (int)blockIdx.y * U * p.lanes * K;
+    const int c = ((int)blockIdx.y * p.lanes + tl) * K;
+    const bool in = c < p.d;
     float zero[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) zero[i] = 0.0f;
@@ -217,11 +253,7 @@ template <typename T, bool VEC, int U> __global__ __launch_bounds__(256) void hy
         for (int64_t v = (int64_t)((int)blockIdx.x - p.sum_groups) * teams + team; v < p.V; v += step) {
             if (p.counts[v] != 0) continue;
             T* row = (T*)p.out + v * p.d;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + (tl + u * p.lanes) * K;
-                if (c < p.d) store_unit<T, VEC>(row, c, p.d, p.pairs, zero);
-            }
+            if (in) store_unit<T, VEC>(row, c, p.d, p.pairs, zero);
         }
         return;
     }
@@ -229,111 +261,115 @@ template <typename T, bool VEC, int U> __global__ __launch_bounds__(256) void hy
     const int64_t run = (int64_t)blockIdx.x * teams + team, first = run * p.run;
     if (first >= n) return;
     const int64_t last = first + p.run < n ? first + p.run : n;
-    float s[U][K];
+    float s[K];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < K; ++i) s[u][i] = 0.0f;
+    for (int i = 0; i < K; ++i) s[i] = 0.0f;
     bool open = first > 0 && p.sorted[first - 1].x == p.sorted[first].x;  // the value began before this run
     const int next_value = last < n ? p.sorted[last].x : -1;
     for (int64_t i0 = first; i0 < last; i0 += kSumRows) {
         int2 e[kSumRows + 1];
-        float x[kSumRows][U][K];
 #pragma unroll
         for (int k = 0; k < kSumRows; ++k) {
             const int64_t i = i0 + k < last ? i0 + k : last - 1;
             e[k] = p.sorted[i];
         }
         e[kSumRows] = i0 + kSumRows < last ? p.sorted[i0 + kSumRows] : make_int2(next_value, 0);
+        // the last token of a value ends it, here or (at this run's end) in a later run
+        bool ends[kSumRows], on[kSumRows];
+#pragma unroll
+        for (int k = 0; k < kSumRows; ++k) {
+            const bool at_end = i0 + k + 1 >= last;
+            on[k] = (at_end ? next_value : e[k + 1].x) == e[k].x;
+            ends[k] = i0 + k < last && (at_end || !on[k]);
+        }
+        RawUnit<T, VEC> x[kSumRows], old[kSumRows];
 #pragma unroll
         for (int k = 0; k < kSumRows; ++k) {
             const T* row = row_at<T>(p.rows, e[k].y, p.rows_N);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + (tl + u * p.lanes) * K;
-                if (c < p.d) load_unit<T, VEC>(row, c, p.d, p.pairs, x[k][u]);
+            const T* there = (const T*)p.out + (int64_t)e[k].x * p.d;
+            if (in) {
+                x[k].load(row, c, p.d, p.pairs);
+                if (p.accumulate && ends[k]) old[k].load(there, c, p.d, p.pairs);
             }
         }
 #pragma unroll
         for (int k = 0; k < kSumRows; ++k) {
             if (i0 + k >= last) break;
-            const bool at_end = i0 + k + 1 == last;
-            const int following = at_end ? next_value : e[k + 1].x;
+            float y[K];
+            x[k].widen(y);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int i = 0; i < K; ++i) s[i] += y[i];
+            if (!ends[k]) continue;
+            if (in) {
+                if (open || on[k]) {  // a piece
+                    float* part = p.part + (run * 2 + (open ? 0 : 1)) * p.d4 + c;
 #pragma unroll
-                for (int i = 0; i < K; ++i) s[u][i] += x[k][u][i];
-            if (following == e[k].x && !at_end) continue;
-            // a value's last token here: its row, or a piece of it
-            const bool on = following == e[k].x;
+                    for (int i = 0; i < K; i += 4)
+                        if (c + i < p.d4) *(f32x4*)(part + i) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
+                } else {
+                    if (p.accumulate) old[k].widen(y);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + (tl + u * p.lanes) * K;
-                if (c < p.d) {
-                    if (open || on) {
-                        float* part = p.part + (run * 2 + (open ? 0 : 1)) * p.d;
-#pragma unroll
-                        for (int i = 0; i < K; ++i)
-                            if (VEC || c + i < p.d) part[c + i] = s[u][i];
-                    } else {
-                        write_sum<T, VEC>(p, e[k].x, c, s[u]);
-                    }
+                    for (int i = 0; i < K; ++i) y[i] = p.accumulate ? fmaf(s[i], p.scale, y[i]) : s[i] * p.scale;
+                    store_unit<T, VEC>((T*)p.out + (int64_t)e[k].x * p.d, c, p.d, p.pairs, y);
                 }
-#pragma unroll
-                for (int i = 0; i < K; ++i) s[u][i] = 0.0f;
             }
+#pragma unroll
+            for (int i = 0; i < K; ++i) s[i] = 0.0f;
             open = false;
         }
     }
 }
 
-// A workgroup for each run: the value that begins in it and goes on in the next
-// ones, 64 units of its row at a time, every wave some of the pieces.
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_embedding_joins(EmbedArgs p)
+// The values of one group of the sort that reach over runs, 256 channels of them.
+// Of few pieces: each wave its own values.  Of many: all waves some of the pieces, the
+// first wave the waves' sums.
+template <typename T> __global__ __launch_bounds__(kJoinThreads) void hyena_embedding_joins(EmbedArgs p)
 {
-    constexpr int K = kUnit<T>;
-    __shared__ float lds[4][64 * K];
-    const int64_t n = p.sorted[p.total].x;
-    const int64_t run = blockIdx.x, first = run * p.run, end = first + p.run;
-    if (end >= n) return;  // nothing comes after it
-    const int v = p.sorted[end - 1].x;
-    if (p.sorted[end].x != v) return;
-    const int count = p.counts[v];
-    // where it began: in this run, or this workgroup has nothing to do
-    if (first > 0 && p.sorted[first - 1].x == v) return;
-    int64_t begin = first;
-    while (p.sorted[begin].x != v) ++begin;
-    const int64_t pieces = (begin + count - 1) / p.run - run;  // runs after this one
+    __shared__ f32x4 lds[kJoinWaves][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    for (int c0 = 0; c0 < p.d; c0 += 64 * K) {
-        const int c = c0 + lane * K;
-        float s[K];
+    const int c = (int)blockIdx.y * 256 + lane * 4;
+    const int n = p.join_counts[blockIdx.x];
+    const int4* list = p.joins + (int64_t)blockIdx.x * ((p.V + p.groups - 1) / p.groups);
+    const int run_shift = __builtin_ctz(p.run);
+    auto pieces_of = [&](int4 e) { return ((e.y + e.z - 1) >> run_shift) - (e.y >> run_shift) + 1; };
+    auto sum = [&](int4 e, int from, int step) {
+        const int pieces = pieces_of(e);
+        const float* part = p.part + (int64_t)(e.y >> run_shift) * 2 * p.d4 + c;
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+        // the first piece is its run's last, the others their runs' first
+#pragma unroll 8
+        for (int k = from; k < pieces; k += step) s += *(const f32x4*)(part + ((int64_t)k * 2 + (k == 0)) * p.d4);
+        return s;
+    };
+    auto write = [&](int4 e, f32x4 s) {
+        T* row = (T*)p.out + (int64_t)e.x * p.d + c;
+        float old[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (p.accumulate) {
 #pragma unroll
-        for (int i = 0; i < K; ++i) s[i] = 0.0f;
-        if (c < p.d) {
-            if (wave == 0) {
-                const float* part = p.part + (run * 2 + 1) * p.d;
-#pragma unroll
-                for (int i = 0; i < K; ++i)
-                    if (VEC || c + i < p.d) s[i] = part[c + i];
-            }
-#pragma unroll 4
-            for (int64_t k = 1 + wave; k <= pieces; k += 4) {
-                const float* part = p.part + (run + k) * 2 * p.d;
-#pragma unroll
-                for (int i = 0; i < K; ++i)
-                    if (VEC || c + i < p.d) s[i] += part[c + i];
-            }
+            for (int i = 0; i < 4; ++i)
+                if (c + i < p.d) old[i] = load_one<T>(row + i);
         }
-        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < K; ++i) lds[wave][i * 64 + lane] = s[i];
+        for (int i = 0; i < 4; ++i)
+            if (c + i < p.d) store_one<T>(row + i, fmaf(s[i], p.scale, old[i]));
+    };
+    for (int i = wave; i < n; i += kJoinWaves) {
+        const int4 e = list[i];
+        if (pieces_of(e) <= kJoinWaves && c < p.d) write(e, sum(e, 0, 1));
+    }
+    for (int i = 0; i < n; ++i) {
+        const int4 e = list[i];
+        if (pieces_of(e) <= kJoinWaves) continue;
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (c < p.d) s = sum(e, wave, kJoinWaves);
+        lds[wave][lane] = s;
         __syncthreads();
         if (wave == 0 && c < p.d) {
 #pragma unroll
-            for (int i = 0; i < K; ++i) s[i] = lds[0][i * 64 + lane] + lds[1][i * 64 + lane] + lds[2][i * 64 + lane] + lds[3][i * 64 + lane];
-            write_sum<T, VEC>(p, v, c, s);
+            for (int w = 1; w < kJoinWaves; ++w) s += lds[w][lane];
+            write(e, s);
         }
+        __syncthreads();
     }
 }
 
@@ -351,7 +387,8 @@ hyena_status embed_sizes(const hyena_embedding* op)
 
 struct EmbedSpace {
     int64_t run, runs;
-    size_t sorted, counts, part, total;  // byte offsets and the size
+    size_t sorted, counts, joins, join_counts, part, total;  // byte offsets and the size
+    int32_t groups, d4;
 };
 
 EmbedSpace embed_space(const hyena_embedding* op)
@@ -359,54 +396,52 @@ EmbedSpace embed_space(const hyena_embedding* op)
     EmbedSpace w;
     const int64_t T = op->B * op->N;
     const int64_t most = (T + kSumTeams - 1) / kSumTeams;
-    w.run = most < kSumRows ? kSumRows : (most + kSumRows - 1) / kSumRows * kSumRows;
+    w.run = kSumRows;
+    while (w.run < most) w.run *= 2;
     w.runs = (T + w.run - 1) / w.run;
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     w.sorted = 0;
     w.counts = up((size_t)(T + 1) * sizeof(int2));
-    w.part = w.counts + up((size_t)op->V * 4);
-    w.total = w.part + (size_t)w.runs * 2 * (size_t)op->d * 4;
+    w.groups = kSortGroups;
+    while ((op->V + w.groups - 1) / w.groups > kSortValues) w.groups *= 2;
+    w.d4 = (int32_t)((op->d + 3) / 4 * 4);
+    w.joins = w.counts + up((size_t)op->V * 4);
+    w.join_counts = w.joins + up((size_t)((op->V + w.groups - 1) / w.groups * w.groups) * sizeof(int4));
+    w.part = w.join_counts + up((size_t)w.groups * 4);
+    w.total = w.part + (size_t)w.runs * 2 * (size_t)w.d4 * 4;
     return w;
 }
 
+// Lanes of a team, which hold a unit each: 64, or 32 if that leaves fewer of them idle
+// over a row.
 void team_shape(EmbedArgs& a, size_t element)
 {
-    // as many lanes of a wave as leave the fewest idle with at most 4 units each
     const int units = (int)((a.d * element + 15) / 16);
-    int best = 64;
-    for (int n = 64; n >= 1; n /= 2) {
-        const int per = (units + n - 1) / n;
-        if (per > 4) break;
-        if (per * n < ((units + best - 1) / best) * best) best = n;
-    }
-    a.lanes = best;
-    a.per = (units + best - 1) / best;
-}
-
-template <typename T, int U> hyena_status launch_sums(const EmbedArgs& a, bool vec, hipStream_t s)
-{
-    const int block = U * a.lanes * kUnit<T>;
-    const dim3 grid((unsigned)(a.sum_groups + a.fill_groups), (unsigned)((a.d + block - 1) / block));
-    if (vec)
-        HY_LAUNCH(kernel_label("hyena_embedding_sums", type_label<T>(), true, U), (hyena_embedding_sums<T, true, U>), grid, dim3(256), 0, s, a);
-    else
-        HY_LAUNCH(kernel_label("hyena_embedding_sums", type_label<T>(), false, U), (hyena_embedding_sums<T, false, U>), grid, dim3(256), 0, s, a);
-    return launched();
+    auto used = [&](int n) { return (units + n - 1) / n * n; };
+    a.lanes = 64;
+    if (used(32) < used(64)) a.lanes = 32;
 }
 
 template <typename T> hyena_status embed_backward(const EmbedArgs& a, bool vec, int64_t runs, hipStream_t s)
 {
     hyena_status st;
-    HY_LAUNCH(kernel_label("hyena_embedding_sort"), hyena_embedding_sort, dim3((unsigned)a.groups), dim3(kSortThreads),
-              (size_t)((a.V + a.groups - 1) / a.groups) * kSortWaves * 4, s, a);
-    if ((st = launched()) != HYENA_OK) return st;
-    const int u = a.per < 4 ? a.per : 4;
-    st = u == 1 ? launch_sums<T, 1>(a, vec, s) : u == 2 ? launch_sums<T, 2>(a, vec, s) : u == 3 ? launch_sums<T, 3>(a, vec, s) : launch_sums<T, 4>(a, vec, s);
-    if (st != HYENA_OK || runs < 2) return st;
-    if (vec)
-        HY_LAUNCH(kernel_label("hyena_embedding_joins", type_label<T>(), true), (hyena_embedding_joins<T, true>), dim3((unsigned)(runs - 1)), dim3(256), 0, s, a);
+    const dim3 sort_grid((unsigned)a.groups);
+    const size_t sort_lds = (size_t)((a.V + a.groups - 1) / a.groups) * kSortWaves * 4;
+    if (a.N == 0 && a.tokens.t == 1)
+        HY_LAUNCH(kernel_label("hyena_embedding_sort", true), hyena_embedding_sort<true>, sort_grid, dim3(kSortThreads), sort_lds, s, a);
     else
-        HY_LAUNCH(kernel_label("hyena_embedding_joins", type_label<T>(), false), (hyena_embedding_joins<T, false>), dim3((unsigned)(runs - 1)), dim3(256), 0, s, a);
+        HY_LAUNCH(kernel_label("hyena_embedding_sort", false), hyena_embedding_sort<false>, sort_grid, dim3(kSortThreads), sort_lds, s, a);
+    if ((st = launched()) != HYENA_OK) return st;
+    const int block = a.lanes * kUnit<T>;
+    const dim3 grid((unsigned)(a.sum_groups + a.fill_groups), (unsigned)((a.d + block - 1) / block));
+    if (vec)
+        HY_LAUNCH(kernel_label("hyena_embedding_sums", type_label<T>(), true), (hyena_embedding_sums<T, true>), grid, dim3(256), 0, s, a);
+    else
+        HY_LAUNCH(kernel_label("hyena_embedding_sums", type_label<T>(), false), (hyena_embedding_sums<T, false>), grid, dim3(256), 0, s, a);
+    st = launched();
+    if (st != HYENA_OK || runs < 2) return st;
+    HY_LAUNCH(kernel_label("hyena_embedding_joins", type_label<T>()), hyena_embedding_joins<T>,
+              dim3((unsigned)a.groups, (unsigned)((a.d + 255) / 256)), dim3(kJoinThreads), 0, s, a);
     return launched();
 }
 
@@ -505,8 +540,10 @@ hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_row
     a.rows_N = (uint32_t)N;
     a.out = d_table;
     a.accumulate = accumulate != 0;
-    a.groups = kSortGroups;
-    while ((a.V + a.groups - 1) / a.groups > kSortValues) a.groups *= 2;
+    a.groups = w.groups;
+    a.d4 = w.d4;
+    a.joins = (int4*)((char*)scratch + w.joins);
+    a.join_counts = (int32_t*)((char*)scratch + w.join_counts);
     a.run = (int32_t)w.run;
     a.sorted = (int2*)((char*)scratch + w.sorted);
     a.counts = (int32_t*)((char*)scratch + w.counts);

@@ -18,6 +18,7 @@ struct NormArgs {
     int32_t d;
     int32_t lanes;       // of a team that is part of a wave
     int32_t pairs;
+    int32_t weight_vectors;  // weight is 16-byte aligned
     int32_t int8;
     int32_t group_lanes; // 0: a scale for each row
     int32_t groups;      // of a row

@@ -135,6 +135,7 @@ hyena_status hyena_residual_norm_forward(const hyena_residual_norm* op, void* su
     a.x = Rows{x.data, x.batch, x.token};
     a.res = Rows{res.data, res.batch, res.token};
     a.w = op->weight;
+    a.weight_vectors = (uintptr_t)op->weight % 16 == 0;
     a.sum = sum;
     a.y = y;
     a.scales = scales;
@@ -213,6 +214,7 @@ hyena_status hyena_residual_norm_backward(const hyena_residual_norm* op, const h
     a.dy = Rows{dy.data, dy.batch, dy.token};
     a.res = Rows{ds.data, ds.batch, ds.token};
     a.w = op->weight;
+    a.weight_vectors = (uintptr_t)op->weight % 16 == 0;
     a.y = d_x;
     a.dw_part = d_weight ? (float*)scratch : nullptr;
     a.N = (uint32_t)N;

@@ -61,6 +61,26 @@ template <bool WG> __device__ __forceinline__ uint32_t team_max(uint32_t a, int 
 
 __device__ __forceinline__ float rms(float squares, int d, float eps) { return 1.0f / sqrtf(squares / (float)d + eps); }
 
+// The weights of a unit (ones without).
+template <bool VEC, int K> __device__ __forceinline__ void load_weights(const NormArgs& p, int c, float (&w)[K])
+{
+#pragma unroll
+    for (int i = 0; i < K; ++i) w[i] = 1.0f;
+    if (p.w == nullptr || c >= p.d) return;
+    if (VEC && p.weight_vectors) {
+#pragma unroll
+        for (int i = 0; i < K; i += 4) {
+            const f32x4 v = *(const f32x4*)(p.w + c + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i + j] = v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (c + i < p.d) w[i] = p.w[c + i];
+    }
+}
+
 // K units of 8-bit values, K = 4 or 8.
 template <int K> __device__ __forceinline__ void pack8(const float (&y)[K], bool int8, uint32_t (&w)[K / 4])
 {
@@ -89,8 +109,7 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm(NormArgs 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int c = (tl + u * lanes) * K;
-#pragma unroll
-        for (int i = 0; i < K; ++i) w[u][i] = p.w != nullptr && c + i < p.d ? p.w[c + i] : 1.0f;
+        load_weights<VEC>(p, c, w[u]);
     }
     for (int64_t r = (int64_t)blockIdx.x * teams + team; r < p.rows; r += (int64_t)gridDim.x * teams) {
         const T* x = row_at<T>(p.x, r, p.N);
@@ -200,11 +219,9 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(Norm
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int c = (tl + u * lanes) * K;
+        load_weights<VEC>(p, c, w[u]);
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-            w[u][i] = p.w != nullptr && c + i < p.d ? p.w[c + i] : 1.0f;
-            dw[u][i] = 0.0f;
-        }
+        for (int i = 0; i < K; ++i) dw[u][i] = 0.0f;
     }
     for (int64_t r = (int64_t)blockIdx.x * teams + team; r < p.rows; r += (int64_t)gridDim.x * teams) {
         const T* x = row_at<T>(p.x, r, p.N);

@@ -62,6 +62,28 @@ __device__ __forceinline__ void load_unit(const T* row, int c, int d, bool pairs
     }
 }
 
+// A unit as loaded, for loads that are to be under way together: 16-byte accesses
+// keep its 16 bytes and widen them later.
+template <typename T, bool VEC> struct RawUnit {
+    float x[kUnit<T>];
+    __device__ __forceinline__ void load(const T* row, int c, int d, bool pairs) { load_unit<T, false>(row, c, d, pairs, x); }
+    __device__ __forceinline__ void widen(float (&y)[kUnit<T>]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kUnit<T>; ++i) y[i] = x[i];
+    }
+};
+template <typename T> struct RawUnit<T, true> {
+    uint4 v;
+    __device__ __forceinline__ void load(const T* row, int c, int, bool) { v = *(const uint4*)(row + c); }
+    __device__ __forceinline__ void widen(float (&y)[kUnit<T>]) const
+    {
+        const T* e = (const T*)&v;
+#pragma unroll
+        for (int i = 0; i < kUnit<T>; ++i) y[i] = load_one<T>(e + i);
+    }
+};
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_unit(T* row, int c, int d, bool pairs, const float (&x)[kUnit<T>])
 {
