@@ -1,16 +1,26 @@
 // matmul_device.h -- a tile of a matrix product of 16-bit operands on MFMA.
 //
 // C[m][n] = sum over k of A(m, k) B(n, k): a workgroup of WM x WN waves makes a
-// tile of TM x TN, k in steps of 32.  An operand is stored with k or with its own
-// axis contiguous; both go through LDS and come back as the fragments of 16x16x32
-// instructions (8 values of k for each lane):
-//   k contiguous:    an LDS row is 32 values of k, four 16-byte chunks; chunk c of
-//                    row m is kept at c ^ ((m >> 1) & 3), so that the eight lanes
-//                    that one cycle serves read eight different 16-byte slots;
-//   axis contiguous: an LDS row is one k; its 32-byte blocks are kept at
-//                    b ^ key(k), so that the four rows that 16 lanes read together
-//                    lie in different banks.  ds_read_b64_tr_b16 turns 4 k x 16
-//                    values on the way into the registers.
+// tile of TM x TN, k in steps of 32.
+//
+// Operands lie in blocks of 32 columns, [columns / 32][rows][32]: 64 bytes of a row,
+// the rows of a block one after the other.  k is either the columns or the rows:
+//   k in the columns: a step of a tile is W rows of one block, W * 64 bytes in a
+//       piece; 16-byte chunk c of row m is kept in LDS at c ^ ((m >> 1) & 3), so that
+//       the eight lanes that one cycle serves read eight different 16-byte slots
+//       (in pairs: two 16-row fragments take 4 rows of 8 in turn, so that a lane's results of
+//       the two are 8 rows in a row);
+//   k in the rows: a step is 32 rows of W / 32 blocks, 2 KB pieces; the 32-byte half h
+//       of row k is kept at h ^ key(k), so that the rows that lanes read together lie
+//       in different banks.  ds_read_b64_tr_b16 turns 4 k x 16 columns on the way into
+//       the registers.
+// Both bring memory to LDS in contiguous KBs.  (An operand whose rows are whole is read in
+// the same way by its strides, 64 bytes here and there: products of 16384 x 16384 x
+// 768 run at 997 TFLOP/s so, at 1150 to 1390 with blocks.)
+//
+// Loads go to LDS directly, a step ahead of the products (of a step's 512 cycles of
+// matrix instructions per wave little else has to be issued; staged in registers the
+// same product ran at 854).  No bank conflicts.
 // A lane's results: row 4 (lane / 16) + r of a 16 x 16 tile, column lane % 16.
 #pragma once
 
@@ -22,11 +32,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // What a tile reads of one operand: `at` its first byte at k = 0, `end` the end of
 // the memory (what lies there and after it is read as 0), `row` the bytes from one
-// row of the storage to the next.
+// row to the next, `block` from one 32 columns to the next.
 struct Operand {
     const char* at;
     const char* end;
-    int64_t row;
+    int64_t row, block;
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t operand_rsrc(const char* at, const char* end)
@@ -36,52 +46,70 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t operand_rsrc(const char* at, c
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), (short)0, n, 0x00020000);
 }
 
-// One operand of a tile: W rows of the output's axis; KC: k contiguous.
-template <int W, int THREADS, bool KC> struct Stage {
+// 16 bytes of each lane to LDS, side by side from byte `lds` on.  The compiler does
+// not know of these loads: wait_loads before the barrier that publishes them.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, __amdgpu_buffer_rsrc_t r)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
+}
+template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
+// A barrier of what wait_loads has waited for: no other memory access is waited for.
+__device__ __forceinline__ void barrier_only()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+enum Form { kInRows, kInColumns, kInColumnsPaired };  // where k is
+
+// One operand of a tile: W rows of the output's axis.
+template <int W, int THREADS, Form F> struct Stage {
+    static constexpr bool KC = F != kInRows;
     static constexpr int kBytes = W * 64;           // of a step in LDS
-    static constexpr int kLoads = W * 4 / THREADS;  // 16-byte loads of a thread
-    static_assert(W * 4 % THREADS == 0 && W % 16 == 0, "");
-    static constexpr int kRowChunks = KC ? 4 : W / 8;
-    static constexpr int kBlocks = W / 16;          // 32-byte blocks of a row (axis contiguous)
+    static constexpr int kLoads = W * 4 / THREADS;  // of a thread, 16 bytes each
+    static_assert(W * 4 % THREADS == 0 && W % 32 == 0, "");
 
     uint32_t off[kLoads];  // bytes from `at`
-    u32x4 x[kLoads];
 
-    __device__ __forceinline__ void init(int64_t row)
+    static __device__ __forceinline__ int key(int k) { return ((k >> 1) ^ (k >> 3)) & 1; }
+    static __device__ __forceinline__ int chunk_key(int row)
+    {
+        return F == kInColumnsPaired ? ((row >> 1) & 1) | ((row >> 3) & 1) << 1 : (row >> 1) & 3;
+    }
+    __device__ __forceinline__ void init(const Operand& o)
     {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int n = (int)threadIdx.x + i * THREADS;
-            off[i] = (uint32_t)((n / kRowChunks) * (uint32_t)row + (n % kRowChunks) * 16);
+            const int n = (int)threadIdx.x + i * THREADS, s = n & 3;  // the 16 bytes of LDS that it fills
+            if constexpr (KC) {
+                const int row = n >> 2;
+                off[i] = (uint32_t)row * (uint32_t)o.row + (uint32_t)((s ^ chunk_key(row)) * 16);
+            } else {
+                const int k = (n >> 2) & 31;
+                off[i] = (uint32_t)(n >> 7) * (uint32_t)o.block + (uint32_t)k * (uint32_t)o.row +
+                         (uint32_t)((((s >> 1) ^ key(k)) << 1 | (s & 1)) * 16);
+            }
         }
     }
-    __device__ __forceinline__ void load(const char* at, const char* end)
+    __device__ __forceinline__ void load(uint32_t lds, const char* at, const char* end) const
     {
         const __amdgpu_buffer_rsrc_t r = operand_rsrc(at, end);
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) x[i] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off[i], 0, 0);
+        for (int i = 0; i < kLoads; ++i) load_to_lds(lds + i * THREADS * 16 + wave * 1024, off[i], r);
     }
     // Bytes from one step's first value to the next one's.
-    static __device__ __forceinline__ int64_t step(int64_t row) { return KC ? 64 : 32 * row; }
-    static __device__ __forceinline__ int key(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
-    __device__ __forceinline__ void store(char* lds) const
-    {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int n = (int)threadIdx.x + i * THREADS, row = n / kRowChunks, c = n % kRowChunks;
-            int at;
-            if constexpr (KC) at = row * 64 + ((c ^ ((row >> 1) & 3)) * 16);
-            else at = row * (W * 2) + ((((c >> 1) ^ (key(row) % kBlocks)) << 5) | (c & 1) << 4);
-            *(u32x4*)(lds + at) = x[i];
-        }
-    }
-    // The fragment of the 16 rows at m0.
-    template <typename F> static __device__ __forceinline__ F fragment(const char* lds, int m0)
+    static __device__ __forceinline__ int64_t step(const Operand& o) { return KC ? o.block : 32 * o.row; }
+    // The fragment of the 16 rows at m0 (paired: of 16 of the 32 rows around it).
+    template <typename V> static __device__ __forceinline__ V fragment(const char* lds, int m0)
     {
         const int lane = threadIdx.x & 63;
         if constexpr (KC) {
-            const int m = m0 + (lane & 15), c = lane >> 4;
-            return *(const F*)(lds + m * 64 + ((c ^ ((m >> 1) & 3)) * 16));
+            const int i = lane & 15, c = lane >> 4;
+            const int m = F == kInColumnsPaired ? (m0 & ~31) + 8 * (i >> 2) + ((m0 >> 4) & 1) * 4 + (i & 3) : m0 + i;
+            return *(const V*)(lds + m * 64 + ((c ^ chunk_key(m)) * 16));
         } else {
             typedef __attribute__((address_space(3))) s16x4* at3;
             const int g = lane >> 4, i = lane & 15;
@@ -89,10 +117,10 @@ template <int W, int THREADS, bool KC> struct Stage {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = g * 8 + h * 4 + (i >> 2);
-                const char* p = lds + k * (W * 2) + (((m0 >> 4) ^ (key(k) % kBlocks)) << 5) + (i & 3) * 8;
+                const char* p = lds + (m0 >> 5) * 2048 + k * 64 + ((((m0 >> 4) & 1) ^ key(k)) << 5) + (i & 3) * 8;
                 v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at3)p);
             }
-            return __builtin_bit_cast(F, v);
+            return __builtin_bit_cast(V, v);
         }
     }
 };
@@ -106,35 +134,46 @@ template <int NP> struct Planes {
     static __device__ __forceinline__ int b(int i) { return NP == 1 ? 0 : (0x010201 >> (4 * i)) & 15; }
 };
 
-// E: uint16_t (bfloat16) or _Float16.
-template <typename E, int TM, int TN, int WM, int WN, bool AK, bool BK, int NP> struct MatTile {
+// E: uint16_t (bfloat16) or _Float16.  STAGES - 1 steps are under way.
+template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, int STAGES> struct MatTile {
     static constexpr int kThreads = WM * WN * 64;
-    using A = Stage<TM, kThreads, AK>;
-    using B = Stage<TN, kThreads, BK>;
-    static constexpr int kStep = A::kBytes + B::kBytes, kLds = 2 * kStep;
+    using A = Stage<TM, kThreads, AF>;
+    using B = Stage<TN, kThreads, BF>;
+    static constexpr int kStep = A::kBytes + B::kBytes, kLds = STAGES * kStep;
     static constexpr int MI = TM / WM / 16, NI = TN / WN / 16;
     using frag = typename Mx<E>::frag;
 
     f32x4 c[MI][NI];
 
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
     // aplane, bplane: bytes between planes.  steps: of 32 values of k, at least 1.
+    // Ends behind a barrier after the last read of lds.
     __device__ __forceinline__ void run(char* lds, const Operand& oa, int64_t aplane, const Operand& ob, int64_t bplane,
                                         int steps)
     {
         const int wave = threadIdx.x >> 6;
         const int m0 = wave / WN * (TM / WM), n0 = wave % WN * (TN / WN);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        clear();
         A a;
         B b;
-        a.init(oa.row);
-        b.init(ob.row);
-        const int64_t astep = A::step(oa.row), bstep = B::step(ob.row);
+        a.init(oa);
+        b.init(ob);
+        const int64_t astep = A::step(oa), bstep = B::step(ob);
         const int total = steps * Planes<NP>::kPairs;
+        const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
         int pair = 0, left = steps;
-        auto move = [&](const char*& pa, const char*& ea, const char*& pb, const char*& eb) {
+        const char *pa = oa.at + Planes<NP>::a(0) * aplane, *ea = oa.end + Planes<NP>::a(0) * aplane;
+        const char *pb = ob.at + Planes<NP>::b(0) * bplane, *eb = ob.end + Planes<NP>::b(0) * bplane;
+        auto issue = [&](int stage) {
+            a.load(base + stage * kStep, pa, ea);
+            b.load(base + stage * kStep + A::kBytes, pb, eb);
             pa += astep;
             pb += bstep;
             if (NP > 1 && --left == 0 && ++pair < Planes<NP>::kPairs) {
@@ -143,37 +182,30 @@ template <typename E, int TM, int TN, int WM, int WN, bool AK, bool BK, int NP> 
                 pb = ob.at + Planes<NP>::b(pair) * bplane, eb = ob.end + Planes<NP>::b(pair) * bplane;
             }
         };
-        const char *pa = oa.at + Planes<NP>::a(0) * aplane, *ea = oa.end + Planes<NP>::a(0) * aplane;
-        const char *pb = ob.at + Planes<NP>::b(0) * bplane, *eb = ob.end + Planes<NP>::b(0) * bplane;
-        a.load(pa, ea);
-        b.load(pb, eb);
-        move(pa, ea, pb, eb);
-        a.store(lds);
-        b.store(lds + A::kBytes);
-        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i)
+            if (i < total) issue(i);
+        int now = 0, into = STAGES - 1;
         for (int s = 0; s < total; ++s) {
-            const char* now = lds + (s & 1) * kStep;
-            char* next = lds + ((s + 1) & 1) * kStep;
-            if (s + 1 < total) {
-                a.load(pa, ea);
-                b.load(pb, eb);
-                move(pa, ea, pb, eb);
-            }
+            // this step's loads are done: those of later steps may be under way
+            if (STAGES > 2 && s + STAGES - 1 <= total) wait_loads<(STAGES - 2) * (A::kLoads + B::kLoads)>();
+            else wait_loads<0>();
+            barrier_only();
+            if (s + STAGES - 1 < total) issue(into);
+            const char* at = lds + now * kStep;
             frag fa[MI], fb[NI];
 #pragma unroll
-            for (int j = 0; j < NI; ++j) fb[j] = B::template fragment<frag>(now + A::kBytes, n0 + 16 * j);
+            for (int j = 0; j < NI; ++j) fb[j] = B::template fragment<frag>(at + A::kBytes, n0 + 16 * j);
 #pragma unroll
-            for (int i = 0; i < MI; ++i) fa[i] = A::template fragment<frag>(now, m0 + 16 * i);
+            for (int i = 0; i < MI; ++i) fa[i] = A::template fragment<frag>(at, m0 + 16 * i);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < NI; ++j) c[i][j] = Mx<E>::mma(fa[i], fb[j], c[i][j]);
-            if (s + 1 < total) {
-                a.store(next);
-                b.store(next + A::kBytes);
-            }
-            __syncthreads();
+            now = now + 1 == STAGES ? 0 : now + 1;
+            into = into + 1 == STAGES ? 0 : into + 1;
         }
+        barrier_only();
     }
 };
 

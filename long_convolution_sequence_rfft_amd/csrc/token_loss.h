@@ -34,14 +34,14 @@ struct LossArgs {
     int32_t* target;       // [tokens]
     float* weight;         // [tokens] d_loss
     float* lse2;           // [tokens] lse / ln 2
-    char* rows;            // gathered x: [planes][tokens rounded up][kd], 16-bit
+    char* rows;            // gathered x: [planes][kd / 32][tokens rounded up][32], 16-bit
     int64_t rows_plane;    // bytes
-    const char* values;    // the table as matrix operand: itself, or [planes][V][kd]
-    int64_t values_row, values_plane;
+    const char* values;    // the table as matrix operand: itself, or [planes][kd / 32][V][32]
+    int64_t values_row, values_block, values_plane, values_bytes;  // bytes: of a row, 32 channels, a plane; the first plane's
     float2* part;          // [tiles of values][tokens rounded up]: largest, sum
-    float* hit;            // [tokens] the target's logit
-    char* g;               // [planes][tokens rounded up][chunk]
-    int64_t g_row, g_plane;
+    float* hit;            // [tokens] the target's logit; backward: what rounding took from G there
+    char* g;               // [planes][chunk / 32][tokens rounded up][32]
+    int64_t g_plane;
     float* acc;            // [splits][tokens rounded up][acc_row] d_x
     int64_t tokens;        // rounded up
     int32_t acc_row;

@@ -9,9 +9,9 @@ constexpr const char* kWho = "token loss";
 
 // G of a piece of the vocabulary takes about this much, or a tile of values if that
 // is more.
-constexpr int64_t kGradBytes = (int64_t)256 << 20;
-// Workgroups that d_x's sums are cut for.
-constexpr int64_t kSplitGroups = 512;
+constexpr int64_t kGradBytes = (int64_t)1024 << 20;
+// Workgroups that d_x's sums are cut for, and into which part of their time.
+constexpr int64_t kSplitGroups = 512, kSplitParts = 4;
 
 hyena_status refuse(const char* what) { return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(kWho) + ": " + what); }
 
@@ -25,7 +25,13 @@ hyena_status loss_sizes(const hyena_token_loss* op)
     return check_io(kWho, op->io_dtype);
 }
 
-bool needs_pack(const hyena_token_loss* op) { return op->io_dtype == HYENA_F32 || op->d % 8 != 0; }
+// Calls of more tokens than this bring the table into the matrix operands' form first.
+constexpr int64_t kPackTokens = 256;
+
+bool needs_pack(const hyena_token_loss* op)
+{
+    return op->io_dtype == HYENA_F32 || op->d % 8 != 0 || op->B * op->N > kPackTokens;
+}
 
 // Sizes, and with a scratch the addresses in it; returns the bytes.
 size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a)
@@ -55,17 +61,20 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     a.rows_plane = (int64_t)tokens * a.kd * 2;
     a.rows = take((size_t)(planes * a.rows_plane));
     if (needs_pack(op)) {
-        a.values_row = (int64_t)a.kd * 2;
-        a.values_plane = (int64_t)a.V * a.values_row;
+        a.values_row = 64;
+        a.values_block = (int64_t)a.V * 64;
+        a.values_bytes = a.values_plane = a.kd / 32 * a.values_block;
         a.values = take((size_t)(planes * a.values_plane));
     } else {
         a.values_row = (int64_t)a.d * 2;
+        a.values_block = 64;
         a.values_plane = 0;
+        a.values_bytes = (int64_t)a.V * a.values_row;
         a.values = (const char*)op->table;
     }
+    a.hit = (float*)take(tokens * 4);
     if (!grad) {
         a.part = (float2*)take((size_t)((a.V + kLossValues - 1) / kLossValues) * tokens * 8);
-        a.hit = (float*)take(tokens * 4);
         return at;
     }
     a.place = (int32_t*)take((size_t)a.total * 4);
@@ -74,13 +83,17 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     const int64_t whole = (a.V + kLossValues - 1) / kLossValues, fit = kGradBytes / (a.tokens * 2 * planes * kLossValues);
     int64_t tiles = fit < 1 ? 1 : fit < whole ? fit : whole;
     const int64_t pieces = (whole + tiles - 1) / tiles;
-    tiles = (whole + pieces - 1) / pieces;  // pieces of one size
+    tiles = (whole + pieces - 1) / pieces;  // pieces of one size, and as many tiles for each XCD
+    if (tiles > 8) tiles = (tiles + 7) / 8 * 8;
     a.chunk = (int32_t)(tiles * kLossValues);
-    a.g_row = (int64_t)a.chunk * 2;
-    a.g_plane = a.tokens * a.g_row;
+    a.g_plane = a.tokens * a.chunk * 2;
     a.g = take((size_t)(planes * a.g_plane));
-    const int64_t base = (a.tokens / kGradRows) * ((a.d + kGradChannels - 1) / kGradChannels);
-    int64_t splits = kSplitGroups / base;
+    // d_x's sums over a piece are cut so that their workgroups, which come last, take a part
+    // of what all of the piece's work takes on kSplitGroups of them
+    const int64_t channel_tiles = (a.d + kGradChannels - 1) / kGradChannels, dx_tiles = a.tokens / kGradRows * channel_tiles;
+    const int64_t dx_steps = a.chunk / 32, table_steps = a.tokens / 32, table_tiles = a.chunk / kGradRows * channel_tiles;
+    const int64_t share = (dx_tiles * dx_steps + table_tiles * table_steps) / kSplitGroups;
+    int64_t splits = share < 1 ? 16 : (kSplitParts * dx_steps + share - 1) / share;
     const int64_t most = a.chunk / 512 < 1 ? 1 : a.chunk / 512;  // a part has 512 values at least
     splits = splits < 1 ? 1 : splits > most ? most : splits > 16 ? 16 : splits;
     a.splits = (int32_t)splits;

@@ -29,7 +29,7 @@ template <> struct LossType<float> {
 };
 
 // Eight float32 values as P planes of E, by cutting (bfloat16, P = 3) or rounding.
-template <typename E, int P> __device__ __forceinline__ void store_planes8(char* to, int64_t plane, f32x8 x)
+template <typename E, int P> __device__ __forceinline__ void store_planes(char* to, int64_t plane, f32x8 x)
 {
     Split<E, P> s;
     s.set(x);
@@ -104,7 +104,7 @@ template <typename T, bool VEC, bool GRAD> __global__ __launch_bounds__(1024) vo
     }
     for (int64_t a = begin + wave; a < end; a += 16) {
         const T* x = a < before ? row_at<T>(p.x, p.index[a], p.x_N) : nullptr;
-        char* to = p.rows + a * p.kd * 2;
+        char* to = p.rows + a * 64;
         for (int c = lane * 8; c < p.kd; c += 512) {
             f32x8 v = {};
             if (x != nullptr && c < p.d) {
@@ -123,7 +123,7 @@ template <typename T, bool VEC, bool GRAD> __global__ __launch_bounds__(1024) vo
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = e[i];
             }
-            store_planes8<E, P>(to + c * 2, p.rows_plane, v);
+            store_planes<E, P>(to + (c >> 5) * p.tokens * 64 + (c & 31) * 2, p.rows_plane, v);
         }
     }
     if constexpr (GRAD) {
@@ -153,7 +153,7 @@ template <typename T, bool VEC, bool GRAD> __global__ __launch_bounds__(1024) vo
     }
 }
 
-// The table in rows of kd, as P planes.
+// The table in blocks of 32 channels, [kd / 32][V][32], as P planes.
 template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_loss_pack(LossArgs p)
 {
     using E = typename LossType<T>::E;
@@ -161,7 +161,7 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_los
     const int lane = threadIdx.x & 63;
     for (int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); v < p.V; v += (int64_t)gridDim.x * 4) {
         const T* row = (const T*)p.table + v * p.d;
-        char* to = const_cast<char*>(p.values) + v * p.values_row;
+        char* to = const_cast<char*>(p.values) + v * 64;
         for (int c = lane * 8; c < p.kd; c += 512) {
             f32x8 x = {};
 #pragma unroll
@@ -173,50 +173,86 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_los
 #pragma unroll
                 for (int i = 0; i < kUnit<T>; ++i) x[h + i] = e[i];
             }
-            store_planes8<E, P>(to + c * 2, p.values_plane, x);
+            store_planes<E, P>(to + (c >> 5) * p.values_block + (c & 31) * 2, p.values_plane, x);
         }
     }
 }
 
+// The workgroups of one XCD (every eighth) take tiles of the same rows or columns
+// side by side, so that what they share comes from its L2: `inner` tiles of one axis,
+// `outer` of the other; the outer axis is dealt out to the XCDs.
+__device__ __forceinline__ bool deal(int64_t id, int inner, int outer, int& i, int& o)
+{
+    const int64_t local = id >> 3;
+    i = (int)(local % inner);
+    const int64_t k = local / inner * 8 + (id & 7);
+    o = (int)k;
+    return k < outer;
+}
+inline int64_t dealt(int64_t inner, int64_t outer) { return inner * ((outer + 7) / 8 * 8); }
+
+// Tiles of values of one XCD whose part of the table stays in its L2 while the tokens'
+// tiles go by.
+constexpr int kLossGroup = 6;
+
 // Logits of kLossValues values (rows of the tile) and kLossTokens tokens (columns).
-template <typename T, bool GRAD> __global__ __launch_bounds__(256, 2) void hyena_loss_logits(LossArgs p)
+template <typename T, bool GRAD> __global__ __launch_bounds__(256, LossType<T>::P == 1 ? 3 : 2) void hyena_loss_logits(LossArgs p, int value_tiles)
 {
     using E = typename LossType<T>::E;
     constexpr int P = LossType<T>::P;
-    using Tile = MatTile<E, kLossValues, kLossTokens, 2, 2, true, true, P>;
+    using Tile = MatTile<E, kLossValues, kLossTokens, 2, 2, kInColumnsPaired, kInColumns, P, 2>;
     __shared__ __attribute__((aligned(16))) char lds[Tile::kLds];
     const int64_t count = *p.count;
-    const int64_t t0 = (int64_t)blockIdx.y * kLossTokens;
-    if (t0 >= count) return;
-    const int32_t v0 = p.first + (int32_t)blockIdx.x * kLossValues;
+    // XCD x has the tiles of values x, x + 8, ..., kLossGroup of them at a time
+    const int token_tiles = (int)(p.tokens / kLossTokens);
+    const int64_t local = blockIdx.x >> 3, each = (int64_t)kLossGroup * token_tiles;
+    const int mine = (value_tiles + 7) / 8, group = (int)(local / each), in_group = mine - group * kLossGroup;
+    const int width = in_group < kLossGroup ? in_group : kLossGroup;
+    const int64_t rest = local - group * each;
+    const int value_tile = (group * kLossGroup + (int)(rest % width)) * 8 + (int)(blockIdx.x & 7);
+    const int64_t t0 = rest / width * kLossTokens;
+    if (t0 >= count || value_tile >= value_tiles) return;
+    const int32_t v0 = p.first + value_tile * kLossValues;
     Tile tile;
-    const Operand values{p.values + (int64_t)v0 * p.values_row, p.values + (int64_t)p.V * p.values_row, p.values_row};
-    const Operand rows{p.rows + t0 * p.kd * 2, p.rows + p.tokens * p.kd * 2, (int64_t)p.kd * 2};
+    const Operand values{p.values + (int64_t)v0 * p.values_row, p.values + p.values_bytes, p.values_row, p.values_block};
+    const Operand rows{p.rows + t0 * 64, p.rows + p.rows_plane, 64, p.tokens * 64};
     tile.run(lds, values, p.values_plane, rows, p.rows_plane, p.kd / 32);
 
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4;
     const int wm = wave / 2, wn = wave % 2;
     const float scale2 = p.scale * kLog2e;
-    const bool whole = v0 + kLossValues <= p.V;
+    const int first = wm * (kLossValues / 2) + 8 * g;  // this lane's values: first + at(i) + r
+    auto at = [](int i) { return 32 * (i >> 1) + 4 * (i & 1); };
+    const int left = p.V - v0;                         // values of the tile that there are
     if constexpr (!GRAD) {
-        __shared__ float2 halves[2][kLossTokens];
+        float2* halves = (float2*)lds;  // [2][kLossTokens]
 #pragma unroll
         for (int j = 0; j < Tile::NI; ++j) {
             const int n = wn * (kLossTokens / 2) + 16 * j + (lane & 15);
             const int64_t t = t0 + n;
-            const int target = t < count ? p.target[t] - v0 : -1;
+#pragma unroll
+            for (int i = 0; i < Tile::MI; ++i) tile.c[i][j] *= scale2;
+            if (left < kLossValues) {
+#pragma unroll
+                for (int i = 0; i < Tile::MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (first + at(i) + r >= left) tile.c[i][j][r] = -INFINITY;
+            }
+            const int target = t < count ? p.target[t] - v0 - first : -1;
+            if (__any((uint32_t)target < (uint32_t)(kLossValues / 2))) {
+                float hit = 0.0f;
+#pragma unroll
+                for (int i = 0; i < Tile::MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) hit = target == at(i) + r ? tile.c[i][j][r] : hit;
+                if ((uint32_t)target < (uint32_t)(kLossValues / 2) && (target & 31) < 8) p.hit[t] = hit;
+            }
             float m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < Tile::MI; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int v = wm * (kLossValues / 2) + 16 * i + 4 * g + r;
-                    float l = tile.c[i][j][r] * scale2;
-                    if (!whole && v0 + v >= p.V) l = -INFINITY;
-                    if (v == target) p.hit[t] = l;
-                    tile.c[i][j][r] = l;
-                    m = fmaxf(m, l);
-                }
+                for (int r = 0; r < 4; ++r) m = fmaxf(m, tile.c[i][j][r]);
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
             const float base = m == -INFINITY ? 0.0f : m;  // (no value of the tile's half is in the vocabulary)
@@ -227,55 +263,64 @@ template <typename T, bool GRAD> __global__ __launch_bounds__(256, 2) void hyena
                 for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(tile.c[i][j][r] - base);
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
-            if (g == 0) halves[wm][n] = make_float2(m, s);
+            if (g == 0) halves[wm * kLossTokens + n] = make_float2(m, s);
         }
         __syncthreads();
         if (threadIdx.x < kLossTokens) {
-            const float2 a = halves[0][threadIdx.x], b = halves[1][threadIdx.x];
+            const float2 a = halves[threadIdx.x], b = halves[kLossTokens + threadIdx.x];
             const float m = fmaxf(a.x, b.x);
             // (the first half always has a value)
             const float s = a.y * __builtin_amdgcn_exp2f(a.x - m) + b.y * __builtin_amdgcn_exp2f(b.x - m);
-            p.part[(int64_t)blockIdx.x * p.tokens + t0 + threadIdx.x] = make_float2(m, s);
+            p.part[(int64_t)value_tile * p.tokens + t0 + threadIdx.x] = make_float2(m, s);
         }
     } else {
         const float up = p.norm[0];
+        const bool rim = left < kLossValues || t0 + kLossTokens > count;
 #pragma unroll
         for (int j = 0; j < Tile::NI; ++j) {
             const int n = wn * (kLossTokens / 2) + 16 * j + (lane & 15);
             const int64_t t = t0 + n;
             const bool in = t < count;
-            const int target = in ? p.target[t] - v0 : -1;
+            const int target = in ? p.target[t] - v0 - first : -1;
             const float lse2 = in ? p.lse2[t] : 0.0f, weight = in ? p.weight[t] * up : 0.0f;
-            char* to = p.g + t * p.g_row + ((int64_t)blockIdx.x * kLossValues) * 2;
 #pragma unroll
-            for (int i = 0; i < Tile::MI; ++i) {
-                const int v = wm * (kLossValues / 2) + 16 * i + 4 * g;
-                f32x4 x;
+            for (int i = 0; i < Tile::MI; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float q = __builtin_amdgcn_exp2f(fmaf(tile.c[i][j][r], scale2, -lse2));
-                    if (v + r == target) q -= 1.0f;
-                    q *= weight;
-                    if (!in || (!whole && v0 + v + r >= p.V)) q = 0.0f;
-                    x[r] = q;
-                }
-                if constexpr (P == 1) {
-                    *(typename Mx<E>::vec4*)(to + v * 2) = Mx<E>::narrow(x);
-                } else {
+                for (int r = 0; r < 4; ++r)
+                    tile.c[i][j][r] = weight * __builtin_amdgcn_exp2f(fmaf(tile.c[i][j][r], scale2, -lse2));
+            if (rim) {  // zeros where no token or no value is
 #pragma unroll
-                    for (int k = 0; k < P; ++k) {
-                        const typename Mx<E>::vec4 y = Mx<E>::narrow(x);
-                        *(typename Mx<E>::vec4*)(to + v * 2 + k * p.g_plane) = y;
-                        x -= Mx<E>::widen(y);
-                    }
-                }
+                for (int i = 0; i < Tile::MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (!in || first + at(i) + r >= left) tile.c[i][j][r] = 0.0f;
             }
+            if (__any((uint32_t)target < (uint32_t)(kLossValues / 2))) {
+                float off = 0.0f;
+#pragma unroll
+                for (int i = 0; i < Tile::MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (target == at(i) + r) {
+                            tile.c[i][j][r] -= weight;
+                            if constexpr (P == 1) {
+                                E rounded;
+                                store_one<E>(&rounded, tile.c[i][j][r]);
+                                off = tile.c[i][j][r] - load_one<E>(&rounded);
+                            }
+                        }
+                if (P == 1 && (uint32_t)target < (uint32_t)(kLossValues / 2) && (target & 31) < 8) p.hit[t] = off;
+            }
+            char* to = p.g + (int64_t)((value_tile * kLossValues + wm * (kLossValues / 2)) >> 5) * p.tokens * 64 + t * 64 + g * 16;
+#pragma unroll
+            for (int i = 0; i < Tile::MI; i += 2)
+                store_planes<E, P>(to + (int64_t)(i >> 1) * p.tokens * 64, p.g_plane, join8(tile.c[i][j], tile.c[i + 1][j]));
         }
     }
 }
 
 // Loss and lse of 16 tokens: 16 threads each go through the tiles' sums.
-template <int kUnused> __global__ __launch_bounds__(256) void hyena_loss_join(LossArgs p, int tiles)
+template <typename T> __global__ __launch_bounds__(256) void hyena_loss_join(LossArgs p, int tiles)
 {
     __shared__ float2 lds[16][17];
     const int64_t count = *p.count, a = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
@@ -306,34 +351,30 @@ template <int kUnused> __global__ __launch_bounds__(256) void hyena_loss_join(Lo
     }
 }
 
-// The first `tiles` workgroups: d_table of kGradRows values of this piece and
-// kGradChannels channels.  The others: a share of d_x of kGradRows tokens, the sum
-// over one of p.splits parts of the piece's values.
-template <typename T> __global__ __launch_bounds__(256, 2) void hyena_loss_products(LossArgs p, int table_tiles, int channel_tiles)
+// The first table_groups workgroups: d_table of kGradRows values of this piece and
+// kGradChannels channels.  The others, shorter ones: a share of d_x of kGradRows tokens,
+// the sum over one of p.splits parts of the piece's values.
+template <typename T> __global__ __launch_bounds__(256, 2) void hyena_loss_products(LossArgs p, int table_groups, int channel_tiles)
 {
     using E = typename LossType<T>::E;
     constexpr int P = LossType<T>::P;
-    using Table = MatTile<E, kGradChannels, kGradRows, 2, 2, false, false, P>;
-    using Dx = MatTile<E, kGradChannels, kGradRows, 2, 2, false, true, P>;
+    using Table = MatTile<E, kGradChannels, kGradRows, 2, 2, kInRows, kInRows, P, 2>;
+    using Dx = MatTile<E, kGradChannels, kGradRows, 2, 2, kInRows, kInColumns, P, 2>;
     __shared__ __attribute__((aligned(16))) char lds[Table::kLds];
     const int64_t count = *p.count;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4;
     const int wm = wave / 2, wn = wave % 2;
     const int32_t values = p.V - p.first < p.chunk ? p.V - p.first : p.chunk;  // of this piece
-    if ((int)blockIdx.x < table_tiles) {
-        const int c0 = (int)blockIdx.x % channel_tiles * kGradChannels;
-        const int32_t v0 = (int)blockIdx.x / channel_tiles * kGradRows;
+    int channel_tile, o;
+    if ((int)blockIdx.x < table_groups) {
+        if (!deal(blockIdx.x, channel_tiles, (values + kGradRows - 1) / kGradRows, channel_tile, o)) return;
+        const int c0 = channel_tile * kGradChannels;
+        const int32_t v0 = o * kGradRows;
         Table tile;
-        const Operand x{p.rows + c0 * 2, p.rows + p.tokens * p.kd * 2, (int64_t)p.kd * 2};
-        const Operand y{p.g + (int64_t)v0 * 2, p.g + p.tokens * p.g_row, p.g_row};
-        if (count > 0) {
-            tile.run(lds, x, p.rows_plane, y, p.g_plane, (int)((count + 31) / 32));
-        } else {
-#pragma unroll
-            for (int i = 0; i < Table::MI; ++i)
-#pragma unroll
-                for (int j = 0; j < Table::NI; ++j) tile.c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
+        const Operand x{p.rows + (int64_t)(c0 >> 5) * p.tokens * 64, p.rows + p.rows_plane, 64, p.tokens * 64};
+        const Operand y{p.g + (int64_t)(v0 >> 5) * p.tokens * 64, p.g + p.g_plane, 64, p.tokens * 64};
+        if (count > 0) tile.run(lds, x, p.rows_plane, y, p.g_plane, (int)((count + 31) / 32));
+        else tile.clear();
         const float down = p.norm[1];
 #pragma unroll
         for (int j = 0; j < Table::NI; ++j) {
@@ -355,11 +396,9 @@ template <typename T> __global__ __launch_bounds__(256, 2) void hyena_loss_produ
         }
         return;
     }
-    int64_t b = (int64_t)blockIdx.x - table_tiles;
-    const int c0 = (int)(b % channel_tiles) * kGradChannels;
-    b /= channel_tiles;
-    const int split = (int)(b % p.splits);
-    const int64_t t0 = b / p.splits * kGradRows;
+    if (!deal((int64_t)blockIdx.x - table_groups, channel_tiles, (int)(p.tokens / kGradRows) * p.splits, channel_tile, o)) return;
+    const int c0 = channel_tile * kGradChannels, split = o % p.splits;
+    const int64_t t0 = (int64_t)(o / p.splits) * kGradRows;
     if (t0 >= count) return;
     // this part's values, whole steps of 32
     const int steps = (values + 31) / 32, per = (steps + p.splits - 1) / p.splits;
@@ -367,14 +406,12 @@ template <typename T> __global__ __launch_bounds__(256, 2) void hyena_loss_produ
     if (k0 >= k1 && p.first != 0) return;
     Dx tile;
     if (k0 < k1) {
-        const Operand x{p.values + (int64_t)(p.first + 32 * k0) * p.values_row + c0 * 2, p.values + (int64_t)p.V * p.values_row, p.values_row};
-        const Operand y{p.g + t0 * p.g_row + k0 * 64, p.g + p.tokens * p.g_row, p.g_row};
+        const Operand x{p.values + (int64_t)(p.first + 32 * k0) * p.values_row + (int64_t)(c0 >> 5) * p.values_block,
+                        p.values + p.values_bytes, p.values_row, p.values_block};
+        const Operand y{p.g + (int64_t)k0 * p.tokens * 64 + t0 * 64, p.g + p.g_plane, 64, p.tokens * 64};
         tile.run(lds, x, p.values_plane, y, p.g_plane, k1 - k0);
     } else {
-#pragma unroll
-        for (int i = 0; i < Dx::MI; ++i)
-#pragma unroll
-            for (int j = 0; j < Dx::NI; ++j) tile.c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        tile.clear();
     }
 #pragma unroll
     for (int j = 0; j < Dx::NI; ++j) {
@@ -414,6 +451,14 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_los
                         for (int e = 0; e < 4; ++e) x[i + e] += y[e];
                     }
                 }
+                if constexpr (LossType<T>::P == 1) {
+                    // G at the target is rounded like the others; its rest, which one row of the table bears
+                    const float off = p.hit[a];
+                    float w[K];
+                    load_unit<T, VEC>((const T*)p.table + (int64_t)p.target[a] * p.d, c, p.d, p.d % 2 == 0, w);
+#pragma unroll
+                    for (int i = 0; i < K; ++i) x[i] = fmaf(off, w[i], x[i]);
+                }
 #pragma unroll
                 for (int i = 0; i < K; ++i) x[i] *= down;
             }
@@ -448,9 +493,9 @@ template <typename T> hyena_status loss_forward(const LossArgs& a, bool pack, bo
     if (st != HYENA_OK) return st;
     const int tiles = (a.V + kLossValues - 1) / kLossValues;
     HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), false), (hyena_loss_logits<T, false>),
-              dim3((unsigned)tiles, (unsigned)(a.tokens / kLossTokens)), dim3(256), 0, s, a);
+              dim3((unsigned)dealt(a.tokens / kLossTokens, tiles)), dim3(256), 0, s, a, tiles);
     if ((st = launched()) != HYENA_OK) return st;
-    HY_LAUNCH(kernel_label("hyena_loss_join", 0), hyena_loss_join<0>, dim3((unsigned)((a.total + 15) / 16)), dim3(256), 0, s, a, tiles);
+    HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>()), hyena_loss_join<T>, dim3((unsigned)((a.total + 15) / 16)), dim3(256), 0, s, a, tiles);
     return launched();
 }
 
@@ -463,13 +508,14 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
     for (int64_t first = 0; first < a.V; first += a.chunk) {
         b.first = (int32_t)first;
         const int values = a.V - first < a.chunk ? (int)(a.V - first) : a.chunk;
-        const dim3 grid((unsigned)((values + kLossValues - 1) / kLossValues), (unsigned)(a.tokens / kLossTokens));
-        HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), true), (hyena_loss_logits<T, true>), grid, dim3(256), 0, s, b);
+        const int tiles = (values + kLossValues - 1) / kLossValues;
+        HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), true), (hyena_loss_logits<T, true>),
+                  dim3((unsigned)dealt(a.tokens / kLossTokens, tiles)), dim3(256), 0, s, b, tiles);
         if ((st = launched()) != HYENA_OK) return st;
-        const int table_tiles = a.d_table ? channel_tiles * ((values + kGradRows - 1) / kGradRows) : 0;
-        const int64_t dx_tiles = a.d_x ? (int64_t)channel_tiles * a.splits * (a.tokens / kGradRows) : 0;
+        const int64_t table_tiles = a.d_table ? dealt(channel_tiles, (values + kGradRows - 1) / kGradRows) : 0;
+        const int64_t dx_tiles = a.d_x ? dealt(channel_tiles, a.splits * (a.tokens / kGradRows)) : 0;
         HY_LAUNCH(kernel_label("hyena_loss_products", type_label<T>()), hyena_loss_products<T>, dim3((unsigned)(table_tiles + dx_tiles)),
-                  dim3(256), 0, s, b, table_tiles, channel_tiles);
+                  dim3(256), 0, s, b, (int)table_tiles, channel_tiles);
         if ((st = launched()) != HYENA_OK) return st;
     }
     if (a.d_x == nullptr) return HYENA_OK;

@@ -205,14 +205,14 @@ def test_gradient_against_differences():
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_several_pieces_of_the_vocabulary(dtype):
-    # G of 12288 tokens fits 256 MiB for a part of these 20011 values: against products in
-    # float64 on the GPU, at some rows
+    # G of 16500 tokens fits 1 GiB for a part of these 40009 values (float32: a quarter): against
+    # products in float64 on the GPU
     import torch
     say(f"[gpu] token_loss in pieces {dtype}")
-    B, N, V, d = 3, 4096, 20011, 64
+    B, N, V, d = 3, 5500, 40009, 64
     x, table, target, d_loss = make((B, N, V, d), dtype, 4, masked=0.1)
     plan = hyena.TokenLoss(B, N, V, d, io_dtype=IO[dtype])
-    assert plan.backward_bytes < 3 * 2 * B * N * V
+    assert plan.backward_bytes < (3 if dtype == "f32" else 1) * 2 * B * N * V
     loss, lse = plan.forward(x, table, target)
     dx, dt = plan.backward(d_loss, x, table, target, lse)
     live = ((target >= 0) & (target < V)).view(-1)
