@@ -8,6 +8,8 @@ namespace hy {
 // Tokens and values of the vocabulary of a tile of logits; channels and rows of a
 // tile of the gradients.
 constexpr int kLossTokens = 128, kLossValues = 256;
+constexpr int kFewValues = 64;  // of calls of few tokens
+inline int value_tile(bool few) { return few ? kFewValues : kLossValues; }
 constexpr int kGradRows = 128, kGradChannels = 256;
 
 struct LossArgs {
@@ -18,6 +20,7 @@ struct LossArgs {
     int32_t kd;            // d rounded up to 32: the width of gathered rows
     int32_t pairs;
     int32_t each;          // tokens of a workgroup of the gather
+    int32_t few;           // few tokens: their own kernels
     float scale;
     const void* table;     // as given
     const float* lse_in;
@@ -40,7 +43,7 @@ struct LossArgs {
     int64_t values_row, values_block, values_plane, values_bytes;  // bytes: of a row, 32 channels, a plane; the first plane's
     float2* part;          // [tiles of values][tokens rounded up]: largest, sum
     float* hit;            // [tokens] the target's logit; backward: what rounding took from G there
-    char* g;               // [planes][chunk / 32][tokens rounded up][32]
+    char* g;               // [planes][chunk / 32][tokens rounded up][32]; of few tokens float32 [values rounded up][16]
     int64_t g_plane;
     float* acc;            // [splits][tokens rounded up][acc_row] d_x
     int64_t tokens;        // rounded up

@@ -25,12 +25,24 @@ hyena_status loss_sizes(const hyena_token_loss* op)
     return check_io(kWho, op->io_dtype);
 }
 
-// Calls of more tokens than this bring the table into the matrix operands' form first.
-constexpr int64_t kPackTokens = 256;
+// Calls of at most this many tokens have their own kernels: forward, in 16 bits and in
+// float32 (whose table is read as given then), and backward.
+constexpr int32_t kFewGroups = 256;  // workgroups of 256 channels, backward
+constexpr int64_t kFewTokens = 32, kFewTokensF32 = 128, kFewTokensGrad = 4, kFewTokensGradF32 = 16;
+// Others of more tokens than this bring the table into the matrix operands' form first.
+constexpr int64_t kPackTokens = 4096;
 
-bool needs_pack(const hyena_token_loss* op)
+bool is_few(const hyena_token_loss* op, bool grad)
 {
-    return op->io_dtype == HYENA_F32 || op->d % 8 != 0 || op->B * op->N > kPackTokens;
+    const bool f32 = op->io_dtype == HYENA_F32;
+    return op->B * op->N <= (grad ? (f32 ? kFewTokensGradF32 : kFewTokensGrad) : f32 ? kFewTokensF32 : kFewTokens);
+}
+
+bool needs_pack(const hyena_token_loss* op, bool grad)
+{
+    if (op->io_dtype == HYENA_F32) return !is_few(op, grad);
+    // 16-byte loads need rows that are made of them (float32's any 4-byte address)
+    return op->d % 8 != 0 || (!is_few(op, grad) && op->B * op->N > kPackTokens);
 }
 
 // Sizes, and with a scratch the addresses in it; returns the bytes.
@@ -41,7 +53,8 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     a.V = (int32_t)op->V;
     a.d = (int32_t)op->d;
     a.kd = (int32_t)((op->d + 31) / 32 * 32);
-    a.tokens = (a.total + kLossTokens - 1) / kLossTokens * kLossTokens;
+    a.few = is_few(op, grad);
+    a.tokens = a.few && grad ? 32 : (a.total + kLossTokens - 1) / kLossTokens * kLossTokens;
     a.scale = op->scale;
     a.table = op->table;
     // a workgroup of the gather for 64 tokens, or at most 512 of them
@@ -60,13 +73,13 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     a.target = (int32_t*)take(tokens * 4);
     a.rows_plane = (int64_t)tokens * a.kd * 2;
     a.rows = take((size_t)(planes * a.rows_plane));
-    if (needs_pack(op)) {
+    if (needs_pack(op, grad)) {
         a.values_row = 64;
         a.values_block = (int64_t)a.V * 64;
         a.values_bytes = a.values_plane = a.kd / 32 * a.values_block;
         a.values = take((size_t)(planes * a.values_plane));
     } else {
-        a.values_row = (int64_t)a.d * 2;
+        a.values_row = (int64_t)a.d * (int64_t)element_bytes(op->io_dtype);
         a.values_block = 64;
         a.values_plane = 0;
         a.values_bytes = (int64_t)a.V * a.values_row;
@@ -74,12 +87,20 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     }
     a.hit = (float*)take(tokens * 4);
     if (!grad) {
-        a.part = (float2*)take((size_t)((a.V + kLossValues - 1) / kLossValues) * tokens * 8);
+        a.part = (float2*)take((size_t)((a.V + value_tile(a.few) - 1) / value_tile(a.few)) * tokens * 8);
         return at;
     }
     a.place = (int32_t*)take((size_t)a.total * 4);
     a.weight = (float*)take(tokens * 4);
     a.lse2 = (float*)take(tokens * 4);
+    a.acc_row = (int32_t)((a.d + 3) / 4 * 4);
+    if (a.few) {
+        a.chunk = a.V;
+        a.g = take((size_t)((a.V + kFewValues - 1) / kFewValues) * kFewValues * 16 * 4);
+        a.splits = kFewGroups;
+        a.acc = (float*)take((size_t)a.splits * tokens * (size_t)a.acc_row * 4);
+        return at;
+    }
     const int64_t whole = (a.V + kLossValues - 1) / kLossValues, fit = kGradBytes / (a.tokens * 2 * planes * kLossValues);
     int64_t tiles = fit < 1 ? 1 : fit < whole ? fit : whole;
     const int64_t pieces = (whole + tiles - 1) / tiles;
@@ -93,11 +114,11 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     const int64_t channel_tiles = (a.d + kGradChannels - 1) / kGradChannels, dx_tiles = a.tokens / kGradRows * channel_tiles;
     const int64_t dx_steps = a.chunk / 32, table_steps = a.tokens / 32, table_tiles = a.chunk / kGradRows * channel_tiles;
     const int64_t share = (dx_tiles * dx_steps + table_tiles * table_steps) / kSplitGroups;
-    int64_t splits = share < 1 ? 16 : (kSplitParts * dx_steps + share - 1) / share;
+    int64_t splits = share < 1 ? 64 : (kSplitParts * dx_steps + share - 1) / share;
     const int64_t most = a.chunk / 512 < 1 ? 1 : a.chunk / 512;  // a part has 512 values at least
-    splits = splits < 1 ? 1 : splits > most ? most : splits > 16 ? 16 : splits;
+    const int64_t cap = a.tokens <= 1024 ? 64 : 16;
+    splits = splits < 1 ? 1 : splits > most ? most : splits > cap ? cap : splits;
     a.splits = (int32_t)splits;
-    a.acc_row = (int32_t)((a.d + 3) / 4 * 4);
     a.acc = (float*)take((size_t)splits * tokens * (size_t)a.acc_row * 4);
     return at;
 }
@@ -168,7 +189,7 @@ hyena_status hyena_token_loss_forward(const hyena_token_loss* op, float* loss, f
     a.loss = loss;
     a.lse = lse;
     return by_io(op->io_dtype, [&](auto* t) {
-        return loss_forward<std::remove_pointer_t<decltype(t)>>(a, needs_pack(op), units, (hipStream_t)stream);
+        return loss_forward<std::remove_pointer_t<decltype(t)>>(a, needs_pack(op, false), units, (hipStream_t)stream);
     });
 }
 
@@ -194,7 +215,7 @@ hyena_status hyena_token_loss_backward(const hyena_token_loss* op, const hyena_r
     a.d_x = d_x;
     a.d_table = d_table;
     return by_io(op->io_dtype, [&](auto* t) {
-        return loss_backward<std::remove_pointer_t<decltype(t)>>(a, needs_pack(op), units, (hipStream_t)stream);
+        return loss_backward<std::remove_pointer_t<decltype(t)>>(a, needs_pack(op, true), units, (hipStream_t)stream);
     });
 }
 

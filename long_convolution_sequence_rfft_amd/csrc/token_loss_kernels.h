@@ -5,6 +5,7 @@
 //   hyena_loss_pack     the table as a matrix operand, where it is not one as given
 //   hyena_loss_logits   a tile of logits; forward: each token's largest and the sum
 //                       of the exponentials over the tile's values; backward: G
+//   hyena_loss_few      the same for few tokens, hyena_loss_few_grads their gradients
 //   hyena_loss_join     the tiles' sums joined: loss, lse
 //   hyena_loss_products d_table of a piece of the vocabulary, and its share of d_x
 //   hyena_loss_finish   d_x from its sums
@@ -196,11 +197,12 @@ inline int64_t dealt(int64_t inner, int64_t outer) { return inner * ((outer + 7)
 constexpr int kLossGroup = 6;
 
 // Logits of kLossValues values (rows of the tile) and kLossTokens tokens (columns).
-template <typename T, bool GRAD> __global__ __launch_bounds__(256, LossType<T>::P == 1 ? 3 : 2) void hyena_loss_logits(LossArgs p, int value_tiles)
+template <typename T, bool GRAD>
+__global__ __launch_bounds__(256, LossType<T>::P == 1 ? 3 : 2) void hyena_loss_logits(LossArgs p, int value_tiles)
 {
     using E = typename LossType<T>::E;
-    constexpr int P = LossType<T>::P;
-    using Tile = MatTile<E, kLossValues, kLossTokens, 2, 2, kInColumnsPaired, kInColumns, P, 2>;
+    constexpr int P = LossType<T>::P, WM = 2, WN = 2;
+    using Tile = MatTile<E, kLossValues, kLossTokens, WM, WN, kInColumnsPaired, kInColumns, P, 2>;
     __shared__ __attribute__((aligned(16))) char lds[Tile::kLds];
     const int64_t count = *p.count;
     // XCD x has the tiles of values x, x + 8, ..., kLossGroup of them at a time
@@ -219,16 +221,16 @@ template <typename T, bool GRAD> __global__ __launch_bounds__(256, LossType<T>::
     tile.run(lds, values, p.values_plane, rows, p.rows_plane, p.kd / 32);
 
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4;
-    const int wm = wave / 2, wn = wave % 2;
+    const int wm = wave / WN, wn = wave % WN;
     const float scale2 = p.scale * kLog2e;
-    const int first = wm * (kLossValues / 2) + 8 * g;  // this lane's values: first + at(i) + r
+    const int first = wm * (kLossValues / WM) + 8 * g;  // this lane's values: first + at(i) + r
     auto at = [](int i) { return 32 * (i >> 1) + 4 * (i & 1); };
     const int left = p.V - v0;                         // values of the tile that there are
     if constexpr (!GRAD) {
         float2* halves = (float2*)lds;  // [2][kLossTokens]
 #pragma unroll
         for (int j = 0; j < Tile::NI; ++j) {
-            const int n = wn * (kLossTokens / 2) + 16 * j + (lane & 15);
+            const int n = wn * (kLossTokens / WN) + 16 * j + (lane & 15);
             const int64_t t = t0 + n;
 #pragma unroll
             for (int i = 0; i < Tile::MI; ++i) tile.c[i][j] *= scale2;
@@ -240,13 +242,13 @@ template <typename T, bool GRAD> __global__ __launch_bounds__(256, LossType<T>::
                         if (first + at(i) + r >= left) tile.c[i][j][r] = -INFINITY;
             }
             const int target = t < count ? p.target[t] - v0 - first : -1;
-            if (__any((uint32_t)target < (uint32_t)(kLossValues / 2))) {
+            if (__any((uint32_t)target < (uint32_t)(kLossValues / WM))) {
                 float hit = 0.0f;
 #pragma unroll
                 for (int i = 0; i < Tile::MI; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) hit = target == at(i) + r ? tile.c[i][j][r] : hit;
-                if ((uint32_t)target < (uint32_t)(kLossValues / 2) && (target & 31) < 8) p.hit[t] = hit;
+                if ((uint32_t)target < (uint32_t)(kLossValues / WM) && (target & 31) < 8) p.hit[t] = hit;
             }
             float m = -INFINITY;
 #pragma unroll
@@ -278,7 +280,7 @@ template <typename T, bool GRAD> __global__ __launch_bounds__(256, LossType<T>::
         const bool rim = left < kLossValues || t0 + kLossTokens > count;
 #pragma unroll
         for (int j = 0; j < Tile::NI; ++j) {
-            const int n = wn * (kLossTokens / 2) + 16 * j + (lane & 15);
+            const int n = wn * (kLossTokens / WN) + 16 * j + (lane & 15);
             const int64_t t = t0 + n;
             const bool in = t < count;
             const int target = in ? p.target[t] - v0 - first : -1;
@@ -295,7 +297,7 @@ template <typename T, bool GRAD> __global__ __launch_bounds__(256, LossType<T>::
                     for (int r = 0; r < 4; ++r)
                         if (!in || first + at(i) + r >= left) tile.c[i][j][r] = 0.0f;
             }
-            if (__any((uint32_t)target < (uint32_t)(kLossValues / 2))) {
+            if (__any((uint32_t)target < (uint32_t)(kLossValues / WM))) {
                 float off = 0.0f;
 #pragma unroll
                 for (int i = 0; i < Tile::MI; ++i)
@@ -309,9 +311,9 @@ template <typename T, bool GRAD> __global__ __launch_bounds__(256, LossType<T>::
                                 off = tile.c[i][j][r] - load_one<E>(&rounded);
                             }
                         }
-                if (P == 1 && (uint32_t)target < (uint32_t)(kLossValues / 2) && (target & 31) < 8) p.hit[t] = off;
+                if (P == 1 && (uint32_t)target < (uint32_t)(kLossValues / WM) && (target & 31) < 8) p.hit[t] = off;
             }
-            char* to = p.g + (int64_t)((value_tile * kLossValues + wm * (kLossValues / 2)) >> 5) * p.tokens * 64 + t * 64 + g * 16;
+            char* to = p.g + (int64_t)((value_tile * kLossValues + wm * (kLossValues / WM)) >> 5) * p.tokens * 64 + t * 64 + g * 16;
 #pragma unroll
             for (int i = 0; i < Tile::MI; i += 2)
                 store_planes<E, P>(to + (int64_t)(i >> 1) * p.tokens * 64, p.g_plane, join8(tile.c[i][j], tile.c[i + 1][j]));
@@ -319,31 +321,251 @@ template <typename T, bool GRAD> __global__ __launch_bounds__(256, LossType<T>::
     }
 }
 
-// Loss and lse of 16 tokens: 16 threads each go through the tiles' sums.
-template <typename T> __global__ __launch_bounds__(256) void hyena_loss_join(LossArgs p, int tiles)
+// Two sums of exponentials, each with what was taken from its exponents.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2)
 {
-    __shared__ float2 lds[16][17];
+    const float top = fmaxf(m, m2);
+    const float base = top == -INFINITY ? 0.0f : top;  // both are empty
+    s = s * __builtin_amdgcn_exp2f(m - base) + s2 * __builtin_amdgcn_exp2f(m2 - base);
+    m = top;
+}
+
+// Logits of few tokens: each wave has 16 values and 16 N tokens, and takes its operands
+// from memory to its registers.  Bound by reading the table once, four steps ahead of the
+// products; nothing of it is shared, so nothing goes through LDS.  A table in float32 is
+// read as given and becomes three terms in the registers.  Backward G stays float32,
+// [values of the vocabulary rounded up][16].
+template <typename T, int N, bool GRAD> __global__ __launch_bounds__(256) void hyena_loss_few(LossArgs p)
+{
+    using E = typename LossType<T>::E;
+    using frag = typename Mx<E>::frag;
+    constexpr int P = LossType<T>::P, kAhead = 4;
+    static_assert(!GRAD || N == 1, "");
+    __shared__ float2 lds[4][16 * N];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+    const int64_t count = *p.count, t0 = (int64_t)blockIdx.y * (16 * N);
+    if (t0 >= count) return;
+    const int32_t v0 = (int32_t)blockIdx.x * kFewValues + wave * 16;
+    const int left = p.V - v0;  // values that there are
+    f32x4 c[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) c[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int steps = p.kd / 32;
+    const int64_t rows_block = p.tokens * 64;
+    const uint32_t boff = i * 64 + g * 16;
+    auto load_b = [&](const char* b0, int s, frag (&fb)[N]) {
+        const __amdgpu_buffer_rsrc_t r = operand_rsrc(b0 + t0 * 64 + s * rows_block, b0 + p.rows_plane);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            fb[j] = __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(boff + j * 1024), 0, 0));
+    };
+    if (left > 0) {
+        if constexpr (P == 3) {
+            const uint32_t aoff = (uint32_t)i * (uint32_t)p.values_row + g * 32;
+            const char* at = p.values + (int64_t)v0 * p.values_row;
+            f32x8 a[2][kAhead];
+            auto load = [&](int s, f32x8 (&fa)[kAhead]) {
+                const __amdgpu_buffer_rsrc_t r = operand_rsrc(at + s * 128, p.values + p.values_bytes);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const f32x4 lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(aoff + k * 128), 0, 0));
+                    const f32x4 hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(aoff + k * 128 + 16), 0, 0));
+                    fa[k] = join8(lo, hi);
+                }
+            };
+            auto multiply = [&](int s, const f32x8 (&fa)[kAhead]) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (s + k >= steps) break;
+                    Split<E, 3> x;
+                    x.set(fa[k]);
+                    frag b[3][N];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) load_b(p.rows + n * p.rows_plane, s + k, b[n]);
+#pragma unroll
+                    for (int q = 0; q < Planes<3>::kPairs; ++q)
+#pragma unroll
+                        for (int j = 0; j < N; ++j) c[j] = Mx<E>::mma(x.f[Planes<3>::a(q)], b[Planes<3>::b(q)][j], c[j]);
+                }
+            };
+            load(0, a[0]);
+            for (int s = 0; s < steps; s += 2 * kAhead) {
+                if (s + kAhead < steps) load(s + kAhead, a[1]);
+                multiply(s, a[0]);
+                if (s + 2 * kAhead < steps) load(s + 2 * kAhead, a[0]);
+                multiply(s + kAhead, a[1]);
+            }
+        } else {
+            const uint32_t aoff = (uint32_t)i * (uint32_t)p.values_row + g * 16;
+            const char *at = p.values + (int64_t)v0 * p.values_row, *end = p.values + p.values_bytes;
+            frag a[2][kAhead], b[2][kAhead][N];
+            auto load = [&](int s, frag (&fa)[kAhead], frag (&fb)[kAhead][N]) {
+                const __amdgpu_buffer_rsrc_t r = operand_rsrc(at + s * p.values_block, end);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    fa[k] = __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(aoff + (uint32_t)k * (uint32_t)p.values_block), 0, 0));
+                    load_b(p.rows, s + k, fb[k]);
+                }
+            };
+            auto multiply = [&](int s, const frag (&fa)[kAhead], const frag (&fb)[kAhead][N]) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (s + k < steps) {
+#pragma unroll
+                        for (int j = 0; j < N; ++j) c[j] = Mx<E>::mma(fa[k], fb[k][j], c[j]);
+                    }
+            };
+            load(0, a[0], b[0]);
+            for (int s = 0; s < steps; s += 2 * kAhead) {
+                if (s + kAhead < steps) load(s + kAhead, a[1], b[1]);
+                multiply(s, a[0], b[0]);
+                if (s + 2 * kAhead < steps) load(s + 2 * kAhead, a[0], b[0]);
+                multiply(s + kAhead, a[1], b[1]);
+            }
+        }
+    }
+    const float scale2 = p.scale * kLog2e;
+    if constexpr (!GRAD) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int64_t t = t0 + 16 * j + i;
+            const int target = t < count ? p.target[t] - v0 - 4 * g : -1;
+            float m = -INFINITY, s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                c[j][r] = 4 * g + r < left ? c[j][r] * scale2 : -INFINITY;
+                if (target == r) p.hit[t] = c[j][r];
+                m = fmaxf(m, c[j][r]);
+            }
+            m = fmaxf(m, __shfl_xor(m, 16));
+            m = fmaxf(m, __shfl_xor(m, 32));
+            const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(c[j][r] - base);
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (g == 0) lds[wave][16 * j + i] = make_float2(m, s);
+        }
+        __syncthreads();
+        if (threadIdx.x < 16 * N) {
+            float m = -INFINITY, s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) join(m, s, lds[w][threadIdx.x].x, lds[w][threadIdx.x].y);
+            p.part[(int64_t)blockIdx.x * p.tokens + t0 + threadIdx.x] = make_float2(m, s);
+        }
+    } else {
+        const bool in = i < count;
+        const int target = in ? p.target[i] - v0 - 4 * g : -1;
+        const float lse2 = in ? p.lse2[i] : 0.0f, weight = in ? p.weight[i] : 0.0f;
+        float* to = (float*)p.g + (int64_t)(v0 + 4 * g) * 16 + i;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float q = __builtin_amdgcn_exp2f(fmaf(c[0][r], scale2, -lse2));
+            to[r * 16] = in && 4 * g + r < left ? weight * (target == r ? q - 1.0f : q) : 0.0f;
+        }
+    }
+}
+
+// Gradients of at most N tokens: a wave takes the values of its part one after the
+// other, 256 channels of them, adds their share to d_x and makes their rows of d_table.
+// Bound by reading and writing the two tables; G of a value is the same for all lanes.
+template <typename T, int N, bool VEC> __global__ __launch_bounds__(256) void hyena_loss_few_grads(LossArgs p)
+{
+    __shared__ f32x4 lds[3][N][64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int c = (int)blockIdx.y * 256 + lane * 4;
+    const int count = (int)*p.count;
+    auto load4 = [&](const T* row) {
+        f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (VEC) {
+            if (c < p.d) y = Mx<T>::widen(*(const typename Mx<T>::vec4*)(row + c));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.d) y[e] = load_one<T>(row + c + e);
+        }
+        return y;
+    };
+    f32x4 x[N], dx[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        x[t] = dx[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (t < count && c < p.d) {
+            // the gathered rows are matrix operands; here they are read as given
+            const T* row = row_at<T>(p.x, p.index[t], p.x_N);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.d) x[t][e] = load_one<T>(row + c + e);
+        }
+    }
+    const int parts = (int)gridDim.x * 4, part = (int)blockIdx.x * 4 + wave, each = (p.V + parts - 1) / parts;
+    const int v0 = part * each, v1 = v0 + each < p.V ? v0 + each : p.V;
+    for (int v4 = v0; v4 < v1; v4 += 4) {
+        // G of four values for 16 tokens, an element of it in each lane
+        const float g = ((const float*)p.g)[(int64_t)v4 * 16 + lane];
+        f32x4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = load4((const T*)p.table + (int64_t)(v4 + k < v1 ? v4 + k : v1 - 1) * p.d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int v = v4 + k;
+            if (v >= v1) break;
+            f32x4 dw = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                const float q = t < count ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), k * 16 + t)) : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dx[t][e] = fmaf(q, w[k][e], dx[t][e]);
+                    dw[e] = fmaf(q, x[t][e], dw[e]);
+                }
+            }
+            if (p.d_table == nullptr) continue;
+            dw *= p.scale;
+            T* to = (T*)p.d_table + (int64_t)v * p.d + c;
+            if (VEC) {
+                if (c < p.d) *(typename Mx<T>::vec4*)to = Mx<T>::narrow(dw);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < p.d) store_one<T>(to + e, dw[e]);
+            }
+        }
+    }
+    if (p.d_x == nullptr) return;
+    if (wave > 0) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) lds[wave - 1][t][lane] = dx[t];
+    }
+    __syncthreads();
+    if (wave == 0 && c < p.d) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            if (t >= count) break;
+            f32x4 s = dx[t];
+#pragma unroll
+            for (int w = 0; w < 3; ++w) s += lds[w][t][lane];
+            *(f32x4*)(p.acc + ((int64_t)blockIdx.x * p.tokens + t) * p.acc_row + c) = s;
+        }
+    }
+}
+
+template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_join(LossArgs p, int tiles)
+{
+    __shared__ float2 lds[16][16];
     const int64_t count = *p.count, a = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
-    const int k = threadIdx.x >> 4;
     if ((int64_t)blockIdx.x * 16 >= count) return;
     float m = -INFINITY, s = 0.0f;
-#pragma unroll 4
-    for (int i = k; i < tiles; i += 16) {
+#pragma unroll 8
+    for (int i = threadIdx.x >> 4; i < tiles; i += 64) {
         const float2 x = p.part[(int64_t)i * p.tokens + a];
-        const float top = fmaxf(m, x.x);
-        s = s * __builtin_amdgcn_exp2f(m - top) + x.y * __builtin_amdgcn_exp2f(x.x - top);
-        m = top;
+        join(m, s, x.x, x.y);
     }
-    lds[k][threadIdx.x & 15] = make_float2(m, s);
+    for (int k = 16; k < 64; k *= 2) join(m, s, __shfl_xor(m, k), __shfl_xor(s, k));
+    if ((threadIdx.x & 63) < 16) lds[threadIdx.x >> 6][threadIdx.x & 15] = make_float2(m, s);
     __syncthreads();
-    if (k == 0 && a < count) {
-        for (int i = 1; i < 16; ++i) {
-            const float2 x = lds[i][threadIdx.x];
-            if (x.x == -INFINITY) continue;  // fewer tiles than threads
-            const float top = fmaxf(m, x.x);
-            s = s * __builtin_amdgcn_exp2f(m - top) + x.y * __builtin_amdgcn_exp2f(x.x - top);
-            m = top;
-        }
+    if (threadIdx.x < 16 && a < count) {
+        for (int i = 1; i < 16; ++i) join(m, s, lds[i][threadIdx.x].x, lds[i][threadIdx.x].y);
         const float log2s = __builtin_amdgcn_logf(s);
         const int32_t t = p.index[a];
         p.lse[t] = (m + log2s) * kLn2;
@@ -428,41 +650,51 @@ template <typename T> __global__ __launch_bounds__(256, 2) void hyena_loss_produ
     }
 }
 
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_loss_finish(LossArgs p)
+// d_x of a token from its sums, by ROWS waves for each token (few tokens have many sums).
+template <typename T, int ROWS> __global__ __launch_bounds__(ROWS == 1 ? 256 : 1024) void hyena_loss_finish(LossArgs p)
 {
-    constexpr int K = kUnit<T>;
-    const int lane = threadIdx.x & 63;
-    const float down = p.norm[1];
-    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < p.total; t += (int64_t)gridDim.x * 4) {
+    constexpr int kWaves = ROWS == 1 ? 4 : 16, kTokens = kWaves / ROWS;
+    __shared__ f32x4 lds[ROWS == 1 ? 1 : kWaves][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, part = wave % ROWS;
+    const float down = p.few ? p.scale : p.norm[1];
+    for (int64_t t = (int64_t)blockIdx.x * kTokens + wave / ROWS; t < p.total; t += (int64_t)gridDim.x * kTokens) {
         const int32_t a = p.place[t];
         T* to = (T*)p.d_x + t * p.d;
-        for (int c = lane * K; c < p.d; c += 64 * K) {
-            float x[K];
-#pragma unroll
-            for (int i = 0; i < K; ++i) x[i] = 0.0f;
-            if (a >= 0) {
-                for (int s = 0; s < p.splits; ++s) {
-                    const float* from = p.acc + ((int64_t)s * p.tokens + a) * p.acc_row + c;
-#pragma unroll
-                    for (int i = 0; i < K; i += 4) {
-                        if (c + i >= p.acc_row) break;
-                        const f32x4 y = *(const f32x4*)(from + i);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[i + e] += y[e];
-                    }
-                }
-                if constexpr (LossType<T>::P == 1) {
-                    // G at the target is rounded like the others; its rest, which one row of the table bears
-                    const float off = p.hit[a];
-                    float w[K];
-                    load_unit<T, VEC>((const T*)p.table + (int64_t)p.target[a] * p.d, c, p.d, p.d % 2 == 0, w);
-#pragma unroll
-                    for (int i = 0; i < K; ++i) x[i] = fmaf(off, w[i], x[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < K; ++i) x[i] *= down;
+        for (int c0 = 0; c0 < p.d; c0 += 256) {
+            const int c = c0 + lane * 4;
+            f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (a >= 0 && c < p.d) {
+                const float* from = p.acc + (int64_t)a * p.acc_row + c;
+#pragma unroll 4
+                for (int s = part; s < p.splits; s += ROWS) x += *(const f32x4*)(from + (int64_t)s * p.tokens * p.acc_row);
             }
-            store_unit<T, VEC>(to, c, p.d, p.d % 2 == 0, x);
+            if constexpr (ROWS > 1) {
+                lds[wave][lane] = x;
+                __syncthreads();
+                if (part == 0) {
+#pragma unroll
+                    for (int w = 1; w < ROWS; ++w) x += lds[wave + w][lane];
+                }
+                __syncthreads();
+                if (part != 0) continue;
+            }
+            if (c >= p.d) continue;
+            if (LossType<T>::P == 1 && a >= 0 && !p.few) {
+                // G at the target is rounded like the others; its rest, which one row of the table bears
+                const float off = p.hit[a];
+                const T* w = (const T*)p.table + (int64_t)p.target[a] * p.d + c;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < p.d) x[e] = fmaf(off, load_one<T>(w + e), x[e]);
+            }
+            x *= down;
+            if (p.d % 4 == 0) {
+                *(typename Mx<T>::vec4*)(to + c) = Mx<T>::narrow(x);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < p.d) store_one<T>(to + c + e, x[e]);
+            }
         }
     }
 }
@@ -487,15 +719,47 @@ template <typename T, bool GRAD> hyena_status loss_begin(const LossArgs& a, bool
     return launched();
 }
 
+template <typename T, int N, bool GRAD> hyena_status loss_few(const LossArgs& a, int tiles, hipStream_t s)
+{
+    const dim3 grid((unsigned)tiles, (unsigned)((a.total + 16 * N - 1) / (16 * N)));
+    HY_LAUNCH(kernel_label("hyena_loss_few", type_label<T>(), N, GRAD), (hyena_loss_few<T, N, GRAD>), grid, dim3(256), 0, s, a);
+    return launched();
+}
+
+template <typename T, bool GRAD> hyena_status loss_logits(const LossArgs& a, int tiles, hipStream_t s)
+{
+    if (!a.few) {
+        HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), GRAD), (hyena_loss_logits<T, GRAD>),
+                  dim3((unsigned)dealt(a.tokens / kLossTokens, tiles)), dim3(256), 0, s, a, tiles);
+        return launched();
+    }
+    if constexpr (!GRAD) {
+        if constexpr (LossType<T>::P == 3) {
+            if (a.total > 64) return loss_few<T, 8, false>(a, tiles, s);
+            if (a.total > 32) return loss_few<T, 4, false>(a, tiles, s);
+        }
+        if (a.total > 16) return loss_few<T, 2, false>(a, tiles, s);
+    }
+    return loss_few<T, 1, GRAD>(a, tiles, s);
+}
+
+template <typename T, int N> hyena_status loss_few_grads(const LossArgs& a, hipStream_t s)
+{
+    const dim3 grid((unsigned)a.splits, (unsigned)((a.d + 255) / 256));
+    if (a.d % 4 == 0)
+        HY_LAUNCH(kernel_label("hyena_loss_few_grads", type_label<T>(), N, true), (hyena_loss_few_grads<T, N, true>), grid, dim3(256), 0, s, a);
+    else
+        HY_LAUNCH(kernel_label("hyena_loss_few_grads", type_label<T>(), N, false), (hyena_loss_few_grads<T, N, false>), grid, dim3(256), 0, s, a);
+    return launched();
+}
+
 template <typename T> hyena_status loss_forward(const LossArgs& a, bool pack, bool units, hipStream_t s)
 {
     hyena_status st = loss_begin<T, false>(a, pack, units, s);
     if (st != HYENA_OK) return st;
-    const int tiles = (a.V + kLossValues - 1) / kLossValues;
-    HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), false), (hyena_loss_logits<T, false>),
-              dim3((unsigned)dealt(a.tokens / kLossTokens, tiles)), dim3(256), 0, s, a, tiles);
-    if ((st = launched()) != HYENA_OK) return st;
-    HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>()), hyena_loss_join<T>, dim3((unsigned)((a.total + 15) / 16)), dim3(256), 0, s, a, tiles);
+    const int tiles = (a.V + value_tile(a.few) - 1) / value_tile(a.few);
+    if ((st = loss_logits<T, false>(a, tiles, s)) != HYENA_OK) return st;
+    HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>()), hyena_loss_join<T>, dim3((unsigned)((a.total + 15) / 16)), dim3(1024), 0, s, a, tiles);
     return launched();
 }
 
@@ -508,10 +772,11 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
     for (int64_t first = 0; first < a.V; first += a.chunk) {
         b.first = (int32_t)first;
         const int values = a.V - first < a.chunk ? (int)(a.V - first) : a.chunk;
-        const int tiles = (values + kLossValues - 1) / kLossValues;
-        HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), true), (hyena_loss_logits<T, true>),
-                  dim3((unsigned)dealt(a.tokens / kLossTokens, tiles)), dim3(256), 0, s, b, tiles);
-        if ((st = launched()) != HYENA_OK) return st;
+        if ((st = loss_logits<T, true>(b, (values + value_tile(a.few) - 1) / value_tile(a.few), s)) != HYENA_OK) return st;
+        if (a.few) {  // all of the vocabulary is one piece
+            if ((st = a.total <= 4 ? loss_few_grads<T, 4>(a, s) : loss_few_grads<T, 16>(a, s)) != HYENA_OK) return st;
+            break;
+        }
         const int64_t table_tiles = a.d_table ? dealt(channel_tiles, (values + kGradRows - 1) / kGradRows) : 0;
         const int64_t dx_tiles = a.d_x ? dealt(channel_tiles, a.splits * (a.tokens / kGradRows)) : 0;
         HY_LAUNCH(kernel_label("hyena_loss_products", type_label<T>()), hyena_loss_products<T>, dim3((unsigned)(table_tiles + dx_tiles)),
@@ -519,12 +784,12 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
         if ((st = launched()) != HYENA_OK) return st;
     }
     if (a.d_x == nullptr) return HYENA_OK;
-    const int64_t need = (a.total + 3) / 4;
+    const int64_t need = a.splits <= 8 ? (a.total + 3) / 4 : a.total;
     const dim3 grid((unsigned)(need < 4096 ? need : 4096));
-    if (a.d % kUnit<T> == 0)
-        HY_LAUNCH(kernel_label("hyena_loss_finish", type_label<T>(), true), (hyena_loss_finish<T, true>), grid, dim3(256), 0, s, a);
+    if (a.splits <= 8)
+        HY_LAUNCH(kernel_label("hyena_loss_finish", type_label<T>(), 1), (hyena_loss_finish<T, 1>), grid, dim3(256), 0, s, a);
     else
-        HY_LAUNCH(kernel_label("hyena_loss_finish", type_label<T>(), false), (hyena_loss_finish<T, false>), grid, dim3(256), 0, s, a);
+        HY_LAUNCH(kernel_label("hyena_loss_finish", type_label<T>(), 16), (hyena_loss_finish<T, 16>), grid, dim3(1024), 0, s, a);
     return launched();
 }
 
