@@ -50,7 +50,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t operand_rsrc(const char* at, c
 // not know of these loads: wait_loads before the barrier that publishes them.
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, __amdgpu_buffer_rsrc_t r)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory", "m0");
 }
 template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 

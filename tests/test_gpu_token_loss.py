@@ -260,3 +260,80 @@ def test_streams_and_replayed_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, both()))
+
+
+@pytest.mark.parametrize("tokens", [2, 4, 5, 15, 16, 17, 31, 32, 33, 64, 65, 128, 129, 257])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_kernels_of_few_tokens_at_their_limits(dtype, tokens):
+    # V that is no multiple of any tile; rows made of 16-byte pieces, and not
+    run((1, tokens, 777, 72), dtype, masked=0.0)
+    run((1, tokens, 131, 45), dtype, masked=0.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_few_tokens_of_many(dtype):
+    # the call is large, what takes part is not: tiles and rows behind the last token
+    for count in (0, 1, 31, 33, 128):
+        x, table, target, d_loss = make((2, 300, 321, 40), dtype, 9, masked=0.0)
+        flat = target.view(-1)
+        flat[count:] = -1
+        run((2, 300, 321, 40), dtype, inputs=(x, table, target, d_loss))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_wide_rows(dtype):
+    run((1, 70, 90, 2100), dtype)
+    run((1, 3, 50, 16384), dtype, masked=0.0)
+    run((1, 140, 40, 16380), dtype)
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 5000])
+def test_tables_past_32_bits(tokens):
+    # 2^21 + 77 rows of 1024 in bf16 are 4.3 GB: all rows but a few are zeros, and so are their logits
+    import torch
+    V, d = (1 << 21) + 77, 1024
+    say(f"[gpu] token_loss with a table past 32 bits, {tokens} tokens")
+    gen = torch.Generator().manual_seed(3)
+    at = torch.tensor([0, 5, V // 2, V - 2, V - 1])
+    table = torch.zeros((V, d), dtype=torch.bfloat16, device="cuda")
+    rows = torch.randn((5, d), generator=gen).bfloat16()
+    table[at.cuda()] = rows.cuda()
+    x = torch.randn((1, tokens, d), generator=gen).bfloat16()
+    target = at[torch.arange(tokens) % 5].to(torch.int32)[None].cuda()
+    plan = hyena.TokenLoss(1, tokens, V, d, io_dtype=hyena.HYENA_BF16, scale=0.2)
+    loss, lse = plan.forward(x.cuda(), table, target)
+    l = 0.2 * x[0].double() @ rows.double().t()
+    m = l.max(-1, keepdim=True).values.clamp(min=0)
+    want = (torch.exp(l - m).sum(-1) + (V - 5) * torch.exp(-m[:, 0])).log() + m[:, 0]
+    assert float((lse[0].cpu().double() - want).abs().max()) < 1e-4
+    hit = l[torch.arange(tokens), torch.arange(tokens) % 5]
+    assert float((loss[0].cpu().double() - (want - hit)).abs().max()) < 2e-4
+    if tokens > 1000:  # (G of 2^21 values would take 85 pieces)
+        return
+    dx, dt = plan.backward(torch.ones((1, tokens), device="cuda"), x.cuda(), table, target, lse)
+    g = torch.exp(l - want[:, None])
+    g[torch.arange(tokens), torch.arange(tokens) % 5] -= 1
+    u = ends_ref.HALF_STEP["bf16"]
+    assert float((dx[0].cpu().double() - 0.2 * g @ rows.double()).abs().max()) < 3 * u * 0.2 * float((g.abs() @ rows.double().abs()).max())
+    ref = 0.2 * g.t() @ x[0].double()
+    assert float((dt[at.cuda()].cpu().double() - ref).abs().max()) < 3 * u * 0.2 * float((g.abs().t() @ x[0].double().abs()).max())
+    p = torch.exp(-want)  # of a row of zeros
+    other = 0.2 * (p[:, None] * x[0].double()).sum(0)
+    for v in (1, V // 2 + 1, V - 3):
+        assert float((dt[v].cpu().double() - other).abs().max()) < 3 * u * 0.2 * float((p[:, None] * x[0].double().abs()).sum(0).max())
+
+
+def test_an_infinity_in_one_token_stays_there():
+    import torch
+    for dtype, shape in (("bf16", (1, 200, 300, 64)), ("bf16", (1, 3, 300, 64)), ("f32", (1, 40, 300, 64))):
+        x, table, target, d_loss = make(shape, dtype, 2, masked=0.0)
+        plan = hyena.TokenLoss(*shape, io_dtype=IO[dtype])
+        loss, lse = plan.forward(x, table, target)
+        x2 = x.clone()
+        x2[0, 1, 5] = float("nan")
+        loss2, lse2 = plan.forward(x2, table, target)
+        keep = torch.arange(shape[1], device="cuda") != 1
+        assert torch.isnan(loss2[0, 1]) and torch.equal(loss[0, keep], loss2[0, keep]) and torch.equal(lse[0, keep], lse2[0, keep])
+        dx, _ = plan.backward(d_loss, x, table, target, lse, want_table=False)
+        dx2, _ = plan.backward(d_loss, x2, table, target, lse2, want_table=False)
+        assert torch.equal(dx[0, keep], dx2[0, keep])
