@@ -8,8 +8,10 @@ namespace hy {
 // Tokens and values of the vocabulary of a tile of logits; channels and rows of a
 // tile of the gradients.
 constexpr int kLossTokens = 128, kLossValues = 256;
-constexpr int kFewValues = 64;  // of calls of few tokens
-inline int value_tile(bool few) { return few ? kFewValues : kLossValues; }
+// Workgroups of the logits of few tokens, which take tiles of 16 values in turn.
+constexpr int kFewLogits = 512;
+inline int loss_tiles(int64_t V) { return (int)((V + kLossValues - 1) / kLossValues); }
+inline int few_groups(int64_t V) { return (V + 15) / 16 < kFewLogits ? (int)((V + 15) / 16) : kFewLogits; }
 constexpr int kGradRows = 128, kGradChannels = 256;
 
 struct LossArgs {

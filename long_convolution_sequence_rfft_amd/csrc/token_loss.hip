@@ -87,7 +87,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     }
     a.hit = (float*)take(tokens * 4);
     if (!grad) {
-        a.part = (float2*)take((size_t)((a.V + value_tile(a.few) - 1) / value_tile(a.few)) * tokens * 8);
+        a.part = (float2*)take((size_t)(a.few ? few_groups(a.V) : loss_tiles(a.V)) * tokens * 8);
         return at;
     }
     a.place = (int32_t*)take((size_t)a.total * 4);
@@ -96,7 +96,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     a.acc_row = (int32_t)((a.d + 3) / 4 * 4);
     if (a.few) {
         a.chunk = a.V;
-        a.g = take((size_t)((a.V + kFewValues - 1) / kFewValues) * kFewValues * 16 * 4);
+        a.g = take((size_t)((a.V + 15) / 16) * 16 * 16 * 4);
         a.splits = kFewGroups;
         a.acc = (float*)take((size_t)a.splits * tokens * (size_t)a.acc_row * 4);
         return at;

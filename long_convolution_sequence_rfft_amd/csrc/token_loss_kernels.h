@@ -330,138 +330,151 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2)
     m = top;
 }
 
-// Logits of few tokens: each wave has 16 values and 16 N tokens, and takes its operands
-// from memory to its registers.  Bound by reading the table once, four steps ahead of the
-// products; nothing of it is shared, so nothing goes through LDS.  A table in float32 is
-// read as given and becomes three terms in the registers.  Backward G stays float32,
-// [values of the vocabulary rounded up][16].
+// Logits of few tokens, 16 N of them: bound by reading the table once.  Workgroups take
+// tiles of 16 values in turn, so that all of them together read one piece of the table after
+// the other (a part of the table for each workgroup was a third slower); within a tile each
+// wave has a quarter of the channels.  The operands go from memory to the registers, the
+// next piece ahead of the products; the waves' sums are joined in LDS.  A table in float32
+// is read as given and becomes three terms in the registers.  Forward a workgroup keeps each
+// token's largest and sum; backward G stays float32, [values rounded up][16].
 template <typename T, int N, bool GRAD> __global__ __launch_bounds__(256) void hyena_loss_few(LossArgs p)
 {
     using E = typename LossType<T>::E;
     using frag = typename Mx<E>::frag;
-    constexpr int P = LossType<T>::P, kAhead = 4;
+    using Raw = std::conditional_t<LossType<T>::P == 3, f32x8, frag>;  // as loaded
+    constexpr int P = LossType<T>::P, kPiece = P == 3 && N > 1 ? 3 : 6;        // steps of a piece
     static_assert(!GRAD || N == 1, "");
-    __shared__ float2 lds[4][16 * N];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+    __shared__ f32x4 lds[2][4][N][64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
     const int64_t count = *p.count, t0 = (int64_t)blockIdx.y * (16 * N);
     if (t0 >= count) return;
-    const int32_t v0 = (int32_t)blockIdx.x * kFewValues + wave * 16;
-    const int left = p.V - v0;  // values that there are
-    f32x4 c[N];
+    const int tiles = (p.V + 15) / 16, steps = p.kd / 32, each = (steps + 3) / 4, pieces = (each + kPiece - 1) / kPiece;
+    const int k0 = wave * each, k1 = k0 + each < steps ? k0 + each : steps;  // this wave's steps (none: k0 >= k1)
+    const int64_t rows_block = p.tokens * 64, step_bytes = P == 3 ? 128 : p.values_block;
+    const uint32_t aoff = (uint32_t)i * (uint32_t)p.values_row + g * (P == 3 ? 32 : 16), boff = i * 64 + g * 16;
+    const char* end = p.values + p.values_bytes;
+    auto load_a = [&](int tile, int s, Raw (&a)[kPiece]) {
+        const __amdgpu_buffer_rsrc_t r = operand_rsrc(p.values + (int64_t)tile * 16 * p.values_row + s * step_bytes, end);
 #pragma unroll
-    for (int j = 0; j < N; ++j) c[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = p.kd / 32;
-    const int64_t rows_block = p.tokens * 64;
-    const uint32_t boff = i * 64 + g * 16;
-    auto load_b = [&](const char* b0, int s, frag (&fb)[N]) {
-        const __amdgpu_buffer_rsrc_t r = operand_rsrc(b0 + t0 * 64 + s * rows_block, b0 + p.rows_plane);
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            fb[j] = __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(boff + j * 1024), 0, 0));
-    };
-    if (left > 0) {
-        if constexpr (P == 3) {
-            const uint32_t aoff = (uint32_t)i * (uint32_t)p.values_row + g * 32;
-            const char* at = p.values + (int64_t)v0 * p.values_row;
-            f32x8 a[2][kAhead];
-            auto load = [&](int s, f32x8 (&fa)[kAhead]) {
-                const __amdgpu_buffer_rsrc_t r = operand_rsrc(at + s * 128, p.values + p.values_bytes);
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const f32x4 lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(aoff + k * 128), 0, 0));
-                    const f32x4 hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(aoff + k * 128 + 16), 0, 0));
-                    fa[k] = join8(lo, hi);
-                }
-            };
-            auto multiply = [&](int s, const f32x8 (&fa)[kAhead]) {
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    if (s + k >= steps) break;
-                    Split<E, 3> x;
-                    x.set(fa[k]);
-                    frag b[3][N];
-#pragma unroll
-                    for (int n = 0; n < 3; ++n) load_b(p.rows + n * p.rows_plane, s + k, b[n]);
-#pragma unroll
-                    for (int q = 0; q < Planes<3>::kPairs; ++q)
-#pragma unroll
-                        for (int j = 0; j < N; ++j) c[j] = Mx<E>::mma(x.f[Planes<3>::a(q)], b[Planes<3>::b(q)][j], c[j]);
-                }
-            };
-            load(0, a[0]);
-            for (int s = 0; s < steps; s += 2 * kAhead) {
-                if (s + kAhead < steps) load(s + kAhead, a[1]);
-                multiply(s, a[0]);
-                if (s + 2 * kAhead < steps) load(s + 2 * kAhead, a[0]);
-                multiply(s + kAhead, a[1]);
-            }
-        } else {
-            const uint32_t aoff = (uint32_t)i * (uint32_t)p.values_row + g * 16;
-            const char *at = p.values + (int64_t)v0 * p.values_row, *end = p.values + p.values_bytes;
-            frag a[2][kAhead], b[2][kAhead][N];
-            auto load = [&](int s, frag (&fa)[kAhead], frag (&fb)[kAhead][N]) {
-                const __amdgpu_buffer_rsrc_t r = operand_rsrc(at + s * p.values_block, end);
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    fa[k] = __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(aoff + (uint32_t)k * (uint32_t)p.values_block), 0, 0));
-                    load_b(p.rows, s + k, fb[k]);
-                }
-            };
-            auto multiply = [&](int s, const frag (&fa)[kAhead], const frag (&fb)[kAhead][N]) {
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (s + k < steps) {
-#pragma unroll
-                        for (int j = 0; j < N; ++j) c[j] = Mx<E>::mma(fa[k], fb[k][j], c[j]);
-                    }
-            };
-            load(0, a[0], b[0]);
-            for (int s = 0; s < steps; s += 2 * kAhead) {
-                if (s + kAhead < steps) load(s + kAhead, a[1], b[1]);
-                multiply(s, a[0], b[0]);
-                if (s + 2 * kAhead < steps) load(s + 2 * kAhead, a[0], b[0]);
-                multiply(s + kAhead, a[1], b[1]);
+        for (int k = 0; k < kPiece; ++k) {
+            const uint32_t off = aoff + (uint32_t)k * (uint32_t)step_bytes;
+            if constexpr (P == 3) {
+                const f32x4 lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+                const f32x4 hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off + 16, 0, 0));
+                a[k] = join8(lo, hi);
+            } else {
+                a[k] = __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
             }
         }
-    }
+    };
+    frag b[kPiece][P][N];
+    auto load_b = [&](int s) {
+#pragma unroll
+        for (int n = 0; n < P; ++n) {
+            const char* plane = p.rows + n * p.rows_plane;
+            const __amdgpu_buffer_rsrc_t r = operand_rsrc(plane + t0 * 64 + s * rows_block, plane + p.rows_plane);
+#pragma unroll
+            for (int k = 0; k < kPiece; ++k)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    b[k][n][j] = __builtin_bit_cast(frag, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(boff + j * 1024 + (uint32_t)k * (uint32_t)rows_block), 0, 0));
+        }
+    };
     const float scale2 = p.scale * kLog2e;
+    // the waves take turns at the 16s of tokens
+    constexpr int kOwn = (N + 3) / 4;
+    float top[kOwn], sum[kOwn];
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) top[o] = -INFINITY, sum[o] = 0.0f;
+    f32x4 c[N];
+    // tile and piece of it that are loaded next
+    int next_tile = blockIdx.x, next_piece = 0;
+    auto ahead = [&](Raw (&a)[kPiece]) {
+        if (next_tile < tiles) load_a(next_tile, k0 + next_piece * kPiece, a);
+        if (++next_piece == pieces) next_piece = 0, next_tile += gridDim.x;
+    };
+    int tile = blockIdx.x, piece = 0, half = 0;
+    auto work = [&](const Raw (&a)[kPiece]) {
+        if (piece == 0) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) c[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        const int s = k0 + piece * kPiece;
+        if (pieces > 1) load_b(s);
+#pragma unroll
+        for (int k = 0; k < kPiece; ++k) {
+            if (s + k >= k1) break;
+            if constexpr (P == 3) {
+                Split<E, 3> x;
+                x.set(a[k]);
+#pragma unroll
+                for (int q = 0; q < Planes<3>::kPairs; ++q)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) c[j] = Mx<E>::mma(x.f[Planes<3>::a(q)], b[k][Planes<3>::b(q)][j], c[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) c[j] = Mx<E>::mma(a[k], b[k][0][j], c[j]);
+            }
+        }
+        if (++piece < pieces) return;
+        piece = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) lds[half][wave][j][lane] = c[j];
+        __syncthreads();  // (the other half is written before the next one, and read after it)
+        const int left = p.V - tile * 16;
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int j = o * 4 + wave;
+            if (j >= N) break;
+            f32x4 l = lds[half][0][j][lane];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) l += lds[half][w][j][lane];
+            const int64_t t = t0 + 16 * j + i;
+            const int target = t < count ? p.target[t] - tile * 16 - 4 * g : -1;
+            if constexpr (!GRAD) {
+                float m = -INFINITY, e = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    l[r] = 4 * g + r < left ? l[r] * scale2 : -INFINITY;
+                    if (target == r) p.hit[t] = l[r];
+                    m = fmaxf(m, l[r]);
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) e += __builtin_amdgcn_exp2f(l[r] - base);
+                join(top[o], sum[o], m, e);
+            } else {
+                const bool in = t < count;
+                const float lse2 = in ? p.lse2[t] : 0.0f, weight = in ? p.weight[t] : 0.0f;
+                float* to = (float*)p.g + (int64_t)(tile * 16 + 4 * g) * 16 + i;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float q = __builtin_amdgcn_exp2f(fmaf(l[r], scale2, -lse2));
+                    to[r * 16] = in && 4 * g + r < left ? weight * (target == r ? q - 1.0f : q) : 0.0f;
+                }
+            }
+        }
+        half ^= 1;
+        tile += gridDim.x;
+    };
+    if (pieces == 1) load_b(k0);
+    Raw a0[kPiece], a1[kPiece];
+    ahead(a0);
+    while (true) {
+        if (tile >= tiles) break;
+        ahead(a1);
+        work(a0);
+        if (tile >= tiles) break;
+        ahead(a0);
+        work(a1);
+    }
     if constexpr (!GRAD) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int64_t t = t0 + 16 * j + i;
-            const int target = t < count ? p.target[t] - v0 - 4 * g : -1;
-            float m = -INFINITY, s = 0.0f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                c[j][r] = 4 * g + r < left ? c[j][r] * scale2 : -INFINITY;
-                if (target == r) p.hit[t] = c[j][r];
-                m = fmaxf(m, c[j][r]);
-            }
-            m = fmaxf(m, __shfl_xor(m, 16));
-            m = fmaxf(m, __shfl_xor(m, 32));
-            const float base = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(c[j][r] - base);
-            s += __shfl_xor(s, 16);
-            s += __shfl_xor(s, 32);
-            if (g == 0) lds[wave][16 * j + i] = make_float2(m, s);
-        }
-        __syncthreads();
-        if (threadIdx.x < 16 * N) {
-            float m = -INFINITY, s = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) join(m, s, lds[w][threadIdx.x].x, lds[w][threadIdx.x].y);
-            p.part[(int64_t)blockIdx.x * p.tokens + t0 + threadIdx.x] = make_float2(m, s);
-        }
-    } else {
-        const bool in = i < count;
-        const int target = in ? p.target[i] - v0 - 4 * g : -1;
-        const float lse2 = in ? p.lse2[i] : 0.0f, weight = in ? p.weight[i] : 0.0f;
-        float* to = (float*)p.g + (int64_t)(v0 + 4 * g) * 16 + i;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float q = __builtin_amdgcn_exp2f(fmaf(c[0][r], scale2, -lse2));
-            to[r * 16] = in && 4 * g + r < left ? weight * (target == r ? q - 1.0f : q) : 0.0f;
+        for (int o = 0; o < kOwn; ++o) {
+            const int j = o * 4 + wave;
+            if (j >= N) break;
+            for (int k = 16; k < 64; k *= 2) join(top[o], sum[o], __shfl_xor(top[o], k), __shfl_xor(sum[o], k));
+            if (g == 0) p.part[(int64_t)blockIdx.x * p.tokens + t0 + 16 * j + i] = make_float2(top[o], sum[o]);
         }
     }
 }
@@ -757,7 +770,7 @@ template <typename T> hyena_status loss_forward(const LossArgs& a, bool pack, bo
 {
     hyena_status st = loss_begin<T, false>(a, pack, units, s);
     if (st != HYENA_OK) return st;
-    const int tiles = (a.V + value_tile(a.few) - 1) / value_tile(a.few);
+    const int tiles = a.few ? few_groups(a.V) : loss_tiles(a.V);
     if ((st = loss_logits<T, false>(a, tiles, s)) != HYENA_OK) return st;
     HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>()), hyena_loss_join<T>, dim3((unsigned)((a.total + 15) / 16)), dim3(1024), 0, s, a, tiles);
     return launched();
@@ -772,7 +785,7 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
     for (int64_t first = 0; first < a.V; first += a.chunk) {
         b.first = (int32_t)first;
         const int values = a.V - first < a.chunk ? (int)(a.V - first) : a.chunk;
-        if ((st = loss_logits<T, true>(b, (values + value_tile(a.few) - 1) / value_tile(a.few), s)) != HYENA_OK) return st;
+        if ((st = loss_logits<T, true>(b, a.few ? few_groups(a.V) : loss_tiles(values), s)) != HYENA_OK) return st;
         if (a.few) {  // all of the vocabulary is one piece
             if ((st = a.total <= 4 ? loss_few_grads<T, 4>(a, s) : loss_few_grads<T, 16>(a, s)) != HYENA_OK) return st;
             break;
