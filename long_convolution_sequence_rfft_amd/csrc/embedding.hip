@@ -10,7 +10,9 @@
 //       workgroup's in a cut by ranges).  It reads all tokens twice: counts its
 //       values (each wave its own part of the tokens), which with the count of the
 //       tokens of lower groups gives every value a place, then writes its tokens
-//       there, in order.  One launch, and no workgroup waits for another.
+//       there, in order.  One launch, and no workgroup waits for another.  Of many
+//       tokens hyena_embedding_deal first makes lists: each workgroup deals its 4096
+//       tokens out to the groups, which then read what is theirs only.
 //   hyena_embedding_sums   teams of lanes take runs of the sorted list of one
 //       length, so a value that is everywhere is shared out like any other.  A
 //       value that lies within one run is done: its row is written.  One that
@@ -30,6 +32,11 @@ constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortGroups = 256;   // at least; more where a group would have more values than kSortValues
 constexpr int kSortValues = 384;   // counters of a wave: 24 KB of LDS in all
 constexpr int kSortTokens = 16;    // of a lane, in four loads
+constexpr int kDealTokens = 4096;  // of a workgroup that deals
+constexpr int kDealGroups = 1024;  // at most
+// Calls of fewer tokens are not dealt (values of a text in a vocabulary of 50257, dealt and
+// sorted, against sorted only: 65536 tokens 20 and 19 us, 2^20 tokens 129 and 410).
+constexpr int64_t kDealCalls = 131072;
 constexpr int kSortKept = 512;     // tokens of its values that a wave keeps: 32 KB of LDS in all
 constexpr int kSumRows = 4;        // gradient rows of a team under way
 constexpr int64_t kSumTeams = 4096;  // runs are no shorter than kSumRows, and as short as this many of them allow
@@ -54,6 +61,9 @@ struct EmbedArgs {
     int2* sorted;        // [total] value and token, in order; [total].x the number of tokens that take part
     int4* joins;         // [V] values that reach over runs, where they begin, tokens: group g's from g * values on
     int32_t* join_counts;  // [groups]
+    int2* dealt;         // [blocks of kDealTokens] value and token, by groups; NULL: the sort reads the tokens
+    int32_t* deal_starts;  // [groups + 1][blocks] where a group begins in a block
+    int32_t deal_blocks;
     float* part;         // [runs][2][d4]: sums that reach over a run's start and over its end
     int32_t d4;          // d rounded up to 4
 };
@@ -116,6 +126,77 @@ __device__ __forceinline__ int workgroup_sum(int x, int* lds)
     return x;
 }
 
+// kDealTokens tokens by groups, in the order they are read within each.
+template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embedding_deal(EmbedArgs p)
+{
+    extern __shared__ int counters[];  // [waves][groups]
+    __shared__ int lds[kSortWaves];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, bits = __builtin_ctz(p.groups);
+    const int64_t first = (int64_t)blockIdx.x * kDealTokens;
+    int* own = counters + wave * p.groups;
+    for (int i = threadIdx.x; i < p.groups * kSortWaves; i += kSortThreads) counters[i] = 0;
+    __syncthreads();
+    static_assert(kDealTokens == 4 * kSortThreads, "");
+    int v[4], at[4];
+    const int64_t t0 = first + wave * 256 + 4 * lane;
+    if (DENSE && t0 + 4 <= p.total) {
+        const Four x = *(const Four*)((const int32_t*)p.tokens.p + t0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = x.v[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = t0 + k < p.total ? token_at(p, t0 + k) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const bool in = (uint32_t)v[k] < (uint32_t)p.V;
+        const int group = v[k] & (p.groups - 1);
+        uint64_t same = __ballot(in);  // the lanes of one group
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t ones = __ballot(group >> b & 1);
+            same &= group >> b & 1 ? ones : ~ones;
+        }
+        if (in) {
+            const int before = own[group], rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+            at[k] = before + rank;
+            own[group] = before + __popcll(same);  // every lane of the group the same value
+        }
+    }
+    __syncthreads();
+    // counts to places: thread i has group i
+    const int i = threadIdx.x;
+    int mine = 0;
+    if (i < p.groups)
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = counters[w * p.groups + i];
+            counters[w * p.groups + i] = mine;
+            mine += c;
+        }
+    int before = mine;
+    for (int m = 1; m < 64; m *= 2) {
+        const int up = __shfl_up(before, m);
+        if (lane >= m) before += up;
+    }
+    if (lane == 63) lds[wave] = before;
+    __syncthreads();
+    before -= mine;
+    int all = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        if (w < wave) before += lds[w];
+        all += lds[w];
+    }
+    if (i < p.groups) {
+        for (int w = 0; w < kSortWaves; ++w) counters[w * p.groups + i] += before;
+        p.deal_starts[(int64_t)i * p.deal_blocks + blockIdx.x] = before;
+    }
+    if (i == 0) p.deal_starts[(int64_t)p.groups * p.deal_blocks + blockIdx.x] = all;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if ((uint32_t)v[k] < (uint32_t)p.V)
+            p.dealt[first + own[v[k] & (p.groups - 1)] + at[k]] = make_int2(v[k], (int)(t0 + k));
+}
+
 template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embedding_sort(EmbedArgs p)
 {
     extern __shared__ int counters[];  // [waves][values]
@@ -124,15 +205,45 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
     const int group = blockIdx.x, shift = __builtin_ctz(p.groups);
     const int values = (p.V - group + p.groups - 1) >> shift;  // v = group + groups * i, i < values
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    // each wave a part of the tokens, whole 64s of them
-    const int64_t each = ((p.total + 64 * kSortWaves - 1) / (64 * kSortWaves)) * 64;
+    // each wave a part of the tokens (whole 64s of them) or of the blocks that were dealt out
+    const int blocks = (p.deal_blocks + kSortWaves - 1) / kSortWaves;
+    const int b0 = blocks * wave, b1 = b0 + blocks < p.deal_blocks ? b0 + blocks : p.deal_blocks;
+    const int64_t each = p.dealt != nullptr ? (int64_t)blocks * kDealTokens : ((p.total + 64 * kSortWaves - 1) / (64 * kSortWaves)) * 64;
     const int64_t first = each * wave, last = first + each < p.total ? first + each : p.total;
 
     for (int i = threadIdx.x; i < values * kSortWaves; i += kSortThreads) counters[i] = 0;
     if (threadIdx.x == 0) join_count = 0;
     __syncthreads();
     int lower = 0, all = 0;
+    // this wave's dealt tokens of the group, 64 at a time: f(there is one, value, token)
+    auto each_dealt = [&](auto f) {
+        const int32_t *lo = p.deal_starts + (int64_t)group * p.deal_blocks, *hi = lo + p.deal_blocks;
+        for (int b = b0; b < b1; ++b) {
+            const int n = hi[b] - lo[b];
+            const int2* list = p.dealt + (int64_t)b * kDealTokens + lo[b];
+            for (int k = 0; k < n; k += 64) {
+                const bool own = k + lane < n;
+                const int2 e = own ? list[k + lane] : make_int2(0, 0);
+                f(own, e.x, (int64_t)e.y);
+            }
+        }
+    };
     int n_own = 0;  // this wave's tokens of the group's values; the first kSortKept are kept: i << 22 | place in its part
+    if (p.dealt != nullptr) {
+        const int32_t *lo = p.deal_starts + (int64_t)group * p.deal_blocks, *end = p.deal_starts + (int64_t)p.groups * p.deal_blocks;
+        for (int b = threadIdx.x; b < p.deal_blocks; b += kSortThreads) {
+            lower += lo[b];
+            all += end[b];
+        }
+        each_dealt([&](bool own, int v, int64_t t) {
+            const int i = v >> shift;
+            if (own) {
+                atomicAdd(&counters[wave * values + i], 1);
+                if (n_own + lane < kSortKept) kept[wave][n_own + lane] = (uint32_t)i << 22 | (uint32_t)(t - first);
+            }
+            n_own += __popcll(__ballot(own));
+        });
+    } else
     for (int64_t t0 = first; t0 < last; t0 += 64 * kSortTokens) {
         int v[kSortTokens];
         load_tokens<DENSE>(p, t0, last, v);
@@ -228,6 +339,10 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
         return;
     }
     // too many to keep: the tokens again
+    if (p.dealt != nullptr) {
+        each_dealt([&](bool own, int v, int64_t t) { put(own, v >> shift, t); });
+        return;
+    }
     for (int64_t t0 = first; t0 < last; t0 += 64 * kSortTokens) {
         int v[kSortTokens];
         load_tokens<DENSE>(p, t0, last, v);
@@ -387,7 +502,8 @@ hyena_status embed_sizes(const hyena_embedding* op)
 
 struct EmbedSpace {
     int64_t run, runs;
-    size_t sorted, counts, joins, join_counts, part, total;  // byte offsets and the size
+    size_t sorted, counts, joins, join_counts, dealt, deal_starts, part, total;  // byte offsets and the size
+    int32_t deal_blocks;  // 0: not dealt
     int32_t groups, d4;
 };
 
@@ -407,7 +523,10 @@ EmbedSpace embed_space(const hyena_embedding* op)
     w.d4 = (int32_t)((op->d + 3) / 4 * 4);
     w.joins = w.counts + up((size_t)op->V * 4);
     w.join_counts = w.joins + up((size_t)((op->V + w.groups - 1) / w.groups * w.groups) * sizeof(int4));
-    w.part = w.join_counts + up((size_t)w.groups * 4);
+    w.deal_blocks = T >= kDealCalls && w.groups <= kDealGroups ? (int32_t)((T + kDealTokens - 1) / kDealTokens) : 0;
+    w.dealt = w.join_counts + up((size_t)w.groups * 4);
+    w.deal_starts = w.dealt + up((size_t)w.deal_blocks * kDealTokens * sizeof(int2));
+    w.part = w.deal_starts + up((size_t)(w.groups + 1) * (size_t)w.deal_blocks * 4);
     w.total = w.part + (size_t)w.runs * 2 * (size_t)w.d4 * 4;
     return w;
 }
@@ -425,9 +544,19 @@ void team_shape(EmbedArgs& a, size_t element)
 template <typename T> hyena_status embed_backward(const EmbedArgs& a, bool vec, int64_t runs, hipStream_t s)
 {
     hyena_status st;
+    const bool dense = a.N == 0 && a.tokens.t == 1;
+    if (a.dealt != nullptr) {
+        const dim3 grid((unsigned)a.deal_blocks);
+        const size_t lds = (size_t)a.groups * kSortWaves * 4;
+        if (dense)
+            HY_LAUNCH(kernel_label("hyena_embedding_deal", true), hyena_embedding_deal<true>, grid, dim3(kSortThreads), lds, s, a);
+        else
+            HY_LAUNCH(kernel_label("hyena_embedding_deal", false), hyena_embedding_deal<false>, grid, dim3(kSortThreads), lds, s, a);
+        if ((st = launched()) != HYENA_OK) return st;
+    }
     const dim3 sort_grid((unsigned)a.groups);
     const size_t sort_lds = (size_t)((a.V + a.groups - 1) / a.groups) * kSortWaves * 4;
-    if (a.N == 0 && a.tokens.t == 1)
+    if (dense)
         HY_LAUNCH(kernel_label("hyena_embedding_sort", true), hyena_embedding_sort<true>, sort_grid, dim3(kSortThreads), sort_lds, s, a);
     else
         HY_LAUNCH(kernel_label("hyena_embedding_sort", false), hyena_embedding_sort<false>, sort_grid, dim3(kSortThreads), sort_lds, s, a);
@@ -548,6 +677,9 @@ hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_row
     a.sorted = (int2*)((char*)scratch + w.sorted);
     a.counts = (int32_t*)((char*)scratch + w.counts);
     a.part = (float*)((char*)scratch + w.part);
+    a.deal_blocks = w.deal_blocks;
+    a.dealt = w.deal_blocks ? (int2*)((char*)scratch + w.dealt) : nullptr;
+    a.deal_starts = (int32_t*)((char*)scratch + w.deal_starts);
     const int64_t teams = 256 / a.lanes;
     a.sum_groups = (int32_t)((w.runs + teams - 1) / teams);
     const int64_t fill = (a.V + teams - 1) / teams;

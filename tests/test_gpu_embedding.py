@@ -168,3 +168,16 @@ def test_replayed_graphs_match_eager_calls():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, plan.forward(at, table)) and torch.equal(g, plan.backward(d_out, at))
+
+
+@pytest.mark.parametrize("kind", ["text", "even", "same", "padded"])
+def test_calls_of_many_tokens(kind):
+    # from 131072 tokens on they are dealt out to the groups of values first
+    rng = np.random.default_rng(8)
+    for (B, N, V, d), strided in (((1, 131072, 1000, 8), False), ((3, 45000, 50000, 4), True), ((2, 70001, 300000, 4), False)):
+        tok = text(rng, (B, N), V) if kind == "text" else rng.integers(0, V, (B, N))
+        if kind == "same":
+            tok[:] = V // 2
+        if kind == "padded":
+            tok[:, N // 3:] = -1
+        run((B, N, V, d), "f32", tokens=tok, strided=strided, accumulate=kind == "even")
