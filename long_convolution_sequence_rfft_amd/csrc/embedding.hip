@@ -40,7 +40,7 @@ constexpr int64_t kDealCalls = 131072;
 constexpr int kSortKept = 512;     // tokens of its values that a wave keeps: 32 KB of LDS in all
 constexpr int kSumRows = 4;        // gradient rows of a team under way
 constexpr int64_t kSumTeams = 4096;  // runs are no shorter than kSumRows, and as short as this many of them allow
-constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64;
+constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / 64;
 
 struct EmbedArgs {
     Rows tokens, rows;   // rows: d_out
@@ -50,7 +50,6 @@ struct EmbedArgs {
     uint32_t N, rows_N;  // row_at, of the tokens and of the rows
     int32_t V, d;
     int32_t lanes;       // of a team, a power of two
-    int32_t pairs;
     int32_t accumulate;
     float scale;
     int32_t groups;      // of the sort, a power of two
@@ -93,7 +92,7 @@ template <bool DENSE> __device__ __forceinline__ void load_tokens(const EmbedArg
     }
 }
 
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_embedding_gather(EmbedArgs p)
+template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_embedding_gather(EmbedArgs p)
 {
     constexpr int K = kUnit<T>;
     const int teams = 256 / p.lanes, team = threadIdx.x / p.lanes, tl = threadIdx.x % p.lanes;
@@ -104,12 +103,10 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_emb
         T* out = (T*)p.out + t * p.d;
         for (int c = tl * K; c < p.d; c += p.lanes * K) {
             float x[K];
-#pragma unroll
-            for (int i = 0; i < K; ++i) x[i] = 0.0f;
-            if (in) load_unit<T, VEC>(row, c, p.d, p.pairs, x);
+            if (in) load_unit<T, UNITS>(row, c, p.d, x);
 #pragma unroll
             for (int i = 0; i < K; ++i) x[i] = in ? x[i] * p.scale : 0.0f;
-            store_unit<T, VEC>(out, c, p.d, p.pairs, x);
+            store_unit<T, UNITS>(out, c, p.d, x);
         }
     }
 }
@@ -353,12 +350,11 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
 }
 
 // blockIdx.y: which of the row's blocks of `lanes` units.
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_embedding_sums(EmbedArgs p)
+template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_embedding_sums(EmbedArgs p)
 {
     constexpr int K = kUnit<T>;
     const int teams = 256 / p.lanes, team = threadIdx.x / p.lanes, tl = threadIdx.x % p.lanes;
     const int c = ((int)blockIdx.y * p.lanes + tl) * K;
-    const bool in = c < p.d;
     float zero[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) zero[i] = 0.0f;
@@ -368,7 +364,7 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_emb
         for (int64_t v = (int64_t)((int)blockIdx.x - p.sum_groups) * teams + team; v < p.V; v += step) {
             if (p.counts[v] != 0) continue;
             T* row = (T*)p.out + v * p.d;
-            if (in) store_unit<T, VEC>(row, c, p.d, p.pairs, zero);
+            store_unit<T, UNITS>(row, c, p.d, zero);
         }
         return;
     }
@@ -397,15 +393,13 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_emb
             on[k] = (at_end ? next_value : e[k + 1].x) == e[k].x;
             ends[k] = i0 + k < last && (at_end || !on[k]);
         }
-        RawUnit<T, VEC> x[kSumRows], old[kSumRows];
+        Unit<T, UNITS> x[kSumRows], old[kSumRows];
 #pragma unroll
         for (int k = 0; k < kSumRows; ++k) {
             const T* row = row_at<T>(p.rows, e[k].y, p.rows_N);
             const T* there = (const T*)p.out + (int64_t)e[k].x * p.d;
-            if (in) {
-                x[k].load(row, c, p.d, p.pairs);
-                if (p.accumulate && ends[k]) old[k].load(there, c, p.d, p.pairs);
-            }
+            x[k].load(row, c, p.d);
+            if (p.accumulate && ends[k]) old[k].load(there, c, p.d);
         }
 #pragma unroll
         for (int k = 0; k < kSumRows; ++k) {
@@ -415,18 +409,16 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_emb
 #pragma unroll
             for (int i = 0; i < K; ++i) s[i] += y[i];
             if (!ends[k]) continue;
-            if (in) {
-                if (open || on[k]) {  // a piece
-                    float* part = p.part + (run * 2 + (open ? 0 : 1)) * p.d4 + c;
+            if (open || on[k]) {  // a piece
+                float* part = p.part + (run * 2 + (open ? 0 : 1)) * p.d4 + c;
 #pragma unroll
-                    for (int i = 0; i < K; i += 4)
-                        if (c + i < p.d4) *(f32x4*)(part + i) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
-                } else {
-                    if (p.accumulate) old[k].widen(y);
+                for (int i = 0; i < K; i += 4)
+                    if (c + i < p.d4) *(f32x4*)(part + i) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
+            } else {
+                if (p.accumulate) old[k].widen(y);
 #pragma unroll
-                    for (int i = 0; i < K; ++i) y[i] = p.accumulate ? fmaf(s[i], p.scale, y[i]) : s[i] * p.scale;
-                    store_unit<T, VEC>((T*)p.out + (int64_t)e[k].x * p.d, c, p.d, p.pairs, y);
-                }
+                for (int i = 0; i < K; ++i) y[i] = p.accumulate ? fmaf(s[i], p.scale, y[i]) : s[i] * p.scale;
+                store_unit<T, UNITS>((T*)p.out + (int64_t)e[k].x * p.d, c, p.d, y);
             }
 #pragma unroll
             for (int i = 0; i < K; ++i) s[i] = 0.0f;
@@ -541,7 +533,7 @@ void team_shape(EmbedArgs& a, size_t element)
     if (used(32) < used(64)) a.lanes = 32;
 }
 
-template <typename T> hyena_status embed_backward(const EmbedArgs& a, bool vec, int64_t runs, hipStream_t s)
+template <typename T> hyena_status embed_backward(const EmbedArgs& a, bool units, int64_t runs, hipStream_t s)
 {
     hyena_status st;
     const bool dense = a.N == 0 && a.tokens.t == 1;
@@ -563,11 +555,11 @@ template <typename T> hyena_status embed_backward(const EmbedArgs& a, bool vec, 
     if ((st = launched()) != HYENA_OK) return st;
     const int block = a.lanes * kUnit<T>;
     const dim3 grid((unsigned)(a.sum_groups + a.fill_groups), (unsigned)((a.d + block - 1) / block));
-    if (vec)
-        HY_LAUNCH(kernel_label("hyena_embedding_sums", type_label<T>(), true), (hyena_embedding_sums<T, true>), grid, dim3(256), 0, s, a);
-    else
-        HY_LAUNCH(kernel_label("hyena_embedding_sums", type_label<T>(), false), (hyena_embedding_sums<T, false>), grid, dim3(256), 0, s, a);
-    st = launched();
+    st = by_units(units, [&](auto u) {
+        constexpr bool UNITS = decltype(u)::value;
+        HY_LAUNCH(kernel_label("hyena_embedding_sums", type_label<T>(), UNITS), (hyena_embedding_sums<T, UNITS>), grid, dim3(256), 0, s, a);
+        return launched();
+    });
     if (st != HYENA_OK || runs < 2) return st;
     HY_LAUNCH(kernel_label("hyena_embedding_joins", type_label<T>()), hyena_embedding_joins<T>,
               dim3((unsigned)a.groups, (unsigned)((a.d + 255) / 256)), dim3(kJoinThreads), 0, s, a);
@@ -614,20 +606,18 @@ hyena_status hyena_embedding_forward(const hyena_embedding* op, const void* tabl
     RowShape made(op->d, e);
     made.dense(table);
     made.dense(out);
-    a.pairs = made.made_of() >= kMadeOfPairs;
     a.table = table;
     a.out = out;
     const int64_t teams = 256 / a.lanes, need = (a.total + teams - 1) / teams, most = (int64_t)1 << 20;
     const dim3 grid((unsigned)(need < most ? need : most));
-    const bool vec = made.made_of() == kMadeOfUnits;
     const hipStream_t s = (hipStream_t)stream;
     return by_io(op->io_dtype, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        if (vec)
-            HY_LAUNCH(kernel_label("hyena_embedding_gather", type_label<T>(), true), (hyena_embedding_gather<T, true>), grid, dim3(256), 0, s, a);
-        else
-            HY_LAUNCH(kernel_label("hyena_embedding_gather", type_label<T>(), false), (hyena_embedding_gather<T, false>), grid, dim3(256), 0, s, a);
-        return launched();
+        return by_units(made.units(), [&](auto u) {
+            constexpr bool UNITS = decltype(u)::value;
+            HY_LAUNCH(kernel_label("hyena_embedding_gather", type_label<T>(), UNITS), (hyena_embedding_gather<T, UNITS>), grid, dim3(256), 0, s, a);
+            return launched();
+        });
     });
 }
 
@@ -661,7 +651,6 @@ hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_row
     RowShape made(op->d, e);
     made.add(rows);
     made.dense(d_table);
-    a.pairs = made.made_of() >= kMadeOfPairs;
     int64_t N = op->N;
     hyena_rows* one[1] = {&rows};
     flatten_rows(one, 1, op->B, &N);
@@ -684,9 +673,8 @@ hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_row
     a.sum_groups = (int32_t)((w.runs + teams - 1) / teams);
     const int64_t fill = (a.V + teams - 1) / teams;
     a.fill_groups = a.accumulate ? 0 : (int32_t)(fill < 2048 ? fill : 2048);
-    const bool vec = made.made_of() == kMadeOfUnits;
     return by_io(op->io_dtype, [&](auto* t) {
-        return embed_backward<std::remove_pointer_t<decltype(t)>>(a, vec, w.runs, (hipStream_t)stream);
+        return embed_backward<std::remove_pointer_t<decltype(t)>>(a, made.units(), w.runs, (hipStream_t)stream);
     });
 }
 

@@ -17,7 +17,6 @@ struct NormArgs {
     uint32_t N;          // row_at
     int32_t d;
     int32_t lanes;       // of a team that is part of a wave
-    int32_t pairs;
     int32_t weight_vectors;  // weight is 16-byte aligned
     int32_t int8;
     int32_t group_lanes; // 0: a scale for each row
@@ -26,9 +25,14 @@ struct NormArgs {
     float eps;
 };
 
+// Units of a lane where a workgroup holds a row: 16 channels, which with three tensors and
+// the sums for the weights' gradient fill the registers of 1024 threads.
+template <typename T> constexpr int kWideUnits = 16 / kUnit<T>;
+
 struct NormLaunch {
-    bool vec, workgroup;
-    int units;           // per lane
+    bool units;          // rows are made of whole aligned units
+    bool workgroup;
+    int per;             // units of a lane
     int threads;
     int64_t groups;      // workgroups
 };

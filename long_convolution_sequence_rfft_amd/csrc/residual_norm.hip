@@ -46,15 +46,15 @@ hyena_status norm_sizes(const hyena_residual_norm* op)
 
 // Teams: as many lanes of a wave, a power of two, as leave the fewest idle with at
 // most 4 units each; wider rows take a workgroup.  least: lanes of a group of scales.
-NormLaunch shape(const NormArgs& a, size_t element, bool vec, bool grad, int least, int32_t* lanes)
+NormLaunch shape(const NormArgs& a, size_t element, bool whole, bool grad, int least, int32_t* lanes)
 {
     NormLaunch l{};
-    l.vec = vec;
+    l.units = whole;
     const int units = (int)((a.d * element + 15) / 16);
     l.workgroup = units > 256;
     if (l.workgroup) {
-        l.threads = units > 1024 ? 1024 : 256;
-        l.units = (units + l.threads - 1) / l.threads;
+        l.per = (int)element;  // kWideUnits
+        l.threads = ((units + l.per - 1) / l.per + 63) / 64 * 64;
         *lanes = l.threads;
     } else {
         int best = 64;
@@ -64,11 +64,11 @@ NormLaunch shape(const NormArgs& a, size_t element, bool vec, bool grad, int lea
             if (per * n < ((units + best - 1) / best) * best) best = n;
         }
         l.threads = 256;
-        l.units = (units + best - 1) / best;
+        l.per = (units + best - 1) / best;
         *lanes = best;
     }
     const int64_t teams = l.workgroup ? 1 : 256 / *lanes, need = (a.rows + teams - 1) / teams;
-    const int64_t most = (grad ? kNormGradGroups : kNormGroups) / (l.threads / 256);
+    const int64_t most = (grad ? kNormGradGroups : kNormGroups) * 256 / l.threads;
     l.groups = need < most ? need : most;
     return l;
 }
@@ -126,9 +126,8 @@ hyena_status hyena_residual_norm_forward(const hyena_residual_norm* op, void* su
     made.add(x);
     if (added) made.add(res), made.dense(sum);
     if (!eight) made.dense(y);
-    bool vec = made.made_of() == kMadeOfUnits;
-    if (eight) vec = vec && (uintptr_t)y % 4 == 0 && op->d % 4 == 0;
-    a.pairs = made.made_of() >= kMadeOfPairs;
+    // (8-bit rows of whole units are written by 4 bytes)
+    const bool units = made.units() && (!eight || (uintptr_t)y % 4 == 0);
     int64_t N = op->N;
     hyena_rows* all_rows[2] = {&x, &res};
     flatten_rows(all_rows, added ? 2 : 1, op->B, &N);
@@ -148,7 +147,7 @@ hyena_status hyena_residual_norm_forward(const hyena_residual_norm* op, void* su
     a.largest = a.int8 ? 127.0f : 448.0f;
     a.inverse = 1.0f / a.largest;
     a.eps = op->eps;
-    const NormLaunch l = shape(a, e, vec, false, a.group_lanes, &a.lanes);
+    const NormLaunch l = shape(a, e, units, false, a.group_lanes, &a.lanes);
     return by_io(op->io_dtype, [&](auto* t) {
         return norm_launch<std::remove_pointer_t<decltype(t)>>(a, l, eight ? 1 : 0, (hipStream_t)stream);
     });
@@ -193,8 +192,7 @@ hyena_status hyena_residual_norm_backward(const hyena_residual_norm* op, const h
     made.add(dy);
     if (more) made.add(ds);
     made.dense(d_x);
-    a.pairs = made.made_of() >= kMadeOfPairs;
-    const NormLaunch l = shape(a, e, made.made_of() == kMadeOfUnits, true, 1, &a.lanes);
+    const NormLaunch l = shape(a, e, made.units(), true, 1, &a.lanes);
 
     const bool on = more && d_x == ds.data && (op->N == 1 || ds.token == op->d) && (op->B == 1 || ds.batch == op->N * op->d);
     const Span ins[4] = {rows_span(x, op->B, op->N, op->d, e), rows_span(dy, op->B, op->N, op->d, e),

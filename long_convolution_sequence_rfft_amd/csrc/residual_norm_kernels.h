@@ -62,12 +62,12 @@ template <bool WG> __device__ __forceinline__ uint32_t team_max(uint32_t a, int 
 __device__ __forceinline__ float rms(float squares, int d, float eps) { return 1.0f / sqrtf(squares / (float)d + eps); }
 
 // The weights of a unit (ones without).
-template <bool VEC, int K> __device__ __forceinline__ void load_weights(const NormArgs& p, int c, float (&w)[K])
+template <bool UNITS, int K> __device__ __forceinline__ void load_weights(const NormArgs& p, int c, float (&w)[K])
 {
 #pragma unroll
     for (int i = 0; i < K; ++i) w[i] = 1.0f;
     if (p.w == nullptr || c >= p.d) return;
-    if (VEC && p.weight_vectors) {
+    if (UNITS && p.weight_vectors) {
 #pragma unroll
         for (int i = 0; i < K; i += 4) {
             const f32x4 v = *(const f32x4*)(p.w + c + i);
@@ -98,7 +98,7 @@ template <int K> __device__ __forceinline__ void pack8(const float (&y)[K], bool
     }
 }
 
-template <typename T, bool VEC, bool WG, int U, bool EIGHT>
+template <typename T, bool UNITS, bool WG, int U, bool EIGHT>
 __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm(NormArgs p)
 {
     constexpr int K = kUnit<T>;
@@ -108,37 +108,25 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm(NormArgs 
     float w[U][K];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int c = (tl + u * lanes) * K;
-        load_weights<VEC>(p, c, w[u]);
+        load_weights<UNITS>(p, (tl + u * lanes) * K, w[u]);
     }
     for (int64_t r = (int64_t)blockIdx.x * teams + team; r < p.rows; r += (int64_t)gridDim.x * teams) {
         const T* x = row_at<T>(p.x, r, p.N);
         const T* res = p.res.p != nullptr ? row_at<T>(p.res, r, p.N) : nullptr;
         float s[U][K];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = (tl + u * lanes) * K;
-#pragma unroll
-            for (int i = 0; i < K; ++i) s[u][i] = 0.0f;
-            if (c < p.d) load_unit<T, VEC>(x, c, p.d, p.pairs, s[u]);
-        }
+        for (int u = 0; u < U; ++u) load_unit<T, UNITS>(x, (tl + u * lanes) * K, p.d, s[u]);
         if (res != nullptr) {
             float y[U][K];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = (tl + u * lanes) * K;
-                if (c < p.d) {
-                    load_unit<T, VEC>(res, c, p.d, p.pairs, y[u]);
+                load_unit<T, UNITS>(res, (tl + u * lanes) * K, p.d, y[u]);
 #pragma unroll
-                    for (int i = 0; i < K; ++i) s[u][i] += y[u][i];
-                }
+                for (int i = 0; i < K; ++i) s[u][i] += y[u][i];
             }
             T* sum = (T*)p.sum + r * p.d;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = (tl + u * lanes) * K;
-                if (c < p.d) store_unit<T, VEC>(sum, c, p.d, p.pairs, s[u]);
-            }
+            for (int u = 0; u < U; ++u) store_unit<T, UNITS>(sum, (tl + u * lanes) * K, p.d, s[u]);
         }
         float squares = 0.0f, none = 0.0f;
 #pragma unroll
@@ -154,10 +142,7 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm(NormArgs 
         if constexpr (!EIGHT) {
             T* y = (T*)p.y + r * p.d;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = (tl + u * lanes) * K;
-                if (c < p.d) store_unit<T, VEC>(y, c, p.d, p.pairs, s[u]);
-            }
+            for (int u = 0; u < U; ++u) store_unit<T, UNITS>(y, (tl + u * lanes) * K, p.d, s[u]);
         } else {
             uint32_t top[U], row = 0;
 #pragma unroll
@@ -191,7 +176,7 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm(NormArgs 
                     for (int i = 0; i < K; ++i) v[i] = some ? s[u][i] * down : 0.0f;
                     uint32_t q[K / 4];
                     pack8<K>(v, p.int8, q);
-                    if (VEC) {
+                    if (UNITS) {
 #pragma unroll
                         for (int i = 0; i < K / 4; ++i) *(uint32_t*)(y + c + 4 * i) = q[i];
                     } else {
@@ -207,7 +192,7 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm(NormArgs 
     }
 }
 
-template <typename T, bool VEC, bool WG, int U>
+template <typename T, bool UNITS, bool WG, int U>
 __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(NormArgs p)
 {
     constexpr int K = kUnit<T>;
@@ -218,8 +203,7 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(Norm
     float w[U][K], dw[U][K];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int c = (tl + u * lanes) * K;
-        load_weights<VEC>(p, c, w[u]);
+        load_weights<UNITS>(p, (tl + u * lanes) * K, w[u]);
 #pragma unroll
         for (int i = 0; i < K; ++i) dw[u][i] = 0.0f;
     }
@@ -229,21 +213,15 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(Norm
         float s[U][K], dy[U][K], ds[U][K];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = (tl + u * lanes) * K;
+            load_unit<T, UNITS>(x, (tl + u * lanes) * K, p.d, s[u]);
+            load_unit<T, UNITS>(dyr, (tl + u * lanes) * K, p.d, dy[u]);
 #pragma unroll
-            for (int i = 0; i < K; ++i) s[u][i] = dy[u][i] = ds[u][i] = 0.0f;
-            if (c < p.d) {
-                load_unit<T, VEC>(x, c, p.d, p.pairs, s[u]);
-                load_unit<T, VEC>(dyr, c, p.d, p.pairs, dy[u]);
-            }
+            for (int i = 0; i < K; ++i) ds[u][i] = 0.0f;
         }
         if (p.res.p != nullptr) {
             const T* dsr = row_at<T>(p.res, r, p.N);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = (tl + u * lanes) * K;
-                if (c < p.d) load_unit<T, VEC>(dsr, c, p.d, p.pairs, ds[u]);
-            }
+            for (int u = 0; u < U; ++u) load_unit<T, UNITS>(dsr, (tl + u * lanes) * K, p.d, ds[u]);
         }
         float squares = 0.0f, along = 0.0f;
 #pragma unroll
@@ -258,39 +236,37 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(Norm
         T* dx = (T*)p.y + r * p.d;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = (tl + u * lanes) * K;
 #pragma unroll
             for (int i = 0; i < K; ++i) {
                 const float n = s[u][i] * rstd;
                 s[u][i] = fmaf(rstd, fmaf(-n, mean, dy[u][i] * w[u][i]), ds[u][i]);
                 dw[u][i] = fmaf(dy[u][i], n, dw[u][i]);
             }
-            if (c < p.d) store_unit<T, VEC>(dx, c, p.d, p.pairs, s[u]);
+            store_unit<T, UNITS>(dx, (tl + u * lanes) * K, p.d, s[u]);
         }
     }
     if (p.dw_part == nullptr) return;
     float* part = p.dw_part + (int64_t)blockIdx.x * p.d;
     if constexpr (WG) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = (tl + u * lanes) * K;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < K; ++i)
-                if (c + i < p.d) part[c + i] = dw[u][i];
-        }
+            for (int i = 0; i < K; ++i) {
+                const int c = (tl + u * lanes) * K + i;
+                if (c < p.d) part[c] = dw[u][i];
+            }
     } else {
         // the teams of a wave, then the waves, in their order
         const int wave = threadIdx.x >> 6;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = (tl + u * lanes) * K;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < K; ++i) {
+                const int c = (tl + u * lanes) * K + i;
                 float v = dw[u][i];
                 for (int m = lanes; m < 64; m *= 2) v += __shfl_xor(v, m);
-                if ((threadIdx.x & 63) < (unsigned)lanes && c + i < p.d) sums[wave * p.d + c + i] = v;
+                if ((threadIdx.x & 63) < (unsigned)lanes && c < p.d) sums[wave * p.d + c] = v;
             }
-        }
         __syncthreads();
         for (int c = threadIdx.x; c < p.d; c += 256) {
             float v = 0.0f;
@@ -301,34 +277,33 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(Norm
     }
 }
 
-template <typename T, bool VEC, bool WG, int U, int KIND> hyena_status norm_as(const NormArgs& a, const NormLaunch& l, hipStream_t s)
+template <typename T, bool UNITS, bool WG, int U, int KIND> hyena_status norm_as(const NormArgs& a, const NormLaunch& l, hipStream_t s)
 {
     if constexpr (KIND == 2)
-        HY_LAUNCH(kernel_label("hyena_residual_norm_grad", type_label<T>(), VEC, WG, U), (hyena_residual_norm_grad<T, VEC, WG, U>),
+        HY_LAUNCH(kernel_label("hyena_residual_norm_grad", type_label<T>(), UNITS, WG, U), (hyena_residual_norm_grad<T, UNITS, WG, U>),
                   dim3((unsigned)l.groups), dim3((unsigned)l.threads), WG ? 0 : (size_t)4 * a.d * sizeof(float), s, a);
     else
-        HY_LAUNCH(kernel_label("hyena_residual_norm", type_label<T>(), VEC, WG, U, KIND == 1), (hyena_residual_norm<T, VEC, WG, U, KIND == 1>),
+        HY_LAUNCH(kernel_label("hyena_residual_norm", type_label<T>(), UNITS, WG, U, KIND == 1), (hyena_residual_norm<T, UNITS, WG, U, KIND == 1>),
                   dim3((unsigned)l.groups), dim3((unsigned)l.threads), 0, s, a);
     return launched();
 }
 
-template <typename T, bool VEC, int KIND> hyena_status norm_sized(const NormArgs& a, const NormLaunch& l, hipStream_t s)
+template <typename T, bool UNITS, int KIND> hyena_status norm_sized(const NormArgs& a, const NormLaunch& l, hipStream_t s)
 {
-    if (l.workgroup) return l.units <= 2 ? norm_as<T, VEC, true, 2, KIND>(a, l, s) : norm_as<T, VEC, true, 4, KIND>(a, l, s);
-    if (l.units == 1) return norm_as<T, VEC, false, 1, KIND>(a, l, s);
-    if (l.units == 2) return norm_as<T, VEC, false, 2, KIND>(a, l, s);
-    if (l.units == 3) return norm_as<T, VEC, false, 3, KIND>(a, l, s);
-    return norm_as<T, VEC, false, 4, KIND>(a, l, s);
+    if (l.workgroup) return norm_as<T, UNITS, true, kWideUnits<T>, KIND>(a, l, s);
+    if (l.per == 1) return norm_as<T, UNITS, false, 1, KIND>(a, l, s);
+    if (l.per == 2) return norm_as<T, UNITS, false, 2, KIND>(a, l, s);
+    if (l.per == 3) return norm_as<T, UNITS, false, 3, KIND>(a, l, s);
+    return norm_as<T, UNITS, false, 4, KIND>(a, l, s);
 }
 
 template <typename T> hyena_status norm_launch(const NormArgs& a, const NormLaunch& l, int kind, hipStream_t s)
 {
-    if (l.vec) {
-        if (kind == 0) return norm_sized<T, true, 0>(a, l, s);
-        return kind == 1 ? norm_sized<T, true, 1>(a, l, s) : norm_sized<T, true, 2>(a, l, s);
-    }
-    if (kind == 0) return norm_sized<T, false, 0>(a, l, s);
-    return kind == 1 ? norm_sized<T, false, 1>(a, l, s) : norm_sized<T, false, 2>(a, l, s);
+    return by_units(l.units, [&](auto u) {
+        constexpr bool UNITS = decltype(u)::value;
+        if (kind == 0) return norm_sized<T, UNITS, 0>(a, l, s);
+        return kind == 1 ? norm_sized<T, UNITS, 1>(a, l, s) : norm_sized<T, UNITS, 2>(a, l, s);
+    });
 }
 
 }  // namespace hy

@@ -20,7 +20,6 @@ struct LossArgs {
     int64_t total;         // B * N
     int32_t V, d;
     int32_t kd;            // d rounded up to 32: the width of gathered rows
-    int32_t pairs;
     int32_t each;          // tokens of a workgroup of the gather
     int32_t few;           // few tokens: their own kernels
     float scale;

@@ -143,8 +143,7 @@ hyena_status loss_args(const hyena_token_loss* op, void* scratch, bool grad, con
     ins[3] = d_loss ? rows_span(dl, op->B, op->N, 1, 4) : Span{nullptr, 0};
     RowShape made(op->d, e);
     made.add(x);
-    *units = made.made_of() == kMadeOfUnits;
-    a.pairs = made.made_of() >= kMadeOfPairs;
+    *units = made.units();
     hyena_rows* v[3] = {&x, &targets, &dl};
     uint32_t* n[3] = {&a.x_N, &a.targets_N, &a.d_loss_N};
     Rows* to[3] = {&a.x, &a.targets, &a.d_loss};

@@ -52,7 +52,7 @@ __device__ __forceinline__ int workgroup_sum16(int x, int* lds)
 
 // Each workgroup counts the tokens that take part before its own, lists its own
 // after them and gathers their rows of x.
-template <typename T, bool VEC, bool GRAD> __global__ __launch_bounds__(1024) void hyena_loss_gather(LossArgs p)
+template <typename T, bool UNITS, bool GRAD> __global__ __launch_bounds__(1024) void hyena_loss_gather(LossArgs p)
 {
     using E = typename LossType<T>::E;
     constexpr int P = LossType<T>::P;
@@ -111,13 +111,11 @@ template <typename T, bool VEC, bool GRAD> __global__ __launch_bounds__(1024) vo
             if (x != nullptr && c < p.d) {
                 float e[8];
                 if constexpr (kUnit<T> == 8) {
-                    load_unit<T, VEC>(x, c, p.d, p.pairs, e);
+                    load_unit<T, UNITS>(x, c, p.d, e);
                 } else {
                     float lo[kUnit<T>], hi[kUnit<T>];
-                    load_unit<T, VEC>(x, c, p.d, p.pairs, lo);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) hi[i] = 0.0f;
-                    if (c + 4 < p.d) load_unit<T, VEC>(x, c + 4, p.d, p.pairs, hi);
+                    load_unit<T, UNITS>(x, c, p.d, lo);
+                    load_unit<T, UNITS>(x, c + 4, p.d, hi);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = lo[i], e[4 + i] = hi[i];
                 }
@@ -155,7 +153,7 @@ template <typename T, bool VEC, bool GRAD> __global__ __launch_bounds__(1024) vo
 }
 
 // The table in blocks of 32 channels, [kd / 32][V][32], as P planes.
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_loss_pack(LossArgs p)
+template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_loss_pack(LossArgs p)
 {
     using E = typename LossType<T>::E;
     constexpr int P = LossType<T>::P;
@@ -168,9 +166,7 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void hyena_los
 #pragma unroll
             for (int h = 0; h < 8; h += kUnit<T>) {
                 float e[kUnit<T>];
-#pragma unroll
-                for (int i = 0; i < kUnit<T>; ++i) e[i] = 0.0f;
-                if (c + h < p.d) load_unit<T, VEC>(row, c + h, p.d, p.pairs, e);
+                load_unit<T, UNITS>(row, c + h, p.d, e);
 #pragma unroll
                 for (int i = 0; i < kUnit<T>; ++i) x[h + i] = e[i];
             }
@@ -482,7 +478,7 @@ template <typename T, int N, bool GRAD> __global__ __launch_bounds__(256) void h
 // Gradients of at most N tokens: a wave takes the values of its part one after the
 // other, 256 channels of them, adds their share to d_x and makes their rows of d_table.
 // Bound by reading and writing the two tables; G of a value is the same for all lanes.
-template <typename T, int N, bool VEC> __global__ __launch_bounds__(256) void hyena_loss_few_grads(LossArgs p)
+template <typename T, int N, bool UNITS> __global__ __launch_bounds__(256) void hyena_loss_few_grads(LossArgs p)
 {
     __shared__ f32x4 lds[3][N][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -490,7 +486,7 @@ template <typename T, int N, bool VEC> __global__ __launch_bounds__(256) void hy
     const int count = (int)*p.count;
     auto load4 = [&](const T* row) {
         f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (VEC) {
+        if (UNITS) {
             if (c < p.d) y = Mx<T>::widen(*(const typename Mx<T>::vec4*)(row + c));
         } else {
 #pragma unroll
@@ -536,7 +532,7 @@ template <typename T, int N, bool VEC> __global__ __launch_bounds__(256) void hy
             if (p.d_table == nullptr) continue;
             dw *= p.scale;
             T* to = (T*)p.d_table + (int64_t)v * p.d + c;
-            if (VEC) {
+            if (UNITS) {
                 if (c < p.d) *(typename Mx<T>::vec4*)to = Mx<T>::narrow(dw);
             } else {
 #pragma unroll
@@ -721,14 +717,12 @@ template <typename T, bool GRAD> hyena_status loss_begin(const LossArgs& a, bool
     else
         HY_LAUNCH(kernel_label("hyena_loss_gather", type_label<T>(), false, GRAD), (hyena_loss_gather<T, false, GRAD>), grid, dim3(1024), 0, s, a);
     if ((st = launched()) != HYENA_OK || !pack) return st;
-    LossArgs b = a;
-    b.pairs = a.d % 2 == 0;
     const int64_t need = ((int64_t)a.V + 3) / 4;
     const dim3 pgrid((unsigned)(need < 4096 ? need : 4096));
     if (a.d % kUnit<T> == 0)
-        HY_LAUNCH(kernel_label("hyena_loss_pack", type_label<T>(), true), (hyena_loss_pack<T, true>), pgrid, dim3(256), 0, s, b);
+        HY_LAUNCH(kernel_label("hyena_loss_pack", type_label<T>(), true), (hyena_loss_pack<T, true>), pgrid, dim3(256), 0, s, a);
     else
-        HY_LAUNCH(kernel_label("hyena_loss_pack", type_label<T>(), false), (hyena_loss_pack<T, false>), pgrid, dim3(256), 0, s, b);
+        HY_LAUNCH(kernel_label("hyena_loss_pack", type_label<T>(), false), (hyena_loss_pack<T, false>), pgrid, dim3(256), 0, s, a);
     return launched();
 }
 
