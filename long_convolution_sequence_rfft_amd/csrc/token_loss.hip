@@ -10,6 +10,8 @@ constexpr const char* kWho = "token loss";
 // G of a piece of the vocabulary takes about this much, or a tile of values if that
 // is more.
 constexpr int64_t kGradBytes = (int64_t)1024 << 20;
+// The sums of a piece's tiles, forward (a launch of it then stays below 2^32 threads, too).
+constexpr int64_t kPartBytes = (int64_t)256 << 20;
 // Workgroups that d_x's sums are cut for, and into which part of their time.
 constexpr int64_t kSplitGroups = 512, kSplitParts = 4;
 
@@ -43,6 +45,15 @@ bool needs_pack(const hyena_token_loss* op, bool grad)
     if (op->io_dtype == HYENA_F32) return !is_few(op, grad);
     // 16-byte loads need rows that are made of them (float32's any 4-byte address)
     return op->d % 8 != 0 || (!is_few(op, grad) && op->B * op->N > kPackTokens);
+}
+
+// Tiles of values of a piece, if `fit` of all are to be one: pieces of about one size, of as
+// many tiles for each XCD.
+int64_t even_pieces(int64_t all, int64_t fit)
+{
+    if (fit >= all) return all;
+    const int64_t pieces = fit < 1 ? all : (all + fit - 1) / fit, tiles = (all + pieces - 1) / pieces;
+    return tiles <= 8 ? tiles : (tiles + 7) / 8 * 8;
 }
 
 // Sizes, and with a scratch the addresses in it; returns the bytes.
@@ -86,8 +97,12 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
         a.values = (const char*)op->table;
     }
     a.hit = (float*)take(tokens * 4);
+    const int64_t whole = loss_tiles(a.V);
     if (!grad) {
-        a.part = (float2*)take((size_t)(a.few ? few_groups(a.V) : loss_tiles(a.V)) * tokens * 8);
+        const int64_t fit = kPartBytes / (a.tokens * 8), tiles = a.few ? few_groups(a.V) : even_pieces(whole, fit);
+        a.chunk = a.few ? a.V : (int32_t)(tiles * kLossValues);
+        a.part = (float2*)take((size_t)tiles * tokens * 8);
+        a.running = (float2*)take(tiles < whole && !a.few ? tokens * 8 : 0);
         return at;
     }
     a.place = (int32_t*)take((size_t)a.total * 4);
@@ -101,11 +116,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
         a.acc = (float*)take((size_t)a.splits * tokens * (size_t)a.acc_row * 4);
         return at;
     }
-    const int64_t whole = (a.V + kLossValues - 1) / kLossValues, fit = kGradBytes / (a.tokens * 2 * planes * kLossValues);
-    int64_t tiles = fit < 1 ? 1 : fit < whole ? fit : whole;
-    const int64_t pieces = (whole + tiles - 1) / tiles;
-    tiles = (whole + pieces - 1) / pieces;  // pieces of one size, and as many tiles for each XCD
-    if (tiles > 8) tiles = (tiles + 7) / 8 * 8;
+    const int64_t tiles = even_pieces(whole, kGradBytes / (a.tokens * 2 * planes * kLossValues));
     a.chunk = (int32_t)(tiles * kLossValues);
     a.g_plane = a.tokens * a.chunk * 2;
     a.g = take((size_t)(planes * a.g_plane));

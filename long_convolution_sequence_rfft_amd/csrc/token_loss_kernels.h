@@ -559,7 +559,9 @@ template <typename T, int N, bool UNITS> __global__ __launch_bounds__(256) void 
     }
 }
 
-template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_join(LossArgs p, int tiles)
+// tiles: of this piece of the vocabulary; what came before it is in p.running, unless it is
+// the first, and what is behind the last one is the result.
+template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_join(LossArgs p, int tiles, bool last)
 {
     __shared__ float2 lds[16][16];
     const int64_t count = *p.count, a = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
@@ -575,6 +577,11 @@ template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_join(Lo
     __syncthreads();
     if (threadIdx.x < 16 && a < count) {
         for (int i = 1; i < 16; ++i) join(m, s, lds[i][threadIdx.x].x, lds[i][threadIdx.x].y);
+        if (p.first != 0) join(m, s, p.running[a].x, p.running[a].y);
+        if (!last) {
+            p.running[a] = make_float2(m, s);
+            return;
+        }
         const float log2s = __builtin_amdgcn_logf(s);
         const int32_t t = p.index[a];
         p.lse[t] = (m + log2s) * kLn2;
@@ -764,10 +771,16 @@ template <typename T> hyena_status loss_forward(const LossArgs& a, bool pack, bo
 {
     hyena_status st = loss_begin<T, false>(a, pack, units, s);
     if (st != HYENA_OK) return st;
-    const int tiles = a.few ? few_groups(a.V) : loss_tiles(a.V);
-    if ((st = loss_logits<T, false>(a, tiles, s)) != HYENA_OK) return st;
-    HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>()), hyena_loss_join<T>, dim3((unsigned)((a.total + 15) / 16)), dim3(1024), 0, s, a, tiles);
-    return launched();
+    LossArgs b = a;
+    for (int64_t first = 0; first < a.V; first += a.chunk) {
+        b.first = (int32_t)first;
+        const bool last = first + a.chunk >= a.V;
+        const int tiles = a.few ? few_groups(a.V) : loss_tiles(last ? a.V - first : a.chunk);
+        if ((st = loss_logits<T, false>(b, tiles, s)) != HYENA_OK) return st;
+        HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>()), hyena_loss_join<T>, dim3((unsigned)((a.total + 15) / 16)), dim3(1024), 0, s, b, tiles, last);
+        if ((st = launched()) != HYENA_OK) return st;
+    }
+    return HYENA_OK;
 }
 
 template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, bool units, hipStream_t s)

@@ -337,3 +337,22 @@ def test_an_infinity_in_one_token_stays_there():
         dx, _ = plan.backward(d_loss, x, table, target, lse, want_table=False)
         dx2, _ = plan.backward(d_loss, x2, table, target, lse2, want_table=False)
         assert torch.equal(dx[0, keep], dx2[0, keep])
+
+
+def test_many_tokens_in_pieces_forward():
+    # the sums of 600000 tokens' tiles do not fit one piece: some of the tokens against float64
+    import torch
+    T, V, d = 600000, 20011, 16
+    say("[gpu] token_loss forward in pieces")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((1, T, d), generator=gen, device="cuda").bfloat16()
+    table = torch.randn((V, d), generator=gen, device="cuda").bfloat16()
+    target = torch.randint(-1, V, (1, T), generator=gen, device="cuda", dtype=torch.int32)
+    loss, lse = hyena.TokenLoss(1, T, V, d, io_dtype=hyena.HYENA_BF16).forward(x, table, target)
+    for rows in (slice(0, 1500), slice(T // 2, T // 2 + 1500), slice(T - 1500, T)):
+        l = x[0, rows].double() @ table.double().t().contiguous()
+        t = target[0, rows].long()
+        ref = torch.where(t >= 0, torch.logsumexp(l, -1), 0)
+        hit = l.gather(1, t.clamp(min=0)[:, None])[:, 0]
+        assert float((lse[0, rows] - ref).abs().max()) < 1e-4
+        assert float((loss[0, rows] - torch.where(t >= 0, ref - hit, 0)).abs().max()) < 2e-4
