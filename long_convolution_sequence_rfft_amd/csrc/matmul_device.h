@@ -21,6 +21,10 @@
 // Loads go to LDS directly, a step ahead of the products (of a step's 512 cycles of
 // matrix instructions per wave little else has to be issued; staged in registers the
 // same product ran at 854).  No bank conflicts.
+//
+// With several planes a step has all planes of both operands, so that each is loaded once for
+// the products it takes part in, and the products of less than the first planes are summed
+// apart and added last.
 // A lane's results: row 4 (lane / 16) + r of a 16 x 16 tile, column lane % 16.
 #pragma once
 
@@ -54,10 +58,11 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, __amdgpu
 }
 template <int N> __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
-// A barrier of what wait_loads has waited for: no other memory access is waited for.
+// A barrier of what wait_loads has waited for and of this wave's reads of LDS, which what is
+// loaded behind it may overwrite: no other memory access is waited for.
 __device__ __forceinline__ void barrier_only()
 {
-    asm volatile("" ::: "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -139,7 +144,7 @@ template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, 
     static constexpr int kThreads = WM * WN * 64;
     using A = Stage<TM, kThreads, AF>;
     using B = Stage<TN, kThreads, BF>;
-    static constexpr int kStep = A::kBytes + B::kBytes, kLds = STAGES * kStep;
+    static constexpr int kStep = NP * (A::kBytes + B::kBytes), kLds = STAGES * kStep;
     static constexpr int MI = TM / WM / 16, NI = TN / WN / 16;
     using frag = typename Mx<E>::frag;
 
@@ -151,6 +156,20 @@ template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, 
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NI; ++j) c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // One step's products, of one plane.
+    __device__ __forceinline__ void products(const char* at, int m0, int n0)
+    {
+        frag fa[MI], fb[NI];
+#pragma unroll
+        for (int j = 0; j < NI; ++j) fb[j] = B::template fragment<frag>(at + NP * A::kBytes, n0 + 16 * j);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[i] = A::template fragment<frag>(at, m0 + 16 * i);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) c[i][j] = Mx<E>::mma(fa[i], fb[j], c[i][j]);
     }
 
     // aplane, bplane: bytes between planes.  steps: of 32 values of k, at least 1.
@@ -166,44 +185,67 @@ template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, 
         a.init(oa);
         b.init(ob);
         const int64_t astep = A::step(oa), bstep = B::step(ob);
-        const int total = steps * Planes<NP>::kPairs;
         const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
-        int pair = 0, left = steps;
-        const char *pa = oa.at + Planes<NP>::a(0) * aplane, *ea = oa.end + Planes<NP>::a(0) * aplane;
-        const char *pb = ob.at + Planes<NP>::b(0) * bplane, *eb = ob.end + Planes<NP>::b(0) * bplane;
+        const char *pa = oa.at, *pb = ob.at;
         auto issue = [&](int stage) {
-            a.load(base + stage * kStep, pa, ea);
-            b.load(base + stage * kStep + A::kBytes, pb, eb);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                a.load(base + stage * kStep + n * A::kBytes, pa + n * aplane, oa.end + n * aplane);
+                b.load(base + stage * kStep + NP * A::kBytes + n * B::kBytes, pb + n * bplane, ob.end + n * bplane);
+            }
             pa += astep;
             pb += bstep;
-            if (NP > 1 && --left == 0 && ++pair < Planes<NP>::kPairs) {
-                left = steps;
-                pa = oa.at + Planes<NP>::a(pair) * aplane, ea = oa.end + Planes<NP>::a(pair) * aplane;
-                pb = ob.at + Planes<NP>::b(pair) * bplane, eb = ob.end + Planes<NP>::b(pair) * bplane;
-            }
         };
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i)
-            if (i < total) issue(i);
-        int now = 0, into = STAGES - 1;
-        for (int s = 0; s < total; ++s) {
-            // this step's loads are done: those of later steps may be under way
-            if (STAGES > 2 && s + STAGES - 1 <= total) wait_loads<(STAGES - 2) * (A::kLoads + B::kLoads)>();
-            else wait_loads<0>();
-            barrier_only();
-            if (s + STAGES - 1 < total) issue(into);
-            const char* at = lds + now * kStep;
-            frag fa[MI], fb[NI];
-#pragma unroll
-            for (int j = 0; j < NI; ++j) fb[j] = B::template fragment<frag>(at + A::kBytes, n0 + 16 * j);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) fa[i] = A::template fragment<frag>(at, m0 + 16 * i);
+            if (i < steps) issue(i);
+        // (with several planes the smaller products have sums of their own)
+        f32x4 low[NP == 1 ? 1 : MI][NP == 1 ? 1 : NI];
+        if constexpr (NP > 1) {
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int j = 0; j < NI; ++j) c[i][j] = Mx<E>::mma(fa[i], fb[j], c[i][j]);
+                for (int j = 0; j < NI; ++j) low[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        int now = 0, into = STAGES - 1;
+        for (int s = 0; s < steps; ++s) {
+            // this step's loads are done: those of later steps may be under way
+            if (STAGES > 2 && s + STAGES - 1 <= steps) wait_loads<(STAGES - 2) * NP * (A::kLoads + B::kLoads)>();
+            else wait_loads<0>();
+            barrier_only();
+            if (s + STAGES - 1 < steps) issue(into);
+            const char* at = lds + now * kStep;
+            if constexpr (NP == 1) {
+                products(at, m0, n0);
+            } else {
+                frag fb[NP][NI];
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+#pragma unroll
+                    for (int j = 0; j < NI; ++j)
+                        fb[n][j] = B::template fragment<frag>(at + NP * A::kBytes + n * B::kBytes, n0 + 16 * j);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    frag fa[NP];
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) fa[n] = A::template fragment<frag>(at + n * A::kBytes, m0 + 16 * i);
+#pragma unroll
+                    for (int q = 0; q < Planes<NP>::kPairs; ++q)
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) {
+                            f32x4& to = q + 1 == Planes<NP>::kPairs ? c[i][j] : low[i][j];
+                            to = Mx<E>::mma(fa[Planes<NP>::a(q)], fb[Planes<NP>::b(q)][j], to);
+                        }
+                }
+            }
             now = now + 1 == STAGES ? 0 : now + 1;
             into = into + 1 == STAGES ? 0 : into + 1;
+        }
+        if constexpr (NP > 1) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) c[i][j] += low[i][j];
         }
         barrier_only();
     }
