@@ -98,6 +98,21 @@ template <int W, int THREADS, Form F> struct Stage {
             }
         }
     }
+    // k in the rows: the row of this thread's loads in a step, and loads of any row there (at
+    // kNoRow zeros).
+    static constexpr uint32_t kNoRow = 0x7ffffff0;
+    static __device__ __forceinline__ int row_of_step() { return (int)(threadIdx.x >> 2) & 31; }
+    __device__ __forceinline__ void init_rows(const Operand& o, uint32_t row_bytes)
+    {
+        static_assert(!KC && THREADS % 128 == 0, "");
+        const int s = threadIdx.x & 3, at = (((s >> 1) ^ key(row_of_step())) << 1 | (s & 1)) * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            off[i] = row_bytes == kNoRow ? kNoRow
+                                         : (uint32_t)(((int)threadIdx.x + i * THREADS) >> 7) * (uint32_t)o.block + row_bytes + (uint32_t)at;
+    }
+    // Where value (k, m) of a step lies.
+    static __device__ __forceinline__ int place(int k, int m) { return (m >> 5) * 2048 + k * 64 + ((((m >> 4) & 1) ^ key(k)) << 5) + (m & 15) * 2; }
     __device__ __forceinline__ void load(uint32_t lds, const char* at, const char* end) const
     {
         const __amdgpu_buffer_rsrc_t r = operand_rsrc(at, end);

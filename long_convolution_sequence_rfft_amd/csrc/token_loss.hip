@@ -14,6 +14,8 @@ constexpr int64_t kGradBytes = (int64_t)1024 << 20;
 constexpr int64_t kPartBytes = (int64_t)256 << 20;
 // Workgroups that d_x's sums are cut for, and into which part of their time.
 constexpr int64_t kSplitGroups = 512, kSplitParts = 4;
+// Steps of 32 tokens that a part of d_table's sums has at least.
+constexpr int64_t kTableSteps = 4;
 
 hyena_status refuse(const char* what) { return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(kWho) + ": " + what); }
 
@@ -124,13 +126,17 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     // of what all of the piece's work takes on kSplitGroups of them
     const int64_t channel_tiles = (a.d + kGradChannels - 1) / kGradChannels, dx_tiles = a.tokens / kGradRows * channel_tiles;
     const int64_t dx_steps = a.chunk / 32, table_steps = a.tokens / 32, table_tiles = a.chunk / kGradRows * channel_tiles;
-    const int64_t share = (dx_tiles * dx_steps + table_tiles * table_steps) / kSplitGroups;
-    int64_t splits = share < 1 ? 64 : (kSplitParts * dx_steps + share - 1) / share;
+    const int64_t all = (dx_tiles * dx_steps + table_tiles * table_steps) / kSplitGroups, share = all < 1 ? 1 : all;
+    int64_t splits = (kSplitParts * dx_steps + share - 1) / share;
     const int64_t most = a.chunk / 512 < 1 ? 1 : a.chunk / 512;  // a part has 512 values at least
     const int64_t cap = a.tokens <= 1024 ? 64 : 16;
     splits = splits < 1 ? 1 : splits > most ? most : splits > cap ? cap : splits;
     a.splits = (int32_t)splits;
     a.acc = (float*)take((size_t)splits * tokens * (size_t)a.acc_row * 4);
+    // d_table's over the tokens, where one of them would take longer than that
+    const int64_t table_splits = (table_steps + share - 1) / share, table_most = table_steps / kTableSteps;
+    a.table_splits = (int32_t)(table_splits <= 1 || table_most <= 1 ? 1 : table_splits < table_most ? table_splits : table_most);
+    a.table_acc = (float*)take(a.table_splits == 1 ? 0 : (size_t)a.table_splits * (size_t)a.chunk * (size_t)a.acc_row * 4);
     return at;
 }
 

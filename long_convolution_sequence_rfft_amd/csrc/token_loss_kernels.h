@@ -8,6 +8,7 @@
 //   hyena_loss_few      the same for few tokens, hyena_loss_few_grads their gradients
 //   hyena_loss_join     the tiles' sums joined: loss, lse
 //   hyena_loss_products d_table of a piece of the vocabulary, and its share of d_x
+//   hyena_loss_table    d_table of a piece from its sums, where the tokens are cut
 //   hyena_loss_finish   d_x from its sums
 // Bound by the matrix instructions: 2 tokens V d operations forward, 6 backward.
 #pragma once
@@ -195,6 +196,10 @@ inline int64_t dealt(int64_t inner, int64_t outer) { return inner * ((outer + 7)
 // Tiles of values of one XCD whose part of the table stays in its L2 while the tokens'
 // tiles go by.
 constexpr int kLossGroup = 6;
+// Fewer tiles of values than this, and fewer than tiles of tokens: the tokens' tiles are dealt
+// out to the XCDs.
+constexpr int kDealValues = 64;
+inline __host__ __device__ bool deal_tokens(int value_tiles, int token_tiles) { return value_tiles < kDealValues && value_tiles < token_tiles; }
 
 // Two sums of exponentials, each with what was taken from its exponents.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2)
@@ -214,14 +219,20 @@ __global__ __launch_bounds__(LossType<T>::kThreads, LossType<T>::P == 1 ? 3 : 2)
     using Tile = MatTile<E, kLossValues, kLossTokens, WM, WN, kInColumnsPaired, kInColumns, P, 2>;
     __shared__ __attribute__((aligned(16))) char lds[Tile::kLds];
     const int64_t count = *p.count;
-    // XCD x has the tiles of values x, x + 8, ..., kLossGroup of them at a time
     const int token_tiles = (int)(p.tokens / kLossTokens);
-    const int64_t local = blockIdx.x >> 3, each = (int64_t)kLossGroup * token_tiles;
-    const int mine = (value_tiles + 7) / 8, group = (int)(local / each), in_group = mine - group * kLossGroup;
-    const int width = in_group < kLossGroup ? in_group : kLossGroup;
-    const int64_t rest = local - group * each;
-    const int value_tile = (group * kLossGroup + (int)(rest % width)) * 8 + (int)(blockIdx.x & 7);
-    const int64_t t0 = rest / width * kLossTokens;
+    int value_tile, token_tile;
+    if (deal_tokens(value_tiles, token_tiles)) {
+        deal(blockIdx.x, value_tiles, token_tiles, value_tile, token_tile);
+    } else {
+        // XCD x has the tiles of values x, x + 8, ..., kLossGroup of them at a time
+        const int64_t local = blockIdx.x >> 3, each = (int64_t)kLossGroup * token_tiles;
+        const int mine = (value_tiles + 7) / 8, group = (int)(local / each), in_group = mine - group * kLossGroup;
+        const int width = in_group < kLossGroup ? in_group : kLossGroup;
+        const int64_t rest = local - group * each;
+        value_tile = (group * kLossGroup + (int)(rest % width)) * 8 + (int)(blockIdx.x & 7);
+        token_tile = (int)(rest / width);
+    }
+    const int64_t t0 = (int64_t)token_tile * kLossTokens;
     if (t0 >= count || value_tile >= value_tiles) return;
     const int32_t v0 = p.first + value_tile * kLossValues;
     Tile tile;
@@ -592,9 +603,76 @@ template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_join(Lo
     }
 }
 
+// G at the target is rounded like the others, but one row of d_table (and d_x) bears its rest:
+// in the first steps of a training all tokens' targets have nearly one G, and one rest.  So
+// the rests of the tokens t0 to t1 whose targets are among a tile's values, from first on, are
+// one more product behind the tile's others: their rows of x by a matrix with one value in
+// a row, 32 of them in a step.  (Gradient of 16 bits, 108 tokens and 50257 values: the
+// error of d_table is that of its rounding so, 1.6 times that without.)
+template <typename E, typename Tile>
+__device__ __forceinline__ void add_rests(Tile& tile, char* lds, const LossArgs& p, const Operand& x, int32_t first, int64_t t0, int64_t t1)
+{
+    constexpr int kWaves = Tile::kThreads / 64, kKept = 1024, kAhead = 8;  // tokens that a wave lists, loads under way
+    using B = typename Tile::B;
+    static_assert(64 + kWaves * kKept * 4 <= Tile::kStep, "");
+    int* counts = (int*)(lds + Tile::kStep);
+    int* list = counts + 16;
+    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t each = (t1 - t0 + Tile::kThreads - 1) / Tile::kThreads * 64;
+    const int64_t end = t0 + each * (wave + 1) < t1 ? t0 + each * (wave + 1) : t1;
+    int64_t at = t0 + each * wave;
+    while (true) {
+        int n = 0;
+        for (; at < end && n <= kKept - 64 * kAhead; at += 64 * kAhead) {
+            int v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) v[k] = at + 64 * k + lane < end ? p.target[at + 64 * k + lane] - first : -1;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const bool own = (uint32_t)v[k] < (uint32_t)kGradRows;
+                const uint64_t all = __ballot(own);
+                if (own) list[wave * kKept + n + __popcll(all & (((uint64_t)1 << lane) - 1))] = (int)at + 64 * k + lane;
+                n += __popcll(all);
+            }
+        }
+        if (lane == 0) counts[wave] = n | (at < end) << 30;
+        __syncthreads();
+        int total = 0, more = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            more |= counts[w] >> 30;
+            total += counts[w] & 0x3fffffff;
+        }
+        for (int s = 0; s < total; s += 32) {
+            const int k = Tile::A::row_of_step();
+            int token = -1;
+            if (s + k < total) {
+                int i = s + k, w = 0;
+                while (i >= (counts[w] & 0x3fffffff)) i -= counts[w++] & 0x3fffffff;
+                token = list[w * kKept + i];
+            }
+            typename Tile::A a;
+            a.init_rows(x, token < 0 ? Tile::A::kNoRow : (uint32_t)token * 64);
+            a.load(base, x.at, x.end);
+            for (int i = threadIdx.x; i < B::kBytes / 16; i += Tile::kThreads) ((uint4*)(lds + Tile::A::kBytes))[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+            if (token >= 0 && threadIdx.x < 128 && (threadIdx.x & 3) == 0)
+                store_one<E>((E*)(lds + Tile::A::kBytes + B::place(k, p.target[token] - first)), p.hit[token]);
+            wait_loads<0>();
+            __syncthreads();
+            tile.products(lds, wave / 2 * (kGradChannels / 2), wave % 2 * (kGradRows / 2));
+            __syncthreads();
+        }
+        if (!more) return;
+        __syncthreads();
+    }
+}
+
 // The first table_groups workgroups: d_table of kGradRows values of this piece and
-// kGradChannels channels.  The others, shorter ones: a share of d_x of kGradRows tokens,
-// the sum over one of p.splits parts of the piece's values.
+// kGradChannels channels, the sum over one of p.table_splits parts of the tokens.  The
+// others, shorter ones: a share of d_x of kGradRows tokens, the sum over one of p.splits
+// parts of the piece's values.
 template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) void hyena_loss_products(LossArgs p, int table_groups, int channel_tiles)
 {
     using E = typename LossType<T>::E;
@@ -608,14 +686,22 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
     const int32_t values = p.V - p.first < p.chunk ? p.V - p.first : p.chunk;  // of this piece
     int channel_tile, o;
     if ((int)blockIdx.x < table_groups) {
-        if (!deal(blockIdx.x, channel_tiles, (values + kGradRows - 1) / kGradRows, channel_tile, o)) return;
-        const int c0 = channel_tile * kGradChannels;
-        const int32_t v0 = o * kGradRows;
+        if (!deal(blockIdx.x, channel_tiles, (values + kGradRows - 1) / kGradRows * p.table_splits, channel_tile, o)) return;
+        const int c0 = channel_tile * kGradChannels, split = o % p.table_splits;
+        const int32_t v0 = o / p.table_splits * kGradRows;
+        const int steps = (int)((count + 31) / 32), per = (steps + p.table_splits - 1) / p.table_splits;
+        const int k0 = split * per, k1 = k0 + per < steps ? k0 + per : steps;
         Table tile;
-        const Operand x{p.rows + (int64_t)(c0 >> 5) * p.tokens * 64, p.rows + p.rows_plane, 64, p.tokens * 64};
-        const Operand y{p.g + (int64_t)(v0 >> 5) * p.tokens * 64, p.g + p.g_plane, 64, p.tokens * 64};
-        if (count > 0) tile.run(lds, x, p.rows_plane, y, p.g_plane, (int)((count + 31) / 32));
-        else tile.clear();
+        if (k0 < k1) {
+            Operand x{p.rows + (int64_t)(c0 >> 5) * p.tokens * 64, p.rows + p.rows_plane, 64, p.tokens * 64};
+            const Operand y{p.g + (int64_t)(v0 >> 5) * p.tokens * 64 + (int64_t)k0 * 2048, p.g + p.g_plane, 64, p.tokens * 64};
+            x.at += (int64_t)k0 * 2048;
+            tile.run(lds, x, p.rows_plane, y, p.g_plane, k1 - k0);
+            x.at -= (int64_t)k0 * 2048;
+            if constexpr (P == 1) add_rests<E>(tile, lds, p, x, p.first + v0, (int64_t)k0 * 32, (int64_t)k1 * 32 < count ? (int64_t)k1 * 32 : count);
+        } else {
+            tile.clear();
+        }
         const float down = p.norm[1];
 #pragma unroll
         for (int j = 0; j < Table::NI; ++j) {
@@ -625,6 +711,10 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
 #pragma unroll
             for (int i = 0; i < Table::MI; ++i) {
                 const int c = c0 + wm * (kGradChannels / WM) + 16 * i + 4 * g;
+                if (p.table_splits > 1) {
+                    if (c < p.acc_row) *(f32x4*)(p.table_acc + ((int64_t)split * p.chunk + v) * p.acc_row + c) = tile.c[i][j];
+                    continue;
+                }
                 const f32x4 r = tile.c[i][j] * down;
                 if (p.d % 4 == 0) {
                     if (c < p.d) *(typename Mx<T>::vec4*)(to + c) = Mx<T>::narrow(r);
@@ -669,6 +759,34 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
     }
 }
 
+// A row of d_table of a piece from its sums, 256 channels of it: each of 16 waves some of them.
+template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_table(LossArgs p)
+{
+    __shared__ f32x4 lds[16][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int c = (int)blockIdx.y * 256 + lane * 4;
+    const float* from = p.table_acc + (int64_t)blockIdx.x * p.acc_row + c;
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < p.d) {
+#pragma unroll 4
+        for (int s = wave; s < p.table_splits; s += 16) x += *(const f32x4*)(from + (int64_t)s * p.chunk * p.acc_row);
+    }
+    lds[wave][lane] = x;
+    __syncthreads();
+    if (wave != 0 || c >= p.d) return;
+#pragma unroll
+    for (int w = 1; w < 16; ++w) x += lds[w][lane];
+    x *= p.norm[1];
+    T* to = (T*)p.d_table + (int64_t)(p.first + blockIdx.x) * p.d + c;
+    if (p.d % 4 == 0) {
+        *(typename Mx<T>::vec4*)to = Mx<T>::narrow(x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < p.d) store_one<T>(to + e, x[e]);
+    }
+}
+
 // d_x of a token from its sums, by ROWS waves for each token (few tokens have many sums).
 template <typename T, int ROWS> __global__ __launch_bounds__(ROWS == 1 ? 256 : 1024) void hyena_loss_finish(LossArgs p)
 {
@@ -699,7 +817,7 @@ template <typename T, int ROWS> __global__ __launch_bounds__(ROWS == 1 ? 256 : 1
             }
             if (c >= p.d) continue;
             if (LossType<T>::P == 1 && a >= 0 && !p.few) {
-                // G at the target is rounded like the others; its rest, which one row of the table bears
+                // the rest of G at the target
                 const float off = p.hit[a];
                 const T* w = (const T*)p.table + (int64_t)p.target[a] * p.d + c;
 #pragma unroll
@@ -746,8 +864,9 @@ template <typename T, int N, bool GRAD> hyena_status loss_few(const LossArgs& a,
 template <typename T, bool GRAD> hyena_status loss_logits(const LossArgs& a, int tiles, hipStream_t s)
 {
     if (!a.few) {
+        const int token_tiles = (int)(a.tokens / kLossTokens);
         HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), GRAD), (hyena_loss_logits<T, GRAD>),
-                  dim3((unsigned)dealt(a.tokens / kLossTokens, tiles)), dim3(LossType<T>::kThreads), 0, s, a, tiles);
+                  dim3((unsigned)(deal_tokens(tiles, token_tiles) ? dealt(tiles, token_tiles) : dealt(token_tiles, tiles))), dim3(LossType<T>::kThreads), 0, s, a, tiles);
         return launched();
     }
     if constexpr (!GRAD) {
@@ -800,10 +919,14 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
             if ((st = a.total <= 4 ? loss_few_grads<T, 4>(a, s) : loss_few_grads<T, 16>(a, s)) != HYENA_OK) return st;
             break;
         }
-        const int64_t table_tiles = a.d_table ? dealt(channel_tiles, (values + kGradRows - 1) / kGradRows) : 0;
+        const int64_t table_tiles = a.d_table ? dealt(channel_tiles, (int64_t)((values + kGradRows - 1) / kGradRows) * a.table_splits) : 0;
         const int64_t dx_tiles = a.d_x ? dealt(channel_tiles, a.splits * (a.tokens / kGradRows)) : 0;
         HY_LAUNCH(kernel_label("hyena_loss_products", type_label<T>()), hyena_loss_products<T>, dim3((unsigned)(table_tiles + dx_tiles)),
                   dim3(LossType<T>::kThreads), 0, s, b, (int)table_tiles, channel_tiles);
+        if ((st = launched()) != HYENA_OK) return st;
+        if (a.d_table == nullptr || a.table_splits == 1) continue;
+        HY_LAUNCH(kernel_label("hyena_loss_table", type_label<T>()), hyena_loss_table<T>, dim3((unsigned)values, (unsigned)((a.d + 255) / 256)),
+                  dim3(1024), 0, s, b);
         if ((st = launched()) != HYENA_OK) return st;
     }
     if (a.d_x == nullptr) return HYENA_OK;
