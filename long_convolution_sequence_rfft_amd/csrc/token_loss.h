@@ -8,9 +8,15 @@ namespace hy {
 // Tokens and values of the vocabulary of a tile of logits; channels and rows of a
 // tile of the gradients.
 constexpr int kLossTokens = 128, kLossValues = 256;
+// The same where whole tiles are few.
+constexpr int kSmallTile = 64;
 // Workgroups of the logits of few tokens, which take tiles of 16 values in turn.
 constexpr int kFewLogits = 512;
-inline int loss_tiles(int64_t V) { return (int)((V + kLossValues - 1) / kLossValues); }
+inline int loss_tiles(int64_t V, bool small = false)
+{
+    const int tile = small ? kSmallTile : kLossValues;
+    return (int)((V + tile - 1) / tile);
+}
 inline int few_groups(int64_t V) { return (V + 15) / 16 < kFewLogits ? (int)((V + 15) / 16) : kFewLogits; }
 constexpr int kGradRows = 128, kGradChannels = 256;
 
@@ -22,6 +28,7 @@ struct LossArgs {
     int32_t kd;            // d rounded up to 32: the width of gathered rows
     int32_t each;          // tokens of a workgroup of the gather
     int32_t few;           // few tokens: their own kernels
+    int32_t small;         // tiles of logits of kSmallTile
     float scale;
     const void* table;     // as given
     const float* lse_in;

@@ -12,6 +12,10 @@ constexpr const char* kWho = "token loss";
 constexpr int64_t kGradBytes = (int64_t)1024 << 20;
 // The sums of a piece's tiles, forward (a launch of it then stays below 2^32 threads, too).
 constexpr int64_t kPartBytes = (int64_t)256 << 20;
+// Logits of no more tiles than this are made in small ones (width 1024, of 2, 32, 128 and 256 tiles:
+// in 16 bits 19, 20, 29 and 44 us so, 31, 32, 34 and 35 us in large ones; in float32 32, 31, 64
+// and 115 us so, 72, 73, 76 and 82 us in large ones; width 256 in 16 bits: 14, 14, 17, 23 and 18, 20, 19, 20).
+constexpr int64_t kSmallTiles = 128;
 // Workgroups that d_x's sums are cut for, and into which part of their time.
 constexpr int64_t kSplitGroups = 512, kSplitParts = 4;
 // Steps of 32 tokens that a part of d_table's sums has at least.
@@ -67,6 +71,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     a.d = (int32_t)op->d;
     a.kd = (int32_t)((op->d + 31) / 32 * 32);
     a.few = is_few(op, grad);
+    a.small = !a.few && (int64_t)loss_tiles(a.V) * ((a.total + kLossTokens - 1) / kLossTokens) <= kSmallTiles;
     a.tokens = a.few && grad ? 32 : (a.total + kLossTokens - 1) / kLossTokens * kLossTokens;
     a.scale = op->scale;
     a.table = op->table;
@@ -100,6 +105,11 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     }
     a.hit = (float*)take(tokens * 4);
     const int64_t whole = loss_tiles(a.V);
+    if (!grad && a.small) {
+        a.chunk = a.V;
+        a.part = (float2*)take((size_t)loss_tiles(a.V, true) * tokens * 8);
+        return at;
+    }
     if (!grad) {
         const int64_t fit = kPartBytes / (a.tokens * 8), tiles = a.few ? few_groups(a.V) : even_pieces(whole, fit);
         a.chunk = a.few ? a.V : (int32_t)(tiles * kLossValues);

@@ -9,7 +9,7 @@
 //   hyena_loss_join     the tiles' sums joined: loss, lse
 //   hyena_loss_products d_table of a piece of the vocabulary, and its share of d_x
 //   hyena_loss_table    d_table of a piece from its sums, where the tokens are cut
-//   hyena_loss_finish   d_x from its sums
+//   hyena_loss_finish   d_x from its sums (hyena_loss_finish_few where they are many)
 // Bound by the matrix instructions: 2 tokens V d operations forward, 6 backward.
 #pragma once
 
@@ -66,7 +66,7 @@ template <typename T, bool UNITS, bool GRAD> __global__ __launch_bounds__(1024) 
     const int64_t first = (int64_t)blockIdx.x * p.each, last = first + p.each < p.total ? first + p.each : p.total;
     auto takes_part = [&](int64_t t) { return (uint32_t)*row_at<int32_t>(p.targets, t, p.targets_N) < (uint32_t)p.V; };
     int n = 0;
-#pragma unroll 4
+#pragma unroll 16
     for (int64_t t = threadIdx.x; t < first; t += 1024) n += takes_part(t);
     int64_t before = workgroup_sum16(n, lds);
     const int64_t begin = before;
@@ -102,33 +102,47 @@ template <typename T, bool UNITS, bool GRAD> __global__ __launch_bounds__(1024) 
         before += total;
     }
     __syncthreads();  // index is read back below
-    // rows, a wave each, and after the last one zeros up to a whole step of 32
-    int64_t end = before;
+    // rows: teams of lanes with a unit of 8 channels each, kRows rows of a team under way
+    constexpr int kRows = 4, kUnits = 8 / kUnit<T>;
+    int lanes = 64;
+    while (lanes * 4 >= p.kd) lanes /= 2;
+    const int teams = 1024 / lanes, team = threadIdx.x / lanes, tl = threadIdx.x % lanes;
+    for (int64_t a0 = begin + team; a0 < before; a0 += kRows * teams) {
+        const T* x[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t a = a0 + k * teams < before ? a0 + k * teams : before - 1;
+            x[k] = row_at<T>(p.x, p.index[a], p.x_N);
+        }
+        for (int c = tl * 8; c < p.kd; c += lanes * 8) {
+            Unit<T, UNITS> u[kRows][kUnits];
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+#pragma unroll
+                for (int h = 0; h < kUnits; ++h) u[k][h].load(x[k], c + h * kUnit<T>, p.d);
+            char* to = p.rows + (c >> 5) * p.tokens * 64 + (c & 31) * 2;
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                if (a0 + k * teams >= before) break;
+                f32x8 v;
+#pragma unroll
+                for (int h = 0; h < kUnits; ++h) {
+                    float e[kUnit<T>];
+                    u[k][h].widen(e);
+#pragma unroll
+                    for (int i = 0; i < kUnit<T>; ++i) v[h * kUnit<T> + i] = e[i];
+                }
+                store_planes<E, P>(to + (a0 + k * teams) * 64, p.rows_plane, v);
+            }
+        }
+    }
     if (blockIdx.x + 1 == gridDim.x) {
         if (threadIdx.x == 0) *p.count = before;
-        end = (before + 31) / 32 * 32;
-    }
-    for (int64_t a = begin + wave; a < end; a += 16) {
-        const T* x = a < before ? row_at<T>(p.x, p.index[a], p.x_N) : nullptr;
-        char* to = p.rows + a * 64;
-        for (int c = lane * 8; c < p.kd; c += 512) {
-            f32x8 v = {};
-            if (x != nullptr && c < p.d) {
-                float e[8];
-                if constexpr (kUnit<T> == 8) {
-                    load_unit<T, UNITS>(x, c, p.d, e);
-                } else {
-                    float lo[kUnit<T>], hi[kUnit<T>];
-                    load_unit<T, UNITS>(x, c, p.d, lo);
-                    load_unit<T, UNITS>(x, c + 4, p.d, hi);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) e[i] = lo[i], e[4 + i] = hi[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = e[i];
-            }
-            store_planes<E, P>(to + (c >> 5) * p.tokens * 64 + (c & 31) * 2, p.rows_plane, v);
-        }
+        // after the last one zeros up to a whole step of 32
+        const f32x8 none = {};
+        for (int64_t a = before + team; a < (before + 31) / 32 * 32; a += teams)
+            for (int c = tl * 8; c < p.kd; c += lanes * 8)
+                store_planes<E, P>(p.rows + a * 64 + (c >> 5) * p.tokens * 64 + (c & 31) * 2, p.rows_plane, none);
     }
     if constexpr (GRAD) {
         // binary16 holds G over the power of two above the largest |d_loss|, times 2^15
@@ -210,16 +224,24 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2)
     m = top;
 }
 
-// Logits of kLossValues values (rows of the tile) and kLossTokens tokens (columns).
-template <typename T, bool GRAD>
-__global__ __launch_bounds__(LossType<T>::kThreads, LossType<T>::P == 1 ? 3 : 2) void hyena_loss_logits(LossArgs p, int value_tiles)
+// Logits of TM values (rows of the tile) and TN tokens (columns).  Small tiles have more of
+// their short steps under way.
+template <typename T, bool SMALL> struct LogitsTile {
+    static constexpr int TM = SMALL ? kSmallTile : kLossValues, TN = SMALL ? kSmallTile : kLossTokens;
+    static constexpr int P = LossType<T>::P, WM = SMALL ? 2 : LossType<T>::WM, WN = SMALL ? 2 : LossType<T>::WN;
+    static constexpr int kThreads = WM * WN * 64, kStages = SMALL ? (P == 1 ? 4 : 3) : 2;
+    static constexpr int kWaves = P == 1 && !SMALL ? 3 : 2;  // of a SIMD
+};
+template <typename T, bool GRAD, bool SMALL>
+__global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SMALL>::kWaves)) void hyena_loss_logits(LossArgs p, int value_tiles)
 {
+    using L = LogitsTile<T, SMALL>;
     using E = typename LossType<T>::E;
-    constexpr int P = LossType<T>::P, WM = LossType<T>::WM, WN = LossType<T>::WN;
-    using Tile = MatTile<E, kLossValues, kLossTokens, WM, WN, kInColumnsPaired, kInColumns, P, 2>;
+    constexpr int P = L::P, WM = L::WM, WN = L::WN, TM = L::TM, TN = L::TN;
+    using Tile = MatTile<E, TM, TN, WM, WN, kInColumnsPaired, kInColumns, P, L::kStages>;
     __shared__ __attribute__((aligned(16))) char lds[Tile::kLds];
     const int64_t count = *p.count;
-    const int token_tiles = (int)(p.tokens / kLossTokens);
+    const int token_tiles = (int)(p.tokens / TN);
     int value_tile, token_tile;
     if (deal_tokens(value_tiles, token_tiles)) {
         deal(blockIdx.x, value_tiles, token_tiles, value_tile, token_tile);
@@ -232,9 +254,9 @@ __global__ __launch_bounds__(LossType<T>::kThreads, LossType<T>::P == 1 ? 3 : 2)
         value_tile = (group * kLossGroup + (int)(rest % width)) * 8 + (int)(blockIdx.x & 7);
         token_tile = (int)(rest / width);
     }
-    const int64_t t0 = (int64_t)token_tile * kLossTokens;
+    const int64_t t0 = (int64_t)token_tile * TN;
     if (t0 >= count || value_tile >= value_tiles) return;
-    const int32_t v0 = p.first + value_tile * kLossValues;
+    const int32_t v0 = p.first + value_tile * TM;
     Tile tile;
     const Operand values{p.values + (int64_t)v0 * p.values_row, p.values + p.values_bytes, p.values_row, p.values_block};
     const Operand rows{p.rows + t0 * 64, p.rows + p.rows_plane, 64, p.tokens * 64};
@@ -243,18 +265,18 @@ __global__ __launch_bounds__(LossType<T>::kThreads, LossType<T>::P == 1 ? 3 : 2)
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4;
     const int wm = wave / WN, wn = wave % WN;
     const float scale2 = p.scale * kLog2e;
-    const int first = wm * (kLossValues / WM) + 8 * g;  // this lane's values: first + at(i) + r
+    const int first = wm * (TM / WM) + 8 * g;  // this lane's values: first + at(i) + r
     auto at = [](int i) { return 32 * (i >> 1) + 4 * (i & 1); };
     const int left = p.V - v0;                         // values of the tile that there are
     if constexpr (!GRAD) {
-        float2* shares = (float2*)lds;  // [WM][kLossTokens]
+        float2* shares = (float2*)lds;  // [WM][TN]
 #pragma unroll
         for (int j = 0; j < Tile::NI; ++j) {
-            const int n = wn * (kLossTokens / WN) + 16 * j + (lane & 15);
+            const int n = wn * (TN / WN) + 16 * j + (lane & 15);
             const int64_t t = t0 + n;
 #pragma unroll
             for (int i = 0; i < Tile::MI; ++i) tile.c[i][j] *= scale2;
-            if (left < kLossValues) {
+            if (left < TM) {
 #pragma unroll
                 for (int i = 0; i < Tile::MI; ++i)
 #pragma unroll
@@ -262,13 +284,13 @@ __global__ __launch_bounds__(LossType<T>::kThreads, LossType<T>::P == 1 ? 3 : 2)
                         if (first + at(i) + r >= left) tile.c[i][j][r] = -INFINITY;
             }
             const int target = t < count ? p.target[t] - v0 - first : -1;
-            if (__any((uint32_t)target < (uint32_t)(kLossValues / WM))) {
+            if (__any((uint32_t)target < (uint32_t)(TM / WM))) {
                 float hit = 0.0f;
 #pragma unroll
                 for (int i = 0; i < Tile::MI; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) hit = target == at(i) + r ? tile.c[i][j][r] : hit;
-                if ((uint32_t)target < (uint32_t)(kLossValues / WM) && (target & 31) < 8) p.hit[t] = hit;
+                if ((uint32_t)target < (uint32_t)(TM / WM) && (target & 31) < 8) p.hit[t] = hit;
             }
             float m = -INFINITY;
 #pragma unroll
@@ -285,21 +307,21 @@ __global__ __launch_bounds__(LossType<T>::kThreads, LossType<T>::P == 1 ? 3 : 2)
                 for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(tile.c[i][j][r] - base);
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
-            if (g == 0) shares[wm * kLossTokens + n] = make_float2(m, s);
+            if (g == 0) shares[wm * TN + n] = make_float2(m, s);
         }
         __syncthreads();
-        if (threadIdx.x < kLossTokens) {
+        if (threadIdx.x < TN) {
             float2 a = shares[threadIdx.x];
 #pragma unroll
-            for (int w = 1; w < WM; ++w) join(a.x, a.y, shares[w * kLossTokens + threadIdx.x].x, shares[w * kLossTokens + threadIdx.x].y);
+            for (int w = 1; w < WM; ++w) join(a.x, a.y, shares[w * TN + threadIdx.x].x, shares[w * TN + threadIdx.x].y);
             p.part[(int64_t)value_tile * p.tokens + t0 + threadIdx.x] = a;
         }
     } else {
         const float up = p.norm[0];
-        const bool rim = left < kLossValues || t0 + kLossTokens > count;
+        const bool rim = left < TM || t0 + TN > count;
 #pragma unroll
         for (int j = 0; j < Tile::NI; ++j) {
-            const int n = wn * (kLossTokens / WN) + 16 * j + (lane & 15);
+            const int n = wn * (TN / WN) + 16 * j + (lane & 15);
             const int64_t t = t0 + n;
             const bool in = t < count;
             const int target = in ? p.target[t] - v0 - first : -1;
@@ -316,7 +338,7 @@ __global__ __launch_bounds__(LossType<T>::kThreads, LossType<T>::P == 1 ? 3 : 2)
                     for (int r = 0; r < 4; ++r)
                         if (!in || first + at(i) + r >= left) tile.c[i][j][r] = 0.0f;
             }
-            if (__any((uint32_t)target < (uint32_t)(kLossValues / WM))) {
+            if (__any((uint32_t)target < (uint32_t)(TM / WM))) {
                 float off = 0.0f;
 #pragma unroll
                 for (int i = 0; i < Tile::MI; ++i)
@@ -330,9 +352,9 @@ __global__ __launch_bounds__(LossType<T>::kThreads, LossType<T>::P == 1 ? 3 : 2)
                                 off = tile.c[i][j][r] - load_one<E>(&rounded);
                             }
                         }
-                if (P == 1 && (uint32_t)target < (uint32_t)(kLossValues / WM) && (target & 31) < 8) p.hit[t] = off;
+                if (P == 1 && (uint32_t)target < (uint32_t)(TM / WM) && (target & 31) < 8) p.hit[t] = off;
             }
-            char* to = p.g + (int64_t)((value_tile * kLossValues + wm * (kLossValues / WM)) >> 5) * p.tokens * 64 + t * 64 + g * 16;
+            char* to = p.g + (int64_t)((value_tile * TM + wm * (TM / WM)) >> 5) * p.tokens * 64 + t * 64 + g * 16;
 #pragma unroll
             for (int i = 0; i < Tile::MI; i += 2)
                 store_planes<E, P>(to + (int64_t)(i >> 1) * p.tokens * 64, p.g_plane, join8(tile.c[i][j], tile.c[i + 1][j]));
@@ -574,23 +596,28 @@ template <typename T, int N, bool UNITS> __global__ __launch_bounds__(256) void 
 }
 
 // tiles: of this piece of the vocabulary; what came before it is in p.running, unless it is
-// the first, and what is behind the last one is the result.
-template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_join(LossArgs p, int tiles, bool last)
+// the first, and what is behind the last one is the result.  TOKENS of a workgroup, 16, or
+// where tiles are few 256 (2^18 tokens, 1 tile: JOIN_A us, with 16 51).
+template <typename T, int TOKENS> __global__ __launch_bounds__(1024) void hyena_loss_join(LossArgs p, int tiles, bool last)
 {
-    __shared__ float2 lds[16][16];
-    const int64_t count = *p.count, a = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
-    if ((int64_t)blockIdx.x * 16 >= count) return;
+    constexpr int kLanes = TOKENS < 64 ? TOKENS : 64, kParts = TOKENS < 64 ? 16 : 1024 / TOKENS;  // of a wave's tokens; to be joined at last
+    __shared__ float2 lds[kParts][TOKENS];
+    const int own = threadIdx.x % TOKENS;
+    const int64_t count = *p.count, a = (int64_t)blockIdx.x * TOKENS + own;
+    if ((int64_t)blockIdx.x * TOKENS >= count) return;
     float m = -INFINITY, s = 0.0f;
+    if (a < p.tokens) {
 #pragma unroll 8
-    for (int i = threadIdx.x >> 4; i < tiles; i += 64) {
-        const float2 x = p.part[(int64_t)i * p.tokens + a];
-        join(m, s, x.x, x.y);
+        for (int i = threadIdx.x / TOKENS; i < tiles; i += 1024 / TOKENS) {
+            const float2 x = p.part[(int64_t)i * p.tokens + a];
+            join(m, s, x.x, x.y);
+        }
     }
-    for (int k = 16; k < 64; k *= 2) join(m, s, __shfl_xor(m, k), __shfl_xor(s, k));
-    if ((threadIdx.x & 63) < 16) lds[threadIdx.x >> 6][threadIdx.x & 15] = make_float2(m, s);
+    for (int k = kLanes; k < 64; k *= 2) join(m, s, __shfl_xor(m, k), __shfl_xor(s, k));
+    if ((threadIdx.x & 63) < kLanes) lds[TOKENS < 64 ? threadIdx.x >> 6 : threadIdx.x / TOKENS][own] = make_float2(m, s);
     __syncthreads();
-    if (threadIdx.x < 16 && a < count) {
-        for (int i = 1; i < 16; ++i) join(m, s, lds[i][threadIdx.x].x, lds[i][threadIdx.x].y);
+    if (threadIdx.x < TOKENS && a < count) {
+        for (int i = 1; i < kParts; ++i) join(m, s, lds[i][own].x, lds[i][own].y);
         if (p.first != 0) join(m, s, p.running[a].x, p.running[a].y);
         if (!last) {
             p.running[a] = make_float2(m, s);
@@ -787,54 +814,104 @@ template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_table(L
     }
 }
 
-// d_x of a token from its sums, by ROWS waves for each token (few tokens have many sums).
-template <typename T, int ROWS> __global__ __launch_bounds__(ROWS == 1 ? 256 : 1024) void hyena_loss_finish(LossArgs p)
+// 4 channels of d_x of a token, x their sum.
+template <typename T> __device__ __forceinline__ void store_dx(const LossArgs& p, int64_t t, int c, f32x4 x)
 {
-    constexpr int kWaves = ROWS == 1 ? 4 : 16, kTokens = kWaves / ROWS;
-    __shared__ f32x4 lds[ROWS == 1 ? 1 : kWaves][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, part = wave % ROWS;
+    T* to = (T*)p.d_x + t * p.d + c;
+    if (p.d % 4 == 0) {
+        *(typename Mx<T>::vec4*)to = Mx<T>::narrow(x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < p.d) store_one<T>(to + e, x[e]);
+    }
+}
+
+// The rest of G at the target times its row of the table.
+template <typename T> __device__ __forceinline__ f32x4 target_rest(const LossArgs& p, int target, float rest, int c)
+{
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (LossType<T>::P == 1) {
+        const T* w = (const T*)p.table + (int64_t)target * p.d + c;
+        if (p.d % 4 == 0) {
+            x = Mx<T>::widen(*(const typename Mx<T>::vec4*)w) * rest;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.d) x[e] = rest * load_one<T>(w + e);
+        }
+    }
+    return x;
+}
+
+// d_x of tokens from their sums, a wave for kTokens tokens.
+template <typename T, int kTokens> __global__ __launch_bounds__(256) void hyena_loss_finish(LossArgs p)
+{
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const float down = p.norm[1];
+    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * kTokens; t0 < p.total; t0 += (int64_t)gridDim.x * 4 * kTokens) {
+        int32_t a[kTokens], target[kTokens];
+        float rest[kTokens];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) a[k] = t0 + k < p.total ? p.place[t0 + k] : -1;
+        if constexpr (LossType<T>::P == 1) {
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) {
+                target[k] = a[k] >= 0 ? p.target[a[k]] : 0;
+                rest[k] = a[k] >= 0 ? p.hit[a[k]] : 0.0f;
+            }
+        }
+        for (int c = lane * 4; c < p.d; c += 256) {
+            f32x4 x[kTokens];
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) {
+                x[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if constexpr (LossType<T>::P == 1) x[k] = target_rest<T>(p, target[k], rest[k], c);
+            }
+#pragma unroll 2
+            for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+                for (int k = 0; k < kTokens; ++k)  // (a token that takes no part has some row's sum and drops it)
+                    x[k] += *(const f32x4*)(p.acc + ((int64_t)s * p.tokens + (a[k] < 0 ? 0 : a[k])) * p.acc_row + c);
+            }
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k)
+                if (t0 + k < p.total) store_dx<T>(p, t0 + k, c, a[k] < 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : x[k] * down);
+        }
+    }
+}
+
+// The same by 16 waves for each token: few tokens have many sums.
+template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_finish_few(LossArgs p)
+{
+    __shared__ f32x4 lds[16][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const float down = p.few ? p.scale : p.norm[1];
-    for (int64_t t = (int64_t)blockIdx.x * kTokens + wave / ROWS; t < p.total; t += (int64_t)gridDim.x * kTokens) {
+    for (int64_t t = blockIdx.x; t < p.total; t += gridDim.x) {
         const int32_t a = p.place[t];
-        T* to = (T*)p.d_x + t * p.d;
         for (int c0 = 0; c0 < p.d; c0 += 256) {
             const int c = c0 + lane * 4;
             f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
             if (a >= 0 && c < p.d) {
                 const float* from = p.acc + (int64_t)a * p.acc_row + c;
 #pragma unroll 4
-                for (int s = part; s < p.splits; s += ROWS) x += *(const f32x4*)(from + (int64_t)s * p.tokens * p.acc_row);
+                for (int s = wave; s < p.splits; s += 16) x += *(const f32x4*)(from + (int64_t)s * p.tokens * p.acc_row);
             }
-            if constexpr (ROWS > 1) {
-                lds[wave][lane] = x;
-                __syncthreads();
-                if (part == 0) {
+            lds[wave][lane] = x;
+            __syncthreads();
+            if (wave == 0 && c < p.d) {
 #pragma unroll
-                    for (int w = 1; w < ROWS; ++w) x += lds[wave + w][lane];
-                }
-                __syncthreads();
-                if (part != 0) continue;
+                for (int w = 1; w < 16; ++w) x += lds[w][lane];
+                if (LossType<T>::P == 1 && a >= 0 && !p.few) x += target_rest<T>(p, p.target[a], p.hit[a], c);
+                store_dx<T>(p, t, c, x * down);
             }
-            if (c >= p.d) continue;
-            if (LossType<T>::P == 1 && a >= 0 && !p.few) {
-                // the rest of G at the target
-                const float off = p.hit[a];
-                const T* w = (const T*)p.table + (int64_t)p.target[a] * p.d + c;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < p.d) x[e] = fmaf(off, load_one<T>(w + e), x[e]);
-            }
-            x *= down;
-            if (p.d % 4 == 0) {
-                *(typename Mx<T>::vec4*)(to + c) = Mx<T>::narrow(x);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < p.d) store_one<T>(to + c + e, x[e]);
-            }
+            __syncthreads();
         }
     }
 }
+
+// Calls of fewer tokens: a wave of hyena_loss_finish has one token, not four.
+constexpr int64_t kFinishTokens = 16384;
 
 template <typename T, bool GRAD> hyena_status loss_begin(const LossArgs& a, bool pack, bool units, hipStream_t s)
 {
@@ -864,9 +941,12 @@ template <typename T, int N, bool GRAD> hyena_status loss_few(const LossArgs& a,
 template <typename T, bool GRAD> hyena_status loss_logits(const LossArgs& a, int tiles, hipStream_t s)
 {
     if (!a.few) {
-        const int token_tiles = (int)(a.tokens / kLossTokens);
-        HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), GRAD), (hyena_loss_logits<T, GRAD>),
-                  dim3((unsigned)(deal_tokens(tiles, token_tiles) ? dealt(tiles, token_tiles) : dealt(token_tiles, tiles))), dim3(LossType<T>::kThreads), 0, s, a, tiles);
+        const int token_tiles = (int)(a.tokens / (a.small ? kSmallTile : kLossTokens));
+        const dim3 grid((unsigned)(deal_tokens(tiles, token_tiles) ? dealt(tiles, token_tiles) : dealt(token_tiles, tiles)));
+        if (a.small)
+            HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), GRAD, true), (hyena_loss_logits<T, GRAD, true>), grid, dim3((LogitsTile<T, true>::kThreads)), 0, s, a, tiles);
+        else
+            HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), GRAD, false), (hyena_loss_logits<T, GRAD, false>), grid, dim3((LogitsTile<T, false>::kThreads)), 0, s, a, tiles);
         return launched();
     }
     if constexpr (!GRAD) {
@@ -897,9 +977,12 @@ template <typename T> hyena_status loss_forward(const LossArgs& a, bool pack, bo
     for (int64_t first = 0; first < a.V; first += a.chunk) {
         b.first = (int32_t)first;
         const bool last = first + a.chunk >= a.V;
-        const int tiles = a.few ? few_groups(a.V) : loss_tiles(last ? a.V - first : a.chunk);
+        const int tiles = a.few ? few_groups(a.V) : loss_tiles(last ? a.V - first : a.chunk, a.small);
         if ((st = loss_logits<T, false>(b, tiles, s)) != HYENA_OK) return st;
-        HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>()), hyena_loss_join<T>, dim3((unsigned)((a.total + 15) / 16)), dim3(1024), 0, s, b, tiles, last);
+        if (tiles > 16)
+            HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>(), 16), (hyena_loss_join<T, 16>), dim3((unsigned)((a.total + 15) / 16)), dim3(1024), 0, s, b, tiles, last);
+        else
+            HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>(), 256), (hyena_loss_join<T, 256>), dim3((unsigned)((a.total + 255) / 256)), dim3(1024), 0, s, b, tiles, last);
         if ((st = launched()) != HYENA_OK) return st;
     }
     return HYENA_OK;
@@ -914,7 +997,7 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
     for (int64_t first = 0; first < a.V; first += a.chunk) {
         b.first = (int32_t)first;
         const int values = a.V - first < a.chunk ? (int)(a.V - first) : a.chunk;
-        if ((st = loss_logits<T, true>(b, a.few ? few_groups(a.V) : loss_tiles(values), s)) != HYENA_OK) return st;
+        if ((st = loss_logits<T, true>(b, a.few ? few_groups(a.V) : loss_tiles(values, a.small), s)) != HYENA_OK) return st;
         if (a.few) {  // all of the vocabulary is one piece
             if ((st = a.total <= 4 ? loss_few_grads<T, 4>(a, s) : loss_few_grads<T, 16>(a, s)) != HYENA_OK) return st;
             break;
@@ -930,12 +1013,15 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
         if ((st = launched()) != HYENA_OK) return st;
     }
     if (a.d_x == nullptr) return HYENA_OK;
-    const int64_t need = a.splits <= 8 ? (a.total + 3) / 4 : a.total;
+    const int tokens = a.total < kFinishTokens ? 1 : 4;  // of a wave
+    const int64_t need = a.splits <= 8 ? (a.total + 4 * tokens - 1) / (4 * tokens) : a.total;
     const dim3 grid((unsigned)(need < 4096 ? need : 4096));
-    if (a.splits <= 8)
+    if (a.splits <= 8 && tokens == 1)
         HY_LAUNCH(kernel_label("hyena_loss_finish", type_label<T>(), 1), (hyena_loss_finish<T, 1>), grid, dim3(256), 0, s, a);
+    else if (a.splits <= 8)
+        HY_LAUNCH(kernel_label("hyena_loss_finish", type_label<T>(), 4), (hyena_loss_finish<T, 4>), grid, dim3(256), 0, s, a);
     else
-        HY_LAUNCH(kernel_label("hyena_loss_finish", type_label<T>(), 16), (hyena_loss_finish<T, 16>), grid, dim3(1024), 0, s, a);
+        HY_LAUNCH(kernel_label("hyena_loss_finish_few", type_label<T>()), hyena_loss_finish_few<T>, grid, dim3(1024), 0, s, a);
     return launched();
 }
 

@@ -356,3 +356,54 @@ def test_many_tokens_in_pieces_forward():
         hit = l.gather(1, t.clamp(min=0)[:, None])[:, 0]
         assert float((lse[0, rows] - ref).abs().max()) < 1e-4
         assert float((loss[0, rows] - torch.where(t >= 0, ref - hit, 0)).abs().max()) < 2e-4
+
+
+MORE = [
+    # whole tiles of logits, with rims on both axes; few values and many tokens: tokens dealt out and cut
+    (1, 2100, 2305, 40), (1, 130, 33000, 33), (1, 33000, 65, 17), (3, 4000, 16, 256), (1, 9000, 200, 40), (1, 2396, 277, 25),
+    (2, 600, 700, 513),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", MORE)
+def test_shapes_of_tiles_against_float64(case, dtype):
+    import torch
+    plan, x, table, target, d_loss, loss, lse = run(case, dtype)
+    again = plan.forward(x, table, target) + plan.backward(d_loss, x, table, target, lse)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+    more = plan.backward(d_loss, x, table, target, lse)
+    assert torch.equal(again[2], more[0]) and torch.equal(again[3], more[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("case", [(1, 6000, 33000, 256), (1, 150, 300, 96), (1, 5000, 40, 64)])
+def test_gradient_of_a_row_that_all_tokens_have_as_target(case, dtype):
+    # G at the target is -(1 + 0.95 u) (1 - p) for every token, and x positive: that rounding's error, u of
+    # the row in every channel, must not be in it.  Behind it is u for the row's own, u^2 for
+    # the rest's, and what check_grad has for the sum.
+    import torch
+    B, N, V, d = case
+    say(f"[gpu] token_loss, one target for all {case} {dtype}")
+    u = ends_ref.HALF_STEP[dtype]
+    x, table, target, _ = make(case, dtype, 11, masked=0.0)
+    x, table = x.abs() + 0.5, table * 0.1
+    row = V * 3 // 7
+    target.fill_(row)
+    target[0, N // 2] = -1
+    dl = float(np.float32(1 + 0.95 * u))
+    d_loss = torch.full((B, N), dl, device="cuda")
+    plan = hyena.TokenLoss(B, N, V, d, io_dtype=IO[dtype])
+    loss, lse = plan.forward(x, table, target)
+    _, dt = plan.backward(d_loss, x, table, target, lse, want_dx=False)
+    live = target.view(-1).cpu().numpy() == row
+    xs, ws = f64(x)[0][live], f64(table)[row]
+    size = np.abs(xs) @ np.abs(ws)
+    p = np.exp(xs @ ws - f64(lse)[0][live])
+    g = dl * (p - 1)
+    r = 2 * (d + 8) * 2.0 ** -24 * size + 2.0 ** -20 + 2.0 ** -21 * size
+    dg = dl * (r * p + 2.0 ** -23) + u * u * np.abs(g) + (2.0 ** -38 if dtype == "f16" else 0.0)
+    ref = g @ xs
+    bound = u * np.abs(ref) + (dg + (N + 16) * 2.0 ** -24 * np.abs(g)) @ np.abs(xs)
+    assert np.all((1.95 * u - 2 * u * u) * np.abs(ref) > bound)  # (the error of one rounding more would show)
+    compare(dt[row], ref, bound, "d_table of the target")
