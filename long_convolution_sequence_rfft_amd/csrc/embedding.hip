@@ -19,6 +19,10 @@
 //       reaches over a run's end leaves its sum there.  Other workgroups of the
 //       same launch write the zeros of values without tokens.
 //   hyena_embedding_joins  adds the pieces of values that reach over runs.
+// A table of few values needs no sorting: in hyena_embedding_few each team of lanes has its
+// tokens, one after the other, and sums of all values in LDS, which
+// hyena_embedding_few_join adds up (2^18 tokens, 16 values, width 256: 64 us so, 130 sorted;
+// 2^20 tokens, 4 values, width 64: 63 and 899).
 // Bound by memory: each gradient row is read once, each row of the table written
 // once.
 #include "rows.h"
@@ -31,6 +35,11 @@ constexpr const char* kWho = "embedding";
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortGroups = 256;   // at least; more where a group would have more values than kSortValues
 constexpr int kSortValues = 384;   // counters of a wave: 24 KB of LDS in all
+// From kDealGroups groups on, which all read all tokens, they have up to this many (16384 tokens of 10^6
+// values: the sort takes 35 us so, 92 with 4096 groups): 96 KB.
+constexpr int kSortMostValues = 1536;
+constexpr int kPlaceBits = 21;
+static_assert(kSortMostValues <= 1 << (32 - kPlaceBits), "");
 constexpr int kSortTokens = 16;    // of a lane, in four loads
 constexpr int kDealTokens = 4096;  // of a workgroup that deals
 constexpr int kDealGroups = 1024;  // at most
@@ -40,6 +49,9 @@ constexpr int64_t kDealCalls = 131072;
 constexpr int kSortKept = 512;     // tokens of its values that a wave keeps: 32 KB of LDS in all
 constexpr int kSumRows = 4;        // gradient rows of a team under way
 constexpr int64_t kSumTeams = 4096;  // runs are no shorter than kSumRows, and as short as this many of them allow
+constexpr int kFewValues = 32;     // tables of no more values than this
+constexpr int kFewRows = 8;        // gradient rows of a team under way
+constexpr int kFewGroups = 512;    // workgroups at most
 constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / 64;
 
 struct EmbedArgs {
@@ -56,7 +68,7 @@ struct EmbedArgs {
     int32_t run;         // tokens of a run, a power of two
     int32_t sum_groups;  // workgroups of the sums, fill_groups behind them
     int32_t fill_groups;
-    int32_t* counts;     // [V]
+    int32_t* counts;     // [V]; few values: [few_groups] which of them a workgroup has tokens of, by bits
     int2* sorted;        // [total] value and token, in order; [total].x the number of tokens that take part
     int4* joins;         // [V] values that reach over runs, where they begin, tokens: group g's from g * values on
     int32_t* join_counts;  // [groups]
@@ -65,6 +77,7 @@ struct EmbedArgs {
     int32_t deal_blocks;
     float* part;         // [runs][2][d4]: sums that reach over a run's start and over its end
     int32_t d4;          // d rounded up to 4
+    int32_t few_groups;  // few values: workgroups, each with a part [V][d4]
 };
 
 __device__ __forceinline__ int token_at(const EmbedArgs& p, int64_t t) { return *row_at<int32_t>(p.tokens, t, p.N); }
@@ -225,7 +238,7 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
             }
         }
     };
-    int n_own = 0;  // this wave's tokens of the group's values; the first kSortKept are kept: i << 22 | place in its part
+    int n_own = 0;  // this wave's tokens of the group's values; the first kSortKept are kept: i << kPlaceBits | place in its part
     if (p.dealt != nullptr) {
         const int32_t *lo = p.deal_starts + (int64_t)group * p.deal_blocks, *end = p.deal_starts + (int64_t)p.groups * p.deal_blocks;
         for (int b = threadIdx.x; b < p.deal_blocks; b += kSortThreads) {
@@ -236,7 +249,7 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
             const int i = v >> shift;
             if (own) {
                 atomicAdd(&counters[wave * values + i], 1);
-                if (n_own + lane < kSortKept) kept[wave][n_own + lane] = (uint32_t)i << 22 | (uint32_t)(t - first);
+                if (n_own + lane < kSortKept) kept[wave][n_own + lane] = (uint32_t)i << kPlaceBits | (uint32_t)(t - first);
             }
             n_own += __popcll(__ballot(own));
         });
@@ -263,7 +276,7 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
                 const int at = n_own + __popcll(who & (((uint64_t)1 << lane) - 1)), i = v[k + j] >> shift;
                 if (own) {
                     atomicAdd(&counters[wave * values + i], 1);
-                    if (at < kSortKept) kept[wave][at] = (uint32_t)i << 22 | (uint32_t)(t0 - first + 64 * k + 4 * lane + j);
+                    if (at < kSortKept) kept[wave][at] = (uint32_t)i << kPlaceBits | (uint32_t)(t0 - first + 64 * k + 4 * lane + j);
                 }
                 n_own += __popcll(who);
             }
@@ -327,11 +340,11 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
             left &= ~all_same;
         }
     };
-    if (n_own <= kSortKept && each <= 1 << 22) {
+    if (n_own <= kSortKept && each <= 1 << kPlaceBits) {
         for (int k = 0; k < n_own; k += 64) {
             const bool own = k + lane < n_own;
             const uint32_t x = own ? kept[wave][k + lane] : 0;
-            put(own, (int)(x >> 22), first + (x & 0x3fffff));
+            put(own, (int)(x >> kPlaceBits), first + (x & ((1 << kPlaceBits) - 1)));
         }
         return;
     }
@@ -480,6 +493,103 @@ template <typename T> __global__ __launch_bounds__(kJoinThreads) void hyena_embe
     }
 }
 
+// Tokens of a team of p.lanes lanes, four channels each; blockIdx.y: which 256 channels.
+template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_embedding_few(EmbedArgs p)
+{
+    extern __shared__ f32x4 few_sums[];  // [teams][V][lanes]
+    __shared__ uint32_t any;             // bit v: value v has a token
+    static_assert(kFewValues <= 32, "");
+    if (threadIdx.x == 0) any = 0;
+    uint32_t seen = 0;
+    const int teams = 256 / p.lanes, team = threadIdx.x / p.lanes, tl = threadIdx.x % p.lanes;
+    const int c = (int)blockIdx.y * 256 + tl * 4;
+    f32x4* own = few_sums + (size_t)team * p.V * p.lanes + tl;
+    for (int v = 0; v < p.V; ++v) own[v * p.lanes] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t parts = (int64_t)gridDim.x * teams, each = (p.total + parts - 1) / parts;
+    const int64_t first = ((int64_t)blockIdx.x * teams + team) * each, last = first + each < p.total ? first + each : p.total;
+    // kFewRows rows are under way while those before them are added, and the tokens behind them
+    struct Rows8 {
+        int v[kFewRows];
+        typename Mx<T>::vec4 x[kFewRows];
+    } a, b;
+    auto tokens = [&](int64_t t0, Rows8& r) {
+#pragma unroll
+        for (int k = 0; k < kFewRows; ++k) r.v[k] = t0 + k < last ? token_at(p, t0 + k) : -1;
+    };
+    auto rows = [&](int64_t t0, Rows8& r) {
+#pragma unroll
+        for (int k = 0; k < kFewRows; ++k) {
+            r.x[k] = typename Mx<T>::vec4{};
+            if ((uint32_t)r.v[k] >= (uint32_t)p.V) continue;
+            const T* row = row_at<T>(p.rows, t0 + k, p.rows_N) + c;
+            if (UNITS) {
+                if (c < p.d) r.x[k] = *(const typename Mx<T>::vec4*)row;
+            } else {
+                T* e = (T*)&r.x[k];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < p.d) e[i] = row[i];
+            }
+        }
+    };
+    auto add = [&](const Rows8& r) {
+#pragma unroll
+        for (int k = 0; k < kFewRows; ++k)
+            if ((uint32_t)r.v[k] < (uint32_t)p.V) {
+                own[r.v[k] * p.lanes] += Mx<T>::widen(r.x[k]);
+                seen |= 1u << r.v[k];
+            }
+    };
+    tokens(first, a);
+    rows(first, a);
+    tokens(first + kFewRows, b);
+    for (int64_t t0 = first; t0 < last; t0 += 2 * kFewRows) {
+        rows(t0 + kFewRows, b);
+        add(a);
+        tokens(t0 + 2 * kFewRows, a);
+        rows(t0 + 2 * kFewRows, a);
+        add(b);
+        tokens(t0 + 3 * kFewRows, b);
+    }
+    __syncthreads();
+    if (tl == 0) atomicOr(&any, seen);
+    // the teams' sums in their order
+    for (int i = threadIdx.x; i < p.V * p.lanes; i += 256) {
+        f32x4 sum = few_sums[i];
+        for (int k = 1; k < teams; ++k) sum += few_sums[(size_t)k * p.V * p.lanes + i];
+        const int at = (int)blockIdx.y * 256 + i % p.lanes * 4;
+        if (at < p.d) *(f32x4*)(p.part + ((int64_t)blockIdx.x * p.V + i / p.lanes) * p.d4 + at) = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && blockIdx.y == 0) p.counts[blockIdx.x] = (int32_t)any;
+}
+
+// blockIdx.x: the value, blockIdx.y: which 256 channels; each of 16 waves some of the parts.
+template <typename T> __global__ __launch_bounds__(1024) void hyena_embedding_few_join(EmbedArgs p)
+{
+    __shared__ f32x4 lds[16][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int c = (int)blockIdx.y * 256 + lane * 4;
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < p.d) {
+#pragma unroll 8
+        for (int g = wave; g < p.few_groups; g += 16) s += *(const f32x4*)(p.part + ((int64_t)g * p.V + blockIdx.x) * p.d4 + c);
+    }
+    lds[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0) return;
+    uint32_t seen = 0;
+    for (int g = lane; g < p.few_groups; g += 64) seen |= (uint32_t)p.counts[g];
+    const bool some = __any(seen >> blockIdx.x & 1);
+    if (!some && p.accumulate) return;
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += lds[w][lane];
+    T* row = (T*)p.out + (int64_t)blockIdx.x * p.d + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (c + i < p.d) store_one<T>(row + i, !some ? 0.0f : p.accumulate ? fmaf(s[i], p.scale, load_one<T>(row + i)) : s[i] * p.scale);
+}
+
 hyena_status refuse(const char* what) { return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(kWho) + ": " + what); }
 
 hyena_status embed_sizes(const hyena_embedding* op)
@@ -497,12 +607,26 @@ struct EmbedSpace {
     size_t sorted, counts, joins, join_counts, dealt, deal_starts, part, total;  // byte offsets and the size
     int32_t deal_blocks;  // 0: not dealt
     int32_t groups, d4;
+    int32_t few_groups, few_lanes;  // 0: the tokens are sorted
 };
 
 EmbedSpace embed_space(const hyena_embedding* op)
 {
-    EmbedSpace w;
+    EmbedSpace w{};
     const int64_t T = op->B * op->N;
+    w.d4 = (int32_t)((op->d + 3) / 4 * 4);
+    w.few_groups = w.few_lanes = 0;
+    if (op->V <= kFewValues) {
+        // lanes of a team: a power of two, as many as channels ask for
+        w.few_lanes = 64;
+        while (w.few_lanes > 8 && w.few_lanes / 2 * 4 >= w.d4) w.few_lanes /= 2;
+        const int64_t teams = 256 / w.few_lanes, need = (T + teams * 2 * kFewRows - 1) / (teams * 2 * kFewRows);
+        w.few_groups = (int32_t)(need < kFewGroups ? need : kFewGroups);
+        w.counts = 0;
+        w.part = (size_t)(w.few_groups + 63) / 64 * 256;
+        w.total = w.part + (size_t)w.few_groups * (size_t)op->V * (size_t)w.d4 * 4;
+        return w;
+    }
     const int64_t most = (T + kSumTeams - 1) / kSumTeams;
     w.run = kSumRows;
     while (w.run < most) w.run *= 2;
@@ -511,8 +635,7 @@ EmbedSpace embed_space(const hyena_embedding* op)
     w.sorted = 0;
     w.counts = up((size_t)(T + 1) * sizeof(int2));
     w.groups = kSortGroups;
-    while ((op->V + w.groups - 1) / w.groups > kSortValues) w.groups *= 2;
-    w.d4 = (int32_t)((op->d + 3) / 4 * 4);
+    while ((op->V + w.groups - 1) / w.groups > (w.groups < kDealGroups ? kSortValues : kSortMostValues)) w.groups *= 2;
     w.joins = w.counts + up((size_t)op->V * 4);
     w.join_counts = w.joins + up((size_t)((op->V + w.groups - 1) / w.groups * w.groups) * sizeof(int4));
     w.deal_blocks = T >= kDealCalls && w.groups <= kDealGroups ? (int32_t)((T + kDealTokens - 1) / kDealTokens) : 0;
@@ -524,19 +647,31 @@ EmbedSpace embed_space(const hyena_embedding* op)
 }
 
 // Lanes of a team, which hold a unit each: 64, or 32 if that leaves fewer of them idle
-// over a row.
+// over a row, or as few as a narrow row has (2^20 rows of 64 in bf16: 30 us so, 98 by 32).
 void team_shape(EmbedArgs& a, size_t element)
 {
     const int units = (int)((a.d * element + 15) / 16);
     auto used = [&](int n) { return (units + n - 1) / n * n; };
     a.lanes = 64;
     if (used(32) < used(64)) a.lanes = 32;
+    while (a.lanes > 4 && a.lanes / 2 >= units) a.lanes /= 2;
 }
 
 template <typename T> hyena_status embed_backward(const EmbedArgs& a, bool units, int64_t runs, hipStream_t s)
 {
     hyena_status st;
     const bool dense = a.N == 0 && a.tokens.t == 1;
+    const dim3 few_grid((unsigned)a.few_groups, (unsigned)((a.d + 255) / 256));
+    if (a.few_groups > 0) {
+        st = by_units(units, [&](auto u) {
+            constexpr bool UNITS = decltype(u)::value;
+            HY_LAUNCH(kernel_label("hyena_embedding_few", type_label<T>(), UNITS), (hyena_embedding_few<T, UNITS>), few_grid, dim3(256), (size_t)a.V * 4096, s, a);
+            return launched();
+        });
+        if (st != HYENA_OK) return st;
+        HY_LAUNCH(kernel_label("hyena_embedding_few_join", type_label<T>()), hyena_embedding_few_join<T>, dim3((unsigned)a.V, few_grid.y), dim3(1024), 0, s, a);
+        return launched();
+    }
     if (a.dealt != nullptr) {
         const dim3 grid((unsigned)a.deal_blocks);
         const size_t lds = (size_t)a.groups * kSortWaves * 4;
@@ -658,14 +793,20 @@ hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_row
     a.rows_N = (uint32_t)N;
     a.out = d_table;
     a.accumulate = accumulate != 0;
-    a.groups = w.groups;
     a.d4 = w.d4;
+    a.part = (float*)((char*)scratch + w.part);
+    a.counts = (int32_t*)((char*)scratch + w.counts);
+    a.few_groups = w.few_groups;
+    const hipStream_t s = (hipStream_t)stream;
+    if (w.few_groups > 0) {
+        a.lanes = w.few_lanes;
+        return by_io(op->io_dtype, [&](auto* t) { return embed_backward<std::remove_pointer_t<decltype(t)>>(a, made.units(), 0, s); });
+    }
+    a.groups = w.groups;
     a.joins = (int4*)((char*)scratch + w.joins);
     a.join_counts = (int32_t*)((char*)scratch + w.join_counts);
     a.run = (int32_t)w.run;
     a.sorted = (int2*)((char*)scratch + w.sorted);
-    a.counts = (int32_t*)((char*)scratch + w.counts);
-    a.part = (float*)((char*)scratch + w.part);
     a.deal_blocks = w.deal_blocks;
     a.dealt = w.deal_blocks ? (int2*)((char*)scratch + w.dealt) : nullptr;
     a.deal_starts = (int32_t*)((char*)scratch + w.deal_starts);
@@ -674,7 +815,7 @@ hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_row
     const int64_t fill = (a.V + teams - 1) / teams;
     a.fill_groups = a.accumulate ? 0 : (int32_t)(fill < 2048 ? fill : 2048);
     return by_io(op->io_dtype, [&](auto* t) {
-        return embed_backward<std::remove_pointer_t<decltype(t)>>(a, made.units(), w.runs, (hipStream_t)stream);
+        return embed_backward<std::remove_pointer_t<decltype(t)>>(a, made.units(), w.runs, s);
     });
 }
 

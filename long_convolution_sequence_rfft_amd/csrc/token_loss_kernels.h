@@ -597,7 +597,7 @@ template <typename T, int N, bool UNITS> __global__ __launch_bounds__(256) void 
 
 // tiles: of this piece of the vocabulary; what came before it is in p.running, unless it is
 // the first, and what is behind the last one is the result.  TOKENS of a workgroup, 16, or
-// where tiles are few 256 (2^18 tokens, 1 tile: JOIN_A us, with 16 51).
+// where tiles are few 256 (2^18 tokens, 1 tile: 7 us, with 16 51).
 template <typename T, int TOKENS> __global__ __launch_bounds__(1024) void hyena_loss_join(LossArgs p, int tiles, bool last)
 {
     constexpr int kLanes = TOKENS < 64 ? TOKENS : 64, kParts = TOKENS < 64 ? 16 : 1024 / TOKENS;  // of a wave's tokens; to be joined at last

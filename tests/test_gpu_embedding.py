@@ -181,3 +181,44 @@ def test_calls_of_many_tokens(kind):
         if kind == "padded":
             tok[:, N // 3:] = -1
         run((B, N, V, d), "f32", tokens=tok, strided=strided, accumulate=kind == "even")
+
+
+FEW = [
+    # B, N, V, d: around the limit of tables of few values; teams of 8 to 64 lanes; several blocks of channels
+    (1, 1, 32, 5), (2, 75, 31, 4), (1, 3000, 32, 1030), (3, 1111, 4, 100), (1, 70000, 16, 33), (1, 9000, 5, 256), (2, 500, 33, 40),
+    (1, 40000, 2, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", FEW)
+def test_tables_of_few_values(case, dtype):
+    rng = np.random.default_rng(6)
+    run(case, dtype, tokens=rng.integers(0, case[2], case[:2]))
+    run(case, dtype, strided=True, bad=True, scale=-0.7)
+    run(case, dtype, accumulate=True, tokens=rng.integers(0, (case[2] + 1) // 2, case[:2]))
+
+
+def test_rows_without_tokens_keep_their_bits():
+    import torch
+    for V in (9, 300):
+        at = torch.tensor([[3, -1, 3, V]], dtype=torch.int32, device="cuda")
+        d_out = torch.ones((1, 4, 8), device="cuda")
+        old = torch.full((V, 8), -0.0, device="cuda")
+        old[0, 0] = float("nan")
+        bits = old.view(torch.int32).clone()
+        plan = hyena.Embedding(1, 4, V, 8, scale=-2.0)
+        plan.backward(d_out, at, d_table=old)
+        rows = torch.arange(V, device="cuda") != 3
+        assert torch.equal(old.view(torch.int32)[rows], bits[rows]) and bool((old[3] == -4).all())
+        new = plan.backward(d_out, at)
+        assert not new.view(torch.int32)[rows].any() and bool((new[3] == -4).all())
+
+
+@pytest.mark.parametrize("case", [(1, 3000, 1200000, 4), (2, 70001, 1200000, 4), (1, 900, 1600000, 4)])
+def test_tables_of_very_many_values(case):
+    rng = np.random.default_rng(4)
+    tok = rng.integers(0, case[2], case[:2])
+    tok[0, ::3] = case[2] - 1
+    tok[0, 1::7] = case[2] // 1024 * 1024 - 1
+    run(case, "f32", tokens=tok)
