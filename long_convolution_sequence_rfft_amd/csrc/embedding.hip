@@ -231,10 +231,13 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
         for (int b = b0; b < b1; ++b) {
             const int n = hi[b] - lo[b];
             const int2* list = p.dealt + (int64_t)b * kDealTokens + lo[b];
-            for (int k = 0; k < n; k += 64) {
-                const bool own = k + lane < n;
-                const int2 e = own ? list[k + lane] : make_int2(0, 0);
-                f(own, e.x, (int64_t)e.y);
+            for (int k0 = 0; k0 < n; k0 += 256) {
+                int2 e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) e[k] = k0 + 64 * k + lane < n ? list[k0 + 64 * k + lane] : make_int2(0, 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k0 + 64 * k < n) f(k0 + 64 * k + lane < n, e[k].x, (int64_t)e[k].y);
             }
         }
     };
@@ -247,11 +250,16 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
         }
         each_dealt([&](bool own, int v, int64_t t) {
             const int i = v >> shift;
-            if (own) {
-                atomicAdd(&counters[wave * values + i], 1);
-                if (n_own + lane < kSortKept) kept[wave][n_own + lane] = (uint32_t)i << kPlaceBits | (uint32_t)(t - first);
+            const uint64_t who = __ballot(own);
+            // (of one value all at once: 131072 tokens of one value 89 us so, 162 with an atomic of each lane)
+            int* to = &counters[wave * values + i];
+            if (__ballot(own && i != __builtin_amdgcn_readfirstlane(i)) == 0) {
+                if (own) *to += __popcll(who);  // every lane the same value
+            } else if (own) {
+                atomicAdd(to, 1);
             }
-            n_own += __popcll(__ballot(own));
+            if (own && n_own + lane < kSortKept) kept[wave][n_own + lane] = (uint32_t)i << kPlaceBits | (uint32_t)(t - first);
+            n_own += __popcll(who);
         });
     } else
     for (int64_t t0 = first; t0 < last; t0 += 64 * kSortTokens) {
