@@ -36,7 +36,7 @@ hyena_status loss_sizes(const hyena_token_loss* op)
 // Calls of at most this many tokens have their own kernels: forward, in 16 bits and in
 // float32 (whose table is read as given then), and backward.
 constexpr int32_t kFewGroups = 256;  // workgroups of 256 channels, backward
-constexpr int64_t kFewTokens = 32, kFewTokensF32 = 128, kFewTokensGrad = 4, kFewTokensGradF32 = 16;
+constexpr int64_t kFewTokens = 32, kFewTokensF32 = 64, kFewTokensGrad = 4, kFewTokensGradF32 = 16;
 // Others of more tokens than this bring the table into the matrix operands' form first.
 constexpr int64_t kPackTokens = 4096;
 

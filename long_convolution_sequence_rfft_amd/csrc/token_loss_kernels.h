@@ -369,17 +369,28 @@ __global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SM
 // next piece ahead of the products; the waves' sums are joined in LDS.  A table in float32
 // is read as given and becomes three terms in the registers.  Forward a workgroup keeps each
 // token's largest and sum; backward G stays float32, [values rounded up][16].
-template <typename T, int N, bool GRAD> __global__ __launch_bounds__(256) void hyena_loss_few(LossArgs p)
+//
+// OWN: there is no gather before it.  The call has at most 16 N tokens, in rows of whole
+// units, and each workgroup finds by itself which take part, while its first piece of the
+// table is under way, and reads their rows as given (8 tokens in bf16: OWN_A us so, 27
+// with a gather).
+template <typename T, int N, bool GRAD, bool OWN> __global__ __launch_bounds__(256) void hyena_loss_few(LossArgs p)
 {
     using E = typename LossType<T>::E;
     using frag = typename Mx<E>::frag;
     using Raw = std::conditional_t<LossType<T>::P == 3, f32x8, frag>;  // as loaded
     constexpr int P = LossType<T>::P, kPiece = P == 3 && N > 1 ? 3 : 6;        // steps of a piece
-    static_assert(!GRAD || N == 1, "");
+    static_assert(!GRAD || (N == 1 && !OWN), "");
+    static_assert(N <= 4, "");
     __shared__ f32x4 lds[2][4][N][64];
+    __shared__ int own_index[16 * N], own_target[16 * N];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
-    const int64_t count = *p.count, t0 = (int64_t)blockIdx.y * (16 * N);
-    if (t0 >= count) return;
+    const int64_t t0 = (int64_t)blockIdx.y * (16 * N);
+    int64_t count = 0;
+    if constexpr (!OWN) {
+        count = *p.count;
+        if (t0 >= count) return;
+    }
     const int tiles = (p.V + 15) / 16, steps = p.kd / 32, each = (steps + 3) / 4, pieces = (each + kPiece - 1) / kPiece;
     const int k0 = wave * each, k1 = k0 + each < steps ? k0 + each : steps;  // this wave's steps (none: k0 >= k1)
     const int64_t rows_block = p.tokens * 64, step_bytes = P == 3 ? 128 : p.values_block;
@@ -400,7 +411,30 @@ template <typename T, int N, bool GRAD> __global__ __launch_bounds__(256) void h
         }
     };
     frag b[kPiece][P][N];
+    const T* own_row[N];
     auto load_b = [&](int s) {
+        if constexpr (OWN) {
+#pragma unroll
+            for (int k = 0; k < kPiece; ++k)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int c = (s + k) * 32 + g * 8;
+                    if constexpr (P == 1) {
+                        Unit<T, true> u;
+                        u.load(own_row[j], c, p.d);
+                        b[k][0][j] = __builtin_bit_cast(frag, u.v);
+                    } else {
+                        Unit<T, true> lo, hi;
+                        lo.load(own_row[j], c, p.d);
+                        hi.load(own_row[j], c + 4, p.d);
+                        Split<E, P> x;
+                        x.set(join8(__builtin_bit_cast(f32x4, lo.v), __builtin_bit_cast(f32x4, hi.v)));
+#pragma unroll
+                        for (int n = 0; n < P; ++n) b[k][n][j] = x.f[n];
+                    }
+                }
+            return;
+        }
 #pragma unroll
         for (int n = 0; n < P; ++n) {
             const char* plane = p.rows + n * p.rows_plane;
@@ -462,7 +496,8 @@ template <typename T, int N, bool GRAD> __global__ __launch_bounds__(256) void h
 #pragma unroll
             for (int w = 1; w < 4; ++w) l += lds[half][w][j][lane];
             const int64_t t = t0 + 16 * j + i;
-            const int target = t < count ? p.target[t] - tile * 16 - 4 * g : -1;
+            int target = -1;
+            if (t < count) target = (OWN ? own_target[t] : p.target[t]) - tile * 16 - 4 * g;
             if constexpr (!GRAD) {
                 float m = -INFINITY, e = 0.0f;
 #pragma unroll
@@ -489,9 +524,32 @@ template <typename T, int N, bool GRAD> __global__ __launch_bounds__(256) void h
         half ^= 1;
         tile += gridDim.x;
     };
-    if (pieces == 1) load_b(k0);
     Raw a0[kPiece], a1[kPiece];
     ahead(a0);
+    if constexpr (OWN) {
+        const int target = lane < p.total ? *row_at<int32_t>(p.targets, lane, p.targets_N) : -1;
+        const bool in = (uint32_t)target < (uint32_t)p.V;
+        const uint64_t all = __ballot(in);
+        const int at = __popcll(all & (((uint64_t)1 << lane) - 1));
+        count = __popcll(all);
+        if (wave == 0) {
+            if (in) own_index[at] = lane, own_target[at] = target;
+            if (blockIdx.x == 0) {  // for the join
+                if (lane == 0) *p.count = count;
+                if (in) {
+                    p.index[at] = lane;
+                } else if (lane < p.total) {
+                    p.loss[lane] = 0.0f;
+                    p.lse[lane] = 0.0f;
+                }
+            }
+        }
+        if (count == 0) return;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < N; ++j) own_row[j] = row_at<T>(p.x, own_index[16 * j + i < count ? 16 * j + i : count - 1], p.x_N);
+    }
+    if (pieces == 1) load_b(k0);
     while (true) {
         if (tile >= tiles) break;
         ahead(a1);
@@ -931,14 +989,17 @@ template <typename T, bool GRAD> hyena_status loss_begin(const LossArgs& a, bool
     return launched();
 }
 
-template <typename T, int N, bool GRAD> hyena_status loss_few(const LossArgs& a, int tiles, hipStream_t s)
+template <typename T, int N, bool GRAD, bool OWN> hyena_status loss_few(const LossArgs& a, int tiles, hipStream_t s)
 {
     const dim3 grid((unsigned)tiles, (unsigned)((a.total + 16 * N - 1) / (16 * N)));
-    HY_LAUNCH(kernel_label("hyena_loss_few", type_label<T>(), N, GRAD), (hyena_loss_few<T, N, GRAD>), grid, dim3(256), 0, s, a);
+    HY_LAUNCH(kernel_label("hyena_loss_few", type_label<T>(), N, GRAD, OWN), (hyena_loss_few<T, N, GRAD, OWN>), grid, dim3(256), 0, s, a);
     return launched();
 }
 
-template <typename T, bool GRAD> hyena_status loss_logits(const LossArgs& a, int tiles, hipStream_t s)
+// Whether the logits' kernel of a forward pass finds the tokens by itself.
+template <typename T> bool finds_tokens(const LossArgs& a, bool units) { return a.few && units && a.total <= (LossType<T>::P == 1 ? 32 : 16); }
+
+template <typename T, bool GRAD> hyena_status loss_logits(const LossArgs& a, bool units, int tiles, hipStream_t s)
 {
     if (!a.few) {
         const int token_tiles = (int)(a.tokens / (a.small ? kSmallTile : kLossTokens));
@@ -949,14 +1010,18 @@ template <typename T, bool GRAD> hyena_status loss_logits(const LossArgs& a, int
             HY_LAUNCH(kernel_label("hyena_loss_logits", type_label<T>(), GRAD, false), (hyena_loss_logits<T, GRAD, false>), grid, dim3((LogitsTile<T, false>::kThreads)), 0, s, a, tiles);
         return launched();
     }
-    if constexpr (!GRAD) {
-        if constexpr (LossType<T>::P == 3) {
-            if (a.total > 64) return loss_few<T, 8, false>(a, tiles, s);
-            if (a.total > 32) return loss_few<T, 4, false>(a, tiles, s);
+    if constexpr (GRAD) {
+        return loss_few<T, 1, true, false>(a, tiles, s);
+    } else {
+        if (finds_tokens<T>(a, units)) {
+            if constexpr (LossType<T>::P == 1)
+                if (a.total > 16) return loss_few<T, 2, false, true>(a, tiles, s);
+            return loss_few<T, 1, false, true>(a, tiles, s);
         }
-        if (a.total > 16) return loss_few<T, 2, false>(a, tiles, s);
+        if constexpr (LossType<T>::P == 3)
+            if (a.total > 32) return loss_few<T, 4, false, false>(a, tiles, s);
+        return a.total > 16 ? loss_few<T, 2, false, false>(a, tiles, s) : loss_few<T, 1, false, false>(a, tiles, s);
     }
-    return loss_few<T, 1, GRAD>(a, tiles, s);
 }
 
 template <typename T, int N> hyena_status loss_few_grads(const LossArgs& a, hipStream_t s)
@@ -971,14 +1036,15 @@ template <typename T, int N> hyena_status loss_few_grads(const LossArgs& a, hipS
 
 template <typename T> hyena_status loss_forward(const LossArgs& a, bool pack, bool units, hipStream_t s)
 {
-    hyena_status st = loss_begin<T, false>(a, pack, units, s);
+    hyena_status st = HYENA_OK;
+    if (!finds_tokens<T>(a, units)) st = loss_begin<T, false>(a, pack, units, s);
     if (st != HYENA_OK) return st;
     LossArgs b = a;
     for (int64_t first = 0; first < a.V; first += a.chunk) {
         b.first = (int32_t)first;
         const bool last = first + a.chunk >= a.V;
         const int tiles = a.few ? few_groups(a.V) : loss_tiles(last ? a.V - first : a.chunk, a.small);
-        if ((st = loss_logits<T, false>(b, tiles, s)) != HYENA_OK) return st;
+        if ((st = loss_logits<T, false>(b, units, tiles, s)) != HYENA_OK) return st;
         if (tiles > 16)
             HY_LAUNCH(kernel_label("hyena_loss_join", type_label<T>(), 16), (hyena_loss_join<T, 16>), dim3((unsigned)((a.total + 15) / 16)), dim3(1024), 0, s, b, tiles, last);
         else
@@ -997,7 +1063,7 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
     for (int64_t first = 0; first < a.V; first += a.chunk) {
         b.first = (int32_t)first;
         const int values = a.V - first < a.chunk ? (int)(a.V - first) : a.chunk;
-        if ((st = loss_logits<T, true>(b, a.few ? few_groups(a.V) : loss_tiles(values, a.small), s)) != HYENA_OK) return st;
+        if ((st = loss_logits<T, true>(b, units, a.few ? few_groups(a.V) : loss_tiles(values, a.small), s)) != HYENA_OK) return st;
         if (a.few) {  // all of the vocabulary is one piece
             if ((st = a.total <= 4 ? loss_few_grads<T, 4>(a, s) : loss_few_grads<T, 16>(a, s)) != HYENA_OK) return st;
             break;
