@@ -123,7 +123,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     a.acc_row = (int32_t)((a.d + 3) / 4 * 4);
     if (a.few) {
         a.chunk = a.V;
-        a.g = take((size_t)((a.V + 15) / 16) * 16 * 16 * 4);
+        a.g = take((size_t)((a.V + 15) / 16 * 16 + 3) * 16 * 4);  // (read four values at a time)
         a.splits = kFewGroups;
         a.acc = (float*)take((size_t)a.splits * tokens * (size_t)a.acc_row * 4);
         return at;

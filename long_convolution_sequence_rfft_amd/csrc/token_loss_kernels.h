@@ -372,7 +372,7 @@ __global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SM
 //
 // OWN: there is no gather before it.  The call has at most 16 N tokens, in rows of whole
 // units, and each workgroup finds by itself which take part, while its first piece of the
-// table is under way, and reads their rows as given (8 tokens in bf16: OWN_A us so, 27
+// table is under way, and reads their rows as given (8 tokens in bf16: 21 us so, 28
 // with a gather).
 template <typename T, int N, bool GRAD, bool OWN> __global__ __launch_bounds__(256) void hyena_loss_few(LossArgs p)
 {
@@ -1065,7 +1065,11 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
         const int values = a.V - first < a.chunk ? (int)(a.V - first) : a.chunk;
         if ((st = loss_logits<T, true>(b, units, a.few ? few_groups(a.V) : loss_tiles(values, a.small), s)) != HYENA_OK) return st;
         if (a.few) {  // all of the vocabulary is one piece
-            if ((st = a.total <= 4 ? loss_few_grads<T, 4>(a, s) : loss_few_grads<T, 16>(a, s)) != HYENA_OK) return st;
+            if (a.total <= 4) st = loss_few_grads<T, 4>(a, s);
+            if constexpr (LossType<T>::P == 3) {
+                if (a.total > 4) st = a.total <= 8 ? loss_few_grads<T, 8>(a, s) : loss_few_grads<T, 16>(a, s);
+            }
+            if (st != HYENA_OK) return st;
             break;
         }
         const int64_t table_tiles = a.d_table ? dealt(channel_tiles, (int64_t)((values + kGradRows - 1) / kGradRows) * a.table_splits) : 0;
