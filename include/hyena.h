@@ -519,9 +519,9 @@ typedef struct hyena_rows {
 /*
  * Embedding: out[b][n] = scale * table[tokens[b][n]], rounded once, and the
  * table's gradient d_table[v] = scale * sum of d_out[b][n] over the tokens that
- * are v, summed in float32 in the tokens' order and rounded once.  A token
- * outside 0..V-1 takes no part: its row of out is zeros, its row of d_out is not
- * read.
+ * are v, summed in float32, in an order that only the call's sizes and tokens decide,
+ * and rounded once.  A token outside 0..V-1 takes no part: its row of out is zeros,
+ * its row of d_out is not read.
  *
  * table, out and d_table are dense, [V][d] and [B][N][d], in the io dtype, aligned
  * to their element.  B * N at most 2^30, V at most 2^24, d at most 65536.
@@ -561,6 +561,10 @@ hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_row
  * channels (d a multiple of it), or a whole row (group 0).  E4M3 is the form with
  * 448 as its largest value and no infinities.  A group whose largest is below
  * 2^-100 is zeros with the scale 0; one that holds a NaN has a NaN scale.
+ *
+ * A row has a norm where the sum of its squares is a float32 number and, with eps, is
+ * not 0: a row of zeros with eps = 0 gives NaN (its gradient, too), and one whose squares
+ * sum past float32's largest number zeros.
  *
  * s (if there is a residual) and y are dense [B][N][d], scales [B][N][d / group]
  * (group 0: [B][N][1]).  d at most 16384, B * N at most 2^31 - 1.
@@ -618,11 +622,12 @@ hyena_status hyena_residual_norm_backward(const hyena_residual_norm* op, const h
  * Precision.  Products of 16-bit operands are accumulated in float32, in float32
  * storage each operand is three bfloat16 terms (24 bits) and the six largest of their
  * nine products are summed; lse and loss are float32.  With 16-bit storage the
- * gradients pass through G rounded to that type; in binary16 G is divided by the
- * largest |d_loss| first and kept times 2^15, so that probabilities down to
+ * gradients of more than 4 tokens pass through G rounded to that type, but at the target,
+ * which is most of G, what its rounding takes is added to both gradients; in binary16 G is
+ * divided by the largest |d_loss| first and kept times 2^15, so that probabilities down to
  * 2^-29 keep all its bits.  In float32 storage x, table and scale must be such that the logits and
  * all values are finite; elsewhere too an infinity or a NaN in the table reaches
- * every token, one in x its own token and d_table.
+ * every token, one in x its own token and d_table.  d_loss must be finite.
  *
  * The table is dense [V][d] and 16-byte aligned, as are d_x ([B][N][d]) and
  * d_table ([V][d]), all in the io dtype.  x, targets and d_loss are views.  d and V

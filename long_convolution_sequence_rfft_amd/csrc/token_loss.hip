@@ -144,7 +144,8 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     a.splits = (int32_t)splits;
     a.acc = (float*)take((size_t)splits * tokens * (size_t)a.acc_row * 4);
     // d_table's over the tokens, where one of them would take longer than that
-    const int64_t table_splits = (table_steps + share - 1) / share, table_most = table_steps / kTableSteps;
+    const int64_t part = planes == 3 ? 2 * share : share;  // (float32: a compute unit holds one workgroup, not two)
+    const int64_t table_splits = (table_steps + part - 1) / part, table_most = table_steps / kTableSteps;
     a.table_splits = (int32_t)(table_splits <= 1 || table_most <= 1 ? 1 : table_splits < table_most ? table_splits : table_most);
     a.table_acc = (float*)take(a.table_splits == 1 ? 0 : (size_t)a.table_splits * (size_t)a.chunk * (size_t)a.acc_row * 4);
     return at;

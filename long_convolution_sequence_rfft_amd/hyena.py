@@ -135,6 +135,7 @@ class TokenLossOp(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("x", Rows),
                 ("table", ctypes.c_void_p), ("targets", Rows)]
 
+
 _lock = threading.Lock()
 _lib = None
 
