@@ -35,8 +35,9 @@ hyena_status loss_sizes(const hyena_token_loss* op)
 
 // Calls of at most this many tokens have their own kernels: forward, in 16 bits and in
 // float32 (whose table is read as given then), and backward.
-constexpr int32_t kFewGroups = 256;  // workgroups of 256 channels, backward
 constexpr int64_t kFewTokens = 32, kFewTokensF32 = 64, kFewTokensGrad = 4, kFewTokensGradF32 = 16;
+// Workgroups of 256 channels, backward.
+constexpr int32_t kFewGroups = 512, kFewGroupsF32 = 256;
 // Others of more tokens than this bring the table into the matrix operands' form first.
 constexpr int64_t kPackTokens = 4096;
 
@@ -124,7 +125,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     if (a.few) {
         a.chunk = a.V;
         a.g = take((size_t)((a.V + 15) / 16 * 16 + 3) * 16 * 4);  // (read four values at a time)
-        a.splits = kFewGroups;
+        a.splits = planes == 3 ? kFewGroupsF32 : kFewGroups;
         a.acc = (float*)take((size_t)a.splits * tokens * (size_t)a.acc_row * 4);
         return at;
     }

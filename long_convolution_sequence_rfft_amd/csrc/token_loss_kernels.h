@@ -939,32 +939,29 @@ template <typename T, int kTokens> __global__ __launch_bounds__(256) void hyena_
     }
 }
 
-// The same by 16 waves for each token: few tokens have many sums.
+// The same by 16 waves for each token and 256 channels: few tokens have many sums.
 template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_finish_few(LossArgs p)
 {
     __shared__ f32x4 lds[16][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = (int)blockIdx.y * 256 + lane * 4;
     const float down = p.few ? p.scale : p.norm[1];
     for (int64_t t = blockIdx.x; t < p.total; t += gridDim.x) {
         const int32_t a = p.place[t];
-        for (int c0 = 0; c0 < p.d; c0 += 256) {
-            const int c = c0 + lane * 4;
-            f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (a >= 0 && c < p.d) {
-                const float* from = p.acc + (int64_t)a * p.acc_row + c;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (a >= 0 && c < p.d) {
+            const float* from = p.acc + (int64_t)a * p.acc_row + c;
 #pragma unroll 4
-                for (int s = wave; s < p.splits; s += 16) x += *(const f32x4*)(from + (int64_t)s * p.tokens * p.acc_row);
-            }
-            lds[wave][lane] = x;
-            __syncthreads();
-            if (wave == 0 && c < p.d) {
-#pragma unroll
-                for (int w = 1; w < 16; ++w) x += lds[w][lane];
-                if (LossType<T>::P == 1 && a >= 0 && !p.few) x += target_rest<T>(p, p.target[a], p.hit[a], c);
-                store_dx<T>(p, t, c, x * down);
-            }
-            __syncthreads();
+            for (int s = wave; s < p.splits; s += 16) x += *(const f32x4*)(from + (int64_t)s * p.tokens * p.acc_row);
         }
+        lds[wave][lane] = x;
+        __syncthreads();
+        if (wave == 0 && c < p.d) {
+#pragma unroll
+            for (int w = 1; w < 16; ++w) x += lds[w][lane];
+            if (LossType<T>::P == 1 && a >= 0 && !p.few) x += target_rest<T>(p, p.target[a], p.hit[a], c);
+            store_dx<T>(p, t, c, x * down);
+        }
+        __syncthreads();
     }
 }
 
@@ -1066,9 +1063,7 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
         if ((st = loss_logits<T, true>(b, units, a.few ? few_groups(a.V) : loss_tiles(values, a.small), s)) != HYENA_OK) return st;
         if (a.few) {  // all of the vocabulary is one piece
             if (a.total <= 4) st = loss_few_grads<T, 4>(a, s);
-            if constexpr (LossType<T>::P == 3) {
-                if (a.total > 4) st = a.total <= 8 ? loss_few_grads<T, 8>(a, s) : loss_few_grads<T, 16>(a, s);
-            }
+            else if constexpr (LossType<T>::P == 3) st = a.total <= 8 ? loss_few_grads<T, 8>(a, s) : loss_few_grads<T, 16>(a, s);
             if (st != HYENA_OK) return st;
             break;
         }
@@ -1091,7 +1086,7 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
     else if (a.splits <= 8)
         HY_LAUNCH(kernel_label("hyena_loss_finish", type_label<T>(), 4), (hyena_loss_finish<T, 4>), grid, dim3(256), 0, s, a);
     else
-        HY_LAUNCH(kernel_label("hyena_loss_finish_few", type_label<T>()), hyena_loss_finish_few<T>, grid, dim3(1024), 0, s, a);
+        HY_LAUNCH(kernel_label("hyena_loss_finish_few", type_label<T>()), hyena_loss_finish_few<T>, dim3(grid.x, (unsigned)((a.d + 255) / 256)), dim3(1024), 0, s, a);
     return launched();
 }
 
