@@ -579,7 +579,8 @@ template <typename T, int N, bool GRAD, bool OWN> __global__ __launch_bounds__(2
 // Gradients of at most N tokens: a wave takes the values of its part one after the
 // other, 256 channels of them, adds their share to d_x and makes their rows of d_table.
 // Bound by reading and writing the two tables (8 tokens in float32: 65 us for 309 MB); G of a
-// value is the same for all lanes.
+// value is the same for all lanes.  d_table goes past the caches, which leaves the table there
+// for the next call's logits (4 tokens in float32, a call: 115 us through them, 108 so).
 template <typename T, int N, bool UNITS> __global__ __launch_bounds__(256) void hyena_loss_few_grads(LossArgs p)
 {
     __shared__ f32x4 lds[3][N][64];
@@ -635,7 +636,7 @@ template <typename T, int N, bool UNITS> __global__ __launch_bounds__(256) void 
             dw *= p.scale;
             T* to = (T*)p.d_table + (int64_t)v * p.d + c;
             if (UNITS) {
-                if (c < p.d) *(typename Mx<T>::vec4*)to = Mx<T>::narrow(dw);
+                if (c < p.d) __builtin_nontemporal_store(Mx<T>::narrow(dw), (typename Mx<T>::vec4*)to);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
