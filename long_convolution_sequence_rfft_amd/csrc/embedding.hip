@@ -2,7 +2,7 @@
 // gradient by sorted tokens (include/hyena.h).
 //
 // Forward is a gather: 4 bytes of a token, then its row, read and written once (16384 tokens of
-// width 768 in bf16 8.4 us, the table's rows mostly from the last-level cache; 32 tokens 3.0).
+// width 768 in bf16 8.4 us, the table's rows mostly from the last-level cache; 32 tokens 3.2).
 //
 // Backward.  Sums in an order that atomics decide would differ from call to call,
 // so tokens are sorted first, in their order within each value:
@@ -25,9 +25,9 @@
 // hyena_embedding_few_join adds up (2^18 tokens, 16 values, width 256: 64 us so, 130 sorted;
 // 2^20 tokens, 4 values, width 64: 63 and 899).
 // Bound by memory: each gradient row is read once, each row of the table written
-// once.  8192 tokens of 31999 values, width 770 in float32: sort 8.6, sums 19.8 (125 MB, most
-// of it zeros), joins 5.2 us.  65536 tokens of a text of 50257 values, width 768 in bf16, added to a
-// gradient: 20.0, 40.2 (164 MB), 13.2 us; the sort is bound by all groups reading all tokens from
+// once.  8192 tokens of 31999 values, width 770 in float32: sort 8.3, sums 26.6 (119 MB, most
+// of it zeros), joins 5.3 us.  65536 tokens of a text of 50257 values, width 768 in bf16, added to a
+// gradient: 19.7, 37.6 (162 MB), 13.3 us; the sort is bound by all groups reading all tokens from
 // the L2, the joins by the few values that are in most runs.
 #include "rows.h"
 

@@ -11,12 +11,12 @@
 //   hyena_loss_table    d_table of a piece from its sums, where the tokens are cut
 //   hyena_loss_finish   d_x from its sums (hyena_loss_finish_few where they are many)
 // Bound by the matrix instructions, 2 tokens V d operations forward, 6 backward, and these by the
-// power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1106 us, 1143 TFLOP/s (the
-// matrix units are busy for 66% of the cycles, of 1.65 GHz; a large product of the
-// library's reaches 1279, this one 953).  12288 of them backward: logits 908 us (1045 TFLOP/s; they
-// write G, 1.2 GB), products 1912 us (992; of two products of the library's 944 and 822; the
-// matrix units are busy for 53% of the cycles, of 1.79 GHz).  2048 tokens, 31999 values in float32, whose six
-// products are counted: 522 us (1157) and 1003 us (1205).
+// power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1073 us, 1179 TFLOP/s (the
+// matrix units are busy for 66% of the cycles, of 1.70 GHz; a large product of the
+// library's reaches 1279, this one 953).  12288 of them backward: logits 896 us (1058 TFLOP/s; they
+// write G, 1.2 GB), products 1885 us (1007; of two products of the library's 944 and 822; the
+// matrix units are busy for 53% of the cycles, of 1.82 GHz).  2048 tokens, 31999 values in float32, whose six
+// products are counted: 506 us (1194) and 975 us (1239).
 #pragma once
 
 #include "matmul_device.h"
@@ -369,7 +369,7 @@ __global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SM
 }
 
 // Logits of few tokens, 16 N of them: bound by reading the table once (8 tokens of width 768 in bf16,
-// 50257 values: 16.8 us for 77 MB).  Workgroups take
+// 50257 values: 16.5 us for 77 MB).  Workgroups take
 // tiles of 16 values in turn, so that all of them together read one piece of the table after
 // the other (a part of the table for each workgroup was a third slower); within a tile each
 // wave has a quarter of the channels.  The operands go from memory to the registers, the
