@@ -46,8 +46,8 @@ struct Operand {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t operand_rsrc(const char* at, const char* end)
 {
     const int64_t left = end - at;
-    const int n = left <= 0 ? 0 : left < 0x7fffffff ? (int)left : 0x7fffffff;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), (short)0, n, 0x00020000);
+    const uint32_t n = left <= 0 ? 0u : left < 0xffffff00 ? (uint32_t)left : 0xffffff00u;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), (short)0, (int)n, 0x00020000);
 }
 
 // 16 bytes of each lane to LDS, side by side from byte `lds` on.  The compiler does
@@ -100,7 +100,7 @@ template <int W, int THREADS, Form F> struct Stage {
     }
     // k in the rows: the row of this thread's loads in a step, and loads of any row there (at
     // kNoRow zeros).
-    static constexpr uint32_t kNoRow = 0x7ffffff0;
+    static constexpr uint32_t kNoRow = 0xfffffff0;
     static __device__ __forceinline__ int row_of_step() { return (int)(threadIdx.x >> 2) & 31; }
     __device__ __forceinline__ void init_rows(const Operand& o, uint32_t row_bytes)
     {

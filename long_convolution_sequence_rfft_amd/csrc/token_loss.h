@@ -47,6 +47,7 @@ struct LossArgs {
     float* weight;         // [tokens] d_loss
     float* lse2;           // [tokens] lse / ln 2
     char* rows;            // gathered x: [planes][kd / 32][tokens rounded up][32], 16-bit
+    int64_t block;         // bytes from 32 channels (values) of rows (g) to the next
     int64_t rows_plane;    // bytes
     const char* values;    // the table as matrix operand: itself, or [planes][kd / 32][V][32]
     int64_t values_row, values_block, values_plane, values_bytes;  // bytes: of a row, 32 channels, a plane; the first plane's

@@ -126,7 +126,7 @@ template <typename T, bool UNITS, bool GRAD> __global__ __launch_bounds__(1024) 
             for (int k = 0; k < kRows; ++k)
 #pragma unroll
                 for (int h = 0; h < kUnits; ++h) u[k][h].load(x[k], c + h * kUnit<T>, p.d);
-            char* to = p.rows + (c >> 5) * p.tokens * 64 + (c & 31) * 2;
+            char* to = p.rows + (c >> 5) * p.block + (c & 31) * 2;
 #pragma unroll
             for (int k = 0; k < kRows; ++k) {
                 if (a0 + k * teams >= before) break;
@@ -148,7 +148,7 @@ template <typename T, bool UNITS, bool GRAD> __global__ __launch_bounds__(1024) 
         const f32x8 none = {};
         for (int64_t a = before + team; a < (before + 31) / 32 * 32; a += teams)
             for (int c = tl * 8; c < p.kd; c += lanes * 8)
-                store_planes<E, P>(p.rows + a * 64 + (c >> 5) * p.tokens * 64 + (c & 31) * 2, p.rows_plane, none);
+                store_planes<E, P>(p.rows + a * 64 + (c >> 5) * p.block + (c & 31) * 2, p.rows_plane, none);
     }
     if constexpr (GRAD) {
         // binary16 holds G over the power of two above the largest |d_loss|, times 2^15
@@ -265,7 +265,7 @@ __global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SM
     const int32_t v0 = p.first + value_tile * TM;
     Tile tile;
     const Operand values{p.values + (int64_t)v0 * p.values_row, p.values + p.values_bytes, p.values_row, p.values_block};
-    const Operand rows{p.rows + t0 * 64, p.rows + p.rows_plane, 64, p.tokens * 64};
+    const Operand rows{p.rows + t0 * 64, p.rows + p.rows_plane, 64, p.block};
     tile.run(lds, values, p.values_plane, rows, p.rows_plane, p.kd / 32);
 
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4;
@@ -360,10 +360,10 @@ __global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SM
                         }
                 if (P == 1 && (uint32_t)target < (uint32_t)(TM / WM) && (target & 31) < 8) p.hit[t] = off;
             }
-            char* to = p.g + (int64_t)((value_tile * TM + wm * (TM / WM)) >> 5) * p.tokens * 64 + t * 64 + g * 16;
+            char* to = p.g + (int64_t)((value_tile * TM + wm * (TM / WM)) >> 5) * p.block + t * 64 + g * 16;
 #pragma unroll
             for (int i = 0; i < Tile::MI; i += 2)
-                store_planes<E, P>(to + (int64_t)(i >> 1) * p.tokens * 64, p.g_plane, join8(tile.c[i][j], tile.c[i + 1][j]));
+                store_planes<E, P>(to + (int64_t)(i >> 1) * p.block, p.g_plane, join8(tile.c[i][j], tile.c[i + 1][j]));
         }
     }
 }
@@ -400,7 +400,7 @@ template <typename T, int N, bool GRAD, bool OWN> __global__ __launch_bounds__(2
     }
     const int tiles = (p.V + 15) / 16, steps = p.kd / 32, each = (steps + 3) / 4, pieces = (each + kPiece - 1) / kPiece;
     const int k0 = wave * each, k1 = k0 + each < steps ? k0 + each : steps;  // this wave's steps (none: k0 >= k1)
-    const int64_t rows_block = p.tokens * 64, step_bytes = P == 3 ? 128 : p.values_block;
+    const int64_t rows_block = p.block, step_bytes = P == 3 ? 128 : p.values_block;
     const uint32_t aoff = (uint32_t)i * (uint32_t)p.values_row + g * (P == 3 ? 32 : 16), boff = i * 64 + g * 16;
     const char* end = p.values + p.values_bytes;
     auto load_a = [&](int tile, int s, Raw (&a)[kPiece]) {
@@ -791,8 +791,8 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
         const int k0 = split * per, k1 = k0 + per < steps ? k0 + per : steps;
         Table tile;
         if (k0 < k1) {
-            Operand x{p.rows + (int64_t)(c0 >> 5) * p.tokens * 64, p.rows + p.rows_plane, 64, p.tokens * 64};
-            const Operand y{p.g + (int64_t)(v0 >> 5) * p.tokens * 64 + (int64_t)k0 * 2048, p.g + p.g_plane, 64, p.tokens * 64};
+            Operand x{p.rows + (int64_t)(c0 >> 5) * p.block, p.rows + p.rows_plane, 64, p.block};
+            const Operand y{p.g + (int64_t)(v0 >> 5) * p.block + (int64_t)k0 * 2048, p.g + p.g_plane, 64, p.block};
             x.at += (int64_t)k0 * 2048;
             tile.run(lds, x, p.rows_plane, y, p.g_plane, k1 - k0);
             x.at -= (int64_t)k0 * 2048;
@@ -837,7 +837,7 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
     if (k0 < k1) {
         const Operand x{p.values + (int64_t)(p.first + 32 * k0) * p.values_row + (int64_t)(c0 >> 5) * p.values_block,
                         p.values + p.values_bytes, p.values_row, p.values_block};
-        const Operand y{p.g + (int64_t)k0 * p.tokens * 64 + t0 * 64, p.g + p.g_plane, 64, p.tokens * 64};
+        const Operand y{p.g + (int64_t)k0 * p.block + t0 * 64, p.g + p.g_plane, 64, p.block};
         tile.run(lds, x, p.values_plane, y, p.g_plane, k1 - k0);
     } else {
         tile.clear();

@@ -407,3 +407,45 @@ def test_gradient_of_a_row_that_all_tokens_have_as_target(case, dtype):
     bound = u * np.abs(ref) + (dg + (N + 16) * 2.0 ** -24 * np.abs(g)) @ np.abs(xs)
     assert np.all((1.95 * u - 2 * u * u) * np.abs(ref) > bound)  # (the error of one rounding more would show)
     compare(dt[row], ref, bound, "d_table of the target")
+
+
+def test_as_many_tokens_as_there_may_be():
+    # 2^22 tokens: offsets within a tile's blocks pass 2^31.  The last ones have targets, and a few
+    # before them; against products in float64 on the GPU
+    import torch
+    T, V, d = 1 << 22, 300, 256
+    say("[gpu] token_loss of 2^22 tokens")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((1, T, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    table = (torch.randn((V, d), generator=gen, device="cuda") * 0.1).bfloat16()
+    target = torch.randint(0, V, (1, T), generator=gen, device="cuda", dtype=torch.int32)
+    target[0, 1000] = -1
+    target[0, 5000:5900] = V
+    d_loss = torch.full((1, 1), 0.77, device="cuda").expand(1, T)
+    plan = hyena.TokenLoss(1, T, V, d, io_dtype=hyena.HYENA_BF16)
+    loss, lse = plan.forward(x, table, target)
+    dx, dt = plan.backward(d_loss, x, table, target, lse)
+    w = table.double()
+    wt = w.t().contiguous()
+    sums = torch.zeros((V, d), dtype=torch.float64, device="cuda")
+    u = ends_ref.HALF_STEP["bf16"]
+    for a in range(0, T, 1 << 17):
+        rows = slice(a, a + (1 << 17))
+        xs, t = x[0, rows].double(), target[0, rows].long()
+        live = (t >= 0) & (t < V)
+        l = xs @ wt
+        ref = torch.where(live, torch.logsumexp(l, -1), 0)
+        assert float((lse[0, rows] - ref).abs().max()) < 2e-4
+        g = torch.exp(l - lse[0, rows, None].double())
+        hit = t.clamp(0, V - 1)
+        assert float((loss[0, rows] - torch.where(live, ref - l.gather(1, hit[:, None])[:, 0], 0)).abs().max()) < 4e-4
+        g[torch.arange(len(t), device="cuda"), hit] -= 1
+        g = torch.where(live[:, None], 0.77 * g, 0)
+        sums += g.t().contiguous() @ xs
+        want = g @ w
+        # every element of G rounded, and the result; 0.77 * 2e-4 of every probability's error in lse
+        off = (dx[0, rows].double() - want).abs() - u * want.abs() - (u + 2e-4) * (g.abs() @ w.abs())
+        assert float(off.max()) <= 2.0 ** -20
+    off = float(torch.linalg.vector_norm(dt.double() - sums) / torch.linalg.vector_norm(sums))
+    say(f"[gpu]   error norm of d_table {off:.3g}")
+    assert off < 2 * u  # the norm of the errors: half a step of G and half a step of the result
