@@ -62,6 +62,7 @@ struct LossArgs {
     int32_t chunk;         // values of a piece of the vocabulary
     int32_t first;         // of this piece
     int32_t splits;        // of the sum over a piece's values, for d_x
+    int32_t direct;        // one piece, one part: d_x is not summed up but written
     int32_t table_splits;  // of the sum over the tokens, for d_table
     float* table_acc;      // [table_splits][chunk][acc_row] d_table of a piece, where there is more than one
 };

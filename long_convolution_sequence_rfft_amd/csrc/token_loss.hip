@@ -159,12 +159,10 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     const int64_t most = a.chunk / 512 < 1 ? 1 : a.chunk / 512;  // a part has 512 values at least
     const int64_t cap = a.tokens <= 1024 ? 64 : 16;
     splits = splits < 1 ? 1 : splits > most ? most : splits > cap ? cap : splits;
-    // a power of two, so that an XCD has workgroups of one part (or few), which share its piece of the
-    // table (16384 tokens: 3 parts read 4.1 GB for a piece of G, 4 2.4; the time is the same)
-    for (int64_t p2 = 1; p2 < 2 * splits; p2 *= 2)
-        if (p2 >= splits && p2 <= most) splits = p2;
     a.splits = (int32_t)splits;
-    a.acc = (float*)take((size_t)splits * tokens * (size_t)a.acc_row * 4);
+    // (2^18 tokens, 16 values, width 256: 345 us so, 457 through a sum)
+    a.direct = splits == 1 && a.chunk >= a.V;
+    a.acc = (float*)take(a.direct ? 0 : (size_t)splits * tokens * (size_t)a.acc_row * 4);
     // d_table's over the tokens, where one of them would take longer than that
     const int64_t part = planes == 3 ? 2 * share : share;  // (float32: a compute unit holds one workgroup, not two)
     const int64_t table_splits = (table_steps + part - 1) / part, table_most = table_steps / kTableSteps;

@@ -10,6 +10,7 @@
 //   hyena_loss_products d_table of a piece of the vocabulary, and its share of d_x
 //   hyena_loss_table    d_table of a piece from its sums, where the tokens are cut
 //   hyena_loss_finish   d_x from its sums (hyena_loss_finish_few where they are many)
+//   hyena_loss_zeros    zeros for the other tokens, where the products write d_x themselves
 // Bound by the matrix instructions, 2 tokens V d operations forward, 6 backward, and these by the
 // power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1073 us, 1179 TFLOP/s (the
 // matrix units are busy for 66% of the cycles, of 1.70 GHz; a large product of the
@@ -763,6 +764,36 @@ __device__ __forceinline__ void add_rests(Tile& tile, char* lds, const LossArgs&
     }
 }
 
+// 4 channels of d_x of a token, x their sum.
+template <typename T> __device__ __forceinline__ void store_dx(const LossArgs& p, int64_t t, int c, f32x4 x)
+{
+    T* to = (T*)p.d_x + t * p.d + c;
+    if (p.d % 4 == 0) {
+        *(typename Mx<T>::vec4*)to = Mx<T>::narrow(x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < p.d) store_one<T>(to + e, x[e]);
+    }
+}
+
+// The rest of G at the target times its row of the table.
+template <typename T> __device__ __forceinline__ f32x4 target_rest(const LossArgs& p, int target, float rest, int c)
+{
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (LossType<T>::P == 1) {
+        const T* w = (const T*)p.table + (int64_t)target * p.d + c;
+        if (p.d % 4 == 0) {
+            x = Mx<T>::widen(*(const typename Mx<T>::vec4*)w) * rest;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.d) x[e] = rest * load_one<T>(w + e);
+        }
+    }
+    return x;
+}
+
 // One launch, so that neither product waits for the other's last workgroups.  Tiles of 256
 // channels by 128 rows and two workgroups a compute unit: three of fewer registers spill 22 and
 // take twice as long, tiles of 256 by 256 in one workgroup 2072 us instead of 1905.
@@ -770,7 +801,7 @@ __device__ __forceinline__ void add_rests(Tile& tile, char* lds, const LossArgs&
 // The first table_groups workgroups: d_table of kGradRows values of this piece and
 // kGradChannels channels, the sum over one of p.table_splits parts of the tokens.  The
 // others, shorter ones: a share of d_x of kGradRows tokens, the sum over one of p.splits
-// parts of the piece's values.
+// parts of the piece's values; or (p.direct) all of it, as d_x itself.
 template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) void hyena_loss_products(LossArgs p, int table_groups, int channel_tiles)
 {
     using E = typename LossType<T>::E;
@@ -842,6 +873,24 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
     } else {
         tile.clear();
     }
+    if (p.direct) {
+        const float down = p.norm[1];
+#pragma unroll
+        for (int j = 0; j < Dx::NI; ++j) {
+            const int64_t a = t0 + wn * (kGradRows / WN) + 16 * j + (lane & 15);
+            if (a >= count) continue;
+            const int32_t t = p.index[a];
+            int target = 0;
+            float rest = 0.0f;
+            if constexpr (P == 1) target = p.target[a], rest = p.hit[a];
+#pragma unroll
+            for (int i = 0; i < Dx::MI; ++i) {
+                const int c = c0 + wm * (kGradChannels / WM) + 16 * i + 4 * g;
+                if (c < p.d) store_dx<T>(p, t, c, (tile.c[i][j] + target_rest<T>(p, target, rest, c)) * down);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < Dx::NI; ++j) {
         const int64_t t = t0 + wn * (kGradRows / WN) + 16 * j + (lane & 15);
@@ -885,36 +934,6 @@ template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_table(L
     }
 }
 
-// 4 channels of d_x of a token, x their sum.
-template <typename T> __device__ __forceinline__ void store_dx(const LossArgs& p, int64_t t, int c, f32x4 x)
-{
-    T* to = (T*)p.d_x + t * p.d + c;
-    if (p.d % 4 == 0) {
-        *(typename Mx<T>::vec4*)to = Mx<T>::narrow(x);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < p.d) store_one<T>(to + e, x[e]);
-    }
-}
-
-// The rest of G at the target times its row of the table.
-template <typename T> __device__ __forceinline__ f32x4 target_rest(const LossArgs& p, int target, float rest, int c)
-{
-    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (LossType<T>::P == 1) {
-        const T* w = (const T*)p.table + (int64_t)target * p.d + c;
-        if (p.d % 4 == 0) {
-            x = Mx<T>::widen(*(const typename Mx<T>::vec4*)w) * rest;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < p.d) x[e] = rest * load_one<T>(w + e);
-        }
-    }
-    return x;
-}
-
 // d_x of tokens from their sums, a wave for kTokens tokens.
 template <typename T, int kTokens> __global__ __launch_bounds__(256) void hyena_loss_finish(LossArgs p)
 {
@@ -952,7 +971,18 @@ template <typename T, int kTokens> __global__ __launch_bounds__(256) void hyena_
     }
 }
 
-// The same by 16 waves for each token and 256 channels: few tokens have many sums.
+// Zeros for d_x of the tokens that take no part, where the others' is written directly.
+template <typename T> __global__ __launch_bounds__(256) void hyena_loss_zeros(LossArgs p)
+{
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 64; t0 < p.total; t0 += (int64_t)gridDim.x * 256) {
+        uint64_t none = __ballot(t0 + lane < p.total && p.place[t0 + lane] < 0);
+        for (; none != 0; none &= none - 1)
+            for (int c = lane * 4; c < p.d; c += 256) store_dx<T>(p, t0 + __builtin_ctzll(none), c, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+    }
+}
+
+// d_x by 16 waves for each token and 256 channels: few tokens have many sums.
 template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_finish_few(LossArgs p)
 {
     __shared__ f32x4 lds[16][64];
@@ -1092,6 +1122,11 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
         if ((st = launched()) != HYENA_OK) return st;
     }
     if (a.d_x == nullptr) return HYENA_OK;
+    if (a.direct) {
+        const int64_t groups = (a.total + 255) / 256;
+        HY_LAUNCH(kernel_label("hyena_loss_zeros", type_label<T>()), hyena_loss_zeros<T>, dim3((unsigned)(groups < 4096 ? groups : 4096)), dim3(256), 0, s, a);
+        return launched();
+    }
     const int tokens = a.total < kFinishTokens ? 1 : 4;  // of a wave
     const int64_t need = a.splits <= 8 ? (a.total + 4 * tokens - 1) / (4 * tokens) : a.total;
     const dim3 grid((unsigned)(need < 4096 ? need : 4096));
