@@ -12,12 +12,12 @@
 //   hyena_loss_finish   d_x from its sums (hyena_loss_finish_few where they are many)
 //   hyena_loss_zeros    zeros for the other tokens, where the products write d_x themselves
 // Bound by the matrix instructions, 2 tokens V d operations forward, 6 backward, and these by the
-// power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1073 us, 1179 TFLOP/s (the
+// power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1079 us, 1172 TFLOP/s (the
 // matrix units are busy for 66% of the cycles, of 1.70 GHz; a large product of the
-// library's reaches 1279, this one 953).  12288 of them backward: logits 896 us (1058 TFLOP/s; they
-// write G, 1.2 GB), products 1885 us (1007; of two products of the library's 944 and 822; the
+// library's reaches 1279, this one 953).  12288 of them backward: logits 882 us (1076 TFLOP/s; they
+// write G, 1.2 GB), products 1882 us (1008; of two products of the library's 944 and 822; the
 // matrix units are busy for 53% of the cycles, of 1.82 GHz).  2048 tokens, 31999 values in float32, whose six
-// products are counted: 506 us (1194) and 975 us (1239).
+// products are counted: 506 us (1193) and 968 us (1248).
 #pragma once
 
 #include "matmul_device.h"
