@@ -19,7 +19,9 @@
 //       value that lies within one run is done: its row is written.  One that
 //       reaches over a run's end leaves its sum there.  Other workgroups of the
 //       same launch write the zeros of values without tokens.
-//   hyena_embedding_joins  adds the pieces of values that reach over runs.
+//       The runs of a workgroup that is all one value's leave one sum.
+//   hyena_embedding_joins  adds the pieces of values that reach over runs (65536 tokens of one value:
+//       8 us, 36 with a piece for each run).
 // A table of few values needs no sorting: in hyena_embedding_few each team of lanes has its
 // tokens, one after the other, and sums of all values in LDS, which
 // hyena_embedding_few_join adds up (2^18 tokens, 16 values, width 256: 64 us so, 130 sorted;
@@ -406,6 +408,10 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
     }
     const int64_t n = p.sorted[p.total].x;  // tokens that take part
     const int64_t run = (int64_t)blockIdx.x * teams + team, first = run * p.run;
+    // a workgroup whose runs all lie inside one value leaves one sum: at its first run's start
+    __shared__ float inside[256][K + 1];
+    const int64_t before = (int64_t)blockIdx.x * teams * p.run - 1, behind = before + 1 + (int64_t)teams * p.run;
+    const bool whole = before >= 0 && behind < n && p.sorted[before].x == p.sorted[behind].x;
     if (first >= n) return;
     const int64_t last = first + p.run < n ? first + p.run : n;
     float s[K];
@@ -429,13 +435,14 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
             on[k] = (at_end ? next_value : e[k + 1].x) == e[k].x;
             ends[k] = i0 + k < last && (at_end || !on[k]);
         }
-        // (past the caches, gradients in turn: 65536 tokens 69 us, 75 through them)
+        // (loads past the caches are faster by 8% for 100 MB that come from memory, and slower by a third
+        // for rows that the caches hold, as those of a backward pass mostly are)
         Unit<T, UNITS> x[kSumRows], old[kSumRows];
 #pragma unroll
         for (int k = 0; k < kSumRows; ++k) {
             const T* row = row_at<T>(p.rows, e[k].y, p.rows_N);
             const T* there = (const T*)p.out + (int64_t)e[k].x * p.d;
-            x[k].template load<true>(row, c, p.d);
+            x[k].load(row, c, p.d);
             if (p.accumulate && ends[k]) old[k].load(there, c, p.d);
         }
 #pragma unroll
@@ -446,7 +453,10 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
 #pragma unroll
             for (int i = 0; i < K; ++i) s[i] += y[i];
             if (!ends[k]) continue;
-            if (open || on[k]) {  // a piece
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < K; ++i) inside[threadIdx.x][i] = s[i];
+            } else if (open || on[k]) {  // a piece
                 float* part = p.part + (run * 2 + (open ? 0 : 1)) * p.d4 + c;
 #pragma unroll
                 for (int i = 0; i < K; i += 4)
@@ -462,6 +472,16 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
             open = false;
         }
     }
+    if (!whole) return;
+    __syncthreads();
+    if (team != 0) return;
+    for (int k = 0; k < teams; ++k)  // (s is 0 behind a piece)
+#pragma unroll
+        for (int i = 0; i < K; ++i) s[i] += inside[k * p.lanes + tl][i];
+    float* part = p.part + run * 2 * p.d4 + c;
+#pragma unroll
+    for (int i = 0; i < K; i += 4)
+        if (c + i < p.d4) *(f32x4*)(part + i) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
 }
 
 // The values of one group of the sort that reach over runs, 256 channels of them.
@@ -474,15 +494,35 @@ template <typename T> __global__ __launch_bounds__(kJoinThreads) void hyena_embe
     const int c = (int)blockIdx.y * 256 + lane * 4;
     const int n = p.join_counts[blockIdx.x];
     const int4* list = p.joins + (int64_t)blockIdx.x * ((p.V + p.groups - 1) / p.groups);
-    const int run_shift = __builtin_ctz(p.run);
-    auto pieces_of = [&](int4 e) { return ((e.y + e.z - 1) >> run_shift) - (e.y >> run_shift) + 1; };
-    auto sum = [&](int4 e, int from, int step) {
-        const int pieces = pieces_of(e);
-        const float* part = p.part + (int64_t)(e.y >> run_shift) * 2 * p.d4 + c;
+    // a value's pieces: runs up to the first workgroup of the sums that is all its own, such
+    // workgroups, and the runs behind them
+    const int run_shift = __builtin_ctz(p.run), group_shift = run_shift + __builtin_ctz(256 / p.lanes);
+    struct Pieces {
+        int first, runs, group, groups, rest, all;
+    };
+    auto pieces_of = [&](int4 e) {
+        const int first = e.y >> run_shift, last = (e.y + e.z - 1) >> run_shift, wide = group_shift - run_shift;
+        // workgroup g is all its own where the tokens before and behind it are, too
+        const int g0 = (e.y >> group_shift) + 1, g1 = (e.y + e.z - 1) >> group_shift;
+        Pieces q;
+        q.first = first;
+        q.groups = g1 > g0 ? g1 - g0 : 0;
+        q.group = g0 << wide;
+        q.runs = q.groups ? q.group - first : last - first + 1;
+        q.rest = q.groups ? g1 << wide : 0;
+        q.all = q.groups ? q.runs + q.groups + (last - q.rest + 1) : q.runs;
+        return q;
+    };
+    auto sum = [&](const Pieces& q, int from, int step) {
+        const float* part = p.part + c;
+        const int wide = group_shift - run_shift;
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
         // the first piece is its run's last, the others their runs' first
 #pragma unroll 8
-        for (int k = from; k < pieces; k += step) s += *(const f32x4*)(part + ((int64_t)k * 2 + (k == 0)) * p.d4);
+        for (int k = from; k < q.all; k += step) {
+            const int in = k - q.runs, run = in < 0 ? q.first + k : in < q.groups ? q.group + (in << wide) : q.rest + in - q.groups;
+            s += *(const f32x4*)(part + ((int64_t)run * 2 + (k == 0)) * p.d4);
+        }
         return s;
     };
     auto write = [&](int4 e, f32x4 s) {
@@ -499,13 +539,15 @@ template <typename T> __global__ __launch_bounds__(kJoinThreads) void hyena_embe
     };
     for (int i = wave; i < n; i += kJoinWaves) {
         const int4 e = list[i];
-        if (pieces_of(e) <= kJoinWaves && c < p.d) write(e, sum(e, 0, 1));
+        const Pieces q = pieces_of(e);
+        if (q.all <= kJoinWaves && c < p.d) write(e, sum(q, 0, 1));
     }
     for (int i = 0; i < n; ++i) {
         const int4 e = list[i];
-        if (pieces_of(e) <= kJoinWaves) continue;
+        const Pieces q = pieces_of(e);
+        if (q.all <= kJoinWaves) continue;
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (c < p.d) s = sum(e, wave, kJoinWaves);
+        if (c < p.d) s = sum(q, wave, kJoinWaves);
         lds[wave][lane] = s;
         __syncthreads();
         if (wave == 0 && c < p.d) {

@@ -49,13 +49,11 @@ template <typename T> struct __attribute__((packed, aligned(sizeof(T)))) Loose {
 template <typename T, bool UNITS> struct Unit {
     static constexpr int K = kUnit<T>;
     uint4 v;
-    // ONCE: of a row that nothing reads again soon
-    template <bool ONCE = false> __device__ __forceinline__ void load(const T* row, int c, int d)
+    __device__ __forceinline__ void load(const T* row, int c, int d)
     {
         if constexpr (UNITS) {
             // no branch, so that loads stay together (gradient of 65536 tokens 38 us with one, 28 without)
-            const u32x4* at = (const u32x4*)(row + (c < d ? c : 0));
-            const u32x4 x = ONCE ? __builtin_nontemporal_load(at) : *at;
+            const uint4 x = *(const uint4*)(row + (c < d ? c : 0));
             v = make_uint4(c < d ? x.x : 0, c < d ? x.y : 0, c < d ? x.z : 0, c < d ? x.w : 0);
             return;
         }
@@ -99,11 +97,11 @@ template <typename T, bool UNITS> struct Unit {
     }
 };
 
-template <typename T, bool UNITS, bool ONCE = false>
+template <typename T, bool UNITS>
 __device__ __forceinline__ void load_unit(const T* row, int c, int d, float (&x)[kUnit<T>])
 {
     Unit<T, UNITS> y;
-    y.template load<ONCE>(row, c, d);
+    y.load(row, c, d);
     y.widen(x);
 }
 template <typename T, bool UNITS>

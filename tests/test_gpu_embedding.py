@@ -222,3 +222,17 @@ def test_tables_of_very_many_values(case):
     tok[0, ::3] = case[2] - 1
     tok[0, 1::7] = case[2] // 1024 * 1024 - 1
     run(case, "f32", tokens=tok)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 256), ("bf16", 600), ("bf16", 36), ("f16", 129)])
+def test_values_that_fill_workgroups(dtype, d):
+    # runs of 4 tokens by workgroups of 4 to 32 teams: values that begin and end at, before and
+    # after their borders, and have one, some or many of them to themselves
+    rng = np.random.default_rng(9)
+    counts = np.concatenate([np.arange(1, 70), [127, 128, 129, 130, 255, 256, 257, 258, 400, 511, 513, 1025, 16, 16, 32, 32, 64, 64, 4, 4]])
+    rng.shuffle(counts)
+    tok = np.repeat(rng.permutation(120)[:len(counts)], counts)
+    rng.shuffle(tok)
+    run((1, len(tok), 120, d), dtype, tokens=tok[None])
+    run((1, len(tok), 120, d), dtype, tokens=tok[None], accumulate=True, bad=True)
+    run((1, 5000, 120, d), dtype, tokens=np.full((1, 5000), 119))
