@@ -384,9 +384,6 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
     constexpr int K = kUnit<T>;
     const int teams = 256 / p.lanes, team = threadIdx.x / p.lanes, tl = threadIdx.x % p.lanes;
     const int c = ((int)blockIdx.y * p.lanes + tl) * K;
-    float zero[K];
-#pragma unroll
-    for (int i = 0; i < K; ++i) zero[i] = 0.0f;
     if ((int)blockIdx.x >= p.sum_groups) {
         // zeros where no token is, whole rows
         const int64_t step = (int64_t)p.fill_groups * gridDim.y * teams;
@@ -406,24 +403,24 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
         }
         return;
     }
-    const int64_t n = p.sorted[p.total].x;  // tokens that take part
-    const int64_t run = (int64_t)blockIdx.x * teams + team, first = run * p.run;
+    const int n = p.sorted[p.total].x;  // tokens that take part
+    const int run = (int)blockIdx.x * teams + team, first = run * p.run;
     // a workgroup whose runs all lie inside one value leaves one sum: at its first run's start
     __shared__ float inside[256][K + 1];
-    const int64_t before = (int64_t)blockIdx.x * teams * p.run - 1, behind = before + 1 + (int64_t)teams * p.run;
+    const int before = (int)blockIdx.x * teams * p.run - 1, behind = before + 1 + teams * p.run;
     const bool whole = before >= 0 && behind < n && p.sorted[before].x == p.sorted[behind].x;
     if (first >= n) return;
-    const int64_t last = first + p.run < n ? first + p.run : n;
+    const int last = first + p.run < n ? first + p.run : n;
     float s[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) s[i] = 0.0f;
     bool open = first > 0 && p.sorted[first - 1].x == p.sorted[first].x;  // the value began before this run
     const int next_value = last < n ? p.sorted[last].x : -1;
-    for (int64_t i0 = first; i0 < last; i0 += kSumRows) {
+    for (int i0 = first; i0 < last; i0 += kSumRows) {
         int2 e[kSumRows + 1];
 #pragma unroll
         for (int k = 0; k < kSumRows; ++k) {
-            const int64_t i = i0 + k < last ? i0 + k : last - 1;
+            const int i = i0 + k < last ? i0 + k : last - 1;
             e[k] = p.sorted[i];
         }
         e[kSumRows] = i0 + kSumRows < last ? p.sorted[i0 + kSumRows] : make_int2(next_value, 0);
@@ -457,7 +454,7 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
 #pragma unroll
                 for (int i = 0; i < K; ++i) inside[threadIdx.x][i] = s[i];
             } else if (open || on[k]) {  // a piece
-                float* part = p.part + (run * 2 + (open ? 0 : 1)) * p.d4 + c;
+                float* part = p.part + ((int64_t)run * 2 + (open ? 0 : 1)) * p.d4 + c;
 #pragma unroll
                 for (int i = 0; i < K; i += 4)
                     if (c + i < p.d4) *(f32x4*)(part + i) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
@@ -478,7 +475,7 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
     for (int k = 0; k < teams; ++k)  // (s is 0 behind a piece)
 #pragma unroll
         for (int i = 0; i < K; ++i) s[i] += inside[k * p.lanes + tl][i];
-    float* part = p.part + run * 2 * p.d4 + c;
+    float* part = p.part + (int64_t)run * 2 * p.d4 + c;
 #pragma unroll
     for (int i = 0; i < K; i += 4)
         if (c + i < p.d4) *(f32x4*)(part + i) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
