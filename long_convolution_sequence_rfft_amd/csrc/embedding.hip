@@ -2,7 +2,7 @@
 // gradient by sorted tokens (include/hyena.h).
 //
 // Forward is a gather: 4 bytes of a token, then its row, read and written once (16384 tokens of
-// width 768 in bf16 8.4 us, the table's rows mostly from the last-level cache; 32 tokens 3.2).
+// width 768 in bf16 8.4 us, the table's rows mostly from the last-level cache; 32 tokens 3.0).
 //
 // Backward.  Sums in an order that atomics decide would differ from call to call,
 // so tokens are sorted first, in their order within each value:
@@ -27,10 +27,10 @@
 // hyena_embedding_few_join adds up (2^18 tokens, 16 values, width 256: 64 us so, 130 sorted;
 // 2^20 tokens, 4 values, width 64: 63 and 899).
 // Bound by memory: each gradient row is read once, each row of the table written
-// once.  8192 tokens of 31999 values, width 770 in float32: sort 8.3, sums 26.6 (119 MB, most
-// of it zeros), joins 5.3 us.  65536 tokens of a text of 50257 values, width 768 in bf16, added to a
-// gradient: 19.7, 37.6 (162 MB), 13.3 us; the sort is bound by all groups reading all tokens from
-// the L2, the joins by the few values that are in most runs.
+// once.  8192 tokens of 31999 values, width 770 in float32: sort 8.2, sums 27.0 (119 MB, most
+// of it zeros), joins 5.5 us.  65536 tokens of a text of 50257 values, width 768 in bf16, added to a
+// gradient: 20.0, 40.2 (161 MB), 9.6 us; the sort is bound by all groups reading all tokens from
+// the L2.
 #include "rows.h"
 
 namespace hy {
@@ -55,7 +55,8 @@ constexpr int64_t kDealCalls = 131072;
 constexpr int kSortKept = 512;     // tokens of its values that a wave keeps: 32 KB of LDS in all
 constexpr int kSumRows = 4;        // gradient rows of a team under way (8: 73.5 us in all for 65536 tokens, 4: 64.7)
 // Runs are no shorter than kSumRows, and as short as this many of them allow: fewer leave the
-// sums waiting, more the joins (65536 tokens in all: 2048 61.8, 4096 60.9, 8192 72.2 us).
+// sums waiting, more the joins (65536 tokens in all: 2048 61.8, 4096 60.9, 8192 72.2 us); 4096 of width 768 in bf16 are one round of six
+// waves a SIMD, which the sums' registers allow (five: 75 us instead of 70).
 constexpr int64_t kSumTeams = 4096;
 constexpr int kFewValues = 32;     // tables of no more values than this
 constexpr int kFewRows = 8;        // gradient rows of a team under way

@@ -12,12 +12,12 @@
 //   hyena_loss_finish   d_x from its sums (hyena_loss_finish_few where they are many)
 //   hyena_loss_zeros    zeros for the other tokens, where the products write d_x themselves
 // Bound by the matrix instructions, 2 tokens V d operations forward, 6 backward, and these by the
-// power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1079 us, 1172 TFLOP/s (the
-// matrix units are busy for 66% of the cycles, of 1.70 GHz; a large product of the
-// library's reaches 1279, this one 953).  12288 of them backward: logits 882 us (1076 TFLOP/s; they
-// write G, 1.2 GB), products 1882 us (1008; of two products of the library's 944 and 822; the
-// matrix units are busy for 53% of the cycles, of 1.82 GHz).  2048 tokens, 31999 values in float32, whose six
-// products are counted: 506 us (1193) and 968 us (1248).
+// power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1091 us, 1159 TFLOP/s (the
+// matrix units are busy for 66% of the cycles, of 1.68 GHz; a large product of the
+// library's reaches 1279, this one 953).  12288 of them backward: logits 887 us (1069 TFLOP/s; they
+// write G, 1.2 GB), products 1904 us (996; of two products of the library's 944 and 822; the
+// matrix units are busy for 53% of the cycles, of 1.80 GHz).  2048 tokens, 31999 values in float32, whose six
+// products are counted: 513 us (1177) and 984 us (1228).
 #pragma once
 
 #include "matmul_device.h"
@@ -370,7 +370,7 @@ __global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SM
 }
 
 // Logits of few tokens, 16 N of them: bound by reading the table once (8 tokens of width 768 in bf16,
-// 50257 values: 16.5 us for 77 MB).  Workgroups take
+// 50257 values: 17.0 us for 77 MB).  Workgroups take
 // tiles of 16 values in turn, so that all of them together read one piece of the table after
 // the other (a part of the table for each workgroup was a third slower); within a tile each
 // wave has a quarter of the channels.  The operands go from memory to the registers, the
