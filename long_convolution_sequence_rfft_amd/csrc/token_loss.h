@@ -56,7 +56,8 @@ struct LossArgs {
     float* hit;            // [tokens] the target's logit; backward: what rounding took from G there
     char* g;               // [planes][chunk / 32][tokens rounded up][32]; of few tokens float32 [values rounded up][16]
     int64_t g_plane;
-    float* acc;            // [splits][tokens rounded up][acc_row] d_x
+    float* acc;            // [splits][acc_tokens][acc_row] d_x
+    int64_t acc_tokens;    // tokens rounded up; of few tokens as many as there are
     int64_t tokens;        // rounded up
     int32_t acc_row;
     int32_t chunk;         // values of a piece of the vocabulary

@@ -143,7 +143,8 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
         a.chunk = a.V;
         a.g = take((size_t)((a.V + 15) / 16 * 16 + 3) * 16 * 4);  // (read four values at a time)
         a.splits = planes == 3 ? kFewGroupsF32 : kFewGroups;
-        a.acc = (float*)take((size_t)a.splits * tokens * (size_t)a.acc_row * 4);
+        a.acc_tokens = a.total;
+        a.acc = (float*)take((size_t)a.splits * (size_t)a.total * (size_t)a.acc_row * 4);
         return at;
     }
     const int64_t tiles = even_pieces(whole, kGradBytes / (a.tokens * 2 * planes * kLossValues));
@@ -161,6 +162,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     splits = splits < 1 ? 1 : splits > most ? most : splits > cap ? cap : splits;
     a.splits = (int32_t)splits;
     // (2^18 tokens, 16 values, width 256: 345 us so, 457 through a sum)
+    a.acc_tokens = a.tokens;
     a.direct = splits == 1 && a.chunk >= a.V;
     a.acc = (float*)take(a.direct ? 0 : (size_t)splits * tokens * (size_t)a.acc_row * 4);
     // d_table's over the tokens, where one of them would take longer than that

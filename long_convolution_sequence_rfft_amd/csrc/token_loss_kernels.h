@@ -658,7 +658,7 @@ template <typename T, int N, bool UNITS> __global__ __launch_bounds__(256) void 
             f32x4 s = dx[t];
 #pragma unroll
             for (int w = 0; w < 3; ++w) s += lds[w][t][lane];
-            *(f32x4*)(p.acc + ((int64_t)blockIdx.x * p.tokens + t) * p.acc_row + c) = s;
+            *(f32x4*)(p.acc + ((int64_t)blockIdx.x * p.acc_tokens + t) * p.acc_row + c) = s;
         }
     }
 }
@@ -994,7 +994,7 @@ template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_finish_
         if (a >= 0 && c < p.d) {
             const float* from = p.acc + (int64_t)a * p.acc_row + c;
 #pragma unroll 4
-            for (int s = wave; s < p.splits; s += 16) x += *(const f32x4*)(from + (int64_t)s * p.tokens * p.acc_row);
+            for (int s = wave; s < p.splits; s += 16) x += *(const f32x4*)(from + (int64_t)s * p.acc_tokens * p.acc_row);
         }
         lds[wave][lane] = x;
         __syncthreads();
