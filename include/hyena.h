@@ -621,11 +621,11 @@ hyena_status hyena_residual_norm_backward(const hyena_residual_norm* op, const h
  *
  * Precision.  Products of 16-bit operands are accumulated in float32, in float32
  * storage each operand is three bfloat16 terms (24 bits) and the six largest of their
- * nine products are summed; lse and loss are float32.  With 16-bit storage the
- * gradients of more than 4 tokens pass through G rounded to that type, but at the target,
- * which is most of G, what its rounding takes is added to both gradients; in binary16 G is
- * divided by the largest |d_loss| first and kept times 2^15, so that probabilities down to
- * 2^-29 keep all its bits.  In float32 storage x, table and scale must be such that the logits and
+ * nine products are summed; lse and loss are float32.  With 16-bit storage G is
+ * float32 for few tokens and two terms of that type for more, whose sum is off by 2^-16 of G in
+ * bfloat16 and by 2^-22 in binary16 (there G is divided by the largest |d_loss| first and
+ * kept times 2^15: also off by 2^-39 of the largest |d_loss|): the gradients are rounded
+ * to the storage type once, at the end.  In float32 storage x, table and scale must be such that the logits and
  * all values are finite; elsewhere too an infinity or a NaN in the table reaches
  * every token, one in x its own token and d_table.  d_loss must be finite.
  *

@@ -23,8 +23,9 @@
 // same product ran at 854).  No bank conflicts.
 //
 // With several planes a step has all planes of both operands, so that each is loaded once for
-// the products it takes part in, and the products of less than the first planes are summed
-// apart and added last.
+// the products it takes part in.  Where both have several, the products of less than the first
+// planes are summed apart and added last; where only B has (an operand of more bits than its
+// type by one that is as given), all are one sum.
 // A lane's results: row 4 (lane / 16) + r of a 16 x 16 tile, column lane % 16.
 #pragma once
 
@@ -98,21 +99,6 @@ template <int W, int THREADS, Form F> struct Stage {
             }
         }
     }
-    // k in the rows: the row of this thread's loads in a step, and loads of any row there (at
-    // kNoRow zeros).
-    static constexpr uint32_t kNoRow = 0xfffffff0;
-    static __device__ __forceinline__ int row_of_step() { return (int)(threadIdx.x >> 2) & 31; }
-    __device__ __forceinline__ void init_rows(const Operand& o, uint32_t row_bytes)
-    {
-        static_assert(!KC && THREADS % 128 == 0, "");
-        const int s = threadIdx.x & 3, at = (((s >> 1) ^ key(row_of_step())) << 1 | (s & 1)) * 16;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            off[i] = row_bytes == kNoRow ? kNoRow
-                                         : (uint32_t)(((int)threadIdx.x + i * THREADS) >> 7) * (uint32_t)o.block + row_bytes + (uint32_t)at;
-    }
-    // Where value (k, m) of a step lies.
-    static __device__ __forceinline__ int place(int k, int m) { return (m >> 5) * 2048 + k * 64 + ((((m >> 4) & 1) ^ key(k)) << 5) + (m & 15) * 2; }
     __device__ __forceinline__ void load(uint32_t lds, const char* at, const char* end) const
     {
         const __amdgpu_buffer_rsrc_t r = operand_rsrc(at, end);
@@ -154,12 +140,13 @@ template <int NP> struct Planes {
     static __device__ __forceinline__ int b(int i) { return NP == 1 ? 0 : (0x010201 >> (4 * i)) & 15; }
 };
 
-// E: uint16_t (bfloat16) or _Float16.  STAGES - 1 steps are under way.
-template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, int STAGES> struct MatTile {
+// E: uint16_t (bfloat16) or _Float16.  NP planes of A, NB of B.  STAGES - 1 steps are under way.
+template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, int NB, int STAGES> struct MatTile {
+    static_assert(NP == 1 || NB == NP, "");
     static constexpr int kThreads = WM * WN * 64;
     using A = Stage<TM, kThreads, AF>;
     using B = Stage<TN, kThreads, BF>;
-    static constexpr int kStep = NP * (A::kBytes + B::kBytes), kLds = STAGES * kStep;
+    static constexpr int kStep = NP * A::kBytes + NB * B::kBytes, kLds = STAGES * kStep;
     static constexpr int MI = TM / WM / 16, NI = TN / WN / 16;
     using frag = typename Mx<E>::frag;
 
@@ -173,18 +160,22 @@ template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, 
             for (int j = 0; j < NI; ++j) c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // One step's products, of one plane.
+    // One step's products of one plane of A, the smaller ones first.
     __device__ __forceinline__ void products(const char* at, int m0, int n0)
     {
-        frag fa[MI], fb[NI];
+        frag fa[MI], fb[NB][NI];
 #pragma unroll
-        for (int j = 0; j < NI; ++j) fb[j] = B::template fragment<frag>(at + NP * A::kBytes, n0 + 16 * j);
+        for (int n = NB - 1; n >= 0; --n)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) fb[n][j] = B::template fragment<frag>(at + A::kBytes + n * B::kBytes, n0 + 16 * j);
 #pragma unroll
         for (int i = 0; i < MI; ++i) fa[i] = A::template fragment<frag>(at, m0 + 16 * i);
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int n = NB - 1; n >= 0; --n)
 #pragma unroll
-            for (int j = 0; j < NI; ++j) c[i][j] = Mx<E>::mma(fa[i], fb[j], c[i][j]);
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) c[i][j] = Mx<E>::mma(fa[i], fb[n][j], c[i][j]);
     }
 
     // aplane, bplane: bytes between planes.  steps: of 32 values of k, at least 1.
@@ -204,8 +195,8 @@ template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, 
         const char *pa = oa.at, *pb = ob.at;
         auto issue = [&](int stage) {
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                a.load(base + stage * kStep + n * A::kBytes, pa + n * aplane, oa.end + n * aplane);
+            for (int n = 0; n < NB; ++n) {
+                if (n < NP) a.load(base + stage * kStep + n * A::kBytes, pa + n * aplane, oa.end + n * aplane);
                 b.load(base + stage * kStep + NP * A::kBytes + n * B::kBytes, pb + n * bplane, ob.end + n * bplane);
             }
             pa += astep;
@@ -225,7 +216,7 @@ template <typename E, int TM, int TN, int WM, int WN, Form AF, Form BF, int NP, 
         int now = 0, into = STAGES - 1;
         for (int s = 0; s < steps; ++s) {
             // this step's loads are done: those of later steps may be under way
-            if (STAGES > 2 && s + STAGES - 1 <= steps) wait_loads<(STAGES - 2) * NP * (A::kLoads + B::kLoads)>();
+            if (STAGES > 2 && s + STAGES - 1 <= steps) wait_loads<(STAGES - 2) * (NP * A::kLoads + NB * B::kLoads)>();
             else wait_loads<0>();
             barrier_only();
             if (s + STAGES - 1 < steps) issue(into);

@@ -53,7 +53,7 @@ struct LossArgs {
     int64_t values_row, values_block, values_plane, values_bytes;  // bytes: of a row, 32 channels, a plane; the first plane's
     float2* part;          // [tiles of a piece's values][tokens rounded up]: largest, sum
     float2* running;       // [tokens] the same of the pieces before, where there is more than one
-    float* hit;            // [tokens] the target's logit; backward: what rounding took from G there
+    float* hit;            // [tokens] forward: the target's logit
     char* g;               // [planes][chunk / 32][tokens rounded up][32]; of few tokens float32 [values rounded up][16]
     int64_t g_plane;
     float* acc;            // [splits][acc_tokens][acc_row] d_x

@@ -82,7 +82,7 @@ int64_t even_pieces(int64_t all, int64_t fit)
 // Sizes, and with a scratch the addresses in it; returns the bytes.
 size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a)
 {
-    const int64_t planes = op->io_dtype == HYENA_F32 ? 3 : 1;
+    const int64_t planes = op->io_dtype == HYENA_F32 ? 3 : 1, grad_planes = planes == 3 ? 3 : 2;  // kGradPlanes
     a.total = op->B * op->N;
     a.V = (int32_t)op->V;
     a.d = (int32_t)op->d;
@@ -121,7 +121,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
         a.values_bytes = (int64_t)a.V * a.values_row;
         a.values = (const char*)op->table;
     }
-    a.hit = (float*)take(tokens * 4);
+    if (!grad) a.hit = (float*)take(tokens * 4);
     const int64_t whole = loss_tiles(a.V);
     if (!grad && a.small) {
         a.chunk = a.V;
@@ -147,10 +147,10 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
         a.acc = (float*)take((size_t)a.splits * (size_t)a.total * (size_t)a.acc_row * 4);
         return at;
     }
-    const int64_t tiles = even_pieces(whole, kGradBytes / (a.tokens * 2 * planes * kLossValues));
+    const int64_t tiles = even_pieces(whole, kGradBytes / (a.tokens * 2 * grad_planes * kLossValues));
     a.chunk = (int32_t)(tiles * kLossValues);
     a.g_plane = a.chunk / 32 * a.block;
-    a.g = take((size_t)(planes * a.g_plane));
+    a.g = take((size_t)(grad_planes * a.g_plane));
     // d_x's sums over a piece are cut so that their workgroups, which come last, take a part
     // of what all of the piece's work takes on kSplitGroups of them
     const int64_t channel_tiles = (a.d + kGradChannels - 1) / kGradChannels, dx_tiles = a.tokens / kGradRows * channel_tiles;

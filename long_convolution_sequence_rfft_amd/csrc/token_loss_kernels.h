@@ -15,7 +15,7 @@
 // power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1091 us, 1159 TFLOP/s (the
 // matrix units are busy for 66% of the cycles, of 1.68 GHz; a large product of the
 // library's reaches 1279, this one 953).  12288 of them backward: logits 887 us (1069 TFLOP/s; they
-// write G, 1.2 GB), products 1904 us (996; of two products of the library's 944 and 822; the
+// write G, 2.5 GB), products 1904 us (996; of two products of the library's 944 and 822; the
 // matrix units are busy for 53% of the cycles, of 1.80 GHz).  2048 tokens, 31999 values in float32, whose six
 // products are counted: 513 us (1177) and 984 us (1228).
 #pragma once
@@ -41,13 +41,32 @@ template <> struct LossType<float> {
     static constexpr int P = 3, WM = 4, WN = 2, kThreads = WM * WN * 64;
 };
 
-// Eight float32 values as P planes of E, by cutting (bfloat16, P = 3) or rounding.
+// Eight float32 values as P planes of E, by cutting (bfloat16, P = 3) or rounding (P = 1).
 template <typename E, int P> __device__ __forceinline__ void store_planes(char* to, int64_t plane, f32x8 x)
 {
     Split<E, P> s;
     s.set(x);
 #pragma unroll
     for (int n = 0; n < P; ++n) *(typename Mx<E>::frag*)(to + n * plane) = s.f[n];
+}
+
+// Planes of G.  It is float32, and with 16-bit storage two terms of that type (rounded, what is
+// left rounded): off by 2^-16 of itself in bfloat16, 2^-22 in binary16, so that the gradients'
+// rounding is their results' only.  One term leaves as much again in every row of d_table that is
+// nobody's target, and more in sums that cancel (d_x: G of a token sums to 0); its products take
+// half the matrix instructions (16384 tokens, a quarter masked, 50257 values, width 768 in bf16: logits
+// 890 us with one, 1370 with two, products 1890 and 3150).
+template <typename T> constexpr int kGradPlanes = LossType<T>::P == 1 ? 2 : LossType<T>::P;
+template <typename T> __device__ __forceinline__ void store_grads(char* to, int64_t plane, f32x8 x)
+{
+    using E = typename LossType<T>::E;
+    if constexpr (LossType<T>::P == 1) {
+        const typename Mx<E>::frag first = Mx<E>::narrow8(x);
+        *(typename Mx<E>::frag*)to = first;
+        *(typename Mx<E>::frag*)(to + plane) = Mx<E>::narrow8(x - Mx<E>::widen8(first));
+    } else {
+        store_planes<E, kGradPlanes<T>>(to, plane, x);
+    }
 }
 
 __device__ __forceinline__ int workgroup_sum16(int x, int* lds)
@@ -245,7 +264,7 @@ __global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SM
     using L = LogitsTile<T, SMALL>;
     using E = typename LossType<T>::E;
     constexpr int P = L::P, WM = L::WM, WN = L::WN, TM = L::TM, TN = L::TN;
-    using Tile = MatTile<E, TM, TN, WM, WN, kInColumnsPaired, kInColumns, P, L::kStages>;
+    using Tile = MatTile<E, TM, TN, WM, WN, kInColumnsPaired, kInColumns, P, P, L::kStages>;
     __shared__ __attribute__((aligned(16))) char lds[Tile::kLds];
     const int64_t count = *p.count;
     const int token_tiles = (int)(p.tokens / TN);
@@ -346,25 +365,16 @@ __global__ __launch_bounds__((LogitsTile<T, SMALL>::kThreads), (LogitsTile<T, SM
                         if (!in || first + at(i) + r >= left) tile.c[i][j][r] = 0.0f;
             }
             if (__any((uint32_t)target < (uint32_t)(TM / WM))) {
-                float off = 0.0f;
 #pragma unroll
                 for (int i = 0; i < Tile::MI; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (target == at(i) + r) {
-                            tile.c[i][j][r] -= weight;
-                            if constexpr (P == 1) {
-                                E rounded;
-                                store_one<E>(&rounded, tile.c[i][j][r]);
-                                off = tile.c[i][j][r] - load_one<E>(&rounded);
-                            }
-                        }
-                if (P == 1 && (uint32_t)target < (uint32_t)(TM / WM) && (target & 31) < 8) p.hit[t] = off;
+                        if (target == at(i) + r) tile.c[i][j][r] -= weight;
             }
             char* to = p.g + (int64_t)((value_tile * TM + wm * (TM / WM)) >> 5) * p.block + t * 64 + g * 16;
 #pragma unroll
             for (int i = 0; i < Tile::MI; i += 2)
-                store_planes<E, P>(to + (int64_t)(i >> 1) * p.block, p.g_plane, join8(tile.c[i][j], tile.c[i + 1][j]));
+                store_grads<T>(to + (int64_t)(i >> 1) * p.block, p.g_plane, join8(tile.c[i][j], tile.c[i + 1][j]));
         }
     }
 }
@@ -698,72 +708,6 @@ template <typename T, int TOKENS> __global__ __launch_bounds__(1024) void hyena_
     }
 }
 
-// G at the target is rounded like the others, but one row of d_table (and d_x) bears its rest:
-// in the first steps of a training all tokens' targets have nearly one G, and one rest.  So
-// the rests of the tokens t0 to t1 whose targets are among a tile's values, from first on, are
-// one more product behind the tile's others: their rows of x by a matrix with one value in
-// a row, 32 of them in a step.  (Gradient of 16 bits, 108 tokens and 50257 values: the
-// error of d_table is that of its rounding so, 1.6 times that without.)
-template <typename E, typename Tile>
-__device__ __forceinline__ void add_rests(Tile& tile, char* lds, const LossArgs& p, const Operand& x, int32_t first, int64_t t0, int64_t t1)
-{
-    constexpr int kWaves = Tile::kThreads / 64, kKept = 1024, kAhead = 8;  // tokens that a wave lists, loads under way
-    using B = typename Tile::B;
-    static_assert(64 + kWaves * kKept * 4 <= Tile::kStep, "");
-    int* counts = (int*)(lds + Tile::kStep);
-    int* list = counts + 16;
-    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t each = (t1 - t0 + Tile::kThreads - 1) / Tile::kThreads * 64;
-    const int64_t end = t0 + each * (wave + 1) < t1 ? t0 + each * (wave + 1) : t1;
-    int64_t at = t0 + each * wave;
-    while (true) {
-        int n = 0;
-        for (; at < end && n <= kKept - 64 * kAhead; at += 64 * kAhead) {
-            int v[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) v[k] = at + 64 * k + lane < end ? p.target[at + 64 * k + lane] - first : -1;
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const bool own = (uint32_t)v[k] < (uint32_t)kGradRows;
-                const uint64_t all = __ballot(own);
-                if (own) list[wave * kKept + n + __popcll(all & (((uint64_t)1 << lane) - 1))] = (int)at + 64 * k + lane;
-                n += __popcll(all);
-            }
-        }
-        if (lane == 0) counts[wave] = n | (at < end) << 30;
-        __syncthreads();
-        int total = 0, more = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            more |= counts[w] >> 30;
-            total += counts[w] & 0x3fffffff;
-        }
-        for (int s = 0; s < total; s += 32) {
-            const int k = Tile::A::row_of_step();
-            int token = -1;
-            if (s + k < total) {
-                int i = s + k, w = 0;
-                while (i >= (counts[w] & 0x3fffffff)) i -= counts[w++] & 0x3fffffff;
-                token = list[w * kKept + i];
-            }
-            typename Tile::A a;
-            a.init_rows(x, token < 0 ? Tile::A::kNoRow : (uint32_t)token * 64);
-            a.load(base, x.at, x.end);
-            for (int i = threadIdx.x; i < B::kBytes / 16; i += Tile::kThreads) ((uint4*)(lds + Tile::A::kBytes))[i] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-            if (token >= 0 && threadIdx.x < 128 && (threadIdx.x & 3) == 0)
-                store_one<E>((E*)(lds + Tile::A::kBytes + B::place(k, p.target[token] - first)), p.hit[token]);
-            wait_loads<0>();
-            __syncthreads();
-            tile.products(lds, wave / 2 * (kGradChannels / 2), wave % 2 * (kGradRows / 2));
-            __syncthreads();
-        }
-        if (!more) return;
-        __syncthreads();
-    }
-}
-
 // 4 channels of d_x of a token, x their sum.
 template <typename T> __device__ __forceinline__ void store_dx(const LossArgs& p, int64_t t, int c, f32x4 x)
 {
@@ -775,23 +719,6 @@ template <typename T> __device__ __forceinline__ void store_dx(const LossArgs& p
         for (int e = 0; e < 4; ++e)
             if (c + e < p.d) store_one<T>(to + e, x[e]);
     }
-}
-
-// The rest of G at the target times its row of the table.
-template <typename T> __device__ __forceinline__ f32x4 target_rest(const LossArgs& p, int target, float rest, int c)
-{
-    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (LossType<T>::P == 1) {
-        const T* w = (const T*)p.table + (int64_t)target * p.d + c;
-        if (p.d % 4 == 0) {
-            x = Mx<T>::widen(*(const typename Mx<T>::vec4*)w) * rest;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < p.d) x[e] = rest * load_one<T>(w + e);
-        }
-    }
-    return x;
 }
 
 // One launch, so that neither product waits for the other's last workgroups.  Tiles of 256
@@ -806,8 +733,9 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
 {
     using E = typename LossType<T>::E;
     constexpr int P = LossType<T>::P, WM = LossType<T>::WM, WN = LossType<T>::WN;
-    using Table = MatTile<E, kGradChannels, kGradRows, WM, WN, kInRows, kInRows, P, 2>;
-    using Dx = MatTile<E, kGradChannels, kGradRows, WM, WN, kInRows, kInColumns, P, 2>;
+    constexpr int GP = kGradPlanes<T>;
+    using Table = MatTile<E, kGradChannels, kGradRows, WM, WN, kInRows, kInRows, P, GP, 2>;
+    using Dx = MatTile<E, kGradChannels, kGradRows, WM, WN, kInRows, kInColumns, P, GP, 2>;
     __shared__ __attribute__((aligned(16))) char lds[Table::kLds];
     const int64_t count = *p.count;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4;
@@ -822,12 +750,9 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
         const int k0 = split * per, k1 = k0 + per < steps ? k0 + per : steps;
         Table tile;
         if (k0 < k1) {
-            Operand x{p.rows + (int64_t)(c0 >> 5) * p.block, p.rows + p.rows_plane, 64, p.block};
+            const Operand x{p.rows + (int64_t)(c0 >> 5) * p.block + (int64_t)k0 * 2048, p.rows + p.rows_plane, 64, p.block};
             const Operand y{p.g + (int64_t)(v0 >> 5) * p.block + (int64_t)k0 * 2048, p.g + p.g_plane, 64, p.block};
-            x.at += (int64_t)k0 * 2048;
             tile.run(lds, x, p.rows_plane, y, p.g_plane, k1 - k0);
-            x.at -= (int64_t)k0 * 2048;
-            if constexpr (P == 1) add_rests<E>(tile, lds, p, x, p.first + v0, (int64_t)k0 * 32, (int64_t)k1 * 32 < count ? (int64_t)k1 * 32 : count);
         } else {
             tile.clear();
         }
@@ -880,13 +805,10 @@ template <typename T> __global__ __launch_bounds__(LossType<T>::kThreads, 2) voi
             const int64_t a = t0 + wn * (kGradRows / WN) + 16 * j + (lane & 15);
             if (a >= count) continue;
             const int32_t t = p.index[a];
-            int target = 0;
-            float rest = 0.0f;
-            if constexpr (P == 1) target = p.target[a], rest = p.hit[a];
 #pragma unroll
             for (int i = 0; i < Dx::MI; ++i) {
                 const int c = c0 + wm * (kGradChannels / WM) + 16 * i + 4 * g;
-                if (c < p.d) store_dx<T>(p, t, c, (tile.c[i][j] + target_rest<T>(p, target, rest, c)) * down);
+                if (c < p.d) store_dx<T>(p, t, c, tile.c[i][j] * down);
             }
         }
         return;
@@ -940,24 +862,13 @@ template <typename T, int kTokens> __global__ __launch_bounds__(256) void hyena_
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const float down = p.norm[1];
     for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * kTokens; t0 < p.total; t0 += (int64_t)gridDim.x * 4 * kTokens) {
-        int32_t a[kTokens], target[kTokens];
-        float rest[kTokens];
+        int32_t a[kTokens];
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) a[k] = t0 + k < p.total ? p.place[t0 + k] : -1;
-        if constexpr (LossType<T>::P == 1) {
-#pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                target[k] = a[k] >= 0 ? p.target[a[k]] : 0;
-                rest[k] = a[k] >= 0 ? p.hit[a[k]] : 0.0f;
-            }
-        }
         for (int c = lane * 4; c < p.d; c += 256) {
             f32x4 x[kTokens];
 #pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                x[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                if constexpr (LossType<T>::P == 1) x[k] = target_rest<T>(p, target[k], rest[k], c);
-            }
+            for (int k = 0; k < kTokens; ++k) x[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 2
             for (int s = 0; s < p.splits; ++s) {
 #pragma unroll
@@ -1001,7 +912,6 @@ template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_finish_
         if (wave == 0 && c < p.d) {
 #pragma unroll
             for (int w = 1; w < 16; ++w) x += lds[w][lane];
-            if (LossType<T>::P == 1 && a >= 0 && !p.few) x += target_rest<T>(p, p.target[a], p.hit[a], c);
             store_dx<T>(p, t, c, x * down);
         }
         __syncthreads();

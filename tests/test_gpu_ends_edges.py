@@ -1,0 +1,60 @@
+"""Where the embedding, the norm of whole tokens and the loss over a vocabulary could lose
+what their sums are made of: precision that depends on a call's size, and sizes at which
+one kernel hands over to another.  Tolerances stand at each test."""
+import numpy as np
+import pytest
+
+import ends_ref
+from gpu_util import say
+from long_convolution_sequence_rfft_amd import hyena
+from test_gpu_recurrence import IO, f64, torch_dtype
+
+pytestmark = pytest.mark.gpu
+
+
+def rounded(a, dtype):
+    """float64 values as the storage type holds them."""
+    import torch
+    return torch.from_numpy(np.asarray(a, dtype=np.float64)).to(torch_dtype(dtype)).double().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("case", [(5, 300, 40), (17, 131, 45), (150, 2000, 96), (1200, 3500, 64), (4200, 1100, 40), (4000, 15, 40), (3000, 259, 300)])
+def test_loss_gradients_round_only_their_results(case, dtype):
+    # All tokens are alike, and so are all rows of the table but the target's, which is zeros: G is
+    # 1 + 0.95 u beside it, a value that the storage type rounds to 1.  Such a rounding would be in
+    # every sum, 0.95 u of it beside the result's own u.  Behind that: what a probability is off by
+    # (r, of two float32 logits, the exponential and lse), two terms of G (u^2; binary16's
+    # subnormals 2^-39 of the largest |d_loss|), 2^-22 for the product with d_loss and the factor, and the
+    # sum of K terms in float32.
+    import torch
+    T, V, d = case
+    say(f"[gpu] token_loss, gradients of values beside the target {case} {dtype}")
+    u = ends_ref.HALF_STEP[dtype]
+    gen = torch.Generator().manual_seed(T)
+    dt = torch_dtype(dtype)
+    x = (torch.rand(d, generator=gen) + 0.5).to(dt)
+    w = ((torch.rand(d, generator=gen) + 0.5) / d).to(dt)
+    row = V * 3 // 7
+    table = w.expand(V, d).clone()
+    table[row] = 0.0
+    xs, target = x.expand(1, T, d).contiguous().cuda(), torch.full((1, T), row, dtype=torch.int32, device="cuda")
+    plan = hyena.TokenLoss(1, T, V, d, io_dtype=IO[dtype])
+    _, lse = plan.forward(xs, table.cuda(), target)
+    assert bool((lse == lse[0, 0]).all())
+    xd, wd = f64(x), f64(w)
+    p = np.exp(xd @ wd - float(lse[0, 0]))
+    dl = float(np.float32((1 + 0.95 * u) / p))
+    g = dl * p
+    dx, d_table = plan.backward(torch.full((1, T), dl, device="cuda"), xs, table.cuda(), target, lse)
+    size = np.abs(xd) @ np.abs(wd)
+    r = 2 * (d + 8) * 2.0 ** -24 * size + 2.0 ** -20 + 2.0 ** -21 * size
+    dg = (r + u * u + 2.0 ** -22) * g + (2.0 ** -39 * dl if dtype == "f16" else 0.0)
+    for got, n, of, what in ((dx[0], V - 1, wd, "dx"), (d_table[torch.arange(V) != row], T, xd, "d_table")):
+        ref = n * g * of
+        bound = u * np.abs(ref) + n * (dg + (n + 16) * 2.0 ** -24 * g) * np.abs(of)
+        once_more = rounded(n * float(rounded(g, dtype)) * of, dtype)
+        assert np.any(np.abs(once_more - ref) > bound)  # the test tells the two apart
+        err = np.abs(f64(got) - ref)
+        say(f"[gpu]   {what}: worst error / bound {float(np.max(err / bound)):.3f}")
+        assert np.all(err <= bound), what
