@@ -46,12 +46,13 @@ hyena_status loss_sizes(const hyena_token_loss* op)
 // Calls of at most this many tokens have their own kernels: forward, in 16 bits and in
 // float32 (whose table is read as given then), and backward.  With 50257 values of width 768,
 // by them and by the others: forward in 16 bits 4 tokens 21 and 39 us, 32 23 and 40; in float32 8 38 and
-// 153, 64 121 and 157 (128 186 and 159); backward in 16 bits 4 tokens 75 and 107 (8 98 and 101); in
-// float32 8 123 and 318, 16 182 and 319.
-constexpr int64_t kFewTokens = 32, kFewTokensF32 = 64, kFewTokensGrad = 4, kFewTokensGradF32 = 16;
+// 153, 64 121 and 157 (128 186 and 159); backward in 16 bits 4 tokens 69 and 108, 8 88 and 108 (12 169 and
+// 108, for twice the sums in the registers); in float32 8 120 and 315, 16 177 and 315.
+constexpr int64_t kFewTokens = 32, kFewTokensF32 = 64, kFewTokensGrad = 8, kFewTokensGradF32 = 16;
 // Workgroups of 256 channels, backward: more have more loads under way, and more sums of d_x
-// behind them (256 and 512: 4 tokens in 16 bits 85 and 75 us, 8 in float32 123 and 131).
-constexpr int32_t kFewGroups = 512, kFewGroupsF32 = 256;
+// behind them (256 and 512: 4 tokens in 16 bits 74 and 69 us, 8 88 and 96; 8 in float32 123 and 131).
+constexpr int32_t kFewGroups = 256, kFewGroupsHalf = 512;
+constexpr int64_t kFewGroupsTokens = 4;  // in 16 bits, at most: kFewGroupsHalf
 // Others of more tokens than this bring the table into the matrix operands' form first (in that
 // form and as given, forward: 1024 tokens 128 and 103 us, 4096 314 and 304, 8192 573 and 575, 16384 1062
 // and 1117; backward 383 and 370, 1133 and 1123, 8192 1939 and 1960).
@@ -142,7 +143,7 @@ size_t lay_out(const hyena_token_loss* op, bool grad, void* scratch, LossArgs& a
     if (a.few) {
         a.chunk = a.V;
         a.g = take((size_t)((a.V + 15) / 16 * 16 + 3) * 16 * 4);  // (read four values at a time)
-        a.splits = planes == 3 ? kFewGroupsF32 : kFewGroups;
+        a.splits = planes == 1 && a.total <= kFewGroupsTokens ? kFewGroupsHalf : kFewGroups;
         a.acc_tokens = a.total;
         a.acc = (float*)take((size_t)a.splits * (size_t)a.total * (size_t)a.acc_row * 4);
         return at;

@@ -1017,7 +1017,8 @@ template <typename T> hyena_status loss_backward(const LossArgs& a, bool pack, b
         if ((st = loss_logits<T, true>(b, units, a.few ? few_groups(a.V) : loss_tiles(values, a.small), s)) != HYENA_OK) return st;
         if (a.few) {  // all of the vocabulary is one piece
             if (a.total <= 4) st = loss_few_grads<T, 4>(a, s);
-            else if constexpr (LossType<T>::P == 3) st = a.total <= 8 ? loss_few_grads<T, 8>(a, s) : loss_few_grads<T, 16>(a, s);
+            else if (a.total <= 8) st = loss_few_grads<T, 8>(a, s);
+            else if constexpr (LossType<T>::P == 3) st = loss_few_grads<T, 16>(a, s);
             if (st != HYENA_OK) return st;
             break;
         }

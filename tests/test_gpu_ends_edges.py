@@ -8,6 +8,7 @@ import ends_ref
 from gpu_util import say
 from long_convolution_sequence_rfft_amd import hyena
 from test_gpu_recurrence import IO, f64, torch_dtype
+from test_gpu_token_loss import run as loss_run
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,11 @@ def test_loss_gradients_round_only_their_results(case, dtype):
         err = np.abs(f64(got) - ref)
         say(f"[gpu]   {what}: worst error / bound {float(np.max(err / bound)):.3f}")
         assert np.all(err <= bound), what
+
+
+@pytest.mark.parametrize("tokens", [7, 8, 9, 10])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_loss_of_few_tokens_at_the_limit_of_eight(dtype, tokens):
+    # rows made of 16-byte pieces, and not; values that are no multiple of a wave's four
+    loss_run((1, tokens, 777, 72), dtype, masked=0.0)
+    loss_run((tokens, 1, 3001, 301), dtype, masked=0.3)
