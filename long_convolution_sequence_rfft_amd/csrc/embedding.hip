@@ -133,6 +133,16 @@ template <typename T, bool UNITS> __global__ __launch_bounds__(256) void hyena_e
     }
 }
 
+// The lanes of a wave pass values to each other through LDS: what lies before this is done for
+// all of them, and nothing behind it is moved ahead.  (A wave's LDS accesses are done in
+// order; this holds the compiler to theirs.)
+__device__ __forceinline__ void wave_exchange()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // Sum of one value over a workgroup's threads.
 __device__ __forceinline__ int workgroup_sum(int x, int* lds)
 {
@@ -175,11 +185,11 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
             const uint64_t ones = __ballot(group >> b & 1);
             same &= group >> b & 1 ? ones : ~ones;
         }
-        if (in) {
-            const int before = own[group], rank = __popcll(same & (((uint64_t)1 << lane) - 1));
-            at[k] = before + rank;
-            own[group] = before + __popcll(same);  // every lane of the group the same value
-        }
+        const int before = in ? own[group] : 0, rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+        at[k] = before + rank;
+        wave_exchange();  // every lane has read before one writes
+        if (in && rank == 0) own[group] = before + __popcll(same);
+        wave_exchange();
     }
     __syncthreads();
     // counts to places: thread i has group i
@@ -263,7 +273,7 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
             // (of one value all at once: 131072 tokens of one value 89 us so, 162 with an atomic of each lane)
             int* to = &counters[wave * values + i];
             if (__ballot(own && i != __builtin_amdgcn_readfirstlane(i)) == 0) {
-                if (own) *to += __popcll(who);  // every lane the same value
+                if (lane == 0) atomicAdd(to, __popcll(who));  // (the first lane has a token wherever one has)
             } else if (own) {
                 atomicAdd(to, 1);
             }
@@ -352,8 +362,10 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
             const uint64_t all_same = __ballot(same);
             int* counter = &counters[wave * values + one];
             const int place = *counter;
+            wave_exchange();  // every lane has read before one writes
             if (same) p.sorted[place + __popcll(all_same & (((uint64_t)1 << lane) - 1))] = make_int2(group + p.groups * i, (int)t);
-            *counter = place + __popcll(all_same);  // every lane the same value
+            if (lane == 0) *counter = place + __popcll(all_same);
+            wave_exchange();
             left &= ~all_same;
         }
     };
