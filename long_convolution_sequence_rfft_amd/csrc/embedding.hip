@@ -48,9 +48,10 @@ constexpr int kPlaceBits = 21;
 static_assert(kSortMostValues <= 1 << (32 - kPlaceBits), "");
 constexpr int kSortTokens = 16;    // of a lane, in four loads
 constexpr int kDealTokens = 4096;  // of a workgroup that deals
-constexpr int kDealGroups = 1024;  // at most
+constexpr int kDealGroups = 1024;  // at most; the lists of more of the sort's groups are one, of those with the same lower bits
 // Calls of fewer tokens are not dealt (values of a text in a vocabulary of 50257, dealt and
-// sorted, against sorted only: 65536 tokens 20 and 19 us, 2^20 tokens 129 and 410).
+// sorted, against sorted only: 65536 tokens 20 and 19 us, 2^20 tokens 129 and 410; 2^20 of 1600000 values, of
+// which two groups share a list, 199 and 820).
 constexpr int64_t kDealCalls = 131072;
 constexpr int kSortKept = 512;     // tokens of its values that a wave keeps: 32 KB of LDS in all
 constexpr int kSumRows = 4;        // gradient rows of a team under way (8: 73.5 us in all for 65536 tokens, 4: 64.7)
@@ -81,8 +82,9 @@ struct EmbedArgs {
     int2* sorted;        // [total] value and token, in order; [total].x the number of tokens that take part
     int4* joins;         // [V] values that reach over runs, where they begin, tokens: group g's from g * values on
     int32_t* join_counts;  // [groups]
-    int2* dealt;         // [blocks of kDealTokens] value and token, by groups; NULL: the sort reads the tokens
-    int32_t* deal_starts;  // [groups + 1][blocks] where a group begins in a block
+    int2* dealt;         // [blocks of kDealTokens] value and token, by lists; NULL: the sort reads the tokens
+    int32_t* deal_starts;  // [deal_groups + 1][blocks] where a list begins in a block
+    int32_t deal_groups;   // lists, a power of two
     int32_t deal_blocks;
     float* part;         // [runs][2][d4]: sums that reach over a run's start and over its end
     int32_t d4;          // d rounded up to 4
@@ -155,15 +157,16 @@ __device__ __forceinline__ int workgroup_sum(int x, int* lds)
     return x;
 }
 
-// kDealTokens tokens by groups, in the order they are read within each.
+// kDealTokens tokens by lists (of value v: v % deal_groups), in the order they are read within each.
 template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embedding_deal(EmbedArgs p)
 {
     extern __shared__ int counters[];  // [waves][groups]
     __shared__ int lds[kSortWaves];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, bits = __builtin_ctz(p.groups);
+    const int groups = p.deal_groups;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, bits = __builtin_ctz(groups);
     const int64_t first = (int64_t)blockIdx.x * kDealTokens;
-    int* own = counters + wave * p.groups;
-    for (int i = threadIdx.x; i < p.groups * kSortWaves; i += kSortThreads) counters[i] = 0;
+    int* own = counters + wave * groups;
+    for (int i = threadIdx.x; i < groups * kSortWaves; i += kSortThreads) counters[i] = 0;
     __syncthreads();
     static_assert(kDealTokens == 4 * kSortThreads, "");
     int v[4], at[4];
@@ -179,7 +182,7 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const bool in = (uint32_t)v[k] < (uint32_t)p.V;
-        const int group = v[k] & (p.groups - 1);
+        const int group = v[k] & (groups - 1);
         uint64_t same = __ballot(in);  // the lanes of one group
         for (int b = 0; b < bits; ++b) {
             const uint64_t ones = __ballot(group >> b & 1);
@@ -195,10 +198,10 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
     // counts to places: thread i has group i
     const int i = threadIdx.x;
     int mine = 0;
-    if (i < p.groups)
+    if (i < groups)
         for (int w = 0; w < kSortWaves; ++w) {
-            const int c = counters[w * p.groups + i];
-            counters[w * p.groups + i] = mine;
+            const int c = counters[w * groups + i];
+            counters[w * groups + i] = mine;
             mine += c;
         }
     int before = mine;
@@ -214,16 +217,16 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
         if (w < wave) before += lds[w];
         all += lds[w];
     }
-    if (i < p.groups) {
-        for (int w = 0; w < kSortWaves; ++w) counters[w * p.groups + i] += before;
+    if (i < groups) {
+        for (int w = 0; w < kSortWaves; ++w) counters[w * groups + i] += before;
         p.deal_starts[(int64_t)i * p.deal_blocks + blockIdx.x] = before;
     }
-    if (i == 0) p.deal_starts[(int64_t)p.groups * p.deal_blocks + blockIdx.x] = all;
+    if (i == 0) p.deal_starts[(int64_t)groups * p.deal_blocks + blockIdx.x] = all;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if ((uint32_t)v[k] < (uint32_t)p.V)
-            p.dealt[first + own[v[k] & (p.groups - 1)] + at[k]] = make_int2(v[k], (int)(t0 + k));
+            p.dealt[first + own[v[k] & (groups - 1)] + at[k]] = make_int2(v[k], (int)(t0 + k));
 }
 
 template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embedding_sort(EmbedArgs p)
@@ -244,9 +247,10 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
     if (threadIdx.x == 0) join_count = 0;
     __syncthreads();
     int lower = 0, all = 0;
-    // this wave's dealt tokens of the group, 64 at a time: f(there is one, value, token)
+    // this wave's dealt tokens of the group's list, 64 at a time: f(there is one, value, token)
+    const int list_of = group & (p.deal_groups - 1);
     auto each_dealt = [&](auto f) {
-        const int32_t *lo = p.deal_starts + (int64_t)group * p.deal_blocks, *hi = lo + p.deal_blocks;
+        const int32_t *lo = p.deal_starts + (int64_t)list_of * p.deal_blocks, *hi = lo + p.deal_blocks;
         for (int b = b0; b < b1; ++b) {
             const int n = hi[b] - lo[b];
             const int2* list = p.dealt + (int64_t)b * kDealTokens + lo[b];
@@ -262,22 +266,27 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
     };
     int n_own = 0;  // this wave's tokens of the group's values; the first kSortKept are kept: i << kPlaceBits | place in its part
     if (p.dealt != nullptr) {
-        const int32_t *lo = p.deal_starts + (int64_t)group * p.deal_blocks, *end = p.deal_starts + (int64_t)p.groups * p.deal_blocks;
+        // lower groups: those of lower lists, and of its own list the lower ones
+        const int32_t *lo = p.deal_starts + (int64_t)list_of * p.deal_blocks, *end = p.deal_starts + (int64_t)p.deal_groups * p.deal_blocks;
         for (int b = threadIdx.x; b < p.deal_blocks; b += kSortThreads) {
             lower += lo[b];
             all += end[b];
         }
-        each_dealt([&](bool own, int v, int64_t t) {
+        each_dealt([&](bool there, int v, int64_t t) {
             const int i = v >> shift;
+            const bool own = there && (v & (p.groups - 1)) == group;
+            lower += there && (v & (p.groups - 1)) < group;
             const uint64_t who = __ballot(own);
+            if (who == 0) return;
             // (of one value all at once: 131072 tokens of one value 89 us so, 162 with an atomic of each lane)
             int* to = &counters[wave * values + i];
-            if (__ballot(own && i != __builtin_amdgcn_readfirstlane(i)) == 0) {
-                if (lane == 0) atomicAdd(to, __popcll(who));  // (the first lane has a token wherever one has)
+            const int one = __builtin_ctzll(who), at = n_own + __popcll(who & (((uint64_t)1 << lane) - 1));
+            if (__ballot(own && i != __builtin_amdgcn_readlane(i, one)) == 0) {
+                if (lane == one) atomicAdd(to, __popcll(who));
             } else if (own) {
                 atomicAdd(to, 1);
             }
-            if (own && n_own + lane < kSortKept) kept[wave][n_own + lane] = (uint32_t)i << kPlaceBits | (uint32_t)(t - first);
+            if (own && at < kSortKept) kept[wave][at] = (uint32_t)i << kPlaceBits | (uint32_t)(t - first);
             n_own += __popcll(who);
         });
     } else
@@ -379,7 +388,7 @@ template <bool DENSE> __global__ __launch_bounds__(kSortThreads) void hyena_embe
     }
     // too many to keep: the tokens again
     if (p.dealt != nullptr) {
-        each_dealt([&](bool own, int v, int64_t t) { put(own, v >> shift, t); });
+        each_dealt([&](bool there, int v, int64_t t) { put(there && (v & (p.groups - 1)) == group, v >> shift, t); });
         return;
     }
     for (int64_t t0 = first; t0 < last; t0 += 64 * kSortTokens) {
@@ -682,7 +691,7 @@ struct EmbedSpace {
     int64_t run, runs;
     size_t sorted, counts, joins, join_counts, dealt, deal_starts, part, total;  // byte offsets and the size
     int32_t deal_blocks;  // 0: not dealt
-    int32_t groups, d4;
+    int32_t groups, deal_groups, d4;
     int32_t few_groups, few_lanes;  // 0: the tokens are sorted
 };
 
@@ -714,10 +723,11 @@ EmbedSpace embed_space(const hyena_embedding* op)
     while ((op->V + w.groups - 1) / w.groups > (w.groups < kDealGroups ? kSortValues : kSortMostValues)) w.groups *= 2;
     w.joins = w.counts + up((size_t)op->V * 4);
     w.join_counts = w.joins + up((size_t)((op->V + w.groups - 1) / w.groups * w.groups) * sizeof(int4));
-    w.deal_blocks = T >= kDealCalls && w.groups <= kDealGroups ? (int32_t)((T + kDealTokens - 1) / kDealTokens) : 0;
+    w.deal_groups = w.groups < kDealGroups ? w.groups : kDealGroups;
+    w.deal_blocks = T >= kDealCalls ? (int32_t)((T + kDealTokens - 1) / kDealTokens) : 0;
     w.dealt = w.join_counts + up((size_t)w.groups * 4);
     w.deal_starts = w.dealt + up((size_t)w.deal_blocks * kDealTokens * sizeof(int2));
-    w.part = w.deal_starts + up((size_t)(w.groups + 1) * (size_t)w.deal_blocks * 4);
+    w.part = w.deal_starts + up((size_t)(w.deal_groups + 1) * (size_t)w.deal_blocks * 4);
     w.total = w.part + (size_t)w.runs * 2 * (size_t)w.d4 * 4;
     return w;
 }
@@ -750,7 +760,7 @@ template <typename T> hyena_status embed_backward(const EmbedArgs& a, bool units
     }
     if (a.dealt != nullptr) {
         const dim3 grid((unsigned)a.deal_blocks);
-        const size_t lds = (size_t)a.groups * kSortWaves * 4;
+        const size_t lds = (size_t)a.deal_groups * kSortWaves * 4;
         if (dense)
             HY_LAUNCH(kernel_label("hyena_embedding_deal", true), hyena_embedding_deal<true>, grid, dim3(kSortThreads), lds, s, a);
         else
@@ -884,6 +894,7 @@ hyena_status hyena_embedding_backward(const hyena_embedding* op, const hyena_row
     a.run = (int32_t)w.run;
     a.sorted = (int2*)((char*)scratch + w.sorted);
     a.deal_blocks = w.deal_blocks;
+    a.deal_groups = w.deal_groups;
     a.dealt = w.deal_blocks ? (int2*)((char*)scratch + w.dealt) : nullptr;
     a.deal_starts = (int32_t*)((char*)scratch + w.deal_starts);
     const int64_t teams = 256 / a.lanes;

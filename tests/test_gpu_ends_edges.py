@@ -7,6 +7,7 @@ import pytest
 import ends_ref
 from gpu_util import say
 from long_convolution_sequence_rfft_amd import hyena
+from test_gpu_embedding import run as embedding_run
 from test_gpu_recurrence import IO, f64, torch_dtype
 from test_gpu_token_loss import run as loss_run
 
@@ -67,3 +68,21 @@ def test_loss_of_few_tokens_at_the_limit_of_eight(dtype, tokens):
     # rows made of 16-byte pieces, and not; values that are no multiple of a wave's four
     loss_run((1, tokens, 777, 72), dtype, masked=0.0)
     loss_run((tokens, 1, 3001, 301), dtype, masked=0.3)
+
+
+@pytest.mark.parametrize("case,strided", [((1, 140001, 1600001, 4), False), ((2, 70001, 5000003, 2), True)])
+def test_many_tokens_of_a_table_beyond_the_dealt_groups(case, strided):
+    # more values than 1024 groups of the sort hold: several groups share a list of dealt tokens.  Some
+    # values have many tokens, more than a wave keeps; neighbours of the same list have some, too
+    B, N, V, d = case
+    rng = np.random.default_rng(7)
+    tok = rng.integers(0, V, (B, N))
+    tok[:, ::3] = 1024 * 5 + 3
+    tok[:, 1::9] = 3
+    tok[:, 2::9] = 1024 * (V // 1024 - 1) + 3
+    hyena.hyena_timing_begin(64)
+    try:
+        embedding_run(case, "f32", tokens=tok, strided=strided)
+    finally:
+        kernels, _ = hyena.hyena_timing_end()
+    assert any("hyena_embedding_deal" in k for k in kernels)
