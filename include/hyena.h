@@ -599,6 +599,7 @@ hyena_status hyena_residual_norm_scratch_bytes(const hyena_residual_norm* op, si
  * gradient of the sum, which is that of x and of the residual alike:
  *   n = s r, r = 1 / sqrt(mean(s^2) + eps),  d_n = weight d_y
  *   d_x = d_sum + r (d_n - n mean(d_n n)),   d_weight = sum over tokens of d_y n
+ * d_weight is summed in float64, but for 16 tokens at a time, which are in float32.
  * d_weight: float32 [d], or NULL (then no scratch is needed).  d_x may be d_sum's own memory where
  * that is dense; otherwise outputs must not overlap an input or each other. */
 hyena_status hyena_residual_norm_backward(const hyena_residual_norm* op, const hyena_rows* d_y,

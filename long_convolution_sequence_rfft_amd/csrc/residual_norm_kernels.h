@@ -198,12 +198,18 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm(NormArgs 
     }
 }
 
+// Rows of a team whose part of the weights' gradient is summed in float32; such sums go to
+// float64 ones in LDS, so that what is lost does not grow with the rows (256 equal rows of a team in
+// one float32 sum are up to 63 2^-24 off, 16 of them 4.5 2^-24; gradients of 16384 rows of 768 in bf16
+// 18.6 us with one sum, 19.2 so, of 2^20 rows of 256 366 and 385).
+constexpr int kWeightRows = 16;
+
 template <typename T, bool UNITS, bool WG, int U>
 __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(NormArgs p)
 {
     constexpr int K = kUnit<T>;
     __shared__ float lds[32];
-    extern __shared__ float sums[];  // parts of a wave each: [4][d]
+    extern __shared__ double sums[];  // [teams][whole units of a row], an element one lane's
     const int lanes = WG ? (int)blockDim.x : p.lanes;
     const int teams = WG ? 1 : 256 / lanes, team = WG ? 0 : (int)threadIdx.x / lanes, tl = WG ? (int)threadIdx.x : (int)threadIdx.x % lanes;
     float w[U][K], dw[U][K];
@@ -213,6 +219,26 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(Norm
 #pragma unroll
         for (int i = 0; i < K; ++i) dw[u][i] = 0.0f;
     }
+    const int width = (p.d + K - 1) / K * K;
+    int rows = 0;        // in dw
+    bool more = false;   // there are sums in LDS
+    // dw to LDS.  (Its addresses are not to be held in registers over the rows.)
+    auto put_sums = [&]() {
+        int at = (team * width + tl * K) * (int)sizeof(double);
+        asm volatile("" : "+v"(at));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if ((tl + u * lanes) * K >= p.d) break;
+            double* own = (double*)((char*)sums + at + u * lanes * K * (int)sizeof(double));
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+                own[i] = (more ? own[i] : 0.0) + (double)dw[u][i];
+                dw[u][i] = 0.0f;
+            }
+        }
+        rows = 0;
+        more = true;
+    };
     for (int64_t r = (int64_t)blockIdx.x * teams + team; r < p.rows; r += (int64_t)gridDim.x * teams) {
         const T* x = row_at<T>(p.x, r, p.N);
         const T* dyr = row_at<T>(p.dy, r, p.N);
@@ -250,36 +276,24 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void hyena_residual_norm_grad(Norm
             }
             store_unit<T, UNITS>(dx, (tl + u * lanes) * K, p.d, s[u]);
         }
+        if (++rows == kWeightRows && p.dw_part != nullptr) put_sums();
     }
     if (p.dw_part == nullptr) return;
     float* part = p.dw_part + (int64_t)blockIdx.x * p.d;
-    if constexpr (WG) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < K; ++i) {
-                const int c = (tl + u * lanes) * K + i;
-                if (c < p.d) part[c] = dw[u][i];
-            }
-    } else {
-        // the teams of a wave, then the waves, in their order
-        const int wave = threadIdx.x >> 6;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < K; ++i) {
-                const int c = (tl + u * lanes) * K + i;
-                float v = dw[u][i];
-                for (int m = lanes; m < 64; m *= 2) v += __shfl_xor(v, m);
-                if ((threadIdx.x & 63) < (unsigned)lanes && c < p.d) sums[wave * p.d + c] = v;
-            }
+    put_sums();
+    // the upper half of many teams onto the lower one, the last four together
+    int left = teams;
+    for (; left > 4; left /= 2) {
         __syncthreads();
-        for (int c = threadIdx.x; c < p.d; c += 256) {
-            float v = 0.0f;
+        for (int k = threadIdx.x; k < left / 2 * width; k += (int)blockDim.x) sums[k] += sums[k + left / 2 * width];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.d; c += (int)blockDim.x) {
+        double x = sums[c];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v += sums[k * p.d + c];
-            part[c] = v;
-        }
+        for (int k = 1; k < 4; ++k)
+            if (k < left) x += sums[k * width + c];
+        part[c] = (float)x;
     }
 }
 
@@ -287,7 +301,7 @@ template <typename T, bool UNITS, bool WG, int U, int KIND> hyena_status norm_as
 {
     if constexpr (KIND == 2)
         HY_LAUNCH(kernel_label("hyena_residual_norm_grad", type_label<T>(), UNITS, WG, U), (hyena_residual_norm_grad<T, UNITS, WG, U>),
-                  dim3((unsigned)l.groups), dim3((unsigned)l.threads), WG ? 0 : (size_t)4 * a.d * sizeof(float), s, a);
+                  dim3((unsigned)l.groups), dim3((unsigned)l.threads), a.dw_part ? (size_t)(WG ? 1 : 256 / a.lanes) * ((a.d + kUnit<T> - 1) / kUnit<T> * kUnit<T>) * sizeof(double) : 0, s, a);
     else
         HY_LAUNCH(kernel_label("hyena_residual_norm", type_label<T>(), UNITS, WG, U, KIND == 1), (hyena_residual_norm<T, UNITS, WG, U, KIND == 1>),
                   dim3((unsigned)l.groups), dim3((unsigned)l.threads), 0, s, a);

@@ -86,3 +86,46 @@ def test_many_tokens_of_a_table_beyond_the_dealt_groups(case, strided):
     finally:
         kernels, _ = hyena.hyena_timing_end()
     assert any("hyena_embedding_deal" in k for k in kernels)
+
+
+@pytest.mark.parametrize("rows,d", [((1 << 19) + 5, 256), (1 << 18, 1028)])
+def test_norm_weight_gradient_of_very_many_rows(rows, d):
+    # All rows are alike, +-1 and the same gradient, so that every term is exact. A team sums 16 of
+    # them in float32, at worst 8.5 2^-24 off ((2 + ... + 16) / 16), which is the whole sum's error too; a
+    # workgroup's part and the result are rounded: 2 2^-24.  The team's rows in one float32 sum would be
+    # off by more, the rounding of each step being the same one over and over.
+    import torch
+    say(f"[gpu] norm, weight's gradient of {rows} rows of {d}")
+    gen = torch.Generator().manual_seed(3)
+    dy = (0.5 + 0.5 * torch.rand(d, generator=gen))
+    x = torch.where(torch.rand(d, generator=gen) < 0.5, -1.0, 1.0)
+    plan = hyena.ResidualNorm(1, rows, d, eps=0.0)
+    _, dw = plan.backward(dy.cuda().expand(1, rows, d), x.cuda().expand(1, rows, d), torch.ones(d, device="cuda"))
+    ref = rows * f64(dy) * f64(x)
+    bound = 10.5 * 2.0 ** -24 * np.abs(ref)
+    chain = np.cumsum(np.broadcast_to(dy.numpy(), (256, d)), axis=0, dtype=np.float32)[-1].astype(np.float64)
+    assert np.any(np.abs(chain / 256 - f64(dy)) > 10.5 * 2.0 ** -24 * f64(dy))  # (256 rows of a team so)
+    err = np.abs(f64(dw) - ref)
+    say(f"[gpu]   worst error / bound {float(np.max(err / bound)):.3f}")
+    assert np.all(err <= bound)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", [(1, 40000, 8), (1, 20000, 2048), (2, 9001, 96), (1, 30000, 33), (1, 2100, 5000), (1, 1500, 16380)])
+def test_norm_gradients_of_teams_of_many_rows(case, dtype):
+    # more rows for a team than it sums in float32, with some left at its end, by teams of every
+    # width; against float64 on the GPU, at the tolerances of the other tests of the norm
+    import torch
+    B, N, d = case
+    say(f"[gpu] norm gradients {case} {dtype}")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dt = torch_dtype(dtype)
+    s, dy = (torch.randn(case, generator=gen, device="cuda").to(dt) for _ in range(2))
+    w = 1 + 0.2 * torch.randn(d, generator=gen, device="cuda")
+    dx, dw = hyena.ResidualNorm(*case, io_dtype=IO[dtype]).backward(dy, s, w)
+    n = s.double() * torch.rsqrt(s.double().square().mean(-1, keepdim=True) + float(np.float32(1e-6)))
+    ref = (dy.double() * n).sum((0, 1))
+    size = (dy.double() * n).abs().sum((0, 1))
+    assert bool(((dw.double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 2.0 ** -20 * size).all())
+    again = hyena.ResidualNorm(*case, io_dtype=IO[dtype]).backward(dy, s, w)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
