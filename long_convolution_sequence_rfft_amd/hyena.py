@@ -1032,13 +1032,13 @@ class ResidualNorm(_Tokens):
     _FORMATS = {None: HYENA_NORM_IO, "e4m3": HYENA_NORM_E4M3, "int8": HYENA_NORM_INT8}
 
     def __init__(self, B, N, d, io_dtype=HYENA_F32, eps=1e-6, quantized=None, group=None, device="cuda"):
-        self._place(io_dtype, device)
-        if quantized not in self._FORMATS:
+        if quantized is not None and quantized not in ("e4m3", "int8"):
             raise ValueError(f"quantized must be None, 'e4m3' or 'int8', got {quantized!r}")
         if group is not None and (quantized is None or group not in (32, 64, 128)):
             raise ValueError(f"group must be None, or 32, 64 or 128 with quantized, got {group!r}")
         if group is not None and int(d) % group:
             raise ValueError(f"d must be a multiple of group, got {d} and {group}")
+        self._place(io_dtype, device)
         self.B, self.N, self.d, self.eps = int(B), int(N), int(d), float(eps)
         self.quantized, self.group = quantized, group
         st, self.scratch_bytes = hyena_residual_norm_scratch_bytes(self._op(0, (0, 0, 0), (0, 0, 0)))
