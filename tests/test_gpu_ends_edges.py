@@ -129,3 +129,46 @@ def test_norm_gradients_of_teams_of_many_rows(case, dtype):
     assert bool(((dw.double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 2.0 ** -20 * size).all())
     again = hyena.ResidualNorm(*case, io_dtype=IO[dtype]).backward(dy, s, w)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+def test_gradients_of_a_packed_table_past_32_bits():
+    # More than 4096 tokens: the table of 2^21 + 77 rows of 1024 in bf16 (4.3 GB) is packed, and G is made in
+    # many pieces.  All rows but five are zeros, and so are their logits; those five, their neighbours
+    # and others are compared.  Tolerances: those of the loss's other tests (r of a probability
+    # from two logits' sums of absolute values), two terms of G, sums of as many terms as are not 0.
+    import torch
+    T, V, d, scale = 5000, (1 << 21) + 77, 1024, 0.2
+    say(f"[gpu] token_loss gradients, packed table past 32 bits, {T} tokens")
+    u = ends_ref.HALF_STEP["bf16"]
+    gen = torch.Generator().manual_seed(3)
+    at = torch.tensor([0, 5, V // 2, V - 2, V - 1])
+    rows = torch.randn((5, d), generator=gen).bfloat16()
+    table = torch.zeros((V, d), dtype=torch.bfloat16, device="cuda")
+    table[at.cuda()] = rows.cuda()
+    x = torch.randn((1, T, d), generator=gen).bfloat16()
+    hit = torch.arange(T) % 5
+    hit[::7] = -1
+    target = torch.where(hit >= 0, at[hit], -1).to(torch.int32)[None].cuda()
+    plan = hyena.TokenLoss(1, T, V, d, io_dtype=hyena.HYENA_BF16, scale=scale)
+    _, lse = plan.forward(x.cuda(), table, target)
+    dx, dt = plan.backward(torch.ones((1, T), device="cuda"), x.cuda(), table, target, lse)
+    live = (hit >= 0).numpy()
+    xs, ws, y = f64(x)[0][live], f64(rows), hit.numpy()[live]
+    s = float(np.float32(scale))
+    size = s * np.abs(xs) @ np.abs(ws).T
+    p = np.exp(s * xs @ ws.T - f64(lse)[0][live][:, None])
+    g = p.copy()
+    g[np.arange(len(y)), y] -= 1
+    r = 2 * (d + 8) * 2.0 ** -24 * size.max(-1) + 2.0 ** -20 + 2.0 ** -21 * size.max(-1)
+    dg = r[:, None] * p + 2.0 ** -23 + u * u * np.abs(g)
+    ref = s * g @ ws
+    bound = u * np.abs(ref) + s * (dg + 21 * 2.0 ** -24 * np.abs(g)) @ np.abs(ws)
+    assert np.all(np.abs(f64(dx)[0][live] - ref) <= bound) and not f64(dx)[0][~live].any()
+    ref = s * g.T @ xs
+    bound = u * np.abs(ref) + s * (dg + (len(y) + 16) * 2.0 ** -24 * np.abs(g)).T @ np.abs(xs)
+    assert np.all(np.abs(f64(dt[at.cuda()]) - ref) <= bound)
+    p = np.exp(-f64(lse)[0][live])  # of a row of zeros
+    ref = s * p @ xs
+    bound = u * np.abs(ref) + s * (p * (r + u * u + (len(y) + 16) * 2.0 ** -24)) @ np.abs(xs)
+    for v in (1, 4, 6, V // 2 - 1, V // 2 + 1, V // 3, V - 3):
+        assert np.all(np.abs(f64(dt[v]) - ref) <= bound + ends_ref.TINY["bf16"]), v
