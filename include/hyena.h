@@ -618,7 +618,8 @@ hyena_status hyena_residual_norm_backward(const hyena_residual_norm* op, const h
  *
  * A token whose target is outside 0..V-1 takes no part: its loss, lse and d_x are
  * zeros, nothing of it reaches d_table, and its rows of x and d_loss are not read.
- * Such tokens cost nothing: the rows of the others are gathered first.
+ * No products are made for such tokens: the rows of the others are gathered first.  But kernels,
+ * scratch and what a large call does to the table first go by B * N.
  *
  * Precision.  Products of 16-bit operands are accumulated in float32, in float32
  * storage each operand is three bfloat16 terms (24 bits) and the six largest of their
