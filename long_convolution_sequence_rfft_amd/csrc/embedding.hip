@@ -54,10 +54,12 @@ constexpr int kDealGroups = 1024;  // at most; the lists of more of the sort's g
 // which two groups share a list, 199 and 820).
 constexpr int64_t kDealCalls = 131072;
 constexpr int kSortKept = 512;     // tokens of its values that a wave keeps: 32 KB of LDS in all
-constexpr int kSumRows = 4;        // gradient rows of a team under way (8: 73.5 us in all for 65536 tokens, 4: 64.7)
+// Gradient rows of a team under way (gradient of 65536 tokens of a text, width 768 in bf16, added to one that is
+// there, inputs that come from memory, in all: 8 73.0 us, 4 68.8).
+constexpr int kSumRows = 4;
 // Runs are no shorter than kSumRows, and as short as this many of them allow: fewer leave the
-// sums waiting, more the joins (65536 tokens in all: 2048 61.8, 4096 60.9, 8192 72.2 us); 4096 of width 768 in bf16 are one round of six
-// waves a SIMD, which the sums' registers allow (five: 75 us instead of 70).
+// sums waiting, more the joins (the same gradient: 2048 77.3, 4096 68.8, 8192 73.3 us; sums 51, 41 and 41,
+// joins 10, 12 and 17).  4096 of width 768 in bf16 are one round of six waves a SIMD.
 constexpr int64_t kSumTeams = 4096;
 constexpr int kFewValues = 32;     // tables of no more values than this
 constexpr int kFewRows = 8;        // gradient rows of a team under way

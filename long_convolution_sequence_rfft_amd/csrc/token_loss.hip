@@ -8,8 +8,8 @@ namespace {
 constexpr const char* kWho = "token loss";
 
 // G of a piece of the vocabulary takes about this much, or a tile of values if that
-// is more (gradients of 16384 tokens, 50257 values, width 768: in pieces of 256 MB 3184, 512 MB 3033, 1 GiB 2815,
-// 2 GiB 2715 us).
+// is more (gradients of 16384 tokens, a quarter masked, 50257 values, width 768: in pieces of 256 MB 5105,
+// 512 MB 5050, 1 GiB 4540, 2 GiB 4255 us; the last 6% are not worth as much scratch again).
 constexpr int64_t kGradBytes = (int64_t)1024 << 20;
 // The sums of a piece's tiles, forward: larger ones would be written to memory and read back,
 // and a launch could have more than 2^32 threads.
@@ -19,16 +19,17 @@ constexpr int64_t kPartBytes = (int64_t)256 << 20;
 // and 115 us so, 72, 73, 76 and 82 us in large ones; width 256 in 16 bits: 14, 14, 17, 23 and 18, 20, 19, 20).
 constexpr int64_t kSmallTiles = 128;
 // Rows that the blocks of gathered rows and of G are apart from each other beyond their tokens: at a power
-// of two a step's pieces of all of a tile's blocks would share one place in the caches (2048 tokens in
-// float32: 1506 us without, 1484 so; logits of 16384 in bf16, backward: 907 and 884).
+// of two a step's pieces of all of a tile's blocks would share one place in the caches (the same
+// gradients' logits: 1400 us without, 1378 so).
 constexpr int64_t kBlockRows = 32;
 // Workgroups that d_x's sums are cut for, and into which part of their time: they come last,
 // and the shorter they are the sooner the last one ends, but each adds to d_x's sums (the
-// same gradients: 1 part 2894, 2 2924, 3 2902, 4 2780, 6 2787 us).
+// same gradients: 1 part 4700, 2 4380, 4 4480, 6 4390 us; of 2048 tokens, 31999 values in float32
+// 1725, 1630, 1497 and 1488).
 constexpr int64_t kSplitGroups = 512, kSplitParts = 4;
 // Steps of 32 tokens that a part of d_table's sums has at least.  They are cut so that no part takes
-// longer than a workgroup's share of the piece's work (16384 tokens, 2048 values: 170 us so; of
-// twice the share 266, of half of it 166).
+// longer than a workgroup's share of the piece's work (16384 tokens, 2048 values: 315 us so, of
+// twice the share 325, of half of it 336; 65536 tokens, 16 values: 154, 188 and 154).
 constexpr int64_t kTableSteps = 4;
 
 hyena_status refuse(const char* what) { return fail(HYENA_ERR_INVALID_ARGUMENT, std::string(kWho) + ": " + what); }
@@ -55,7 +56,7 @@ constexpr int32_t kFewGroups = 256, kFewGroupsHalf = 512;
 constexpr int64_t kFewGroupsTokens = 4;  // in 16 bits, at most: kFewGroupsHalf
 // Others of more tokens than this bring the table into the matrix operands' form first (in that
 // form and as given, forward: 1024 tokens 128 and 103 us, 4096 314 and 304, 8192 573 and 575, 16384 1062
-// and 1117; backward 383 and 370, 1133 and 1123, 8192 1939 and 1960).
+// and 1117; backward 460 and 446, 1473 and 1465, 2840 and 2856, 5890 and 6023).
 constexpr int64_t kPackTokens = 4096;
 
 bool is_few(const hyena_token_loss* op, bool grad)

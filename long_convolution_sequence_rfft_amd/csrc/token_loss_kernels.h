@@ -722,8 +722,9 @@ template <typename T> __device__ __forceinline__ void store_dx(const LossArgs& p
 }
 
 // One launch, so that neither product waits for the other's last workgroups.  Tiles of 256
-// channels by 128 rows and two workgroups a compute unit: three of fewer registers spill 22 and
-// take twice as long, tiles of 256 by 256 in one workgroup 2072 us instead of 1905.
+// channels by 128 rows and two workgroups a compute unit: with one term of G three of fewer
+// registers spilled 22 and took twice as long, tiles of 256 by 256 in one workgroup 2072 us
+// instead of 1905.
 //
 // The first table_groups workgroups: d_table of kGradRows values of this piece and
 // kGradChannels channels, the sum over one of p.table_splits parts of the tokens.  The
@@ -918,8 +919,8 @@ template <typename T> __global__ __launch_bounds__(1024) void hyena_loss_finish_
     }
 }
 
-// Calls of fewer tokens: a wave of hyena_loss_finish has one token, not four (300 tokens: 8 us with
-// one, 14 with four; 16384 36 and 28).
+// Calls of fewer tokens: a wave of hyena_loss_finish has one token, not four (300 tokens, 2048 values:
+// 6.5 us with one, 8.1 with four; 8192 tokens 31 and 30; 16384 tokens, 50257 values 34 and 32).
 constexpr int64_t kFinishTokens = 16384;
 
 template <typename T, bool GRAD> hyena_status loss_begin(const LossArgs& a, bool pack, bool units, hipStream_t s)
