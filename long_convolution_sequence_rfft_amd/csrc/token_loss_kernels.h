@@ -11,13 +11,15 @@
 //   hyena_loss_table    d_table of a piece from its sums, where the tokens are cut
 //   hyena_loss_finish   d_x from its sums (hyena_loss_finish_few where they are many)
 //   hyena_loss_zeros    zeros for the other tokens, where the products write d_x themselves
-// Bound by the matrix instructions, 2 tokens V d operations forward, 6 backward, and these by the
-// power the card may take.  16384 tokens, 50257 values, width 768 in bf16: logits 1091 us, 1159 TFLOP/s (the
-// matrix units are busy for 66% of the cycles, of 1.68 GHz; a large product of the
-// library's reaches 1279, this one 953).  12288 of them backward: logits 887 us (1069 TFLOP/s; they
-// write G, 2.5 GB), products 1904 us (996; of two products of the library's 944 and 822; the
-// matrix units are busy for 53% of the cycles, of 1.80 GHz).  2048 tokens, 31999 values in float32, whose six
-// products are counted: 513 us (1177) and 984 us (1228).
+//
+// Bound by the matrix instructions, 2 tokens V d operations forward, 10 backward with 16-bit storage
+// (6, and G's products by two terms each), and these by the power the card may take.  16384 tokens, 50257
+// values, width 768 in bf16: logits 1090 to 1120 us, 1130 to 1160 TFLOP/s (the matrix units are
+// busy for 66% of the cycles, of 1.64 to 1.68 GHz; a large product of the library's reaches 1279,
+// this one 953).  12288 of them backward: logits 1360 us, of which the 2.5 GB of G's two terms take a third; products 3150 us
+// (1205 TFLOP/s; of one term two products of the library's 944 and 822; the matrix units are busy for
+// 72% of the cycles, of 1.60 GHz).  2048 tokens, 31999 values in float32, whose six products are
+// counted: 515 us (1172) and 988 us (1222).
 #pragma once
 
 #include "matmul_device.h"
@@ -589,7 +591,7 @@ template <typename T, int N, bool GRAD, bool OWN> __global__ __launch_bounds__(2
 
 // Gradients of at most N tokens: a wave takes the values of its part one after the
 // other, 256 channels of them, adds their share to d_x and makes their rows of d_table.
-// Bound by reading and writing the two tables (8 tokens in float32: 65 us for 309 MB); G of a
+// Bound by reading and writing the two tables (8 tokens in float32: 72 us for 319 MB); G of a
 // value is the same for all lanes.  d_table goes past the caches, which leaves the table there
 // for the next call's logits (4 tokens in float32, a call: 115 us through them, 108 so).
 template <typename T, int N, bool UNITS> __global__ __launch_bounds__(256) void hyena_loss_few_grads(LossArgs p)
